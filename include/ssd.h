@@ -393,6 +393,243 @@ ssd_status ssd_causal_conv1d_tokens(int64_t B, int64_t S, int64_t C, int64_t W, 
 ssd_status ssd_gated_rmsnorm(int64_t rows, int64_t D, int64_t groups, float eps, int32_t dtype, const void *x,
                              const void *z, const float *w, void *out, void *stream);
 
+/*
+ * Selective scan: the state-space recurrence with a decay per channel AND
+ * state (A [D,N]) and a step per channel, where the SSD above has one decay
+ * and one step per head.  For every batch row b, token t and channel c, with
+ * group g = c / (D/G):
+ *
+ *     d_t    = clamp(softplus(dt[b,t,c] + dt_bias[c]))   bias / softplus / clamp optional
+ *     h_t[:] = exp(d_t A[c,:]) h_{t-1}[:] + d_t x[b,t,c] B[b,t,g,:]
+ *     y[b,t,c] = (h_t . C[b,t,g,:] + Dskip[c] x[b,t,c]) * silu(z[b,t,c])
+ *
+ * Shapes and types:
+ *   x, z, y        [B,L,D]    x_dtype (z optional)
+ *   dt             [B,L,D]    dt_dtype: x_dtype or SSD_F32
+ *   A              [D,N] fp32; Dskip, dt_bias [D] fp32 (optional)
+ *   Bm, Cm         [B,L,G,N]  x_dtype
+ *   initial_state, final_state  [B,D,N] fp32 (optional; NULL = zero / not returned)
+ *   lengths        [B] int32, device (optional): row b has lengths[b] tokens
+ *                  (clamped to 0..L), what follows is padding: nothing of it
+ *                  is read, y is 0 there, and final_state is the state after
+ *                  the row's last token (initial_state for an empty row)
+ * x, dt, z, Bm and Cm are read through strides: element (b, t, i) is at
+ * b * stride[0] + t * stride[1] + i, strides in elements, both zero meaning
+ * dense.  So slices of a projection's output are read in place.  y is dense.
+ * Every dim > 0, N <= 128, D % G == 0.  fp32 arithmetic and states.  No
+ * alignment is required beyond the types' own.
+ * A sequence is cut into segments walked in parallel when B and D alone do not
+ * fill the GPU; the cut depends on the shape and the GPU's SM count only.
+ * workspace: device, 256-byte aligned, ssd_selective_scan_workspace_size()
+ * bytes (may be 0; then NULL is accepted).  Enqueue only.
+ */
+typedef struct {
+    int64_t B, L, D, N, G;
+    const void *x;
+    const void *dt;
+    const float *A;
+    const void *Bm;
+    const void *Cm;
+    const float *Dskip;
+    const void *z;
+    const float *dt_bias;
+    const float *initial_state;
+    const int32_t *lengths;
+    void *y;
+    float *final_state;
+    int64_t x_stride[2], dt_stride[2], z_stride[2], b_stride[2], c_stride[2];
+    int32_t x_dtype, dt_dtype; /* ssd_dtype */
+    int32_t dt_softplus;       /* nonzero: softplus(dt + bias) */
+    float dt_min, dt_max;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_scan_args;
+
+ssd_status ssd_selective_scan_workspace_size(const ssd_scan_args *args, size_t *bytes);
+ssd_status ssd_selective_scan(const ssd_scan_args *args, void *stream);
+
+/*
+ * Backward of the selective scan: gradients of sum(dy * y) + sum(dfinal *
+ * final_state).  The states are recomputed from the inputs (y, final_state
+ * and the workspace of `fwd` are ignored).
+ *   dy       [B,L,D] x_dtype, dense          dfinal  [B,D,N] fp32 or NULL
+ *   dx       [B,L,D] x_dtype                 ddt     [B,L,D] dt_dtype (raw dt)
+ *   dB, dC   [B,L,G,N] x_dtype               dA      [D,N] fp32
+ *   dD       [D] fp32, required with Dskip   dz      [B,L,D] x_dtype, required with z
+ *   ddt_bias [D] fp32, required with dt_bias dh0     [B,D,N] fp32 or NULL
+ * Outputs are dense; a row's padding gets zeros.  The clamp passes no gradient
+ * where it is active.  Sums run in a fixed order: bitwise reproducible.
+ * workspace: device, 256-byte aligned, ssd_selective_scan_bwd_workspace_size()
+ * bytes (it holds the state before every eighth token).  Enqueue only.
+ */
+typedef struct {
+    ssd_scan_args fwd;
+    const void *dy;
+    const float *dfinal;
+    void *dx;
+    void *ddt;
+    float *dA;
+    void *dB;
+    void *dC;
+    float *dD;
+    void *dz;
+    float *ddt_bias;
+    float *dh0;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_scan_bwd_args;
+
+ssd_status ssd_selective_scan_bwd_workspace_size(const ssd_scan_bwd_args *args, size_t *bytes);
+ssd_status ssd_selective_scan_bwd(const ssd_scan_bwd_args *args, void *stream);
+
+/*
+ * One token of the selective scan for each of B sequences, from carried states.
+ *   x, z, y [B,D] x_dtype; dt [B,D] dt_dtype; Bm, Cm [B,G,N] x_dtype; rows of
+ *   x, dt, z, Bm, Cm are `*_row` elements apart (0 = dense); y dense
+ *   state, state_out  [nslots,D,N] fp32; equal for an update in place
+ *   slots             [B] int32, device, or NULL (row b uses slot b, nslots = B).
+ *                     A row whose slot is outside 0..nslots-1 is left out: its y
+ *                     is 0 and no state is touched.  Rows must not share a slot.
+ */
+typedef struct {
+    int64_t B, D, N, G, nslots;
+    const void *x;
+    const void *dt;
+    const float *A;
+    const void *Bm;
+    const void *Cm;
+    const float *Dskip;
+    const void *z;
+    const float *dt_bias;
+    const float *state;
+    float *state_out;
+    const int32_t *slots;
+    void *y;
+    int64_t x_row, dt_row, z_row, b_row, c_row;
+    int32_t x_dtype, dt_dtype;
+    int32_t dt_softplus;
+    float dt_min, dt_max;
+} ssd_scan_step_args;
+
+ssd_status ssd_selective_scan_step(const ssd_scan_step_args *args, void *stream);
+
+/*
+ * The short causal convolution in front of the scan, with a carried state:
+ *   y[b,t,c] = act(bias[c] + sum_{k<W} w[c,k] v[b,t-(W-1)+k,c]),  act = SiLU (silu != 0) or none,
+ * where v is x from token 0 on and the row's initial_state before it:
+ * v[b,-(W-1)+j] = initial_state[b,j] (zeros when NULL).  final_state holds the
+ * last W-1 entries of v, what the next call of the same sequence starts from.
+ *   x [B,L,C] dtype, strided like the scan's; y [B,L,C] dense
+ *   w [C,W] fp32, 1 <= W <= 8; bias [C] fp32 or NULL
+ *   initial_state, final_state [B,W-1,C] dtype (optional)
+ *   lengths [B] int32, device (optional): as for the scan
+ */
+typedef struct {
+    int64_t B, L, C, W;
+    const void *x;
+    int64_t x_stride[2];
+    const float *w;
+    const float *bias;
+    const void *initial_state;
+    const int32_t *lengths;
+    void *y;
+    void *final_state;
+    int32_t dtype;
+    int32_t silu;
+} ssd_conv_args;
+
+ssd_status ssd_causal_conv_carry(const ssd_conv_args *args, void *stream);
+
+/* Its backward: gradients of sum(dy * y) + sum(dfinal * final_state).  dy, dx
+ * [B,L,C] dtype, dense; dfinal, dh0 [B,W-1,C] dtype (optional); dw [C,W] fp32;
+ * dbias [C] fp32, required with bias.  y and final_state of `fwd` are ignored.
+ * Sums run in a fixed order.  workspace as elsewhere. */
+typedef struct {
+    ssd_conv_args fwd;
+    const void *dy;
+    const void *dfinal;
+    void *dx;
+    float *dw;
+    float *dbias;
+    void *dh0;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_conv_bwd_args;
+
+ssd_status ssd_causal_conv_bwd_workspace_size(const ssd_conv_bwd_args *args, size_t *bytes);
+ssd_status ssd_causal_conv_bwd(const ssd_conv_bwd_args *args, void *stream);
+
+/* One token of the convolution for each of B sequences: x [B,C] (rows x_row
+ * apart, 0 = dense), y [B,C]; state, state_out [nslots,W-1,C] dtype, equal for
+ * an update in place; slots as for ssd_selective_scan_step. */
+typedef struct {
+    int64_t B, C, W, nslots;
+    const void *x;
+    int64_t x_row;
+    const float *w;
+    const float *bias;
+    const void *state;
+    void *state_out;
+    const int32_t *slots;
+    void *y;
+    int32_t dtype;
+    int32_t silu;
+} ssd_conv_step_args;
+
+ssd_status ssd_causal_conv_step(const ssd_conv_step_args *args, void *stream);
+
+/*
+ * Block norm: the end of one block and the beginning of the next in one pass,
+ *   p  = o / rms(o) * w_post     (p = o when w_post is NULL)
+ *   r' = r + scale * gate * p    (scale, gate: 1 when NULL)
+ *   n  = r' / rms(r') * w_pre,   rms(v) = sqrt(mean(v^2) + eps) over a row.
+ * n is of r' as stored, rounded to the stream's type.  Without o, r' = r and
+ * only n is written (the norm before the first block).
+ *   o, n      [rows,D] dtype
+ *   r, r_out  [rows,D] stream_dtype: dtype or SSD_F32; r_out may be r
+ *   gate      [rows/rows_per_gate, D] dtype: 1 for a gate per token, a
+ *             sequence's length for a gate per sequence
+ *   w_post, w_pre, scale  [D] fp32
+ * D <= 16384.
+ */
+typedef struct {
+    int64_t rows, D, rows_per_gate;
+    const void *o;
+    const void *r;
+    const void *gate;
+    const float *w_post;
+    const float *w_pre;
+    const float *scale;
+    void *n;
+    void *r_out;
+    int32_t dtype, stream_dtype;
+    float eps;
+} ssd_block_norm_args;
+
+ssd_status ssd_block_norm(const ssd_block_norm_args *args, void *stream);
+
+/* Its backward, from o, r_out (read), gate, the weights and the gradients dn
+ * [rows,D] dtype of n and dr_out [rows,D] stream_dtype of r' from above (NULL =
+ * zero): dr [rows,D] stream_dtype, dw_pre [D]; with o also d_o [rows,D] dtype,
+ * dw_post, dscale [D] fp32 and dgate (gate's shape and type), each required
+ * with its input.  r and n of `fwd` are ignored.  Sums run in a fixed order. */
+typedef struct {
+    ssd_block_norm_args fwd;
+    const void *dn;
+    const void *dr_out;
+    void *d_o;
+    void *dr;
+    void *dgate;
+    float *dw_post;
+    float *dw_pre;
+    float *dscale;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_block_norm_bwd_args;
+
+ssd_status ssd_block_norm_bwd_workspace_size(const ssd_block_norm_bwd_args *args, size_t *bytes);
+ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream);
+
 /* Self-test of the bounded device-side waits (no counterpart on the pages;
  * the pages' kernels report errors only as exceptions on the host).  Every
  * mbarrier wait in the tensor-core kernels gives up after a time limit

@@ -22,6 +22,11 @@ import threading
 import torch
 
 from . import _build
+from . import selective as _selective
+from .selective import (SsdBlockNormArgs, SsdBlockNormBwdArgs, SsdConvArgs, SsdConvBwdArgs, SsdConvStepArgs, SsdScanArgs,
+                        SsdScanBwdArgs, SsdScanStepArgs, block_norm, block_norm_bwd, causal_conv1d_bwd,
+                        causal_conv1d_carry, causal_conv1d_step, make_conv_args, make_scan_args, selective_scan,
+                        selective_scan_bwd, selective_scan_step)
 
 __all__ = [
     "SSD_F32", "SSD_F16", "SSD_BF16", "SSD_OPS_F32", "SSD_OPS_F16", "SSD_OPS_BF16",
@@ -33,6 +38,9 @@ __all__ = [
     "ssd_segment_log_decay", "ssd_state_fold", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size",
     "mamba2_ssd_fwd_varlen", "SsdBwdArgs", "ssd_bwd", "ssd_bwd_workspace_size", "mamba2_ssd_bwd",
     "ssd_causal_conv1d", "ssd_gated_rmsnorm", "causal_conv1d", "gated_rmsnorm",
+    "SsdScanArgs", "SsdScanBwdArgs", "SsdScanStepArgs", "make_scan_args", "selective_scan", "selective_scan_bwd",
+    "selective_scan_step", "SsdConvArgs", "SsdConvBwdArgs", "SsdConvStepArgs", "make_conv_args", "causal_conv1d_carry",
+    "causal_conv1d_bwd", "causal_conv1d_step", "SsdBlockNormArgs", "SsdBlockNormBwdArgs", "block_norm", "block_norm_bwd",
 ]
 
 SSD_F32, SSD_F16, SSD_BF16 = 0, 1, 2
@@ -134,6 +142,7 @@ _SIGS = {
     "ssd_fwd_varlen": [_P, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p],
     "ssd_state_fold": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+    **_selective.SIGNATURES,
 }
 
 

@@ -1,0 +1,310 @@
+// scan_common.cuh -- what the selective-scan kernels share: the parameter
+// block, loads of four channels at a time, the step d_t and packed fp32 math.
+#pragma once
+
+#include "ssd_internal.cuh"
+
+namespace ssd {
+
+struct ScanParams {
+    int B, L, D, N, G;
+    const void *x, *dt, *Bm, *Cm, *z;
+    const float *A, *Dskip, *dt_bias, *h0;
+    const int32_t *lengths;
+    void *y;
+    float *final_state;
+    long long xs[2], dts[2], zs[2], bs[2], cs[2];  // strides (batch, token) in elements
+    int dt32;                                      // dt is fp32
+    int softplus, has_limit;
+    float dt_min, dt_max;
+    // segments: tokens [s seg_len, (s+1) seg_len) of every row; seg_len a multiple of 32
+    int nseg, seg_len;
+    float *seg_states;  // [B,nseg,D,N] state entering a segment (slot 0 unused)
+    float *seg_sum;     // [B,nseg,D]   sum of d over a segment
+    int tiles;          // channel tiles per group
+    // backward
+    const void *dy;
+    const float *dfinal;
+    float *ckpt;        // [B,ceil(L/8),D,N] state before every eighth token
+    float *adj;         // [B,nseg,D,N] adjoint state after a segment (last slot unused)
+    void *dx, *ddt, *dz;
+    float *dh0;
+    float *part_bc;     // [G*tiles,B,L,2*NP] per-tile dB and dC
+    float *part_a;      // [B*nseg,D,N]
+    float *part_d;      // [2,B*nseg,D] dD, ddt_bias
+};
+
+// One token per sequence (scan_step.cu).
+struct ScanStepParams {
+    int B, D, N, G;
+    long long nslots;
+    const void *x, *dt, *Bm, *Cm, *z;
+    const float *A, *Dskip, *dt_bias, *state;
+    float *state_out;
+    const int32_t *slots;
+    void *y;
+    long long x_row, dt_row, z_row, b_row, c_row;
+    int dt32, softplus, has_limit;
+    float dt_min, dt_max;
+};
+cudaError_t launch_scan_step(const ScanStepParams &p, int io, cudaStream_t s);
+
+struct ConvStepParams {
+    int B, C, W;
+    long long nslots, x_row;
+    const void *x;
+    const float *w, *bias;
+    const void *state;
+    void *state_out;
+    const int32_t *slots;
+    void *y;
+    int silu;
+};
+cudaError_t launch_conv_step(const ConvStepParams &p, int io, cudaStream_t s);
+
+// The convolution over prompts and its backward (conv_carry.cu).
+struct ConvParams {
+    int B, L, C, W;
+    const void *x;
+    long long xs[2];
+    const float *w, *bias;
+    const void *h0;
+    const int32_t *lengths;
+    void *y, *final_state;
+    int silu;
+    // backward
+    const void *dy, *dfinal;
+    void *dx, *dh0;
+    float *dw, *dbias;
+    float *part;  // [rows, W + 1, C] sums of dw (first W) and dbias
+};
+cudaError_t launch_conv(const ConvParams &p, int io, cudaStream_t s);
+cudaError_t launch_conv_bwd(const ConvParams &p, int io, cudaStream_t s);
+long long conv_bwd_part_rows(int B, int L, int C);
+
+// The block norm and its backward (block_norm.cu).
+struct BlockNormParams {
+    long long rows, rows_per_gate;
+    int D;
+    const void *o, *r, *gate;
+    const float *w_post, *w_pre, *scale;
+    void *n, *r_out;
+    float eps;
+    // backward
+    const void *dn, *dr_out;
+    void *d_o, *dr, *dgate;
+    float *dw_post, *dw_pre, *dscale;
+    float *part;          // [chunks, 2, D]
+    long long chunk_rows;  // rows per chunk; a chunk lies within one gate's rows
+    long long chunks;
+};
+cudaError_t launch_block_norm(const BlockNormParams &p, int io, int sio, cudaStream_t s);
+cudaError_t launch_block_norm_bwd(const BlockNormParams &p, int io, int sio, cudaStream_t s);
+void block_norm_chunks(BlockNormParams &p);
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kCkpt = 8;  // tokens between stored states (backward)
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Two fp32 numbers in one register pair; a packed operation takes one issue
+// slot for both.
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+
+// Four consecutive elements as loaded, 8 bytes (16-bit types) or 16.
+struct Raw4 {
+    uint32_t w[4];
+};
+
+// vec: the address is aligned to the four elements and all four exist; else nv of them, one by one.
+template <int IO>
+__device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool vec, int nv) {
+    Raw4 r = {{0u, 0u, 0u, 0u}};
+    if (IO == IO_F32) {
+        const uint32_t *p = static_cast<const uint32_t *>(base) + i;
+        if (vec) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+            r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < nv) r.w[j] = __ldg(p + j);
+        }
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + i;
+        if (vec) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            r.w[0] = u.x; r.w[1] = u.y;
+        } else {
+            uint32_t e[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < nv) e[j] = __ldg(p + j);
+            r.w[0] = e[0] | (e[1] << 16);
+            r.w[1] = e[2] | (e[3] << 16);
+        }
+    }
+    return r;
+}
+
+template <int IO>
+__device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
+    if (IO == IO_F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r.w[j]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (IO == IO_BF16) {
+                v[2 * q] = __uint_as_float(r.w[q] << 16);
+                v[2 * q + 1] = __uint_as_float(r.w[q] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[q]));
+                v[2 * q] = f.x; v[2 * q + 1] = f.y;
+            }
+        }
+    }
+}
+
+template <int IO>
+__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, bool vec, int nv, int dt32) {
+    if (IO != IO_F32 && dt32) return load_raw4<IO_F32>(base, i, vec, nv);
+    return load_raw4<IO>(base, i, vec, nv);
+}
+
+template <int IO>
+__device__ __forceinline__ void unpack4_dt(const Raw4 &r, float (&v)[4], int dt32) {
+    if (IO != IO_F32 && dt32) unpack4<IO_F32>(r, v);
+    else unpack4<IO>(r, v);
+}
+
+template <int IO>
+__device__ __forceinline__ void store4_io(void *base, long long i, bool vec, int nv, const float (&v)[4]) {
+    if (!vec) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < nv) st_io<IO>(base, (size_t)(i + j), v[j]);
+        return;
+    }
+    if (IO == IO_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint2 u;
+        if (IO == IO_BF16) {
+            __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+            u.x = *reinterpret_cast<uint32_t *>(&a); u.y = *reinterpret_cast<uint32_t *>(&b);
+        } else {
+            __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+            u.x = *reinterpret_cast<uint32_t *>(&a); u.y = *reinterpret_cast<uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = u;
+    }
+}
+
+// Four fp32 values of a [*,N] row from column n on; zeros past N.
+__device__ __forceinline__ void load_n4(const float *base, long long i, int n, int N, bool vec, float (&v)[4]) {
+    if (vec && n + 4 <= N) {
+        const float4 f = *reinterpret_cast<const float4 *>(base + i);
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = n + j < N ? base[i + j] : 0.f;
+    }
+}
+
+__device__ __forceinline__ void store_n4(float *base, long long i, int n, int N, bool vec, float a, float b, float c,
+                                         float d) {
+    if (vec && n + 4 <= N) {
+        *reinterpret_cast<float4 *>(base + i) = make_float4(a, b, c, d);
+    } else {
+        const float v[4] = {a, b, c, d};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < N) base[i + j] = v[j];
+    }
+}
+
+__device__ __forceinline__ bool aligned_n4(const float *p, int N) {
+    return N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+// Whether four elements from c0 + 4 q on, at any (batch, token), sit on a boundary of four elements.
+template <int IO>
+__device__ __forceinline__ bool vec4_ok(const void *p, const long long (&st)[2], long long c0) {
+    constexpr int kBytes = IO == IO_F32 ? 16 : 8;
+    return (reinterpret_cast<uintptr_t>(p) % kBytes) == 0 && st[0] % 4 == 0 && st[1] % 4 == 0 && c0 % 4 == 0;
+}
+
+template <int IO>
+__device__ __forceinline__ bool vec4_row(const void *p, long long row) {
+    return (reinterpret_cast<uintptr_t>(p) % (IO == IO_F32 ? 16 : 8)) == 0 && row % 4 == 0;
+}
+
+// d_t of one raw step.  softplus(v) = max(v, 0) + log1p(w), w = exp(-|v|) in
+// (0, 1]: log1p(w) = w P(w) with P of degree 8 fitted for the smallest
+// relative error on [0, 1] (1.6e-7 with fp32 evaluation), which keeps the full
+// relative precision of small steps, where log(1 + w) loses it.  w is exp2 of
+// the rounded product |v| log2(e) corrected to first order by the product's
+// rounding error.  sig = d softplus / dv = 1 / (1 + exp(-v)), zero where the clamp is active.
+struct StepOut {
+    float d, sig;
+};
+
+template <bool SIG>
+__device__ __forceinline__ StepOut step_of(float raw, float bias, int softplus, int has_limit, float dmin, float dmax) {
+    StepOut o;
+    const float v = raw + bias;
+    o.sig = 1.f;
+    if (softplus) {
+        const float av = -fminf(fabsf(v), 100.f);  // exp(-100) is 0 in fp32's normal range
+        const float t = av * kLog2e;
+        const float e = fmaf(av, 1.92596299e-8f, fmaf(av, kLog2e, -t));  // log2(e) - fl(log2(e))
+        const float w0 = ex2(t);
+        const float w = fmaf(w0, e * kLn2, w0);
+        float p = 0.005232690833508968f;
+        p = fmaf(p, w, -0.029505228623747826f);
+        p = fmaf(p, w, 0.07822594791650772f);
+        p = fmaf(p, w, -0.13663245737552643f);
+        p = fmaf(p, w, 0.19106008112430573f);
+        p = fmaf(p, w, -0.2484298199415207f);
+        p = fmaf(p, w, 0.3331909775733948f);
+        p = fmaf(p, w, -0.4999949336051941f);
+        p = fmaf(p, w, 0.9999999403953552f);
+        float m;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "f"(0.f));
+        o.d = fmaf(w, p, m);
+        if (SIG) o.sig = __fdividef(v >= 0.f ? 1.f : w, 1.f + w);
+    } else {
+        o.d = v;
+    }
+    if (has_limit) {
+        if (SIG && (o.d < dmin || o.d > dmax)) o.sig = 0.f;
+        o.d = fminf(fmaxf(o.d, dmin), dmax);
+    }
+    return o;
+}
+
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+cudaError_t launch_scan(const ScanParams &p, int io, cudaStream_t s);
+cudaError_t launch_scan_ckpt(const ScanParams &p, int io, cudaStream_t s);
+cudaError_t launch_scan_adjoint(const ScanParams &p, int io, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanParams &p, int io, void *dB, void *dC, float *dA, float *dD, float *dbias,
+                            cudaStream_t s);
+int scan_bwd_tiles(const ScanParams &p);
+int scan_sm_count();
+
+// n-columns are dealt four to a lane: lanes per channel for N states.
+inline int scan_lanes(int64_t N) {
+    int l = 2;
+    while (l * 4 < N) l *= 2;
+    return l;
+}
+
+}  // namespace ssd

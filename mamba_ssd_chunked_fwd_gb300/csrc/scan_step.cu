@@ -1,0 +1,161 @@
+// scan_step.cu -- one token of the selective scan and of its convolution for
+// each of B sequences, from carried states in a pool of slots.
+//
+//   scan:  h' = exp(d A[c,:]) h + d x[c] B,  y[c] = (h' . C + Dskip[c] x[c]) silu(z[c])
+//   conv:  y[c] = silu(bias[c] + sum_k w[c,k] v[k]),  v = (state rows, x);  state' = v[1:]
+//
+// Both read and write their state once and are bound by it: 8 N bytes per
+// channel for the scan, 4 (W-1) bytes for a 16-bit convolution.
+#include "scan_common.cuh"
+
+namespace ssd {
+
+namespace {
+
+// LPC lanes hold a channel's states, four to a lane, so a warp reads and
+// writes 512 consecutive bytes of the state; the LPC lanes' parts of y meet in
+// xor exchanges.  Each lane repeats its channel's softplus: about 30 operations
+// beside 32 bytes of state.  CPT channels per lane, their loads issued
+// together; B and C are loaded once for them.
+constexpr int kStepThreads = 128;
+
+template <int IO, int LPC, int CPT>
+__global__ void __launch_bounds__(kStepThreads)
+scan_step_kernel(ScanStepParams p) {
+    constexpr int kCh = kStepThreads / LPC;  // channels per CTA and round
+    const int b = blockIdx.y;
+    const int ln = threadIdx.x % LPC, n0 = ln * 4;
+    const int cb = blockIdx.x * (kCh * CPT) + threadIdx.x / LPC;
+    const long long slot = p.slots ? __ldg(p.slots + b) : b;
+    const bool live = slot >= 0 && slot < p.nslots;
+    const long long s0 = slot * p.D * p.N;
+    const bool vs = aligned_n4(p.state, p.N) && aligned_n4(p.state_out, p.N), va = aligned_n4(p.A, p.N);
+    const int dg = p.D / p.G;
+    float s[CPT][4], a[CPT][4], x[CPT], raw[CPT], z[CPT], bv[CPT][4], cv[CPT][4];
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+        const int c = cb + k * kCh;
+        if (!live || c >= p.D) continue;
+        load_n4(p.state + s0, (long long)c * p.N + n0, n0, p.N, vs, s[k]);
+        load_n4(p.A, (long long)c * p.N + n0, n0, p.N, va, a[k]);
+        x[k] = ld_io<IO>(p.x, (size_t)(b * p.x_row + c));
+        raw[k] = IO != IO_F32 && p.dt32 ? ld_io<IO_F32>(p.dt, (size_t)(b * p.dt_row + c))
+                                        : ld_io<IO>(p.dt, (size_t)(b * p.dt_row + c));
+        z[k] = p.z ? ld_io<IO>(p.z, (size_t)(b * p.z_row + c)) : 0.f;
+        const long long gn = (long long)(c / dg) * p.N + n0;
+        const bool vb = p.N % 4 == 0;
+        const bool vbb = vb && vec4_row<IO>(p.Bm, p.b_row), vcc = vb && vec4_row<IO>(p.Cm, p.c_row);
+        unpack4<IO>(load_raw4<IO>(p.Bm, b * p.b_row + gn, vbb && n0 < p.N, p.N - n0), bv[k]);
+        unpack4<IO>(load_raw4<IO>(p.Cm, b * p.c_row + gn, vcc && n0 < p.N, p.N - n0), cv[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+        const int c = cb + k * kCh;
+        const bool in = live && c < p.D;
+        float acc = 0.f;
+        if (in) {
+            const float d = step_of<false>(raw[k], p.dt_bias ? __ldg(p.dt_bias + c) : 0.f, p.softplus, p.has_limit,
+                                           p.dt_min, p.dt_max).d;
+            const float dx = d * x[k];
+            float o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = fmaf(ex2(d * (a[k][j] * kLog2e)), s[k][j], dx * bv[k][j]);
+                acc = fmaf(o[j], cv[k][j], acc);
+            }
+            store_n4(p.state_out + s0, (long long)c * p.N + n0, n0, p.N, vs, o[0], o[1], o[2], o[3]);
+        }
+#pragma unroll
+        for (int off = LPC / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        if (ln == 0 && c < p.D) {
+            float y = 0.f;
+            if (live) {
+                y = p.Dskip ? fmaf(__ldg(p.Dskip + c), x[k], acc) : acc;
+                if (p.z) y *= silu_fast(z[k]);
+            }
+            st_io<IO>(p.y, (size_t)b * p.D + c, y);
+        }
+    }
+}
+
+template <int IO, int LPC>
+cudaError_t launch_step_as(const ScanStepParams &p, cudaStream_t s) {
+    constexpr int kCh = kStepThreads / LPC;
+    // Four channels per lane once that still gives every SM eight CTAs: more bytes in flight per lane;
+    // below that one channel per lane spreads the few channels over more SMs.
+    const long long ctas4 = (long long)p.B * ((p.D + 4 * kCh - 1) / (4 * kCh));
+    if (ctas4 >= 8LL * scan_sm_count())
+        scan_step_kernel<IO, LPC, 4><<<dim3((p.D + 4 * kCh - 1) / (4 * kCh), p.B), kStepThreads, 0, s>>>(p);
+    else
+        scan_step_kernel<IO, LPC, 1><<<dim3((p.D + kCh - 1) / kCh, p.B), kStepThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int IO>
+cudaError_t launch_step_io(const ScanStepParams &p, cudaStream_t s) {
+    switch (scan_lanes(p.N)) {
+        case 2: return launch_step_as<IO, 2>(p, s);
+        case 4: return launch_step_as<IO, 4>(p, s);
+        case 8: return launch_step_as<IO, 8>(p, s);
+        case 16: return launch_step_as<IO, 16>(p, s);
+        case 32: return launch_step_as<IO, 32>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// One thread per channel; the W-1 state rows of a sequence are dense, so a
+// warp's accesses are consecutive.
+template <int IO>
+__global__ void __launch_bounds__(256)
+conv_step_kernel(ConvStepParams p) {
+    const int b = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= p.C) return;
+    const long long slot = p.slots ? __ldg(p.slots + b) : b;
+    if (slot < 0 || slot >= p.nslots) {
+        st_io<IO>(p.y, (size_t)b * p.C + c, 0.f);
+        return;
+    }
+    using T = typename IoTraits<IO>::T;
+    const long long s0 = slot * (p.W - 1) * p.C + c;
+    const T *in = static_cast<const T *>(p.state) + s0;
+    T *out = static_cast<T *>(p.state_out) + s0;
+    T v[8];
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (k < p.W - 1) v[k] = in[(long long)k * p.C];
+    const T x = static_cast<const T *>(p.x)[b * p.x_row + c];
+    float acc = p.bias ? __ldg(p.bias + c) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (k < p.W - 1) {
+            acc = fmaf(__ldg(p.w + (long long)c * p.W + k), IoTraits<IO>::to_f(v[k]), acc);
+            if (k > 0) out[(long long)(k - 1) * p.C] = v[k];
+        }
+    acc = fmaf(__ldg(p.w + (long long)c * p.W + p.W - 1), IoTraits<IO>::to_f(x), acc);
+    if (p.W > 1) out[(long long)(p.W - 2) * p.C] = x;
+    st_io<IO>(p.y, (size_t)b * p.C + c, p.silu ? silu_fast(acc) : acc);
+}
+
+}  // namespace
+
+cudaError_t launch_scan_step(const ScanStepParams &p, int io, cudaStream_t s) {
+    switch (io) {
+        case IO_F32: return launch_step_io<IO_F32>(p, s);
+        case IO_F16: return launch_step_io<IO_F16>(p, s);
+        case IO_BF16: return launch_step_io<IO_BF16>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_conv_step(const ConvStepParams &p, int io, cudaStream_t s) {
+    const dim3 grid((p.C + 255) / 256, p.B);
+    switch (io) {
+        case IO_F32: conv_step_kernel<IO_F32><<<grid, 256, 0, s>>>(p); break;
+        case IO_F16: conv_step_kernel<IO_F16><<<grid, 256, 0, s>>>(p); break;
+        case IO_BF16: conv_step_kernel<IO_BF16><<<grid, 256, 0, s>>>(p); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

@@ -1,0 +1,486 @@
+"""Selective scan, its short convolution, and the block norm: Python binding.
+
+Like the rest of the package this only marshals torch tensors into the C ABI of
+``include/ssd.h``: every step runs in ``libssd_gb300.so`` on the current stream
+of the tensors' device, and a bad argument raises ``SsdError`` (from the
+library) or ``ValueError`` (a shape, type or device the binding cannot express).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+_i64, _i32, _f32, _ptr_t, _size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+
+
+class SsdScanArgs(ctypes.Structure):
+    """Mirror of ``ssd_scan_args`` in include/ssd.h."""
+    _fields_ = ([(n, _i64) for n in ("B", "L", "D", "N", "G")]
+                + [(n, _ptr_t) for n in ("x", "dt", "A", "Bm", "Cm", "Dskip", "z", "dt_bias", "initial_state", "lengths",
+                                         "y", "final_state")]
+                + [(n, _i64 * 2) for n in ("x_stride", "dt_stride", "z_stride", "b_stride", "c_stride")]
+                + [("x_dtype", _i32), ("dt_dtype", _i32), ("dt_softplus", _i32), ("dt_min", _f32), ("dt_max", _f32),
+                   ("workspace", _ptr_t), ("workspace_bytes", _size)])
+
+
+class SsdScanBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_scan_bwd_args`` in include/ssd.h."""
+    _fields_ = ([("fwd", SsdScanArgs)]
+                + [(n, _ptr_t) for n in ("dy", "dfinal", "dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0",
+                                         "workspace")]
+                + [("workspace_bytes", _size)])
+
+
+class SsdScanStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_scan_step_args`` in include/ssd.h."""
+    _fields_ = ([(n, _i64) for n in ("B", "D", "N", "G", "nslots")]
+                + [(n, _ptr_t) for n in ("x", "dt", "A", "Bm", "Cm", "Dskip", "z", "dt_bias", "state", "state_out", "slots",
+                                         "y")]
+                + [(n, _i64) for n in ("x_row", "dt_row", "z_row", "b_row", "c_row")]
+                + [("x_dtype", _i32), ("dt_dtype", _i32), ("dt_softplus", _i32), ("dt_min", _f32), ("dt_max", _f32)])
+
+
+class SsdConvArgs(ctypes.Structure):
+    """Mirror of ``ssd_conv_args`` in include/ssd.h."""
+    _fields_ = ([(n, _i64) for n in ("B", "L", "C", "W")] + [("x", _ptr_t), ("x_stride", _i64 * 2)]
+                + [(n, _ptr_t) for n in ("w", "bias", "initial_state", "lengths", "y", "final_state")]
+                + [("dtype", _i32), ("silu", _i32)])
+
+
+class SsdConvBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_conv_bwd_args`` in include/ssd.h."""
+    _fields_ = ([("fwd", SsdConvArgs)] + [(n, _ptr_t) for n in ("dy", "dfinal", "dx", "dw", "dbias", "dh0", "workspace")]
+                + [("workspace_bytes", _size)])
+
+
+class SsdConvStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_conv_step_args`` in include/ssd.h."""
+    _fields_ = ([(n, _i64) for n in ("B", "C", "W", "nslots")] + [("x", _ptr_t), ("x_row", _i64)]
+                + [(n, _ptr_t) for n in ("w", "bias", "state", "state_out", "slots", "y")]
+                + [("dtype", _i32), ("silu", _i32)])
+
+
+class SsdBlockNormArgs(ctypes.Structure):
+    """Mirror of ``ssd_block_norm_args`` in include/ssd.h."""
+    _fields_ = ([(n, _i64) for n in ("rows", "D", "rows_per_gate")]
+                + [(n, _ptr_t) for n in ("o", "r", "gate", "w_post", "w_pre", "scale", "n", "r_out")]
+                + [("dtype", _i32), ("stream_dtype", _i32), ("eps", _f32)])
+
+
+class SsdBlockNormBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_block_norm_bwd_args`` in include/ssd.h."""
+    _fields_ = ([("fwd", SsdBlockNormArgs)]
+                + [(n, _ptr_t) for n in ("dn", "dr_out", "d_o", "dr", "dgate", "dw_post", "dw_pre", "dscale", "workspace")]
+                + [("workspace_bytes", _size)])
+
+
+def _sized(cls):
+    return [ctypes.POINTER(cls), ctypes.POINTER(_size)]
+
+
+def _called(cls):
+    return [ctypes.POINTER(cls), _ptr_t]
+
+
+SIGNATURES = {
+    "ssd_selective_scan_workspace_size": _sized(SsdScanArgs),
+    "ssd_selective_scan": _called(SsdScanArgs),
+    "ssd_selective_scan_bwd_workspace_size": _sized(SsdScanBwdArgs),
+    "ssd_selective_scan_bwd": _called(SsdScanBwdArgs),
+    "ssd_selective_scan_step": _called(SsdScanStepArgs),
+    "ssd_causal_conv_carry": _called(SsdConvArgs),
+    "ssd_causal_conv_bwd_workspace_size": _sized(SsdConvBwdArgs),
+    "ssd_causal_conv_bwd": _called(SsdConvBwdArgs),
+    "ssd_causal_conv_step": _called(SsdConvStepArgs),
+    "ssd_block_norm": _called(SsdBlockNormArgs),
+    "ssd_block_norm_bwd_workspace_size": _sized(SsdBlockNormBwdArgs),
+    "ssd_block_norm_bwd": _called(SsdBlockNormBwdArgs),
+}
+
+_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _host():
+    """The package's loader and error check (imported late: the package imports this module)."""
+    import mamba_ssd_chunked_fwd_gb300 as pkg
+    return pkg
+
+
+def _call(name, args, device):
+    pkg = _host()
+    with torch.cuda.device(device):
+        pkg._check(getattr(pkg.load_library(), name)(ctypes.byref(args), pkg._stream_handle(device)), name)
+
+
+def _bytes(name, args, device):
+    pkg = _host()
+    out = _size(0)
+    with torch.cuda.device(device):
+        pkg._check(getattr(pkg.load_library(), name)(ctypes.byref(args), ctypes.byref(out)), name)
+    return int(out.value)
+
+
+def _work(name, args, device):
+    """Sizes args' workspace by the library's query and allocates it; the tensor must outlive the call."""
+    n = _bytes(name, args, device)
+    ws = torch.empty(max(n, 256), device=device, dtype=torch.uint8)
+    args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
+    return ws
+
+
+def _code(t, what):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _dense(t, shape, dtype, device, what):
+    """The address of a dense tensor of this shape and type, or None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _tokens(t, shape, dtype, device, what):
+    """(address, (batch stride, token stride)) of a [B,L,...] tensor whose tokens are dense."""
+    if t is None:
+        return None, (0, 0)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.numel() and not t[0, 0].is_contiguous():
+        raise ValueError(f"{what}: the values of a token must be contiguous")
+    if t.numel() and any(s < 0 for s in t.stride()):
+        raise ValueError(f"{what}: negative strides")
+    st = [int(t.stride(0)), int(t.stride(1))]
+    if t.shape[0] == 1:
+        st[0] = 0
+    if t.shape[1] == 1:
+        st[1] = 0
+    if st == [0, 0] and (t.shape[0] > 1 or t.shape[1] > 1):
+        raise ValueError(f"{what}: broadcast over every token")
+    return t.data_ptr(), tuple(st)
+
+
+def _rows(t, shape, dtype, device, what):
+    """(address, row stride) of a [B,...] tensor whose rows are dense."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{what}: the values of a row must be contiguous")
+    if t.shape[0] == 1:
+        return t.data_ptr(), 0
+    if t.stride(0) <= 0:
+        raise ValueError(f"{what}: rows must be apart")
+    return t.data_ptr(), int(t.stride(0))
+
+
+def _ndim(t, n, what):
+    if t.dim() != n:
+        raise ValueError(f"{what}: {t.dim()} dimensions, expected {n}")
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} takes CUDA tensors")
+
+
+def _dt_dtype(x, dt, what="dt"):
+    if dt.dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"{what}: dtype {dt.dtype}, expected {x.dtype} or torch.float32")
+    return dt.dtype
+
+
+# ---- selective scan ----------------------------------------------------------
+
+def make_scan_args(x, dt, A, B, C, *, y=None, final_state=None, D=None, z=None, dt_bias=None, initial_states=None,
+                   lengths=None, dt_softplus=False, dt_limit=(0.0, math.inf)) -> SsdScanArgs:
+    """Fill an ``ssd_scan_args`` from tensors (no copies).  x, dt, z [B,L,D] and
+    B, C [B,L,G,N] may be strided over batch and tokens."""
+    _ndim(x, 3, "x"), _ndim(B, 4, "B"), _ndim(A, 2, "A")
+    (Bb, L, Dm), (G, N), dev, f32 = x.shape, B.shape[2:], x.device, torch.float32
+    a = SsdScanArgs()
+    a.B, a.L, a.D, a.N, a.G = Bb, L, Dm, N, G
+    a.x_dtype = _code(x, "x")
+    dtt = _dt_dtype(x, dt)
+    a.dt_dtype = _CODES[dtt]
+    a.x, a.x_stride[:] = _tokens(x, (Bb, L, Dm), x.dtype, dev, "x")
+    a.dt, a.dt_stride[:] = _tokens(dt, (Bb, L, Dm), dtt, dev, "dt")
+    a.z, a.z_stride[:] = _tokens(z, (Bb, L, Dm), x.dtype, dev, "z")
+    a.Bm, a.b_stride[:] = _tokens(B, (Bb, L, G, N), x.dtype, dev, "B")
+    a.Cm, a.c_stride[:] = _tokens(C, (Bb, L, G, N), x.dtype, dev, "C")
+    a.A = _dense(A, (Dm, N), f32, dev, "A")
+    a.Dskip = _dense(D, (Dm,), f32, dev, "D")
+    a.dt_bias = _dense(dt_bias, (Dm,), f32, dev, "dt_bias")
+    a.initial_state = _dense(initial_states, (Bb, Dm, N), f32, dev, "initial_states")
+    a.lengths = _dense(lengths, (Bb,), torch.int32, dev, "lengths")
+    a.y = _dense(y, (Bb, L, Dm), x.dtype, dev, "y")
+    a.final_state = _dense(final_state, (Bb, Dm, N), f32, dev, "final_state")
+    a.dt_softplus = 1 if dt_softplus else 0
+    a.dt_min, a.dt_max = float(dt_limit[0]), float(dt_limit[1])
+    return a
+
+
+def selective_scan(x, dt, A, B, C, dt_softplus=False, return_final_state=False, *, D=None, z=None, dt_bias=None,
+                   dt_limit=(0.0, math.inf), initial_states=None, lengths=None, out=None):
+    """Selective scan over prompts on the GPU: for every channel c of D and state n of N
+
+        h_t = exp(d_t A[c]) h_{t-1} + d_t x_t B_t,   y_t = (h_t . C_t + D x_t) silu(z_t),
+        d_t = clamp(softplus(dt_t + dt_bias))
+
+    Returns y [B,L,D], or (y, final_state [B,D,N] fp32).  x, z [B,L,D] and B, C
+    [B,L,G,N] share a dtype (fp32, fp16, bf16), dt [B,L,D] has it too or is
+    fp32; they may be slices of wider tensors along the last dimension.  A
+    [D,N], D, dt_bias [D] and initial_states [B,D,N] are fp32.  ``lengths``
+    (int32 [B], on the GPU): tokens per row; y is 0 past them."""
+    _cuda(x, "selective_scan")
+    y = out if out is not None else torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    fin = torch.empty((x.shape[0], x.shape[2], A.shape[1]), device=x.device, dtype=torch.float32) if return_final_state else None
+    a = make_scan_args(x, dt, A, B, C, y=y, final_state=fin, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
+                       lengths=lengths, dt_softplus=dt_softplus, dt_limit=dt_limit)
+    ws = _work("ssd_selective_scan_workspace_size", a, x.device)  # noqa: F841
+    _call("ssd_selective_scan", a, x.device)
+    return (y, fin) if return_final_state else y
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, dt_softplus=False, *, dfinal=None, D=None, z=None, dt_bias=None,
+                       dt_limit=(0.0, math.inf), initial_states=None, lengths=None, want_dh0=None):
+    """Gradients of sum(dy * y) + sum(dfinal * final_state) of ``selective_scan``
+    with these inputs.  Returns a dict: dx, ddt, dA, dB, dC and, where the
+    matching input is given, dD, dz, ddt_bias, dh0 (``want_dh0`` overrides the
+    last).  dx, dB, dC, dz have x's dtype, ddt has dt's, the others are fp32."""
+    _cuda(x, "selective_scan_bwd")
+    dev, f32 = x.device, torch.float32
+
+    def like(t):
+        return torch.empty(t.shape, device=dev, dtype=t.dtype)
+
+    a = SsdScanBwdArgs()
+    a.fwd = make_scan_args(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states, lengths=lengths,
+                           dt_softplus=dt_softplus, dt_limit=dt_limit)
+    state = (x.shape[0], x.shape[2], A.shape[1])
+    a.dy = _dense(dy, x.shape, x.dtype, dev, "dy")
+    a.dfinal = _dense(dfinal, state, f32, dev, "dfinal")
+    g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C)}
+    if D is not None:
+        g["dD"] = like(D)
+    if z is not None:
+        g["dz"] = like(z)
+    if dt_bias is not None:
+        g["ddt_bias"] = like(dt_bias)
+    if want_dh0 if want_dh0 is not None else initial_states is not None:
+        g["dh0"] = torch.empty(state, device=dev, dtype=f32)
+    for k, t in g.items():
+        setattr(a, k, t.data_ptr())
+    ws = _work("ssd_selective_scan_bwd_workspace_size", a, dev)  # noqa: F841
+    _call("ssd_selective_scan_bwd", a, dev)
+    return g
+
+
+def selective_scan_step(x, dt, A, B, C, state, dt_softplus=False, *, state_out=None, slots=None, D=None, z=None,
+                        dt_bias=None, dt_limit=(0.0, math.inf), out=None):
+    """One token of the scan for each row: x, dt, z [B,D], B, C [B,G,N]; advances
+    ``state`` [S,D,N] fp32 in place, or into ``state_out``; returns y [B,D].
+    ``slots`` (int32 [B], on the GPU): the row's place in the state pool (default
+    its own index); a row whose slot is outside the pool gives 0 and moves no
+    state.  Rows must not share a slot."""
+    _cuda(x, "selective_scan_step")
+    _ndim(x, 2, "x"), _ndim(B, 3, "B"), _ndim(state, 3, "state"), _ndim(A, 2, "A")
+    (Bb, Dm), (G, N), dev, f32 = x.shape, B.shape[1:], x.device, torch.float32
+    y = out if out is not None else torch.empty(x.shape, device=dev, dtype=x.dtype)
+    a = SsdScanStepArgs()
+    a.B, a.D, a.N, a.G, a.nslots = Bb, Dm, N, G, state.shape[0]
+    a.x_dtype = _code(x, "x")
+    dtt = _dt_dtype(x, dt)
+    a.dt_dtype = _CODES[dtt]
+    a.x, a.x_row = _rows(x, (Bb, Dm), x.dtype, dev, "x")
+    a.dt, a.dt_row = _rows(dt, (Bb, Dm), dtt, dev, "dt")
+    a.z, a.z_row = _rows(z, (Bb, Dm), x.dtype, dev, "z")
+    a.Bm, a.b_row = _rows(B, (Bb, G, N), x.dtype, dev, "B")
+    a.Cm, a.c_row = _rows(C, (Bb, G, N), x.dtype, dev, "C")
+    a.A = _dense(A, (Dm, N), f32, dev, "A")
+    a.Dskip = _dense(D, (Dm,), f32, dev, "D")
+    a.dt_bias = _dense(dt_bias, (Dm,), f32, dev, "dt_bias")
+    pool = (state.shape[0], Dm, N)
+    a.state = _dense(state, pool, f32, dev, "state")
+    a.state_out = _dense(state if state_out is None else state_out, pool, f32, dev, "state_out")
+    a.slots = _dense(slots, (Bb,), torch.int32, dev, "slots")
+    a.y = _dense(y, (Bb, Dm), x.dtype, dev, "out")
+    a.dt_softplus = 1 if dt_softplus else 0
+    a.dt_min, a.dt_max = float(dt_limit[0]), float(dt_limit[1])
+    _call("ssd_selective_scan_step", a, dev)
+    return y
+
+
+# ---- its convolution ---------------------------------------------------------
+
+def make_conv_args(x, w, bias=None, *, y=None, final_state=None, initial_state=None, lengths=None, silu=True) -> SsdConvArgs:
+    """Fill an ``ssd_conv_args`` from tensors (no copies)."""
+    _ndim(x, 3, "x"), _ndim(w, 2, "w")
+    (Bb, L, Cc), W, dev = x.shape, w.shape[1], x.device
+    a = SsdConvArgs()
+    a.B, a.L, a.C, a.W = Bb, L, Cc, W
+    a.dtype = _code(x, "x")
+    a.x, a.x_stride[:] = _tokens(x, (Bb, L, Cc), x.dtype, dev, "x")
+    a.w = _dense(w, (Cc, W), torch.float32, dev, "w")
+    a.bias = _dense(bias, (Cc,), torch.float32, dev, "bias")
+    a.initial_state = _dense(initial_state, (Bb, W - 1, Cc), x.dtype, dev, "initial_state")
+    a.lengths = _dense(lengths, (Bb,), torch.int32, dev, "lengths")
+    a.y = _dense(y, (Bb, L, Cc), x.dtype, dev, "y")
+    a.final_state = _dense(final_state, (Bb, W - 1, Cc), x.dtype, dev, "final_state")
+    a.silu = 1 if silu else 0
+    return a
+
+
+def causal_conv1d_carry(x, w, bias=None, silu=True, *, initial_state=None, lengths=None, return_final_state=False, out=None):
+    """Depthwise causal conv1d over token-major prompts x [B,L,C] (may be strided
+    over batch and tokens), continuing from ``initial_state`` [B,W-1,C] (the
+    inputs before the first token; default zeros), then SiLU.  w [C,W], bias [C]
+    fp32, W <= 8.  Returns y, or (y, final_state [B,W-1,C] in x's dtype);
+    ``lengths`` as in ``selective_scan``."""
+    _cuda(x, "causal_conv1d_carry")
+    y = out if out is not None else torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    fin = torch.empty((x.shape[0], w.shape[1] - 1, x.shape[2]), device=x.device, dtype=x.dtype) if return_final_state else None
+    a = make_conv_args(x, w, bias, y=y, final_state=fin, initial_state=initial_state, lengths=lengths, silu=silu)
+    _call("ssd_causal_conv_carry", a, x.device)
+    return (y, fin) if return_final_state else y
+
+
+def causal_conv1d_bwd(x, w, dy, bias=None, silu=True, *, dfinal=None, initial_state=None, lengths=None, want_dh0=None):
+    """Gradients of sum(dy * y) + sum(dfinal * final_state) of
+    ``causal_conv1d_carry``: a dict of dx, dw, and dbias and dh0 where bias and
+    initial_state are given (``want_dh0`` overrides the last)."""
+    _cuda(x, "causal_conv1d_bwd")
+    dev = x.device
+    a = SsdConvBwdArgs()
+    a.fwd = make_conv_args(x, w, bias, initial_state=initial_state, lengths=lengths, silu=silu)
+    state = (x.shape[0], w.shape[1] - 1, x.shape[2])
+    a.dy = _dense(dy, x.shape, x.dtype, dev, "dy")
+    a.dfinal = _dense(dfinal, state, x.dtype, dev, "dfinal")
+    g = {"dx": torch.empty(x.shape, device=dev, dtype=x.dtype), "dw": torch.empty_like(w)}
+    if bias is not None:
+        g["dbias"] = torch.empty_like(bias)
+    if want_dh0 if want_dh0 is not None else initial_state is not None:
+        g["dh0"] = torch.empty(state, device=dev, dtype=x.dtype)
+    for k, t in g.items():
+        setattr(a, k, t.data_ptr())
+    ws = _work("ssd_causal_conv_bwd_workspace_size", a, dev)  # noqa: F841
+    _call("ssd_causal_conv_bwd", a, dev)
+    return g
+
+
+def causal_conv1d_step(x, state, w, bias=None, silu=True, *, state_out=None, slots=None, out=None):
+    """One token of the convolution for each row: x [B,C]; advances ``state``
+    [S,W-1,C] (x's dtype) in place, or into ``state_out``; returns y [B,C].
+    ``slots`` as in ``selective_scan_step``."""
+    _cuda(x, "causal_conv1d_step")
+    _ndim(x, 2, "x"), _ndim(w, 2, "w"), _ndim(state, 3, "state")
+    (Bb, Cc), W, dev = x.shape, w.shape[1], x.device
+    y = out if out is not None else torch.empty(x.shape, device=dev, dtype=x.dtype)
+    a = SsdConvStepArgs()
+    a.B, a.C, a.W, a.nslots = Bb, Cc, W, state.shape[0]
+    a.dtype = _code(x, "x")
+    a.x, a.x_row = _rows(x, (Bb, Cc), x.dtype, dev, "x")
+    a.w = _dense(w, (Cc, W), torch.float32, dev, "w")
+    a.bias = _dense(bias, (Cc,), torch.float32, dev, "bias")
+    pool = (state.shape[0], W - 1, Cc)
+    a.state = _dense(state, pool, x.dtype, dev, "state")
+    a.state_out = _dense(state if state_out is None else state_out, pool, x.dtype, dev, "state_out")
+    a.slots = _dense(slots, (Bb,), torch.int32, dev, "slots")
+    a.y = _dense(y, (Bb, Cc), x.dtype, dev, "out")
+    a.silu = 1 if silu else 0
+    _call("ssd_causal_conv_step", a, dev)
+    return y
+
+
+# ---- block norm --------------------------------------------------------------
+
+def _norm_args(o, r, w_pre, w_post, gate, scale, eps, like):
+    """The shared part; ``like`` is a tensor of o's shape and dtype."""
+    if r.dim() < 1:
+        raise ValueError("r: at least one dimension")
+    D, dev, f32 = r.shape[-1], r.device, torch.float32
+    rows = r.numel() // max(D, 1)
+    a = SsdBlockNormArgs()
+    a.rows, a.D, a.rows_per_gate = rows, D, 1
+    a.dtype, a.stream_dtype = _code(like, "o"), _code(r, "r")
+    a.o = _dense(o, r.shape, like.dtype, dev, "o")
+    if gate is not None:
+        lead = 1
+        if tuple(gate.shape) != tuple(r.shape):  # [B, D] for [B, ..., D]
+            if gate.dim() != 2 or r.dim() < 2 or gate.shape != (r.shape[0], D):
+                raise ValueError(f"gate: shape {tuple(gate.shape)}, expected {tuple(r.shape)} or {(r.shape[0], D)}")
+            lead = rows // max(r.shape[0], 1)
+        a.rows_per_gate = lead
+        a.gate = _dense(gate, gate.shape, like.dtype, dev, "gate")
+    a.w_post = _dense(w_post, (D,), f32, dev, "w_post")
+    a.w_pre = _dense(w_pre, (D,), f32, dev, "w_pre")
+    a.scale = _dense(scale, (D,), f32, dev, "scale")
+    a.eps = float(eps)
+    return a
+
+
+def block_norm(o, r, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5, dtype=None, out=None, r_out=None):
+    """The end of one block and the norm before the next:
+
+        r' = r + scale * gate * (o / rms(o) * w_post),   n = r' / rms(r') * w_pre
+
+    Returns (n, r').  o [..., D] (None: only the norm of r, in ``dtype`` or r's);
+    the residual stream r has o's dtype or fp32; gate, in o's dtype, has o's
+    shape or is [B, D] for o [B, ..., D]; w_post (None: o is added as it is),
+    w_pre and scale [D] fp32.  ``r_out`` may be r itself."""
+    _cuda(r, "block_norm")
+    like = o if o is not None else torch.empty(0, device=r.device, dtype=dtype or r.dtype)
+    a = _norm_args(o, r, w_pre, w_post, gate, scale, eps, like)
+    n = out if out is not None else torch.empty(r.shape, device=r.device, dtype=like.dtype)
+    a.r = _dense(r, r.shape, r.dtype, r.device, "r")
+    a.n = _dense(n, r.shape, like.dtype, r.device, "out")
+    if o is not None:
+        r_out = r_out if r_out is not None else torch.empty_like(r)
+        a.r_out = _dense(r_out, r.shape, r.dtype, r.device, "r_out")
+    _call("ssd_block_norm", a, r.device)
+    return n, (r_out if o is not None else r)
+
+
+def block_norm_bwd(dn, dr_out, o, r_out, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5):
+    """Gradients of sum(dn * n) + sum(dr_out * r') of ``block_norm`` from its
+    stored r' (``r_out``): a dict of dr, dw_pre, and with o also do, and dw_post,
+    dgate, dscale where those inputs are given.  ``dr_out`` may be None."""
+    _cuda(dn, "block_norm_bwd")
+    dev = dn.device
+    a = SsdBlockNormBwdArgs()
+    a.fwd = _norm_args(o, r_out, w_pre, w_post, gate, scale, eps, dn)
+    a.fwd.r_out = _dense(r_out, r_out.shape, r_out.dtype, dev, "r_out")
+    a.dn = _dense(dn, r_out.shape, dn.dtype, dev, "dn")
+    a.dr_out = _dense(dr_out, r_out.shape, r_out.dtype, dev, "dr_out")
+    g = {"dr": torch.empty_like(r_out), "dw_pre": torch.empty_like(w_pre)}
+    if o is not None:
+        g["do"] = torch.empty_like(o)
+    for name, t in (("dw_post", w_post), ("dgate", gate), ("dscale", scale)):
+        if t is not None:
+            g[name] = torch.empty_like(t)
+    for k, t in g.items():
+        setattr(a, "d_o" if k == "do" else k, t.data_ptr())
+    ws = _work("ssd_block_norm_bwd_workspace_size", a, dev)  # noqa: F841
+    _call("ssd_block_norm_bwd", a, dev)
+    return g
