@@ -47,9 +47,9 @@ __device__ __forceinline__ float round_io(float v) {
     return IoTraits<SIO>::to_f(IoTraits<SIO>::from_f(v));
 }
 
-template <int IO, int SIO, int K>
+template <int IO, int SIO, int K, bool VEC>
 __global__ void __launch_bounds__(K <= 2 ? 256 : 512)
-block_norm_kernel(BlockNormParams p, int vec) {
+block_norm_kernel(BlockNormParams p) {
     __shared__ float red[2][1][32];
     const int tpr = blockDim.x;
     float wp[K][4], ws[K][4];  // w_pre; scale w_post
@@ -70,11 +70,9 @@ block_norm_kernel(BlockNormParams p, int vec) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            if (nv > 0) {
-                rr[k] = load_raw4<SIO>(p.r, base + c, vec, nv);
-                if (p.o) ro[k] = load_raw4<IO>(p.o, base + c, vec, nv);
-                if (p.gate) rg[k] = load_raw4<IO>(p.gate, gbase + c, vec, nv);
-            }
+            rr[k] = load_raw4<SIO, VEC, false>(p.r, base + c, nv > 0, nv);
+            ro[k] = load_raw4<IO, VEC>(p.o, base + c, nv > 0 && p.o, nv);
+            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, nv > 0 && p.gate, nv);
         }
         float inv = 1.f;
         if (p.o && p.w_post) {
@@ -83,7 +81,7 @@ block_norm_kernel(BlockNormParams p, int vec) {
             for (int k = 0; k < K; ++k)
                 if ((threadIdx.x + tpr * k) * 4 < p.D) {
                     float o[4];
-                    unpack4<IO>(ro[k], o);
+                    unpack4<IO, VEC>(ro[k], o);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) ss[0] = fmaf(o[j], o[j], ss[0]);
                 }
@@ -95,14 +93,14 @@ block_norm_kernel(BlockNormParams p, int vec) {
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
             if (nv <= 0) continue;
-            unpack4<SIO>(rr[k], r[k]);
+            unpack4<SIO, VEC>(rr[k], r[k]);
             if (p.o) {
                 float o[4], g[4] = {1.f, 1.f, 1.f, 1.f};
-                unpack4<IO>(ro[k], o);
-                if (p.gate) unpack4<IO>(rg[k], g);
+                unpack4<IO, VEC>(ro[k], o);
+                if (p.gate) unpack4<IO, VEC>(rg[k], g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[k][j] = round_io<SIO>(fmaf(g[j] * ws[k][j], o[j] * inv, r[k][j]));
-                store4_io<SIO>(p.r_out, base + c, vec, nv, r[k]);
+                store4_io<SIO, VEC>(p.r_out, base + c, nv, r[k]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) ss[0] = j < nv ? fmaf(r[k][j], r[k][j], ss[0]) : ss[0];
@@ -116,15 +114,15 @@ block_norm_kernel(BlockNormParams p, int vec) {
             float n[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) n[j] = r[k][j] * inv2 * wp[k][j];
-            store4_io<IO>(p.n, base + c, vec, nv, n);
+            store4_io<IO, VEC>(p.n, base + c, nv, n);
         }
         if (!(p.o && p.w_post) && blockDim.x > 32) __syncthreads();  // one reduction per row only: its slot is free again
     }
 }
 
-template <int IO, int SIO, int K>
+template <int IO, int SIO, int K, bool VEC>
 __global__ void __launch_bounds__(512, 1)
-block_norm_bwd_kernel(BlockNormParams p, int vec) {
+block_norm_bwd_kernel(BlockNormParams p) {
     __shared__ float red[2][3][32];
     const int tpr = blockDim.x;
     const long long chunk = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -156,24 +154,20 @@ block_norm_bwd_kernel(BlockNormParams p, int vec) {
         Raw4 ro[K], rr[K], rg[K], rn[K], rd[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Raw4 zero = {{0u, 0u, 0u, 0u}};
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            ro[k] = rr[k] = rg[k] = rn[k] = rd[k] = zero;
-            if (nv > 0) {
-                rr[k] = load_raw4<SIO>(p.r_out, base + c, vec, nv);
-                rn[k] = load_raw4<IO>(p.dn, base + c, vec, nv);
-                if (p.dr_out) rd[k] = load_raw4<SIO>(p.dr_out, base + c, vec, nv);
-                if (p.o) ro[k] = load_raw4<IO>(p.o, base + c, vec, nv);
-                if (p.gate) rg[k] = load_raw4<IO>(p.gate, gbase + c, vec, nv);
-            }
+            rr[k] = load_raw4<SIO, VEC>(p.r_out, base + c, nv > 0, nv);
+            rn[k] = load_raw4<IO, VEC>(p.dn, base + c, nv > 0, nv);
+            rd[k] = load_raw4<SIO, VEC>(p.dr_out, base + c, nv > 0 && p.dr_out, nv);
+            ro[k] = load_raw4<IO, VEC>(p.o, base + c, nv > 0 && p.o, nv);
+            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, nv > 0 && p.gate, nv);
         }
         float s[3] = {0.f, 0.f, 0.f};  // |r'|^2, dn w_pre . r', |o|^2
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float r[4], n[4], o[4];
-            unpack4<SIO>(rr[k], r);
-            unpack4<IO>(rn[k], n);
-            unpack4<IO>(ro[k], o);
+            unpack4<SIO, VEC>(rr[k], r);
+            unpack4<IO, VEC>(rn[k], n);
+            unpack4<IO, VEC>(ro[k], o);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[0] = fmaf(r[j], r[j], s[0]);
@@ -187,9 +181,9 @@ block_norm_bwd_kernel(BlockNormParams p, int vec) {
         // dr of four elements: (v - r' inv2^2 mean(v r')) inv2 + dr_out
         auto dr_of = [&](int k, float (&dr)[4]) {
             float r[4], n[4];
-            unpack4<SIO>(rr[k], r);
-            unpack4<IO>(rn[k], n);
-            unpack4<SIO>(rd[k], dr);
+            unpack4<SIO, VEC>(rr[k], r);
+            unpack4<IO, VEC>(rn[k], n);
+            unpack4<SIO, VEC>(rd[k], dr);
 #pragma unroll
             for (int j = 0; j < 4; ++j) dr[j] = fmaf(fmaf(-r[j], m2, n[j] * wp[k][j]), inv2, dr[j]);
         };
@@ -200,15 +194,15 @@ block_norm_bwd_kernel(BlockNormParams p, int vec) {
             if (nv <= 0) continue;
             float dr[4], r[4], n[4];
             dr_of(k, dr);
-            unpack4<SIO>(rr[k], r);
-            unpack4<IO>(rn[k], n);
-            store4_io<SIO>(p.dr, base + c, vec, nv, dr);
+            unpack4<SIO, VEC>(rr[k], r);
+            unpack4<IO, VEC>(rn[k], n);
+            store4_io<SIO, VEC>(p.dr, base + c, nv, dr);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc2[k][j] = fmaf(n[j], r[j] * inv2, acc2[k][j]);
             if (!p.o) continue;
             float o[4], g[4] = {1.f, 1.f, 1.f, 1.f}, dg[4];
-            unpack4<IO>(ro[k], o);
-            if (p.gate) unpack4<IO>(rg[k], g);
+            unpack4<IO, VEC>(ro[k], o);
+            if (p.gate) unpack4<IO, VEC>(rg[k], g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float dh = dr[j] * (o[j] * inv);  // dr hat_o
@@ -216,7 +210,7 @@ block_norm_bwd_kernel(BlockNormParams p, int vec) {
                 t[0] = fmaf(g[j] * dr[j] * ws[k][j], o[j], t[0]);
                 acc1[k][j] += seq_gate ? dh : dh * g[j];
             }
-            if (p.gate && !seq_gate) store4_io<IO>(p.dgate, base + c, vec, nv, dg);
+            if (p.gate && !seq_gate) store4_io<IO, VEC>(p.dgate, base + c, nv, dg);
         }
         if (!p.o) {
             if (blockDim.x > 32) __syncthreads();  // the slot is free again
@@ -230,11 +224,11 @@ block_norm_bwd_kernel(BlockNormParams p, int vec) {
             if (nv <= 0) continue;
             float dr[4], o[4], g[4] = {1.f, 1.f, 1.f, 1.f};
             dr_of(k, dr);
-            unpack4<IO>(ro[k], o);
-            if (p.gate) unpack4<IO>(rg[k], g);
+            unpack4<IO, VEC>(ro[k], o);
+            if (p.gate) unpack4<IO, VEC>(rg[k], g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = fmaf(-o[j], m, g[j] * dr[j] * ws[k][j]) * inv;
-            store4_io<IO>(p.d_o, base + c, vec, nv, o);
+            store4_io<IO, VEC>(p.d_o, base + c, nv, o);
         }
     }
     float *part = p.part + chunk * 2 * p.D;
@@ -304,32 +298,33 @@ bool norm_vec(const BlockNormParams &p, int io, int sio) {
 }
 
 template <int IO, int SIO, int K>
-cudaError_t launch_norm_as(const BlockNormParams &p, int vec, cudaStream_t s) {
+cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
+    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_kernel<IO, SIO, K, true> : block_norm_kernel<IO, SIO, K, false>;
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block_norm_kernel<IO, SIO, K>, block.x * block.y, 0) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block.x * block.y, 0) !=
             cudaSuccess || per_sm < 1) {
         (void)cudaGetLastError();
         per_sm = 1;
     }
     const long long need = (p.rows + block.y - 1) / block.y, most = (long long)scan_sm_count() * per_sm;
-    block_norm_kernel<IO, SIO, K><<<(unsigned)(need < most ? need : most), block, 0, s>>>(p, vec);
+    kernel<<<(unsigned)(need < most ? need : most), block, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int IO, int SIO>
-cudaError_t launch_norm_io(const BlockNormParams &p, int io, int sio, cudaStream_t s) {
-    const int vec = norm_vec(p, io, sio);
-    if (p.D <= 128) return launch_norm_as<IO, SIO, 1>(p, vec, s);
-    if (p.D <= 2048) return launch_norm_as<IO, SIO, 2>(p, vec, s);
-    if (p.D <= 8192) return launch_norm_as<IO, SIO, 4>(p, vec, s);
-    return launch_norm_as<IO, SIO, 8>(p, vec, s);
+cudaError_t launch_norm_io(const BlockNormParams &p, cudaStream_t s) {
+    if (p.D <= 128) return launch_norm_as<IO, SIO, 1>(p, s);
+    if (p.D <= 2048) return launch_norm_as<IO, SIO, 2>(p, s);
+    if (p.D <= 8192) return launch_norm_as<IO, SIO, 4>(p, s);
+    return launch_norm_as<IO, SIO, 8>(p, s);
 }
 
 template <int IO, int SIO, int K>
-cudaError_t launch_norm_bwd_as(const BlockNormParams &p, int vec, cudaStream_t s) {
+cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
-    block_norm_bwd_kernel<IO, SIO, K><<<(unsigned)((p.chunks + block.y - 1) / block.y), block, 0, s>>>(p, vec);
+    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_bwd_kernel<IO, SIO, K, true> : block_norm_bwd_kernel<IO, SIO, K, false>;
+    kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     block_norm_sum_kernel<IO><<<(p.D + 31) / 32, dim3(32, 32), 0, s>>>(p);
@@ -337,12 +332,11 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, int vec, cudaStream_t s
 }
 
 template <int IO, int SIO>
-cudaError_t launch_norm_bwd_io(const BlockNormParams &p, int io, int sio, cudaStream_t s) {
-    const int vec = norm_vec(p, io, sio);
-    if (p.D <= 128) return launch_norm_bwd_as<IO, SIO, 1>(p, vec, s);
-    if (p.D <= 4096) return launch_norm_bwd_as<IO, SIO, 2>(p, vec, s);
-    if (p.D <= 8192) return launch_norm_bwd_as<IO, SIO, 4>(p, vec, s);
-    return launch_norm_bwd_as<IO, SIO, 8>(p, vec, s);
+cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
+    if (p.D <= 128) return launch_norm_bwd_as<IO, SIO, 1>(p, s);
+    if (p.D <= 4096) return launch_norm_bwd_as<IO, SIO, 2>(p, s);
+    if (p.D <= 8192) return launch_norm_bwd_as<IO, SIO, 4>(p, s);
+    return launch_norm_bwd_as<IO, SIO, 8>(p, s);
 }
 
 }  // namespace
@@ -359,11 +353,11 @@ void block_norm_chunks(BlockNormParams &p) {
 }
 
 #define SSD_NORM_DISPATCH(FN)                                                     \
-    if (io == IO_F32 && sio == IO_F32) return FN<IO_F32, IO_F32>(p, io, sio, s);  \
-    if (io == IO_F16 && sio == IO_F16) return FN<IO_F16, IO_F16>(p, io, sio, s);  \
-    if (io == IO_F16 && sio == IO_F32) return FN<IO_F16, IO_F32>(p, io, sio, s);  \
-    if (io == IO_BF16 && sio == IO_BF16) return FN<IO_BF16, IO_BF16>(p, io, sio, s); \
-    if (io == IO_BF16 && sio == IO_F32) return FN<IO_BF16, IO_F32>(p, io, sio, s); \
+    if (io == IO_F32 && sio == IO_F32) return FN<IO_F32, IO_F32>(p, s);  \
+    if (io == IO_F16 && sio == IO_F16) return FN<IO_F16, IO_F16>(p, s);  \
+    if (io == IO_F16 && sio == IO_F32) return FN<IO_F16, IO_F32>(p, s);  \
+    if (io == IO_BF16 && sio == IO_BF16) return FN<IO_BF16, IO_BF16>(p, s); \
+    if (io == IO_BF16 && sio == IO_F32) return FN<IO_BF16, IO_F32>(p, s); \
     return cudaErrorInvalidValue;
 
 cudaError_t launch_block_norm(const BlockNormParams &p, int io, int sio, cudaStream_t s) {

@@ -21,15 +21,12 @@ constexpr int kCtaTokens = kCy * kRun;
 constexpr int kAhead = 8;
 
 // v at token t as loaded: x inside the row, the carried rows before it, zeros elsewhere.
-template <int IO>
-__device__ __forceinline__ Raw4 conv_value(const ConvParams &p, int b, long long t, int len, int c, bool vx, bool vh,
-                                           int nv) {
-    if (t >= 0) {
-        if (t < len) return load_raw4<IO>(p.x, b * p.xs[0] + t * p.xs[1] + c, vx, nv);
-    } else if (p.h0 && t >= -(long long)(p.W - 1)) {
-        return load_raw4<IO>(p.h0, ((long long)b * (p.W - 1) + t + p.W - 1) * p.C + c, vh, nv);
-    }
-    return Raw4{{0u, 0u, 0u, 0u}};
+template <int IO, bool VEC>
+__device__ __forceinline__ Raw4 conv_value(const ConvParams &p, int b, long long t, int len, int c, int nv) {
+    const bool carried = t < 0;
+    const void *base = carried ? p.h0 : p.x;
+    const long long i = carried ? ((long long)b * (p.W - 1) + t + p.W - 1) * p.C + c : b * p.xs[0] + t * p.xs[1] + c;
+    return load_raw4<IO, VEC>(base, i, carried ? p.h0 && t >= -(long long)(p.W - 1) : t < len, nv);
 }
 
 // Taps sit right-aligned in KT slots (slot KT-1 is the current token), so every index is a constant.
@@ -46,39 +43,34 @@ __device__ __forceinline__ void load_taps(const ConvParams &p, int c, int nv, fl
     }
 }
 
-template <int IO, int KT>
+template <int IO, int KT, bool VEC>
 __global__ void __launch_bounds__(kCx * kCy)
 conv_carry_kernel(ConvParams p) {
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     if (c >= p.C) return;
     const int nv = min(4, p.C - c), b = blockIdx.z;
     const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
-    const long long dense[2] = {0, p.C};
-    const bool full = nv == 4;
-    const bool vx = full && vec4_ok<IO>(p.x, p.xs, c), vh = full && vec4_ok<IO>(p.h0, dense, c);
     if (blockIdx.y == gridDim.y - 1) {  // the last W-1 entries of v
         if (!p.final_state) return;
-        const bool vf = full && vec4_ok<IO>(p.final_state, dense, c);
         for (int j = threadIdx.y; j < p.W - 1; j += kCy) {
             float v[4];
-            unpack4<IO>(conv_value<IO>(p, b, (long long)len + j - (p.W - 1), len, c, vx, vh, nv), v);
-            store4_io<IO>(p.final_state, ((long long)b * (p.W - 1) + j) * p.C + c, vf, nv, v);
+            unpack4<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)len + j - (p.W - 1), len, c, nv), v);
+            store4_io<IO, VEC>(p.final_state, ((long long)b * (p.W - 1) + j) * p.C + c, nv, v);
         }
         return;
     }
-    const bool vy = full && vec4_ok<IO>(p.y, dense, c);
     const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
     if (t0 >= t1) return;
     float w[KT][4], bias[4], win[KT][4];
     load_taps<KT>(p, c, nv, w, bias);
 #pragma unroll
     for (int s = 1; s < KT; ++s)  // slots 0..KT-2 of the first step are tokens t0-KT+1 .. t0-1
-        unpack4<IO>(conv_value<IO>(p, b, (long long)t0 - KT + s, len, c, vx, vh, nv), win[s]);
+        unpack4<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
     for (int t = t0; t < t1; t += kAhead) {
         Raw4 r[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (t + i < t1) r[i] = conv_value<IO>(p, b, t + i, len, c, vx, vh, nv);
+            r[i] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + (t + i) * p.xs[1] + c, t + i < min(t1, len), nv);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (t + i >= t1) break;
@@ -87,7 +79,7 @@ conv_carry_kernel(ConvParams p) {
             for (int s = 0; s < KT - 1; ++s)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) win[s][j] = win[s + 1][j];
-            unpack4<IO>(r[i], win[KT - 1]);
+            unpack4<IO, VEC>(r[i], win[KT - 1]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float a = bias[j];
@@ -96,7 +88,7 @@ conv_carry_kernel(ConvParams p) {
                 if (p.silu) a = silu_fast(a);
                 o[j] = t + i < len ? a : 0.f;
             }
-            store4_io<IO>(p.y, ((long long)b * p.L + t + i) * p.C + c, vy, nv, o);
+            store4_io<IO, VEC>(p.y, ((long long)b * p.L + t + i) * p.C + c, nv, o);
         }
     }
 }
@@ -105,15 +97,13 @@ conv_carry_kernel(ConvParams p) {
 // reaches back into the run), recomputing pre from the window.  dw and dbias gather in
 // registers over the run, then over the CTA's runs in shared memory in a fixed
 // order, and leave as one row of partial sums per CTA.
-template <int IO, int KT>
+template <int IO, int KT, bool VEC>
 __global__ void __launch_bounds__(kCx * kCy)
 conv_bwd_kernel(ConvParams p) {
     __shared__ float red[kCy][kCx * 4];
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     const int nv = min(4, p.C - c), b = blockIdx.z;
     const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
-    const long long dense[2] = {0, p.C};
-    const bool full = nv == 4;
     const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
     float dw[KT][4], db[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -121,14 +111,11 @@ conv_bwd_kernel(ConvParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) dw[s][j] = 0.f;
     if (c < p.C && t0 < t1) {
-        const bool vx = full && vec4_ok<IO>(p.x, p.xs, c), vh = full && vec4_ok<IO>(p.h0, dense, c);
-        const bool vdy = full && vec4_ok<IO>(p.dy, dense, c), vdx = full && vec4_ok<IO>(p.dx, dense, c);
-        const bool vf = full && vec4_ok<IO>(p.dfinal, dense, c), vdh = full && vec4_ok<IO>(p.dh0, dense, c);
         float w[KT][4], bias[4], win[KT][4], dp[KT][4];  // dp[i]: of token t - i
         load_taps<KT>(p, c, nv, w, bias);
 #pragma unroll
         for (int s = 1; s < KT; ++s)
-            unpack4<IO>(conv_value<IO>(p, b, (long long)t0 - KT + s, len, c, vx, vh, nv), win[s]);
+            unpack4<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
 #pragma unroll
         for (int s = 0; s < KT; ++s)
 #pragma unroll
@@ -138,12 +125,9 @@ conv_bwd_kernel(ConvParams p) {
             Raw4 r[kAhead], rg[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                rg[i] = Raw4{{0u, 0u, 0u, 0u}};
-                r[i] = Raw4{{0u, 0u, 0u, 0u}};
-                if (t + i < tend && t + i < len) {
-                    r[i] = conv_value<IO>(p, b, t + i, len, c, vx, vh, nv);
-                    rg[i] = load_raw4<IO>(p.dy, ((long long)b * p.L + t + i) * p.C + c, vdy, nv);
-                }
+                const bool ok = t + i < min(tend, len);
+                r[i] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + (t + i) * p.xs[1] + c, ok, nv);
+                rg[i] = load_raw4<IO, VEC>(p.dy, ((long long)b * p.L + t + i) * p.C + c, ok, nv);
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
@@ -157,9 +141,9 @@ conv_bwd_kernel(ConvParams p) {
                 for (int s = KT - 1; s > 0; --s)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) dp[s][j] = dp[s - 1][j];
-                unpack4<IO>(r[i], win[KT - 1]);
+                unpack4<IO, VEC>(r[i], win[KT - 1]);
                 float g[4], o[4];
-                unpack4<IO>(rg[i], g);
+                unpack4<IO, VEC>(rg[i], g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (p.silu) {
@@ -183,16 +167,16 @@ conv_bwd_kernel(ConvParams p) {
                 const int tau = tt - (KT - 1);  // the entry of v this step completes
                 if (tau >= len - (p.W - 1) && tau < len && p.dfinal) {
                     float f[4];
-                    unpack4<IO>(load_raw4<IO>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, vf, nv), f);
+                    unpack4<IO, VEC>(load_raw4<IO, VEC>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, true, nv), f);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[j] += f[j];
                 }
                 if (tau < 0) {
                     if (t0 == 0 && p.dh0 && tau >= -(p.W - 1))
-                        store4_io<IO>(p.dh0, ((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c, vdh, nv, o);
+                        store4_io<IO, VEC>(p.dh0, ((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c, nv, o);
                 } else if (tau >= t0) {
                     if (tau >= len) o[0] = o[1] = o[2] = o[3] = 0.f;
-                    store4_io<IO>(p.dx, ((long long)b * p.L + tau) * p.C + c, vdx, nv, o);
+                    store4_io<IO, VEC>(p.dx, ((long long)b * p.L + tau) * p.C + c, nv, o);
                 }
             }
         }
@@ -232,19 +216,30 @@ conv_bwd_sum_kernel(ConvParams p, int rows) {
     else if (p.dbias) p.dbias[c] = a;
 }
 
+// Whether every tensor moves in aligned groups of four channels (absent ones do).
+bool conv_vec(const ConvParams &p, int io) {
+    bool ok = p.C % 4 == 0 && vec4_strided(p.x, io, p.xs);
+    for (const void *q : {p.h0, (const void *)p.y, (const void *)p.final_state, p.dy, p.dfinal, (const void *)p.dx,
+                          (const void *)p.dh0})
+        ok = ok && vec4_aligned(q, io);
+    return ok;
+}
+
 template <int IO>
 cudaError_t launch_conv_io(const ConvParams &p, cudaStream_t s) {
     const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens + 1, p.B);
-    if (p.W <= 4) conv_carry_kernel<IO, 4><<<grid, dim3(kCx, kCy), 0, s>>>(p);
-    else conv_carry_kernel<IO, 8><<<grid, dim3(kCx, kCy), 0, s>>>(p);
+    auto *kernel = conv_vec(p, IO) ? (p.W <= 4 ? conv_carry_kernel<IO, 4, true> : conv_carry_kernel<IO, 8, true>)
+                                   : (p.W <= 4 ? conv_carry_kernel<IO, 4, false> : conv_carry_kernel<IO, 8, false>);
+    kernel<<<grid, dim3(kCx, kCy), 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int IO>
 cudaError_t launch_conv_bwd_io(const ConvParams &p, cudaStream_t s) {
     const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens, p.B);
-    if (p.W <= 4) conv_bwd_kernel<IO, 4><<<grid, dim3(kCx, kCy), 0, s>>>(p);
-    else conv_bwd_kernel<IO, 8><<<grid, dim3(kCx, kCy), 0, s>>>(p);
+    auto *kernel = conv_vec(p, IO) ? (p.W <= 4 ? conv_bwd_kernel<IO, 4, true> : conv_bwd_kernel<IO, 8, true>)
+                                   : (p.W <= 4 ? conv_bwd_kernel<IO, 4, false> : conv_bwd_kernel<IO, 8, false>);
+    kernel<<<grid, dim3(kCx, kCy), 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     conv_bwd_sum_kernel<<<dim3((p.C + 31) / 32, p.W + 1), dim3(32, 8), 0, s>>>(p, (int)conv_bwd_part_rows(p.B, p.L, p.C));

@@ -115,49 +115,106 @@ __device__ __forceinline__ float ex2(float v) {
 // Two fp32 numbers in one register pair; a packed operation takes one issue
 // slot for both.
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
+
+// exp(d A) from A log2(e): ex2.approx is low by 0.5 to 3e-8 on average for the
+// exponents of a slow decay (measured over [-0.5, -1e-5]), and a state that
+// remembers a thousand tokens multiplies that.  2.4e-8 added to the exponent
+// centres the result (mean error within 1.2e-8 there, the conversion's own
+// rounding being 3e-8); d = 0 still gives exactly 1.
+constexpr float kDecayCentre = 2.4e-8f;
+__device__ __forceinline__ float2 decay2(float2 d, float2 a2) {
+    const float2 v = __ffma2_rn(d, a2, make_float2(kDecayCentre, kDecayCentre));
+    return make_float2(ex2(v.x), ex2(v.y));
+}
 
 // Four consecutive elements as loaded, 8 bytes (16-bit types) or 16.
 struct Raw4 {
     uint32_t w[4];
 };
 
-// vec: the address is aligned to the four elements and all four exist; else nv of them, one by one.
-template <int IO>
-__device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool vec, int nv) {
+// Predicated loads: a branch around a load (or a choice between two) would make
+// the compiler wait for its data where the paths meet again, one latency per
+// load; a predicated load leaves them all in flight.  What is not loaded stays as it was.
+__device__ __forceinline__ void ldg_v4(uint32_t (&w)[4], const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void ldg_v2(uint32_t (&w)[4], const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"((uint32_t)ok));
+}
+// Without the read-only path: tensors that the same thread writes later (updates in place).
+__device__ __forceinline__ void ld_v4(uint32_t (&w)[4], const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"((uint32_t)ok) : "memory");
+}
+__device__ __forceinline__ void ld_v2(uint32_t (&w)[4], const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"((uint32_t)ok) : "memory");
+}
+__device__ __forceinline__ void ld_u32(uint32_t &w, const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
+                 : "+r"(w) : "l"(p), "r"((uint32_t)ok) : "memory");
+}
+__device__ __forceinline__ void ld_u16(uint16_t &w, const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
+                 : "+h"(w) : "l"(p), "r"((uint32_t)ok) : "memory");
+}
+__device__ __forceinline__ void ldg_u32(uint32_t &w, const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(w) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void ldg_u16(uint16_t &w, const void *p, bool ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "+h"(w) : "l"(p), "r"((uint32_t)ok));
+}
+
+// Elements i .. i+3, where `ok`; zeros otherwise.  VEC: the address is aligned to
+// four elements and all four exist; else the first nv of them, one by one.
+// RO: through the read-only path.
+template <int IO, bool VEC, bool RO = true>
+__device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool ok, int nv) {
     Raw4 r = {{0u, 0u, 0u, 0u}};
     if (IO == IO_F32) {
         const uint32_t *p = static_cast<const uint32_t *>(base) + i;
-        if (vec) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-            r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+        if (VEC) {
+            if (RO) ldg_v4(r.w, p, ok);
+            else ld_v4(r.w, p, ok);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < nv) r.w[j] = __ldg(p + j);
+            for (int j = 0; j < 4; ++j) {
+                if (RO) ldg_u32(r.w[j], p + j, ok && j < nv);
+                else ld_u32(r.w[j], p + j, ok && j < nv);
+            }
         }
     } else {
         const uint16_t *p = static_cast<const uint16_t *>(base) + i;
-        if (vec) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-            r.w[0] = u.x; r.w[1] = u.y;
-        } else {
-            uint32_t e[4] = {0u, 0u, 0u, 0u};
+        if (VEC) {
+            if (RO) ldg_v2(r.w, p, ok);
+            else ld_v2(r.w, p, ok);
+        } else {  // one to a word; unpack4 reads them there
+            uint16_t e[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < nv) e[j] = __ldg(p + j);
-            r.w[0] = e[0] | (e[1] << 16);
-            r.w[1] = e[2] | (e[3] << 16);
+            for (int j = 0; j < 4; ++j) {
+                if (RO) ldg_u16(e[j], p + j, ok && j < nv);
+                else ld_u16(e[j], p + j, ok && j < nv);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.w[j] = e[j];
         }
     }
     return r;
 }
 
-template <int IO>
+template <int IO, bool VEC>
 __device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
     if (IO == IO_F32) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r.w[j]);
+    } else if (!VEC) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = IO == IO_BF16 ? __uint_as_float(r.w[j] << 16) : __half2float(__ushort_as_half((unsigned short)r.w[j]));
     } else {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -172,21 +229,46 @@ __device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
     }
 }
 
+// One element, where `ok`.
 template <int IO>
-__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, bool vec, int nv, int dt32) {
-    if (IO != IO_F32 && dt32) return load_raw4<IO_F32>(base, i, vec, nv);
-    return load_raw4<IO>(base, i, vec, nv);
+__device__ __forceinline__ float load_one(const void *base, long long i, bool ok) {
+    if (IO == IO_F32) {
+        uint32_t w = 0;
+        ldg_u32(w, static_cast<const uint32_t *>(base) + i, ok);
+        return __uint_as_float(w);
+    }
+    uint16_t h = 0;
+    ldg_u16(h, static_cast<const uint16_t *>(base) + i, ok);
+    return IO == IO_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
-template <int IO>
+// dt, in the tensors' type or in fp32.
+template <int IO, bool VEC>
+__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, bool ok, int nv, int dt32) {
+    if (IO == IO_F32) return load_raw4<IO_F32, VEC>(base, i, ok, nv);
+    Raw4 r = load_raw4<IO, VEC>(base, i, ok && !dt32, nv);
+    const uint32_t *p = static_cast<const uint32_t *>(base) + i;
+    if (VEC) {
+        ldg_v4(r.w, p, ok && dt32);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ldg_u32(r.w[j], p + j, ok && dt32 && j < nv);
+    }
+    return r;
+}
+
+template <int IO, bool VEC>
 __device__ __forceinline__ void unpack4_dt(const Raw4 &r, float (&v)[4], int dt32) {
-    if (IO != IO_F32 && dt32) unpack4<IO_F32>(r, v);
-    else unpack4<IO>(r, v);
+    unpack4<IO, VEC>(r, v);
+    if (IO != IO_F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = dt32 ? __uint_as_float(r.w[j]) : v[j];
+    }
 }
 
-template <int IO>
-__device__ __forceinline__ void store4_io(void *base, long long i, bool vec, int nv, const float (&v)[4]) {
-    if (!vec) {
+template <int IO, bool VEC>
+__device__ __forceinline__ void store4_io(void *base, long long i, int nv, const float (&v)[4]) {
+    if (!VEC) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j < nv) st_io<IO>(base, (size_t)(i + j), v[j]);
@@ -234,16 +316,10 @@ __device__ __forceinline__ bool aligned_n4(const float *p, int N) {
     return N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
-// Whether four elements from c0 + 4 q on, at any (batch, token), sit on a boundary of four elements.
-template <int IO>
-__device__ __forceinline__ bool vec4_ok(const void *p, const long long (&st)[2], long long c0) {
-    constexpr int kBytes = IO == IO_F32 ? 16 : 8;
-    return (reinterpret_cast<uintptr_t>(p) % kBytes) == 0 && st[0] % 4 == 0 && st[1] % 4 == 0 && c0 % 4 == 0;
-}
-
-template <int IO>
-__device__ __forceinline__ bool vec4_row(const void *p, long long row) {
-    return (reinterpret_cast<uintptr_t>(p) % (IO == IO_F32 ? 16 : 8)) == 0 && row % 4 == 0;
+// Whether groups of four elements of a [B,L,...] tensor sit on boundaries of four elements (host).
+inline bool vec4_aligned(const void *p, int io) { return reinterpret_cast<uintptr_t>(p) % (io == IO_F32 ? 16 : 8) == 0; }
+inline bool vec4_strided(const void *p, int io, const long long (&st)[2]) {
+    return vec4_aligned(p, io) && st[0] % 4 == 0 && st[1] % 4 == 0;
 }
 
 // d_t of one raw step.  softplus(v) = max(v, 0) + log1p(w), w = exp(-|v|) in

@@ -19,7 +19,7 @@ namespace {
 // together; B and C are loaded once for them.
 constexpr int kStepThreads = 128;
 
-template <int IO, int LPC, int CPT>
+template <int IO, int LPC, int CPT, bool VEC>
 __global__ void __launch_bounds__(kStepThreads)
 scan_step_kernel(ScanStepParams p) {
     constexpr int kCh = kStepThreads / LPC;  // channels per CTA and round
@@ -29,24 +29,24 @@ scan_step_kernel(ScanStepParams p) {
     const long long slot = p.slots ? __ldg(p.slots + b) : b;
     const bool live = slot >= 0 && slot < p.nslots;
     const long long s0 = slot * p.D * p.N;
-    const bool vs = aligned_n4(p.state, p.N) && aligned_n4(p.state_out, p.N), va = aligned_n4(p.A, p.N);
-    const int dg = p.D / p.G;
-    float s[CPT][4], a[CPT][4], x[CPT], raw[CPT], z[CPT], bv[CPT][4], cv[CPT][4];
+    const int dg = p.D / p.G, nn = p.N - n0;
+    Raw4 rs[CPT], ra[CPT], rb[CPT], rc[CPT];
+    float x[CPT], raw[CPT], z[CPT], bias[CPT], skip[CPT];
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {
+    for (int k = 0; k < CPT; ++k) {  // every load first
         const int c = cb + k * kCh;
-        if (!live || c >= p.D) continue;
-        load_n4(p.state + s0, (long long)c * p.N + n0, n0, p.N, vs, s[k]);
-        load_n4(p.A, (long long)c * p.N + n0, n0, p.N, va, a[k]);
-        x[k] = ld_io<IO>(p.x, (size_t)(b * p.x_row + c));
-        raw[k] = IO != IO_F32 && p.dt32 ? ld_io<IO_F32>(p.dt, (size_t)(b * p.dt_row + c))
-                                        : ld_io<IO>(p.dt, (size_t)(b * p.dt_row + c));
-        z[k] = p.z ? ld_io<IO>(p.z, (size_t)(b * p.z_row + c)) : 0.f;
-        const long long gn = (long long)(c / dg) * p.N + n0;
-        const bool vb = p.N % 4 == 0;
-        const bool vbb = vb && vec4_row<IO>(p.Bm, p.b_row), vcc = vb && vec4_row<IO>(p.Cm, p.c_row);
-        unpack4<IO>(load_raw4<IO>(p.Bm, b * p.b_row + gn, vbb && n0 < p.N, p.N - n0), bv[k]);
-        unpack4<IO>(load_raw4<IO>(p.Cm, b * p.c_row + gn, vcc && n0 < p.N, p.N - n0), cv[k]);
+        const bool ok = live && c < p.D, okn = ok && nn > 0;
+        const long long i = (long long)c * p.N + n0, gn = (long long)(c / dg) * p.N + n0;
+        rs[k] = load_raw4<IO_F32, VEC, false>(p.state, s0 + i, okn, nn);
+        ra[k] = load_raw4<IO_F32, VEC>(p.A, i, okn, nn);
+        rb[k] = load_raw4<IO, VEC>(p.Bm, b * p.b_row + gn, okn, nn);
+        rc[k] = load_raw4<IO, VEC>(p.Cm, b * p.c_row + gn, okn, nn);
+        x[k] = load_one<IO>(p.x, b * p.x_row + c, ok);
+        raw[k] = load_one<IO>(p.dt, b * p.dt_row + c, ok && (IO == IO_F32 || !p.dt32));
+        if (IO != IO_F32) raw[k] += load_one<IO_F32>(p.dt, b * p.dt_row + c, ok && p.dt32);  // one of the two is 0
+        z[k] = load_one<IO>(p.z, b * p.z_row + c, ok && p.z);
+        bias[k] = load_one<IO_F32>(p.dt_bias, c, ok && p.dt_bias);
+        skip[k] = load_one<IO_F32>(p.Dskip, c, ok && p.Dskip);
     }
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
@@ -54,23 +54,26 @@ scan_step_kernel(ScanStepParams p) {
         const bool in = live && c < p.D;
         float acc = 0.f;
         if (in) {
-            const float d = step_of<false>(raw[k], p.dt_bias ? __ldg(p.dt_bias + c) : 0.f, p.softplus, p.has_limit,
-                                           p.dt_min, p.dt_max).d;
+            const float d = step_of<false>(raw[k], bias[k], p.softplus, p.has_limit, p.dt_min, p.dt_max).d;
             const float dx = d * x[k];
-            float o[4];
+            float o[4], s[4], a[4], bv[4], cv[4];
+            unpack4<IO_F32, VEC>(rs[k], s);
+            unpack4<IO_F32, VEC>(ra[k], a);
+            unpack4<IO, VEC>(rb[k], bv);
+            unpack4<IO, VEC>(rc[k], cv);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = fmaf(ex2(d * (a[k][j] * kLog2e)), s[k][j], dx * bv[k][j]);
-                acc = fmaf(o[j], cv[k][j], acc);
+                o[j] = fmaf(ex2(fmaf(d, a[j] * kLog2e, kDecayCentre)), s[j], dx * bv[j]);
+                acc = fmaf(o[j], cv[j], acc);
             }
-            store_n4(p.state_out + s0, (long long)c * p.N + n0, n0, p.N, vs, o[0], o[1], o[2], o[3]);
+            store_n4(p.state_out + s0, (long long)c * p.N + n0, n0, p.N, VEC, o[0], o[1], o[2], o[3]);
         }
 #pragma unroll
         for (int off = LPC / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
         if (ln == 0 && c < p.D) {
             float y = 0.f;
             if (live) {
-                y = p.Dskip ? fmaf(__ldg(p.Dskip + c), x[k], acc) : acc;
+                y = p.Dskip ? fmaf(skip[k], x[k], acc) : acc;
                 if (p.z) y *= silu_fast(z[k]);
             }
             st_io<IO>(p.y, (size_t)b * p.D + c, y);
@@ -84,10 +87,14 @@ cudaError_t launch_step_as(const ScanStepParams &p, cudaStream_t s) {
     // Four channels per lane once that still gives every SM eight CTAs: more bytes in flight per lane;
     // below that one channel per lane spreads the few channels over more SMs.
     const long long ctas4 = (long long)p.B * ((p.D + 4 * kCh - 1) / (4 * kCh));
-    if (ctas4 >= 8LL * scan_sm_count())
-        scan_step_kernel<IO, LPC, 4><<<dim3((p.D + 4 * kCh - 1) / (4 * kCh), p.B), kStepThreads, 0, s>>>(p);
-    else
-        scan_step_kernel<IO, LPC, 1><<<dim3((p.D + kCh - 1) / kCh, p.B), kStepThreads, 0, s>>>(p);
+    const bool vec = p.N % 4 == 0 && vec4_aligned(p.state, IO_F32) && vec4_aligned(p.state_out, IO_F32) &&
+                     vec4_aligned(p.A, IO_F32) && vec4_aligned(p.Bm, IO) && vec4_aligned(p.Cm, IO) &&
+                     p.b_row % 4 == 0 && p.c_row % 4 == 0;
+    const bool many = ctas4 >= 8LL * scan_sm_count();
+    const dim3 grid(many ? (p.D + 4 * kCh - 1) / (4 * kCh) : (p.D + kCh - 1) / kCh, p.B);
+    auto *kernel = many ? (vec ? scan_step_kernel<IO, LPC, 4, true> : scan_step_kernel<IO, LPC, 4, false>)
+                        : (vec ? scan_step_kernel<IO, LPC, 1, true> : scan_step_kernel<IO, LPC, 1, false>);
+    kernel<<<grid, kStepThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

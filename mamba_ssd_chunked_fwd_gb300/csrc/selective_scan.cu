@@ -78,7 +78,7 @@ __device__ __forceinline__ void reduce_quad(float (&v)[4], int lane) {
     for (int off = 4; off < LPC; off <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
 }
 
-template <int IO, int LPC, int MODE>
+template <int IO, int LPC, int MODE, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 scan_walk_kernel(ScanParams p) {
     using S = WalkShape<LPC>;
@@ -162,7 +162,7 @@ scan_walk_kernel(ScanParams p) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 dd = dup(d[j]), ww = dup(w[j]);
-                        const float2 e0 = ex2_2(__fmul2_rn(dd, a2[j][0])), e1 = ex2_2(__fmul2_rn(dd, a2[j][1]));
+                        const float2 e0 = decay2(dd, a2[j][0]), e1 = decay2(dd, a2[j][1]);
                         if (kRev) {  // a_t (p + ds_t C_t)
                             h[j][0] = __fmul2_rn(e0, __ffma2_rn(ww, b0, h[j][0]));
                             h[j][1] = __fmul2_rn(e1, __ffma2_rn(ww, b1, h[j][1]));
@@ -209,19 +209,11 @@ scan_walk_kernel(ScanParams p) {
     const int q = ta % S::kQuads;  // the thread's quad of channels is the same in every unit
     const int nv = min(4, nch - q * 4);
     const long long cq = c0 + q * 4;
-    const bool full = nv == 4;
     const void *xin = kRev ? p.dy : p.x;
-    const long long dys[2] = {(long long)p.L * p.D, p.D};
-    const bool vx = full && (kRev ? vec4_ok<IO>(p.dy, dys, cq) : vec4_ok<IO>(p.x, p.xs, cq));
-    const bool vdt = full && (IO != IO_F32 && p.dt32 ? vec4_ok<IO_F32>(p.dt, p.dts, cq) : vec4_ok<IO>(p.dt, p.dts, cq));
-    const bool vz = full && p.z && vec4_ok<IO>(p.z, p.zs, cq);
-    const bool vy = full && kY && vec4_ok<IO>(p.y, dys, cq);
     const void *bm = kRev ? p.Cm : p.Bm;
     const long long bb = kRev ? p.cs[0] : p.bs[0], bt = kRev ? p.cs[1] : p.bs[1];
-    const long long xb = kRev ? dys[0] : p.xs[0], xt = kRev ? dys[1] : p.xs[1];
+    const long long xb = kRev ? (long long)p.L * p.D : p.xs[0], xt = kRev ? p.D : p.xs[1];
     const long long gn = (long long)g * p.N;
-    const bool vb = p.N % 4 == 0 && (kRev ? vec4_ok<IO>(p.Cm, p.cs, gn) : vec4_ok<IO>(p.Bm, p.bs, gn));
-    const bool vc = p.N % 4 == 0 && vec4_ok<IO>(p.Cm, p.cs, gn);
     float bias[4] = {0.f, 0.f, 0.f, 0.f}, skip[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -237,21 +229,19 @@ scan_walk_kernel(ScanParams p) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int unit = ta + kSideThreads * u, i = k * kT + unit / S::kQuads;
-            if (unit < kT * S::kQuads && i < ntok && nv > 0) {
-                const long long t = token(i);
-                rx[u] = load_raw4<IO>(xin, b * xb + t * xt + cq, vx, nv);
-                rdt[u] = load_raw4_dt<IO>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, vdt, nv, p.dt32);
-                if (kRev && p.z) rz[u] = load_raw4<IO>(p.z, b * p.zs[0] + t * p.zs[1] + cq, vz, nv);
-            }
+            const bool ok = unit < kT * S::kQuads && i < ntok && nv > 0;
+            const long long t = token(i);
+            rx[u] = load_raw4<IO, VEC>(xin, b * xb + t * xt + cq, ok, nv);
+            rdt[u] = load_raw4_dt<IO, VEC>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, ok, nv, p.dt32);
+            if (kRev) rz[kRev ? u : 0] = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
         }
 #pragma unroll
         for (int u = 0; u < kBu; ++u) {
             const int unit = ta + kSideThreads * u, i = k * kT + unit / LPC, n = unit % LPC * 4;
-            if (unit < kT * LPC && i < ntok && n < p.N) {
-                const long long t = token(i);
-                rb[u] = load_raw4<IO>(bm, b * bb + t * bt + gn + n, vb, p.N - n);
-                if (kY) rc[u] = load_raw4<IO>(p.Cm, b * p.cs[0] + t * p.cs[1] + gn + n, vc, p.N - n);
-            }
+            const bool ok = unit < kT * LPC && i < ntok && n < p.N;
+            const long long t = token(i);
+            rb[u] = load_raw4<IO, VEC>(bm, b * bb + t * bt + gn + n, ok, p.N - n);
+            if (kY) rc[kY ? u : 0] = load_raw4<IO, VEC>(p.Cm, b * p.cs[0] + t * p.cs[1] + gn + n, ok, p.N - n);
         }
     };
     auto stage_tile = [&](int k) {
@@ -263,10 +253,10 @@ scan_walk_kernel(ScanParams p) {
             float d[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
             if (i < ntok && nv > 0) {
                 float x[4], dt[4];
-                unpack4<IO>(rx[u], x);
-                unpack4_dt<IO>(rdt[u], dt, p.dt32);
+                unpack4<IO, VEC>(rx[u], x);
+                unpack4_dt<IO, VEC>(rdt[u], dt, p.dt32);
                 float z[4];
-                if (kRev && p.z) unpack4<IO>(rz[kRev ? u : 0], z);
+                if (kRev && p.z) unpack4<IO, VEC>(rz[kRev ? u : 0], z);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < nv) {
@@ -284,11 +274,11 @@ scan_walk_kernel(ScanParams p) {
             if (unit >= kT * LPC) continue;
             const bool in = k * kT + tl < ntok && n < p.N;
             float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (in) unpack4<IO>(rb[u], v);
+            if (in) unpack4<IO, VEC>(rb[u], v);
             *reinterpret_cast<float4 *>(&s_b[buf][tl * kNp + n]) = make_float4(v[0], v[1], v[2], v[3]);
             if (kY) {
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
-                if (in) unpack4<IO>(rc[kY ? u : 0], c);
+                if (in) unpack4<IO, VEC>(rc[kY ? u : 0], c);
                 *reinterpret_cast<float4 *>(&s_c[kY ? buf : 0][kY ? tl * kNp + n : 0]) = make_float4(c[0], c[1], c[2], c[3]);
             }
         }
@@ -299,11 +289,10 @@ scan_walk_kernel(ScanParams p) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int unit = ta + kSideThreads * u, i = k * kT + unit / S::kQuads;
-            if (unit < kT * S::kQuads && i < ntok && nv > 0) {
-                const long long t = token(i);
-                if (p.Dskip) ex[u] = load_raw4<IO>(p.x, b * p.xs[0] + t * p.xs[1] + cq, vx, nv);
-                if (p.z) ez[u] = load_raw4<IO>(p.z, b * p.zs[0] + t * p.zs[1] + cq, vz, nv);
-            }
+            const bool ok = unit < kT * S::kQuads && i < ntok && nv > 0;
+            const long long t = token(i);
+            ex[u] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + t * p.xs[1] + cq, ok && p.Dskip, nv);
+            ez[u] = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -313,17 +302,17 @@ scan_walk_kernel(ScanParams p) {
             float y[4] = {y4.x, y4.y, y4.z, y4.w};
             if (p.Dskip) {
                 float x[4];
-                unpack4<IO>(ex[u], x);
+                unpack4<IO, VEC>(ex[u], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] = fmaf(skip[j], x[j], y[j]);
             }
             if (p.z) {
                 float z[4];
-                unpack4<IO>(ez[u], z);
+                unpack4<IO, VEC>(ez[u], z);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] *= silu_fast(z[j]);
             }
-            store4_io<IO>(p.y, ((long long)b * p.L + tb + i) * p.D + cq, vy, nv, y);
+            store4_io<IO, VEC>(p.y, ((long long)b * p.L + tb + i) * p.D + cq, nv, y);
         }
     };
 
@@ -386,11 +375,23 @@ scan_fold_adj_kernel(ScanParams p) {
     }
 }
 
+// Whether every tensor the side warps touch moves in aligned groups of four.
+bool walk_vec(const ScanParams &p, int io, int mode) {
+    const long long dense[2] = {(long long)p.L * p.D, p.D};
+    const bool adj = mode == WALK_ADJ, y = mode == WALK_Y;
+    return p.D / p.G % 4 == 0 && p.N % 4 == 0 && (adj || vec4_strided(p.x, io, p.xs)) &&
+           vec4_strided(p.dt, p.dt32 ? (int)IO_F32 : io, p.dts) && (adj || vec4_strided(p.Bm, io, p.bs)) &&
+           (!(adj || y) || (vec4_strided(p.Cm, io, p.cs) && (!p.z || vec4_strided(p.z, io, p.zs)))) &&
+           (!y || vec4_strided(p.y, io, dense)) && (!adj || vec4_strided(p.dy, io, dense));
+}
+
 template <int IO, int LPC, int MODE>
 cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
     p.tiles = (p.D / p.G + WalkShape<LPC>::kDc - 1) / WalkShape<LPC>::kDc;
     const int segs = MODE == WALK_SEG || MODE == WALK_ADJ ? p.nseg - 1 : p.nseg;
-    scan_walk_kernel<IO, LPC, MODE><<<dim3(p.G * p.tiles, segs, p.B), kWalkThreads, 0, s>>>(p);
+    const dim3 grid(p.G * p.tiles, segs, p.B);
+    if (walk_vec(p, IO, MODE)) scan_walk_kernel<IO, LPC, MODE, true><<<grid, kWalkThreads, 0, s>>>(p);
+    else scan_walk_kernel<IO, LPC, MODE, false><<<grid, kWalkThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -72,7 +72,7 @@ struct GroupSum {
     }
 };
 
-template <int IO, int LPC>
+template <int IO, int LPC, bool VEC>
 __global__ void __launch_bounds__(kBthreads, 2)
 scan_bwd_kernel(ScanParams p) {
     using S = BwdShape<LPC>;
@@ -134,7 +134,7 @@ scan_bwd_kernel(ScanParams p) {
             float *so = s_o + buf * 3 * kTile, *sp = s_p + (buf * kBw + warp) * kT * 2 * kNp;
 #pragma unroll 1
             for (int t8 = (min(kT, ntok - k * kT) - 1) / 8 * 8; t8 >= 0; t8 -= 8) {  // staged as d = 0 past the last token
-                float2 h[2][2], ah[8][2][2];
+                float2 h[2][2], ah[8][2][2], da8[2][2];  // da8: dA of these eight tokens, then added to the long sum
 #pragma unroll
                 for (int j = 0; j < 2; ++j) h[j][0] = hn[j][0], h[j][1] = hn[j][1];
                 if (k * kT + t8 >= 8) load_state(k * kT + t8 - 8, hn);
@@ -148,8 +148,8 @@ scan_bwd_kernel(ScanParams p) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float2 dd = dup(j ? d2.y : d2.x), ww = dup(j ? w2.y : w2.x);
-                        ah[tt][j][0] = __fmul2_rn(ex2_2(__fmul2_rn(dd, a2[j][0])), h[j][0]);
-                        ah[tt][j][1] = __fmul2_rn(ex2_2(__fmul2_rn(dd, a2[j][1])), h[j][1]);
+                        ah[tt][j][0] = __fmul2_rn(decay2(dd, a2[j][0]), h[j][0]);
+                        ah[tt][j][1] = __fmul2_rn(decay2(dd, a2[j][1]), h[j][1]);
                         h[j][0] = __ffma2_rn(ww, b0, ah[tt][j][0]);
                         h[j][1] = __ffma2_rn(ww, b1, ah[tt][j][1]);
                     }
@@ -182,10 +182,10 @@ scan_bwd_kernel(ScanParams p) {
                         const float2 vb = __ffma2_rn(q1, b1, __fmul2_rn(q0, b0));
                         const float2 vr = __ffma2_rn(x1, a2[j][1], __fmul2_rn(x0, a2[j][0]));
                         const float2 vc = __ffma2_rn(h1, cc1, __fmul2_rn(h0, cc0));
-                        da[j][0] = __ffma2_rn(dd, x0, da[j][0]);
-                        da[j][1] = __ffma2_rn(dd, x1, da[j][1]);
-                        q[j][0] = __fmul2_rn(ex2_2(__fmul2_rn(dd, a2[j][0])), q0);
-                        q[j][1] = __fmul2_rn(ex2_2(__fmul2_rn(dd, a2[j][1])), q1);
+                        da8[j][0] = tt == 7 ? __fmul2_rn(dd, x0) : __ffma2_rn(dd, x0, da8[j][0]);
+                        da8[j][1] = tt == 7 ? __fmul2_rn(dd, x1) : __ffma2_rn(dd, x1, da8[j][1]);
+                        q[j][0] = __fmul2_rn(decay2(dd, a2[j][0]), q0);
+                        q[j][1] = __fmul2_rn(decay2(dd, a2[j][1]), q1);
                         r[j][0] = vb.x + vb.y;
                         r[j][1] = vr.x + vr.y;
                         r[j][2] = vc.x + vc.y;
@@ -211,6 +211,11 @@ scan_bwd_kernel(ScanParams p) {
                         }
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    da[j][0] = __fadd2_rn(da[j][0], da8[j][0]);
+                    da[j][1] = __fadd2_rn(da[j][1], da8[j][1]);
+                }
             }
             __syncthreads();
         }
@@ -234,15 +239,8 @@ scan_bwd_kernel(ScanParams p) {
     const int qd = ta % S::kQuads;
     const int nv = min(4, nch - qd * 4);
     const long long cq = c0 + qd * 4;
-    const bool full = nv == 4;
     const long long dense[2] = {(long long)p.L * p.D, p.D};
-    const bool vx = full && vec4_ok<IO>(p.x, p.xs, cq), vz = full && p.z && vec4_ok<IO>(p.z, p.zs, cq);
-    const bool vdt = full && (IO != IO_F32 && p.dt32 ? vec4_ok<IO_F32>(p.dt, p.dts, cq) : vec4_ok<IO>(p.dt, p.dts, cq));
-    const bool vdy = full && vec4_ok<IO>(p.dy, dense, cq), vdx = full && vec4_ok<IO>(p.dx, dense, cq);
-    const bool vdz = full && vec4_ok<IO>(p.dz, dense, cq);
-    const bool vddt = full && (IO != IO_F32 && p.dt32 ? vec4_ok<IO_F32>(p.ddt, dense, cq) : vec4_ok<IO>(p.ddt, dense, cq));
     const long long gn = (long long)g * p.N;
-    const bool vb = p.N % 4 == 0 && vec4_ok<IO>(p.Bm, p.bs, gn), vc = p.N % 4 == 0 && vec4_ok<IO>(p.Cm, p.cs, gn);
     float bias[4] = {0.f, 0.f, 0.f, 0.f}, skip[4] = {0.f, 0.f, 0.f, 0.f};
     float acc_d[4] = {0.f, 0.f, 0.f, 0.f}, acc_b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -252,26 +250,25 @@ scan_bwd_kernel(ScanParams p) {
             if (p.Dskip) skip[j] = __ldg(p.Dskip + cq + j);
         }
     Raw4 rx[kU], rdt[kU], rdy[kU], rz[kU], rb[kBu], rc[kBu];
-    auto load_unit = [&](long long t, Raw4 &x, Raw4 &dt, Raw4 &dy, Raw4 &z) {
-        x = load_raw4<IO>(p.x, b * p.xs[0] + t * p.xs[1] + cq, vx, nv);
-        dt = load_raw4_dt<IO>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, vdt, nv, p.dt32);
-        dy = load_raw4<IO>(p.dy, b * dense[0] + t * dense[1] + cq, vdy, nv);
-        if (p.z) z = load_raw4<IO>(p.z, b * p.zs[0] + t * p.zs[1] + cq, vz, nv);
+    auto load_unit = [&](long long t, bool ok, Raw4 &x, Raw4 &dt, Raw4 &dy, Raw4 &z) {
+        x = load_raw4<IO, VEC>(p.x, b * p.xs[0] + t * p.xs[1] + cq, ok, nv);
+        dt = load_raw4_dt<IO, VEC>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, ok, nv, p.dt32);
+        dy = load_raw4<IO, VEC>(p.dy, b * dense[0] + t * dense[1] + cq, ok, nv);
+        z = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
     };
     auto load_tile = [&](int i) {
         const int k = nt - 1 - i;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int unit = ta + kBside * u, t = k * kT + unit / S::kQuads;
-            if (unit < kT * S::kQuads && t < ntok && nv > 0) load_unit(tb + t, rx[u], rdt[u], rdy[u], rz[u]);
+            load_unit(tb + t, unit < kT * S::kQuads && t < ntok && nv > 0, rx[u], rdt[u], rdy[u], rz[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBu; ++u) {
             const int unit = ta + kBside * u, t = k * kT + unit / LPC, n = unit % LPC * 4;
-            if (unit < kT * LPC && t < ntok && n < p.N) {
-                rb[u] = load_raw4<IO>(p.Bm, b * p.bs[0] + (long long)(tb + t) * p.bs[1] + gn + n, vb, p.N - n);
-                rc[u] = load_raw4<IO>(p.Cm, b * p.cs[0] + (long long)(tb + t) * p.cs[1] + gn + n, vc, p.N - n);
-            }
+            const bool ok = unit < kT * LPC && t < ntok && n < p.N;
+            rb[u] = load_raw4<IO, VEC>(p.Bm, b * p.bs[0] + (long long)(tb + t) * p.bs[1] + gn + n, ok, p.N - n);
+            rc[u] = load_raw4<IO, VEC>(p.Cm, b * p.cs[0] + (long long)(tb + t) * p.cs[1] + gn + n, ok, p.N - n);
         }
     };
     auto stage_tile = [&](int i) {
@@ -283,10 +280,10 @@ scan_bwd_kernel(ScanParams p) {
             float d[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f}, gg[4] = {0.f, 0.f, 0.f, 0.f};
             if (k * kT + tl < ntok && nv > 0) {
                 float x[4], dt[4], dy[4], z[4];
-                unpack4<IO>(rx[u], x);
-                unpack4_dt<IO>(rdt[u], dt, p.dt32);
-                unpack4<IO>(rdy[u], dy);
-                if (p.z) unpack4<IO>(rz[u], z);
+                unpack4<IO, VEC>(rx[u], x);
+                unpack4_dt<IO, VEC>(rdt[u], dt, p.dt32);
+                unpack4<IO, VEC>(rdy[u], dy);
+                if (p.z) unpack4<IO, VEC>(rz[u], z);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < nv) {
@@ -306,8 +303,8 @@ scan_bwd_kernel(ScanParams p) {
             if (unit >= kT * LPC) continue;
             float v[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
             if (k * kT + tl < ntok && n < p.N) {
-                unpack4<IO>(rb[u], v);
-                unpack4<IO>(rc[u], c);
+                unpack4<IO, VEC>(rb[u], v);
+                unpack4<IO, VEC>(rc[u], c);
             }
             *reinterpret_cast<float4 *>(s_b + (buf * kT + tl) * kNp + n) = make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4 *>(s_c + (buf * kT + tl) * kNp + n) = make_float4(c[0], c[1], c[2], c[3]);
@@ -319,7 +316,7 @@ scan_bwd_kernel(ScanParams p) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int unit = ta + kBside * u, t = k * kT + unit / S::kQuads;
-            if (unit < kT * S::kQuads && t < ntok && nv > 0) load_unit(tb + t, ex[u], edt[u], edy[u], ez[u]);
+            load_unit(tb + t, unit < kT * S::kQuads && t < ntok && nv > 0, ex[u], edt[u], edy[u], ez[u]);
         }
         // dB and dC of the tile over the walk warps
         for (int e = ta; e < kT * 2 * kNp; e += kBside) {
@@ -345,8 +342,8 @@ scan_bwd_kernel(ScanParams p) {
             const float qb[4] = {b4.x, b4.y, b4.z, b4.w}, qr[4] = {r4.x, r4.y, r4.z, r4.w};
             const float hc[4] = {c4.x, c4.y, c4.z, c4.w};
             float x[4], dt[4], dx[4], ddt[4];
-            unpack4<IO>(ex[u], x);
-            unpack4_dt<IO>(edt[u], dt, p.dt32);
+            unpack4<IO, VEC>(ex[u], x);
+            unpack4_dt<IO, VEC>(edt[u], dt, p.dt32);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float sig = p.softplus ? sigmoid_f(dt[j] + bias[j]) : 1.f;
@@ -360,19 +357,19 @@ scan_bwd_kernel(ScanParams p) {
                 }
             }
             const long long at = ((long long)b * p.L + tb + t) * p.D + cq;
-            store4_io<IO>(p.dx, at, vdx, nv, dx);
-            if (IO != IO_F32 && p.dt32) store4_io<IO_F32>(p.ddt, at, vddt, nv, ddt);
-            else store4_io<IO>(p.ddt, at, vddt, nv, ddt);
+            store4_io<IO, VEC>(p.dx, at, nv, dx);
+            if (IO != IO_F32 && p.dt32) store4_io<IO_F32, VEC>(p.ddt, at, nv, ddt);
+            else store4_io<IO, VEC>(p.ddt, at, nv, ddt);
             if (p.z) {
                 float z[4], dy[4], dz[4];
-                unpack4<IO>(ez[u], z);
-                unpack4<IO>(edy[u], dy);
+                unpack4<IO, VEC>(ez[u], z);
+                unpack4<IO, VEC>(edy[u], dy);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float sg = sigmoid_f(z[j]);
                     dz[j] = dy[j] * fmaf(skip[j], x[j], hc[j]) * (sg * fmaf(z[j], 1.f - sg, 1.f));
                 }
-                store4_io<IO>(p.dz, at, vdz, nv, dz);
+                store4_io<IO, VEC>(p.dz, at, nv, dz);
             }
         }
     };
@@ -464,14 +461,24 @@ scan_bwd_bc_kernel(ScanParams p, int np, void *dB, void *dC) {
     st_io<IO>(e < np ? dB : dC, (size_t)((bt * p.G + g) * p.N + n), v);
 }
 
+bool bwd_vec(const ScanParams &p, int io) {
+    const long long dense[2] = {(long long)p.L * p.D, p.D};
+    const int dio = p.dt32 ? (int)IO_F32 : io;
+    return p.D / p.G % 4 == 0 && p.N % 4 == 0 && vec4_strided(p.x, io, p.xs) && vec4_strided(p.dt, dio, p.dts) &&
+           vec4_strided(p.Bm, io, p.bs) && vec4_strided(p.Cm, io, p.cs) && (!p.z || vec4_strided(p.z, io, p.zs)) &&
+           vec4_strided(p.dy, io, dense) && vec4_strided(p.dx, io, dense) && vec4_strided(p.ddt, dio, dense) &&
+           (!p.z || vec4_strided(p.dz, io, dense));
+}
+
 template <int IO, int LPC>
 cudaError_t launch_bwd_as(ScanParams p, void *dB, void *dC, cudaStream_t s) {
     using S = BwdShape<LPC>;
     constexpr int kBytes = S::kFloats * (int)sizeof(float);
     p.tiles = scan_bwd_tiles(p);
-    cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<IO, LPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    auto *kernel = bwd_vec(p, IO) ? scan_bwd_kernel<IO, LPC, true> : scan_bwd_kernel<IO, LPC, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    scan_bwd_kernel<IO, LPC><<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, kBytes, s>>>(p);
+    kernel<<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, kBytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long per = (long long)p.B * p.L * 2 * S::kNp;
     scan_bwd_bc_kernel<IO><<<dim3((unsigned)((per + 255) / 256), p.G), 256, 0, s>>>(p, S::kNp, dB, dC);
