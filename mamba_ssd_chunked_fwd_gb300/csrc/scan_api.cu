@@ -64,23 +64,23 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
     return check_limit(a->dt_min, a->dt_max);
 }
 
-// The cut of the sequences.  A walk costs `walk` per token and CTA slot whatever
-// the number of CTAs up to what the SMs hold at once (two per SM, `slots`); one
-// segment is one walk of L tokens, `n` segments are two of L / n (the first gives
-// each segment's entering state) and a fold of n dependent steps.  Below two
-// segments per row of work nothing is gained, so n doubles from 2 while the
-// modelled time falls.  Units: one token step of a walk, about 60 ns; a fold step
-// and a launch in the same units.
-void choose_segments(ssd::ScanParams &p, int walks) {
+// The cut of the sequences into n segments.  A CTA of a walk advances a token in
+// about 0.1 us whether it has its SM alone or shares it with another (0.17 us for
+// two), so a walk of L tokens by few CTAs is cut until there is a CTA per SM.  The
+// cut costs a first walk (each segment's state from zero; backwards another
+// for the adjoint, too) and a fold of n dependent steps.  Units: tokens of the
+// forward's walk; the factors are the walks' measured times beside it, a
+// fold step is 6 and a launch 30.
+void choose_segments(ssd::ScanParams &p, bool backward) {
     const int lanes = ssd::scan_lanes(p.N);
     const int dc = 4 * (32 / lanes) * 4;
-    const long long ctas = (long long)p.B * p.G * ((p.D / p.G + dc - 1) / dc);
-    const long long slots = 2LL * ssd::scan_sm_count();
+    const double sms = ssd::scan_sm_count();
+    const double ctas = (double)p.B * p.G * ((p.D / p.G + dc - 1) / dc);
+    auto waves = [&](double k) { return k <= sms ? 1. : k <= 2 * sms ? 2. : k / sms; };
     auto cost = [&](long long n) {
-        const long long len = ((p.L + n - 1) / n + 31) / 32 * 32;
-        const long long waves = (ctas * n + slots - 1) / slots;
-        const double walk = (double)waves * (double)len;
-        return n == 1 ? walk * walks : walk * (walks + 0.7 * walks) + walks * (2.0 * (double)n + 100.0);
+        const double len = (double)(((p.L + n - 1) / n + 31) / 32 * 32), w = waves(ctas * n), w1 = waves(ctas * (n - 1));
+        if (!backward) return w * len + (n > 1 ? 0.7 * w1 * len + 6. * n + 60. : 0.);
+        return 0.8 * w * len + 1.5 * waves(2 * ctas * n) * len + (n > 1 ? 1.5 * w1 * len + 12. * n + 120. : 0.);
     };
     long long best = 1;
     for (long long n = 2; n <= 1024 && (p.L + n - 1) / n >= 32; n = n < 8 ? n + 1 : n + n / 4)
@@ -211,7 +211,7 @@ ssd_status ssd_selective_scan_workspace_size(const ssd_scan_args *a, size_t *byt
     if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
     ssd::ScanParams p = {};
     if ((st = make_scan(a, p)) != SSD_OK) return st;
-    choose_segments(p, 1);
+    choose_segments(p, false);
     *bytes = scan_layout(p).total;
     return ok();
 }
@@ -223,7 +223,7 @@ ssd_status ssd_selective_scan(const ssd_scan_args *a, void *stream) {
     if (!a->y) return fail(SSD_ERR_INVALID_ARG, "y is required");
     ssd::ScanParams p = {};
     if ((st = make_scan(a, p)) != SSD_OK) return st;
-    choose_segments(p, 1);
+    choose_segments(p, false);
     const ScanLayout l = scan_layout(p);
     if ((st = check_workspace(a->workspace, a->workspace_bytes, l.total)) != SSD_OK) return st;
     char *ws = static_cast<char *>(a->workspace);
@@ -240,7 +240,7 @@ ssd_status ssd_selective_scan_bwd_workspace_size(const ssd_scan_bwd_args *b, siz
     if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
     ssd::ScanParams p = {};
     if ((st = make_scan(&b->fwd, p)) != SSD_OK) return st;
-    choose_segments(p, 2);
+    choose_segments(p, true);
     *bytes = scan_bwd_layout(p).total;
     return ok();
 }
@@ -257,7 +257,7 @@ ssd_status ssd_selective_scan_bwd(const ssd_scan_bwd_args *b, void *stream) {
     if (a->dt_bias && !b->ddt_bias) return fail(SSD_ERR_INVALID_ARG, "ddt_bias is required with dt_bias");
     ssd::ScanParams p = {};
     if ((st = make_scan(a, p)) != SSD_OK) return st;
-    choose_segments(p, 2);
+    choose_segments(p, true);
     const ScanBwdLayout l = scan_bwd_layout(p);
     if ((st = check_workspace(b->workspace, b->workspace_bytes, l.total)) != SSD_OK) return st;
     char *ws = static_cast<char *>(b->workspace);

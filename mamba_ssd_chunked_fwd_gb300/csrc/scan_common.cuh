@@ -115,6 +115,7 @@ __device__ __forceinline__ float ex2(float v) {
 // Two fp32 numbers in one register pair; a packed operation takes one issue
 // slot for both.
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
 // exp(d A) from A log2(e): ex2.approx is low by 0.5 to 3e-8 on average for the
 // exponents of a slow decay (measured over [-0.5, -1e-5]), and a state that
@@ -132,48 +133,48 @@ struct Raw4 {
     uint32_t w[4];
 };
 
-// Predicated loads: a branch around a load (or a choice between two) would make
+// Predicated loads (where `ok` > 0): a branch around a load (or a choice between two) would make
 // the compiler wait for its data where the paths meet again, one latency per
 // load; a predicated load leaves them all in flight.  What is not loaded stays as it was.
-__device__ __forceinline__ void ldg_v4(uint32_t (&w)[4], const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"((uint32_t)ok));
+__device__ __forceinline__ void ldg_v4(uint32_t (&w)[4], const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(ok));
 }
-__device__ __forceinline__ void ldg_v2(uint32_t (&w)[4], const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
-                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"((uint32_t)ok));
+__device__ __forceinline__ void ldg_v2(uint32_t (&w)[4], const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(ok));
 }
 // Without the read-only path: tensors that the same thread writes later (updates in place).
-__device__ __forceinline__ void ld_v4(uint32_t (&w)[4], const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"((uint32_t)ok) : "memory");
+__device__ __forceinline__ void ld_v4(uint32_t (&w)[4], const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(ok) : "memory");
 }
-__device__ __forceinline__ void ld_v2(uint32_t (&w)[4], const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
-                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"((uint32_t)ok) : "memory");
+__device__ __forceinline__ void ld_v2(uint32_t (&w)[4], const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %3, 0;\n\t@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(ok) : "memory");
 }
-__device__ __forceinline__ void ld_u32(uint32_t &w, const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
-                 : "+r"(w) : "l"(p), "r"((uint32_t)ok) : "memory");
+__device__ __forceinline__ void ld_u32(uint32_t &w, const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %2, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
+                 : "+r"(w) : "l"(p), "r"(ok) : "memory");
 }
-__device__ __forceinline__ void ld_u16(uint16_t &w, const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
-                 : "+h"(w) : "l"(p), "r"((uint32_t)ok) : "memory");
+__device__ __forceinline__ void ld_u16(uint16_t &w, const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}"
+                 : "+h"(w) : "l"(p), "r"(ok) : "memory");
 }
-__device__ __forceinline__ void ldg_u32(uint32_t &w, const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
-                 : "+r"(w) : "l"(p), "r"((uint32_t)ok));
+__device__ __forceinline__ void ldg_u32(uint32_t &w, const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(w) : "l"(p), "r"(ok));
 }
-__device__ __forceinline__ void ldg_u16(uint16_t &w, const void *p, bool ok) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
-                 : "+h"(w) : "l"(p), "r"((uint32_t)ok));
+__device__ __forceinline__ void ldg_u16(uint16_t &w, const void *p, int ok) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.gt.s32 q, %2, 0;\n\t@q ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "+h"(w) : "l"(p), "r"(ok));
 }
 
 // Elements i .. i+3, where `ok`; zeros otherwise.  VEC: the address is aligned to
 // four elements and all four exist; else the first nv of them, one by one.
 // RO: through the read-only path.
 template <int IO, bool VEC, bool RO = true>
-__device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool ok, int nv) {
+__device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, int ok, int nv) {
     Raw4 r = {{0u, 0u, 0u, 0u}};
     if (IO == IO_F32) {
         const uint32_t *p = static_cast<const uint32_t *>(base) + i;
@@ -183,8 +184,8 @@ __device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool ok
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (RO) ldg_u32(r.w[j], p + j, ok && j < nv);
-                else ld_u32(r.w[j], p + j, ok && j < nv);
+                if (RO) ldg_u32(r.w[j], p + j, j < nv ? ok : 0);
+                else ld_u32(r.w[j], p + j, j < nv ? ok : 0);
             }
         }
     } else {
@@ -196,8 +197,8 @@ __device__ __forceinline__ Raw4 load_raw4(const void *base, long long i, bool ok
             uint16_t e[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (RO) ldg_u16(e[j], p + j, ok && j < nv);
-                else ld_u16(e[j], p + j, ok && j < nv);
+                if (RO) ldg_u16(e[j], p + j, j < nv ? ok : 0);
+                else ld_u16(e[j], p + j, j < nv ? ok : 0);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) r.w[j] = e[j];
@@ -229,6 +230,121 @@ __device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
     }
 }
 
+// Copies from global to shared memory that run on while the thread goes on
+// (cp.async); the thread that issued them waits with cp_wait.  What is not read is filled with zeros.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// One 16-byte chunk of a row (8 or 4 elements, of which the first n exist) into
+// shared memory.  VEC: the chunk is aligned and whole (n is all or none).  fp32
+// of any alignment goes element by element, still asynchronously; unaligned
+// 16-bit elements have no asynchronous form and are loaded, all at once, and stored.
+template <int IO, bool VEC>
+__device__ __forceinline__ void copy_chunk(void *dst, const char *src, int n) {
+    if (VEC) {
+        cp_async16(dst, n > 0 ? src : nullptr, n > 0 ? 16 : 0);
+    } else if (IO == IO_F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cp_async4(static_cast<float *>(dst) + j, j < n ? src + 4 * j : nullptr, j < n ? 4 : 0);
+    } else {
+        uint16_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            e[j] = 0;
+            ldg_u16(e[j], src + 2 * j, j < n);
+        }
+        uint4 u;
+        u.x = e[0] | ((uint32_t)e[1] << 16); u.y = e[2] | ((uint32_t)e[3] << 16);
+        u.z = e[4] | ((uint32_t)e[5] << 16); u.w = e[6] | ((uint32_t)e[7] << 16);
+        *static_cast<uint4 *>(dst) = u;
+    }
+}
+
+// A chunk from shared memory as pairs of floats.
+template <int IO>
+__device__ __forceinline__ void read_chunk(const void *src, float2 *v) {
+    const uint4 u = *static_cast<const uint4 *>(src);
+    if (IO == IO_F32) {
+        v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (IO == IO_BF16) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else v[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        }
+    }
+}
+
+// A chunk's values to global memory, the first n of them (VEC: all, aligned).
+template <int IO, bool VEC>
+__device__ __forceinline__ void store_chunk(char *dst, int n, const float2 *v) {
+    constexpr int kPairs = IO == IO_F32 ? 2 : 4;
+    if (n <= 0) return;
+    if (VEC) {
+        uint4 u;
+        uint32_t *w = &u.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (IO == IO_F32) {
+                w[i] = __float_as_uint(i & 1 ? v[i / 2].y : v[i / 2].x);
+            } else if (IO == IO_BF16) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(v[i].x, v[i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&a);
+            } else {
+                const __half2 a = __floats2half2_rn(v[i].x, v[i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&a);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst) = u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            if (2 * i < n) st_io<IO>(dst, 2 * i, v[i].x);
+            if (2 * i + 1 < n) st_io<IO>(dst, 2 * i + 1, v[i].y);
+        }
+    }
+}
+
+// Pairs of a chunk into or out of fp32 shared memory.  `flip` (threads of odd
+// groups of four): the halves of an 8-element chunk go in the other order, since
+// threads 32 bytes apart would meet in a bank.
+template <int KP>
+__device__ __forceinline__ void spread(float *dst, const float2 *v, bool flip) {
+    const float4 a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    if (KP == 2) {
+        *reinterpret_cast<float4 *>(dst) = a;
+        return;
+    }
+    const float4 c = make_float4(v[KP - 2].x, v[KP - 2].y, v[KP - 1].x, v[KP - 1].y);
+    *reinterpret_cast<float4 *>(dst + (flip ? 4 : 0)) = flip ? c : a;
+    *reinterpret_cast<float4 *>(dst + (flip ? 0 : 4)) = flip ? a : c;
+}
+template <int KP>
+__device__ __forceinline__ void gather(const float *src, float2 *v, bool flip) {
+    float4 a = *reinterpret_cast<const float4 *>(src + (KP == 4 && flip ? 4 : 0));
+    if (KP == 4) {
+        const float4 c = *reinterpret_cast<const float4 *>(src + (flip ? 0 : 4)), lo = flip ? c : a, hi = flip ? a : c;
+        v[KP - 2] = make_float2(hi.x, hi.y);
+        v[KP - 1] = make_float2(hi.z, hi.w);
+        a = lo;
+    }
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+}
+
 // One element, where `ok`.
 template <int IO>
 __device__ __forceinline__ float load_one(const void *base, long long i, bool ok) {
@@ -244,15 +360,15 @@ __device__ __forceinline__ float load_one(const void *base, long long i, bool ok
 
 // dt, in the tensors' type or in fp32.
 template <int IO, bool VEC>
-__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, bool ok, int nv, int dt32) {
+__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, int ok, int nv, int dt32) {
     if (IO == IO_F32) return load_raw4<IO_F32, VEC>(base, i, ok, nv);
-    Raw4 r = load_raw4<IO, VEC>(base, i, ok && !dt32, nv);
+    Raw4 r = load_raw4<IO, VEC>(base, i, dt32 ? 0 : ok, nv);
     const uint32_t *p = static_cast<const uint32_t *>(base) + i;
     if (VEC) {
-        ldg_v4(r.w, p, ok && dt32);
+        ldg_v4(r.w, p, dt32 ? ok : 0);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ldg_u32(r.w[j], p + j, ok && dt32 && j < nv);
+        for (int j = 0; j < 4; ++j) ldg_u32(r.w[j], p + j, dt32 && j < nv ? ok : 0);
     }
     return r;
 }
@@ -317,6 +433,11 @@ __device__ __forceinline__ bool aligned_n4(const float *p, int N) {
 }
 
 // Whether groups of four elements of a [B,L,...] tensor sit on boundaries of four elements (host).
+inline bool chunk_aligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+inline bool chunk_strided(const void *p, int io, const long long (&st)[2]) {
+    const int n = io == IO_F32 ? 4 : 8;
+    return chunk_aligned(p) && st[0] % n == 0 && st[1] % n == 0;
+}
 inline bool vec4_aligned(const void *p, int io) { return reinterpret_cast<uintptr_t>(p) % (io == IO_F32 ? 16 : 8) == 0; }
 inline bool vec4_strided(const void *p, int io, const long long (&st)[2]) {
     return vec4_aligned(p, io) && st[0] % 4 == 0 && st[1] % 4 == 0;
@@ -365,6 +486,52 @@ __device__ __forceinline__ StepOut step_of(float raw, float bias, int softplus, 
     }
     return o;
 }
+
+// step_of for 2 K channels at once, d only: v holds raw + bias.  The options are
+// tested once around all of them, so that the K chains of operations interleave.
+template <int K>
+__device__ __forceinline__ void steps_of(float2 (&v)[K], int softplus, int has_limit, float dmin, float dmax) {
+    if (softplus) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const float2 av = make_float2(-fminf(fabsf(v[i].x), 100.f), -fminf(fabsf(v[i].y), 100.f));
+            const float2 t = __fmul2_rn(av, dup(kLog2e));
+            const float2 e = __ffma2_rn(av, dup(1.92596299e-8f), __ffma2_rn(av, dup(kLog2e), make_float2(-t.x, -t.y)));
+            const float2 w0 = ex2_2(t);
+            const float2 w = __ffma2_rn(w0, __fmul2_rn(e, dup(kLn2)), w0);
+            float2 p = dup(0.005232690833508968f);
+            p = __ffma2_rn(p, w, dup(-0.029505228623747826f));
+            p = __ffma2_rn(p, w, dup(0.07822594791650772f));
+            p = __ffma2_rn(p, w, dup(-0.13663245737552643f));
+            p = __ffma2_rn(p, w, dup(0.19106008112430573f));
+            p = __ffma2_rn(p, w, dup(-0.2484298199415207f));
+            p = __ffma2_rn(p, w, dup(0.3331909775733948f));
+            p = __ffma2_rn(p, w, dup(-0.4999949336051941f));
+            p = __ffma2_rn(p, w, dup(0.9999999403953552f));
+            float2 m;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.x) : "f"(v[i].x), "f"(0.f));
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.y) : "f"(v[i].y), "f"(0.f));
+            v[i] = __ffma2_rn(w, p, m);
+        }
+    }
+    if (has_limit) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            v[i] = make_float2(fminf(fmaxf(v[i].x, dmin), dmax), fminf(fmaxf(v[i].y, dmin), dmax));
+    }
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// sigmoid and silu of two numbers; 1 + exp(-v) = inf gives 0, the limit.
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 e = __fadd2_rn(ex2_2(__fmul2_rn(v, dup(-kLog2e))), dup(1.f));
+    return make_float2(rcp_approx(e.x), rcp_approx(e.y));
+}
+__device__ __forceinline__ float2 silu2(float2 v) { return __fmul2_rn(v, sigmoid2(v)); }
 
 __device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 

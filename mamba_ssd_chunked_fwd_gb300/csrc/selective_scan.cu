@@ -36,58 +36,85 @@ enum WalkMode {
 
 constexpr int kWalkWarps = 4, kSideThreads = 128, kWalkThreads = kWalkWarps * 32 + kSideThreads;
 
-template <int LPC>
+// NPT states per lane, four channels: LPC = N / NPT lanes hold a channel.
+template <int IO, int LPC, int NPT>
 struct WalkShape {
-    static constexpr int kGroups = 32 / LPC;            // channel quads per warp
+    static constexpr int kGroups = 32 / LPC;              // channel quads per warp
     static constexpr int kDc = kWalkWarps * kGroups * 4;  // channels per CTA
-    static constexpr int kNp = LPC * 4;
-    static constexpr int kT = LPC == 2 ? 8 : LPC == 8 ? 32 : 16;  // tokens per tile
-    static constexpr int kQuads = kDc / 4;
-    static constexpr int kUnits = (kT * kQuads + kSideThreads - 1) / kSideThreads;   // quads of a token per side thread
-    static constexpr int kBcUnits = (kT * LPC + kSideThreads - 1) / kSideThreads;
+    static constexpr int kNp = LPC * NPT;
+    // tokens per tile: fp32 tiles are half as long, so that two CTAs' rings fit an SM
+    static constexpr int kElems = IO == IO_F32 ? 1024 : 2048;
+    static constexpr int kMost = kNp <= 16 ? 32 : kNp > 64 && IO == IO_F32 ? 8 : 16;
+    static constexpr int kT = kElems / kDc < kMost ? kElems / kDc : kMost;
+    // Side threads deal in chunks of 16 bytes of the tensors' type.  A thread's
+    // chunk of channels is fixed and its tokens are kUStep apart (threads past
+    // a tile's tokens idle); likewise B and C.
+    static constexpr int kEs = IO == IO_F32 ? 4 : 2, kCh = 16 / kEs, kPairs = kCh / 2;
+    static constexpr int kChunks = kDc / kCh;
+    static constexpr int kUStep = kSideThreads / kChunks < kT ? kSideThreads / kChunks : kT;
+    static constexpr int kUnits = kT / kUStep;
+    static constexpr int kBcChunks = kNp / kCh;
+    static constexpr int kBcStep = kSideThreads / kBcChunks < kT ? kSideThreads / kBcChunks : kT;
+    static constexpr int kBcUnits = kT / kBcStep;
+    // The ring of tiles as loaded: from the one being finished to kAhead past the one being staged.
+    static constexpr int kAhead = 2, kSlots = kAhead + 3;
+    static constexpr int kRawTile = kT * kDc * kEs, kRawBc = kT * kNp * kEs;
 };
 
-// Sums v[0..3] (one per channel of the quad) over the LPC lanes of a group.
-// While a lane holds several channels, each exchange halves them.  Returns
-// the number of channels left in v[0..]; `first` is the first one's index.
-template <int LPC>
-__device__ __forceinline__ void reduce_quad(float (&v)[4], int lane) {
-    if (LPC == 2) {
-        const bool hi = lane & 1;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float keep = hi ? v[k + 2] : v[k], send = hi ? v[k] : v[k + 2];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
-        }
-        return;
+// Bytes of shared memory: d, d x, B (and C), two buffers each; the ring: x, dt, z, B, C.
+template <int IO, int LPC, int NPT, int MODE>
+struct WalkSmem {
+    using S = WalkShape<IO, LPC, NPT>;
+    static constexpr bool kY = MODE == WALK_Y, kZ = MODE == WALK_Y || MODE == WALK_ADJ;
+    static constexpr int kStage = (2 * 2 * S::kT * S::kDc + (kY ? 4 : 2) * S::kT * S::kNp) * 4;
+    static constexpr int slot(int dt32) {  // dt may be wider than x
+        return S::kRawTile * (1 + (kZ ? 1 : 0)) + (dt32 ? S::kT * S::kDc * 4 : S::kRawTile) + S::kRawBc * (kY ? 2 : 1);
     }
-    {
-        const bool hi = lane & 2;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float keep = hi ? v[k + 2] : v[k], send = hi ? v[k] : v[k + 2];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
-        }
-    }
-    {
-        const bool hi = lane & 1;
-        const float keep = hi ? v[1] : v[0], send = hi ? v[0] : v[1];
-        v[0] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
-    }
-#pragma unroll
-    for (int off = 4; off < LPC; off <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-}
+    static constexpr int bytes(int dt32) { return kStage + S::kSlots * slot(dt32); }
+};
 
-template <int IO, int LPC, int MODE, bool VEC>
+// Sums v[0..15] (four tokens of four channels, token-major) over the LPC lanes
+// of a group.  While a lane holds several values, an exchange halves them: lane
+// bit 0 chooses the pair of tokens, bit 1 the token, bit 2 the pair of channels
+// and so on, so that 16 values take 12 exchanges over four lanes and each lane
+// is left with one token's four channels.  Returns the index of v[0].
+template <int LPC>
+struct QuadSum {
+    static constexpr int kLeft = LPC == 1 ? 16 : LPC == 2 ? 8 : LPC == 4 ? 4 : LPC == 8 ? 2 : 1;
+    static __device__ __forceinline__ int run(float (&v)[16], int lane) {
+        int idx = 0, cnt = 16;
+#pragma unroll
+        for (int off = 1; off < LPC; off <<= 1) {
+            if (cnt > 1) {
+                const bool hi = lane & off;
+                cnt >>= 1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < cnt) {
+                        const float keep = hi ? v[i + cnt] : v[i], send = hi ? v[i] : v[i + cnt];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+                    }
+                idx += hi ? cnt : 0;
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+            }
+        }
+        return idx;
+    }
+};
+
+template <int IO, int LPC, int NPT, int MODE, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 scan_walk_kernel(ScanParams p) {
-    using S = WalkShape<LPC>;
-    constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits;
-    constexpr bool kY = MODE == WALK_Y, kRev = MODE == WALK_ADJ;
-    __shared__ __align__(16) float s_d[2][kT * kDc];
-    __shared__ __align__(16) float s_w[2][kT * kDc];  // d x (backwards: the gated dy); y in its place afterwards
-    __shared__ __align__(16) float s_b[2][kT * kNp];  // B (backwards: C)
-    __shared__ __align__(16) float s_c[kY ? 2 : 1][kY ? kT * kNp : 4];
+    using S = WalkShape<IO, LPC, NPT>;
+    constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kH = NPT / 2;
+    constexpr bool kY = MODE == WALK_Y, kRev = MODE == WALK_ADJ, kZ = kY || kRev;
+    extern __shared__ __align__(16) float smem[];
+    float *s_d = smem;                            // [2][kT][kDc]
+    float *s_w = s_d + 2 * kT * kDc;              // d x (backwards: the gated dy); y in its place afterwards
+    float *s_b = s_w + 2 * kT * kDc;              // [2][kT][kNp] B (backwards: C)
+    float *s_c = s_b + 2 * kT * kNp;              // only with y
+    char *ring = reinterpret_cast<char *>(s_b + (kY ? 4 : 2) * kT * kNp);
 
     const int g = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
     const int seg = MODE == WALK_ADJ ? blockIdx.y + 1 : blockIdx.y, b = blockIdx.z;
@@ -101,8 +128,8 @@ scan_walk_kernel(ScanParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp < kWalkWarps) {
-        const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 4, n0 = ln * 4;
-        float2 h[4][2], a2[4][2];
+        const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 4, n0 = ln * NPT;
+        float2 h[4][kH], a2[4][kH];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         const float *start = nullptr;
         if (MODE == WALK_Y || MODE == WALK_CKPT)
@@ -114,222 +141,308 @@ scan_walk_kernel(ScanParams p) {
             start = seg == p.nseg - 1 && p.dfinal ? p.dfinal + (long long)b * p.D * p.N : nullptr;
         const bool va = aligned_n4(p.A, p.N), vs = aligned_n4(start, p.N);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float a[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-            if (ch0 + j < nch) {
-                const long long i = (long long)(c0 + ch0 + j) * p.N + n0;
-                load_n4(p.A, i, n0, p.N, va, a);
-                if (start) load_n4(start, i, n0, p.N, vs, s);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int m = 0; m < NPT; m += 4) {
+                float a[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+                if (ch0 + j < nch) {
+                    const long long i = (long long)(c0 + ch0 + j) * p.N + n0 + m;
+                    load_n4(p.A, i, n0 + m, p.N, va, a);
+                    if (start) load_n4(start, i, n0 + m, p.N, vs, s);
+                }
+                // the decay as a power of two: exp(d A) = 2^(d A log2 e)
+                a2[j][m / 2] = make_float2(a[0] * kLog2e, a[1] * kLog2e);
+                a2[j][m / 2 + 1] = make_float2(a[2] * kLog2e, a[3] * kLog2e);
+                h[j][m / 2] = make_float2(s[0], s[1]);
+                h[j][m / 2 + 1] = make_float2(s[2], s[3]);
             }
-            // the decay as a power of two: exp(d A) = 2^(d A log2 e)
-            a2[j][0] = make_float2(a[0] * kLog2e, a[1] * kLog2e);
-            a2[j][1] = make_float2(a[2] * kLog2e, a[3] * kLog2e);
-            h[j][0] = make_float2(s[0], s[1]);
-            h[j][1] = make_float2(s[2], s[3]);
-        }
+        auto store_state = [&](float *base, long long row, bool vec) {  // row: of [*, N]
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (ch0 + j < nch)
+#pragma unroll
+                    for (int m = 0; m < NPT; m += 4)
+                        store_n4(base, (row + j) * p.N + n0 + m, n0 + m, p.N, vec, h[j][m / 2].x, h[j][m / 2].y,
+                                 h[j][m / 2 + 1].x, h[j][m / 2 + 1].y);
+        };
         __syncthreads();  // tile 0 staged
         for (int k = 0; k < nt; ++k) {
             const int buf = k & 1;
-            const float *sd = s_d[buf] + ch0, *sb = s_b[buf] + n0, *sc = s_c[kY ? buf : 0] + n0;
-            float *sw = s_w[buf] + ch0;
+            const float *sd = s_d + buf * kT * kDc + ch0, *sb = s_b + buf * kT * kNp + n0, *sc = s_c + buf * kT * kNp + n0;
+            float *sw = s_w + buf * kT * kDc + ch0;
             const int steps = min(kT, ntok - k * kT);  // rounded up to 4 below: the rest of a tile is staged as d = 0
 #pragma unroll 1
             for (int t4 = 0; t4 < steps; t4 += 4) {
-                if (MODE == WALK_CKPT && t4 % kCkpt == 0) {
-                    const long long ck = (long long)b * ((p.L + kCkpt - 1) / kCkpt) + (tb + k * kT + t4) / kCkpt;
-                    const bool vk = p.N % 4 == 0;
+                if (MODE == WALK_CKPT && (k * kT + t4) % kCkpt == 0)
+                    store_state(p.ckpt, ((long long)b * ((p.L + kCkpt - 1) / kCkpt) + (tb + k * kT + t4) / kCkpt) * p.D +
+                                            c0 + ch0, p.N % 4 == 0);
+// d and d x of the four tokens first: y is stored over d x below, and a load after such a
+                // store would have to wait for it.
+                float4 d4[4], w4[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (ch0 + j < nch)
-                            store_n4(p.ckpt, (ck * p.D + c0 + ch0 + j) * p.N + n0, n0, p.N, vk, h[j][0].x, h[j][0].y,
-                                     h[j][1].x, h[j][1].y);
+                for (int tt = 0; tt < 4; ++tt) {
+                    d4[tt] = *reinterpret_cast<const float4 *>(sd + (t4 + tt) * kDc);
+                    w4[tt] = *reinterpret_cast<const float4 *>(sw + (t4 + tt) * kDc);
                 }
+                float v[16];
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt) {
                     const int t = t4 + tt;
-                    const float4 d4 = *reinterpret_cast<const float4 *>(sd + t * kDc);
-                    const float4 w4 = *reinterpret_cast<const float4 *>(sw + t * kDc);
-                    const float4 b4 = *reinterpret_cast<const float4 *>(sb + t * kNp);
-                    const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
-                    const float d[4] = {d4.x, d4.y, d4.z, d4.w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
-                    float v[4];
-                    float2 cc0, cc1;
-                    if (kY) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(sc + t * kNp);
-                        cc0 = make_float2(c4.x, c4.y);
-                        cc1 = make_float2(c4.z, c4.w);
+                    const float d[4] = {d4[tt].x, d4[tt].y, d4[tt].z, d4[tt].w};
+                    const float w[4] = {w4[tt].x, w4[tt].y, w4[tt].z, w4[tt].w};
+                    float2 bb[kH], cc[kH];
+#pragma unroll
+                    for (int m = 0; m < kH; m += 2) {
+                        const float4 b4 = *reinterpret_cast<const float4 *>(sb + t * kNp + 2 * m);
+                        bb[m] = make_float2(b4.x, b4.y);
+                        bb[m + 1] = make_float2(b4.z, b4.w);
+                        if (kY) {
+                            const float4 c4 = *reinterpret_cast<const float4 *>(sc + t * kNp + 2 * m);
+                            cc[m] = make_float2(c4.x, c4.y);
+                            cc[m + 1] = make_float2(c4.z, c4.w);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 dd = dup(d[j]), ww = dup(w[j]);
-                        const float2 e0 = decay2(dd, a2[j][0]), e1 = decay2(dd, a2[j][1]);
-                        if (kRev) {  // a_t (p + ds_t C_t)
-                            h[j][0] = __fmul2_rn(e0, __ffma2_rn(ww, b0, h[j][0]));
-                            h[j][1] = __fmul2_rn(e1, __ffma2_rn(ww, b1, h[j][1]));
-                        } else {
-                            h[j][0] = __ffma2_rn(e0, h[j][0], __fmul2_rn(ww, b0));
-                            h[j][1] = __ffma2_rn(e1, h[j][1], __fmul2_rn(ww, b1));
+                        float2 acc;
+#pragma unroll
+                        for (int m = 0; m < kH; ++m) {
+                            const float2 e = decay2(dd, a2[j][m]);
+                            if (kRev) h[j][m] = __fmul2_rn(e, __ffma2_rn(ww, bb[m], h[j][m]));  // a_t (p + ds_t C_t)
+                            else h[j][m] = __ffma2_rn(e, h[j][m], __fmul2_rn(ww, bb[m]));
+                            if (kY) acc = m == 0 ? __fmul2_rn(h[j][m], cc[m]) : __ffma2_rn(h[j][m], cc[m], acc);
                         }
-                        if (kY) {
-                            const float2 acc = __ffma2_rn(h[j][1], cc1, __fmul2_rn(h[j][0], cc0));
-                            v[j] = acc.x + acc.y;
-                        }
+                        if (kY) v[tt * 4 + j] = acc.x + acc.y;
                         if (MODE == WALK_SEG) sum[j] += d[j];
                     }
-                    if (kY) {
-                        reduce_quad<LPC>(v, lane);
-                        float *o = sw + t * kDc;
-                        if (LPC == 2) *reinterpret_cast<float2 *>(o + 2 * (lane & 1)) = make_float2(v[0], v[1]);
-                        else if (ln < 4) o[ln] = v[0];  // lane bits 1, 0 chose the channel
+                }
+                if (kY) {
+                    const int idx = QuadSum<LPC>::run(v, lane);
+                    constexpr int kLeft = QuadSum<LPC>::kLeft;
+                    float *o = sw + (t4 + (idx >> 2)) * kDc + (idx & 3);
+                    if (kLeft >= 4) {
+#pragma unroll
+                        for (int i = 0; i < kLeft; i += 4)
+                            *reinterpret_cast<float4 *>(o + i / 4 * kDc) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    } else if (kLeft == 2) {
+                        *reinterpret_cast<float2 *>(o) = make_float2(v[0], v[1]);
+                    } else if (ln < 16) {
+                        *o = v[0];
                     }
                 }
             }
             __syncthreads();
         }
-        float *out = nullptr;
-        if (MODE == WALK_Y && seg == p.nseg - 1 && p.final_state) out = p.final_state + (long long)b * p.D * p.N;
-        if (MODE == WALK_SEG) out = p.seg_states + ((long long)b * p.nseg + seg + 1) * p.D * p.N;
-        if (MODE == WALK_ADJ) out = p.adj + ((long long)b * p.nseg + seg - 1) * p.D * p.N;
-        if (out) {
-            const bool vo = aligned_n4(out, p.N);
+        if (MODE == WALK_Y && seg == p.nseg - 1 && p.final_state)
+            store_state(p.final_state, (long long)b * p.D + c0 + ch0, aligned_n4(p.final_state, p.N));
+        if (MODE == WALK_SEG) {
+            store_state(p.seg_states, ((long long)b * p.nseg + seg + 1) * p.D + c0 + ch0, p.N % 4 == 0);
+            if (ln == 0)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (ch0 + j < nch) {
-                    store_n4(out, (long long)(c0 + ch0 + j) * p.N + n0, n0, p.N, vo, h[j][0].x, h[j][0].y, h[j][1].x,
-                             h[j][1].y);
-                    if (MODE == WALK_SEG && ln == 0)
-                        p.seg_sum[((long long)b * p.nseg + seg) * p.D + c0 + ch0 + j] = sum[j];
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (ch0 + j < nch) p.seg_sum[((long long)b * p.nseg + seg) * p.D + c0 + ch0 + j] = sum[j];
         }
+        if (MODE == WALK_ADJ) store_state(p.adj, ((long long)b * p.nseg + seg - 1) * p.D + c0 + ch0, p.N % 4 == 0);
         return;
     }
 
-    // ---- side warps
+    // ---- side warps.  Every chunk is copied, staged and finished by one thread,
+    // so its copies need no barrier but the thread's own wait, and every tensor
+    // is walked by one pointer and one stride.
     const int ta = threadIdx.x - kWalkWarps * 32;
-    const int q = ta % S::kQuads;  // the thread's quad of channels is the same in every unit
-    const int nv = min(4, nch - q * 4);
-    const long long cq = c0 + q * 4;
+    const int q = ta % S::kChunks, tl0 = ta / S::kChunks;
+    const int nv = min(S::kCh, nch - q * S::kCh);
+    const int mine = nv > 0 && tl0 < kT ? ntok : 0;  // tokens for this thread
+    const long long cq = c0 + (nv > 0 ? q * S::kCh : 0);
+    const long long first = kRev ? tb + ntok - 1 - tl0 : tb + tl0, dir = kRev ? -1 : 1;
+    constexpr int kEs = S::kEs, kP = S::kPairs;
+    const bool wide = IO != IO_F32 && p.dt32;  // dt in fp32 beside 16-bit tensors: two chunks
+    const int dts = wide ? 4 : kEs;
+    auto at = [](const void *base, long long bytes) { return static_cast<const char *>(base) + bytes; };
+    const long long dense0 = (long long)p.L * p.D, dense1 = p.D;
     const void *xin = kRev ? p.dy : p.x;
-    const void *bm = kRev ? p.Cm : p.Bm;
-    const long long bb = kRev ? p.cs[0] : p.bs[0], bt = kRev ? p.cs[1] : p.bs[1];
-    const long long xb = kRev ? (long long)p.L * p.D : p.xs[0], xt = kRev ? p.D : p.xs[1];
-    const long long gn = (long long)g * p.N;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f}, skip[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j < nv) {
-            if (p.dt_bias) bias[j] = __ldg(p.dt_bias + cq + j);
-            if (kY && p.Dskip) skip[j] = __ldg(p.Dskip + cq + j);
-        }
+    const long long xb = kRev ? dense0 : p.xs[0], xt = kRev ? dense1 : p.xs[1];
+    const char *lx = at(xin, (b * xb + first * xt + cq) * kEs);
+    const char *ldt = at(p.dt, (b * p.dts[0] + first * p.dts[1] + cq) * dts);
+    const char *lz = at(p.z, (b * p.zs[0] + first * p.zs[1] + cq) * kEs);
+    char *fy = static_cast<char *>(p.y) + (b * dense0 + first * dense1 + cq) * kEs;
+    const long long sx = dir * S::kUStep * xt * kEs, sdt = dir * S::kUStep * p.dts[1] * dts,
+                    sz = dir * S::kUStep * p.zs[1] * kEs, sy = S::kUStep * dense1 * kEs;
+    const int nb = ta % S::kBcChunks * S::kCh, tlb = ta / S::kBcChunks;
+    const int nbv = min(S::kCh, p.N - nb);
+    const int bmine = nbv > 0 && tlb < kT ? ntok : 0;
+    const long long firstb = kRev ? tb + ntok - 1 - tlb : tb + tlb, gn = (long long)g * p.N + (nbv > 0 ? nb : 0);
+    const char *lb = kRev ? at(p.Cm, (b * p.cs[0] + firstb * p.cs[1] + gn) * kEs) : at(p.Bm, (b * p.bs[0] + firstb * p.bs[1] + gn) * kEs);
+    const char *lc = at(p.Cm, (b * p.cs[0] + firstb * p.cs[1] + gn) * kEs);
+    const long long sb = dir * S::kBcStep * (kRev ? p.cs[1] : p.bs[1]) * kEs, sc = (long long)S::kBcStep * p.cs[1] * kEs;
+    // a thread's chunks in a ring slot: x, z, dt, B, C
+    const int slot = WalkSmem<IO, LPC, NPT, MODE>::slot(wide);
+    const int ox = (tl0 * kDc + q * S::kCh) * kEs, oz = S::kRawTile + ox;
+    const int odt = S::kRawTile * (kZ ? 2 : 1) + (tl0 * kDc + q * S::kCh) * dts;
+    const int ob = S::kRawTile * (kZ ? 2 : 1) + kT * kDc * dts + (tlb * kNp + nb) * kEs;
 
-    Raw4 rx[kU], rdt[kU], rz[kRev ? kU : 1], rb[kBu], rc[kY ? kBu : 1];
-    // token of position i of the walk
-    auto token = [&](int i) { return (long long)(kRev ? tb + ntok - 1 - i : tb + i); };
+    float2 bias[kP], skip[kP];
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+        const bool in0 = 2 * j < nv, in1 = 2 * j + 1 < nv;
+        bias[j] = make_float2(in0 && p.dt_bias ? __ldg(p.dt_bias + cq + 2 * j) : 0.f,
+                              in1 && p.dt_bias ? __ldg(p.dt_bias + cq + 2 * j + 1) : 0.f);
+        skip[j] = make_float2(kY && in0 && p.Dskip ? __ldg(p.Dskip + cq + 2 * j) : 0.f,
+                              kY && in1 && p.Dskip ? __ldg(p.Dskip + cq + 2 * j + 1) : 0.f);
+    }
+
     auto load_tile = [&](int k) {
+        if (k < nt) {
+            char *s = ring + k % S::kSlots * slot;
+            int left = mine - k * kT - tl0;  // > 0: the unit's token exists
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kSideThreads * u, i = k * kT + unit / S::kQuads;
-            const bool ok = unit < kT * S::kQuads && i < ntok && nv > 0;
-            const long long t = token(i);
-            rx[u] = load_raw4<IO, VEC>(xin, b * xb + t * xt + cq, ok, nv);
-            rdt[u] = load_raw4_dt<IO, VEC>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, ok, nv, p.dt32);
-            if (kRev) rz[kRev ? u : 0] = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
-        }
-#pragma unroll
-        for (int u = 0; u < kBu; ++u) {
-            const int unit = ta + kSideThreads * u, i = k * kT + unit / LPC, n = unit % LPC * 4;
-            const bool ok = unit < kT * LPC && i < ntok && n < p.N;
-            const long long t = token(i);
-            rb[u] = load_raw4<IO, VEC>(bm, b * bb + t * bt + gn + n, ok, p.N - n);
-            if (kY) rc[kY ? u : 0] = load_raw4<IO, VEC>(p.Cm, b * p.cs[0] + t * p.cs[1] + gn + n, ok, p.N - n);
-        }
-    };
-    auto stage_tile = [&](int k) {
-        const int buf = k & 1;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kSideThreads * u, tl = unit / S::kQuads, i = k * kT + tl;
-            if (unit >= kT * S::kQuads) continue;
-            float d[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f};
-            if (i < ntok && nv > 0) {
-                float x[4], dt[4];
-                unpack4<IO, VEC>(rx[u], x);
-                unpack4_dt<IO, VEC>(rdt[u], dt, p.dt32);
-                float z[4];
-                if (kRev && p.z) unpack4<IO, VEC>(rz[kRev ? u : 0], z);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < nv) {
-                        d[j] = step_of<false>(dt[j], bias[j], p.softplus, p.has_limit, p.dt_min, p.dt_max).d;
-                        if (kRev) w[j] = p.z ? x[j] * silu_fast(z[j]) : x[j];
-                        else w[j] = d[j] * x[j];
+            for (int u = 0; u < kU; ++u) {
+                const int n = left > 0 ? nv : 0;
+                if (tl0 < kT) {
+                    copy_chunk<IO, VEC>(s + ox + u * S::kUStep * kDc * kEs, lx, n);
+                    char *sd = s + odt + u * S::kUStep * kDc * dts;
+                    if (wide) {
+                        copy_chunk<IO_F32, VEC>(sd, ldt, n);
+                        copy_chunk<IO_F32, VEC>(sd + 16, ldt + 16, n - 4);
+                    } else {
+                        copy_chunk<IO, VEC>(sd, ldt, n);
                     }
+                    if (kZ && p.z) copy_chunk<IO, VEC>(s + oz + u * S::kUStep * kDc * kEs, lz, n);
+                }
+                left -= S::kUStep;
+                lx += sx;
+                ldt += sdt;
+                lz += sz;
             }
-            *reinterpret_cast<float4 *>(&s_d[buf][tl * kDc + q * 4]) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4 *>(&s_w[buf][tl * kDc + q * 4]) = make_float4(w[0], w[1], w[2], w[3]);
-        }
+            int leftb = bmine - k * kT - tlb;
 #pragma unroll
-        for (int u = 0; u < kBu; ++u) {
-            const int unit = ta + kSideThreads * u, tl = unit / LPC, n = unit % LPC * 4;
-            if (unit >= kT * LPC) continue;
-            const bool in = k * kT + tl < ntok && n < p.N;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (in) unpack4<IO, VEC>(rb[u], v);
-            *reinterpret_cast<float4 *>(&s_b[buf][tl * kNp + n]) = make_float4(v[0], v[1], v[2], v[3]);
-            if (kY) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                if (in) unpack4<IO, VEC>(rc[kY ? u : 0], c);
-                *reinterpret_cast<float4 *>(&s_c[kY ? buf : 0][kY ? tl * kNp + n : 0]) = make_float4(c[0], c[1], c[2], c[3]);
+            for (int u = 0; u < kBu; ++u) {
+                const int n = leftb > 0 ? nbv : 0;
+                if (tlb < kT) {
+                    copy_chunk<IO, VEC>(s + ob + u * S::kBcStep * kNp * kEs, lb, n);
+                    if (kY) copy_chunk<IO, VEC>(s + ob + S::kRawBc + u * S::kBcStep * kNp * kEs, lc, n);
+                }
+                leftb -= S::kBcStep;
+                lb += sb;
+                lc += sc;
+            }
+        }
+        cp_commit();  // a group per tile, empty ones at the end
+    };
+    const bool flip = ta & 4;
+    auto stage_tile = [&](int k) {
+        const int buf = k & 1, left = mine - k * kT - tl0;
+        const char *s = ring + k % S::kSlots * slot;
+        if (tl0 < kT) {
+            float2 d[kU * kP], w[kU * kP];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                read_chunk<IO>(s + ox + u * S::kUStep * kDc * kEs, w + u * kP);
+                const char *sd = s + odt + u * S::kUStep * kDc * dts;
+                if (wide) {
+                    read_chunk<IO_F32>(sd, d + u * kP);
+                    if (kP == 4) read_chunk<IO_F32>(sd + 16, d + u * kP + 2);
+                } else {
+                    read_chunk<IO>(sd, d + u * kP);
+                }
+#pragma unroll
+                for (int i = 0; i < kP; ++i) d[u * kP + i] = __fadd2_rn(d[u * kP + i], bias[i]);
+            }
+            steps_of<kU * kP>(d, p.softplus, p.has_limit, p.dt_min, p.dt_max);
+            if (!kRev) {
+#pragma unroll
+                for (int i = 0; i < kU * kP; ++i) w[i] = __fmul2_rn(w[i], d[i]);
+            } else if (p.z) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    float2 z[kP];
+                    read_chunk<IO>(s + oz + u * S::kUStep * kDc * kEs, z);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) w[u * kP + i] = __fmul2_rn(w[u * kP + i], silu2(z[i]));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                // no step past the last token or the group's last channel (x is zero there)
+                const int n = left - u * S::kUStep > 0 ? nv : 0;
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    if (2 * i >= n) d[u * kP + i].x = 0.f, w[u * kP + i].x = 0.f;
+                    if (2 * i + 1 >= n) d[u * kP + i].y = 0.f, w[u * kP + i].y = 0.f;
+                }
+                const int o = buf * kT * kDc + (tl0 + u * S::kUStep) * kDc + q * S::kCh;
+                spread<kP>(s_d + o, d + u * kP, flip);
+                spread<kP>(s_w + o, w + u * kP, flip);
+            }
+        }
+        if (tlb < kT) {
+#pragma unroll
+            for (int u = 0; u < kBu; ++u) {  // zeros where nothing was loaded
+                float2 v[kP];
+                const int o = buf * kT * kNp + (tlb + u * S::kBcStep) * kNp + nb;
+                read_chunk<IO>(s + ob + u * S::kBcStep * kNp * kEs, v);
+                spread<kP>(s_b + o, v, flip);
+                if (kY) {
+                    read_chunk<IO>(s + ob + S::kRawBc + u * S::kBcStep * kNp * kEs, v);
+                    spread<kP>(s_c + o, v, flip);
+                }
             }
         }
     };
-    // The epilogue of a tile; its x is read again (a tile or two after its first read, from L1 or L2).
+    // The epilogue of a tile, in two parts: the y that the next staging overwrites is taken first.
+    float2 y[kY ? kU * kP : 1];
+    auto take_tile = [&](int k) {
+        if (tl0 < kT)
+#pragma unroll
+            for (int u = 0; u < (kY ? kU : 0); ++u)
+                gather<kP>(s_w + (k & 1) * kT * kDc + (tl0 + u * S::kUStep) * kDc + q * S::kCh, y + u * kP, flip);
+    };
     auto finish_tile = [&](int k) {
-        Raw4 ex[kU], ez[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kSideThreads * u, i = k * kT + unit / S::kQuads;
-            const bool ok = unit < kT * S::kQuads && i < ntok && nv > 0;
-            const long long t = token(i);
-            ex[u] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + t * p.xs[1] + cq, ok && p.Dskip, nv);
-            ez[u] = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kSideThreads * u, tl = unit / S::kQuads, i = k * kT + tl;
-            if (unit >= kT * S::kQuads || i >= ntok || nv <= 0) continue;
-            const float4 y4 = *reinterpret_cast<const float4 *>(&s_w[k & 1][tl * kDc + q * 4]);
-            float y[4] = {y4.x, y4.y, y4.z, y4.w};
+        const int left = mine - k * kT - tl0;
+        const char *s = ring + k % S::kSlots * slot;
+        if (tl0 < kT) {
             if (p.Dskip) {
-                float x[4];
-                unpack4<IO, VEC>(ex[u], x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = fmaf(skip[j], x[j], y[j]);
+                for (int u = 0; u < (kY ? kU : 0); ++u) {
+                    float2 x[kP];
+                    read_chunk<IO>(s + ox + u * S::kUStep * kDc * kEs, x);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) y[u * kP + i] = __ffma2_rn(skip[i], x[i], y[u * kP + i]);
+                }
             }
             if (p.z) {
-                float z[4];
-                unpack4<IO, VEC>(ez[u], z);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= silu_fast(z[j]);
+                for (int u = 0; u < (kY ? kU : 0); ++u) {
+                    float2 z[kP];
+                    read_chunk<IO>(s + oz + u * S::kUStep * kDc * kEs, z);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) y[u * kP + i] = __fmul2_rn(y[u * kP + i], silu2(z[i]));
+                }
             }
-            store4_io<IO, VEC>(p.y, ((long long)b * p.L + tb + i) * p.D + cq, nv, y);
+        }
+#pragma unroll
+        for (int u = 0; u < (kY ? kU : 0); ++u) {
+            store_chunk<IO, VEC>(fy, left - u * S::kUStep > 0 ? nv : 0, y + u * kP);
+            fy += sy;
         }
     };
 
-    if (nt > 0) {
-        load_tile(0);
-        stage_tile(0);
-        if (nt > 1) load_tile(1);
-    }
+    // Groups committed at the start of iteration k: tiles 0 .. k + kAhead; tile k + 1 is needed.
+    for (int k = 0; k <= S::kAhead; ++k) load_tile(k);
+    cp_wait<S::kAhead>();
+    if (nt > 0) stage_tile(0);
     __syncthreads();
     for (int k = 0; k < nt; ++k) {
-        if (kY && k > 0) finish_tile(k - 1);
+        load_tile(k + 1 + S::kAhead);  // into the slot of tile k - 2, which is finished
+        if (kY && k > 0) take_tile(k - 1);
+        cp_wait<S::kAhead>();
         if (k + 1 < nt) stage_tile(k + 1);
-        if (k + 2 < nt) load_tile(k + 2);
+        if (kY && k > 0) finish_tile(k - 1);
         __syncthreads();
     }
     if (kY) {
-        if (nt > 0) finish_tile(nt - 1);
+        if (nt > 0) take_tile(nt - 1), finish_tile(nt - 1);
         // padding of this segment: zeros
         const int pad0 = tb + ntok, pad1 = min(p.L, tb + p.seg_len);
         const long long n = (long long)max(0, pad1 - pad0) * nch;
@@ -375,34 +488,38 @@ scan_fold_adj_kernel(ScanParams p) {
     }
 }
 
-// Whether every tensor the side warps touch moves in aligned groups of four.
+// Whether every tensor the side warps touch moves in aligned, whole chunks of 16 bytes.
 bool walk_vec(const ScanParams &p, int io, int mode) {
     const long long dense[2] = {(long long)p.L * p.D, p.D};
     const bool adj = mode == WALK_ADJ, y = mode == WALK_Y;
-    return p.D / p.G % 4 == 0 && p.N % 4 == 0 && (adj || vec4_strided(p.x, io, p.xs)) &&
-           vec4_strided(p.dt, p.dt32 ? (int)IO_F32 : io, p.dts) && (adj || vec4_strided(p.Bm, io, p.bs)) &&
-           (!(adj || y) || (vec4_strided(p.Cm, io, p.cs) && (!p.z || vec4_strided(p.z, io, p.zs)))) &&
-           (!y || vec4_strided(p.y, io, dense)) && (!adj || vec4_strided(p.dy, io, dense));
+    const int ch = io == IO_F32 ? 4 : 8;
+    return p.D / p.G % ch == 0 && p.N % ch == 0 && (adj || chunk_strided(p.x, io, p.xs)) &&
+           chunk_strided(p.dt, p.dt32 ? (int)IO_F32 : io, p.dts) && (adj || chunk_strided(p.Bm, io, p.bs)) &&
+           (!(adj || y) || (chunk_strided(p.Cm, io, p.cs) && (!p.z || chunk_strided(p.z, io, p.zs)))) &&
+           (!y || chunk_strided(p.y, io, dense)) && (!adj || chunk_strided(p.dy, io, dense));
 }
 
-template <int IO, int LPC, int MODE>
+template <int IO, int LPC, int NPT, int MODE>
 cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
-    p.tiles = (p.D / p.G + WalkShape<LPC>::kDc - 1) / WalkShape<LPC>::kDc;
+    constexpr int kDc = WalkShape<IO, LPC, NPT>::kDc;
+    p.tiles = (p.D / p.G + kDc - 1) / kDc;
     const int segs = MODE == WALK_SEG || MODE == WALK_ADJ ? p.nseg - 1 : p.nseg;
-    const dim3 grid(p.G * p.tiles, segs, p.B);
-    if (walk_vec(p, IO, MODE)) scan_walk_kernel<IO, LPC, MODE, true><<<grid, kWalkThreads, 0, s>>>(p);
-    else scan_walk_kernel<IO, LPC, MODE, false><<<grid, kWalkThreads, 0, s>>>(p);
+    const int bytes = WalkSmem<IO, LPC, NPT, MODE>::bytes(IO != IO_F32 && p.dt32);
+    auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, NPT, MODE, true> : scan_walk_kernel<IO, LPC, NPT, MODE, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(p.G * p.tiles, segs, p.B), kWalkThreads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int IO, int MODE>
 cudaError_t launch_walk_io(const ScanParams &p, cudaStream_t s) {
     switch (scan_lanes(p.N)) {
-        case 2: return launch_walk_as<IO, 2, MODE>(p, s);
-        case 4: return launch_walk_as<IO, 4, MODE>(p, s);
-        case 8: return launch_walk_as<IO, 8, MODE>(p, s);
-        case 16: return launch_walk_as<IO, 16, MODE>(p, s);
-        case 32: return launch_walk_as<IO, 32, MODE>(p, s);
+        case 2: return launch_walk_as<IO, 2, 4, MODE>(p, s);
+        case 4: return launch_walk_as<IO, 4, 4, MODE>(p, s);
+        case 8: return launch_walk_as<IO, 8, 4, MODE>(p, s);
+        case 16: return launch_walk_as<IO, 16, 4, MODE>(p, s);
+        case 32: return launch_walk_as<IO, 32, 4, MODE>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -30,18 +30,27 @@ namespace {
 
 constexpr int kBw = 4, kBside = 128, kBthreads = kBw * 32 + kBside;
 
-template <int LPC>
+template <int IO, int LPC>
 struct BwdShape {
     static constexpr int kGroups = 32 / LPC;
     static constexpr int kDc = kBw * kGroups * 2;
     static constexpr int kNp = LPC * 4;
-    static constexpr int kT = LPC == 4 || LPC == 8 ? 16 : 8;
-    static constexpr int kQuads = kDc / 4;
-    static constexpr int kUnits = (kT * kQuads + kBside - 1) / kBside;
-    static constexpr int kBcUnits = (kT * LPC + kBside - 1) / kBside;
+    static constexpr int kT = IO != IO_F32 && (LPC == 4 || LPC == 8) ? 16 : 8;
     static constexpr int kTile = kT * kDc;
+    // side threads deal in chunks of 16 bytes, as in the forward
+    static constexpr int kEs = IO == IO_F32 ? 4 : 2, kCh = 16 / kEs, kPairs = kCh / 2;
+    static constexpr int kChunks = kDc / kCh;
+    static constexpr int kUStep = kBside / kChunks < kT ? kBside / kChunks : kT;
+    static constexpr int kUnits = kT / kUStep;
+    static constexpr int kBcChunks = kNp / kCh;
+    static constexpr int kBcStep = kBside / kBcChunks < kT ? kBside / kBcChunks : kT;
+    static constexpr int kBcUnits = kT / kBcStep;
+    static constexpr int kAhead = 1, kSlots = kAhead + 3;
+    static constexpr int kRawTile = kTile * kEs, kRawBc = kT * kNp * kEs;
+    static constexpr int slot(int wide) { return 3 * kRawTile + (wide ? kTile * 4 : kRawTile) + 2 * kRawBc; }  // x, dy, z, dt, B, C
     // floats: d, dx, ds and three results, two buffers; B and C; dB and dC per warp
     static constexpr int kFloats = 2 * (6 * kTile + 2 * kT * kNp + kBw * kT * 2 * kNp);
+    static constexpr int bytes(int wide) { return kFloats * 4 + kSlots * slot(wide); }
 };
 
 // v[0..7] (dB then dC of the lane's four states) summed over the channel
@@ -75,7 +84,7 @@ struct GroupSum {
 template <int IO, int LPC, bool VEC>
 __global__ void __launch_bounds__(kBthreads, 2)
 scan_bwd_kernel(ScanParams p) {
-    using S = BwdShape<LPC>;
+    using S = BwdShape<IO, LPC>;
     constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kTile = S::kTile;
     extern __shared__ __align__(16) float smem[];
     float *s_d = smem, *s_w = s_d + 2 * kTile, *s_g = s_w + 2 * kTile, *s_o = s_g + 2 * kTile;  // s_o[buf][3][kTile]
@@ -93,7 +102,10 @@ scan_bwd_kernel(ScanParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long bseg = (long long)b * p.nseg + seg;
 
+    // Walk warps hold eight tokens' states and need the registers the side warps
+    // do not: 160 and 96 of the 128 a thread is launched with.
     if (warp < kBw) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 2, n0 = ln * 4;
         float2 a2[2][2], q[2][2], da[2][2];
         const float *start = seg < p.nseg - 1 ? p.adj + bseg * p.D * p.N
@@ -154,14 +166,24 @@ scan_bwd_kernel(ScanParams p) {
                         h[j][1] = __ffma2_rn(ww, b1, ah[tt][j][1]);
                     }
                 }
+// A token's values are loaded before the sums of the token after it are
+                // stored: the stores may alias them, as far as the compiler knows.
+                float2 dn, wn, gn;
+                float4 bn, cn;
+                auto load_token = [&](int t) {
+                    dn = *reinterpret_cast<const float2 *>(sd + t * kDc);
+                    wn = *reinterpret_cast<const float2 *>(sw + t * kDc);
+                    gn = *reinterpret_cast<const float2 *>(sg + t * kDc);
+                    bn = *reinterpret_cast<const float4 *>(sb + t * kNp);
+                    cn = *reinterpret_cast<const float4 *>(sc + t * kNp);
+                };
+                load_token(t8 + 7);
 #pragma unroll
                 for (int tt = 7; tt >= 0; --tt) {
                     const int t = t8 + tt;
-                    const float2 d2 = *reinterpret_cast<const float2 *>(sd + t * kDc);
-                    const float2 w2 = *reinterpret_cast<const float2 *>(sw + t * kDc);
-                    const float2 g2 = *reinterpret_cast<const float2 *>(sg + t * kDc);
-                    const float4 b4 = *reinterpret_cast<const float4 *>(sb + t * kNp);
-                    const float4 c4 = *reinterpret_cast<const float4 *>(sc + t * kNp);
+                    const float2 d2 = dn, w2 = wn, g2 = gn;
+                    const float4 b4 = bn, c4 = cn;
+                    if (tt > 0) load_token(t - 1);
                     const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
                     const float2 cc0 = make_float2(c4.x, c4.y), cc1 = make_float2(c4.z, c4.w);
                     float2 db0, db1, dc0, dc1;
@@ -235,89 +257,146 @@ scan_bwd_kernel(ScanParams p) {
     }
 
     // ---- side warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     const int ta = threadIdx.x - kBw * 32;
-    const int qd = ta % S::kQuads;
-    const int nv = min(4, nch - qd * 4);
-    const long long cq = c0 + qd * 4;
-    const long long dense[2] = {(long long)p.L * p.D, p.D};
-    const long long gn = (long long)g * p.N;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f}, skip[4] = {0.f, 0.f, 0.f, 0.f};
-    float acc_d[4] = {0.f, 0.f, 0.f, 0.f}, acc_b[4] = {0.f, 0.f, 0.f, 0.f};
+    const int qd = ta % S::kChunks, tl0 = ta / S::kChunks;
+    const int nv = min(S::kCh, nch - qd * S::kCh);
+    const long long cq = c0 + (nv > 0 ? qd * S::kCh : 0);
+    constexpr int kEs = S::kEs, kP = S::kPairs;
+    const bool wide = IO != IO_F32 && p.dt32;
+    const int dts = wide ? 4 : kEs;
+    const long long dense0 = (long long)p.L * p.D, dense1 = p.D, gn = (long long)g * p.N;
+    auto at = [](const void *base, long long bytes) { return static_cast<const char *>(base) + bytes; };
+    // the thread's place in token tb + tl0 of every tensor; tiles come last first
+    const long long first = tb + tl0;
+    const char *px = at(p.x, (b * p.xs[0] + first * p.xs[1] + cq) * kEs), *pz = at(p.z, (b * p.zs[0] + first * p.zs[1] + cq) * kEs);
+    const char *pdt = at(p.dt, (b * p.dts[0] + first * p.dts[1] + cq) * dts);
+    const long long oy = b * dense0 + first * dense1 + cq;
+    const char *pdy = at(p.dy, oy * kEs);
+    const int nb = ta % S::kBcChunks * S::kCh, tlb = ta / S::kBcChunks, nbv = min(S::kCh, p.N - nb);
+    const char *pb = at(p.Bm, (b * p.bs[0] + (long long)(tb + tlb) * p.bs[1] + gn + (nbv > 0 ? nb : 0)) * kEs);
+    const char *pc = at(p.Cm, (b * p.cs[0] + (long long)(tb + tlb) * p.cs[1] + gn + (nbv > 0 ? nb : 0)) * kEs);
+    char *ring = reinterpret_cast<char *>(smem + S::kFloats);
+    const int slot = S::slot(wide);
+    const int ox = (tl0 * kDc + qd * S::kCh) * kEs, ody = S::kRawTile + ox, oz = 2 * S::kRawTile + ox;
+    const int odt = 3 * S::kRawTile + (tl0 * kDc + qd * S::kCh) * dts;
+    const int ob = 3 * S::kRawTile + kTile * dts + (tlb * kNp + nb) * kEs;
+    const bool flip = ta & 4;
+    float2 bias[kP], skip[kP], acc_d[kP], acc_b[kP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j < nv) {
-            if (p.dt_bias) bias[j] = __ldg(p.dt_bias + cq + j);
-            if (p.Dskip) skip[j] = __ldg(p.Dskip + cq + j);
-        }
-    Raw4 rx[kU], rdt[kU], rdy[kU], rz[kU], rb[kBu], rc[kBu];
-    auto load_unit = [&](long long t, bool ok, Raw4 &x, Raw4 &dt, Raw4 &dy, Raw4 &z) {
-        x = load_raw4<IO, VEC>(p.x, b * p.xs[0] + t * p.xs[1] + cq, ok, nv);
-        dt = load_raw4_dt<IO, VEC>(p.dt, b * p.dts[0] + t * p.dts[1] + cq, ok, nv, p.dt32);
-        dy = load_raw4<IO, VEC>(p.dy, b * dense[0] + t * dense[1] + cq, ok, nv);
-        z = load_raw4<IO, VEC>(p.z, b * p.zs[0] + t * p.zs[1] + cq, ok && p.z, nv);
-    };
+    for (int j = 0; j < kP; ++j) {
+        const bool in0 = 2 * j < nv, in1 = 2 * j + 1 < nv;
+        bias[j] = make_float2(in0 && p.dt_bias ? __ldg(p.dt_bias + cq + 2 * j) : 0.f,
+                              in1 && p.dt_bias ? __ldg(p.dt_bias + cq + 2 * j + 1) : 0.f);
+        skip[j] = make_float2(in0 && p.Dskip ? __ldg(p.Dskip + cq + 2 * j) : 0.f,
+                              in1 && p.Dskip ? __ldg(p.Dskip + cq + 2 * j + 1) : 0.f);
+        acc_d[j] = acc_b[j] = dup(0.f);
+    }
     auto load_tile = [&](int i) {
-        const int k = nt - 1 - i;
+        if (i < nt) {
+            const int k = nt - 1 - i;
+            char *s = ring + i % S::kSlots * slot;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kBside * u, t = k * kT + unit / S::kQuads;
-            load_unit(tb + t, unit < kT * S::kQuads && t < ntok && nv > 0, rx[u], rdt[u], rdy[u], rz[u]);
-        }
+            for (int u = 0; u < kU; ++u) {
+                const long long t = k * kT + u * S::kUStep;  // from the thread's first token
+                const int n = tl0 + t < ntok ? nv : 0;
+                if (tl0 < kT) {
+                    char *d = s + u * S::kUStep * kDc * kEs;
+                    copy_chunk<IO, VEC>(d + ox, px + t * p.xs[1] * kEs, n);
+                    copy_chunk<IO, VEC>(d + ody, pdy + t * dense1 * kEs, n);
+                    if (p.z) copy_chunk<IO, VEC>(d + oz, pz + t * p.zs[1] * kEs, n);
+                    char *sd = s + odt + u * S::kUStep * kDc * dts;
+                    const char *src = pdt + t * p.dts[1] * dts;
+                    if (wide) {
+                        copy_chunk<IO_F32, VEC>(sd, src, n);
+                        copy_chunk<IO_F32, VEC>(sd + 16, src + 16, n - 4);
+                    } else {
+                        copy_chunk<IO, VEC>(sd, src, n);
+                    }
+                }
+            }
 #pragma unroll
-        for (int u = 0; u < kBu; ++u) {
-            const int unit = ta + kBside * u, t = k * kT + unit / LPC, n = unit % LPC * 4;
-            const bool ok = unit < kT * LPC && t < ntok && n < p.N;
-            rb[u] = load_raw4<IO, VEC>(p.Bm, b * p.bs[0] + (long long)(tb + t) * p.bs[1] + gn + n, ok, p.N - n);
-            rc[u] = load_raw4<IO, VEC>(p.Cm, b * p.cs[0] + (long long)(tb + t) * p.cs[1] + gn + n, ok, p.N - n);
+            for (int u = 0; u < kBu; ++u) {
+                const long long t = k * kT + u * S::kBcStep;
+                const int n = tlb + t < ntok ? nbv : 0;
+                if (tlb < kT) {
+                    copy_chunk<IO, VEC>(s + ob + u * S::kBcStep * kNp * kEs, pb + t * p.bs[1] * kEs, n);
+                    copy_chunk<IO, VEC>(s + ob + S::kRawBc + u * S::kBcStep * kNp * kEs, pc + t * p.cs[1] * kEs, n);
+                }
+            }
         }
+        cp_commit();
     };
     auto stage_tile = [&](int i) {
         const int buf = i & 1, k = nt - 1 - i;
+        const char *s = ring + i % S::kSlots * slot;
+        if (tl0 < kT) {
+            float2 d[kU * kP];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kBside * u, tl = unit / S::kQuads;
-            if (unit >= kT * S::kQuads) continue;
-            float d[4] = {0.f, 0.f, 0.f, 0.f}, w[4] = {0.f, 0.f, 0.f, 0.f}, gg[4] = {0.f, 0.f, 0.f, 0.f};
-            if (k * kT + tl < ntok && nv > 0) {
-                float x[4], dt[4], dy[4], z[4];
-                unpack4<IO, VEC>(rx[u], x);
-                unpack4_dt<IO, VEC>(rdt[u], dt, p.dt32);
-                unpack4<IO, VEC>(rdy[u], dy);
-                if (p.z) unpack4<IO, VEC>(rz[u], z);
+            for (int u = 0; u < kU; ++u) {
+                const char *sd = s + odt + u * S::kUStep * kDc * dts;
+                if (wide) {
+                    read_chunk<IO_F32>(sd, d + u * kP);
+                    if (kP == 4) read_chunk<IO_F32>(sd + 16, d + u * kP + 2);
+                } else {
+                    read_chunk<IO>(sd, d + u * kP);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < nv) {
-                        d[j] = step_of<false>(dt[j], bias[j], p.softplus, p.has_limit, p.dt_min, p.dt_max).d;
-                        w[j] = d[j] * x[j];
-                        gg[j] = p.z ? dy[j] * silu_fast(z[j]) : dy[j];
-                    }
+                for (int j = 0; j < kP; ++j) d[u * kP + j] = __fadd2_rn(d[u * kP + j], bias[j]);
             }
-            const int o = buf * kTile + tl * kDc + qd * 4;
-            *reinterpret_cast<float4 *>(s_d + o) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4 *>(s_w + o) = make_float4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<float4 *>(s_g + o) = make_float4(gg[0], gg[1], gg[2], gg[3]);
-        }
+            steps_of<kU * kP>(d, p.softplus, p.has_limit, p.dt_min, p.dt_max);
 #pragma unroll
-        for (int u = 0; u < kBu; ++u) {
-            const int unit = ta + kBside * u, tl = unit / LPC, n = unit % LPC * 4;
-            if (unit >= kT * LPC) continue;
-            float v[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
-            if (k * kT + tl < ntok && n < p.N) {
-                unpack4<IO, VEC>(rb[u], v);
-                unpack4<IO, VEC>(rc[u], c);
+            for (int u = 0; u < kU; ++u) {
+                const int n = k * kT + tl0 + u * S::kUStep < ntok ? nv : 0;  // nothing past the last token or channel
+                float2 v[kP];
+                const char *c = s + u * S::kUStep * kDc * kEs;
+                const int o = buf * kTile + (tl0 + u * S::kUStep) * kDc + qd * S::kCh;
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    if (2 * j >= n) d[u * kP + j].x = 0.f;
+                    if (2 * j + 1 >= n) d[u * kP + j].y = 0.f;
+                }
+                spread<kP>(s_d + o, d + u * kP, flip);
+                read_chunk<IO>(c + ox, v);  // zeros where nothing was loaded
+#pragma unroll
+                for (int j = 0; j < kP; ++j) v[j] = __fmul2_rn(v[j], d[u * kP + j]);
+                spread<kP>(s_w + o, v, flip);
+                read_chunk<IO>(c + ody, v);
+                if (p.z) {
+                    float2 z[kP];
+                    read_chunk<IO>(c + oz, z);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) v[j] = __fmul2_rn(v[j], silu2(z[j]));
+                }
+                spread<kP>(s_g + o, v, flip);
             }
-            *reinterpret_cast<float4 *>(s_b + (buf * kT + tl) * kNp + n) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(s_c + (buf * kT + tl) * kNp + n) = make_float4(c[0], c[1], c[2], c[3]);
         }
+        if (tlb < kT) {
+#pragma unroll
+            for (int u = 0; u < kBu; ++u) {
+                float2 v[kP];
+                const int o = buf * kT * kNp + (tlb + u * S::kBcStep) * kNp + nb;
+                read_chunk<IO>(s + ob + u * S::kBcStep * kNp * kEs, v);
+                spread<kP>(s_b + o, v, flip);
+                read_chunk<IO>(s + ob + S::kRawBc + u * S::kBcStep * kNp * kEs, v);
+                spread<kP>(s_c + o, v, flip);
+            }
+        }
+    };
+    // A tile's d and ds are taken before the next staging overwrites them.
+    float2 td[kU * kP], tg[kU * kP];
+    auto take_tile = [&](int i) {
+        if (tl0 < kT)
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int o = (i & 1) * kTile + (tl0 + u * S::kUStep) * kDc + qd * S::kCh;
+                gather<kP>(s_d + o, td + u * kP, flip);
+                gather<kP>(s_g + o, tg + u * kP, flip);
+            }
     };
     auto finish_tile = [&](int i) {
         const int buf = i & 1, k = nt - 1 - i;
-        Raw4 ex[kU], edt[kU], edy[kU], ez[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kBside * u, t = k * kT + unit / S::kQuads;
-            load_unit(tb + t, unit < kT * S::kQuads && t < ntok && nv > 0, ex[u], edt[u], edy[u], ez[u]);
-        }
+        const char *s = ring + i % S::kSlots * slot;
         // dB and dC of the tile over the walk warps
         for (int e = ta; e < kT * 2 * kNp; e += kBside) {
             const int t = k * kT + e / (2 * kNp);
@@ -328,65 +407,83 @@ scan_bwd_kernel(ScanParams p) {
             for (int w = 1; w < kBw; ++w) v += sp[w * kT * 2 * kNp];
             p.part_bc[(((long long)blockIdx.x * p.B + b) * p.L + tb + t) * 2 * kNp + e % (2 * kNp)] = v;
         }
+        if (tl0 >= kT) return;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int unit = ta + kBside * u, tl = unit / S::kQuads, t = k * kT + tl;
-            if (unit >= kT * S::kQuads || t >= ntok || nv <= 0) continue;
-            const int o = tl * kDc + qd * 4;
-            const float4 d4 = *reinterpret_cast<const float4 *>(s_d + buf * kTile + o);
-            const float4 g4 = *reinterpret_cast<const float4 *>(s_g + buf * kTile + o);
-            const float4 b4 = *reinterpret_cast<const float4 *>(s_o + (buf * 3 + 0) * kTile + o);
-            const float4 r4 = *reinterpret_cast<const float4 *>(s_o + (buf * 3 + 1) * kTile + o);
-            const float4 c4 = *reinterpret_cast<const float4 *>(s_o + (buf * 3 + 2) * kTile + o);
-            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, ds[4] = {g4.x, g4.y, g4.z, g4.w};
-            const float qb[4] = {b4.x, b4.y, b4.z, b4.w}, qr[4] = {r4.x, r4.y, r4.z, r4.w};
-            const float hc[4] = {c4.x, c4.y, c4.z, c4.w};
-            float x[4], dt[4], dx[4], ddt[4];
-            unpack4<IO, VEC>(ex[u], x);
-            unpack4_dt<IO, VEC>(edt[u], dt, p.dt32);
+            const int t = k * kT + u * S::kUStep;  // from the thread's first token
+            const int n = tl0 + t < ntok ? nv : 0;
+            const int o = (tl0 + u * S::kUStep) * kDc + qd * S::kCh;
+            const char *c = s + u * S::kUStep * kDc * kEs;
+            float2 x[kP], qb[kP], v[kP], sig[kP];
+            read_chunk<IO>(c + ox, x);
+            gather<kP>(s_o + (buf * 3 + 0) * kTile + o, qb, flip);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float sig = p.softplus ? sigmoid_f(dt[j] + bias[j]) : 1.f;
-                if (p.has_limit)
-                    sig = step_of<true>(dt[j], bias[j], p.softplus, p.has_limit, p.dt_min, p.dt_max).sig;
-                dx[j] = fmaf(d[j], qb[j], skip[j] * ds[j]);
-                ddt[j] = fmaf(x[j], qb[j], kLn2 * qr[j]) * sig;
-                if (j < nv) {
-                    acc_d[j] = fmaf(ds[j], x[j], acc_d[j]);
-                    acc_b[j] += ddt[j];
-                }
+            for (int j = 0; j < kP; ++j) {
+                const float2 g2 = tg[u * kP + j];
+                v[j] = __ffma2_rn(td[u * kP + j], qb[j], __fmul2_rn(skip[j], g2));
+                acc_d[j] = __ffma2_rn(g2, x[j], acc_d[j]);  // both zero past the last token
             }
-            const long long at = ((long long)b * p.L + tb + t) * p.D + cq;
-            store4_io<IO, VEC>(p.dx, at, nv, dx);
-            if (IO != IO_F32 && p.dt32) store4_io<IO_F32, VEC>(p.ddt, at, nv, ddt);
-            else store4_io<IO, VEC>(p.ddt, at, nv, ddt);
-            if (p.z) {
-                float z[4], dy[4], dz[4];
-                unpack4<IO, VEC>(ez[u], z);
-                unpack4<IO, VEC>(edy[u], dy);
+            const long long row = oy + t * dense1;
+            store_chunk<IO, VEC>(static_cast<char *>(p.dx) + row * kEs, n, v);
+            const char *sd = s + odt + u * S::kUStep * kDc * dts;
+            if (wide) {
+                read_chunk<IO_F32>(sd, sig);
+                if (kP == 4) read_chunk<IO_F32>(sd + 16, sig + 2);
+            } else {
+                read_chunk<IO>(sd, sig);
+            }
+            gather<kP>(s_o + (buf * 3 + 1) * kTile + o, v, flip);
+            if (p.has_limit) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float sg = sigmoid_f(z[j]);
-                    dz[j] = dy[j] * fmaf(skip[j], x[j], hc[j]) * (sg * fmaf(z[j], 1.f - sg, 1.f));
+                for (int j = 0; j < kP; ++j)
+                    sig[j] = make_float2(step_of<true>(sig[j].x, bias[j].x, p.softplus, 1, p.dt_min, p.dt_max).sig,
+                                         step_of<true>(sig[j].y, bias[j].y, p.softplus, 1, p.dt_min, p.dt_max).sig);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) sig[j] = p.softplus ? sigmoid2(__fadd2_rn(sig[j], bias[j])) : dup(1.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+                v[j] = __fmul2_rn(__ffma2_rn(x[j], qb[j], __fmul2_rn(dup(kLn2), v[j])), sig[j]);
+                if (2 * j < n) acc_b[j].x += v[j].x;
+                if (2 * j + 1 < n) acc_b[j].y += v[j].y;
+            }
+            if (wide) {
+                char *dst = static_cast<char *>(p.ddt) + row * 4;
+                store_chunk<IO_F32, VEC>(dst, n, v);
+                if (kP == 4) store_chunk<IO_F32, VEC>(dst + 16, n - 4, v + 2);
+            } else {
+                store_chunk<IO, VEC>(static_cast<char *>(p.ddt) + row * kEs, n, v);
+            }
+            if (p.z) {
+                float2 z[kP], dy[kP];
+                read_chunk<IO>(c + oz, z);
+                read_chunk<IO>(c + ody, dy);
+                gather<kP>(s_o + (buf * 3 + 2) * kTile + o, v, flip);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const float2 sg = sigmoid2(z[j]);
+                    const float2 slope = __fmul2_rn(sg, __ffma2_rn(z[j], __fadd2_rn(dup(1.f), make_float2(-sg.x, -sg.y)), dup(1.f)));
+                    v[j] = __fmul2_rn(__fmul2_rn(dy[j], __ffma2_rn(skip[j], x[j], v[j])), slope);
                 }
-                store4_io<IO, VEC>(p.dz, at, nv, dz);
+                store_chunk<IO, VEC>(static_cast<char *>(p.dz) + row * kEs, n, v);
             }
         }
     };
 
-    if (nt > 0) {
-        load_tile(0);
-        stage_tile(0);
-        if (nt > 1) load_tile(1);
-    }
+    for (int i = 0; i <= S::kAhead; ++i) load_tile(i);
+    cp_wait<S::kAhead>();
+    if (nt > 0) stage_tile(0);
     __syncthreads();
     for (int i = 0; i < nt; ++i) {
-        if (i > 0) finish_tile(i - 1);
+        load_tile(i + 1 + S::kAhead);
+        if (i > 0) take_tile(i - 1);
+        cp_wait<S::kAhead>();
         if (i + 1 < nt) stage_tile(i + 1);
-        if (i + 2 < nt) load_tile(i + 2);
+        if (i > 0) finish_tile(i - 1);
         __syncthreads();
     }
-    if (nt > 0) finish_tile(nt - 1);
+    if (nt > 0) take_tile(nt - 1), finish_tile(nt - 1);
     {  // padding of this segment: zeros
         const int pad0 = tb + ntok, pad1 = min(p.L, tb + p.seg_len);
         const long long n = (long long)max(0, pad1 - pad0) * nch;
@@ -400,24 +497,26 @@ scan_bwd_kernel(ScanParams p) {
     }
     // dD and ddt_bias over the threads of a quad, in order
     __syncthreads();
-    float *red = s_p;  // [kBside][8]
+    float *red = s_p;  // [kBside][2 kCh]
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        red[ta * 8 + j] = acc_d[j];
-        red[ta * 8 + 4 + j] = acc_b[j];
+    for (int j = 0; j < kP; ++j) {
+        *reinterpret_cast<float2 *>(red + ta * 2 * S::kCh + 2 * j) = acc_d[j];
+        *reinterpret_cast<float2 *>(red + ta * 2 * S::kCh + S::kCh + 2 * j) = acc_b[j];
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kBside) : "memory");
-    if (ta < S::kQuads && nv > 0) {
-        float s[8];
+    if (ta < S::kChunks && nv > 0) {
+        float s[2 * S::kCh];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = 0.f;
-        for (int y = ta; y < kBside; y += S::kQuads)
+        for (int j = 0; j < 2 * S::kCh; ++j) s[j] = 0.f;
+        for (int y = ta; y < kBside; y += S::kChunks)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] += red[y * 8 + j];
-        for (int j = 0; j < nv; ++j) {
-            p.part_d[bseg * p.D + cq + j] = s[j];
-            p.part_d[((long long)p.B * p.nseg + bseg) * p.D + cq + j] = s[4 + j];
-        }
+            for (int j = 0; j < 2 * S::kCh; ++j) s[j] += red[y * 2 * S::kCh + j];
+#pragma unroll
+        for (int j = 0; j < S::kCh; ++j)
+            if (j < nv) {
+                p.part_d[bseg * p.D + cq + j] = s[j];
+                p.part_d[((long long)p.B * p.nseg + bseg) * p.D + cq + j] = s[S::kCh + j];
+            }
     }
 }
 
@@ -463,22 +562,22 @@ scan_bwd_bc_kernel(ScanParams p, int np, void *dB, void *dC) {
 
 bool bwd_vec(const ScanParams &p, int io) {
     const long long dense[2] = {(long long)p.L * p.D, p.D};
-    const int dio = p.dt32 ? (int)IO_F32 : io;
-    return p.D / p.G % 4 == 0 && p.N % 4 == 0 && vec4_strided(p.x, io, p.xs) && vec4_strided(p.dt, dio, p.dts) &&
-           vec4_strided(p.Bm, io, p.bs) && vec4_strided(p.Cm, io, p.cs) && (!p.z || vec4_strided(p.z, io, p.zs)) &&
-           vec4_strided(p.dy, io, dense) && vec4_strided(p.dx, io, dense) && vec4_strided(p.ddt, dio, dense) &&
-           (!p.z || vec4_strided(p.dz, io, dense));
+    const int ch = io == IO_F32 ? 4 : 8, dio = p.dt32 ? (int)IO_F32 : io;
+    return p.D / p.G % ch == 0 && p.N % ch == 0 && chunk_strided(p.x, io, p.xs) && chunk_strided(p.dt, dio, p.dts) &&
+           chunk_strided(p.Bm, io, p.bs) && chunk_strided(p.Cm, io, p.cs) && (!p.z || chunk_strided(p.z, io, p.zs)) &&
+           chunk_strided(p.dy, io, dense) && chunk_strided(p.dx, io, dense) && chunk_strided(p.ddt, dio, dense) &&
+           (!p.z || chunk_strided(p.dz, io, dense));
 }
 
 template <int IO, int LPC>
 cudaError_t launch_bwd_as(ScanParams p, void *dB, void *dC, cudaStream_t s) {
-    using S = BwdShape<LPC>;
-    constexpr int kBytes = S::kFloats * (int)sizeof(float);
+    using S = BwdShape<IO, LPC>;
+    const int bytes = S::bytes(IO != IO_F32 && p.dt32);
     p.tiles = scan_bwd_tiles(p);
     auto *kernel = bwd_vec(p, IO) ? scan_bwd_kernel<IO, LPC, true> : scan_bwd_kernel<IO, LPC, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, kBytes, s>>>(p);
+    kernel<<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, bytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long per = (long long)p.B * p.L * 2 * S::kNp;
     scan_bwd_bc_kernel<IO><<<dim3((unsigned)((per + 255) / 256), p.G), 256, 0, s>>>(p, S::kNp, dB, dC);

@@ -100,33 +100,48 @@ SIGNATURES = {
 }
 
 _CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_byref = ctypes.byref
+_pkg = None
 
 
 def _host():
-    """The package's loader and error check (imported late: the package imports this module)."""
-    import mamba_ssd_chunked_fwd_gb300 as pkg
-    return pkg
+    """The package (its loader and error check); imported late, since it imports this module."""
+    global _pkg
+    if _pkg is None:
+        import mamba_ssd_chunked_fwd_gb300 as _pkg_module
+        _pkg = _pkg_module
+    return _pkg
 
 
-def _call(name, args, device):
-    pkg = _host()
-    with torch.cuda.device(device):
-        pkg._check(getattr(pkg.load_library(), name)(ctypes.byref(args), pkg._stream_handle(device)), name)
+def _call(name, args, dev):
+    """One C entry on the current stream of CUDA device ``dev``."""
+    pkg = _pkg or _host()
+    fn = getattr(pkg._lib or pkg.load_library(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(_byref(args), torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(_byref(args), torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        pkg._check(status, name)
 
 
-def _bytes(name, args, device):
-    pkg = _host()
-    out = _size(0)
-    with torch.cuda.device(device):
-        pkg._check(getattr(pkg.load_library(), name)(ctypes.byref(args), ctypes.byref(out)), name)
-    return int(out.value)
-
-
-def _work(name, args, device):
-    """Sizes args' workspace by the library's query and allocates it; the tensor must outlive the call."""
-    n = _bytes(name, args, device)
-    ws = torch.empty(max(n, 256), device=device, dtype=torch.uint8)
-    args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
+def _work(name, args, t):
+    """Sizes args' workspace by the library's query and allocates it on t's
+    device; the caller holds the tensor until its call is enqueued."""
+    pkg, dev, out = _pkg or _host(), t.get_device(), _size(0)
+    fn = getattr(pkg._lib or pkg.load_library(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(_byref(args), _byref(out))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(_byref(args), _byref(out))
+    if status:
+        pkg._check(status, name)
+    if not out.value:
+        return None
+    ws = torch.empty(out.value, device=t.device, dtype=torch.uint8)
+    args.workspace, args.workspace_bytes = ws.data_ptr(), out.value
     return ws
 
 
@@ -137,62 +152,72 @@ def _code(t, what):
     return code
 
 
-def _dense(t, shape, dtype, device, what):
+def _refuse(t, shape, dtype, dev, what):
+    """Says which of the checks a tensor fails (none: it is not dense)."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, expected CUDA device {dev}")
+    raise ValueError(f"{what}: must be contiguous")
+
+
+def _dense(t, shape, dtype, dev, what):
     """The address of a dense tensor of this shape and type, or None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, shape, dtype, dev, what)
     return t.data_ptr()
 
 
-def _tokens(t, shape, dtype, device, what):
+def _inner_dense(shape, st, lead):
+    """Whether the dimensions after the first ``lead`` are dense among themselves."""
+    want = 1
+    for n, s in zip(reversed(shape[lead:]), reversed(st[lead:])):
+        if n != 1 and s != want:
+            return False
+        want *= n
+    return True
+
+
+_DENSE = (0, 0)
+
+
+def _tokens(t, shape, dtype, dev, what):
     """(address, (batch stride, token stride)) of a [B,L,...] tensor whose tokens are dense."""
     if t is None:
-        return None, (0, 0)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if t.numel() and not t[0, 0].is_contiguous():
+        return None, _DENSE
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, shape, dtype, dev, what)
+    if t.is_contiguous():
+        return t.data_ptr(), _DENSE
+    st = t.stride()
+    if not _inner_dense(shape, st, 2):
         raise ValueError(f"{what}: the values of a token must be contiguous")
-    if t.numel() and any(s < 0 for s in t.stride()):
-        raise ValueError(f"{what}: negative strides")
-    st = [int(t.stride(0)), int(t.stride(1))]
-    if t.shape[0] == 1:
-        st[0] = 0
-    if t.shape[1] == 1:
-        st[1] = 0
-    if st == [0, 0] and (t.shape[0] > 1 or t.shape[1] > 1):
+    st = (0 if shape[0] == 1 else st[0], 0 if shape[1] == 1 else st[1])
+    if st == _DENSE and t.numel():
         raise ValueError(f"{what}: broadcast over every token")
-    return t.data_ptr(), tuple(st)
+    return t.data_ptr(), st
 
 
-def _rows(t, shape, dtype, device, what):
+def _rows(t, shape, dtype, dev, what):
     """(address, row stride) of a [B,...] tensor whose rows are dense."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if t.numel() and not t[0].is_contiguous():
-        raise ValueError(f"{what}: the values of a row must be contiguous")
-    if t.shape[0] == 1:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, shape, dtype, dev, what)
+    if t.is_contiguous():
         return t.data_ptr(), 0
-    if t.stride(0) <= 0:
+    st = t.stride()
+    if not _inner_dense(shape, st, 1):
+        raise ValueError(f"{what}: the values of a row must be contiguous")
+    if shape[0] == 1:
+        return t.data_ptr(), 0
+    if st[0] <= 0:
         raise ValueError(f"{what}: rows must be apart")
-    return t.data_ptr(), int(t.stride(0))
+    return t.data_ptr(), st[0]
 
 
 def _ndim(t, n, what):
@@ -205,9 +230,9 @@ def _cuda(t, name):
         raise ValueError(f"{name} takes CUDA tensors")
 
 
-def _dt_dtype(x, dt, what="dt"):
-    if dt.dtype not in (x.dtype, torch.float32):
-        raise ValueError(f"{what}: dtype {dt.dtype}, expected {x.dtype} or torch.float32")
+def _dt_dtype(x, dt):
+    if dt.dtype is not x.dtype and dt.dtype is not torch.float32:
+        raise ValueError(f"dt: dtype {dt.dtype}, expected {x.dtype} or torch.float32")
     return dt.dtype
 
 
@@ -218,27 +243,22 @@ def make_scan_args(x, dt, A, B, C, *, y=None, final_state=None, D=None, z=None, 
     """Fill an ``ssd_scan_args`` from tensors (no copies).  x, dt, z [B,L,D] and
     B, C [B,L,G,N] may be strided over batch and tokens."""
     _ndim(x, 3, "x"), _ndim(B, 4, "B"), _ndim(A, 2, "A")
-    (Bb, L, Dm), (G, N), dev, f32 = x.shape, B.shape[2:], x.device, torch.float32
-    a = SsdScanArgs()
-    a.B, a.L, a.D, a.N, a.G = Bb, L, Dm, N, G
-    a.x_dtype = _code(x, "x")
-    dtt = _dt_dtype(x, dt)
-    a.dt_dtype = _CODES[dtt]
-    a.x, a.x_stride[:] = _tokens(x, (Bb, L, Dm), x.dtype, dev, "x")
-    a.dt, a.dt_stride[:] = _tokens(dt, (Bb, L, Dm), dtt, dev, "dt")
-    a.z, a.z_stride[:] = _tokens(z, (Bb, L, Dm), x.dtype, dev, "z")
-    a.Bm, a.b_stride[:] = _tokens(B, (Bb, L, G, N), x.dtype, dev, "B")
-    a.Cm, a.c_stride[:] = _tokens(C, (Bb, L, G, N), x.dtype, dev, "C")
-    a.A = _dense(A, (Dm, N), f32, dev, "A")
-    a.Dskip = _dense(D, (Dm,), f32, dev, "D")
-    a.dt_bias = _dense(dt_bias, (Dm,), f32, dev, "dt_bias")
-    a.initial_state = _dense(initial_states, (Bb, Dm, N), f32, dev, "initial_states")
-    a.lengths = _dense(lengths, (Bb,), torch.int32, dev, "lengths")
-    a.y = _dense(y, (Bb, L, Dm), x.dtype, dev, "y")
-    a.final_state = _dense(final_state, (Bb, Dm, N), f32, dev, "final_state")
-    a.dt_softplus = 1 if dt_softplus else 0
-    a.dt_min, a.dt_max = float(dt_limit[0]), float(dt_limit[1])
-    return a
+    xs, dev, f32, io = x.shape, x.get_device(), torch.float32, x.dtype
+    Bb, L, Dm = xs
+    bc = (Bb, L, B.shape[2], B.shape[3])
+    N = bc[3]
+    code, dtt, state = _code(x, "x"), _dt_dtype(x, dt), (Bb, Dm, N)
+    px, sx = _tokens(x, xs, io, dev, "x")
+    pdt, sdt = _tokens(dt, xs, dtt, dev, "dt")
+    pz, sz = _tokens(z, xs, io, dev, "z")
+    pb, sb = _tokens(B, bc, io, dev, "B")
+    pc, sc = _tokens(C, bc, io, dev, "C")
+    return SsdScanArgs(
+        Bb, L, Dm, N, bc[2], px, pdt, _dense(A, (Dm, N), f32, dev, "A"), pb, pc, _dense(D, (Dm,), f32, dev, "D"), pz,
+        _dense(dt_bias, (Dm,), f32, dev, "dt_bias"), _dense(initial_states, state, f32, dev, "initial_states"),
+        _dense(lengths, (Bb,), torch.int32, dev, "lengths"), _dense(y, xs, io, dev, "y"),
+        _dense(final_state, state, f32, dev, "final_state"), sx, sdt, sz, sb, sc, code, _CODES[dtt],
+        1 if dt_softplus else 0, dt_limit[0], dt_limit[1])
 
 
 def selective_scan(x, dt, A, B, C, dt_softplus=False, return_final_state=False, *, D=None, z=None, dt_bias=None,
@@ -258,8 +278,8 @@ def selective_scan(x, dt, A, B, C, dt_softplus=False, return_final_state=False, 
     fin = torch.empty((x.shape[0], x.shape[2], A.shape[1]), device=x.device, dtype=torch.float32) if return_final_state else None
     a = make_scan_args(x, dt, A, B, C, y=y, final_state=fin, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
                        lengths=lengths, dt_softplus=dt_softplus, dt_limit=dt_limit)
-    ws = _work("ssd_selective_scan_workspace_size", a, x.device)  # noqa: F841
-    _call("ssd_selective_scan", a, x.device)
+    ws = _work("ssd_selective_scan_workspace_size", a, x)  # noqa: F841
+    _call("ssd_selective_scan", a, x.get_device())
     return (y, fin) if return_final_state else y
 
 
@@ -279,8 +299,8 @@ def selective_scan_bwd(x, dt, A, B, C, dy, dt_softplus=False, *, dfinal=None, D=
     a.fwd = make_scan_args(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states, lengths=lengths,
                            dt_softplus=dt_softplus, dt_limit=dt_limit)
     state = (x.shape[0], x.shape[2], A.shape[1])
-    a.dy = _dense(dy, x.shape, x.dtype, dev, "dy")
-    a.dfinal = _dense(dfinal, state, f32, dev, "dfinal")
+    a.dy = _dense(dy, x.shape, x.dtype, x.get_device(), "dy")
+    a.dfinal = _dense(dfinal, state, f32, x.get_device(), "dfinal")
     g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C)}
     if D is not None:
         g["dD"] = like(D)
@@ -292,8 +312,8 @@ def selective_scan_bwd(x, dt, A, B, C, dy, dt_softplus=False, *, dfinal=None, D=
         g["dh0"] = torch.empty(state, device=dev, dtype=f32)
     for k, t in g.items():
         setattr(a, k, t.data_ptr())
-    ws = _work("ssd_selective_scan_bwd_workspace_size", a, dev)  # noqa: F841
-    _call("ssd_selective_scan_bwd", a, dev)
+    ws = _work("ssd_selective_scan_bwd_workspace_size", a, x)  # noqa: F841
+    _call("ssd_selective_scan_bwd", a, x.get_device())
     return g
 
 
@@ -306,28 +326,24 @@ def selective_scan_step(x, dt, A, B, C, state, dt_softplus=False, *, state_out=N
     state.  Rows must not share a slot."""
     _cuda(x, "selective_scan_step")
     _ndim(x, 2, "x"), _ndim(B, 3, "B"), _ndim(state, 3, "state"), _ndim(A, 2, "A")
-    (Bb, Dm), (G, N), dev, f32 = x.shape, B.shape[1:], x.device, torch.float32
-    y = out if out is not None else torch.empty(x.shape, device=dev, dtype=x.dtype)
-    a = SsdScanStepArgs()
-    a.B, a.D, a.N, a.G, a.nslots = Bb, Dm, N, G, state.shape[0]
-    a.x_dtype = _code(x, "x")
-    dtt = _dt_dtype(x, dt)
-    a.dt_dtype = _CODES[dtt]
-    a.x, a.x_row = _rows(x, (Bb, Dm), x.dtype, dev, "x")
-    a.dt, a.dt_row = _rows(dt, (Bb, Dm), dtt, dev, "dt")
-    a.z, a.z_row = _rows(z, (Bb, Dm), x.dtype, dev, "z")
-    a.Bm, a.b_row = _rows(B, (Bb, G, N), x.dtype, dev, "B")
-    a.Cm, a.c_row = _rows(C, (Bb, G, N), x.dtype, dev, "C")
-    a.A = _dense(A, (Dm, N), f32, dev, "A")
-    a.Dskip = _dense(D, (Dm,), f32, dev, "D")
-    a.dt_bias = _dense(dt_bias, (Dm,), f32, dev, "dt_bias")
-    pool = (state.shape[0], Dm, N)
-    a.state = _dense(state, pool, f32, dev, "state")
-    a.state_out = _dense(state if state_out is None else state_out, pool, f32, dev, "state_out")
-    a.slots = _dense(slots, (Bb,), torch.int32, dev, "slots")
-    a.y = _dense(y, (Bb, Dm), x.dtype, dev, "out")
-    a.dt_softplus = 1 if dt_softplus else 0
-    a.dt_min, a.dt_max = float(dt_limit[0]), float(dt_limit[1])
+    xs, dev, f32, io = x.shape, x.get_device(), torch.float32, x.dtype
+    Bb, Dm = xs
+    bc = (Bb, B.shape[1], B.shape[2])
+    pool = (state.shape[0], Dm, bc[2])
+    code, dtt = _code(x, "x"), _dt_dtype(x, dt)
+    y = torch.empty(xs, device=x.device, dtype=io) if out is None else out
+    px, rx = _rows(x, xs, io, dev, "x")
+    pdt, rdt = _rows(dt, xs, dtt, dev, "dt")
+    pz, rz = _rows(z, xs, io, dev, "z")
+    pb, rb = _rows(B, bc, io, dev, "B")
+    pc, rc = _rows(C, bc, io, dev, "C")
+    ps = _dense(state, pool, f32, dev, "state")
+    a = SsdScanStepArgs(
+        Bb, Dm, bc[2], bc[1], pool[0], px, pdt, _dense(A, (Dm, bc[2]), f32, dev, "A"), pb, pc,
+        _dense(D, (Dm,), f32, dev, "D"), pz, _dense(dt_bias, (Dm,), f32, dev, "dt_bias"), ps,
+        ps if state_out is None else _dense(state_out, pool, f32, dev, "state_out"),
+        _dense(slots, (Bb,), torch.int32, dev, "slots"), _dense(y, xs, io, dev, "out"), rx, rdt, rz, rb, rc, code,
+        _CODES[dtt], 1 if dt_softplus else 0, dt_limit[0], dt_limit[1])
     _call("ssd_selective_scan_step", a, dev)
     return y
 
@@ -337,19 +353,14 @@ def selective_scan_step(x, dt, A, B, C, state, dt_softplus=False, *, state_out=N
 def make_conv_args(x, w, bias=None, *, y=None, final_state=None, initial_state=None, lengths=None, silu=True) -> SsdConvArgs:
     """Fill an ``ssd_conv_args`` from tensors (no copies)."""
     _ndim(x, 3, "x"), _ndim(w, 2, "w")
-    (Bb, L, Cc), W, dev = x.shape, w.shape[1], x.device
-    a = SsdConvArgs()
-    a.B, a.L, a.C, a.W = Bb, L, Cc, W
-    a.dtype = _code(x, "x")
-    a.x, a.x_stride[:] = _tokens(x, (Bb, L, Cc), x.dtype, dev, "x")
-    a.w = _dense(w, (Cc, W), torch.float32, dev, "w")
-    a.bias = _dense(bias, (Cc,), torch.float32, dev, "bias")
-    a.initial_state = _dense(initial_state, (Bb, W - 1, Cc), x.dtype, dev, "initial_state")
-    a.lengths = _dense(lengths, (Bb,), torch.int32, dev, "lengths")
-    a.y = _dense(y, (Bb, L, Cc), x.dtype, dev, "y")
-    a.final_state = _dense(final_state, (Bb, W - 1, Cc), x.dtype, dev, "final_state")
-    a.silu = 1 if silu else 0
-    return a
+    xs, W, dev, f32, io = x.shape, w.shape[1], x.get_device(), torch.float32, x.dtype
+    Bb, L, Cc = xs
+    code, state = _code(x, "x"), (Bb, W - 1, Cc)
+    px, sx = _tokens(x, xs, io, dev, "x")
+    return SsdConvArgs(
+        Bb, L, Cc, W, px, sx, _dense(w, (Cc, W), f32, dev, "w"), _dense(bias, (Cc,), f32, dev, "bias"),
+        _dense(initial_state, state, io, dev, "initial_state"), _dense(lengths, (Bb,), torch.int32, dev, "lengths"),
+        _dense(y, xs, io, dev, "y"), _dense(final_state, state, io, dev, "final_state"), code, 1 if silu else 0)
 
 
 def causal_conv1d_carry(x, w, bias=None, silu=True, *, initial_state=None, lengths=None, return_final_state=False, out=None):
@@ -362,7 +373,7 @@ def causal_conv1d_carry(x, w, bias=None, silu=True, *, initial_state=None, lengt
     y = out if out is not None else torch.empty(x.shape, device=x.device, dtype=x.dtype)
     fin = torch.empty((x.shape[0], w.shape[1] - 1, x.shape[2]), device=x.device, dtype=x.dtype) if return_final_state else None
     a = make_conv_args(x, w, bias, y=y, final_state=fin, initial_state=initial_state, lengths=lengths, silu=silu)
-    _call("ssd_causal_conv_carry", a, x.device)
+    _call("ssd_causal_conv_carry", a, x.get_device())
     return (y, fin) if return_final_state else y
 
 
@@ -375,8 +386,8 @@ def causal_conv1d_bwd(x, w, dy, bias=None, silu=True, *, dfinal=None, initial_st
     a = SsdConvBwdArgs()
     a.fwd = make_conv_args(x, w, bias, initial_state=initial_state, lengths=lengths, silu=silu)
     state = (x.shape[0], w.shape[1] - 1, x.shape[2])
-    a.dy = _dense(dy, x.shape, x.dtype, dev, "dy")
-    a.dfinal = _dense(dfinal, state, x.dtype, dev, "dfinal")
+    a.dy = _dense(dy, x.shape, x.dtype, x.get_device(), "dy")
+    a.dfinal = _dense(dfinal, state, x.dtype, x.get_device(), "dfinal")
     g = {"dx": torch.empty(x.shape, device=dev, dtype=x.dtype), "dw": torch.empty_like(w)}
     if bias is not None:
         g["dbias"] = torch.empty_like(bias)
@@ -384,8 +395,8 @@ def causal_conv1d_bwd(x, w, dy, bias=None, silu=True, *, dfinal=None, initial_st
         g["dh0"] = torch.empty(state, device=dev, dtype=x.dtype)
     for k, t in g.items():
         setattr(a, k, t.data_ptr())
-    ws = _work("ssd_causal_conv_bwd_workspace_size", a, dev)  # noqa: F841
-    _call("ssd_causal_conv_bwd", a, dev)
+    ws = _work("ssd_causal_conv_bwd_workspace_size", a, x)  # noqa: F841
+    _call("ssd_causal_conv_bwd", a, x.get_device())
     return g
 
 
@@ -395,20 +406,17 @@ def causal_conv1d_step(x, state, w, bias=None, silu=True, *, state_out=None, slo
     ``slots`` as in ``selective_scan_step``."""
     _cuda(x, "causal_conv1d_step")
     _ndim(x, 2, "x"), _ndim(w, 2, "w"), _ndim(state, 3, "state")
-    (Bb, Cc), W, dev = x.shape, w.shape[1], x.device
-    y = out if out is not None else torch.empty(x.shape, device=dev, dtype=x.dtype)
-    a = SsdConvStepArgs()
-    a.B, a.C, a.W, a.nslots = Bb, Cc, W, state.shape[0]
-    a.dtype = _code(x, "x")
-    a.x, a.x_row = _rows(x, (Bb, Cc), x.dtype, dev, "x")
-    a.w = _dense(w, (Cc, W), torch.float32, dev, "w")
-    a.bias = _dense(bias, (Cc,), torch.float32, dev, "bias")
+    xs, W, dev, f32, io = x.shape, w.shape[1], x.get_device(), torch.float32, x.dtype
+    Bb, Cc = xs
     pool = (state.shape[0], W - 1, Cc)
-    a.state = _dense(state, pool, x.dtype, dev, "state")
-    a.state_out = _dense(state if state_out is None else state_out, pool, x.dtype, dev, "state_out")
-    a.slots = _dense(slots, (Bb,), torch.int32, dev, "slots")
-    a.y = _dense(y, (Bb, Cc), x.dtype, dev, "out")
-    a.silu = 1 if silu else 0
+    code = _code(x, "x")
+    y = torch.empty(xs, device=x.device, dtype=io) if out is None else out
+    px, rx = _rows(x, xs, io, dev, "x")
+    ps = _dense(state, pool, io, dev, "state")
+    a = SsdConvStepArgs(
+        Bb, Cc, W, pool[0], px, rx, _dense(w, (Cc, W), f32, dev, "w"), _dense(bias, (Cc,), f32, dev, "bias"), ps,
+        ps if state_out is None else _dense(state_out, pool, io, dev, "state_out"),
+        _dense(slots, (Bb,), torch.int32, dev, "slots"), _dense(y, xs, io, dev, "out"), code, 1 if silu else 0)
     _call("ssd_causal_conv_step", a, dev)
     return y
 
@@ -419,7 +427,7 @@ def _norm_args(o, r, w_pre, w_post, gate, scale, eps, like):
     """The shared part; ``like`` is a tensor of o's shape and dtype."""
     if r.dim() < 1:
         raise ValueError("r: at least one dimension")
-    D, dev, f32 = r.shape[-1], r.device, torch.float32
+    D, dev, f32 = r.shape[-1], r.get_device(), torch.float32
     rows = r.numel() // max(D, 1)
     a = SsdBlockNormArgs()
     a.rows, a.D, a.rows_per_gate = rows, D, 1
@@ -427,8 +435,8 @@ def _norm_args(o, r, w_pre, w_post, gate, scale, eps, like):
     a.o = _dense(o, r.shape, like.dtype, dev, "o")
     if gate is not None:
         lead = 1
-        if tuple(gate.shape) != tuple(r.shape):  # [B, D] for [B, ..., D]
-            if gate.dim() != 2 or r.dim() < 2 or gate.shape != (r.shape[0], D):
+        if gate.shape != r.shape:  # [B, D] for [B, ..., D]
+            if r.dim() < 2 or gate.shape != (r.shape[0], D):
                 raise ValueError(f"gate: shape {tuple(gate.shape)}, expected {tuple(r.shape)} or {(r.shape[0], D)}")
             lead = rows // max(r.shape[0], 1)
         a.rows_per_gate = lead
@@ -453,12 +461,13 @@ def block_norm(o, r, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5, dty
     like = o if o is not None else torch.empty(0, device=r.device, dtype=dtype or r.dtype)
     a = _norm_args(o, r, w_pre, w_post, gate, scale, eps, like)
     n = out if out is not None else torch.empty(r.shape, device=r.device, dtype=like.dtype)
-    a.r = _dense(r, r.shape, r.dtype, r.device, "r")
-    a.n = _dense(n, r.shape, like.dtype, r.device, "out")
+    dev = r.get_device()
+    a.r = _dense(r, r.shape, r.dtype, dev, "r")
+    a.n = _dense(n, r.shape, like.dtype, dev, "out")
     if o is not None:
         r_out = r_out if r_out is not None else torch.empty_like(r)
-        a.r_out = _dense(r_out, r.shape, r.dtype, r.device, "r_out")
-    _call("ssd_block_norm", a, r.device)
+        a.r_out = _dense(r_out, r.shape, r.dtype, dev, "r_out")
+    _call("ssd_block_norm", a, dev)
     return n, (r_out if o is not None else r)
 
 
@@ -467,7 +476,7 @@ def block_norm_bwd(dn, dr_out, o, r_out, w_pre, *, w_post=None, gate=None, scale
     stored r' (``r_out``): a dict of dr, dw_pre, and with o also do, and dw_post,
     dgate, dscale where those inputs are given.  ``dr_out`` may be None."""
     _cuda(dn, "block_norm_bwd")
-    dev = dn.device
+    dev = dn.get_device()
     a = SsdBlockNormBwdArgs()
     a.fwd = _norm_args(o, r_out, w_pre, w_post, gate, scale, eps, dn)
     a.fwd.r_out = _dense(r_out, r_out.shape, r_out.dtype, dev, "r_out")
@@ -481,6 +490,6 @@ def block_norm_bwd(dn, dr_out, o, r_out, w_pre, *, w_post=None, gate=None, scale
             g[name] = torch.empty_like(t)
     for k, t in g.items():
         setattr(a, "d_o" if k == "do" else k, t.data_ptr())
-    ws = _work("ssd_block_norm_bwd_workspace_size", a, dev)  # noqa: F841
+    ws = _work("ssd_block_norm_bwd_workspace_size", a, dn)  # noqa: F841
     _call("ssd_block_norm_bwd", a, dev)
     return g
