@@ -9,10 +9,12 @@
 //   dscale = w_post s,  dw_post = scale s,                       s = sum dr gate hat_o
 //
 // About 11 (backward 30) operations per element against 8 to 16 bytes: bound by
-// HBM.  A row stays in the registers of its threads, K runs of four elements
-// each, between the two reductions, so every tensor moves once; the threads
-// walk rows with the weights (and, backwards, the column sums) in registers.
-// 16-bit rows are kept as loaded and unpacked at each use.
+// HBM.  A row stays, as loaded, in the registers of its threads between the two
+// reductions (runs of four elements, K per thread), so every tensor moves once.
+// Forward: a warp takes rows of up to 2048 elements alone, 64 elements per lane,
+// with no barrier, and every load of a row in flight together; wider rows share
+// several warps.  Backward: 16 elements per thread, since the two column sums
+// stay in registers over a chunk of rows.  The weights come from L1 at each use.
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -42,79 +44,99 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float (*slot)[32]) {
     }
 }
 
-template <int SIO>
-__device__ __forceinline__ float round_io(float v) {
-    return IoTraits<SIO>::to_f(IoTraits<SIO>::from_f(v));
+template <int IO, bool VEC>
+__device__ __forceinline__ void unpack_pairs(const Raw4 &r, float2 (&v)[2]) {
+    float f[4];
+    unpack4<IO, VEC>(r, f);
+    v[0] = make_float2(f[0], f[1]);
+    v[1] = make_float2(f[2], f[3]);
+}
+template <int IO, bool VEC>
+__device__ __forceinline__ Raw4 pack_pairs(const float2 (&v)[2]) {
+    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+    return pack4<IO, VEC>(f);
+}
+// Four of a weight vector [D], or ones.
+template <bool VEC>
+__device__ __forceinline__ void weights(const float *w, int c, int nv, float2 (&v)[2]) {
+    unpack_pairs<IO_F32, VEC>(load_raw4<IO_F32, VEC>(w, c, w && nv > 0, nv), v);
+    if (!w) v[0] = v[1] = dup(1.f);
+}
+// scale w_post
+template <bool VEC>
+__device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, int nv, float2 (&v)[2]) {
+    float2 s[2];
+    weights<VEC>(p.w_post, c, nv, v);
+    weights<VEC>(p.scale, c, nv, s);
+    v[0] = __fmul2_rn(v[0], s[0]);
+    v[1] = __fmul2_rn(v[1], s[1]);
 }
 
 template <int IO, int SIO, int K, bool VEC>
-__global__ void __launch_bounds__(K <= 2 ? 256 : 512)
+__global__ void __launch_bounds__(K < 16 ? 128 : 256)
 block_norm_kernel(BlockNormParams p) {
     __shared__ float red[2][1][32];
     const int tpr = blockDim.x;
-    float wp[K][4], ws[K][4];  // w_pre; scale w_post
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = (threadIdx.x + tpr * k) * 4 + j;
-            const bool in = c < p.D;
-            wp[k][j] = in ? __ldg(p.w_pre + c) : 0.f;
-            ws[k][j] = in ? (p.w_post ? __ldg(p.w_post + c) : 1.f) * (p.scale ? __ldg(p.scale + c) : 1.f) : 0.f;
-        }
     const float inv_d = 1.f / (float)p.D;
     for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < p.rows;
          row += (long long)gridDim.x * blockDim.y) {
         const long long base = row * p.D, gbase = p.gate ? row / p.rows_per_gate * p.D : 0;
-        Raw4 ro[K], rr[K], rg[K];
+        Raw4 ro[K], rr[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            rr[k] = load_raw4<SIO, VEC, false>(p.r, base + c, nv > 0, nv);
-            ro[k] = load_raw4<IO, VEC>(p.o, base + c, nv > 0 && p.o, nv);
-            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, nv > 0 && p.gate, nv);
+            ro[k] = load_raw4<IO, VEC>(p.o, base + c, p.o ? nv : 0, nv);
+            rr[k] = load_raw4<SIO, VEC, false>(p.r, base + c, nv, nv);
         }
         float inv = 1.f;
         if (p.o && p.w_post) {
-            float ss[1] = {0.f};
+            float2 s2 = dup(0.f);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if ((threadIdx.x + tpr * k) * 4 < p.D) {
-                    float o[4];
-                    unpack4<IO, VEC>(ro[k], o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) ss[0] = fmaf(o[j], o[j], ss[0]);
-                }
+            for (int k = 0; k < K; ++k) {  // zeros past the row's end
+                float2 o[2];
+                unpack_pairs<IO, VEC>(ro[k], o);
+                s2 = __ffma2_rn(o[0], o[0], s2);
+                s2 = __ffma2_rn(o[1], o[1], s2);
+            }
+            float ss[1] = {s2.x + s2.y};
             row_sum(ss, red[0]);
             inv = rsqrtf(ss[0] * inv_d + p.eps);
         }
-        float r[K][4], ss[1] = {0.f};
+        float2 s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            if (nv <= 0) continue;
-            unpack4<SIO, VEC>(rr[k], r[k]);
+            float2 r[2];
             if (p.o) {
-                float o[4], g[4] = {1.f, 1.f, 1.f, 1.f};
-                unpack4<IO, VEC>(ro[k], o);
-                if (p.gate) unpack4<IO, VEC>(rg[k], g);
+                float2 o[2], g[2], ws[2];
+                unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.gate, gbase + c, p.gate ? nv : 0, nv), g);
+                post_weights<VEC>(p, c, nv, ws);
+                unpack_pairs<IO, VEC>(ro[k], o);
+                unpack_pairs<SIO, VEC>(rr[k], r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[k][j] = round_io<SIO>(fmaf(g[j] * ws[k][j], o[j] * inv, r[k][j]));
-                store4_io<SIO, VEC>(p.r_out, base + c, nv, r[k]);
+                for (int j = 0; j < 2; ++j) {
+                    if (p.gate) ws[j] = __fmul2_rn(ws[j], g[j]);
+                    r[j] = __ffma2_rn(ws[j], __fmul2_rn(o[j], dup(inv)), r[j]);
+                }
+                rr[k] = pack_pairs<SIO, VEC>(r);  // rounded as it is stored
+                if (nv > 0) store_raw4<SIO, VEC>(p.r_out, base + c, nv, rr[k]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ss[0] = j < nv ? fmaf(r[k][j], r[k][j], ss[0]) : ss[0];
+            unpack_pairs<SIO, VEC>(rr[k], r);
+            s2 = __ffma2_rn(r[0], r[0], s2);
+            s2 = __ffma2_rn(r[1], r[1], s2);
         }
+        float ss[1] = {s2.x + s2.y};
         row_sum(ss, red[1]);
-        const float inv2 = rsqrtf(ss[0] * inv_d + p.eps);
+        const float2 inv2 = dup(rsqrtf(ss[0] * inv_d + p.eps));
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            if (nv <= 0) continue;
-            float n[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) n[j] = r[k][j] * inv2 * wp[k][j];
-            store4_io<IO, VEC>(p.n, base + c, nv, n);
+            float2 r[2], wp[2];
+            weights<VEC>(p.w_pre, c, nv, wp);
+            unpack_pairs<SIO, VEC>(rr[k], r);
+            r[0] = __fmul2_rn(__fmul2_rn(r[0], inv2), wp[0]);
+            r[1] = __fmul2_rn(__fmul2_rn(r[1], inv2), wp[1]);
+            if (nv > 0) store_raw4<IO, VEC>(p.n, base + c, nv, pack_pairs<IO, VEC>(r));
         }
         if (!(p.o && p.w_post) && blockDim.x > 32) __syncthreads();  // one reduction per row only: its slot is free again
     }
@@ -137,17 +159,9 @@ block_norm_bwd_kernel(BlockNormParams p) {
         r0 = chunk * p.chunk_rows;
         r1 = min(p.rows, r0 + p.chunk_rows);
     }
-    float wp[K][4], ws[K][4], acc1[K][4], acc2[K][4];
+    float2 acc1[K][2], acc2[K][2];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = (threadIdx.x + tpr * k) * 4 + j;
-            const bool in = c < p.D;
-            wp[k][j] = in ? __ldg(p.w_pre + c) : 0.f;
-            ws[k][j] = in ? (p.w_post ? __ldg(p.w_post + c) : 1.f) * (p.scale ? __ldg(p.scale + c) : 1.f) : 0.f;
-            acc1[k][j] = acc2[k][j] = 0.f;
-        }
+    for (int k = 0; k < K; ++k) acc1[k][0] = acc1[k][1] = acc2[k][0] = acc2[k][1] = dup(0.f);
     const float inv_d = 1.f / (float)p.D;
     for (long long row = r0; row < r1; ++row) {
         const long long base = row * p.D, gbase = p.gate ? row / p.rows_per_gate * p.D : 0;
@@ -155,80 +169,86 @@ block_norm_bwd_kernel(BlockNormParams p) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            rr[k] = load_raw4<SIO, VEC>(p.r_out, base + c, nv > 0, nv);
-            rn[k] = load_raw4<IO, VEC>(p.dn, base + c, nv > 0, nv);
-            rd[k] = load_raw4<SIO, VEC>(p.dr_out, base + c, nv > 0 && p.dr_out, nv);
-            ro[k] = load_raw4<IO, VEC>(p.o, base + c, nv > 0 && p.o, nv);
-            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, nv > 0 && p.gate, nv);
+            rr[k] = load_raw4<SIO, VEC>(p.r_out, base + c, nv, nv);
+            rn[k] = load_raw4<IO, VEC>(p.dn, base + c, nv, nv);
+            ro[k] = load_raw4<IO, VEC>(p.o, base + c, p.o ? nv : 0, nv);
+            rd[k] = load_raw4<SIO, VEC>(p.dr_out, base + c, p.dr_out ? nv : 0, nv);
+            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, p.gate ? nv : 0, nv);
         }
-        float s[3] = {0.f, 0.f, 0.f};  // |r'|^2, dn w_pre . r', |o|^2
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float r[4], n[4], o[4];
-            unpack4<SIO, VEC>(rr[k], r);
-            unpack4<IO, VEC>(rn[k], n);
-            unpack4<IO, VEC>(ro[k], o);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[0] = fmaf(r[j], r[j], s[0]);
-                s[1] = fmaf(n[j] * wp[k][j], r[j], s[1]);
-                s[2] = fmaf(o[j], o[j], s[2]);
-            }
-        }
-        row_sum(s, red[0]);
-        const float inv2 = rsqrtf(s[0] * inv_d + p.eps), m2 = s[1] * inv_d * inv2 * inv2;
-        const float inv = p.w_post ? rsqrtf(s[2] * inv_d + p.eps) : 1.f;
-        // dr of four elements: (v - r' inv2^2 mean(v r')) inv2 + dr_out
-        auto dr_of = [&](int k, float (&dr)[4]) {
-            float r[4], n[4];
-            unpack4<SIO, VEC>(rr[k], r);
-            unpack4<IO, VEC>(rn[k], n);
-            unpack4<SIO, VEC>(rd[k], dr);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dr[j] = fmaf(fmaf(-r[j], m2, n[j] * wp[k][j]), inv2, dr[j]);
-        };
-        float t[1] = {0.f};  // u . o
+        float2 s0 = dup(0.f), s1 = dup(0.f), s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            if (nv <= 0) continue;
-            float dr[4], r[4], n[4];
-            dr_of(k, dr);
-            unpack4<SIO, VEC>(rr[k], r);
-            unpack4<IO, VEC>(rn[k], n);
-            store4_io<SIO, VEC>(p.dr, base + c, nv, dr);
+            float2 r[2], n[2], o[2], wp[2];
+            weights<VEC>(p.w_pre, c, nv, wp);
+            unpack_pairs<SIO, VEC>(rr[k], r);
+            unpack_pairs<IO, VEC>(rn[k], n);
+            unpack_pairs<IO, VEC>(ro[k], o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc2[k][j] = fmaf(n[j], r[j] * inv2, acc2[k][j]);
-            if (!p.o) continue;
-            float o[4], g[4] = {1.f, 1.f, 1.f, 1.f}, dg[4];
-            unpack4<IO, VEC>(ro[k], o);
-            if (p.gate) unpack4<IO, VEC>(rg[k], g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float dh = dr[j] * (o[j] * inv);  // dr hat_o
-                dg[j] = dh * ws[k][j];
-                t[0] = fmaf(g[j] * dr[j] * ws[k][j], o[j], t[0]);
-                acc1[k][j] += seq_gate ? dh : dh * g[j];
+            for (int j = 0; j < 2; ++j) {
+                s0 = __ffma2_rn(r[j], r[j], s0);
+                s1 = __ffma2_rn(__fmul2_rn(n[j], wp[j]), r[j], s1);
+                s2 = __ffma2_rn(o[j], o[j], s2);
             }
-            if (p.gate && !seq_gate) store4_io<IO, VEC>(p.dgate, base + c, nv, dg);
+        }
+        float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};  // |r'|^2, dn w_pre . r', |o|^2
+        row_sum(s, red[0]);
+        const float inv2 = rsqrtf(s[0] * inv_d + p.eps), m2 = s[1] * inv_d * inv2 * inv2;
+        const float inv = p.w_post ? rsqrtf(s[2] * inv_d + p.eps) : 1.f;
+        float2 t2 = dup(0.f);  // u . o
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
+            float2 dr[2], r[2], n[2], wp[2];
+            weights<VEC>(p.w_pre, c, nv, wp);
+            unpack_pairs<SIO, VEC>(rr[k], r);
+            unpack_pairs<IO, VEC>(rn[k], n);
+            unpack_pairs<SIO, VEC>(rd[k], dr);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // dr = (v - r' inv2^2 mean(v r')) inv2 + dr_out
+                const float2 v = __ffma2_rn(r[j], dup(-m2), __fmul2_rn(n[j], wp[j]));
+                dr[j] = __ffma2_rn(v, dup(inv2), dr[j]);
+                acc2[k][j] = __ffma2_rn(n[j], __fmul2_rn(r[j], dup(inv2)), acc2[k][j]);
+            }
+            if (nv > 0) store_raw4<SIO, VEC>(p.dr, base + c, nv, pack_pairs<SIO, VEC>(dr));
+            if (!p.o) continue;
+            float2 o[2], g[2], ws[2], u[2], dg[2];
+            post_weights<VEC>(p, c, nv, ws);
+            unpack_pairs<IO, VEC>(ro[k], o);
+            if (p.gate) unpack_pairs<IO, VEC>(rg[k], g);
+            else g[0] = g[1] = dup(1.f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 dh = __fmul2_rn(dr[j], __fmul2_rn(o[j], dup(inv)));  // dr hat_o
+                dg[j] = __fmul2_rn(dh, ws[j]);
+                u[j] = __fmul2_rn(__fmul2_rn(g[j], dr[j]), ws[j]);
+                t2 = __ffma2_rn(u[j], o[j], t2);
+                acc1[k][j] = seq_gate ? __fadd2_rn(acc1[k][j], dh) : __ffma2_rn(dh, g[j], acc1[k][j]);
+            }
+            if (p.gate && !seq_gate && nv > 0) store_raw4<IO, VEC>(p.dgate, base + c, nv, pack_pairs<IO, VEC>(dg));
+            // u takes dn's and dr_out's place for the last pass, in 32 bits
+            rn[k].w[2] = __float_as_uint(u[0].x);
+            rn[k].w[3] = __float_as_uint(u[0].y);
+            rd[k].w[2] = __float_as_uint(u[1].x);
+            rd[k].w[3] = __float_as_uint(u[1].y);
         }
         if (!p.o) {
             if (blockDim.x > 32) __syncthreads();  // the slot is free again
             continue;
         }
+        float t[1] = {t2.x + t2.y};
         row_sum(t, red[1]);
         const float m = p.w_post ? t[0] * inv_d * inv * inv : 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            if (nv <= 0) continue;
-            float dr[4], o[4], g[4] = {1.f, 1.f, 1.f, 1.f};
-            dr_of(k, dr);
-            unpack4<IO, VEC>(ro[k], o);
-            if (p.gate) unpack4<IO, VEC>(rg[k], g);
+            float2 o[2];
+            unpack_pairs<IO, VEC>(ro[k], o);
+            const float2 u[2] = {make_float2(__uint_as_float(rn[k].w[2]), __uint_as_float(rn[k].w[3])),
+                                 make_float2(__uint_as_float(rd[k].w[2]), __uint_as_float(rd[k].w[3]))};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = fmaf(-o[j], m, g[j] * dr[j] * ws[k][j]) * inv;
-            store4_io<IO, VEC>(p.d_o, base + c, nv, o);
+            for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[j]), dup(inv));
+            if (nv > 0) store_raw4<IO, VEC>(p.d_o, base + c, nv, pack_pairs<IO, VEC>(o));
         }
     }
     float *part = p.part + chunk * 2 * p.D;
@@ -238,8 +258,8 @@ block_norm_bwd_kernel(BlockNormParams p) {
         for (int j = 0; j < 4; ++j) {
             const int c = (threadIdx.x + tpr * k) * 4 + j;
             if (c < p.D) {
-                part[c] = acc1[k][j];
-                part[p.D + c] = acc2[k][j];
+                part[c] = j & 1 ? acc1[k][j / 2].y : acc1[k][j / 2].x;
+                part[p.D + c] = j & 1 ? acc2[k][j / 2].y : acc2[k][j / 2].x;
             }
         }
 }
@@ -291,10 +311,16 @@ dim3 row_block(int D, int K) {
     return dim3(tpr, tpr == 32 ? 4 : 1);
 }
 
+// Elements per thread, in fours: the fewest that a warp's row takes, up to 16 forwards and 4 (8 for rows
+// past 8192) backwards; wider rows take more warps.
+int norm_k(int D) { return D <= 128 ? 1 : D <= 256 ? 2 : D <= 512 ? 4 : D <= 1024 ? 8 : 16; }
+int norm_bwd_k(int D) { return D <= 128 ? 1 : D <= 256 ? 2 : D <= 8192 ? 4 : 8; }
+
 bool norm_vec(const BlockNormParams &p, int io, int sio) {
     auto ok = [](const void *q, int t) { return reinterpret_cast<uintptr_t>(q) % (t == IO_F32 ? 16 : 8) == 0; };
     return p.D % 4 == 0 && ok(p.o, io) && ok(p.r, sio) && ok(p.gate, io) && ok(p.n, io) && ok(p.r_out, sio) &&
-           ok(p.dn, io) && ok(p.dr_out, sio) && ok(p.d_o, io) && ok(p.dr, sio) && ok(p.dgate, io);
+           ok(p.dn, io) && ok(p.dr_out, sio) && ok(p.d_o, io) && ok(p.dr, sio) && ok(p.dgate, io) &&
+           ok(p.w_post, IO_F32) && ok(p.w_pre, IO_F32) && ok(p.scale, IO_F32);
 }
 
 template <int IO, int SIO, int K>
@@ -314,10 +340,13 @@ cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
 
 template <int IO, int SIO>
 cudaError_t launch_norm_io(const BlockNormParams &p, cudaStream_t s) {
-    if (p.D <= 128) return launch_norm_as<IO, SIO, 1>(p, s);
-    if (p.D <= 2048) return launch_norm_as<IO, SIO, 2>(p, s);
-    if (p.D <= 8192) return launch_norm_as<IO, SIO, 4>(p, s);
-    return launch_norm_as<IO, SIO, 8>(p, s);
+    switch (norm_k(p.D)) {
+        case 1: return launch_norm_as<IO, SIO, 1>(p, s);
+        case 2: return launch_norm_as<IO, SIO, 2>(p, s);
+        case 4: return launch_norm_as<IO, SIO, 4>(p, s);
+        case 8: return launch_norm_as<IO, SIO, 8>(p, s);
+        default: return launch_norm_as<IO, SIO, 16>(p, s);
+    }
 }
 
 template <int IO, int SIO, int K>
@@ -333,17 +362,20 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
 
 template <int IO, int SIO>
 cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
-    if (p.D <= 128) return launch_norm_bwd_as<IO, SIO, 1>(p, s);
-    if (p.D <= 4096) return launch_norm_bwd_as<IO, SIO, 2>(p, s);
-    if (p.D <= 8192) return launch_norm_bwd_as<IO, SIO, 4>(p, s);
-    return launch_norm_bwd_as<IO, SIO, 8>(p, s);
+    switch (norm_bwd_k(p.D)) {
+        case 1: return launch_norm_bwd_as<IO, SIO, 1>(p, s);
+        case 2: return launch_norm_bwd_as<IO, SIO, 2>(p, s);
+        case 4: return launch_norm_bwd_as<IO, SIO, 4>(p, s);
+        default: return launch_norm_bwd_as<IO, SIO, 8>(p, s);
+    }
 }
 
 }  // namespace
 
-// About four chunks of rows per SM; a chunk never spans two gates of several rows.
+// Chunks for about 16 warps per SM, two at least; a chunk never spans two gates of several rows.
 void block_norm_chunks(BlockNormParams &p) {
-    const long long target = 4LL * scan_sm_count();
+    const int warps = row_block(p.D, norm_bwd_k(p.D)).x / 32;
+    const long long target = (warps < 8 ? 16 / warps : 2) * (long long)scan_sm_count();
     const bool seq_gate = p.gate && p.rows_per_gate > 1;
     const long long span = seq_gate ? p.rows_per_gate : p.rows, spans = p.rows / span;
     long long per = (target + spans - 1) / spans;  // chunks per span

@@ -29,22 +29,40 @@ __device__ __forceinline__ Raw4 conv_value(const ConvParams &p, int b, long long
     return load_raw4<IO, VEC>(base, i, carried ? p.h0 && t >= -(long long)(p.W - 1) : t < len, nv);
 }
 
+// Four channels as two pairs: the packed operations take one issue slot for both.
+template <int IO, bool VEC>
+__device__ __forceinline__ void unpack_pairs(const Raw4 &r, float2 (&v)[2]) {
+    float f[4];
+    unpack4<IO, VEC>(r, f);
+    v[0] = make_float2(f[0], f[1]);
+    v[1] = make_float2(f[2], f[3]);
+}
+template <int IO, bool VEC>
+__device__ __forceinline__ void store_pairs(char *dst, int nv, const float2 (&v)[2]) {
+    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+    store4_io<IO, VEC>(dst, 0, nv, f);
+}
+
 // Taps sit right-aligned in KT slots (slot KT-1 is the current token), so every index is a constant.
 template <int KT>
-__device__ __forceinline__ void load_taps(const ConvParams &p, int c, int nv, float (&w)[KT][4], float (&bias)[4]) {
+__device__ __forceinline__ void load_taps(const ConvParams &p, int c, int nv, float2 (&w)[KT][2], float2 (&bias)[2]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int s = 0; s < KT; ++s) {
             const int k = s - (KT - p.W);
-            w[s][j] = k >= 0 && j < nv ? __ldg(p.w + (long long)(c + j) * p.W + k) : 0.f;
+            const float v = k >= 0 && j < nv ? __ldg(p.w + (long long)(c + j) * p.W + k) : 0.f;
+            if (j & 1) w[s][j / 2].y = v;
+            else w[s][j / 2].x = v;
         }
-        bias[j] = p.bias && j < nv ? __ldg(p.bias + c + j) : 0.f;
+        const float v = p.bias && j < nv ? __ldg(p.bias + c + j) : 0.f;
+        if (j & 1) bias[j / 2].y = v;
+        else bias[j / 2].x = v;
     }
 }
 
-template <int IO, int KT, bool VEC>
-__global__ void __launch_bounds__(kCx * kCy)
+template <int IO, int KT, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 6 : 1)
 conv_carry_kernel(ConvParams p) {
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     if (c >= p.C) return;
@@ -59,36 +77,41 @@ conv_carry_kernel(ConvParams p) {
         }
         return;
     }
+    constexpr int kEs = IO == IO_F32 ? 4 : 2;
     const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
     if (t0 >= t1) return;
-    float w[KT][4], bias[4], win[KT][4];
+    float2 w[KT][2], bias[2], win[KT][2];
     load_taps<KT>(p, c, nv, w, bias);
 #pragma unroll
     for (int s = 1; s < KT; ++s)  // slots 0..KT-2 of the first step are tokens t0-KT+1 .. t0-1
-        unpack4<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
+        unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
+    const char *px = static_cast<const char *>(p.x) + (b * p.xs[0] + t0 * p.xs[1] + c) * kEs;
+    char *py = static_cast<char *>(p.y) + (((long long)b * p.L + t0) * p.C + c) * kEs;
+    const long long sx = p.xs[1] * kEs, sy = (long long)p.C * kEs;
+    const int live = min(t1, len);
     for (int t = t0; t < t1; t += kAhead) {
         Raw4 r[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            r[i] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + (t + i) * p.xs[1] + c, t + i < min(t1, len), nv);
+        for (int i = 0; i < kAhead; ++i) {
+            r[i] = load_raw4<IO, VEC>(px, 0, live - t - i, nv);
+            px += sx;
+        }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (t + i >= t1) break;
-            float o[4];
 #pragma unroll
-            for (int s = 0; s < KT - 1; ++s)
+            for (int s = 0; s < KT - 1; ++s) win[s][0] = win[s + 1][0], win[s][1] = win[s + 1][1];
+            unpack_pairs<IO, VEC>(r[i], win[KT - 1]);
+            float2 o[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) win[s][j] = win[s + 1][j];
-            unpack4<IO, VEC>(r[i], win[KT - 1]);
+            for (int j = 0; j < 2; ++j) {
+                float2 a = bias[j];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a = bias[j];
-#pragma unroll
-                for (int s = 0; s < KT; ++s) a = fmaf(w[s][j], win[s][j], a);
-                if (p.silu) a = silu_fast(a);
-                o[j] = t + i < len ? a : 0.f;
+                for (int s = 0; s < KT; ++s) a = __ffma2_rn(w[s][j], win[s][j], a);
+                o[j] = SILU ? silu2(a) : a;
+                if (t + i >= live) o[j] = dup(0.f);
             }
-            store4_io<IO, VEC>(p.y, ((long long)b * p.L + t + i) * p.C + c, nv, o);
+            if (t + i < t1) store_pairs<IO, VEC>(py, nv, o);
+            py += sy;
         }
     }
 }
@@ -97,87 +120,87 @@ conv_carry_kernel(ConvParams p) {
 // reaches back into the run), recomputing pre from the window.  dw and dbias gather in
 // registers over the run, then over the CTA's runs in shared memory in a fixed
 // order, and leave as one row of partial sums per CTA.
-template <int IO, int KT, bool VEC>
-__global__ void __launch_bounds__(kCx * kCy)
+template <int IO, int KT, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 4 : 1)
 conv_bwd_kernel(ConvParams p) {
-    __shared__ float red[kCy][kCx * 4];
+    __shared__ __align__(16) float red[kCy][kCx * 4];
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     const int nv = min(4, p.C - c), b = blockIdx.z;
     const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
     const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
-    float dw[KT][4], db[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kEs = IO == IO_F32 ? 4 : 2;
+    float2 dw[KT][2], db[2] = {dup(0.f), dup(0.f)};
 #pragma unroll
-    for (int s = 0; s < KT; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dw[s][j] = 0.f;
+    for (int s = 0; s < KT; ++s) dw[s][0] = dw[s][1] = dup(0.f);
     if (c < p.C && t0 < t1) {
-        float w[KT][4], bias[4], win[KT][4], dp[KT][4];  // dp[i]: of token t - i
+        float2 w[KT][2], bias[2], win[KT][2], dp[KT][2];  // dp[i]: of token t - i
         load_taps<KT>(p, c, nv, w, bias);
 #pragma unroll
         for (int s = 1; s < KT; ++s)
-            unpack4<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
+            unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
 #pragma unroll
-        for (int s = 0; s < KT; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dp[s][j] = 0.f;
-        const int tend = t1 + KT - 1;
+        for (int s = 0; s < KT; ++s) dp[s][0] = dp[s][1] = dup(0.f);
+        const char *px = static_cast<const char *>(p.x) + (b * p.xs[0] + t0 * p.xs[1] + c) * kEs;
+        const long long o0 = ((long long)b * p.L + t0) * p.C + c;
+        const char *pdy = static_cast<const char *>(p.dy) + o0 * kEs;
+        char *pdx = static_cast<char *>(p.dx) + (o0 - (long long)(KT - 1) * p.C) * kEs;
+        const long long sx = p.xs[1] * kEs, sy = (long long)p.C * kEs;
+        const int tend = t1 + KT - 1, live = min(tend, len);
         for (int t = t0; t < tend; t += kAhead) {
             Raw4 r[kAhead], rg[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const bool ok = t + i < min(tend, len);
-                r[i] = load_raw4<IO, VEC>(p.x, b * p.xs[0] + (t + i) * p.xs[1] + c, ok, nv);
-                rg[i] = load_raw4<IO, VEC>(p.dy, ((long long)b * p.L + t + i) * p.C + c, ok, nv);
+                r[i] = load_raw4<IO, VEC>(px, 0, live - t - i, nv);
+                rg[i] = load_raw4<IO, VEC>(pdy, 0, live - t - i, nv);
+                px += sx;
+                pdy += sy;
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int tt = t + i;
-                if (tt >= tend) break;
 #pragma unroll
-                for (int s = 0; s < KT - 1; ++s)
+                for (int s = 0; s < KT - 1; ++s) win[s][0] = win[s + 1][0], win[s][1] = win[s + 1][1];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) win[s][j] = win[s + 1][j];
+                for (int s = KT - 1; s > 0; --s) dp[s][0] = dp[s - 1][0], dp[s][1] = dp[s - 1][1];
+                unpack_pairs<IO, VEC>(r[i], win[KT - 1]);
+                float2 g[2], o[2];
+                unpack_pairs<IO, VEC>(rg[i], g);  // zeros past the row's tokens
 #pragma unroll
-                for (int s = KT - 1; s > 0; --s)
+                for (int j = 0; j < 2; ++j) {
+                    if (SILU) {  // g silu'(a) = g s (1 + a (1 - s)), s = sigmoid(a)
+                        float2 a = bias[j];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dp[s][j] = dp[s - 1][j];
-                unpack4<IO, VEC>(r[i], win[KT - 1]);
-                float g[4], o[4];
-                unpack4<IO, VEC>(rg[i], g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (p.silu) {
-                        float a = bias[j];
-#pragma unroll
-                        for (int s = 0; s < KT; ++s) a = fmaf(w[s][j], win[s][j], a);
-                        const float sg = sigmoid_f(a);
-                        g[j] = tt < len ? g[j] * sg * fmaf(a, 1.f - sg, 1.f) : 0.f;  // silu'(a)
+                        for (int s = 0; s < KT; ++s) a = __ffma2_rn(w[s][j], win[s][j], a);
+                        const float2 sg = sigmoid2(a);
+                        const float2 rest = __fadd2_rn(dup(1.f), make_float2(-sg.x, -sg.y));
+                        g[j] = __fmul2_rn(__fmul2_rn(g[j], sg), __ffma2_rn(a, rest, dup(1.f)));
+                        if (tt >= live) g[j] = dup(0.f);
                     }
                     dp[0][j] = g[j];
-                    if (tt < t1) {
-                        db[j] += g[j];
+                    const float2 mine = tt < t1 ? g[j] : dup(0.f);
+                    db[j] = __fadd2_rn(db[j], mine);
 #pragma unroll
-                        for (int s = 0; s < KT; ++s) dw[s][j] = fmaf(g[j], win[s][j], dw[s][j]);
-                    }
-                    float a = 0.f;  // the slot of tap k is its age past KT - W empty ones
+                    for (int s = 0; s < KT; ++s) dw[s][j] = __ffma2_rn(mine, win[s][j], dw[s][j]);
+                    float2 a = __fmul2_rn(w[0][j], dp[0][j]);  // the slot of tap k is its age past KT - W empty ones
 #pragma unroll
-                    for (int s = 0; s < KT; ++s) a = fmaf(w[s][j], dp[s][j], a);
+                    for (int s = 1; s < KT; ++s) a = __ffma2_rn(w[s][j], dp[s][j], a);
                     o[j] = a;
                 }
                 const int tau = tt - (KT - 1);  // the entry of v this step completes
-                if (tau >= len - (p.W - 1) && tau < len && p.dfinal) {
-                    float f[4];
-                    unpack4<IO, VEC>(load_raw4<IO, VEC>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, true, nv), f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] += f[j];
+                if (p.dfinal && tt < tend && tau >= len - (p.W - 1) && tau < len) {
+                    float2 f[2];
+                    unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, 1, nv), f);
+                    o[0] = __fadd2_rn(o[0], f[0]);
+                    o[1] = __fadd2_rn(o[1], f[1]);
                 }
                 if (tau < 0) {
                     if (t0 == 0 && p.dh0 && tau >= -(p.W - 1))
-                        store4_io<IO, VEC>(p.dh0, ((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c, nv, o);
-                } else if (tau >= t0) {
-                    if (tau >= len) o[0] = o[1] = o[2] = o[3] = 0.f;
-                    store4_io<IO, VEC>(p.dx, ((long long)b * p.L + tau) * p.C + c, nv, o);
+                        store_pairs<IO, VEC>(static_cast<char *>(p.dh0) + (((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c) * kEs, nv, o);
+                } else if (tau >= t0 && tau < t1) {
+                    if (tau >= len) o[0] = o[1] = dup(0.f);
+                    store_pairs<IO, VEC>(pdx, nv, o);
                 }
+                pdx += sy;
             }
         }
     }
@@ -187,9 +210,10 @@ conv_bwd_kernel(ConvParams p) {
     for (int s = 0; s <= KT; ++s) {
         const int k = s == KT ? p.W : s - (KT - p.W);  // dbias follows the taps
         if (k < 0) continue;
+        const float2 *v = s == KT ? db : dw[s < KT ? s : 0];
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[threadIdx.y][threadIdx.x * 4 + j] = s == KT ? db[j] : dw[s < KT ? s : 0][j];
+        *reinterpret_cast<float2 *>(&red[threadIdx.y][threadIdx.x * 4]) = v[0];
+        *reinterpret_cast<float2 *>(&red[threadIdx.y][threadIdx.x * 4 + 2]) = v[1];
         __syncthreads();
         if (cc < p.C) {
             float a = 0.f;
@@ -228,8 +252,12 @@ bool conv_vec(const ConvParams &p, int io) {
 template <int IO>
 cudaError_t launch_conv_io(const ConvParams &p, cudaStream_t s) {
     const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens + 1, p.B);
-    auto *kernel = conv_vec(p, IO) ? (p.W <= 4 ? conv_carry_kernel<IO, 4, true> : conv_carry_kernel<IO, 8, true>)
-                                   : (p.W <= 4 ? conv_carry_kernel<IO, 4, false> : conv_carry_kernel<IO, 8, false>);
+    static constexpr decltype(&conv_carry_kernel<IO, 4, true, true>) kernels[2][2][2] = {
+        {{conv_carry_kernel<IO, 4, false, false>, conv_carry_kernel<IO, 4, false, true>},
+         {conv_carry_kernel<IO, 4, true, false>, conv_carry_kernel<IO, 4, true, true>}},
+        {{conv_carry_kernel<IO, 8, false, false>, conv_carry_kernel<IO, 8, false, true>},
+         {conv_carry_kernel<IO, 8, true, false>, conv_carry_kernel<IO, 8, true, true>}}};
+    auto *kernel = kernels[p.W > 4][conv_vec(p, IO)][p.silu != 0];
     kernel<<<grid, dim3(kCx, kCy), 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -237,8 +265,12 @@ cudaError_t launch_conv_io(const ConvParams &p, cudaStream_t s) {
 template <int IO>
 cudaError_t launch_conv_bwd_io(const ConvParams &p, cudaStream_t s) {
     const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens, p.B);
-    auto *kernel = conv_vec(p, IO) ? (p.W <= 4 ? conv_bwd_kernel<IO, 4, true> : conv_bwd_kernel<IO, 8, true>)
-                                   : (p.W <= 4 ? conv_bwd_kernel<IO, 4, false> : conv_bwd_kernel<IO, 8, false>);
+    static constexpr decltype(&conv_bwd_kernel<IO, 4, true, true>) kernels[2][2][2] = {
+        {{conv_bwd_kernel<IO, 4, false, false>, conv_bwd_kernel<IO, 4, false, true>},
+         {conv_bwd_kernel<IO, 4, true, false>, conv_bwd_kernel<IO, 4, true, true>}},
+        {{conv_bwd_kernel<IO, 8, false, false>, conv_bwd_kernel<IO, 8, false, true>},
+         {conv_bwd_kernel<IO, 8, true, false>, conv_bwd_kernel<IO, 8, true, true>}}};
+    auto *kernel = kernels[p.W > 4][conv_vec(p, IO)][p.silu != 0];
     kernel<<<grid, dim3(kCx, kCy), 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -382,6 +382,46 @@ __device__ __forceinline__ void unpack4_dt(const Raw4 &r, float (&v)[4], int dt3
     }
 }
 
+// unpack4's inverse, rounding to the type; and the store of what it gives.
+template <int IO, bool VEC>
+__device__ __forceinline__ Raw4 pack4(const float (&v)[4]) {
+    Raw4 r = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (IO == IO_F32) {
+            r.w[j] = __float_as_uint(v[j]);
+        } else {
+            const uint32_t h = IO == IO_BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
+                                             : (uint32_t)__half_as_ushort(__float2half_rn(v[j]));
+            if (!VEC) r.w[j] = h;
+            else r.w[j / 2] |= j & 1 ? h << 16 : h;
+        }
+    }
+    return r;
+}
+template <int IO, bool VEC>
+__device__ __forceinline__ void store_raw4(void *base, long long i, int nv, const Raw4 &r) {
+    if (IO == IO_F32) {
+        uint32_t *p = static_cast<uint32_t *>(base) + i;
+        if (VEC) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < nv) p[j] = r.w[j];
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(base) + i;
+        if (VEC) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < nv) p[j] = (uint16_t)r.w[j];
+        }
+    }
+}
+
 template <int IO, bool VEC>
 __device__ __forceinline__ void store4_io(void *base, long long i, int nv, const float (&v)[4]) {
     if (!VEC) {

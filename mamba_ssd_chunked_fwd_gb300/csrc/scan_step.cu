@@ -13,88 +13,113 @@ namespace ssd {
 namespace {
 
 // LPC lanes hold a channel's states, four to a lane, so a warp reads and
-// writes 512 consecutive bytes of the state; the LPC lanes' parts of y meet in
-// xor exchanges.  Each lane repeats its channel's softplus: about 30 operations
-// beside 32 bytes of state.  CPT channels per lane, their loads issued
-// together; B and C are loaded once for them.
+// writes 512 consecutive bytes of the state.  A lane takes the same channel of
+// NB sequences: A is loaded once for them, and with NB = 4 lane j of a group
+// works out the step of sequence j (the softplus, about 25 operations) and
+// hands it to the others, then ends up with sequence j's sum over the lanes
+// (halving exchanges), its gate and its store.
 constexpr int kStepThreads = 128;
 
-template <int IO, int LPC, int CPT, bool VEC>
+template <int IO, int LPC, int NB, bool VEC>
 __global__ void __launch_bounds__(kStepThreads)
 scan_step_kernel(ScanStepParams p) {
-    constexpr int kCh = kStepThreads / LPC;  // channels per CTA and round
-    const int b = blockIdx.y;
-    const int ln = threadIdx.x % LPC, n0 = ln * 4;
-    const int cb = blockIdx.x * (kCh * CPT) + threadIdx.x / LPC;
-    const long long slot = p.slots ? __ldg(p.slots + b) : b;
-    const bool live = slot >= 0 && slot < p.nslots;
-    const long long s0 = slot * p.D * p.N;
-    const int dg = p.D / p.G, nn = p.N - n0;
-    Raw4 rs[CPT], ra[CPT], rb[CPT], rc[CPT];
-    float x[CPT], raw[CPT], z[CPT], bias[CPT], skip[CPT];
+    static_assert(NB == 1 || (NB == 4 && LPC >= 4), "one lane of the group per sequence");
+    constexpr int kCh = kStepThreads / LPC;  // channels per CTA
+    const int lane = threadIdx.x & 31, ln = threadIdx.x % LPC, n0 = ln * 4, nn = p.N - n0;
+    const int c = blockIdx.x * kCh + threadIdx.x / LPC;
+    const int b0 = blockIdx.y * NB;
+    const bool ch = c < p.D;
+    const int dg = p.D / p.G;
+    const long long i = (long long)c * p.N + n0, gn = (long long)(c / dg) * p.N + n0;
+    long long s0[NB];
+    bool live[NB];
+    Raw4 rs[NB], rb[NB], rc[NB], ra;
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {  // every load first
-        const int c = cb + k * kCh;
-        const bool ok = live && c < p.D, okn = ok && nn > 0;
-        const long long i = (long long)c * p.N + n0, gn = (long long)(c / dg) * p.N + n0;
-        rs[k] = load_raw4<IO_F32, VEC, false>(p.state, s0 + i, okn, nn);
-        ra[k] = load_raw4<IO_F32, VEC>(p.A, i, okn, nn);
-        rb[k] = load_raw4<IO, VEC>(p.Bm, b * p.b_row + gn, okn, nn);
-        rc[k] = load_raw4<IO, VEC>(p.Cm, b * p.c_row + gn, okn, nn);
-        x[k] = load_one<IO>(p.x, b * p.x_row + c, ok);
-        raw[k] = load_one<IO>(p.dt, b * p.dt_row + c, ok && (IO == IO_F32 || !p.dt32));
-        if (IO != IO_F32) raw[k] += load_one<IO_F32>(p.dt, b * p.dt_row + c, ok && p.dt32);  // one of the two is 0
-        z[k] = load_one<IO>(p.z, b * p.z_row + c, ok && p.z);
-        bias[k] = load_one<IO_F32>(p.dt_bias, c, ok && p.dt_bias);
-        skip[k] = load_one<IO_F32>(p.Dskip, c, ok && p.Dskip);
+    for (int k = 0; k < NB; ++k) {  // every load first
+        const int b = b0 + k;
+        long long slot = -1;
+        if (b < p.B) slot = p.slots ? __ldg(p.slots + b) : b;
+        live[k] = slot >= 0 && slot < p.nslots;
+        s0[k] = slot * p.D * p.N;
     }
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-        const int c = cb + k * kCh;
-        const bool in = live && c < p.D;
-        float acc = 0.f;
-        if (in) {
-            const float d = step_of<false>(raw[k], bias[k], p.softplus, p.has_limit, p.dt_min, p.dt_max).d;
-            const float dx = d * x[k];
-            float o[4], s[4], a[4], bv[4], cv[4];
-            unpack4<IO_F32, VEC>(rs[k], s);
-            unpack4<IO_F32, VEC>(ra[k], a);
-            unpack4<IO, VEC>(rb[k], bv);
-            unpack4<IO, VEC>(rc[k], cv);
+    for (int k = 0; k < NB; ++k) {
+        const int b = b0 + k;
+        const bool ok = live[k] && ch && nn > 0;
+        rs[k] = load_raw4<IO_F32, VEC, false>(p.state, s0[k] + i, ok, nn);
+        rb[k] = load_raw4<IO, VEC>(p.Bm, b * p.b_row + gn, ok, nn);
+        rc[k] = load_raw4<IO, VEC>(p.Cm, b * p.c_row + gn, ok, nn);
+    }
+    ra = load_raw4<IO_F32, VEC>(p.A, i, ch && nn > 0, nn);
+    const int mine = NB == 1 ? 0 : ln & 3, bm = b0 + mine;  // the sequence whose step is this lane's
+    const bool okm = ch && (NB == 1 ? live[0] : mine == 0 ? live[0] : mine == 1 ? live[NB > 1] : mine == 2 ? live[NB > 2 ? 2 : 0] : live[NB > 3 ? 3 : 0]);
+    const float x = load_one<IO>(p.x, bm * p.x_row + c, okm);
+    float raw = load_one<IO>(p.dt, bm * p.dt_row + c, okm && (IO == IO_F32 || !p.dt32));
+    if (IO != IO_F32) raw += load_one<IO_F32>(p.dt, bm * p.dt_row + c, okm && p.dt32);  // one of the two is 0
+    const float z = load_one<IO>(p.z, bm * p.z_row + c, okm && p.z);
+    const float bias = load_one<IO_F32>(p.dt_bias, c, ch && p.dt_bias), skip = load_one<IO_F32>(p.Dskip, c, ch && p.Dskip);
+    const float d = step_of<false>(raw, bias, p.softplus, p.has_limit, p.dt_min, p.dt_max).d, dx = d * x;
+    float a[4], acc[NB];
+    unpack4<IO_F32, VEC>(ra, a);
+    const float2 a0 = make_float2(a[0] * kLog2e, a[1] * kLog2e), a1 = make_float2(a[2] * kLog2e, a[3] * kLog2e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[j] = fmaf(ex2(fmaf(d, a[j] * kLog2e, kDecayCentre)), s[j], dx * bv[j]);
-                acc = fmaf(o[j], cv[j], acc);
-            }
-            store_n4(p.state_out + s0, (long long)c * p.N + n0, n0, p.N, VEC, o[0], o[1], o[2], o[3]);
-        }
+    for (int k = 0; k < NB; ++k) {
+        const int src = (lane & ~(LPC - 1)) | k;
+        const float2 dk = dup(NB == 1 ? d : __shfl_sync(0xffffffffu, d, src));
+        const float2 wk = dup(NB == 1 ? dx : __shfl_sync(0xffffffffu, dx, src));
+        float s[4], bv[4], cv[4];
+        unpack4<IO_F32, VEC>(rs[k], s);
+        unpack4<IO, VEC>(rb[k], bv);
+        unpack4<IO, VEC>(rc[k], cv);
+        const float2 h0 = __ffma2_rn(decay2(dk, a0), make_float2(s[0], s[1]), __fmul2_rn(wk, make_float2(bv[0], bv[1])));
+        const float2 h1 = __ffma2_rn(decay2(dk, a1), make_float2(s[2], s[3]), __fmul2_rn(wk, make_float2(bv[2], bv[3])));
+        const float2 v = __ffma2_rn(h1, make_float2(cv[2], cv[3]), __fmul2_rn(h0, make_float2(cv[0], cv[1])));
+        acc[k] = v.x + v.y;
+        if (live[k] && ch) store_n4(p.state_out + s0[k], i, n0, p.N, VEC, h0.x, h0.y, h1.x, h1.y);
+    }
+    float y;
+    if (NB == 1) {
+        y = acc[0];
 #pragma unroll
-        for (int off = LPC / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        if (ln == 0 && c < p.D) {
-            float y = 0.f;
-            if (live) {
-                y = p.Dskip ? fmaf(skip[k], x[k], acc) : acc;
-                if (p.z) y *= silu_fast(z[k]);
-            }
-            st_io<IO>(p.y, (size_t)b * p.D + c, y);
+        for (int off = LPC / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    } else {  // lane bit 1, then bit 0, choose the sequence a lane is left with: its own
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool hi = lane & 2;
+            const float keep = hi ? acc[NB > 1 ? k + 2 : 0] : acc[NB > 1 ? k : 0], send = hi ? acc[NB > 1 ? k : 0] : acc[NB > 1 ? k + 2 : 0];
+            acc[NB > 1 ? k : 0] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
         }
+        const bool hi = lane & 1;
+        const float keep = hi ? acc[NB > 1] : acc[0], send = hi ? acc[0] : acc[NB > 1];
+        y = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+#pragma unroll
+        for (int off = 4; off < LPC; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+    }
+    if (ln < NB && ch && bm < p.B) {
+        y = p.Dskip ? fmaf(skip, x, y) : y;
+        if (p.z) y *= silu_fast(z);
+        st_io<IO>(p.y, (size_t)bm * p.D + c, okm ? y : 0.f);
     }
 }
 
 template <int IO, int LPC>
 cudaError_t launch_step_as(const ScanStepParams &p, cudaStream_t s) {
     constexpr int kCh = kStepThreads / LPC;
-    // Four channels per lane once that still gives every SM eight CTAs: more bytes in flight per lane;
-    // below that one channel per lane spreads the few channels over more SMs.
-    const long long ctas4 = (long long)p.B * ((p.D + 4 * kCh - 1) / (4 * kCh));
     const bool vec = p.N % 4 == 0 && vec4_aligned(p.state, IO_F32) && vec4_aligned(p.state_out, IO_F32) &&
                      vec4_aligned(p.A, IO_F32) && vec4_aligned(p.Bm, IO) && vec4_aligned(p.Cm, IO) &&
                      p.b_row % 4 == 0 && p.c_row % 4 == 0;
-    const bool many = ctas4 >= 8LL * scan_sm_count();
-    const dim3 grid(many ? (p.D + 4 * kCh - 1) / (4 * kCh) : (p.D + kCh - 1) / kCh, p.B);
-    auto *kernel = many ? (vec ? scan_step_kernel<IO, LPC, 4, true> : scan_step_kernel<IO, LPC, 4, false>)
-                        : (vec ? scan_step_kernel<IO, LPC, 1, true> : scan_step_kernel<IO, LPC, 1, false>);
-    kernel<<<grid, kStepThreads, 0, s>>>(p);
+    const int tiles = (p.D + kCh - 1) / kCh;
+    // Four sequences per lane once that leaves every SM four CTAs; below, one, so
+    // that the few channels reach more SMs.  Two lanes per channel take one.
+    if constexpr (LPC >= 4) {
+        if ((long long)tiles * (p.B / 4) >= 4LL * scan_sm_count()) {
+            auto *kernel = vec ? scan_step_kernel<IO, LPC, 4, true> : scan_step_kernel<IO, LPC, 4, false>;
+            kernel<<<dim3(tiles, (p.B + 3) / 4), kStepThreads, 0, s>>>(p);
+            return cudaGetLastError();
+        }
+    }
+    auto *kernel = vec ? scan_step_kernel<IO, LPC, 1, true> : scan_step_kernel<IO, LPC, 1, false>;
+    kernel<<<dim3(tiles, p.B), kStepThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
