@@ -9,12 +9,11 @@
 //   dscale = w_post s,  dw_post = scale s,                       s = sum dr gate hat_o
 //
 // About 11 (backward 30) operations per element against 8 to 16 bytes: bound by
-// HBM.  A row stays, as loaded, in the registers of its threads between the two
-// reductions (runs of four elements, K per thread), so every tensor moves once.
-// Forward: a warp takes rows of up to 2048 elements alone, 64 elements per lane,
-// with no barrier, and every load of a row in flight together; wider rows share
-// several warps.  Backward: 16 elements per thread, since the two column sums
-// stay in registers over a chunk of rows.  The weights come from L1 at each use.
+// HBM.  The threads of a row own runs of four elements, K per thread, which they
+// copy into slots of their own in shared memory a row ahead, so that the loads of
+// one row run beside the reductions and stores of the one before, need no
+// registers, and every tensor moves once.  Backwards the two column sums and the
+// weights stay in registers over a chunk of rows.
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -52,9 +51,9 @@ __device__ __forceinline__ void unpack_pairs(const Raw4 &r, float2 (&v)[2]) {
     v[1] = make_float2(f[2], f[3]);
 }
 template <int IO, bool VEC>
-__device__ __forceinline__ Raw4 pack_pairs(const float2 (&v)[2]) {
+__device__ __forceinline__ void store_pairs(void *base, long long i, int nv, const float2 (&v)[2]) {
     const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-    return pack4<IO, VEC>(f);
+    store4_io<IO, VEC>(base, i, nv, f);
 }
 // Four of a weight vector [D], or ones.
 template <bool VEC>
@@ -72,29 +71,60 @@ __device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, in
     v[1] = __fmul2_rn(v[1], s[1]);
 }
 
+// The slots of a CTA's threads for one row: NI tensors in the block's type, then NS in the stream's.
+template <int IO, int SIO, int K, int NI, int NS>
+struct NormSlots {
+    static constexpr int kQi = IO == IO_F32 ? 16 : 8, kQs = SIO == IO_F32 ? 16 : 8;
+    static constexpr int kPerThread = K * (NI * kQi + NS * kQs);
+    // of thread `tid` of n: tensor i's quad k
+    static __device__ __forceinline__ int block(int i, int k, int tid, int n) { return (i * K + k) * kQi * n + tid * kQi; }
+    static __device__ __forceinline__ int stream(int i, int k, int tid, int n) {
+        return NI * K * kQi * n + (i * K + k) * kQs * n + tid * kQs;
+    }
+};
+
 template <int IO, int SIO, int K, bool VEC>
-__global__ void __launch_bounds__(K < 16 ? 128 : 256)
-block_norm_kernel(BlockNormParams p) {
+__global__ void __launch_bounds__(1024)
+block_norm_kernel(BlockNormParams p, int stages) {
+    using S = NormSlots<IO, SIO, K, 2, 1>;  // o, gate; r
+    extern __shared__ __align__(16) char ring[];
     __shared__ float red[2][1][32];
-    const int tpr = blockDim.x;
+    constexpr int kEi = IO == IO_F32 ? 4 : 2, kEs = SIO == IO_F32 ? 4 : 2;
+    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + tx;
     const float inv_d = 1.f / (float)p.D;
-    for (long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y; row < p.rows;
-         row += (long long)gridDim.x * blockDim.y) {
-        const long long base = row * p.D, gbase = p.gate ? row / p.rows_per_gate * p.D : 0;
-        Raw4 ro[K], rr[K];
+    const long long step = (long long)gridDim.x * blockDim.y;
+    auto copy = [&](long long row, char *slot) {
+        if (row < p.rows) {
+            const long long base = row * p.D + tx * 4, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 4 : 0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            ro[k] = load_raw4<IO, VEC>(p.o, base + c, p.o ? nv : 0, nv);
-            rr[k] = load_raw4<SIO, VEC, false>(p.r, base + c, nv, nv);
+            for (int k = 0; k < K; ++k) {
+                const int nv = min(4, p.D - (tx + tpr * k) * 4), c = tpr * k * 4;
+                copy_quad<SIO, VEC>(slot + S::stream(0, k, tid, nthr), static_cast<const char *>(p.r) + (base + c) * kEs, nv);
+                if (p.o) copy_quad<IO, VEC>(slot + S::block(0, k, tid, nthr), static_cast<const char *>(p.o) + (base + c) * kEi, nv);
+                if (p.gate) copy_quad<IO, VEC>(slot + S::block(1, k, tid, nthr), static_cast<const char *>(p.gate) + (gbase + c) * kEi, nv);
+            }
         }
+        cp_commit();
+    };
+    long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    char *slot = ring, *next = stages == 2 ? ring + nthr * S::kPerThread : ring;
+    if (stages == 2) copy(row, slot);
+    for (; row < p.rows; row += step) {
+        if (stages == 2) {
+            copy(row + step, next);
+            cp_wait<1>();
+        } else {
+            copy(row, slot);
+            cp_wait<0>();
+        }
+        const long long base = row * p.D + tx * 4;
         float inv = 1.f;
         if (p.o && p.w_post) {
             float2 s2 = dup(0.f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {  // zeros past the row's end
                 float2 o[2];
-                unpack_pairs<IO, VEC>(ro[k], o);
+                read_quad<IO>(slot + S::block(0, k, tid, nthr), o);
                 s2 = __ffma2_rn(o[0], o[0], s2);
                 s2 = __ffma2_rn(o[1], o[1], s2);
             }
@@ -105,23 +135,25 @@ block_norm_kernel(BlockNormParams p) {
         float2 s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
+            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
             float2 r[2];
+            read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
             if (p.o) {
-                float2 o[2], g[2], ws[2];
-                unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.gate, gbase + c, p.gate ? nv : 0, nv), g);
+                float2 o[2], ws[2];
                 post_weights<VEC>(p, c, nv, ws);
-                unpack_pairs<IO, VEC>(ro[k], o);
-                unpack_pairs<SIO, VEC>(rr[k], r);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (p.gate) ws[j] = __fmul2_rn(ws[j], g[j]);
-                    r[j] = __ffma2_rn(ws[j], __fmul2_rn(o[j], dup(inv)), r[j]);
+                read_quad<IO>(slot + S::block(0, k, tid, nthr), o);
+                if (p.gate) {
+                    float2 g[2];
+                    read_quad<IO>(slot + S::block(1, k, tid, nthr), g);
+                    ws[0] = __fmul2_rn(ws[0], g[0]);
+                    ws[1] = __fmul2_rn(ws[1], g[1]);
                 }
-                rr[k] = pack_pairs<SIO, VEC>(r);  // rounded as it is stored
-                if (nv > 0) store_raw4<SIO, VEC>(p.r_out, base + c, nv, rr[k]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) r[j] = __ffma2_rn(ws[j], __fmul2_rn(o[j], dup(inv)), r[j]);
+                write_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);  // rounded as it is stored
+                if (nv > 0) store_pairs<SIO, VEC>(p.r_out, base + tpr * k * 4, nv, r);
+                read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
             }
-            unpack_pairs<SIO, VEC>(rr[k], r);
             s2 = __ffma2_rn(r[0], r[0], s2);
             s2 = __ffma2_rn(r[1], r[1], s2);
         }
@@ -130,23 +162,32 @@ block_norm_kernel(BlockNormParams p) {
         const float2 inv2 = dup(rsqrtf(ss[0] * inv_d + p.eps));
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
+            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
             float2 r[2], wp[2];
             weights<VEC>(p.w_pre, c, nv, wp);
-            unpack_pairs<SIO, VEC>(rr[k], r);
+            read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
             r[0] = __fmul2_rn(__fmul2_rn(r[0], inv2), wp[0]);
             r[1] = __fmul2_rn(__fmul2_rn(r[1], inv2), wp[1]);
-            if (nv > 0) store_raw4<IO, VEC>(p.n, base + c, nv, pack_pairs<IO, VEC>(r));
+            if (nv > 0) store_pairs<IO, VEC>(p.n, base + tpr * k * 4, nv, r);
         }
         if (!(p.o && p.w_post) && blockDim.x > 32) __syncthreads();  // one reduction per row only: its slot is free again
+        char *t = slot;
+        slot = next;
+        next = t;
     }
 }
 
-template <int IO, int SIO, int K, bool VEC>
-__global__ void __launch_bounds__(512, 1)
-block_norm_bwd_kernel(BlockNormParams p) {
+// MAXT: the threads a row may take (fewer leave each more registers).  whole: the
+// slots hold dr_out and the gate too; rows too wide for that load them where they are used.
+template <int IO, int SIO, int K, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1)
+block_norm_bwd_kernel(BlockNormParams p, int stages, int whole) {
+    using S = NormSlots<IO, SIO, K, 3, 2>;   // o, dn, gate; r', dr_out
+    using T = NormSlots<IO, SIO, K, 2, 1>;   // o, dn; r'
+    extern __shared__ __align__(16) char ring[];
     __shared__ float red[2][3][32];
-    const int tpr = blockDim.x;
+    constexpr int kEi = IO == IO_F32 ? 4 : 2, kEs = SIO == IO_F32 ? 4 : 2;
+    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + tx;
     const long long chunk = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (chunk >= p.chunks) return;  // blockDim.y > 1 only for rows of one warp
     const bool seq_gate = p.gate && p.rows_per_gate > 1;
@@ -159,35 +200,57 @@ block_norm_bwd_kernel(BlockNormParams p) {
         r0 = chunk * p.chunk_rows;
         r1 = min(p.rows, r0 + p.chunk_rows);
     }
-    float2 acc1[K][2], acc2[K][2];
+    auto off_o = [&](int k) { return whole ? S::block(0, k, tid, nthr) : T::block(0, k, tid, nthr); };
+    auto off_n = [&](int k) { return whole ? S::block(1, k, tid, nthr) : T::block(1, k, tid, nthr); };
+    auto off_r = [&](int k) { return whole ? S::stream(0, k, tid, nthr) : T::stream(0, k, tid, nthr); };
+    auto copy = [&](long long row, char *slot) {
+        if (row < r1) {
+            const long long base = row * p.D + tx * 4, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 4 : 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) acc1[k][0] = acc1[k][1] = acc2[k][0] = acc2[k][1] = dup(0.f);
+            for (int k = 0; k < K; ++k) {
+                const int nv = min(4, p.D - (tx + tpr * k) * 4), c = tpr * k * 4;
+                copy_quad<SIO, VEC>(slot + off_r(k), static_cast<const char *>(p.r_out) + (base + c) * kEs, nv);
+                copy_quad<IO, VEC>(slot + off_n(k), static_cast<const char *>(p.dn) + (base + c) * kEi, nv);
+                if (p.o) copy_quad<IO, VEC>(slot + off_o(k), static_cast<const char *>(p.o) + (base + c) * kEi, nv);
+                if (!whole) continue;
+                if (p.dr_out) copy_quad<SIO, VEC>(slot + S::stream(1, k, tid, nthr), static_cast<const char *>(p.dr_out) + (base + c) * kEs, nv);
+                if (p.gate) copy_quad<IO, VEC>(slot + S::block(2, k, tid, nthr), static_cast<const char *>(p.gate) + (gbase + c) * kEi, nv);
+            }
+        }
+        cp_commit();
+    };
+    char *slot = ring, *next = stages == 2 ? ring + nthr * (whole ? S::kPerThread : T::kPerThread) : ring;
+    if (stages == 2) copy(r0, slot);
+    float2 acc1[K][2], acc2[K][2], wp[K][2], ws[K][2];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
+        acc1[k][0] = acc1[k][1] = acc2[k][0] = acc2[k][1] = dup(0.f);
+        weights<VEC>(p.w_pre, c, nv, wp[k]);
+        post_weights<VEC>(p, c, nv, ws[k]);
+    }
     const float inv_d = 1.f / (float)p.D;
     for (long long row = r0; row < r1; ++row) {
-        const long long base = row * p.D, gbase = p.gate ? row / p.rows_per_gate * p.D : 0;
-        Raw4 ro[K], rr[K], rg[K], rn[K], rd[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            rr[k] = load_raw4<SIO, VEC>(p.r_out, base + c, nv, nv);
-            rn[k] = load_raw4<IO, VEC>(p.dn, base + c, nv, nv);
-            ro[k] = load_raw4<IO, VEC>(p.o, base + c, p.o ? nv : 0, nv);
-            rd[k] = load_raw4<SIO, VEC>(p.dr_out, base + c, p.dr_out ? nv : 0, nv);
-            rg[k] = load_raw4<IO, VEC>(p.gate, gbase + c, p.gate ? nv : 0, nv);
+        if (stages == 2) {
+            copy(row + 1, next);
+            cp_wait<1>();
+        } else {
+            copy(row, slot);
+            cp_wait<0>();
         }
+        const long long base = row * p.D + tx * 4;
         float2 s0 = dup(0.f), s1 = dup(0.f), s2 = dup(0.f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            float2 r[2], n[2], o[2], wp[2];
-            weights<VEC>(p.w_pre, c, nv, wp);
-            unpack_pairs<SIO, VEC>(rr[k], r);
-            unpack_pairs<IO, VEC>(rn[k], n);
-            unpack_pairs<IO, VEC>(ro[k], o);
+        for (int k = 0; k < K; ++k) {  // zeros past the row's end
+            float2 r[2], n[2], o[2];
+            read_quad<SIO>(slot + off_r(k), r);
+            read_quad<IO>(slot + off_n(k), n);
+            if (p.o) read_quad<IO>(slot + off_o(k), o);
+            else o[0] = o[1] = dup(0.f);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 s0 = __ffma2_rn(r[j], r[j], s0);
-                s1 = __ffma2_rn(__fmul2_rn(n[j], wp[j]), r[j], s1);
+                s1 = __ffma2_rn(__fmul2_rn(n[j], wp[k][j]), r[j], s1);
                 s2 = __ffma2_rn(o[j], o[j], s2);
             }
         }
@@ -195,68 +258,66 @@ block_norm_bwd_kernel(BlockNormParams p) {
         row_sum(s, red[0]);
         const float inv2 = rsqrtf(s[0] * inv_d + p.eps), m2 = s[1] * inv_d * inv2 * inv2;
         const float inv = p.w_post ? rsqrtf(s[2] * inv_d + p.eps) : 1.f;
-        float2 t2 = dup(0.f);  // u . o
+        float2 t2 = dup(0.f), u[K][2];  // u . o
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            float2 dr[2], r[2], n[2], wp[2];
-            weights<VEC>(p.w_pre, c, nv, wp);
-            unpack_pairs<SIO, VEC>(rr[k], r);
-            unpack_pairs<IO, VEC>(rn[k], n);
-            unpack_pairs<SIO, VEC>(rd[k], dr);
+            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
+            const long long at = base + tpr * k * 4;
+            float2 dr[2], r[2], n[2];
+            read_quad<SIO>(slot + off_r(k), r);
+            read_quad<IO>(slot + off_n(k), n);
+            if (!p.dr_out) dr[0] = dr[1] = dup(0.f);
+            else if (whole) read_quad<SIO>(slot + S::stream(1, k, tid, nthr), dr);
+            else unpack_pairs<SIO, VEC>(load_raw4<SIO, VEC>(p.dr_out, at, nv, nv), dr);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {  // dr = (v - r' inv2^2 mean(v r')) inv2 + dr_out
-                const float2 v = __ffma2_rn(r[j], dup(-m2), __fmul2_rn(n[j], wp[j]));
+                const float2 v = __ffma2_rn(r[j], dup(-m2), __fmul2_rn(n[j], wp[k][j]));
                 dr[j] = __ffma2_rn(v, dup(inv2), dr[j]);
                 acc2[k][j] = __ffma2_rn(n[j], __fmul2_rn(r[j], dup(inv2)), acc2[k][j]);
             }
-            if (nv > 0) store_raw4<SIO, VEC>(p.dr, base + c, nv, pack_pairs<SIO, VEC>(dr));
+            if (nv > 0) store_pairs<SIO, VEC>(p.dr, at, nv, dr);
             if (!p.o) continue;
-            float2 o[2], g[2], ws[2], u[2], dg[2];
-            post_weights<VEC>(p, c, nv, ws);
-            unpack_pairs<IO, VEC>(ro[k], o);
-            if (p.gate) unpack_pairs<IO, VEC>(rg[k], g);
-            else g[0] = g[1] = dup(1.f);
+            float2 o[2], g[2], dg[2];
+            read_quad<IO>(slot + off_o(k), o);
+            if (!p.gate) g[0] = g[1] = dup(1.f);
+            else if (whole) read_quad<IO>(slot + S::block(2, k, tid, nthr), g);
+            else unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.gate, row / p.rows_per_gate * p.D + c, nv, nv), g);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 dh = __fmul2_rn(dr[j], __fmul2_rn(o[j], dup(inv)));  // dr hat_o
-                dg[j] = __fmul2_rn(dh, ws[j]);
-                u[j] = __fmul2_rn(__fmul2_rn(g[j], dr[j]), ws[j]);
-                t2 = __ffma2_rn(u[j], o[j], t2);
+                dg[j] = __fmul2_rn(dh, ws[k][j]);
+                u[k][j] = __fmul2_rn(__fmul2_rn(g[j], dr[j]), ws[k][j]);
+                t2 = __ffma2_rn(u[k][j], o[j], t2);
                 acc1[k][j] = seq_gate ? __fadd2_rn(acc1[k][j], dh) : __ffma2_rn(dh, g[j], acc1[k][j]);
             }
-            if (p.gate && !seq_gate && nv > 0) store_raw4<IO, VEC>(p.dgate, base + c, nv, pack_pairs<IO, VEC>(dg));
-            // u takes dn's and dr_out's place for the last pass, in 32 bits
-            rn[k].w[2] = __float_as_uint(u[0].x);
-            rn[k].w[3] = __float_as_uint(u[0].y);
-            rd[k].w[2] = __float_as_uint(u[1].x);
-            rd[k].w[3] = __float_as_uint(u[1].y);
+            if (p.gate && !seq_gate && nv > 0) store_pairs<IO, VEC>(p.dgate, at, nv, dg);
         }
-        if (!p.o) {
-            if (blockDim.x > 32) __syncthreads();  // the slot is free again
-            continue;
-        }
-        float t[1] = {t2.x + t2.y};
-        row_sum(t, red[1]);
-        const float m = p.w_post ? t[0] * inv_d * inv * inv : 0.f;
+        if (p.o) {
+            float t[1] = {t2.x + t2.y};
+            row_sum(t, red[1]);
+            const float m = p.w_post ? t[0] * inv_d * inv * inv : 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (threadIdx.x + tpr * k) * 4, nv = min(4, p.D - c);
-            float2 o[2];
-            unpack_pairs<IO, VEC>(ro[k], o);
-            const float2 u[2] = {make_float2(__uint_as_float(rn[k].w[2]), __uint_as_float(rn[k].w[3])),
-                                 make_float2(__uint_as_float(rd[k].w[2]), __uint_as_float(rd[k].w[3]))};
+            for (int k = 0; k < K; ++k) {
+                const int nv = min(4, p.D - (tx + tpr * k) * 4);
+                float2 o[2];
+                read_quad<IO>(slot + off_o(k), o);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[j]), dup(inv));
-            if (nv > 0) store_raw4<IO, VEC>(p.d_o, base + c, nv, pack_pairs<IO, VEC>(o));
+                for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[k][j]), dup(inv));
+                if (nv > 0) store_pairs<IO, VEC>(p.d_o, base + tpr * k * 4, nv, o);
+            }
+        } else if (blockDim.x > 32) {
+            __syncthreads();  // the slot of the sums is free again
         }
+        char *t = slot;
+        slot = next;
+        next = t;
     }
     float *part = p.part + chunk * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int c = (threadIdx.x + tpr * k) * 4 + j;
+            const int c = (tx + tpr * k) * 4 + j;
             if (c < p.D) {
                 part[c] = j & 1 ? acc1[k][j / 2].y : acc1[k][j / 2].x;
                 part[p.D + c] = j & 1 ? acc2[k][j / 2].y : acc2[k][j / 2].x;
@@ -311,10 +372,11 @@ dim3 row_block(int D, int K) {
     return dim3(tpr, tpr == 32 ? 4 : 1);
 }
 
-// Elements per thread, in fours: the fewest that a warp's row takes, up to 16 forwards and 4 (8 for rows
-// past 8192) backwards; wider rows take more warps.
-int norm_k(int D) { return D <= 128 ? 1 : D <= 256 ? 2 : D <= 512 ? 4 : D <= 1024 ? 8 : 16; }
-int norm_bwd_k(int D) { return D <= 128 ? 1 : D <= 256 ? 2 : D <= 8192 ? 4 : 8; }
+// Runs of four elements per thread: the fewest that a warp's row takes, up to 4 (backwards 8 for rows
+// past 8192, whose registers would not allow more threads); wider rows take more warps.
+int norm_k(int D, bool backward) { return D <= 128 ? 1 : D <= 256 ? 2 : backward && D > 8192 ? 8 : 4; }
+
+constexpr int kNormSmem = 227 * 1024 - 1024;  // the most a CTA may hold, less the sums
 
 bool norm_vec(const BlockNormParams &p, int io, int sio) {
     auto ok = [](const void *q, int t) { return reinterpret_cast<uintptr_t>(q) % (t == IO_F32 ? 16 : 8) == 0; };
@@ -327,46 +389,53 @@ template <int IO, int SIO, int K>
 cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
     auto *kernel = norm_vec(p, IO, SIO) ? block_norm_kernel<IO, SIO, K, true> : block_norm_kernel<IO, SIO, K, false>;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block.x * block.y, 0) !=
-            cudaSuccess || per_sm < 1) {
-        (void)cudaGetLastError();
-        per_sm = 1;
+    const int row = (int)(block.x * block.y) * NormSlots<IO, SIO, K, 2, 1>::kPerThread;
+    const int stages = 2 * row <= kNormSmem ? 2 : 1, bytes = stages * row;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const long long need = (p.rows + block.y - 1) / block.y;
+    long long grid = scan_sm_count();
+    if (need > grid) {  // as many CTAs as the SMs hold, each walking rows
+        int per_sm = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block.x * block.y, bytes);
+        if (e != cudaSuccess) return e;
+        grid *= per_sm > 0 ? per_sm : 1;
     }
-    const long long need = (p.rows + block.y - 1) / block.y, most = (long long)scan_sm_count() * per_sm;
-    kernel<<<(unsigned)(need < most ? need : most), block, 0, s>>>(p);
+    kernel<<<(unsigned)(need < grid ? need : grid), block, bytes, s>>>(p, stages);
     return cudaGetLastError();
 }
 
 template <int IO, int SIO>
 cudaError_t launch_norm_io(const BlockNormParams &p, cudaStream_t s) {
-    switch (norm_k(p.D)) {
+    switch (norm_k(p.D, false)) {
         case 1: return launch_norm_as<IO, SIO, 1>(p, s);
         case 2: return launch_norm_as<IO, SIO, 2>(p, s);
-        case 4: return launch_norm_as<IO, SIO, 4>(p, s);
-        case 8: return launch_norm_as<IO, SIO, 8>(p, s);
-        default: return launch_norm_as<IO, SIO, 16>(p, s);
+        default: return launch_norm_as<IO, SIO, 4>(p, s);
     }
 }
 
-template <int IO, int SIO, int K>
+template <int IO, int SIO, int K, int MAXT>
 cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
-    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_bwd_kernel<IO, SIO, K, true> : block_norm_bwd_kernel<IO, SIO, K, false>;
-    kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_bwd_kernel<IO, SIO, K, true, MAXT> : block_norm_bwd_kernel<IO, SIO, K, false, MAXT>;
+    const int n = block.x * block.y, row = n * NormSlots<IO, SIO, K, 3, 2>::kPerThread;
+    const int whole = row <= kNormSmem, mine = whole ? row : n * NormSlots<IO, SIO, K, 2, 1>::kPerThread;
+    const int stages = 2 * mine <= kNormSmem ? 2 : 1, bytes = stages * mine;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages, whole);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     block_norm_sum_kernel<IO><<<(p.D + 31) / 32, dim3(32, 32), 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int IO, int SIO>
 cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
-    switch (norm_bwd_k(p.D)) {
-        case 1: return launch_norm_bwd_as<IO, SIO, 1>(p, s);
-        case 2: return launch_norm_bwd_as<IO, SIO, 2>(p, s);
-        case 4: return launch_norm_bwd_as<IO, SIO, 4>(p, s);
-        default: return launch_norm_bwd_as<IO, SIO, 8>(p, s);
+    switch (norm_k(p.D, true)) {
+        case 1: return launch_norm_bwd_as<IO, SIO, 1, 128>(p, s);
+        case 2: return launch_norm_bwd_as<IO, SIO, 2, 128>(p, s);
+        case 4: return p.D <= 2048 ? launch_norm_bwd_as<IO, SIO, 4, 128>(p, s) : launch_norm_bwd_as<IO, SIO, 4, 512>(p, s);
+        default: return launch_norm_bwd_as<IO, SIO, 8, 512>(p, s);
     }
 }
 
@@ -374,7 +443,7 @@ cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
 
 // Chunks for about 16 warps per SM, two at least; a chunk never spans two gates of several rows.
 void block_norm_chunks(BlockNormParams &p) {
-    const int warps = row_block(p.D, norm_bwd_k(p.D)).x / 32;
+    const int warps = row_block(p.D, norm_k(p.D, true)).x / 32;
     const long long target = (warps < 8 ? 16 / warps : 2) * (long long)scan_sm_count();
     const bool seq_gate = p.gate && p.rows_per_gate > 1;
     const long long span = seq_gate ? p.rows_per_gate : p.rows, spans = p.rows / span;

@@ -8,7 +8,11 @@
 // against 4 bytes of 16-bit traffic: bound by HBM.  A thread owns four channels
 // over a run of tokens and slides the window in registers, so each token is
 // read once but for the W-1 before its run; a warp's 32 threads cover 128
-// consecutive channels of a token.  Eight tokens' loads go out together.
+// consecutive channels of a token.  Tokens are copied into the thread's own ring in
+// shared memory, two blocks of eight ahead, so the loads run on beside the arithmetic
+// and need neither registers nor a barrier.
+#include <math.h>
+
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -16,9 +20,14 @@ namespace ssd {
 namespace {
 
 constexpr int kCx = 32, kCy = 4;   // threads: channel quads, runs
-constexpr int kRun = 32;           // tokens per thread
-constexpr int kCtaTokens = kCy * kRun;
 constexpr int kAhead = 8;
+constexpr int kRun = 32;  // tokens per thread (backwards: ConvParams::run)
+constexpr int kHalo(int W) { return W <= 4 ? 3 : 7; }  // KT - 1
+
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
 
 // v at token t as loaded: x inside the row, the carried rows before it, zeros elsewhere.
 template <int IO, bool VEC>
@@ -46,14 +55,24 @@ __device__ __forceinline__ void store_pairs(char *dst, int nv, const float2 (&v)
 // Taps sit right-aligned in KT slots (slot KT-1 is the current token), so every index is a constant.
 template <int KT>
 __device__ __forceinline__ void load_taps(const ConvParams &p, int c, int nv, float2 (&w)[KT][2], float2 (&bias)[2]) {
+    const bool rows4 = KT == 4 && p.W == 4 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+        if (rows4) {  // a channel's taps in one load
+            const Raw4 r = load_raw4<IO_F32, true>(p.w, (long long)(c + j) * 4, j < nv, 4);
 #pragma unroll
-        for (int s = 0; s < KT; ++s) {
-            const int k = s - (KT - p.W);
-            const float v = k >= 0 && j < nv ? __ldg(p.w + (long long)(c + j) * p.W + k) : 0.f;
-            if (j & 1) w[s][j / 2].y = v;
-            else w[s][j / 2].x = v;
+            for (int s = 0; s < KT; ++s) {
+                if (j & 1) w[s][j / 2].y = __uint_as_float(r.w[s & 3]);
+                else w[s][j / 2].x = __uint_as_float(r.w[s & 3]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < KT; ++s) {
+                const int k = s - (KT - p.W);
+                const float v = k >= 0 && j < nv ? __ldg(p.w + (long long)(c + j) * p.W + k) : 0.f;
+                if (j & 1) w[s][j / 2].y = v;
+                else w[s][j / 2].x = v;
+            }
         }
         const float v = p.bias && j < nv ? __ldg(p.bias + c + j) : 0.f;
         if (j & 1) bias[j / 2].y = v;
@@ -62,8 +81,10 @@ __device__ __forceinline__ void load_taps(const ConvParams &p, int c, int nv, fl
 }
 
 template <int IO, int KT, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 6 : 1)
+__global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 8 : 1)
 conv_carry_kernel(ConvParams p) {
+    constexpr int kQ = IO == IO_F32 ? 16 : 8;  // bytes of four elements
+    __shared__ __align__(16) char ring[2 * kAhead][kCx * kCy * kQ];
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     if (c >= p.C) return;
     const int nv = min(4, p.C - c), b = blockIdx.z;
@@ -78,29 +99,38 @@ conv_carry_kernel(ConvParams p) {
         return;
     }
     constexpr int kEs = IO == IO_F32 ? 4 : 2;
-    const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
+    const int t0 = (blockIdx.y * kCy + threadIdx.y) * kRun, t1 = min(t0 + kRun, p.L);
     if (t0 >= t1) return;
     float2 w[KT][2], bias[2], win[KT][2];
-    load_taps<KT>(p, c, nv, w, bias);
-#pragma unroll
-    for (int s = 1; s < KT; ++s)  // slots 0..KT-2 of the first step are tokens t0-KT+1 .. t0-1
-        unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
     const char *px = static_cast<const char *>(p.x) + (b * p.xs[0] + t0 * p.xs[1] + c) * kEs;
     char *py = static_cast<char *>(p.y) + (((long long)b * p.L + t0) * p.C + c) * kEs;
     const long long sx = p.xs[1] * kEs, sy = (long long)p.C * kEs;
     const int live = min(t1, len);
-    for (int t = t0; t < t1; t += kAhead) {
-        Raw4 r[kAhead];
+    const int me = (threadIdx.y * kCx + threadIdx.x) * kQ;
+    auto copy = [&](int t) {  // tokens t .. t + kAhead - 1
+        const int slot = (t - t0) & kAhead;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            r[i] = load_raw4<IO, VEC>(px, 0, live - t - i, nv);
+            copy_quad<IO, VEC>(ring[slot + i] + me, px, t + i < live ? nv : 0);
             px += sx;
         }
+        cp_commit();
+    };
+    copy(t0);
+    copy(t0 + kAhead);
+    load_taps<KT>(p, c, nv, w, bias);
+#pragma unroll
+    for (int s = 1; s < KT; ++s)  // slots 0..KT-2 of the first step are tokens t0-KT+1 .. t0-1
+        unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
+    // A block of kAhead tokens; EDGE: some of them are past the run's or the row's end.
+    auto block = [&](int t, auto edge) {
+        constexpr bool EDGE = decltype(edge)::value;
+        const int slot = (t - t0) & kAhead;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
             for (int s = 0; s < KT - 1; ++s) win[s][0] = win[s + 1][0], win[s][1] = win[s + 1][1];
-            unpack_pairs<IO, VEC>(r[i], win[KT - 1]);
+            read_quad<IO>(ring[slot + i] + me, win[KT - 1]);
             float2 o[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -108,11 +138,17 @@ conv_carry_kernel(ConvParams p) {
 #pragma unroll
                 for (int s = 0; s < KT; ++s) a = __ffma2_rn(w[s][j], win[s][j], a);
                 o[j] = SILU ? silu2(a) : a;
-                if (t + i >= live) o[j] = dup(0.f);
+                if (EDGE && t + i >= live) o[j] = dup(0.f);
             }
-            if (t + i < t1) store_pairs<IO, VEC>(py, nv, o);
+            if (!EDGE || t + i < t1) store_pairs<IO, VEC>(py, nv, o);
             py += sy;
         }
+    };
+    for (int t = t0; t < t1; t += kAhead) {
+        cp_wait<1>();
+        if (t + kAhead <= live) block(t, Flag<false>{});
+        else block(t, Flag<true>{});
+        copy(t + 2 * kAhead);
     }
 }
 
@@ -123,21 +159,19 @@ conv_carry_kernel(ConvParams p) {
 template <int IO, int KT, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 4 : 1)
 conv_bwd_kernel(ConvParams p) {
+    constexpr int kQ = IO == IO_F32 ? 16 : 8;
     __shared__ __align__(16) float red[kCy][kCx * 4];
+    extern __shared__ __align__(16) char ring[];  // [2 kAhead][2][kCx kCy] of four elements: x, dy
     const int c = (blockIdx.x * kCx + threadIdx.x) * 4;
     const int nv = min(4, p.C - c), b = blockIdx.z;
     const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
-    const int t0 = blockIdx.y * kCtaTokens + threadIdx.y * kRun, t1 = min(t0 + kRun, p.L);
+    const int t0 = (blockIdx.y * kCy + threadIdx.y) * p.run, t1 = min(t0 + p.run, p.L);
     constexpr int kEs = IO == IO_F32 ? 4 : 2;
     float2 dw[KT][2], db[2] = {dup(0.f), dup(0.f)};
 #pragma unroll
     for (int s = 0; s < KT; ++s) dw[s][0] = dw[s][1] = dup(0.f);
     if (c < p.C && t0 < t1) {
         float2 w[KT][2], bias[2], win[KT][2], dp[KT][2];  // dp[i]: of token t - i
-        load_taps<KT>(p, c, nv, w, bias);
-#pragma unroll
-        for (int s = 1; s < KT; ++s)
-            unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
 #pragma unroll
         for (int s = 0; s < KT; ++s) dp[s][0] = dp[s][1] = dup(0.f);
         const char *px = static_cast<const char *>(p.x) + (b * p.xs[0] + t0 * p.xs[1] + c) * kEs;
@@ -146,15 +180,30 @@ conv_bwd_kernel(ConvParams p) {
         char *pdx = static_cast<char *>(p.dx) + (o0 - (long long)(KT - 1) * p.C) * kEs;
         const long long sx = p.xs[1] * kEs, sy = (long long)p.C * kEs;
         const int tend = t1 + KT - 1, live = min(tend, len);
-        for (int t = t0; t < tend; t += kAhead) {
-            Raw4 r[kAhead], rg[kAhead];
+        constexpr int kLine = kCx * kCy * kQ;
+        char *mine_ring = ring + (threadIdx.y * kCx + threadIdx.x) * kQ;
+        auto copy = [&](int t) {  // tokens t .. t + kAhead - 1
+            char *slot = mine_ring + ((t - t0) & kAhead) * 2 * kLine;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                r[i] = load_raw4<IO, VEC>(px, 0, live - t - i, nv);
-                rg[i] = load_raw4<IO, VEC>(pdy, 0, live - t - i, nv);
+                const int n = t + i < live ? nv : 0;
+                copy_quad<IO, VEC>(slot + 2 * i * kLine, px, n);
+                copy_quad<IO, VEC>(slot + (2 * i + 1) * kLine, pdy, n);
                 px += sx;
                 pdy += sy;
             }
+            cp_commit();
+        };
+        copy(t0);
+        copy(t0 + kAhead);
+        load_taps<KT>(p, c, nv, w, bias);
+#pragma unroll
+        for (int s = 1; s < KT; ++s)
+            unpack_pairs<IO, VEC>(conv_value<IO, VEC>(p, b, (long long)t0 - KT + s, len, c, nv), win[s]);
+        // A block of kAhead tokens; EDGE: some are past the run or the row, or complete entries of v outside them.
+        auto block = [&](int t, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+            const char *slot = mine_ring + ((t - t0) & kAhead) * 2 * kLine;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int tt = t + i;
@@ -162,9 +211,9 @@ conv_bwd_kernel(ConvParams p) {
                 for (int s = 0; s < KT - 1; ++s) win[s][0] = win[s + 1][0], win[s][1] = win[s + 1][1];
 #pragma unroll
                 for (int s = KT - 1; s > 0; --s) dp[s][0] = dp[s - 1][0], dp[s][1] = dp[s - 1][1];
-                unpack_pairs<IO, VEC>(r[i], win[KT - 1]);
+                read_quad<IO>(slot + 2 * i * kLine, win[KT - 1]);
                 float2 g[2], o[2];
-                unpack_pairs<IO, VEC>(rg[i], g);  // zeros past the row's tokens
+                read_quad<IO>(slot + (2 * i + 1) * kLine, g);  // zeros past the row's tokens
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (SILU) {  // g silu'(a) = g s (1 + a (1 - s)), s = sigmoid(a)
@@ -172,12 +221,12 @@ conv_bwd_kernel(ConvParams p) {
 #pragma unroll
                         for (int s = 0; s < KT; ++s) a = __ffma2_rn(w[s][j], win[s][j], a);
                         const float2 sg = sigmoid2(a);
-                        const float2 rest = __fadd2_rn(dup(1.f), make_float2(-sg.x, -sg.y));
-                        g[j] = __fmul2_rn(__fmul2_rn(g[j], sg), __ffma2_rn(a, rest, dup(1.f)));
-                        if (tt >= live) g[j] = dup(0.f);
+                        const float2 slope = __ffma2_rn(__fmul2_rn(a, sg), __ffma2_rn(sg, dup(-1.f), dup(1.f)), sg);
+                        g[j] = __fmul2_rn(g[j], slope);
+                        if (EDGE && tt >= live) g[j] = dup(0.f);
                     }
                     dp[0][j] = g[j];
-                    const float2 mine = tt < t1 ? g[j] : dup(0.f);
+                    const float2 mine = !EDGE || tt < t1 ? g[j] : dup(0.f);
                     db[j] = __fadd2_rn(db[j], mine);
 #pragma unroll
                     for (int s = 0; s < KT; ++s) dw[s][j] = __ffma2_rn(mine, win[s][j], dw[s][j]);
@@ -187,21 +236,31 @@ conv_bwd_kernel(ConvParams p) {
                     o[j] = a;
                 }
                 const int tau = tt - (KT - 1);  // the entry of v this step completes
-                if (p.dfinal && tt < tend && tau >= len - (p.W - 1) && tau < len) {
-                    float2 f[2];
-                    unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, 1, nv), f);
-                    o[0] = __fadd2_rn(o[0], f[0]);
-                    o[1] = __fadd2_rn(o[1], f[1]);
-                }
-                if (tau < 0) {
-                    if (t0 == 0 && p.dh0 && tau >= -(p.W - 1))
-                        store_pairs<IO, VEC>(static_cast<char *>(p.dh0) + (((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c) * kEs, nv, o);
-                } else if (tau >= t0 && tau < t1) {
-                    if (tau >= len) o[0] = o[1] = dup(0.f);
+                if (!EDGE) {
                     store_pairs<IO, VEC>(pdx, nv, o);
+                } else {
+                    if (p.dfinal && tt < tend && tau >= len - (p.W - 1) && tau < len) {
+                        float2 f[2];
+                        unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.dfinal, ((long long)b * (p.W - 1) + tau + p.W - 1 - len) * p.C + c, 1, nv), f);
+                        o[0] = __fadd2_rn(o[0], f[0]);
+                        o[1] = __fadd2_rn(o[1], f[1]);
+                    }
+                    if (tau < 0) {
+                        if (t0 == 0 && p.dh0 && tau >= -(p.W - 1))
+                            store_pairs<IO, VEC>(static_cast<char *>(p.dh0) + (((long long)b * (p.W - 1) + tau + p.W - 1) * p.C + c) * kEs, nv, o);
+                    } else if (tau >= t0 && tau < t1) {
+                        if (tau >= len) o[0] = o[1] = dup(0.f);
+                        store_pairs<IO, VEC>(pdx, nv, o);
+                    }
                 }
                 pdx += sy;
             }
+        };
+        for (int t = t0; t < tend; t += kAhead) {
+            cp_wait<1>();
+            if (t >= t0 + KT - 1 && t + kAhead <= min(t1, live) && t + kAhead - KT < len - (p.W - 1)) block(t, Flag<false>{});
+            else block(t, Flag<true>{});
+            copy(t + 2 * kAhead);
         }
     }
     const long long row = (long long)b * gridDim.y + blockIdx.y;
@@ -251,7 +310,7 @@ bool conv_vec(const ConvParams &p, int io) {
 
 template <int IO>
 cudaError_t launch_conv_io(const ConvParams &p, cudaStream_t s) {
-    const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens + 1, p.B);
+    const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCy * kRun - 1) / (kCy * kRun) + 1, p.B);
     static constexpr decltype(&conv_carry_kernel<IO, 4, true, true>) kernels[2][2][2] = {
         {{conv_carry_kernel<IO, 4, false, false>, conv_carry_kernel<IO, 4, false, true>},
          {conv_carry_kernel<IO, 4, true, false>, conv_carry_kernel<IO, 4, true, true>}},
@@ -264,25 +323,44 @@ cudaError_t launch_conv_io(const ConvParams &p, cudaStream_t s) {
 
 template <int IO>
 cudaError_t launch_conv_bwd_io(const ConvParams &p, cudaStream_t s) {
-    const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), (p.L + kCtaTokens - 1) / kCtaTokens, p.B);
+    const int rows = (int)(conv_bwd_part_rows(p) / p.B);
+    const dim3 grid((p.C + 4 * kCx - 1) / (4 * kCx), rows, p.B);
     static constexpr decltype(&conv_bwd_kernel<IO, 4, true, true>) kernels[2][2][2] = {
         {{conv_bwd_kernel<IO, 4, false, false>, conv_bwd_kernel<IO, 4, false, true>},
          {conv_bwd_kernel<IO, 4, true, false>, conv_bwd_kernel<IO, 4, true, true>}},
         {{conv_bwd_kernel<IO, 8, false, false>, conv_bwd_kernel<IO, 8, false, true>},
          {conv_bwd_kernel<IO, 8, true, false>, conv_bwd_kernel<IO, 8, true, true>}}};
     auto *kernel = kernels[p.W > 4][conv_vec(p, IO)][p.silu != 0];
-    kernel<<<grid, dim3(kCx, kCy), 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    constexpr int kBytes = 2 * kAhead * 2 * kCx * kCy * (IO == IO_F32 ? 16 : 8);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    conv_bwd_sum_kernel<<<dim3((p.C + 31) / 32, p.W + 1), dim3(32, 8), 0, s>>>(p, (int)conv_bwd_part_rows(p.B, p.L, p.C));
+    kernel<<<grid, dim3(kCx, kCy), kBytes, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    conv_bwd_sum_kernel<<<dim3((p.C + 31) / 32, p.W + 1), dim3(32, 8), 0, s>>>(p, rows * p.B);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-long long conv_bwd_part_rows(int B, int L, int C) {
-    (void)C;
-    return (long long)B * ((L + kCtaTokens - 1) / kCtaTokens);
+// The run of a thread backwards: whole blocks of kAhead with the KT-1 tokens after
+// it, as many as make the CTAs' waves (four CTAs per SM) cheapest; a CTA's start
+// (taps, window) and end (sums) cost about two blocks.
+int conv_bwd_run(const ConvParams &p) {
+    const double slots = 4. * scan_sm_count();
+    int best = 0;
+    double least = 0.;
+    for (int m = 2; m <= 16; ++m) {
+        const int run = kAhead * m - kHalo(p.W), rows = (p.L + kCy * run - 1) / (kCy * run);
+        const long long ctas = (long long)((p.C + 4 * kCx - 1) / (4 * kCx)) * rows * p.B;
+        const double cost = ceil((double)ctas / slots) * (m + 2);
+        if (best == 0 || cost < least) best = run, least = cost;
+    }
+    return best;
+}
+
+long long conv_bwd_part_rows(const ConvParams &p) {
+    const int tokens = kCy * p.run;
+    return (long long)p.B * ((p.L + tokens - 1) / tokens);
 }
 
 cudaError_t launch_conv(const ConvParams &p, int io, cudaStream_t s) {

@@ -165,11 +165,12 @@ ssd_status check_conv(const ssd_conv_args *a, ssd::ConvParams &p) {
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.h0 = a->initial_state; p.lengths = a->lengths;
     p.y = a->y; p.final_state = a->final_state; p.silu = a->silu ? 1 : 0;
     if (!strides_of(a->x_stride, a->L, a->C, p.xs)) return fail(SSD_ERR_INVALID_ARG, "strides must be >= 0");
+    p.run = ssd::conv_bwd_run(p);
     return SSD_OK;
 }
 
 size_t conv_bwd_bytes(const ssd::ConvParams &p) {
-    return align_up((size_t)ssd::conv_bwd_part_rows(p.B, p.L, p.C) * (p.W + 1) * p.C * sizeof(float));
+    return align_up((size_t)ssd::conv_bwd_part_rows(p) * (p.W + 1) * p.C * sizeof(float));
 }
 
 ssd_status check_norm(const ssd_block_norm_args *a, ssd::BlockNormParams &p) {

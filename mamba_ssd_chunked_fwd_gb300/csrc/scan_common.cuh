@@ -77,10 +77,12 @@ struct ConvParams {
     void *dx, *dh0;
     float *dw, *dbias;
     float *part;  // [rows, W + 1, C] sums of dw (first W) and dbias
+    int run;      // tokens per thread, conv_bwd_run()
 };
 cudaError_t launch_conv(const ConvParams &p, int io, cudaStream_t s);
 cudaError_t launch_conv_bwd(const ConvParams &p, int io, cudaStream_t s);
-long long conv_bwd_part_rows(int B, int L, int C);
+int conv_bwd_run(const ConvParams &p);
+long long conv_bwd_part_rows(const ConvParams &p);
 
 // The block norm and its backward (block_norm.cu).
 struct BlockNormParams {
@@ -230,6 +232,9 @@ __device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
     }
 }
 
+template <int IO, bool VEC>
+__device__ __forceinline__ void store4_io(void *base, long long i, int nv, const float (&v)[4]);
+
 // Copies from global to shared memory that run on while the thread goes on
 // (cp.async); the thread that issued them waits with cp_wait.  What is not read is filled with zeros.
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
@@ -269,6 +274,47 @@ __device__ __forceinline__ void copy_chunk(void *dst, const char *src, int n) {
         u.z = e[4] | ((uint32_t)e[5] << 16); u.w = e[6] | ((uint32_t)e[7] << 16);
         *static_cast<uint4 *>(dst) = u;
     }
+}
+
+// Four elements of a row, of which the first n exist, in the same way (8 or 16 bytes).
+template <int IO, bool VEC>
+__device__ __forceinline__ void copy_quad(void *dst, const char *src, int n) {
+    if (IO == IO_F32) {
+        copy_chunk<IO_F32, VEC>(dst, src, n);
+    } else if (VEC) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                     "l"(n > 0 ? src : nullptr), "r"(n > 0 ? 8 : 0) : "memory");
+    } else {
+        uint16_t e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            e[j] = 0;
+            ldg_u16(e[j], src + 2 * j, j < n);
+        }
+        *static_cast<uint2 *>(dst) = make_uint2(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16));
+    }
+}
+template <int IO>
+__device__ __forceinline__ void read_quad(const void *src, float2 (&v)[2]) {
+    if (IO == IO_F32) {
+        const float4 f = *static_cast<const float4 *>(src);
+        v[0] = make_float2(f.x, f.y);
+        v[1] = make_float2(f.z, f.w);
+    } else {
+        const uint2 u = *static_cast<const uint2 *>(src);
+        const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (IO == IO_BF16) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else v[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        }
+    }
+}
+
+template <int IO>
+__device__ __forceinline__ void write_quad(void *dst, const float2 (&v)[2]) {
+    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+    store4_io<IO, true>(dst, 0, 4, f);
 }
 
 // A chunk from shared memory as pairs of floats.
@@ -379,46 +425,6 @@ __device__ __forceinline__ void unpack4_dt(const Raw4 &r, float (&v)[4], int dt3
     if (IO != IO_F32) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = dt32 ? __uint_as_float(r.w[j]) : v[j];
-    }
-}
-
-// unpack4's inverse, rounding to the type; and the store of what it gives.
-template <int IO, bool VEC>
-__device__ __forceinline__ Raw4 pack4(const float (&v)[4]) {
-    Raw4 r = {{0u, 0u, 0u, 0u}};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (IO == IO_F32) {
-            r.w[j] = __float_as_uint(v[j]);
-        } else {
-            const uint32_t h = IO == IO_BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
-                                             : (uint32_t)__half_as_ushort(__float2half_rn(v[j]));
-            if (!VEC) r.w[j] = h;
-            else r.w[j / 2] |= j & 1 ? h << 16 : h;
-        }
-    }
-    return r;
-}
-template <int IO, bool VEC>
-__device__ __forceinline__ void store_raw4(void *base, long long i, int nv, const Raw4 &r) {
-    if (IO == IO_F32) {
-        uint32_t *p = static_cast<uint32_t *>(base) + i;
-        if (VEC) {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < nv) p[j] = r.w[j];
-        }
-    } else {
-        uint16_t *p = static_cast<uint16_t *>(base) + i;
-        if (VEC) {
-            *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < nv) p[j] = (uint16_t)r.w[j];
-        }
     }
 }
 

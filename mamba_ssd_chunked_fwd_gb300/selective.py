@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -81,7 +82,16 @@ def _sized(cls):
 
 
 def _called(cls):
-    return [ctypes.POINTER(cls), _ptr_t]
+    return [_ptr_t, _ptr_t]  # the structure by reference, or its bytes
+
+
+def _packer(cls):
+    """The structure's layout for ``struct.pack``: filling it that way costs a
+    fifth of the ctypes constructor, which counts in a call of a few microseconds."""
+    code = {_i64: "q", _i32: "i", _f32: "f", _ptr_t: "P", _size: "N"}
+    packed = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_))
+    pad = ctypes.sizeof(cls) - packed.size  # the structure's tail
+    return struct.Struct(packed.format + "%dx" % pad if pad else packed.format).pack
 
 
 SIGNATURES = {
@@ -99,6 +109,7 @@ SIGNATURES = {
     "ssd_block_norm_bwd": _called(SsdBlockNormBwdArgs),
 }
 
+_pack_scan_step, _pack_conv_step = _packer(SsdScanStepArgs), _packer(SsdConvStepArgs)
 _CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _byref = ctypes.byref
 _pkg = None
@@ -114,14 +125,15 @@ def _host():
 
 
 def _call(name, args, dev):
-    """One C entry on the current stream of CUDA device ``dev``."""
+    """One C entry on the current stream of CUDA device ``dev``; args: a
+    reference to its structure, or the structure's bytes."""
     pkg = _pkg or _host()
     fn = getattr(pkg._lib or pkg.load_library(), name)
     if torch.cuda.current_device() == dev:
-        status = fn(_byref(args), torch._C._cuda_getCurrentRawStream(dev))
+        status = fn(args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(_byref(args), torch._C._cuda_getCurrentRawStream(dev))
+            status = fn(args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         pkg._check(status, name)
 
@@ -164,9 +176,9 @@ def _refuse(t, shape, dtype, dev, what):
 
 
 def _dense(t, shape, dtype, dev, what):
-    """The address of a dense tensor of this shape and type, or None."""
+    """The address of a dense tensor of this shape and type, or 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, shape, dtype, dev, what)
     return t.data_ptr()
@@ -205,7 +217,7 @@ def _tokens(t, shape, dtype, dev, what):
 def _rows(t, shape, dtype, dev, what):
     """(address, row stride) of a [B,...] tensor whose rows are dense."""
     if t is None:
-        return None, 0
+        return 0, 0
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         _refuse(t, shape, dtype, dev, what)
     if t.is_contiguous():
@@ -218,6 +230,14 @@ def _rows(t, shape, dtype, dev, what):
     if st[0] <= 0:
         raise ValueError(f"{what}: rows must be apart")
     return t.data_ptr(), st[0]
+
+
+def _output(x, out):
+    """(tensor, address) of a dense output of x's shape and type: ``out``, or a new one."""
+    if out is not None:
+        return out, _dense(out, x.shape, x.dtype, x.get_device(), "out")
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return y, y.data_ptr()
 
 
 def _ndim(t, n, what):
@@ -274,12 +294,12 @@ def selective_scan(x, dt, A, B, C, dt_softplus=False, return_final_state=False, 
     [D,N], D, dt_bias [D] and initial_states [B,D,N] are fp32.  ``lengths``
     (int32 [B], on the GPU): tokens per row; y is 0 past them."""
     _cuda(x, "selective_scan")
-    y = out if out is not None else torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    y = _output(x, out)[0]
     fin = torch.empty((x.shape[0], x.shape[2], A.shape[1]), device=x.device, dtype=torch.float32) if return_final_state else None
     a = make_scan_args(x, dt, A, B, C, y=y, final_state=fin, D=D, z=z, dt_bias=dt_bias, initial_states=initial_states,
                        lengths=lengths, dt_softplus=dt_softplus, dt_limit=dt_limit)
     ws = _work("ssd_selective_scan_workspace_size", a, x)  # noqa: F841
-    _call("ssd_selective_scan", a, x.get_device())
+    _call("ssd_selective_scan", _byref(a), x.get_device())
     return (y, fin) if return_final_state else y
 
 
@@ -313,7 +333,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, dt_softplus=False, *, dfinal=None, D=
     for k, t in g.items():
         setattr(a, k, t.data_ptr())
     ws = _work("ssd_selective_scan_bwd_workspace_size", a, x)  # noqa: F841
-    _call("ssd_selective_scan_bwd", a, x.get_device())
+    _call("ssd_selective_scan_bwd", _byref(a), x.get_device())
     return g
 
 
@@ -331,18 +351,18 @@ def selective_scan_step(x, dt, A, B, C, state, dt_softplus=False, *, state_out=N
     bc = (Bb, B.shape[1], B.shape[2])
     pool = (state.shape[0], Dm, bc[2])
     code, dtt = _code(x, "x"), _dt_dtype(x, dt)
-    y = torch.empty(xs, device=x.device, dtype=io) if out is None else out
+    y, py = _output(x, out)
     px, rx = _rows(x, xs, io, dev, "x")
     pdt, rdt = _rows(dt, xs, dtt, dev, "dt")
     pz, rz = _rows(z, xs, io, dev, "z")
     pb, rb = _rows(B, bc, io, dev, "B")
     pc, rc = _rows(C, bc, io, dev, "C")
     ps = _dense(state, pool, f32, dev, "state")
-    a = SsdScanStepArgs(
+    a = _pack_scan_step(
         Bb, Dm, bc[2], bc[1], pool[0], px, pdt, _dense(A, (Dm, bc[2]), f32, dev, "A"), pb, pc,
         _dense(D, (Dm,), f32, dev, "D"), pz, _dense(dt_bias, (Dm,), f32, dev, "dt_bias"), ps,
         ps if state_out is None else _dense(state_out, pool, f32, dev, "state_out"),
-        _dense(slots, (Bb,), torch.int32, dev, "slots"), _dense(y, xs, io, dev, "out"), rx, rdt, rz, rb, rc, code,
+        _dense(slots, (Bb,), torch.int32, dev, "slots"), py, rx, rdt, rz, rb, rc, code,
         _CODES[dtt], 1 if dt_softplus else 0, dt_limit[0], dt_limit[1])
     _call("ssd_selective_scan_step", a, dev)
     return y
@@ -370,10 +390,10 @@ def causal_conv1d_carry(x, w, bias=None, silu=True, *, initial_state=None, lengt
     fp32, W <= 8.  Returns y, or (y, final_state [B,W-1,C] in x's dtype);
     ``lengths`` as in ``selective_scan``."""
     _cuda(x, "causal_conv1d_carry")
-    y = out if out is not None else torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    y = _output(x, out)[0]
     fin = torch.empty((x.shape[0], w.shape[1] - 1, x.shape[2]), device=x.device, dtype=x.dtype) if return_final_state else None
     a = make_conv_args(x, w, bias, y=y, final_state=fin, initial_state=initial_state, lengths=lengths, silu=silu)
-    _call("ssd_causal_conv_carry", a, x.get_device())
+    _call("ssd_causal_conv_carry", _byref(a), x.get_device())
     return (y, fin) if return_final_state else y
 
 
@@ -396,7 +416,7 @@ def causal_conv1d_bwd(x, w, dy, bias=None, silu=True, *, dfinal=None, initial_st
     for k, t in g.items():
         setattr(a, k, t.data_ptr())
     ws = _work("ssd_causal_conv_bwd_workspace_size", a, x)  # noqa: F841
-    _call("ssd_causal_conv_bwd", a, x.get_device())
+    _call("ssd_causal_conv_bwd", _byref(a), x.get_device())
     return g
 
 
@@ -410,13 +430,13 @@ def causal_conv1d_step(x, state, w, bias=None, silu=True, *, state_out=None, slo
     Bb, Cc = xs
     pool = (state.shape[0], W - 1, Cc)
     code = _code(x, "x")
-    y = torch.empty(xs, device=x.device, dtype=io) if out is None else out
+    y, py = _output(x, out)
     px, rx = _rows(x, xs, io, dev, "x")
     ps = _dense(state, pool, io, dev, "state")
-    a = SsdConvStepArgs(
+    a = _pack_conv_step(
         Bb, Cc, W, pool[0], px, rx, _dense(w, (Cc, W), f32, dev, "w"), _dense(bias, (Cc,), f32, dev, "bias"), ps,
         ps if state_out is None else _dense(state_out, pool, io, dev, "state_out"),
-        _dense(slots, (Bb,), torch.int32, dev, "slots"), _dense(y, xs, io, dev, "out"), code, 1 if silu else 0)
+        _dense(slots, (Bb,), torch.int32, dev, "slots"), py, code, 1 if silu else 0)
     _call("ssd_causal_conv_step", a, dev)
     return y
 
@@ -467,7 +487,7 @@ def block_norm(o, r, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5, dty
     if o is not None:
         r_out = r_out if r_out is not None else torch.empty_like(r)
         a.r_out = _dense(r_out, r.shape, r.dtype, dev, "r_out")
-    _call("ssd_block_norm", a, dev)
+    _call("ssd_block_norm", _byref(a), dev)
     return n, (r_out if o is not None else r)
 
 
@@ -491,5 +511,5 @@ def block_norm_bwd(dn, dr_out, o, r_out, w_pre, *, w_post=None, gate=None, scale
     for k, t in g.items():
         setattr(a, "d_o" if k == "do" else k, t.data_ptr())
     ws = _work("ssd_block_norm_bwd_workspace_size", a, dn)  # noqa: F841
-    _call("ssd_block_norm_bwd", a, dev)
+    _call("ssd_block_norm_bwd", _byref(a), dev)
     return g
