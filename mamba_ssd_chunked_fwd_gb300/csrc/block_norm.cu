@@ -9,11 +9,11 @@
 //   dscale = w_post s,  dw_post = scale s,                       s = sum dr gate hat_o
 //
 // About 11 (backward 30) operations per element against 8 to 16 bytes: bound by
-// HBM.  The threads of a row own runs of four elements, K per thread, which they
+// HBM.  The threads of a row own units of eight elements, K per thread, which they
 // copy into slots of their own in shared memory a row ahead, so that the loads of
 // one row run beside the reductions and stores of the one before, need no
-// registers, and every tensor moves once.  Backwards the two column sums and the
-// weights stay in registers over a chunk of rows.
+// registers, and every tensor moves once.  The weights, and backwards the two column
+// sums, stay in registers over the rows that the threads walk.
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -43,151 +43,178 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float (*slot)[32]) {
     }
 }
 
+template <int SIO>
+__device__ __forceinline__ float round_io(float v) {
+    return IoTraits<SIO>::to_f(IoTraits<SIO>::from_f(v));
+}
+
+// Eight elements of a row as four pairs, the unit a thread deals in: one chunk of
+// 16 bytes of a 16-bit type, two of fp32.  n of them exist (VEC: all or none).
+template <int IO>
+struct Eight {
+    static constexpr int kEs = IO == IO_F32 ? 4 : 2, kBytes = 8 * kEs;
+};
 template <int IO, bool VEC>
-__device__ __forceinline__ void unpack_pairs(const Raw4 &r, float2 (&v)[2]) {
-    float f[4];
-    unpack4<IO, VEC>(r, f);
-    v[0] = make_float2(f[0], f[1]);
-    v[1] = make_float2(f[2], f[3]);
+__device__ __forceinline__ void copy8(char *dst, const char *src, int n) {
+    copy_chunk<IO, VEC>(dst, src, n);
+    if (IO == IO_F32) copy_chunk<IO, VEC>(dst + 16, src + 16, n - 4);
+}
+template <int IO>
+__device__ __forceinline__ void read8(const char *src, float2 (&v)[4]) {
+    read_chunk<IO>(src, v);
+    if (IO == IO_F32) read_chunk<IO>(src + 16, v + 2);
 }
 template <int IO, bool VEC>
-__device__ __forceinline__ void store_pairs(void *base, long long i, int nv, const float2 (&v)[2]) {
-    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-    store4_io<IO, VEC>(base, i, nv, f);
+__device__ __forceinline__ void store8(char *dst, int n, const float2 (&v)[4]) {
+    store_chunk<IO, VEC>(dst, n, v);
+    if (IO == IO_F32) store_chunk<IO, VEC>(dst + 16, n - 4, v + 2);
 }
-// Four of a weight vector [D], or ones.
+// Straight from global memory: a weight vector (ones when absent), or a tensor that has no slot.
+template <int IO, bool VEC>
+__device__ __forceinline__ void load8(const void *base, long long i, int n, float2 (&v)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float f[4];
+        unpack4<IO, VEC>(load_raw4<IO, VEC>(base, i + 4 * h, base ? n - 4 * h : 0, n - 4 * h), f);
+        v[2 * h] = make_float2(f[0], f[1]);
+        v[2 * h + 1] = make_float2(f[2], f[3]);
+    }
+}
 template <bool VEC>
-__device__ __forceinline__ void weights(const float *w, int c, int nv, float2 (&v)[2]) {
-    unpack_pairs<IO_F32, VEC>(load_raw4<IO_F32, VEC>(w, c, w && nv > 0, nv), v);
-    if (!w) v[0] = v[1] = dup(1.f);
+__device__ __forceinline__ void weights(const float *w, int c, int n, float2 (&v)[4]) {
+    load8<IO_F32, VEC>(w, c, n, v);
+    if (!w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = dup(1.f);
 }
 // scale w_post
 template <bool VEC>
-__device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, int nv, float2 (&v)[2]) {
-    float2 s[2];
-    weights<VEC>(p.w_post, c, nv, v);
-    weights<VEC>(p.scale, c, nv, s);
-    v[0] = __fmul2_rn(v[0], s[0]);
-    v[1] = __fmul2_rn(v[1], s[1]);
+__device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, int n, float2 (&v)[4]) {
+    float2 s[4];
+    weights<VEC>(p.w_post, c, n, v);
+    weights<VEC>(p.scale, c, n, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], s[j]);
 }
 
-// The slots of a CTA's threads for one row: NI tensors in the block's type, then NS in the stream's.
+// The slots of a CTA's threads for one row, K units each: NI tensors in the
+// block's type, then NS in the stream's; a unit's two chunks lie apart, so that
+// neighbouring threads' chunks are neighbours.
 template <int IO, int SIO, int K, int NI, int NS>
 struct NormSlots {
-    static constexpr int kQi = IO == IO_F32 ? 16 : 8, kQs = SIO == IO_F32 ? 16 : 8;
-    static constexpr int kPerThread = K * (NI * kQi + NS * kQs);
-    // of thread `tid` of n: tensor i's quad k
-    static __device__ __forceinline__ int block(int i, int k, int tid, int n) { return (i * K + k) * kQi * n + tid * kQi; }
-    static __device__ __forceinline__ int stream(int i, int k, int tid, int n) {
-        return NI * K * kQi * n + (i * K + k) * kQs * n + tid * kQs;
-    }
+    static constexpr int kPerThread = K * (NI * Eight<IO>::kBytes + NS * Eight<SIO>::kBytes);
 };
 
-template <int IO, int SIO, int K, bool VEC>
-__global__ void __launch_bounds__(1024)
+template <int IO, int SIO, int K, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT)
 block_norm_kernel(BlockNormParams p, int stages) {
     using S = NormSlots<IO, SIO, K, 2, 1>;  // o, gate; r
     extern __shared__ __align__(16) char ring[];
     __shared__ float red[2][1][32];
-    constexpr int kEi = IO == IO_F32 ? 4 : 2, kEs = SIO == IO_F32 ? 4 : 2;
-    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + tx;
+    constexpr int kEi = Eight<IO>::kEs, kEs = Eight<SIO>::kEs, kBi = Eight<IO>::kBytes, kBs = Eight<SIO>::kBytes;
+    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y;
+    char *mine = ring + (threadIdx.y * blockDim.x + tx) * kBi;                   // + (i K + k) line
+    char *mine_s = ring + 2 * K * kBi * nthr + (threadIdx.y * blockDim.x + tx) * kBs;  // + k line_s
+    const int line = nthr * kBi, line_s = nthr * kBs, stage = nthr * S::kPerThread;
     const float inv_d = 1.f / (float)p.D;
     const long long step = (long long)gridDim.x * blockDim.y;
-    auto copy = [&](long long row, char *slot) {
+    auto copy = [&](long long row, int at) {
         if (row < p.rows) {
-            const long long base = row * p.D + tx * 4, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 4 : 0;
+            const long long base = row * p.D + tx * 8, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 8 : 0;
+            const char *r = static_cast<const char *>(p.r) + base * kEs, *o = static_cast<const char *>(p.o) + base * kEi,
+                       *g = static_cast<const char *>(p.gate) + gbase * kEi;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int nv = min(4, p.D - (tx + tpr * k) * 4), c = tpr * k * 4;
-                copy_quad<SIO, VEC>(slot + S::stream(0, k, tid, nthr), static_cast<const char *>(p.r) + (base + c) * kEs, nv);
-                if (p.o) copy_quad<IO, VEC>(slot + S::block(0, k, tid, nthr), static_cast<const char *>(p.o) + (base + c) * kEi, nv);
-                if (p.gate) copy_quad<IO, VEC>(slot + S::block(1, k, tid, nthr), static_cast<const char *>(p.gate) + (gbase + c) * kEi, nv);
+                const int n = min(8, p.D - (tx + tpr * k) * 8);
+                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, n);
+                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, n);
+                if (p.gate) copy8<IO, VEC>(mine + at + (K + k) * line, g + tpr * k * kBi, n);
             }
         }
         cp_commit();
     };
     long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    char *slot = ring, *next = stages == 2 ? ring + nthr * S::kPerThread : ring;
-    if (stages == 2) copy(row, slot);
+    int at = 0;
+    if (stages == 2) copy(row, 0);
+    float2 wp[K][4], ws[K][4];  // w_pre; scale w_post
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (tx + tpr * k) * 8, n = min(8, p.D - c);
+        weights<VEC>(p.w_pre, c, n, wp[k]);
+        post_weights<VEC>(p, c, n, ws[k]);
+    }
     for (; row < p.rows; row += step) {
         if (stages == 2) {
-            copy(row + step, next);
+            copy(row + step, stage - at);
             cp_wait<1>();
         } else {
-            copy(row, slot);
+            copy(row, 0);
             cp_wait<0>();
         }
-        const long long base = row * p.D + tx * 4;
+        const long long base = row * p.D + tx * 8;
         float inv = 1.f;
         if (p.o && p.w_post) {
             float2 s2 = dup(0.f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {  // zeros past the row's end
-                float2 o[2];
-                read_quad<IO>(slot + S::block(0, k, tid, nthr), o);
-                s2 = __ffma2_rn(o[0], o[0], s2);
-                s2 = __ffma2_rn(o[1], o[1], s2);
+                float2 o[4];
+                read8<IO>(mine + at + k * line, o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(o[j], o[j], s2);
             }
             float ss[1] = {s2.x + s2.y};
             row_sum(ss, red[0]);
             inv = rsqrtf(ss[0] * inv_d + p.eps);
         }
-        float2 s2 = dup(0.f);
+        float2 r[K][4], s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
-            float2 r[2];
-            read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
+            const int n = min(8, p.D - (tx + tpr * k) * 8);
+            read8<SIO>(mine_s + at + k * line_s, r[k]);
             if (p.o) {
-                float2 o[2], ws[2];
-                post_weights<VEC>(p, c, nv, ws);
-                read_quad<IO>(slot + S::block(0, k, tid, nthr), o);
+                float2 o[4];
+                read8<IO>(mine + at + k * line, o);
                 if (p.gate) {
-                    float2 g[2];
-                    read_quad<IO>(slot + S::block(1, k, tid, nthr), g);
-                    ws[0] = __fmul2_rn(ws[0], g[0]);
-                    ws[1] = __fmul2_rn(ws[1], g[1]);
+                    float2 g[4];
+                    read8<IO>(mine + at + (K + k) * line, g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = __fmul2_rn(o[j], g[j]);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) r[j] = __ffma2_rn(ws[j], __fmul2_rn(o[j], dup(inv)), r[j]);
-                write_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);  // rounded as it is stored
-                if (nv > 0) store_pairs<SIO, VEC>(p.r_out, base + tpr * k * 4, nv, r);
-                read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = __ffma2_rn(ws[k][j], __fmul2_rn(o[j], dup(inv)), r[k][j]);
+                    r[k][j] = make_float2(round_io<SIO>(v.x), round_io<SIO>(v.y));  // as it is stored
+                }
+                store8<SIO, VEC>(static_cast<char *>(p.r_out) + (base + tpr * k * 8) * kEs, n, r[k]);
             }
-            s2 = __ffma2_rn(r[0], r[0], s2);
-            s2 = __ffma2_rn(r[1], r[1], s2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(r[k][j], r[k][j], s2);
         }
         float ss[1] = {s2.x + s2.y};
         row_sum(ss, red[1]);
         const float2 inv2 = dup(rsqrtf(ss[0] * inv_d + p.eps));
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
-            float2 r[2], wp[2];
-            weights<VEC>(p.w_pre, c, nv, wp);
-            read_quad<SIO>(slot + S::stream(0, k, tid, nthr), r);
-            r[0] = __fmul2_rn(__fmul2_rn(r[0], inv2), wp[0]);
-            r[1] = __fmul2_rn(__fmul2_rn(r[1], inv2), wp[1]);
-            if (nv > 0) store_pairs<IO, VEC>(p.n, base + tpr * k * 4, nv, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[k][j] = __fmul2_rn(__fmul2_rn(r[k][j], inv2), wp[k][j]);
+            store8<IO, VEC>(static_cast<char *>(p.n) + (base + tpr * k * 8) * kEi, min(8, p.D - (tx + tpr * k) * 8), r[k]);
         }
         if (!(p.o && p.w_post) && blockDim.x > 32) __syncthreads();  // one reduction per row only: its slot is free again
-        char *t = slot;
-        slot = next;
-        next = t;
+        if (stages == 2) at = stage - at;
     }
 }
 
-// MAXT: the threads a row may take (fewer leave each more registers).  whole: the
+// MAXT: the threads a row may take (fewer leave each more registers).  WHOLE: the
 // slots hold dr_out and the gate too; rows too wide for that load them where they are used.
-template <int IO, int SIO, int K, bool VEC, int MAXT>
+template <int IO, int SIO, int K, bool VEC, int MAXT, bool WHOLE>
 __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1)
-block_norm_bwd_kernel(BlockNormParams p, int stages, int whole) {
-    using S = NormSlots<IO, SIO, K, 3, 2>;   // o, dn, gate; r', dr_out
-    using T = NormSlots<IO, SIO, K, 2, 1>;   // o, dn; r'
+block_norm_bwd_kernel(BlockNormParams p, int stages) {
+    constexpr int NI = WHOLE ? 3 : 2;
+    using S = NormSlots<IO, SIO, K, NI, WHOLE ? 2 : 1>;  // o, dn, gate; r', dr_out
     extern __shared__ __align__(16) char ring[];
     __shared__ float red[2][3][32];
-    constexpr int kEi = IO == IO_F32 ? 4 : 2, kEs = SIO == IO_F32 ? 4 : 2;
-    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + tx;
+    constexpr int kEi = Eight<IO>::kEs, kEs = Eight<SIO>::kEs, kBi = Eight<IO>::kBytes, kBs = Eight<SIO>::kBytes;
+    const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y;
     const long long chunk = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (chunk >= p.chunks) return;  // blockDim.y > 1 only for rows of one warp
     const bool seq_gate = p.gate && p.rows_per_gate > 1;
@@ -200,97 +227,113 @@ block_norm_bwd_kernel(BlockNormParams p, int stages, int whole) {
         r0 = chunk * p.chunk_rows;
         r1 = min(p.rows, r0 + p.chunk_rows);
     }
-    auto off_o = [&](int k) { return whole ? S::block(0, k, tid, nthr) : T::block(0, k, tid, nthr); };
-    auto off_n = [&](int k) { return whole ? S::block(1, k, tid, nthr) : T::block(1, k, tid, nthr); };
-    auto off_r = [&](int k) { return whole ? S::stream(0, k, tid, nthr) : T::stream(0, k, tid, nthr); };
-    auto copy = [&](long long row, char *slot) {
+    char *mine = ring + (threadIdx.y * blockDim.x + tx) * kBi;                          // + (i K + k) line
+    char *mine_s = ring + NI * K * kBi * nthr + (threadIdx.y * blockDim.x + tx) * kBs;  // + (i K + k) line_s
+    const int line = nthr * kBi, line_s = nthr * kBs, stage = nthr * S::kPerThread;
+    auto copy = [&](long long row, int at) {
         if (row < r1) {
-            const long long base = row * p.D + tx * 4, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 4 : 0;
+            const long long base = row * p.D + tx * 8, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 8 : 0;
+            const char *r = static_cast<const char *>(p.r_out) + base * kEs, *n = static_cast<const char *>(p.dn) + base * kEi,
+                       *o = static_cast<const char *>(p.o) + base * kEi, *d = static_cast<const char *>(p.dr_out) + base * kEs,
+                       *g = static_cast<const char *>(p.gate) + gbase * kEi;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int nv = min(4, p.D - (tx + tpr * k) * 4), c = tpr * k * 4;
-                copy_quad<SIO, VEC>(slot + off_r(k), static_cast<const char *>(p.r_out) + (base + c) * kEs, nv);
-                copy_quad<IO, VEC>(slot + off_n(k), static_cast<const char *>(p.dn) + (base + c) * kEi, nv);
-                if (p.o) copy_quad<IO, VEC>(slot + off_o(k), static_cast<const char *>(p.o) + (base + c) * kEi, nv);
-                if (!whole) continue;
-                if (p.dr_out) copy_quad<SIO, VEC>(slot + S::stream(1, k, tid, nthr), static_cast<const char *>(p.dr_out) + (base + c) * kEs, nv);
-                if (p.gate) copy_quad<IO, VEC>(slot + S::block(2, k, tid, nthr), static_cast<const char *>(p.gate) + (gbase + c) * kEi, nv);
+                const int nv = min(8, p.D - (tx + tpr * k) * 8);
+                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, nv);
+                copy8<IO, VEC>(mine + at + (K + k) * line, n + tpr * k * kBi, nv);
+                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, nv);
+                if (WHOLE && p.dr_out) copy8<SIO, VEC>(mine_s + at + (K + k) * line_s, d + tpr * k * kBs, nv);
+                if (WHOLE && p.gate) copy8<IO, VEC>(mine + at + (2 * K + k) * line, g + tpr * k * kBi, nv);
             }
         }
         cp_commit();
     };
-    char *slot = ring, *next = stages == 2 ? ring + nthr * (whole ? S::kPerThread : T::kPerThread) : ring;
-    if (stages == 2) copy(r0, slot);
-    float2 acc1[K][2], acc2[K][2], wp[K][2], ws[K][2];
+    int at = 0;
+    if (stages == 2) copy(r0, 0);
+    float2 acc1[K][4], acc2[K][4], wp[K][4], ws[K][4];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
-        acc1[k][0] = acc1[k][1] = acc2[k][0] = acc2[k][1] = dup(0.f);
-        weights<VEC>(p.w_pre, c, nv, wp[k]);
-        post_weights<VEC>(p, c, nv, ws[k]);
+        const int c = (tx + tpr * k) * 8, n = min(8, p.D - c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc1[k][j] = acc2[k][j] = dup(0.f);
+        weights<VEC>(p.w_pre, c, n, wp[k]);
+        post_weights<VEC>(p, c, n, ws[k]);
     }
     const float inv_d = 1.f / (float)p.D;
     for (long long row = r0; row < r1; ++row) {
         if (stages == 2) {
-            copy(row + 1, next);
+            copy(row + 1, stage - at);
             cp_wait<1>();
         } else {
-            copy(row, slot);
+            copy(row, 0);
             cp_wait<0>();
         }
-        const long long base = row * p.D + tx * 4;
+        const long long base = row * p.D + tx * 8;
         float2 s0 = dup(0.f), s1 = dup(0.f), s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {  // zeros past the row's end
-            float2 r[2], n[2], o[2];
-            read_quad<SIO>(slot + off_r(k), r);
-            read_quad<IO>(slot + off_n(k), n);
-            if (p.o) read_quad<IO>(slot + off_o(k), o);
-            else o[0] = o[1] = dup(0.f);
+            float2 r[4], n[4];
+            read8<SIO>(mine_s + at + k * line_s, r);
+            read8<IO>(mine + at + (K + k) * line, n);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 s0 = __ffma2_rn(r[j], r[j], s0);
                 s1 = __ffma2_rn(__fmul2_rn(n[j], wp[k][j]), r[j], s1);
-                s2 = __ffma2_rn(o[j], o[j], s2);
+            }
+            if (p.o) {
+                read8<IO>(mine + at + k * line, n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(n[j], n[j], s2);
             }
         }
         float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};  // |r'|^2, dn w_pre . r', |o|^2
         row_sum(s, red[0]);
         const float inv2 = rsqrtf(s[0] * inv_d + p.eps), m2 = s[1] * inv_d * inv2 * inv2;
         const float inv = p.w_post ? rsqrtf(s[2] * inv_d + p.eps) : 1.f;
-        float2 t2 = dup(0.f), u[K][2];  // u . o
+        float2 t2 = dup(0.f), u[K][4];  // u . o
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (tx + tpr * k) * 4, nv = min(4, p.D - c);
-            const long long at = base + tpr * k * 4;
-            float2 dr[2], r[2], n[2];
-            read_quad<SIO>(slot + off_r(k), r);
-            read_quad<IO>(slot + off_n(k), n);
-            if (!p.dr_out) dr[0] = dr[1] = dup(0.f);
-            else if (whole) read_quad<SIO>(slot + S::stream(1, k, tid, nthr), dr);
-            else unpack_pairs<SIO, VEC>(load_raw4<SIO, VEC>(p.dr_out, at, nv, nv), dr);
+            const int c = (tx + tpr * k) * 8, nv = min(8, p.D - c);
+            const long long to = base + tpr * k * 8;
+            float2 dr[4], r[4], n[4];
+            read8<SIO>(mine_s + at + k * line_s, r);
+            read8<IO>(mine + at + (K + k) * line, n);
+            if (WHOLE && p.dr_out) read8<SIO>(mine_s + at + (K + k) * line_s, dr);
+            else load8<SIO, VEC>(p.dr_out, to, nv, dr);  // zeros when absent
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // dr = (v - r' inv2^2 mean(v r')) inv2 + dr_out
+            for (int j = 0; j < 4; ++j) {  // dr = (v - r' inv2^2 mean(v r')) inv2 + dr_out
                 const float2 v = __ffma2_rn(r[j], dup(-m2), __fmul2_rn(n[j], wp[k][j]));
                 dr[j] = __ffma2_rn(v, dup(inv2), dr[j]);
                 acc2[k][j] = __ffma2_rn(n[j], __fmul2_rn(r[j], dup(inv2)), acc2[k][j]);
             }
-            if (nv > 0) store_pairs<SIO, VEC>(p.dr, at, nv, dr);
+            store8<SIO, VEC>(static_cast<char *>(p.dr) + to * kEs, nv, dr);
             if (!p.o) continue;
-            float2 o[2], g[2], dg[2];
-            read_quad<IO>(slot + off_o(k), o);
-            if (!p.gate) g[0] = g[1] = dup(1.f);
-            else if (whole) read_quad<IO>(slot + S::block(2, k, tid, nthr), g);
-            else unpack_pairs<IO, VEC>(load_raw4<IO, VEC>(p.gate, row / p.rows_per_gate * p.D + c, nv, nv), g);
+            float2 o[4];
+            read8<IO>(mine + at + k * line, o);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 dh = __fmul2_rn(dr[j], __fmul2_rn(o[j], dup(inv)));  // dr hat_o
-                dg[j] = __fmul2_rn(dh, ws[k][j]);
-                u[k][j] = __fmul2_rn(__fmul2_rn(g[j], dr[j]), ws[k][j]);
-                t2 = __ffma2_rn(u[k][j], o[j], t2);
-                acc1[k][j] = seq_gate ? __fadd2_rn(acc1[k][j], dh) : __ffma2_rn(dh, g[j], acc1[k][j]);
+            for (int j = 0; j < 4; ++j) {
+                r[j] = __fmul2_rn(dr[j], __fmul2_rn(o[j], dup(inv)));  // dr hat_o
+                u[k][j] = __fmul2_rn(dr[j], ws[k][j]);
             }
-            if (p.gate && !seq_gate && nv > 0) store_pairs<IO, VEC>(p.dgate, at, nv, dg);
+            if (p.gate) {
+                if (!seq_gate) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(r[j], ws[k][j]);
+                    store8<IO, VEC>(static_cast<char *>(p.dgate) + to * kEi, nv, n);
+                }
+                if (WHOLE) read8<IO>(mine + at + (2 * K + k) * line, n);
+                else load8<IO, VEC>(p.gate, row / p.rows_per_gate * p.D + c, nv, n);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[k][j] = __fmul2_rn(u[k][j], n[j]);
+                    if (!seq_gate) r[j] = __fmul2_rn(r[j], n[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t2 = __ffma2_rn(u[k][j], o[j], t2);
+                acc1[k][j] = __fadd2_rn(acc1[k][j], r[j]);
+            }
         }
         if (p.o) {
             float t[1] = {t2.x + t2.y};
@@ -298,26 +341,23 @@ block_norm_bwd_kernel(BlockNormParams p, int stages, int whole) {
             const float m = p.w_post ? t[0] * inv_d * inv * inv : 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int nv = min(4, p.D - (tx + tpr * k) * 4);
-                float2 o[2];
-                read_quad<IO>(slot + off_o(k), o);
+                float2 o[4];
+                read8<IO>(mine + at + k * line, o);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[k][j]), dup(inv));
-                if (nv > 0) store_pairs<IO, VEC>(p.d_o, base + tpr * k * 4, nv, o);
+                for (int j = 0; j < 4; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[k][j]), dup(inv));
+                store8<IO, VEC>(static_cast<char *>(p.d_o) + (base + tpr * k * 8) * kEi, min(8, p.D - (tx + tpr * k) * 8), o);
             }
         } else if (blockDim.x > 32) {
             __syncthreads();  // the slot of the sums is free again
         }
-        char *t = slot;
-        slot = next;
-        next = t;
+        if (stages == 2) at = stage - at;
     }
     float *part = p.part + chunk * 2 * p.D;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = (tx + tpr * k) * 4 + j;
+        for (int j = 0; j < 8; ++j) {
+            const int c = (tx + tpr * k) * 8 + j;
             if (c < p.D) {
                 part[c] = j & 1 ? acc1[k][j / 2].y : acc1[k][j / 2].x;
                 part[p.D + c] = j & 1 ? acc2[k][j / 2].y : acc2[k][j / 2].x;
@@ -366,29 +406,32 @@ block_norm_sum_kernel(BlockNormParams p) {
     if (p.dscale) p.dscale[c] = wpost * s1;
 }
 
-// Threads of a row and rows of a CTA for K runs of four elements per thread.
+// Threads of a row and rows of a CTA for K units of eight elements per thread.
 dim3 row_block(int D, int K) {
-    const int tpr = ((D + 4 * K - 1) / (4 * K) + 31) / 32 * 32;
+    const int tpr = ((D + 8 * K - 1) / (8 * K) + 31) / 32 * 32;
     return dim3(tpr, tpr == 32 ? 4 : 1);
 }
 
-// Runs of four elements per thread: the fewest that a warp's row takes, up to 4 (backwards 8 for rows
-// past 8192, whose registers would not allow more threads); wider rows take more warps.
-int norm_k(int D, bool backward) { return D <= 128 ? 1 : D <= 256 ? 2 : backward && D > 8192 ? 8 : 4; }
+// Units per thread: two, but one for rows that a warp takes so, and backwards four for rows past 8192,
+// whose registers would not allow more threads; wider rows take more warps.
+int norm_k(int D, bool backward) { return D <= 256 ? 1 : backward && D > 8192 ? 4 : 2; }
 
 constexpr int kNormSmem = 227 * 1024 - 1024;  // the most a CTA may hold, less the sums
 
-bool norm_vec(const BlockNormParams &p, int io, int sio) {
-    auto ok = [](const void *q, int t) { return reinterpret_cast<uintptr_t>(q) % (t == IO_F32 ? 16 : 8) == 0; };
-    return p.D % 4 == 0 && ok(p.o, io) && ok(p.r, sio) && ok(p.gate, io) && ok(p.n, io) && ok(p.r_out, sio) &&
-           ok(p.dn, io) && ok(p.dr_out, sio) && ok(p.d_o, io) && ok(p.dr, sio) && ok(p.dgate, io) &&
-           ok(p.w_post, IO_F32) && ok(p.w_pre, IO_F32) && ok(p.scale, IO_F32);
+// Whether every tensor moves in whole, aligned units (absent ones do).
+bool norm_vec(const BlockNormParams &p) {
+    bool ok = p.D % 8 == 0;
+    for (const void *q : {p.o, p.r, p.gate, (const void *)p.n, (const void *)p.r_out, p.dn, p.dr_out, (const void *)p.d_o,
+                          (const void *)p.dr, (const void *)p.dgate, (const void *)p.w_post, (const void *)p.w_pre,
+                          (const void *)p.scale})
+        ok = ok && chunk_aligned(q);
+    return ok;
 }
 
-template <int IO, int SIO, int K>
+template <int IO, int SIO, int K, int MAXT>
 cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
-    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_kernel<IO, SIO, K, true> : block_norm_kernel<IO, SIO, K, false>;
+    auto *kernel = norm_vec(p) ? block_norm_kernel<IO, SIO, K, true, MAXT> : block_norm_kernel<IO, SIO, K, false, MAXT>;
     const int row = (int)(block.x * block.y) * NormSlots<IO, SIO, K, 2, 1>::kPerThread;
     const int stages = 2 * row <= kNormSmem ? 2 : 1, bytes = stages * row;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -407,23 +450,20 @@ cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
 
 template <int IO, int SIO>
 cudaError_t launch_norm_io(const BlockNormParams &p, cudaStream_t s) {
-    switch (norm_k(p.D, false)) {
-        case 1: return launch_norm_as<IO, SIO, 1>(p, s);
-        case 2: return launch_norm_as<IO, SIO, 2>(p, s);
-        default: return launch_norm_as<IO, SIO, 4>(p, s);
-    }
+    if (norm_k(p.D, false) == 1) return launch_norm_as<IO, SIO, 1, 128>(p, s);
+    return p.D <= 8192 ? launch_norm_as<IO, SIO, 2, 512>(p, s) : launch_norm_as<IO, SIO, 2, 1024>(p, s);
 }
 
-template <int IO, int SIO, int K, int MAXT>
+template <int IO, int SIO, int K, int MAXT, bool WHOLE>
 cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
-    auto *kernel = norm_vec(p, IO, SIO) ? block_norm_bwd_kernel<IO, SIO, K, true, MAXT> : block_norm_bwd_kernel<IO, SIO, K, false, MAXT>;
-    const int n = block.x * block.y, row = n * NormSlots<IO, SIO, K, 3, 2>::kPerThread;
-    const int whole = row <= kNormSmem, mine = whole ? row : n * NormSlots<IO, SIO, K, 2, 1>::kPerThread;
-    const int stages = 2 * mine <= kNormSmem ? 2 : 1, bytes = stages * mine;
+    auto *kernel = norm_vec(p) ? block_norm_bwd_kernel<IO, SIO, K, true, MAXT, WHOLE>
+                               : block_norm_bwd_kernel<IO, SIO, K, false, MAXT, WHOLE>;
+    const int row = block.x * block.y * NormSlots<IO, SIO, K, WHOLE ? 3 : 2, WHOLE ? 2 : 1>::kPerThread;
+    const int stages = 2 * row <= kNormSmem ? 2 : 1, bytes = stages * row;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages, whole);
+    kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     block_norm_sum_kernel<IO><<<(p.D + 31) / 32, dim3(32, 32), 0, s>>>(p);
     return cudaGetLastError();
@@ -432,10 +472,10 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
 template <int IO, int SIO>
 cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
     switch (norm_k(p.D, true)) {
-        case 1: return launch_norm_bwd_as<IO, SIO, 1, 128>(p, s);
-        case 2: return launch_norm_bwd_as<IO, SIO, 2, 128>(p, s);
-        case 4: return p.D <= 2048 ? launch_norm_bwd_as<IO, SIO, 4, 128>(p, s) : launch_norm_bwd_as<IO, SIO, 4, 512>(p, s);
-        default: return launch_norm_bwd_as<IO, SIO, 8, 512>(p, s);
+        case 1: return launch_norm_bwd_as<IO, SIO, 1, 128, true>(p, s);
+        case 2: return p.D <= 2048 ? launch_norm_bwd_as<IO, SIO, 2, 128, true>(p, s) : launch_norm_bwd_as<IO, SIO, 2, 512, true>(p, s);
+        // 512 threads' whole slots: 160 KB of 16-bit tensors, too much with fp32 ones
+        default: return launch_norm_bwd_as<IO, SIO, 4, 512, IO != IO_F32 && SIO != IO_F32>(p, s);
     }
 }
 
