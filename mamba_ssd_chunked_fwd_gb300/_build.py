@@ -1,7 +1,9 @@
-"""Build the CUDA library ``libssd_gb300.so`` in-tree with nvcc (sm_103a).
+"""Build the CUDA library ``libssd_gb300.so`` in-tree with nvcc (sm_103a), and
+the Python extension ``_ssd_binding.so`` with g++.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then one ``nvcc
--shared`` link.  Outputs go to ``_build/`` beside this file (git-ignored).
+-shared`` link; ``csrc/binding.cpp`` compiles beside them against torch's
+headers.  Outputs go to ``_build/`` beside this file (git-ignored).
 """
 from __future__ import annotations
 
@@ -10,12 +12,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libssd_gb300.so")
+BINDING = os.path.join(BUILD, "_ssd_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -35,14 +40,30 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]
+        BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_binding():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", f"-I{os.path.join(root, 'include')}",
+           f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(os.path.dirname(_nvcc()), '..', 'include')}",
+           BINDING_SRC, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +84,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
