@@ -64,23 +64,27 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
     return check_limit(a->dt_min, a->dt_max);
 }
 
-// The cut of the sequences into n segments.  A CTA of a walk advances a token in
-// about 0.1 us whether it has its SM alone or shares it with another (0.17 us for
-// two), so a walk of L tokens by few CTAs is cut until there is a CTA per SM.  The
-// cut costs a first walk (each segment's state from zero; backwards another
-// for the adjoint, too) and a fold of n dependent steps.  Units: tokens of the
-// forward's walk; the factors are the walks' measured times beside it, a
-// fold step is 6 and a launch 30.
+// The cut of the sequences into n segments.  A CTA of the forward's walk advances a
+// token in about 0.096 us alone on its SM, two that share one in 0.165 us, so a walk
+// by few CTAs is cut until there are CTAs for the SMs.  The cut costs a first walk
+// (each segment's state from zero, 0.65 of the forward's time; backwards another for
+// the adjoint, too), a fold over the segments, whose states move four times, and
+// two launches.  Unit: the token of a CTA alone; measured from 128 to 16384 tokens,
+// the choice is within 5% of the best of 1 to 128 segments.
 void choose_segments(ssd::ScanParams &p, bool backward) {
     const int lanes = ssd::scan_lanes(p.N);
     const int dc = 4 * (32 / lanes) * 4;
-    const double sms = ssd::scan_sm_count();
-    const double ctas = (double)p.B * p.G * ((p.D / p.G + dc - 1) / dc);
-    auto waves = [&](double k) { return k <= sms ? 1. : k <= 2 * sms ? 2. : k / sms; };
-    auto cost = [&](long long n) {
-        const double len = (double)(((p.L + n - 1) / n + 31) / 32 * 32), w = waves(ctas * n), w1 = waves(ctas * (n - 1));
-        if (!backward) return w * len + (n > 1 ? 0.7 * w1 * len + 6. * n + 60. : 0.);
-        return 0.8 * w * len + 1.5 * waves(2 * ctas * n) * len + (n > 1 ? 1.5 * w1 * len + 12. * n + 120. : 0.);
+    const double sms = ssd::scan_sm_count(), pair = 1.72;
+    const double ctas = (double)p.B * p.G * ((p.D / p.G + dc - 1) / dc), state = (double)p.B * p.D * p.N;
+    auto waves = [&](double k) {
+        const double full = floor(k / (2 * sms)), rest = k - full * 2 * sms;
+        return full * pair + (rest == 0. ? 0. : rest <= sms ? 1. : pair);
+    };
+    auto cost = [&](long long m) {
+        const long long len = ((p.L + m - 1) / m + 31) / 32 * 32, n = (p.L + len - 1) / len;
+        const double walk = waves(ctas * n), first = waves(ctas * (n - 1));
+        const double cut = n > 1 ? 0.65 * first * len + 1.5 * n + 2.5e-5 * state * n + 90. : 0.;
+        return backward ? 0.8 * walk * len + 1.7 * waves(2 * ctas * n) * len + 2. * cut : walk * len + cut;
     };
     long long best = 1;
     for (long long n = 2; n <= 1024 && (p.L + n - 1) / n >= 32; n = n < 8 ? n + 1 : n + n / 4)

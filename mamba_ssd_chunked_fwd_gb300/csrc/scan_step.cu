@@ -135,37 +135,66 @@ cudaError_t launch_step_io(const ScanStepParams &p, cudaStream_t s) {
     }
 }
 
-// One thread per channel; the W-1 state rows of a sequence are dense, so a
-// warp's accesses are consecutive.
-template <int IO>
-__global__ void __launch_bounds__(256)
+// Four channels per thread; the W-1 state rows of a sequence are dense, so a
+// warp's accesses are consecutive.  A row's taps come in one load when W is 4.
+template <int IO, bool VEC>
+__global__ void __launch_bounds__(128)
 conv_step_kernel(ConvStepParams p) {
-    const int b = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+    const int b = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
     if (c >= p.C) return;
+    const int nv = min(4, p.C - c), W1 = p.W - 1;
     const long long slot = p.slots ? __ldg(p.slots + b) : b;
+    const long long out = (long long)b * p.C + c;
     if (slot < 0 || slot >= p.nslots) {
-        st_io<IO>(p.y, (size_t)b * p.C + c, 0.f);
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        store4_io<IO, VEC>(p.y, out, nv, zero);
         return;
     }
-    using T = typename IoTraits<IO>::T;
-    const long long s0 = slot * (p.W - 1) * p.C + c;
-    const T *in = static_cast<const T *>(p.state) + s0;
-    T *out = static_cast<T *>(p.state_out) + s0;
-    T v[8];
+    const long long s0 = slot * W1 * p.C + c;
+    Raw4 r[8];
+    float w[4][8];
 #pragma unroll
-    for (int k = 0; k < 7; ++k)
-        if (k < p.W - 1) v[k] = in[(long long)k * p.C];
-    const T x = static_cast<const T *>(p.x)[b * p.x_row + c];
-    float acc = p.bias ? __ldg(p.bias + c) : 0.f;
+    for (int k = 0; k < 7; ++k) r[k] = load_raw4<IO, VEC, false>(p.state, s0 + (long long)k * p.C, k < W1, nv);
+    const Raw4 rx = load_raw4<IO, VEC>(p.x, b * p.x_row + c, 1, nv);
 #pragma unroll
-    for (int k = 0; k < 7; ++k)
-        if (k < p.W - 1) {
-            acc = fmaf(__ldg(p.w + (long long)c * p.W + k), IoTraits<IO>::to_f(v[k]), acc);
-            if (k > 0) out[(long long)(k - 1) * p.C] = v[k];
+    for (int j = 0; j < 4; ++j) {
+        const long long at = (long long)(c + j) * p.W;
+        if (VEC && p.W == 4) {
+            const Raw4 t = load_raw4<IO_F32, true>(p.w, at, 1, 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[j][k] = k < 4 ? __uint_as_float(t.w[k & 3]) : 0.f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[j][k] = load_one<IO_F32>(p.w, at + k, k < p.W && j < nv);
         }
-    acc = fmaf(__ldg(p.w + (long long)c * p.W + p.W - 1), IoTraits<IO>::to_f(x), acc);
-    if (p.W > 1) out[(long long)(p.W - 2) * p.C] = x;
-    st_io<IO>(p.y, (size_t)b * p.C + c, p.silu ? silu_fast(acc) : acc);
+    }
+    float acc[4], v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = load_one<IO_F32>(p.bias, c + j, p.bias && j < nv);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // the W entries in order: the state's, then x
+        if (k < W1) unpack4<IO, VEC>(r[k < 7 ? k : 0], v);
+        else unpack4<IO, VEC>(rx, v);
+        if (k < p.W) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = fmaf(w[j][k], v[j], acc[j]);
+            if (k > 0) store4_io<IO, VEC>(p.state_out, s0 + (long long)(k - 1) * p.C, nv, v);
+        }
+    }
+    if (p.silu) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = silu_fast(acc[j]);
+    }
+    store4_io<IO, VEC>(p.y, out, nv, acc);
+}
+
+template <int IO>
+cudaError_t launch_conv_step_io(const ConvStepParams &p, cudaStream_t s) {
+    const bool vec = p.C % 4 == 0 && p.x_row % 4 == 0 && vec4_aligned(p.x, IO) && vec4_aligned(p.state, IO) &&
+                     vec4_aligned(p.state_out, IO) && vec4_aligned(p.y, IO) && vec4_aligned(p.w, IO_F32);
+    auto *kernel = vec ? conv_step_kernel<IO, true> : conv_step_kernel<IO, false>;
+    kernel<<<dim3((p.C + 511) / 512, p.B), 128, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -180,14 +209,12 @@ cudaError_t launch_scan_step(const ScanStepParams &p, int io, cudaStream_t s) {
 }
 
 cudaError_t launch_conv_step(const ConvStepParams &p, int io, cudaStream_t s) {
-    const dim3 grid((p.C + 255) / 256, p.B);
     switch (io) {
-        case IO_F32: conv_step_kernel<IO_F32><<<grid, 256, 0, s>>>(p); break;
-        case IO_F16: conv_step_kernel<IO_F16><<<grid, 256, 0, s>>>(p); break;
-        case IO_BF16: conv_step_kernel<IO_BF16><<<grid, 256, 0, s>>>(p); break;
+        case IO_F32: return launch_conv_step_io<IO_F32>(p, s);
+        case IO_F16: return launch_conv_step_io<IO_F16>(p, s);
+        case IO_BF16: return launch_conv_step_io<IO_BF16>(p, s);
         default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace ssd

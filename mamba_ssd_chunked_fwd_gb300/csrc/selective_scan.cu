@@ -452,39 +452,40 @@ scan_walk_kernel(ScanParams p) {
 }
 
 // The state entering every segment, in place: slot s + 1 holds segment s's own
-// state; S(s+1) = exp(A sum_s) S(s) + own(s), in order.
-__global__ void __launch_bounds__(256)
+// state; S(s+1) = exp(A sum_s) S(s) + own(s), in order.  ADJ: the same for the
+// adjoint from the last segment down, slot s holding the adjoint after segment s.
+// Eight segments' values are loaded together: the order of the sums is a chain of
+// multiply-adds, not of memory latencies.
+template <bool ADJ>
+__global__ void __launch_bounds__(128)
 scan_fold_kernel(ScanParams p) {
+    constexpr int kStep = 8;
     const long long dn = (long long)p.D * p.N;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     if (i >= dn) return;
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, n = p.nseg - 2;  // sums of n segments on top of the first slot
     const float a2 = __ldg(p.A + i) * kLog2e;
-    const long long c = i / p.N;
-    float *st = p.seg_states + (long long)b * p.nseg * dn + i;
-    const float *sm = p.seg_sum + (long long)b * p.nseg * p.D + c;
-    float s = st[dn];
-    for (int k = 1; k < p.nseg - 1; ++k) {
-        s = fmaf(ex2(a2 * sm[(long long)k * p.D]), s, st[(k + 1) * dn]);
-        st[(k + 1) * dn] = s;
-    }
-}
-
-// The same for the adjoint, from the last segment down: slot s holds the adjoint after segment s.
-__global__ void __launch_bounds__(256)
-scan_fold_adj_kernel(ScanParams p) {
-    const long long dn = (long long)p.D * p.N;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= dn) return;
-    const int b = blockIdx.y;
-    const float a2 = __ldg(p.A + i) * kLog2e;
-    const long long c = i / p.N;
-    float *st = p.adj + (long long)b * p.nseg * dn + i;
-    const float *sm = p.seg_sum + (long long)b * p.nseg * p.D + c;
-    float s = st[(p.nseg - 2) * dn];
-    for (int k = p.nseg - 2; k > 0; --k) {
-        s = fmaf(ex2(a2 * sm[(long long)k * p.D]), s, st[(k - 1) * dn]);
-        st[(k - 1) * dn] = s;
+    float *st = (ADJ ? p.adj : p.seg_states) + (long long)b * p.nseg * dn + i;
+    const float *sm = p.seg_sum + (long long)b * p.nseg * p.D + i / p.N;
+    float s = st[(ADJ ? n : 1) * dn];
+    for (int k0 = 0; k0 < n; k0 += kStep) {
+        float own[kStep], sum[kStep];
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+            const int k = ADJ ? n - (k0 + j) : k0 + j + 1;  // the segment passed through
+            if (k0 + j < n) {
+                own[j] = st[(ADJ ? k - 1 : k + 1) * dn];
+                sum[j] = __ldg(sm + (long long)k * p.D);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+            const int k = ADJ ? n - (k0 + j) : k0 + j + 1;
+            if (k0 + j < n) {
+                s = fmaf(ex2(a2 * sum[j]), s, own[j]);
+                st[(ADJ ? k - 1 : k + 1) * dn] = s;
+            }
+        }
     }
 }
 
@@ -539,7 +540,7 @@ cudaError_t segment_states(const ScanParams &p, int io, cudaStream_t s) {
     cudaError_t e = launch_walk<WALK_SEG>(p, io, s);
     if (e != cudaSuccess || p.nseg == 2) return e;
     const long long dn = (long long)p.D * p.N;
-    scan_fold_kernel<<<dim3((unsigned)((dn + 255) / 256), p.B), 256, 0, s>>>(p);
+    scan_fold_kernel<false><<<dim3((unsigned)((dn + 127) / 128), p.B), 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -578,7 +579,7 @@ cudaError_t launch_scan_adjoint(const ScanParams &p, int io, cudaStream_t s) {
     cudaError_t e = launch_walk<WALK_ADJ>(p, io, s);
     if (e != cudaSuccess || p.nseg == 2) return e;
     const long long dn = (long long)p.D * p.N;
-    scan_fold_adj_kernel<<<dim3((unsigned)((dn + 255) / 256), p.B), 256, 0, s>>>(p);
+    scan_fold_kernel<true><<<dim3((unsigned)((dn + 127) / 128), p.B), 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -103,9 +103,10 @@ scan_bwd_kernel(ScanParams p) {
     const long long bseg = (long long)b * p.nseg + seg;
 
     // Walk warps hold eight tokens' states and need the registers the side warps
-    // do not: 160 and 96 of the 128 a thread is launched with.
+    // do not: 144 and 112 of the 128 a thread is launched with (152 and 104, 160 and 96
+    // measured 1% and 3% slower).
     if (warp < kBw) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 2, n0 = ln * 4;
         float2 a2[2][2], q[2][2], da[2][2];
         const float *start = seg < p.nseg - 1 ? p.adj + bseg * p.D * p.N
@@ -136,6 +137,7 @@ scan_bwd_kernel(ScanParams p) {
                 h[j][1] = make_float2(v[2], v[3]);
             }
         };
+        const int again = p.L >> 31;
         float2 hn[2][2];
         if (nt > 0) load_state((ntok - 1) / kCkpt * kCkpt, hn);
         __syncthreads();  // the last tile staged
@@ -170,7 +172,10 @@ scan_bwd_kernel(ScanParams p) {
                 // stored: the stores may alias them, as far as the compiler knows.
                 float2 dn, wn, gn;
                 float4 bn, cn;
-                auto load_token = [&](int t) {
+                // `again` is 0, which the compiler cannot know: the values read above are read
+                // anew, since kept from there they would take 64 more registers.
+                auto load_token = [&](int tok) {
+                    const int t = tok + again;
                     dn = *reinterpret_cast<const float2 *>(sd + t * kDc);
                     wn = *reinterpret_cast<const float2 *>(sw + t * kDc);
                     gn = *reinterpret_cast<const float2 *>(sg + t * kDc);
@@ -257,7 +262,7 @@ scan_bwd_kernel(ScanParams p) {
     }
 
     // ---- side warps
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     const int ta = threadIdx.x - kBw * 32;
     const int qd = ta % S::kChunks, tl0 = ta / S::kChunks;
     const int nv = min(S::kCh, nch - qd * S::kCh);
@@ -281,6 +286,7 @@ scan_bwd_kernel(ScanParams p) {
     const int ox = (tl0 * kDc + qd * S::kCh) * kEs, ody = S::kRawTile + ox, oz = 2 * S::kRawTile + ox;
     const int odt = 3 * S::kRawTile + (tl0 * kDc + qd * S::kCh) * dts;
     const int ob = 3 * S::kRawTile + kTile * dts + (tlb * kNp + nb) * kEs;
+    float *pbc = p.part_bc + (((long long)blockIdx.x * p.B + b) * p.L + tb) * 2 * kNp;  // the segment's partial dB and dC
     const bool flip = ta & 4;
     float2 bias[kP], skip[kP], acc_d[kP], acc_b[kP];
 #pragma unroll
@@ -292,14 +298,22 @@ scan_bwd_kernel(ScanParams p) {
                               in1 && p.Dskip ? __ldg(p.Dskip + cq + 2 * j + 1) : 0.f);
         acc_d[j] = acc_b[j] = dup(0.f);
     }
+    // Every pointer stands at the thread's first token of the tile to be copied next.
+    {
+        const long long t = (long long)(nt > 0 ? nt - 1 : 0) * kT;
+        px += t * p.xs[1] * kEs, pz += t * p.zs[1] * kEs, pdt += t * p.dts[1] * dts, pdy += t * dense1 * kEs;
+        pb += t * p.bs[1] * kEs, pc += t * p.cs[1] * kEs;
+    }
+    const long long tx = (long long)kT * p.xs[1] * kEs, tz = (long long)kT * p.zs[1] * kEs, tdt = (long long)kT * p.dts[1] * dts,
+                    tdy = kT * dense1 * kEs, tB = (long long)kT * p.bs[1] * kEs, tC = (long long)kT * p.cs[1] * kEs;
     auto load_tile = [&](int i) {
         if (i < nt) {
             const int k = nt - 1 - i;
             char *s = ring + i % S::kSlots * slot;
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const long long t = k * kT + u * S::kUStep;  // from the thread's first token
-                const int n = tl0 + t < ntok ? nv : 0;
+                const int t = u * S::kUStep;  // from the thread's first token of the tile
+                const int n = k * kT + tl0 + t < ntok ? nv : 0;
                 if (tl0 < kT) {
                     char *d = s + u * S::kUStep * kDc * kEs;
                     copy_chunk<IO, VEC>(d + ox, px + t * p.xs[1] * kEs, n);
@@ -317,13 +331,14 @@ scan_bwd_kernel(ScanParams p) {
             }
 #pragma unroll
             for (int u = 0; u < kBu; ++u) {
-                const long long t = k * kT + u * S::kBcStep;
-                const int n = tlb + t < ntok ? nbv : 0;
+                const int t = u * S::kBcStep;
+                const int n = k * kT + tlb + t < ntok ? nbv : 0;
                 if (tlb < kT) {
                     copy_chunk<IO, VEC>(s + ob + u * S::kBcStep * kNp * kEs, pb + t * p.bs[1] * kEs, n);
                     copy_chunk<IO, VEC>(s + ob + S::kRawBc + u * S::kBcStep * kNp * kEs, pc + t * p.cs[1] * kEs, n);
                 }
             }
+            px -= tx, pz -= tz, pdt -= tdt, pdy -= tdy, pb -= tB, pc -= tC;
         }
         cp_commit();
     };
@@ -398,14 +413,20 @@ scan_bwd_kernel(ScanParams p) {
         const int buf = i & 1, k = nt - 1 - i;
         const char *s = ring + i % S::kSlots * slot;
         // dB and dC of the tile over the walk warps
-        for (int e = ta; e < kT * 2 * kNp; e += kBside) {
-            const int t = k * kT + e / (2 * kNp);
-            if (t >= ntok) break;
-            const float *sp = s_p + buf * kBw * kT * 2 * kNp + e;
-            float v = sp[0];
 #pragma unroll
-            for (int w = 1; w < kBw; ++w) v += sp[w * kT * 2 * kNp];
-            p.part_bc[(((long long)blockIdx.x * p.B + b) * p.L + tb + t) * 2 * kNp + e % (2 * kNp)] = v;
+        for (int e0 = 0; e0 < kT * 2 * kNp; e0 += kBside * 4) {
+            const int e = e0 + ta * 4;
+            if (e < kT * 2 * kNp && k * kT + e / (2 * kNp) < ntok) {
+                const float *sp = s_p + buf * kBw * kT * 2 * kNp + e;
+                float2 lo = dup(0.f), hi = dup(0.f);
+#pragma unroll
+                for (int w = 0; w < kBw; ++w) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sp + w * kT * 2 * kNp);
+                    lo = __fadd2_rn(lo, make_float2(v.x, v.y));
+                    hi = __fadd2_rn(hi, make_float2(v.z, v.w));
+                }
+                *reinterpret_cast<float4 *>(pbc + (long long)k * kT * 2 * kNp + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
         }
         if (tl0 >= kT) return;
 #pragma unroll
@@ -520,44 +541,57 @@ scan_bwd_kernel(ScanParams p) {
     }
 }
 
-// dA, dD and ddt_bias: the parts of every row and segment in order, four interleaved sums.
-__global__ void __launch_bounds__(256)
-scan_bwd_sum_kernel(const float *part, int rows, long long n, float *out) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
+// n rows of partial sums, `stride` apart, in order: four interleaved sums.
+__device__ __forceinline__ float sum_rows(const float *src, int n, long long stride) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    int r = 0;
-    for (; r + 4 <= rows; r += 4)
+    int k = 0;
+    for (; k + 8 <= n; k += 8) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] += __ldg(part + (long long)(r + j) * n + i);
-    for (; r < rows; ++r) s[0] += __ldg(part + (long long)r * n + i);
-    out[i] = (s[0] + s[1]) + (s[2] + s[3]);
+        for (int j = 0; j < 8; ++j) v[j] = __ldg(src + (k + j) * stride);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j & 3] += v[j];
+    }
+    for (; k < n; ++k) s[0] += __ldg(src + k * stride);
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// dB and dC of a token and group over the group's channel tiles, four interleaved sums.
+// The second kernel's sums, by blocks: first dA, dD and ddt_bias over the rows
+// and segments, then dB and dC of a token and group over the group's channel tiles.
+struct ScanSums {
+    int np;
+    long long blocks_a, blocks_d;
+    float *dA, *dD, *dbias;
+    void *dB, *dC;
+};
+
 template <int IO>
 __global__ void __launch_bounds__(256)
-scan_bwd_bc_kernel(ScanParams p, int np, void *dB, void *dC) {
-    const long long per = (long long)p.B * p.L * 2 * np;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= per) return;
-    const int g = blockIdx.y, e = (int)(i % (2 * np)), n = e % np;
+scan_bwd_sums_kernel(ScanParams p, ScanSums o) {
+    const int rows = p.B * p.nseg, np = o.np;
+    long long blk = blockIdx.x;
+    if (blk < o.blocks_a) {
+        const long long n = (long long)p.D * p.N, i = blk * 256 + threadIdx.x;
+        if (i < n) o.dA[i] = sum_rows(p.part_a + i, rows, n);
+        return;
+    }
+    blk -= o.blocks_a;
+    if (blk < o.blocks_d) {
+        const long long i = blk * 256 + threadIdx.x, c = i % p.D;
+        float *dst = i < p.D ? o.dD : o.dbias;
+        if (i < 2 * p.D && dst) dst[c] = sum_rows(p.part_d + (i < p.D ? 0 : (long long)rows * p.D) + c, rows, p.D);
+        return;
+    }
+    blk -= o.blocks_d;
+    const long long per = (long long)p.B * p.L * 2 * np, i = blk * 256 + threadIdx.x;  // over groups, tokens, dB then dC
+    if (i >= per * p.G) return;
+    const int g = (int)(i / per), e = (int)(i % (2 * np)), n = e % np;
     if (n >= p.N) return;
-    const long long bt = i / (2 * np);
+    const long long bt = i % per / (2 * np);
     const int b = (int)(bt / p.L), t = (int)(bt % p.L);
     const int len = p.lengths ? min(max(__ldg(p.lengths + b), 0), p.L) : p.L;
-    float v = 0.f;
-    if (t < len) {
-        const float *src = p.part_bc + (long long)g * p.tiles * per + i;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        int k = 0;
-        for (; k + 4 <= p.tiles; k += 4)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] += __ldg(src + (k + j) * per);
-        for (; k < p.tiles; ++k) s[0] += __ldg(src + k * per);
-        v = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-    st_io<IO>(e < np ? dB : dC, (size_t)((bt * p.G + g) * p.N + n), v);
+    const float v = t < len ? sum_rows(p.part_bc + (long long)g * p.tiles * per + i % per, p.tiles, per) : 0.f;
+    st_io<IO>(e < np ? o.dB : o.dC, (size_t)((bt * p.G + g) * p.N + n), v);
 }
 
 bool bwd_vec(const ScanParams &p, int io) {
@@ -570,7 +604,7 @@ bool bwd_vec(const ScanParams &p, int io) {
 }
 
 template <int IO, int LPC>
-cudaError_t launch_bwd_as(ScanParams p, void *dB, void *dC, cudaStream_t s) {
+cudaError_t launch_bwd_as(ScanParams p, ScanSums o, cudaStream_t s) {
     using S = BwdShape<IO, LPC>;
     const int bytes = S::bytes(IO != IO_F32 && p.dt32);
     p.tiles = scan_bwd_tiles(p);
@@ -579,19 +613,23 @@ cudaError_t launch_bwd_as(ScanParams p, void *dB, void *dC, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel<<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, bytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long per = (long long)p.B * p.L * 2 * S::kNp;
-    scan_bwd_bc_kernel<IO><<<dim3((unsigned)((per + 255) / 256), p.G), 256, 0, s>>>(p, S::kNp, dB, dC);
+    o.np = S::kNp;
+    o.blocks_a = ((long long)p.D * p.N + 255) / 256;
+    o.blocks_d = (2LL * p.D + 255) / 256;
+    const long long blocks = o.blocks_a + o.blocks_d + ((long long)p.B * p.L * 2 * S::kNp * p.G + 255) / 256;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    scan_bwd_sums_kernel<IO><<<(unsigned)blocks, 256, 0, s>>>(p, o);
     return cudaGetLastError();
 }
 
 template <int IO>
-cudaError_t launch_bwd_io(const ScanParams &p, void *dB, void *dC, cudaStream_t s) {
+cudaError_t launch_bwd_io(const ScanParams &p, const ScanSums &o, cudaStream_t s) {
     switch (scan_lanes(p.N)) {
-        case 2: return launch_bwd_as<IO, 2>(p, dB, dC, s);
-        case 4: return launch_bwd_as<IO, 4>(p, dB, dC, s);
-        case 8: return launch_bwd_as<IO, 8>(p, dB, dC, s);
-        case 16: return launch_bwd_as<IO, 16>(p, dB, dC, s);
-        case 32: return launch_bwd_as<IO, 32>(p, dB, dC, s);
+        case 2: return launch_bwd_as<IO, 2>(p, o, s);
+        case 4: return launch_bwd_as<IO, 4>(p, o, s);
+        case 8: return launch_bwd_as<IO, 8>(p, o, s);
+        case 16: return launch_bwd_as<IO, 16>(p, o, s);
+        case 32: return launch_bwd_as<IO, 32>(p, o, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -608,22 +646,13 @@ cudaError_t launch_scan_bwd(const ScanParams &p, int io, void *dB, void *dC, flo
     cudaError_t e = launch_scan_ckpt(p, io, s);
     if (e != cudaSuccess) return e;
     if ((e = launch_scan_adjoint(p, io, s)) != cudaSuccess) return e;
+    const ScanSums o = {0, 0, 0, dA, dD, dbias, dB, dC};
     switch (io) {
-        case IO_F32: e = launch_bwd_io<IO_F32>(p, dB, dC, s); break;
-        case IO_F16: e = launch_bwd_io<IO_F16>(p, dB, dC, s); break;
-        case IO_BF16: e = launch_bwd_io<IO_BF16>(p, dB, dC, s); break;
+        case IO_F32: return launch_bwd_io<IO_F32>(p, o, s);
+        case IO_F16: return launch_bwd_io<IO_F16>(p, o, s);
+        case IO_BF16: return launch_bwd_io<IO_BF16>(p, o, s);
         default: return cudaErrorInvalidValue;
     }
-    if (e != cudaSuccess) return e;
-    const int rows = p.B * p.nseg;
-    auto sum = [&](const float *part, long long n, float *out) {
-        if (!out) return;
-        scan_bwd_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, rows, n, out);
-    };
-    sum(p.part_a, (long long)p.D * p.N, dA);
-    sum(p.part_d, p.D, dD);
-    sum(p.part_d + (long long)rows * p.D, p.D, dbias);
-    return cudaGetLastError();
 }
 
 }  // namespace ssd
