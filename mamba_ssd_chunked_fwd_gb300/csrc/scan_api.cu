@@ -67,8 +67,8 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
 // The cut of the sequences into n segments.  A CTA of the forward's walk advances a
 // token in about 0.096 us alone on its SM, two that share one in 0.165 us, so a walk
 // by few CTAs is cut until there are CTAs for the SMs.  The cut costs a first walk
-// (each segment's state from zero, 0.65 of the forward's time; backwards another for
-// the adjoint, too), a fold over the segments, whose states move four times, and
+// (each segment's state from zero, 0.65 of the forward's time; backwards as many CTAs
+// again walk for the adjoint), a fold over the segments, whose states move four times, and
 // two launches.  Unit: the token of a CTA alone; measured from 128 to 16384 tokens,
 // the choice is within 5% of the best of 1 to 128 segments.
 void choose_segments(ssd::ScanParams &p, bool backward) {
@@ -82,9 +82,9 @@ void choose_segments(ssd::ScanParams &p, bool backward) {
     };
     auto cost = [&](long long m) {
         const long long len = ((p.L + m - 1) / m + 31) / 32 * 32, n = (p.L + len - 1) / len;
-        const double walk = waves(ctas * n), first = waves(ctas * (n - 1));
-        const double cut = n > 1 ? 0.65 * first * len + 1.5 * n + 2.5e-5 * state * n + 90. : 0.;
-        return backward ? 0.8 * walk * len + 1.7 * waves(2 * ctas * n) * len + 2. * cut : walk * len + cut;
+        const double walk = waves(ctas * n), first = waves((backward ? 2. : 1.) * ctas * (n - 1));
+        const double cut = n > 1 ? 0.65 * first * len + 1.5 * n + (backward ? 5e-5 : 2.5e-5) * state * n + 90. : 0.;
+        return (backward ? 0.8 * walk + 1.7 * waves(2 * ctas * n) : walk) * len + cut;
     };
     long long best = 1;
     for (long long n = 2; n <= 1024 && (p.L + n - 1) / n >= 32; n = n < 8 ? n + 1 : n + n / 4)

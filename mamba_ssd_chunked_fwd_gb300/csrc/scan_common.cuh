@@ -582,8 +582,7 @@ __device__ __forceinline__ float2 silu2(float2 v) { return __fmul2_rn(v, sigmoid
 __device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 cudaError_t launch_scan(const ScanParams &p, int io, cudaStream_t s);
-cudaError_t launch_scan_ckpt(const ScanParams &p, int io, cudaStream_t s);
-cudaError_t launch_scan_adjoint(const ScanParams &p, int io, cudaStream_t s);
+cudaError_t launch_scan_ckpt(const ScanParams &p, int io, cudaStream_t s);  // and the adjoint after every segment
 cudaError_t launch_scan_bwd(const ScanParams &p, int io, void *dB, void *dC, float *dA, float *dD, float *dbias,
                             cudaStream_t s);
 int scan_bwd_tiles(const ScanParams &p);

@@ -31,7 +31,8 @@ enum WalkMode {
     WALK_Y = 0,     // y and the final state
     WALK_SEG = 1,   // a segment's state from zero (segment 0: from h0) into slot seg + 1, its sum of d
     WALK_CKPT = 2,  // the state before every eighth token
-    WALK_ADJ = 3    // backwards: a segment's adjoint from zero (the last: from dfinal) into slot seg - 1
+    WALK_ADJ = 3,   // backwards: a segment's adjoint from zero (the last: from dfinal) into slot seg - 1
+    WALK_BOTH = 4   // WALK_SEG and WALK_ADJ of every segment that needs them, in one launch
 };
 
 constexpr int kWalkWarps = 4, kSideThreads = 128, kWalkThreads = kWalkWarps * 32 + kSideThreads;
@@ -104,8 +105,7 @@ struct QuadSum {
 };
 
 template <int IO, int LPC, int NPT, int MODE, bool VEC>
-__global__ void __launch_bounds__(kWalkThreads, 2)
-scan_walk_kernel(ScanParams p) {
+__device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     using S = WalkShape<IO, LPC, NPT>;
     constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kH = NPT / 2;
     constexpr bool kY = MODE == WALK_Y, kRev = MODE == WALK_ADJ, kZ = kY || kRev;
@@ -117,7 +117,7 @@ scan_walk_kernel(ScanParams p) {
     char *ring = reinterpret_cast<char *>(s_b + (kY ? 4 : 2) * kT * kNp);
 
     const int g = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
-    const int seg = MODE == WALK_ADJ ? blockIdx.y + 1 : blockIdx.y, b = blockIdx.z;
+    const int b = blockIdx.z;
     const int dg = p.D / p.G;
     const int c0 = g * dg + tile * kDc;
     const int nch = min(kDc, (g + 1) * dg - c0);
@@ -451,39 +451,51 @@ scan_walk_kernel(ScanParams p) {
     }
 }
 
+template <int IO, int LPC, int NPT, int MODE, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads, 2)
+scan_walk_kernel(ScanParams p) {
+    if (MODE != WALK_BOTH) {
+        walk<IO, LPC, NPT, MODE == WALK_BOTH ? WALK_SEG : MODE, VEC>(p, blockIdx.y);
+    } else if ((int)blockIdx.y < p.nseg - 1) {
+        walk<IO, LPC, NPT, WALK_SEG, VEC>(p, blockIdx.y);
+    } else {
+        walk<IO, LPC, NPT, WALK_ADJ, VEC>(p, blockIdx.y - (p.nseg - 1) + 1);
+    }
+}
+
 // The state entering every segment, in place: slot s + 1 holds segment s's own
-// state; S(s+1) = exp(A sum_s) S(s) + own(s), in order.  ADJ: the same for the
-// adjoint from the last segment down, slot s holding the adjoint after segment s.
+// state; S(s+1) = exp(A sum_s) S(s) + own(s), in order.  blockIdx.z = 1: the same for
+// the adjoint from the last segment down, slot s holding the adjoint after segment s.
 // Eight segments' values are loaded together: the order of the sums is a chain of
 // multiply-adds, not of memory latencies.
-template <bool ADJ>
 __global__ void __launch_bounds__(128)
 scan_fold_kernel(ScanParams p) {
     constexpr int kStep = 8;
+    const bool adj = blockIdx.z;
     const long long dn = (long long)p.D * p.N;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     if (i >= dn) return;
     const int b = blockIdx.y, n = p.nseg - 2;  // sums of n segments on top of the first slot
     const float a2 = __ldg(p.A + i) * kLog2e;
-    float *st = (ADJ ? p.adj : p.seg_states) + (long long)b * p.nseg * dn + i;
+    float *st = (adj ? p.adj : p.seg_states) + (long long)b * p.nseg * dn + i;
     const float *sm = p.seg_sum + (long long)b * p.nseg * p.D + i / p.N;
-    float s = st[(ADJ ? n : 1) * dn];
+    float s = st[(adj ? n : 1) * dn];
     for (int k0 = 0; k0 < n; k0 += kStep) {
         float own[kStep], sum[kStep];
 #pragma unroll
         for (int j = 0; j < kStep; ++j) {
-            const int k = ADJ ? n - (k0 + j) : k0 + j + 1;  // the segment passed through
+            const int k = adj ? n - (k0 + j) : k0 + j + 1;  // the segment passed through
             if (k0 + j < n) {
-                own[j] = st[(ADJ ? k - 1 : k + 1) * dn];
+                own[j] = st[(adj ? k - 1 : k + 1) * dn];
                 sum[j] = __ldg(sm + (long long)k * p.D);
             }
         }
 #pragma unroll
         for (int j = 0; j < kStep; ++j) {
-            const int k = ADJ ? n - (k0 + j) : k0 + j + 1;
+            const int k = adj ? n - (k0 + j) : k0 + j + 1;
             if (k0 + j < n) {
                 s = fmaf(ex2(a2 * sum[j]), s, own[j]);
-                st[(ADJ ? k - 1 : k + 1) * dn] = s;
+                st[(adj ? k - 1 : k + 1) * dn] = s;
             }
         }
     }
@@ -492,10 +504,10 @@ scan_fold_kernel(ScanParams p) {
 // Whether every tensor the side warps touch moves in aligned, whole chunks of 16 bytes.
 bool walk_vec(const ScanParams &p, int io, int mode) {
     const long long dense[2] = {(long long)p.L * p.D, p.D};
-    const bool adj = mode == WALK_ADJ, y = mode == WALK_Y;
+    const bool adj = mode == WALK_BOTH, y = mode == WALK_Y;
     const int ch = io == IO_F32 ? 4 : 8;
-    return p.D / p.G % ch == 0 && p.N % ch == 0 && (adj || chunk_strided(p.x, io, p.xs)) &&
-           chunk_strided(p.dt, p.dt32 ? (int)IO_F32 : io, p.dts) && (adj || chunk_strided(p.Bm, io, p.bs)) &&
+    return p.D / p.G % ch == 0 && p.N % ch == 0 && chunk_strided(p.x, io, p.xs) &&
+           chunk_strided(p.dt, p.dt32 ? (int)IO_F32 : io, p.dts) && chunk_strided(p.Bm, io, p.bs) &&
            (!(adj || y) || (chunk_strided(p.Cm, io, p.cs) && (!p.z || chunk_strided(p.z, io, p.zs)))) &&
            (!y || chunk_strided(p.y, io, dense)) && (!adj || chunk_strided(p.dy, io, dense));
 }
@@ -504,8 +516,9 @@ template <int IO, int LPC, int NPT, int MODE>
 cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
     constexpr int kDc = WalkShape<IO, LPC, NPT>::kDc;
     p.tiles = (p.D / p.G + kDc - 1) / kDc;
-    const int segs = MODE == WALK_SEG || MODE == WALK_ADJ ? p.nseg - 1 : p.nseg;
-    const int bytes = WalkSmem<IO, LPC, NPT, MODE>::bytes(IO != IO_F32 && p.dt32);
+    const int segs = MODE == WALK_SEG ? p.nseg - 1 : MODE == WALK_BOTH ? 2 * (p.nseg - 1) : p.nseg;
+    constexpr int kMost = MODE == WALK_BOTH ? (int)WALK_ADJ : MODE;  // the mode that needs the most
+    const int bytes = WalkSmem<IO, LPC, NPT, kMost>::bytes(IO != IO_F32 && p.dt32);
     auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, NPT, MODE, true> : scan_walk_kernel<IO, LPC, NPT, MODE, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -535,12 +548,13 @@ cudaError_t launch_walk(const ScanParams &p, int io, cudaStream_t s) {
     }
 }
 
-cudaError_t segment_states(const ScanParams &p, int io, cudaStream_t s) {
+// What the segments start from: their states, and backwards their adjoints.
+cudaError_t cut(const ScanParams &p, int io, bool backward, cudaStream_t s) {
     if (p.nseg == 1) return cudaSuccess;
-    cudaError_t e = launch_walk<WALK_SEG>(p, io, s);
+    cudaError_t e = backward ? launch_walk<WALK_BOTH>(p, io, s) : launch_walk<WALK_SEG>(p, io, s);
     if (e != cudaSuccess || p.nseg == 2) return e;
     const long long dn = (long long)p.D * p.N;
-    scan_fold_kernel<false><<<dim3((unsigned)((dn + 127) / 128), p.B), 128, 0, s>>>(p);
+    scan_fold_kernel<<<dim3((unsigned)((dn + 127) / 128), p.B, backward ? 2 : 1), 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -563,24 +577,13 @@ int scan_sm_count() {
 }
 
 cudaError_t launch_scan(const ScanParams &p, int io, cudaStream_t s) {
-    cudaError_t e = segment_states(p, io, s);
-    if (e != cudaSuccess) return e;
-    return launch_walk<WALK_Y>(p, io, s);
+    cudaError_t e = cut(p, io, false, s);
+    return e != cudaSuccess ? e : launch_walk<WALK_Y>(p, io, s);
 }
 
 cudaError_t launch_scan_ckpt(const ScanParams &p, int io, cudaStream_t s) {
-    cudaError_t e = segment_states(p, io, s);
-    if (e != cudaSuccess) return e;
-    return launch_walk<WALK_CKPT>(p, io, s);
-}
-
-cudaError_t launch_scan_adjoint(const ScanParams &p, int io, cudaStream_t s) {
-    if (p.nseg == 1) return cudaSuccess;
-    cudaError_t e = launch_walk<WALK_ADJ>(p, io, s);
-    if (e != cudaSuccess || p.nseg == 2) return e;
-    const long long dn = (long long)p.D * p.N;
-    scan_fold_kernel<true><<<dim3((unsigned)((dn + 127) / 128), p.B), 128, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaError_t e = cut(p, io, true, s);
+    return e != cudaSuccess ? e : launch_walk<WALK_CKPT>(p, io, s);
 }
 
 }  // namespace ssd

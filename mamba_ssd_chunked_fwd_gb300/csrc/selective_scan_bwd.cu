@@ -645,7 +645,6 @@ cudaError_t launch_scan_bwd(const ScanParams &p, int io, void *dB, void *dC, flo
                             cudaStream_t s) {
     cudaError_t e = launch_scan_ckpt(p, io, s);
     if (e != cudaSuccess) return e;
-    if ((e = launch_scan_adjoint(p, io, s)) != cudaSuccess) return e;
     const ScanSums o = {0, 0, 0, dA, dD, dbias, dB, dC};
     switch (io) {
         case IO_F32: return launch_bwd_io<IO_F32>(p, o, s);
