@@ -81,15 +81,15 @@ void choose_segments(ssd::ScanParams &p, bool backward) {
         return full * pair + (rest == 0. ? 0. : rest <= sms ? 1. : pair);
     };
     auto cost = [&](long long m) {
-        const long long len = ((p.L + m - 1) / m + 31) / 32 * 32, n = (p.L + len - 1) / len;
+        const long long len = ((p.L + m - 1) / m + 15) / 16 * 16, n = (p.L + len - 1) / len;
         const double walk = waves(ctas * n), first = waves((backward ? 2. : 1.) * ctas * (n - 1));
         const double cut = n > 1 ? 0.65 * first * len + 1.5 * n + (backward ? 5e-5 : 2.5e-5) * state * n + 90. : 0.;
         return (backward ? 0.8 * walk + 1.7 * waves(2 * ctas * n) : walk) * len + cut;
     };
     long long best = 1;
-    for (long long n = 2; n <= 1024 && (p.L + n - 1) / n >= 32; n = n < 8 ? n + 1 : n + n / 4)
+    for (long long n = 2; n <= 1024 && (p.L + n - 1) / n >= 16; n = n < 8 ? n + 1 : n + n / 4)
         if (cost(n) < cost(best)) best = n;
-    p.seg_len = (int)(((p.L + best - 1) / best + 31) / 32 * 32);
+    p.seg_len = (int)(((p.L + best - 1) / best + 15) / 16 * 16);
     p.nseg = (int)((p.L + p.seg_len - 1) / p.seg_len);
 }
 

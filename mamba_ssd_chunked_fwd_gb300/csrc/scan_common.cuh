@@ -17,7 +17,7 @@ struct ScanParams {
     int dt32;                                      // dt is fp32
     int softplus, has_limit;
     float dt_min, dt_max;
-    // segments: tokens [s seg_len, (s+1) seg_len) of every row; seg_len a multiple of 32
+    // segments: tokens [s seg_len, (s+1) seg_len) of every row; seg_len a multiple of 16
     int nseg, seg_len;
     float *seg_states;  // [B,nseg,D,N] state entering a segment (slot 0 unused)
     float *seg_sum;     // [B,nseg,D]   sum of d over a segment
