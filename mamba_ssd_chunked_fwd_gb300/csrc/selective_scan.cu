@@ -37,12 +37,12 @@ enum WalkMode {
 
 constexpr int kWalkWarps = 4, kSideThreads = 128, kWalkThreads = kWalkWarps * 32 + kSideThreads;
 
-// NPT states per lane, four channels: LPC = N / NPT lanes hold a channel.
-template <int IO, int LPC, int NPT>
+// Four states of four channels per lane: LPC = N / 4 lanes hold a channel.
+template <int IO, int LPC>
 struct WalkShape {
     static constexpr int kGroups = 32 / LPC;              // channel quads per warp
     static constexpr int kDc = kWalkWarps * kGroups * 4;  // channels per CTA
-    static constexpr int kNp = LPC * NPT;
+    static constexpr int kNp = LPC * 4;
     // tokens per tile: fp32 tiles are half as long, so that two CTAs' rings fit an SM
     static constexpr int kElems = IO == IO_F32 ? 1024 : 2048;
     static constexpr int kMost = kNp <= 16 ? 32 : kNp > 64 && IO == IO_F32 ? 8 : 16;
@@ -63,9 +63,9 @@ struct WalkShape {
 };
 
 // Bytes of shared memory: d, d x, B (and C), two buffers each; the ring: x, dt, z, B, C.
-template <int IO, int LPC, int NPT, int MODE>
+template <int IO, int LPC, int MODE>
 struct WalkSmem {
-    using S = WalkShape<IO, LPC, NPT>;
+    using S = WalkShape<IO, LPC>;
     static constexpr bool kY = MODE == WALK_Y, kZ = MODE == WALK_Y || MODE == WALK_ADJ;
     static constexpr int kStage = (2 * 2 * S::kT * S::kDc + (kY ? 4 : 2) * S::kT * S::kNp) * 4;
     static constexpr int slot(int dt32) {  // dt may be wider than x
@@ -81,7 +81,7 @@ struct WalkSmem {
 // is left with one token's four channels.  Returns the index of v[0].
 template <int LPC>
 struct QuadSum {
-    static constexpr int kLeft = LPC == 1 ? 16 : LPC == 2 ? 8 : LPC == 4 ? 4 : LPC == 8 ? 2 : 1;
+    static constexpr int kLeft = LPC == 2 ? 8 : LPC == 4 ? 4 : LPC == 8 ? 2 : 1;
     static __device__ __forceinline__ int run(float (&v)[16], int lane) {
         int idx = 0, cnt = 16;
 #pragma unroll
@@ -104,10 +104,10 @@ struct QuadSum {
     }
 };
 
-template <int IO, int LPC, int NPT, int MODE, bool VEC>
+template <int IO, int LPC, int MODE, bool VEC>
 __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
-    using S = WalkShape<IO, LPC, NPT>;
-    constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kH = NPT / 2;
+    using S = WalkShape<IO, LPC>;
+    constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kH = 2;
     constexpr bool kY = MODE == WALK_Y, kRev = MODE == WALK_ADJ, kZ = kY || kRev;
     extern __shared__ __align__(16) float smem[];
     float *s_d = smem;                            // [2][kT][kDc]
@@ -128,7 +128,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp < kWalkWarps) {
-        const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 4, n0 = ln * NPT;
+        const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 4, n0 = ln * 4;
         float2 h[4][kH], a2[4][kH];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         const float *start = nullptr;
@@ -141,29 +141,24 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
             start = seg == p.nseg - 1 && p.dfinal ? p.dfinal + (long long)b * p.D * p.N : nullptr;
         const bool va = aligned_n4(p.A, p.N), vs = aligned_n4(start, p.N);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int m = 0; m < NPT; m += 4) {
-                float a[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-                if (ch0 + j < nch) {
-                    const long long i = (long long)(c0 + ch0 + j) * p.N + n0 + m;
-                    load_n4(p.A, i, n0 + m, p.N, va, a);
-                    if (start) load_n4(start, i, n0 + m, p.N, vs, s);
-                }
-                // the decay as a power of two: exp(d A) = 2^(d A log2 e)
-                a2[j][m / 2] = make_float2(a[0] * kLog2e, a[1] * kLog2e);
-                a2[j][m / 2 + 1] = make_float2(a[2] * kLog2e, a[3] * kLog2e);
-                h[j][m / 2] = make_float2(s[0], s[1]);
-                h[j][m / 2 + 1] = make_float2(s[2], s[3]);
+        for (int j = 0; j < 4; ++j) {
+            float a[4] = {0.f, 0.f, 0.f, 0.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+            if (ch0 + j < nch) {
+                const long long i = (long long)(c0 + ch0 + j) * p.N + n0;
+                load_n4(p.A, i, n0, p.N, va, a);
+                if (start) load_n4(start, i, n0, p.N, vs, s);
             }
+            // the decay as a power of two: exp(d A) = 2^(d A log2 e)
+            a2[j][0] = make_float2(a[0] * kLog2e, a[1] * kLog2e);
+            a2[j][1] = make_float2(a[2] * kLog2e, a[3] * kLog2e);
+            h[j][0] = make_float2(s[0], s[1]);
+            h[j][1] = make_float2(s[2], s[3]);
+        }
         auto store_state = [&](float *base, long long row, bool vec) {  // row: of [*, N]
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (ch0 + j < nch)
-#pragma unroll
-                    for (int m = 0; m < NPT; m += 4)
-                        store_n4(base, (row + j) * p.N + n0 + m, n0 + m, p.N, vec, h[j][m / 2].x, h[j][m / 2].y,
-                                 h[j][m / 2 + 1].x, h[j][m / 2 + 1].y);
+                    store_n4(base, (row + j) * p.N + n0, n0, p.N, vec, h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y);
         };
         __syncthreads();  // tile 0 staged
         for (int k = 0; k < nt; ++k) {
@@ -176,7 +171,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
                 if (MODE == WALK_CKPT && (k * kT + t4) % kCkpt == 0)
                     store_state(p.ckpt, ((long long)b * ((p.L + kCkpt - 1) / kCkpt) + (tb + k * kT + t4) / kCkpt) * p.D +
                                             c0 + ch0, p.N % 4 == 0);
-// d and d x of the four tokens first: y is stored over d x below, and a load after such a
+                // d and d x of the four tokens first: y is stored over d x below, and a load after such a
                 // store would have to wait for it.
                 float4 d4[4], w4[4];
 #pragma unroll
@@ -190,17 +185,13 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
                     const int t = t4 + tt;
                     const float d[4] = {d4[tt].x, d4[tt].y, d4[tt].z, d4[tt].w};
                     const float w[4] = {w4[tt].x, w4[tt].y, w4[tt].z, w4[tt].w};
-                    float2 bb[kH], cc[kH];
-#pragma unroll
-                    for (int m = 0; m < kH; m += 2) {
-                        const float4 b4 = *reinterpret_cast<const float4 *>(sb + t * kNp + 2 * m);
-                        bb[m] = make_float2(b4.x, b4.y);
-                        bb[m + 1] = make_float2(b4.z, b4.w);
-                        if (kY) {
-                            const float4 c4 = *reinterpret_cast<const float4 *>(sc + t * kNp + 2 * m);
-                            cc[m] = make_float2(c4.x, c4.y);
-                            cc[m + 1] = make_float2(c4.z, c4.w);
-                        }
+                    const float4 b4 = *reinterpret_cast<const float4 *>(sb + t * kNp);
+                    const float2 bb[kH] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+                    float2 cc[kH];
+                    if (kY) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(sc + t * kNp);
+                        cc[0] = make_float2(c4.x, c4.y);
+                        cc[1] = make_float2(c4.z, c4.w);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -277,7 +268,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     const char *lc = at(p.Cm, (b * p.cs[0] + firstb * p.cs[1] + gn) * kEs);
     const long long sb = dir * S::kBcStep * (kRev ? p.cs[1] : p.bs[1]) * kEs, sc = (long long)S::kBcStep * p.cs[1] * kEs;
     // a thread's chunks in a ring slot: x, z, dt, B, C
-    const int slot = WalkSmem<IO, LPC, NPT, MODE>::slot(wide);
+    const int slot = WalkSmem<IO, LPC, MODE>::slot(wide);
     const int ox = (tl0 * kDc + q * S::kCh) * kEs, oz = S::kRawTile + ox;
     const int odt = S::kRawTile * (kZ ? 2 : 1) + (tl0 * kDc + q * S::kCh) * dts;
     const int ob = S::kRawTile * (kZ ? 2 : 1) + kT * kDc * dts + (tlb * kNp + nb) * kEs;
@@ -451,15 +442,15 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     }
 }
 
-template <int IO, int LPC, int NPT, int MODE, bool VEC>
+template <int IO, int LPC, int MODE, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 scan_walk_kernel(ScanParams p) {
     if (MODE != WALK_BOTH) {
-        walk<IO, LPC, NPT, MODE == WALK_BOTH ? WALK_SEG : MODE, VEC>(p, blockIdx.y);
+        walk<IO, LPC, MODE == WALK_BOTH ? WALK_SEG : MODE, VEC>(p, blockIdx.y);
     } else if ((int)blockIdx.y < p.nseg - 1) {
-        walk<IO, LPC, NPT, WALK_SEG, VEC>(p, blockIdx.y);
+        walk<IO, LPC, WALK_SEG, VEC>(p, blockIdx.y);
     } else {
-        walk<IO, LPC, NPT, WALK_ADJ, VEC>(p, blockIdx.y - (p.nseg - 1) + 1);
+        walk<IO, LPC, WALK_ADJ, VEC>(p, blockIdx.y - (p.nseg - 1) + 1);
     }
 }
 
@@ -512,14 +503,14 @@ bool walk_vec(const ScanParams &p, int io, int mode) {
            (!y || chunk_strided(p.y, io, dense)) && (!adj || chunk_strided(p.dy, io, dense));
 }
 
-template <int IO, int LPC, int NPT, int MODE>
+template <int IO, int LPC, int MODE>
 cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
-    constexpr int kDc = WalkShape<IO, LPC, NPT>::kDc;
+    constexpr int kDc = WalkShape<IO, LPC>::kDc;
     p.tiles = (p.D / p.G + kDc - 1) / kDc;
     const int segs = MODE == WALK_SEG ? p.nseg - 1 : MODE == WALK_BOTH ? 2 * (p.nseg - 1) : p.nseg;
     constexpr int kMost = MODE == WALK_BOTH ? (int)WALK_ADJ : MODE;  // the mode that needs the most
-    const int bytes = WalkSmem<IO, LPC, NPT, kMost>::bytes(IO != IO_F32 && p.dt32);
-    auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, NPT, MODE, true> : scan_walk_kernel<IO, LPC, NPT, MODE, false>;
+    const int bytes = WalkSmem<IO, LPC, kMost>::bytes(IO != IO_F32 && p.dt32);
+    auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, MODE, true> : scan_walk_kernel<IO, LPC, MODE, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kernel<<<dim3(p.G * p.tiles, segs, p.B), kWalkThreads, bytes, s>>>(p);
@@ -529,11 +520,11 @@ cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
 template <int IO, int MODE>
 cudaError_t launch_walk_io(const ScanParams &p, cudaStream_t s) {
     switch (scan_lanes(p.N)) {
-        case 2: return launch_walk_as<IO, 2, 4, MODE>(p, s);
-        case 4: return launch_walk_as<IO, 4, 4, MODE>(p, s);
-        case 8: return launch_walk_as<IO, 8, 4, MODE>(p, s);
-        case 16: return launch_walk_as<IO, 16, 4, MODE>(p, s);
-        case 32: return launch_walk_as<IO, 32, 4, MODE>(p, s);
+        case 2: return launch_walk_as<IO, 2, MODE>(p, s);
+        case 4: return launch_walk_as<IO, 4, MODE>(p, s);
+        case 8: return launch_walk_as<IO, 8, MODE>(p, s);
+        case 16: return launch_walk_as<IO, 16, MODE>(p, s);
+        case 32: return launch_walk_as<IO, 32, MODE>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }
