@@ -209,6 +209,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
 template <int IO, int SIO, int K, bool VEC, int MAXT, bool WHOLE>
 __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1)
 block_norm_bwd_kernel(BlockNormParams p, int stages) {
+    tc::pdl_launch_dependents();
     constexpr int NI = WHOLE ? 3 : 2;
     using S = NormSlots<IO, SIO, K, NI, WHOLE ? 2 : 1>;  // o, dn, gate; r', dr_out
     extern __shared__ __align__(16) char ring[];
@@ -370,6 +371,7 @@ template <int IO>
 __global__ void __launch_bounds__(1024)
 block_norm_sum_kernel(BlockNormParams p) {
     __shared__ float red[2][32][33];
+    tc::pdl_wait();
     const int c = blockIdx.x * 32 + threadIdx.x;
     const bool seq_gate = p.gate && p.rows_per_gate > 1, in = c < p.D;
     const float wpost = in && p.w_post ? __ldg(p.w_post + c) : 1.f, scale = in && p.scale ? __ldg(p.scale + c) : 1.f;
@@ -465,8 +467,7 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    block_norm_sum_kernel<IO><<<(p.D + 31) / 32, dim3(32, 32), 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(true, block_norm_sum_kernel<IO>, dim3((p.D + 31) / 32), dim3(32, 32), 0, s, p);
 }
 
 template <int IO, int SIO>

@@ -159,6 +159,7 @@ conv_carry_kernel(ConvParams p) {
 template <int IO, int KT, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kCx * kCy, KT == 4 ? 4 : 1)
 conv_bwd_kernel(ConvParams p) {
+    tc::pdl_launch_dependents();
     constexpr int kQ = IO == IO_F32 ? 16 : 8;
     __shared__ __align__(16) float red[kCy][kCx * 4];
     extern __shared__ __align__(16) char ring[];  // [2 kAhead][2][kCx kCy] of four elements: x, dy
@@ -287,6 +288,7 @@ conv_bwd_kernel(ConvParams p) {
 __global__ void __launch_bounds__(256)
 conv_bwd_sum_kernel(ConvParams p, int rows) {
     __shared__ float red[8][32];
+    tc::pdl_wait();
     const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
     float a = 0.f;
     if (c < p.C)
@@ -336,8 +338,7 @@ cudaError_t launch_conv_bwd_io(const ConvParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel<<<grid, dim3(kCx, kCy), kBytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    conv_bwd_sum_kernel<<<dim3((p.C + 31) / 32, p.W + 1), dim3(32, 8), 0, s>>>(p, rows * p.B);
-    return cudaGetLastError();
+    return launch_kernel(true, conv_bwd_sum_kernel, dim3((p.C + 31) / 32, p.W + 1), dim3(32, 8), 0, s, p, rows * p.B);
 }
 
 }  // namespace

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "ssd_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace ssd {
 
@@ -449,6 +450,26 @@ __device__ __forceinline__ void store4_io(void *base, long long i, int nv, const
         }
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = u;
     }
+}
+
+// A launch that may start while the kernel before it on the stream still runs (`after`):
+// that one has let it with pdl_launch_dependents, and this one's threads all begin with
+// pdl_wait, so nothing is read or written early; what is saved is the gap between the two.
+// What the kernel before wrote is read by plain or L2 loads, never by read-only ones.
+template <class... P, class... A>
+cudaError_t launch_kernel(bool after, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...), last = cudaGetLastError();
+    return e != cudaSuccess ? e : last;
 }
 
 // Four fp32 values of a [*,N] row from column n on; zeros past N.

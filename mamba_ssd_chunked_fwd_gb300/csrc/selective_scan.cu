@@ -445,6 +445,8 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
 template <int IO, int LPC, int MODE, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 scan_walk_kernel(ScanParams p) {
+    if (MODE == WALK_Y || MODE == WALK_CKPT) tc::pdl_wait();
+    if (MODE != WALK_Y) tc::pdl_launch_dependents();
     if (MODE != WALK_BOTH) {
         walk<IO, LPC, MODE == WALK_BOTH ? WALK_SEG : MODE, VEC>(p, blockIdx.y);
     } else if ((int)blockIdx.y < p.nseg - 1) {
@@ -462,6 +464,8 @@ scan_walk_kernel(ScanParams p) {
 __global__ void __launch_bounds__(128)
 scan_fold_kernel(ScanParams p) {
     constexpr int kStep = 8;
+    tc::pdl_wait();
+    tc::pdl_launch_dependents();
     const bool adj = blockIdx.z;
     const long long dn = (long long)p.D * p.N;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
@@ -478,7 +482,7 @@ scan_fold_kernel(ScanParams p) {
             const int k = adj ? n - (k0 + j) : k0 + j + 1;  // the segment passed through
             if (k0 + j < n) {
                 own[j] = st[(adj ? k - 1 : k + 1) * dn];
-                sum[j] = __ldg(sm + (long long)k * p.D);
+                sum[j] = sm[(long long)k * p.D];
             }
         }
 #pragma unroll
@@ -513,8 +517,8 @@ cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
     auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, MODE, true> : scan_walk_kernel<IO, LPC, MODE, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(p.G * p.tiles, segs, p.B), kWalkThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    const bool after = (MODE == WALK_Y || MODE == WALK_CKPT) && p.nseg > 1;  // the cut's kernels
+    return launch_kernel(after, kernel, dim3(p.G * p.tiles, segs, p.B), kWalkThreads, bytes, s, p);
 }
 
 template <int IO, int MODE>
@@ -545,8 +549,7 @@ cudaError_t cut(const ScanParams &p, int io, bool backward, cudaStream_t s) {
     cudaError_t e = backward ? launch_walk<WALK_BOTH>(p, io, s) : launch_walk<WALK_SEG>(p, io, s);
     if (e != cudaSuccess || p.nseg == 2) return e;
     const long long dn = (long long)p.D * p.N;
-    scan_fold_kernel<<<dim3((unsigned)((dn + 127) / 128), p.B, backward ? 2 : 1), 128, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(true, scan_fold_kernel, dim3((unsigned)((dn + 127) / 128), p.B, backward ? 2 : 1), 128, 0, s, p);
 }
 
 int g_scan_sms[64] = {};

@@ -84,6 +84,8 @@ struct GroupSum {
 template <int IO, int LPC, bool VEC>
 __global__ void __launch_bounds__(kBthreads, 2)
 scan_bwd_kernel(ScanParams p) {
+    tc::pdl_wait();
+    tc::pdl_launch_dependents();
     using S = BwdShape<IO, LPC>;
     constexpr int kT = S::kT, kDc = S::kDc, kNp = S::kNp, kU = S::kUnits, kBu = S::kBcUnits, kTile = S::kTile;
     extern __shared__ __align__(16) float smem[];
@@ -548,11 +550,11 @@ __device__ __forceinline__ float sum_rows(const float *src, int n, long long str
     for (; k + 8 <= n; k += 8) {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __ldg(src + (k + j) * stride);
+        for (int j = 0; j < 8; ++j) v[j] = src[(k + j) * stride];
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j & 3] += v[j];
     }
-    for (; k < n; ++k) s[0] += __ldg(src + k * stride);
+    for (; k < n; ++k) s[0] += src[k * stride];
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -568,6 +570,7 @@ struct ScanSums {
 template <int IO>
 __global__ void __launch_bounds__(256)
 scan_bwd_sums_kernel(ScanParams p, ScanSums o) {
+    tc::pdl_wait();
     const int rows = p.B * p.nseg, np = o.np;
     long long blk = blockIdx.x;
     if (blk < o.blocks_a) {
@@ -611,15 +614,14 @@ cudaError_t launch_bwd_as(ScanParams p, ScanSums o, cudaStream_t s) {
     auto *kernel = bwd_vec(p, IO) ? scan_bwd_kernel<IO, LPC, true> : scan_bwd_kernel<IO, LPC, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, bytes, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_kernel(true, kernel, dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, bytes, s, p);
+    if (e != cudaSuccess) return e;
     o.np = S::kNp;
     o.blocks_a = ((long long)p.D * p.N + 255) / 256;
     o.blocks_d = (2LL * p.D + 255) / 256;
     const long long blocks = o.blocks_a + o.blocks_d + ((long long)p.B * p.L * 2 * S::kNp * p.G + 255) / 256;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    scan_bwd_sums_kernel<IO><<<(unsigned)blocks, 256, 0, s>>>(p, o);
-    return cudaGetLastError();
+    return launch_kernel(true, scan_bwd_sums_kernel<IO>, dim3((unsigned)blocks), 256, 0, s, p, o);
 }
 
 template <int IO>
