@@ -48,16 +48,47 @@ __device__ __forceinline__ float round_io(float v) {
     return IoTraits<SIO>::to_f(IoTraits<SIO>::from_f(v));
 }
 
-// Eight elements of a row as four pairs, the unit a thread deals in: one chunk of
-// 16 bytes of a 16-bit type, two of fp32.  n of them exist (VEC: all or none).
+// Eight elements of a row as four pairs, the unit a thread deals in.  VEC: aligned and
+// whole, one chunk of 16 bytes of a 16-bit type, two of fp32, beside its neighbours' chunks.
+// Otherwise the pairs lie `step` elements apart, each beside the neighbours' pairs, so
+// that a warp's accesses stay dense, and n elements are left in the row from the first
+// pair on.  32768 rows of 2048, 2046 and 2047 bf16 elements: 136, 206 and 242 us (396 for
+// 2047 with a thread's eight elements side by side); backwards, 8192 rows: 64, 100 and 129.
 template <int IO>
 struct Eight {
     static constexpr int kEs = IO == IO_F32 ? 4 : 2, kBytes = 8 * kEs;
 };
+// Pairs from a 4-byte boundary, and fp32 elements, are copied asynchronously; other 16-bit
+// elements have no asynchronous form and are loaded, all at once, and stored.
 template <int IO, bool VEC>
-__device__ __forceinline__ void copy8(char *dst, const char *src, int n) {
-    copy_chunk<IO, VEC>(dst, src, n);
-    if (IO == IO_F32) copy_chunk<IO, VEC>(dst + 16, src + 16, n - 4);
+__device__ __forceinline__ void copy8(char *dst, const char *src, int n, int step) {
+    if (VEC || IO == IO_F32) {
+#pragma unroll
+        for (int j = 0; j < (VEC ? Eight<IO>::kBytes / 16 : 8); ++j) {
+            if (VEC) {
+                copy_chunk<IO, true>(dst + 16 * j, src + 16 * j, n);
+            } else {
+                const int e = j / 2 * step + j % 2;
+                cp_async4(dst + 4 * j, e < n ? src + 4LL * e : nullptr, e < n ? 4 : 0);
+            }
+        }
+        return;
+    }
+    const bool even = (reinterpret_cast<size_t>(src) & 3) == 0;  // so are the other pairs: step is even
+    uint16_t e[8];
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int left = n - j * step;
+        const char *at = src + 2LL * j * step;
+        cp_async4_if(even, dst + 4 * j, left > 0 ? at : nullptr, min(max(2 * left, 0), 4));
+        e[2 * j] = e[2 * j + 1] = 0;
+        ldg_u16(e[2 * j], at, !even && left > 0);
+        ldg_u16(e[2 * j + 1], at + 2, !even && left > 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+    if (!even) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <int IO>
 __device__ __forceinline__ void read8(const char *src, float2 (&v)[4]) {
@@ -65,34 +96,58 @@ __device__ __forceinline__ void read8(const char *src, float2 (&v)[4]) {
     if (IO == IO_F32) read_chunk<IO>(src + 16, v + 2);
 }
 template <int IO, bool VEC>
-__device__ __forceinline__ void store8(char *dst, int n, const float2 (&v)[4]) {
-    store_chunk<IO, VEC>(dst, n, v);
-    if (IO == IO_F32) store_chunk<IO, VEC>(dst + 16, n - 4, v + 2);
+__device__ __forceinline__ void store8(char *dst, int n, int step, const float2 (&v)[4]) {
+    if (VEC) {
+        store_chunk<IO, VEC>(dst, n, v);
+        if (IO == IO_F32) store_chunk<IO, VEC>(dst + 16, n, v + 2);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int left = n - j * step;
+        char *at = dst + (long long)j * step * Eight<IO>::kEs;
+        if (IO != IO_F32 && left > 1 && (reinterpret_cast<size_t>(at) & 3) == 0) {
+            *reinterpret_cast<uint32_t *>(at) = pack16<IO>(v[j]);
+        } else {
+            if (left > 0) st_io<IO>(at, 0, v[j].x);
+            if (left > 1) st_io<IO>(at, 1, v[j].y);
+        }
+    }
 }
 // Straight from global memory: a weight vector (ones when absent), or a tensor that has no slot.
 template <int IO, bool VEC>
-__device__ __forceinline__ void load8(const void *base, long long i, int n, float2 (&v)[4]) {
+__device__ __forceinline__ void load8(const void *base, long long i, int n, int step, float2 (&v)[4]) {
+    if (!base) n = 0;
+    if (VEC) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float f[4];
-        unpack4<IO, VEC>(load_raw4<IO, VEC>(base, i + 4 * h, base ? n - 4 * h : 0, n - 4 * h), f);
-        v[2 * h] = make_float2(f[0], f[1]);
-        v[2 * h + 1] = make_float2(f[2], f[3]);
+        for (int h = 0; h < 2; ++h) {
+            float f[4];
+            unpack4<IO, VEC>(load_raw4<IO, VEC>(base, i + 4 * h, n, n - 4 * h), f);
+            v[2 * h] = make_float2(f[0], f[1]);
+            v[2 * h + 1] = make_float2(f[2], f[3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = n - j * step;
+            v[j].x = left > 0 ? ld_io<IO>(base, (size_t)(i + j * step)) : 0.f;
+            v[j].y = left > 1 ? ld_io<IO>(base, (size_t)(i + j * step + 1)) : 0.f;
+        }
     }
 }
 template <bool VEC>
-__device__ __forceinline__ void weights(const float *w, int c, int n, float2 (&v)[4]) {
-    load8<IO_F32, VEC>(w, c, n, v);
+__device__ __forceinline__ void weights(const float *w, int c, int n, int step, float2 (&v)[4]) {
+    load8<IO_F32, VEC>(w, c, n, step, v);
     if (!w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = dup(1.f);
 }
 // scale w_post
 template <bool VEC>
-__device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, int n, float2 (&v)[4]) {
+__device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, int n, int step, float2 (&v)[4]) {
     float2 s[4];
-    weights<VEC>(p.w_post, c, n, v);
-    weights<VEC>(p.scale, c, n, s);
+    weights<VEC>(p.w_post, c, n, step, v);
+    weights<VEC>(p.scale, c, n, step, s);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], s[j]);
 }
@@ -113,6 +168,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
     __shared__ float red[2][1][32];
     constexpr int kEi = Eight<IO>::kEs, kEs = Eight<SIO>::kEs, kBi = Eight<IO>::kBytes, kBs = Eight<SIO>::kBytes;
     const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y;
+    const int cx = tx * (VEC ? 8 : 2), ps = VEC ? 2 : 2 * tpr;  // the first element of unit 0; from pair to pair
     char *mine = ring + (threadIdx.y * blockDim.x + tx) * kBi;                   // + (i K + k) line
     char *mine_s = ring + 2 * K * kBi * nthr + (threadIdx.y * blockDim.x + tx) * kBs;  // + k line_s
     const int line = nthr * kBi, line_s = nthr * kBs, stage = nthr * S::kPerThread;
@@ -120,15 +176,15 @@ block_norm_kernel(BlockNormParams p, int stages) {
     const long long step = (long long)gridDim.x * blockDim.y;
     auto copy = [&](long long row, int at) {
         if (row < p.rows) {
-            const long long base = row * p.D + tx * 8, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 8 : 0;
+            const long long base = row * p.D + cx, gbase = p.gate ? row / p.rows_per_gate * p.D + cx : 0;
             const char *r = static_cast<const char *>(p.r) + base * kEs, *o = static_cast<const char *>(p.o) + base * kEi,
                        *g = static_cast<const char *>(p.gate) + gbase * kEi;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int n = min(8, p.D - (tx + tpr * k) * 8);
-                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, n);
-                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, n);
-                if (p.gate) copy8<IO, VEC>(mine + at + (K + k) * line, g + tpr * k * kBi, n);
+                const int n = p.D - cx - tpr * k * 8;
+                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, n, ps);
+                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, n, ps);
+                if (p.gate) copy8<IO, VEC>(mine + at + (K + k) * line, g + tpr * k * kBi, n, ps);
             }
         }
         cp_commit();
@@ -139,9 +195,9 @@ block_norm_kernel(BlockNormParams p, int stages) {
     float2 wp[K][4], ws[K][4];  // w_pre; scale w_post
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (tx + tpr * k) * 8, n = min(8, p.D - c);
-        weights<VEC>(p.w_pre, c, n, wp[k]);
-        post_weights<VEC>(p, c, n, ws[k]);
+        const int c = cx + tpr * k * 8, n = p.D - c;
+        weights<VEC>(p.w_pre, c, n, ps, wp[k]);
+        post_weights<VEC>(p, c, n, ps, ws[k]);
     }
     for (; row < p.rows; row += step) {
         if (stages == 2) {
@@ -151,7 +207,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
             copy(row, 0);
             cp_wait<0>();
         }
-        const long long base = row * p.D + tx * 8;
+        const long long base = row * p.D + cx;
         float inv = 1.f;
         if (p.o && p.w_post) {
             float2 s2 = dup(0.f);
@@ -169,7 +225,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
         float2 r[K][4], s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int n = min(8, p.D - (tx + tpr * k) * 8);
+            const int n = p.D - cx - tpr * k * 8;
             read8<SIO>(mine_s + at + k * line_s, r[k]);
             if (p.o) {
                 float2 o[4];
@@ -185,7 +241,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
                     const float2 v = __ffma2_rn(ws[k][j], __fmul2_rn(o[j], dup(inv)), r[k][j]);
                     r[k][j] = make_float2(round_io<SIO>(v.x), round_io<SIO>(v.y));  // as it is stored
                 }
-                store8<SIO, VEC>(static_cast<char *>(p.r_out) + (base + tpr * k * 8) * kEs, n, r[k]);
+                store8<SIO, VEC>(static_cast<char *>(p.r_out) + (base + tpr * k * 8) * kEs, n, ps, r[k]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(r[k][j], r[k][j], s2);
@@ -197,7 +253,7 @@ block_norm_kernel(BlockNormParams p, int stages) {
         for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[k][j] = __fmul2_rn(__fmul2_rn(r[k][j], inv2), wp[k][j]);
-            store8<IO, VEC>(static_cast<char *>(p.n) + (base + tpr * k * 8) * kEi, min(8, p.D - (tx + tpr * k) * 8), r[k]);
+            store8<IO, VEC>(static_cast<char *>(p.n) + (base + tpr * k * 8) * kEi, p.D - cx - tpr * k * 8, ps, r[k]);
         }
         if (!(p.o && p.w_post) && blockDim.x > 32) __syncthreads();  // one reduction per row only: its slot is free again
         if (stages == 2) at = stage - at;
@@ -216,6 +272,7 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
     __shared__ float red[2][3][32];
     constexpr int kEi = Eight<IO>::kEs, kEs = Eight<SIO>::kEs, kBi = Eight<IO>::kBytes, kBs = Eight<SIO>::kBytes;
     const int tx = threadIdx.x, tpr = blockDim.x, nthr = blockDim.x * blockDim.y;
+    const int cx = tx * (VEC ? 8 : 2), ps = VEC ? 2 : 2 * tpr;  // the first element of unit 0; from pair to pair
     const long long chunk = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     if (chunk >= p.chunks) return;  // blockDim.y > 1 only for rows of one warp
     const bool seq_gate = p.gate && p.rows_per_gate > 1;
@@ -233,18 +290,18 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
     const int line = nthr * kBi, line_s = nthr * kBs, stage = nthr * S::kPerThread;
     auto copy = [&](long long row, int at) {
         if (row < r1) {
-            const long long base = row * p.D + tx * 8, gbase = p.gate ? row / p.rows_per_gate * p.D + tx * 8 : 0;
+            const long long base = row * p.D + cx, gbase = p.gate ? row / p.rows_per_gate * p.D + cx : 0;
             const char *r = static_cast<const char *>(p.r_out) + base * kEs, *n = static_cast<const char *>(p.dn) + base * kEi,
                        *o = static_cast<const char *>(p.o) + base * kEi, *d = static_cast<const char *>(p.dr_out) + base * kEs,
                        *g = static_cast<const char *>(p.gate) + gbase * kEi;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int nv = min(8, p.D - (tx + tpr * k) * 8);
-                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, nv);
-                copy8<IO, VEC>(mine + at + (K + k) * line, n + tpr * k * kBi, nv);
-                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, nv);
-                if (WHOLE && p.dr_out) copy8<SIO, VEC>(mine_s + at + (K + k) * line_s, d + tpr * k * kBs, nv);
-                if (WHOLE && p.gate) copy8<IO, VEC>(mine + at + (2 * K + k) * line, g + tpr * k * kBi, nv);
+                const int nv = p.D - cx - tpr * k * 8;
+                copy8<SIO, VEC>(mine_s + at + k * line_s, r + tpr * k * kBs, nv, ps);
+                copy8<IO, VEC>(mine + at + (K + k) * line, n + tpr * k * kBi, nv, ps);
+                if (p.o) copy8<IO, VEC>(mine + at + k * line, o + tpr * k * kBi, nv, ps);
+                if (WHOLE && p.dr_out) copy8<SIO, VEC>(mine_s + at + (K + k) * line_s, d + tpr * k * kBs, nv, ps);
+                if (WHOLE && p.gate) copy8<IO, VEC>(mine + at + (2 * K + k) * line, g + tpr * k * kBi, nv, ps);
             }
         }
         cp_commit();
@@ -254,11 +311,11 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
     float2 acc1[K][4], acc2[K][4], wp[K][4], ws[K][4];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (tx + tpr * k) * 8, n = min(8, p.D - c);
+        const int c = cx + tpr * k * 8, n = p.D - c;
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc1[k][j] = acc2[k][j] = dup(0.f);
-        weights<VEC>(p.w_pre, c, n, wp[k]);
-        post_weights<VEC>(p, c, n, ws[k]);
+        weights<VEC>(p.w_pre, c, n, ps, wp[k]);
+        post_weights<VEC>(p, c, n, ps, ws[k]);
     }
     const float inv_d = 1.f / (float)p.D;
     for (long long row = r0; row < r1; ++row) {
@@ -269,7 +326,7 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
             copy(row, 0);
             cp_wait<0>();
         }
-        const long long base = row * p.D + tx * 8;
+        const long long base = row * p.D + cx;
         float2 s0 = dup(0.f), s1 = dup(0.f), s2 = dup(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {  // zeros past the row's end
@@ -294,20 +351,20 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
         float2 t2 = dup(0.f), u[K][4];  // u . o
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (tx + tpr * k) * 8, nv = min(8, p.D - c);
+            const int c = cx + tpr * k * 8, nv = p.D - c;
             const long long to = base + tpr * k * 8;
             float2 dr[4], r[4], n[4];
             read8<SIO>(mine_s + at + k * line_s, r);
             read8<IO>(mine + at + (K + k) * line, n);
             if (WHOLE && p.dr_out) read8<SIO>(mine_s + at + (K + k) * line_s, dr);
-            else load8<SIO, VEC>(p.dr_out, to, nv, dr);  // zeros when absent
+            else load8<SIO, VEC>(p.dr_out, to, nv, ps, dr);  // zeros when absent
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // dr = (v - r' inv2^2 mean(v r')) inv2 + dr_out
                 const float2 v = __ffma2_rn(r[j], dup(-m2), __fmul2_rn(n[j], wp[k][j]));
                 dr[j] = __ffma2_rn(v, dup(inv2), dr[j]);
                 acc2[k][j] = __ffma2_rn(n[j], __fmul2_rn(r[j], dup(inv2)), acc2[k][j]);
             }
-            store8<SIO, VEC>(static_cast<char *>(p.dr) + to * kEs, nv, dr);
+            store8<SIO, VEC>(static_cast<char *>(p.dr) + to * kEs, nv, ps, dr);
             if (!p.o) continue;
             float2 o[4];
             read8<IO>(mine + at + k * line, o);
@@ -320,10 +377,10 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
                 if (!seq_gate) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(r[j], ws[k][j]);
-                    store8<IO, VEC>(static_cast<char *>(p.dgate) + to * kEi, nv, n);
+                    store8<IO, VEC>(static_cast<char *>(p.dgate) + to * kEi, nv, ps, n);
                 }
                 if (WHOLE) read8<IO>(mine + at + (2 * K + k) * line, n);
-                else load8<IO, VEC>(p.gate, row / p.rows_per_gate * p.D + c, nv, n);
+                else load8<IO, VEC>(p.gate, row / p.rows_per_gate * p.D + c, nv, ps, n);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     u[k][j] = __fmul2_rn(u[k][j], n[j]);
@@ -346,7 +403,7 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
                 read8<IO>(mine + at + k * line, o);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = __fmul2_rn(__ffma2_rn(o[j], dup(-m), u[k][j]), dup(inv));
-                store8<IO, VEC>(static_cast<char *>(p.d_o) + (base + tpr * k * 8) * kEi, min(8, p.D - (tx + tpr * k) * 8), o);
+                store8<IO, VEC>(static_cast<char *>(p.d_o) + (base + tpr * k * 8) * kEi, p.D - cx - tpr * k * 8, ps, o);
             }
         } else if (blockDim.x > 32) {
             __syncthreads();  // the slot of the sums is free again
@@ -358,7 +415,7 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = (tx + tpr * k) * 8 + j;
+            const int c = cx + tpr * k * 8 + j / 2 * ps + j % 2;
             if (c < p.D) {
                 part[c] = j & 1 ? acc1[k][j / 2].y : acc1[k][j / 2].x;
                 part[p.D + c] = j & 1 ? acc2[k][j / 2].y : acc2[k][j / 2].x;

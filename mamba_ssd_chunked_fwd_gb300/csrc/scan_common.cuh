@@ -246,16 +246,82 @@ __device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
                  "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async4_if(bool ok, void *dst, const void *src, int bytes) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %3, 0;\n\t@q cp.async.ca.shared.global [%0], [%1], 4, %2;\n\t}" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes), "r"((int)ok) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// A pair of floats as 16-bit elements.
+template <int IO>
+__device__ __forceinline__ uint32_t pack16(float2 v) {
+    if (IO == IO_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t *>(&a);
+    }
+    const __half2 a = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&a);
+}
+
+// Eight 16-bit elements at any address, of which the first n exist, into shared memory:
+// pairs from a 4-byte boundary are copied asynchronously; off it there is no
+// asynchronous form, and the first element, the pairs after it and the last element
+// are loaded, all at once, and stored.  Predicates, no branch: the loads of several calls overlap.
+// The scan of [8,4096,D,16] at D = 4094 and 4095: 958 and 1338 us (1380 both with eight loads
+// of an element each; 692 with whole chunks at D = 4096); gradients of [4,2048,D,16]: 1082
+// and 1205 (1171 both; 822).
+__device__ __forceinline__ void copy_any16(void *dst, const char *src, int n) {
+    const bool even = (reinterpret_cast<size_t>(src) & 3) == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int bytes = min(max(2 * (n - 2 * j), 0), 4);
+        cp_async4_if(even, static_cast<char *>(dst) + 4 * j, bytes > 0 ? src + 4 * j : nullptr, bytes);
+    }
+    const int m = even ? 0 : n;
+    uint16_t first = 0, last = 0;
+    uint32_t pair[5] = {0, 0, 0, 0, 0};  // pair[j]: elements 2 j - 1 and 2 j
+    ldg_u16(first, src, m > 0);
+    ldg_u16(last, src + 2 * (m - 1), m > 0 && !(m & 1));
+#pragma unroll
+    for (int j = 1; j < 4; ++j) ldg_u32(pair[j], src + 4 * j - 2, m > 2 * j);
+    pair[0] = (uint32_t)first << 16;
+#pragma unroll
+    for (int j = 1; j <= 4; ++j)
+        if (m == 2 * j) pair[j] = last;
+    if (!even)
+        *static_cast<uint4 *>(dst) = make_uint4(__byte_perm(pair[0], pair[1], 0x5432), __byte_perm(pair[1], pair[2], 0x5432),
+                                                __byte_perm(pair[2], pair[3], 0x5432), __byte_perm(pair[3], pair[4], 0x5432));
+}
+// The same elements, in pairs of floats, to any address.
+template <int IO>
+__device__ __forceinline__ void store_any16(char *dst, int n, const float2 *v) {
+    uint32_t w[5];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack16<IO>(v[j]);
+    w[4] = 0;
+    if ((reinterpret_cast<size_t>(dst) & 3) == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (2 * j + 1 < n) *reinterpret_cast<uint32_t *>(dst + 4 * j) = w[j];
+            else if (2 * j < n) *reinterpret_cast<uint16_t *>(dst + 4 * j) = (uint16_t)w[j];
+        }
+    } else {
+        if (n > 0) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)w[0];
+#pragma unroll
+        for (int j = 1; j <= 4; ++j) {
+            if (2 * j < n) *reinterpret_cast<uint32_t *>(dst + 4 * j - 2) = __byte_perm(w[j - 1], w[j], 0x5432);
+            else if (2 * j - 1 < n) *reinterpret_cast<uint16_t *>(dst + 4 * j - 2) = (uint16_t)(w[j - 1] >> 16);
+        }
+    }
+}
+
 // One 16-byte chunk of a row (8 or 4 elements, of which the first n exist) into
 // shared memory.  VEC: the chunk is aligned and whole (n is all or none).  fp32
-// of any alignment goes element by element, still asynchronously; unaligned
-// 16-bit elements have no asynchronous form and are loaded, all at once, and stored.
+// of any alignment goes element by element, still asynchronously.
 template <int IO, bool VEC>
 __device__ __forceinline__ void copy_chunk(void *dst, const char *src, int n) {
     if (VEC) {
@@ -264,16 +330,7 @@ __device__ __forceinline__ void copy_chunk(void *dst, const char *src, int n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) cp_async4(static_cast<float *>(dst) + j, j < n ? src + 4 * j : nullptr, j < n ? 4 : 0);
     } else {
-        uint16_t e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            e[j] = 0;
-            ldg_u16(e[j], src + 2 * j, j < n);
-        }
-        uint4 u;
-        u.x = e[0] | ((uint32_t)e[1] << 16); u.y = e[2] | ((uint32_t)e[3] << 16);
-        u.z = e[4] | ((uint32_t)e[5] << 16); u.w = e[6] | ((uint32_t)e[7] << 16);
-        *static_cast<uint4 *>(dst) = u;
+        copy_any16(dst, src, n);
     }
 }
 
@@ -338,7 +395,6 @@ __device__ __forceinline__ void read_chunk(const void *src, float2 *v) {
 // A chunk's values to global memory, the first n of them (VEC: all, aligned).
 template <int IO, bool VEC>
 __device__ __forceinline__ void store_chunk(char *dst, int n, const float2 *v) {
-    constexpr int kPairs = IO == IO_F32 ? 2 : 4;
     if (n <= 0) return;
     if (VEC) {
         uint4 u;
@@ -356,9 +412,11 @@ __device__ __forceinline__ void store_chunk(char *dst, int n, const float2 *v) {
             }
         }
         *reinterpret_cast<uint4 *>(dst) = u;
+    } else if (IO != IO_F32) {
+        store_any16<IO>(dst, n, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
+        for (int i = 0; i < 2; ++i) {
             if (2 * i < n) st_io<IO>(dst, 2 * i, v[i].x);
             if (2 * i + 1 < n) st_io<IO>(dst, 2 * i + 1, v[i].y);
         }
