@@ -446,9 +446,16 @@ block_norm_sum_kernel(BlockNormParams p) {
                 s1 = fmaf(ld_io<IO>(p.gate, (size_t)(gi * p.D + c)), s, s1);
             }
         } else {
-            for (long long q = threadIdx.y; q < p.chunks; q += 32) {
-                s1 += p.part[q * 2 * p.D + c];
-                s2 += p.part[(q * 2 + 1) * p.D + c];
+            for (long long q = threadIdx.y; q < p.chunks; q += 128) {  // four rows' loads together
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool ok = q + 32 * j < p.chunks;
+                    v[j] = ok ? p.part[(q + 32 * j) * 2 * p.D + c] : 0.f;
+                    v[4 + j] = ok ? p.part[((q + 32 * j) * 2 + 1) * p.D + c] : 0.f;
+                }
+                s1 += (v[0] + v[1]) + (v[2] + v[3]);
+                s2 += (v[4] + v[5]) + (v[6] + v[7]);
             }
         }
     }
