@@ -14,6 +14,9 @@
 // one row run beside the reductions and stores of the one before, need no
 // registers, and every tensor moves once.  The weights, and backwards the two column
 // sums, stay in registers over the rows that the threads walk.
+// Measured: [8,4096,2048], bf16 with an fp32 stream and a gate per sequence, 141 us (5.7 TB/s,
+// 84 % of the copy rate); backwards [4,2048,2048] in bf16 with a gate per token 59 us
+// (4.6 TB/s), 9 of them the sum over the 586 partial rows: 16 warps per SM, registers bound.
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -479,7 +482,8 @@ dim3 row_block(int D, int K) {
 }
 
 // Units per thread: two, but one for rows that a warp takes so, and backwards four for rows past 8192,
-// whose registers would not allow more threads; wider rows take more warps.
+// whose registers would not allow more threads; wider rows take more warps.  Rows of 256 with one
+// unit and two: 148 and 154 us (262144 rows); rows of 2048 with one, two and four: 132, 134 and 138.
 int norm_k(int D, bool backward) { return D <= 256 ? 1 : backward && D > 8192 ? 4 : 2; }
 
 constexpr int kNormSmem = 227 * 1024 - 1024;  // the most a CTA may hold, less the sums
@@ -540,6 +544,7 @@ cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
         case 1: return launch_norm_bwd_as<IO, SIO, 1, 128, true>(p, s);
         case 2: return p.D <= 2048 ? launch_norm_bwd_as<IO, SIO, 2, 128, true>(p, s) : launch_norm_bwd_as<IO, SIO, 2, 512, true>(p, s);
         // 512 threads' whole slots: 160 KB of 16-bit tensors, too much with fp32 ones
+        // (2048 rows of 10240: 168 us whole, 201 not)
         default: return launch_norm_bwd_as<IO, SIO, 4, 512, IO != IO_F32 && SIO != IO_F32>(p, s);
     }
 }
@@ -547,6 +552,7 @@ cudaError_t launch_norm_bwd_io(const BlockNormParams &p, cudaStream_t s) {
 }  // namespace
 
 // Chunks for about 16 warps per SM, two at least; a chunk never spans two gates of several rows.
+// (8192 rows of 2048: 66 us with eight warps, 64 with 16, 70 with 32.)
 void block_norm_chunks(BlockNormParams &p) {
     const int warps = row_block(p.D, norm_k(p.D, true)).x / 32;
     const long long target = (warps < 8 ? 16 / warps : 2) * (long long)scan_sm_count();

@@ -69,8 +69,8 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
 // by few CTAs is cut until there are CTAs for the SMs.  The cut costs a first walk
 // (each segment's state from zero, 0.65 of the forward's time; backwards as many CTAs
 // again walk for the adjoint), a fold over the segments, whose states move four times, and
-// two launches.  Unit: the token of a CTA alone; measured from 128 to 16384 tokens,
-// the choice is within 5% of the best of 1 to 128 segments.
+// two launches.  Unit: the token of a CTA alone.  Uncut and cut by this rule: [1,16384,2048,16]
+// 1571 and 278 us, gradients of [2,333,328,8] 121 and 32; where the SMs are full, nothing is cut.
 void choose_segments(ssd::ScanParams &p, bool backward) {
     const int lanes = ssd::scan_lanes(p.N);
     const int dc = 4 * (32 / lanes) * 4;

@@ -21,6 +21,12 @@
 // Segments.  With few rows and channels the sequence is cut: a first walk gives
 // each segment's state from zero and its sum of d, a fold over the segments
 // gives every segment's entering state, then all segments are walked at once.
+// Measured in bf16 with the gate: [8,4096,4096,16] 690 us, 194e9 channel-tokens/s (1.6 TB/s
+// of tensors, 23 % of the copy rate; its exponentials alone take 230 us, with the packed
+// multiply-adds and the sums of y about 410); 256 CTAs fill 84 % of the 304 places.
+// [1,16384,2048,16] cut into segments 275 us (1571 uncut: 16 CTAs); three fp32 rows of
+// 517 tokens and 202 channels 16.5 us (68 uncut).
+// Tried and slower: 8 side warps, CTAs of one or two walk warps, eight states per lane.
 #include "scan_common.cuh"
 
 namespace ssd {

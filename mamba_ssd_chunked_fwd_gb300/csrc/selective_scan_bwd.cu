@@ -22,6 +22,10 @@
 // and over the channel tiles in a second kernel, each in a fixed order.
 // Walk and side warps as in the forward: the side warps stage d, d x, ds, B and
 // C of the next tile and turn the previous tile's sums into dx, ddt and dz.
+// Measured: [4,2048,4096,16] in bf16 with the gate 821 us (41e9 channel-tokens/s, the
+// checkpoint walk included; its bytes alone would take 70 us, its exponentials 115),
+// [4,2048,1024,64] 930 us; [2,333,328,8] in fp32, cut into segments, 32 us in five
+// dependent launches (120 uncut).
 #include "scan_common.cuh"
 
 namespace ssd {
