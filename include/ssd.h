@@ -416,6 +416,8 @@ ssd_status ssd_gated_rmsnorm(int64_t rows, int64_t D, int64_t groups, float eps,
  * x, dt, z, Bm and Cm are read through strides: element (b, t, i) is at
  * b * stride[0] + t * stride[1] + i, strides in elements, both zero meaning
  * dense.  So slices of a projection's output are read in place.  y is dense.
+ * final_state must not overlap initial_state; y may be x, z or dt itself where
+ * that is dense and of y's type, and overlaps no input otherwise.
  * Every dim > 0, N <= 128, D % G == 0.  fp32 arithmetic and states.  No
  * alignment is required beyond the types' own.
  * A sequence is cut into segments walked in parallel when B and D alone do not
@@ -519,9 +521,9 @@ ssd_status ssd_selective_scan_step(const ssd_scan_step_args *args, void *stream)
  * where v is x from token 0 on and the row's initial_state before it:
  * v[b,-(W-1)+j] = initial_state[b,j] (zeros when NULL).  final_state holds the
  * last W-1 entries of v, what the next call of the same sequence starts from.
- *   x [B,L,C] dtype, strided like the scan's; y [B,L,C] dense
+ *   x [B,L,C] dtype, strided like the scan's; y [B,L,C] dense, not overlapping x
  *   w [C,W] fp32, 1 <= W <= 8; bias [C] fp32 or NULL
- *   initial_state, final_state [B,W-1,C] dtype (optional)
+ *   initial_state, final_state [B,W-1,C] dtype (optional), not overlapping each other
  *   lengths [B] int32, device (optional): as for the scan
  */
 typedef struct {

@@ -39,6 +39,14 @@ bool strides_of(const int64_t (&in)[2], int64_t L, int64_t width, long long (&ou
     return in[0] >= 0 && in[1] >= 0;
 }
 
+size_t element(int32_t dtype) { return dtype == SSD_F32 ? 4 : 2; }
+
+// Whether two ranges of memory share bytes (an absent one shares none).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x && y && x < y + nb && y < x + na;
+}
+
 ssd_status check_limit(float dt_min, float dt_max) {
     if (isnan(dt_min) || isnan(dt_max) || !(dt_min <= dt_max))
         return fail(SSD_ERR_INVALID_ARG, "dt_limit must satisfy dt_min <= dt_max");
@@ -228,6 +236,9 @@ ssd_status ssd_selective_scan(const ssd_scan_args *a, void *stream) {
     if (!a->y) return fail(SSD_ERR_INVALID_ARG, "y is required");
     ssd::ScanParams p = {};
     if ((st = make_scan(a, p)) != SSD_OK) return st;
+    const size_t state = (size_t)a->B * a->D * a->N * 4;
+    if (overlap(a->initial_state, state, a->final_state, state))
+        return fail(SSD_ERR_INVALID_ARG, "final_state must not overlap initial_state");
     choose_segments(p, false);
     const ScanLayout l = scan_layout(p);
     if ((st = check_workspace(a->workspace, a->workspace_bytes, l.total)) != SSD_OK) return st;
@@ -324,6 +335,13 @@ ssd_status ssd_causal_conv_carry(const ssd_conv_args *a, void *stream) {
     ssd_status st = check_conv(a, p);
     if (st != SSD_OK) return st;
     if (!a->x || !a->w || !a->y) return fail(SSD_ERR_INVALID_ARG, "x, w and y are required");
+    // a thread reads the tokens before its run, which another one writes
+    const size_t es = element(a->dtype), state = (size_t)a->B * (a->W - 1) * a->C * es;
+    const size_t read = ((size_t)(a->B - 1) * p.xs[0] + (size_t)(a->L - 1) * p.xs[1] + a->C) * es;
+    if (overlap(a->x, read, a->y, (size_t)a->B * a->L * a->C * es))
+        return fail(SSD_ERR_INVALID_ARG, "y must not overlap x");
+    if (overlap(a->initial_state, state, a->final_state, state))
+        return fail(SSD_ERR_INVALID_ARG, "final_state must not overlap initial_state");
     cudaError_t e = ssd::launch_conv(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "causal_conv_carry");
     return ok();

@@ -469,3 +469,23 @@ def test_example_runs_them_together():
     # bf16 activations: a few roundings of 2^-8 each per layer apart
     assert drift < 4 * 2.0 ** -8
     assert losses[-1] < losses[0]
+
+
+@pytest.mark.parametrize("shape", [(1, 700, 96), (4, 130, 4096), (2, 65, 33)])
+@pytest.mark.parametrize("name", ["x", "dt", "z"])
+def test_scan_over_its_own_input(shape, name):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    B, L, D = shape
+    t = {n: torch.randn(shape, generator=gen, device="cuda").bfloat16() for n in ("x", "dt", "z")}
+    A = -torch.rand(D, 16, generator=gen, device="cuda")
+    bc = [torch.randn(B, L, 1, 16, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    want = ssd().selective_scan(t["x"], t["dt"], A, *bc, dt_softplus=True, z=t["z"])
+    got = ssd().selective_scan(t["x"], t["dt"], A, *bc, dt_softplus=True, z=t["z"], out=t[name])
+    assert got.data_ptr() == t[name].data_ptr()
+    assert torch.equal(got, want)
+
+
+def test_conv_refuses_its_own_input_as_output():
+    x = torch.randn(2, 40, 64, device="cuda")
+    with pytest.raises(Exception, match="overlap"):
+        ssd().causal_conv1d_carry(x, torch.ones(64, 4, device="cuda"), out=x)

@@ -276,3 +276,16 @@ def test_plain_gradients_against_differences():
             return sum((o * u).sum() for o, u in zip(f(**{**k, n: k[n] + s * 1e-6 * v}), w))
         slope = (value(1) - value(-1)) / 2e-6
         torch.testing.assert_close((grads[n] * v).sum(), slope, rtol=1e-6, atol=1e-8)
+
+
+@pytest.mark.parametrize("x,x_stride,y,code", [(FAKE, (0, 0), FAKE, 1), (FAKE, (0, 0), FAKE + 2 * 64 * 32 * 4 - 4, 1),
+                                               (FAKE, (128 * 64, 64), FAKE + (128 * 64 + 63 * 64 + 32) * 4 - 4, 1),
+                                               (FAKE + 2 * 64 * 32 * 4 - 4, (0, 0), FAKE, 1)])
+def test_conv_refuses_its_own_input_as_output(x, x_stride, y, code):
+    assert call("ssd_causal_conv_carry", conv_args(x=x, x_stride=x_stride, y=y)) == code
+
+
+@pytest.mark.parametrize("off", [0, 4, -4])
+def test_carried_states_must_not_overlap(off):
+    assert call("ssd_selective_scan", scan_args(initial_state=FAKE, final_state=FAKE + off)) == 1
+    assert call("ssd_causal_conv_carry", conv_args(y=2 * FAKE, initial_state=FAKE, final_state=FAKE + off)) == 1
