@@ -16,7 +16,8 @@
 // sums, stay in registers over the rows that the threads walk.
 // Measured: [8,4096,2048], bf16 with an fp32 stream and a gate per sequence, 141 us (5.7 TB/s,
 // 84 % of the copy rate); backwards [4,2048,2048] in bf16 with a gate per token 59 us
-// (4.6 TB/s), 9 of them the sum over the 586 partial rows: 16 warps per SM, registers bound.
+// (4.6 TB/s): 16 warps per SM, registers bound.  A gate per sequence: 58 us (80 while one thread per column
+// summed a gate's partial rows; one sequence of 500 rows 25 and 109).
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -426,53 +427,75 @@ block_norm_bwd_kernel(BlockNormParams p, int stages) {
         }
 }
 
-// The column sums over the chunks, in a fixed order: 32 interleaved sums per column, then those in turn.
+// The column sums over the chunks, in a fixed order: 64 interleaved sums per column,
+// then those over a warp.  16 columns per CTA, so that 2048 of them reach 128 SMs.
+// With fewer than 64 gates of several rows, the threads of a column share a gate's chunks.
+constexpr int kSumX = 16, kSumY = 64;
+
+// Rows q0, q0 + step, .. below q1 of the partial sums, four rows' loads together.
+__device__ __forceinline__ void sum_chunks(const BlockNormParams &p, int c, long long q0, long long q1, int step, float &s1,
+                                           float &s2) {
+    for (long long q = q0; q < q1; q += 4 * step) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool ok = q + step * j < q1;
+            v[j] = ok ? p.part[(q + step * j) * 2 * p.D + c] : 0.f;
+            v[4 + j] = ok ? p.part[((q + step * j) * 2 + 1) * p.D + c] : 0.f;
+        }
+        s1 += (v[0] + v[1]) + (v[2] + v[3]);
+        s2 += (v[4] + v[5]) + (v[6] + v[7]);
+    }
+}
+
 template <int IO>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kSumX * kSumY)
 block_norm_sum_kernel(BlockNormParams p) {
-    __shared__ float red[2][32][33];
+    __shared__ float red[2][kSumY][kSumX + 1];
     tc::pdl_wait();
-    const int c = blockIdx.x * 32 + threadIdx.x;
-    const bool seq_gate = p.gate && p.rows_per_gate > 1, in = c < p.D;
-    const float wpost = in && p.w_post ? __ldg(p.w_post + c) : 1.f, scale = in && p.scale ? __ldg(p.scale + c) : 1.f;
+    const int x = threadIdx.x, y = threadIdx.y, c = blockIdx.x * kSumX + x;
+    const bool in = c < p.D;
     float s1 = 0.f, s2 = 0.f;
-    if (in) {
-        if (seq_gate) {
-            const long long per = (p.rows_per_gate + p.chunk_rows - 1) / p.chunk_rows, gates = p.rows / p.rows_per_gate;
-            for (long long gi = threadIdx.y; gi < gates; gi += 32) {
-                float s = 0.f;
-                for (long long q = gi * per; q < (gi + 1) * per; ++q) {
-                    s += p.part[q * 2 * p.D + c];
-                    s2 += p.part[(q * 2 + 1) * p.D + c];
-                }
-                st_io<IO>(p.dgate, (size_t)(gi * p.D + c), s * (wpost * scale));
+    if (p.gate && p.rows_per_gate > 1) {
+        const long long per = (p.rows_per_gate + p.chunk_rows - 1) / p.chunk_rows, gates = p.rows / p.rows_per_gate;
+        int split = 1;  // threads per gate
+        while (2 * split * gates <= kSumY) split *= 2;
+        const int sub = y % split;
+        const float w = in ? (p.w_post ? __ldg(p.w_post + c) : 1.f) * (p.scale ? __ldg(p.scale + c) : 1.f) : 0.f;
+        for (long long g0 = 0; g0 < gates; g0 += kSumY / split) {  // more than once only with a thread per gate
+            const long long gi = g0 + y / split;
+            float s = 0.f;
+            if (in && gi < gates) sum_chunks(p, c, gi * per + sub, (gi + 1) * per, split, s, s2);
+            if (split > 1) {
+                red[0][y][x] = s;
+                __syncthreads();
+                if (sub == 0)
+                    for (int k = 1; k < split; ++k) s += red[0][y + k][x];
+                __syncthreads();
+            }
+            if (in && gi < gates && sub == 0) {
+                st_io<IO>(p.dgate, (size_t)(gi * p.D + c), s * w);
                 s1 = fmaf(ld_io<IO>(p.gate, (size_t)(gi * p.D + c)), s, s1);
             }
-        } else {
-            for (long long q = threadIdx.y; q < p.chunks; q += 128) {  // four rows' loads together
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool ok = q + 32 * j < p.chunks;
-                    v[j] = ok ? p.part[(q + 32 * j) * 2 * p.D + c] : 0.f;
-                    v[4 + j] = ok ? p.part[((q + 32 * j) * 2 + 1) * p.D + c] : 0.f;
-                }
-                s1 += (v[0] + v[1]) + (v[2] + v[3]);
-                s2 += (v[4] + v[5]) + (v[6] + v[7]);
-            }
         }
+    } else if (in) {
+        sum_chunks(p, c, y, p.chunks, kSumY, s1, s2);
     }
-    red[0][threadIdx.y][threadIdx.x] = s1;
-    red[1][threadIdx.y][threadIdx.x] = s2;
+    red[0][y][x] = s1;
+    red[1][y][x] = s2;
     __syncthreads();
-    if (threadIdx.y != 0 || !in) return;
-    for (int y = 1; y < 32; ++y) {
-        s1 += red[0][y][threadIdx.x];
-        s2 += red[1][y][threadIdx.x];
+    // a warp per column and sum
+    const int lane = (y * kSumX + x) & 31, job = (y * kSumX + x) >> 5, which = job / kSumX, col = blockIdx.x * kSumX + job % kSumX;
+    float s = red[which][lane][job % kSumX] + red[which][lane + 32][job % kSumX];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane != 0 || col >= p.D) return;
+    if (which == 1) {
+        p.dw_pre[col] = s;
+        return;
     }
-    p.dw_pre[c] = s2;
-    if (p.dw_post) p.dw_post[c] = scale * s1;
-    if (p.dscale) p.dscale[c] = wpost * s1;
+    if (p.dw_post) p.dw_post[col] = (p.scale ? __ldg(p.scale + col) : 1.f) * s;
+    if (p.dscale) p.dscale[col] = (p.w_post ? __ldg(p.w_post + col) : 1.f) * s;
 }
 
 // Threads of a row and rows of a CTA for K units of eight elements per thread.
@@ -535,7 +558,7 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_kernel(true, block_norm_sum_kernel<IO>, dim3((p.D + 31) / 32), dim3(32, 32), 0, s, p);
+    return launch_kernel(true, block_norm_sum_kernel<IO>, dim3((p.D + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, s, p);
 }
 
 template <int IO, int SIO>
