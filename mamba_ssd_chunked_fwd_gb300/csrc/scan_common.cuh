@@ -673,5 +673,9 @@ inline int scan_lanes(int64_t N) {
     while (l * 4 < N) l *= 2;
     return l;
 }
+// Warps of a CTA of the forward's walk.  With two lanes per channel, two: four would hand
+// the four side warps 128 channels, and those would be what the walk waits for ([8,4096,4096,N] in
+// bf16 at N = 8 and 4: 529 and 812 us with two, 668 and 1166 with four).
+constexpr int scan_walk_warps(int lanes) { return lanes == 2 ? 2 : 4; }
 
 }  // namespace ssd

@@ -13,7 +13,7 @@
 // clocks of the SM's 128-byte path) serves 16 state updates, and the packed fp32
 // operations take two states per issue slot.  y is summed over the LPC lanes by
 // halving exchanges.
-// Roles.  A CTA is 4 walk warps (the recurrence) and 4 side warps: these load x,
+// Roles.  A CTA is 4 walk warps (the recurrence; 2 where N <= 8) and 4 side warps: these load x,
 // dt, B and C of the next tile, compute d and d x into shared memory, and
 // finish the previous tile (Dskip x, the gate, the store), so memory latency, the
 // softplus and the gate run beside the recurrence.  One barrier per tile; two
@@ -41,12 +41,13 @@ enum WalkMode {
     WALK_BOTH = 4   // WALK_SEG and WALK_ADJ of every segment that needs them, in one launch
 };
 
-constexpr int kWalkWarps = 4, kSideThreads = 128, kWalkThreads = kWalkWarps * 32 + kSideThreads;
+constexpr int kSideThreads = 128;
 
 // Four states of four channels per lane: LPC = N / 4 lanes hold a channel.
 template <int IO, int LPC>
 struct WalkShape {
     static constexpr int kGroups = 32 / LPC;              // channel quads per warp
+    static constexpr int kWalkWarps = scan_walk_warps(LPC), kThreads = kWalkWarps * 32 + kSideThreads;
     static constexpr int kDc = kWalkWarps * kGroups * 4;  // channels per CTA
     static constexpr int kNp = LPC * 4;
     // tokens per tile: fp32 tiles are half as long, so that two CTAs' rings fit an SM
@@ -133,7 +134,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     const int nt = (ntok + kT - 1) / kT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (warp < kWalkWarps) {
+    if (warp < S::kWalkWarps) {
         const int ln = lane % LPC, ch0 = (warp * S::kGroups + lane / LPC) * 4, n0 = ln * 4;
         float2 h[4][kH], a2[4][kH];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -247,7 +248,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
     // ---- side warps.  Every chunk is copied, staged and finished by one thread,
     // so its copies need no barrier but the thread's own wait, and every tensor
     // is walked by one pointer and one stride.
-    const int ta = threadIdx.x - kWalkWarps * 32;
+    const int ta = threadIdx.x - S::kWalkWarps * 32;
     const int q = ta % S::kChunks, tl0 = ta / S::kChunks;
     const int nv = min(S::kCh, nch - q * S::kCh);
     const int mine = nv > 0 && tl0 < kT ? ntok : 0;  // tokens for this thread
@@ -449,7 +450,7 @@ __device__ __forceinline__ void walk(const ScanParams &p, const int seg) {
 }
 
 template <int IO, int LPC, int MODE, bool VEC>
-__global__ void __launch_bounds__(kWalkThreads, 2)
+__global__ void __launch_bounds__((WalkShape<IO, LPC>::kThreads), 2)
 scan_walk_kernel(ScanParams p) {
     if (MODE == WALK_Y || MODE == WALK_CKPT) tc::pdl_wait();
     if (MODE != WALK_Y) tc::pdl_launch_dependents();
@@ -524,7 +525,7 @@ cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const bool after = (MODE == WALK_Y || MODE == WALK_CKPT) && p.nseg > 1;  // the cut's kernels
-    return launch_kernel(after, kernel, dim3(p.G * p.tiles, segs, p.B), kWalkThreads, bytes, s, p);
+    return launch_kernel(after, kernel, dim3(p.G * p.tiles, segs, p.B), WalkShape<IO, LPC>::kThreads, bytes, s, p);
 }
 
 template <int IO, int MODE>
