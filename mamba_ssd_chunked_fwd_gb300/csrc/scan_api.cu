@@ -81,7 +81,8 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
 // 1571 and 278 us, gradients of [2,333,328,8] 121 and 32; where the SMs are full, nothing is cut.
 void choose_segments(ssd::ScanParams &p, bool backward) {
     const int lanes = ssd::scan_lanes(p.N);
-    const int dc = (backward ? 4 : ssd::scan_walk_warps(lanes)) * (32 / lanes) * 4;  // backward: fitted on CTAs of four walk warps
+    // backwards the model was fitted on CTAs of four walk warps
+    const int dc = (backward ? 4 : ssd::scan_walk_warps(lanes)) * (32 / lanes) * 4;
     const double sms = ssd::scan_sm_count(), pair = 1.72;
     const double ctas = (double)p.B * p.G * ((p.D / p.G + dc - 1) / dc), state = (double)p.B * p.D * p.N;
     auto waves = [&](double k) {
