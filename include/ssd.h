@@ -416,8 +416,9 @@ ssd_status ssd_gated_rmsnorm(int64_t rows, int64_t D, int64_t groups, float eps,
  * x, dt, z, Bm and Cm are read through strides: element (b, t, i) is at
  * b * stride[0] + t * stride[1] + i, strides in elements, both zero meaning
  * dense.  So slices of a projection's output are read in place.  y is dense.
- * final_state must not overlap initial_state; y may be x, z or dt itself where
- * that is dense and of y's type, and overlaps no input otherwise.
+ * y may be x, z or dt itself where that is dense and of y's type.  Otherwise an
+ * output that overlaps an input (its range of memory, gaps between strided rows
+ * included) or the other output is refused.
  * Every dim > 0, N <= 128, D % G == 0.  fp32 arithmetic and states.  No
  * alignment is required beyond the types' own.
  * A sequence is cut into segments walked in parallel when B and D alone do not

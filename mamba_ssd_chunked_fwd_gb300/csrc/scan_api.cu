@@ -4,6 +4,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "scan_common.cuh"
 
 namespace {
@@ -41,10 +43,38 @@ bool strides_of(const int64_t (&in)[2], int64_t L, int64_t width, long long (&ou
 
 size_t element(int32_t dtype) { return dtype == SSD_F32 ? 4 : 2; }
 
-// Whether two ranges of memory share bytes (an absent one shares none).
+// Whether two ranges of memory share bytes (an absent or empty one shares none).
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x && y && x < y + nb && y < x + na;
+    return x && y && na && nb && x < y + nb && y < x + na;
+}
+
+// A tensor's range of memory, under the name that an error gives it.
+struct Span {
+    const void *p;
+    size_t bytes;
+    const char *what;
+};
+
+// An output must lie apart from tensors that other threads read while it is written, and from other outputs.
+ssd_status apart(const Span &out, std::initializer_list<Span> others) {
+    for (const Span &o : others)
+        if (overlap(out.p, out.bytes, o.p, o.bytes)) return fail(SSD_ERR_INVALID_ARG, "%s must not overlap %s", out.what, o.what);
+    return SSD_OK;
+}
+
+// What a [B,L,...] tensor reaches over through its strides; `st` as strides_of gives them.
+Span strided(const void *p, int64_t B, int64_t L, int64_t width, const long long (&st)[2], size_t es, const char *what) {
+    return {p, ((size_t)(B - 1) * st[0] + (size_t)(L - 1) * st[1] + width) * es, what};
+}
+
+// The same for a tensor of y's shape that y may replace: where it is dense, of y's type and
+// at y's address, an element is read by the thread that writes it, before it does, and nothing is left to compare.
+Span replaced(const void *y, int32_t y_dtype, const void *p, int32_t dtype, int64_t B, int64_t L, int64_t width,
+              const long long (&st)[2], const char *what) {
+    const bool dense = (B == 1 || st[0] == L * width) && (L == 1 || st[1] == width);
+    if (p == y && dtype == y_dtype && dense) return {nullptr, 0, what};
+    return strided(p, B, L, width, st, element(dtype), what);
 }
 
 ssd_status check_limit(float dt_min, float dt_max) {
@@ -237,9 +267,20 @@ ssd_status ssd_selective_scan(const ssd_scan_args *a, void *stream) {
     if (!a->y) return fail(SSD_ERR_INVALID_ARG, "y is required");
     ssd::ScanParams p = {};
     if ((st = make_scan(a, p)) != SSD_OK) return st;
-    const size_t state = (size_t)a->B * a->D * a->N * 4;
-    if (overlap(a->initial_state, state, a->final_state, state))
-        return fail(SSD_ERR_INVALID_ARG, "final_state must not overlap initial_state");
+    const size_t f = sizeof(float), es = element(a->x_dtype), state = (size_t)a->B * a->D * a->N * f, gn = a->G * a->N;
+    const Span y = {a->y, (size_t)a->B * a->L * a->D * es, "y"}, fin = {a->final_state, state, "final_state"};
+    const Span B = strided(a->Bm, a->B, a->L, gn, p.bs, es, "B"), C = strided(a->Cm, a->B, a->L, gn, p.cs, es, "C"),
+               A = {a->A, (size_t)a->D * a->N * f, "A"}, Dskip = {a->Dskip, a->D * f, "Dskip"},
+               bias = {a->dt_bias, a->D * f, "dt_bias"}, h0 = {a->initial_state, state, "initial_state"},
+               len = {a->lengths, a->B * sizeof(int32_t), "lengths"};
+    st = apart(y, {replaced(a->y, a->x_dtype, a->x, a->x_dtype, a->B, a->L, a->D, p.xs, "x"),
+                   replaced(a->y, a->x_dtype, a->dt, a->dt_dtype, a->B, a->L, a->D, p.dts, "dt"),
+                   replaced(a->y, a->x_dtype, a->z, a->x_dtype, a->B, a->L, a->D, p.zs, "z"), B, C, A, Dskip, bias, h0, len, fin});
+    if (st != SSD_OK) return st;
+    st = apart(fin, {strided(a->x, a->B, a->L, a->D, p.xs, es, "x"),
+                     strided(a->dt, a->B, a->L, a->D, p.dts, element(a->dt_dtype), "dt"),
+                     strided(a->z, a->B, a->L, a->D, p.zs, es, "z"), B, C, A, Dskip, bias, h0, len});
+    if (st != SSD_OK) return st;
     choose_segments(p, false);
     const ScanLayout l = scan_layout(p);
     if ((st = check_workspace(a->workspace, a->workspace_bytes, l.total)) != SSD_OK) return st;

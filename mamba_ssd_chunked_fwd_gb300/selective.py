@@ -241,7 +241,9 @@ def selective_scan(x, dt, A, B, C, dt_softplus=False, return_final_state=False, 
     [B,L,G,N] share a dtype (fp32, fp16, bf16), dt [B,L,D] has it too or is
     fp32; they may be slices of wider tensors along the last dimension.  A
     [D,N], D, dt_bias [D] and initial_states [B,D,N] are fp32.  ``lengths``
-    (int32 [B], on the GPU): tokens per row; y is 0 past them."""
+    (int32 [B], on the GPU): tokens per row; y is 0 past them.  ``out``: y's
+    memory; it may be x, z or dt itself where that is dense and of y's type, and
+    is refused where it overlaps an input otherwise."""
     return _run("selective_scan", "ssd_selective_scan", x, x, dt, A, B, C, dt_softplus, dt_limit[0], dt_limit[1], D, z, dt_bias,
                 initial_states, lengths, return_final_state, out)
 
