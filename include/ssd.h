@@ -522,10 +522,11 @@ ssd_status ssd_selective_scan_step(const ssd_scan_step_args *args, void *stream)
  * where v is x from token 0 on and the row's initial_state before it:
  * v[b,-(W-1)+j] = initial_state[b,j] (zeros when NULL).  final_state holds the
  * last W-1 entries of v, what the next call of the same sequence starts from.
- *   x [B,L,C] dtype, strided like the scan's; y [B,L,C] dense, not overlapping x
+ *   x [B,L,C] dtype, strided like the scan's; y [B,L,C] dense
  *   w [C,W] fp32, 1 <= W <= 8; bias [C] fp32 or NULL
- *   initial_state, final_state [B,W-1,C] dtype (optional), not overlapping each other
+ *   initial_state, final_state [B,W-1,C] dtype (optional)
  *   lengths [B] int32, device (optional): as for the scan
+ * An output that overlaps an input or the other output is refused.
  */
 typedef struct {
     int64_t B, L, C, W;

@@ -378,12 +378,13 @@ ssd_status ssd_causal_conv_carry(const ssd_conv_args *a, void *stream) {
     if (st != SSD_OK) return st;
     if (!a->x || !a->w || !a->y) return fail(SSD_ERR_INVALID_ARG, "x, w and y are required");
     // a thread reads the tokens before its run, which another one writes
-    const size_t es = element(a->dtype), state = (size_t)a->B * (a->W - 1) * a->C * es;
-    const size_t read = ((size_t)(a->B - 1) * p.xs[0] + (size_t)(a->L - 1) * p.xs[1] + a->C) * es;
-    if (overlap(a->x, read, a->y, (size_t)a->B * a->L * a->C * es))
-        return fail(SSD_ERR_INVALID_ARG, "y must not overlap x");
-    if (overlap(a->initial_state, state, a->final_state, state))
-        return fail(SSD_ERR_INVALID_ARG, "final_state must not overlap initial_state");
+    const size_t f = sizeof(float), es = element(a->dtype), state = (size_t)a->B * (a->W - 1) * a->C * es;
+    const Span y = {a->y, (size_t)a->B * a->L * a->C * es, "y"}, fin = {a->final_state, state, "final_state"};
+    const Span x = strided(a->x, a->B, a->L, a->C, p.xs, es, "x"), w = {a->w, (size_t)a->C * a->W * f, "w"},
+               bias = {a->bias, a->C * f, "bias"}, h0 = {a->initial_state, state, "initial_state"},
+               len = {a->lengths, a->B * sizeof(int32_t), "lengths"};
+    if ((st = apart(y, {x, w, bias, h0, len, fin})) != SSD_OK) return st;
+    if ((st = apart(fin, {x, w, bias, h0, len})) != SSD_OK) return st;
     cudaError_t e = ssd::launch_conv(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "causal_conv_carry");
     return ok();

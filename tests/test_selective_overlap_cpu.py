@@ -76,3 +76,24 @@ def test_scan_reads_through_strides():
     """The far end of a slice of a wider tensor counts."""
     far = AT["Bm"] + (64 * 100 + 63 * 100 + 32) * 2 - 2
     refused("ssd_selective_scan", scan_args(y=far, b_stride=(6400, 100)), "y")
+
+
+CONV = ("x", "w", "bias", "initial_state", "lengths", "y", "final_state")
+CONV_AT = {n: (16 + 4 * i) * MB for i, n in enumerate(CONV)}
+
+
+def conv_args(**over):
+    a = ssd.SsdConvArgs()
+    a.B, a.L, a.C, a.W, a.dtype = 2, 64, 32, 4, 2
+    return place(a, CONV, **over)
+
+
+@pytest.mark.parametrize("name", ["x", "w", "bias", "initial_state", "lengths", "final_state"])
+def test_conv_output_over_what_others_read(name):
+    refused("ssd_causal_conv_carry", conv_args(y=CONV_AT[name]), "y")
+    refused("ssd_causal_conv_carry", conv_args(y=CONV_AT[name] + 4 - Y), "y")
+
+
+@pytest.mark.parametrize("name", ["x", "w", "bias", "initial_state", "lengths"])
+def test_conv_final_state_over_inputs(name):
+    refused("ssd_causal_conv_carry", conv_args(final_state=CONV_AT[name]), "final_state")
