@@ -493,6 +493,8 @@ ssd_status ssd_selective_scan_bwd(const ssd_scan_bwd_args *args, void *stream);
  *   slots             [B] int32, device, or NULL (row b uses slot b, nslots = B).
  *                     A row whose slot is outside 0..nslots-1 is left out: its y
  *                     is 0 and no state is touched.  Rows must not share a slot.
+ * y may be x, dt or z itself where that is dense and of y's type.  Otherwise an
+ * output that overlaps an input, or the other output, is refused.
  */
 typedef struct {
     int64_t B, D, N, G, nslots;
@@ -565,7 +567,8 @@ ssd_status ssd_causal_conv_bwd(const ssd_conv_bwd_args *args, void *stream);
 
 /* One token of the convolution for each of B sequences: x [B,C] (rows x_row
  * apart, 0 = dense), y [B,C]; state, state_out [nslots,W-1,C] dtype, equal for
- * an update in place; slots as for ssd_selective_scan_step. */
+ * an update in place; slots as for ssd_selective_scan_step.  y may be a dense x;
+ * other overlaps of an output are refused. */
 typedef struct {
     int64_t B, C, W, nslots;
     const void *x;

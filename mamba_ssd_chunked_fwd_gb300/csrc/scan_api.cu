@@ -367,6 +367,20 @@ ssd_status ssd_selective_scan_step(const ssd_scan_step_args *a, void *stream) {
     p.softplus = a->dt_softplus ? 1 : 0;
     p.has_limit = limited(a->dt_min, a->dt_max);
     p.dt_min = a->dt_min; p.dt_max = a->dt_max;
+    const size_t f = sizeof(float), es = element(a->x_dtype), pool = (size_t)a->nslots * a->D * a->N * f;
+    const long long xr[2] = {0, p.x_row}, dtr[2] = {0, p.dt_row}, zr[2] = {0, p.z_row}, br[2] = {0, p.b_row}, cr[2] = {0, p.c_row};
+    const Span y = {a->y, (size_t)a->B * a->D * es, "y"}, to = {a->state_out, pool, "state_out"};
+    const Span B = strided(a->Bm, 1, a->B, gn, br, es, "B"), C = strided(a->Cm, 1, a->B, gn, cr, es, "C"),
+               A = {a->A, (size_t)a->D * a->N * f, "A"}, Dskip = {a->Dskip, a->D * f, "Dskip"},
+               bias = {a->dt_bias, a->D * f, "dt_bias"}, slots = {a->slots, a->B * sizeof(int32_t), "slots"},
+               from = {a->state == a->state_out ? nullptr : a->state, pool, "state"};
+    st = apart(y, {replaced(a->y, a->x_dtype, a->x, a->x_dtype, 1, a->B, a->D, xr, "x"),
+                   replaced(a->y, a->x_dtype, a->dt, a->dt_dtype, 1, a->B, a->D, dtr, "dt"),
+                   replaced(a->y, a->x_dtype, a->z, a->x_dtype, 1, a->B, a->D, zr, "z"), B, C, A, Dskip, bias, slots, from, to});
+    if (st != SSD_OK) return st;
+    st = apart(to, {strided(a->x, 1, a->B, a->D, xr, es, "x"), strided(a->dt, 1, a->B, a->D, dtr, element(a->dt_dtype), "dt"),
+                    strided(a->z, 1, a->B, a->D, zr, es, "z"), B, C, A, Dskip, bias, slots, from});
+    if (st != SSD_OK) return st;
     cudaError_t e = ssd::launch_scan_step(p, a->x_dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "selective_scan_step");
     return ok();
@@ -434,6 +448,15 @@ ssd_status ssd_causal_conv_step(const ssd_conv_step_args *a, void *stream) {
     p.x_row = a->x_row ? a->x_row : a->C;
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.state_out = a->state_out; p.slots = a->slots;
     p.y = a->y; p.silu = a->silu ? 1 : 0;
+    const size_t f = sizeof(float), es = element(a->dtype), pool = (size_t)a->nslots * (a->W - 1) * a->C * es;
+    const long long xr[2] = {0, p.x_row};
+    const Span y = {a->y, (size_t)a->B * a->C * es, "y"}, to = {a->state_out, pool, "state_out"};
+    const Span w = {a->w, (size_t)a->C * a->W * f, "w"}, bias = {a->bias, a->C * f, "bias"},
+               slots = {a->slots, a->B * sizeof(int32_t), "slots"},
+               from = {a->state == a->state_out ? nullptr : a->state, pool, "state"};
+    ssd_status st = apart(y, {replaced(a->y, a->dtype, a->x, a->dtype, 1, a->B, a->C, xr, "x"), w, bias, slots, from, to});
+    if (st != SSD_OK) return st;
+    if ((st = apart(to, {strided(a->x, 1, a->B, a->C, xr, es, "x"), w, bias, slots, from})) != SSD_OK) return st;
     cudaError_t e = ssd::launch_conv_step(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "causal_conv_step");
     return ok();

@@ -97,3 +97,75 @@ def test_conv_output_over_what_others_read(name):
 @pytest.mark.parametrize("name", ["x", "w", "bias", "initial_state", "lengths"])
 def test_conv_final_state_over_inputs(name):
     refused("ssd_causal_conv_carry", conv_args(final_state=CONV_AT[name]), "final_state")
+
+
+STEP = ("x", "dt", "A", "Bm", "Cm", "Dskip", "z", "dt_bias", "state", "state_out", "slots", "y")
+STEP_AT = {n: (16 + 4 * i) * MB for i, n in enumerate(STEP)}
+ROWS, POOL = 4 * 32 * 2, 6 * 32 * 16 * 4  # bytes of y and of the states
+
+
+def step_args(**over):
+    a = ssd.SsdScanStepArgs()
+    a.B, a.D, a.N, a.G, a.nslots = 4, 32, 16, 2, 6
+    a.x_dtype = a.dt_dtype = 2
+    a.dt_max = INF
+    return place(a, STEP, **over)
+
+
+@pytest.mark.parametrize("name", ["A", "Bm", "Cm", "Dskip", "dt_bias", "state", "state_out", "slots"])
+def test_step_output_over_what_others_read(name):
+    refused("ssd_selective_scan_step", step_args(y=STEP_AT[name]), "y")
+    refused("ssd_selective_scan_step", step_args(y=STEP_AT[name] + 4 - ROWS), "y")
+
+
+@pytest.mark.parametrize("name", ["x", "dt", "z"])
+def test_step_output_beside_its_own_place(name):
+    for off in (2, 64, 4 - ROWS):
+        refused("ssd_selective_scan_step", step_args(y=STEP_AT[name] + off), "y")
+    row = {"x": "x_row", "dt": "dt_row", "z": "z_row"}[name]
+    refused("ssd_selective_scan_step", step_args(y=STEP_AT[name], **{row: 40}), "y")
+    if name == "dt":
+        refused("ssd_selective_scan_step", step_args(y=STEP_AT[name], dt_dtype=0), "y")
+
+
+@pytest.mark.parametrize("name", ["x", "dt", "z", "A", "Bm", "Cm", "Dskip", "dt_bias", "slots"])
+def test_step_states_over_inputs(name):
+    refused("ssd_selective_scan_step", step_args(state_out=STEP_AT[name]), "state_out")
+    refused("ssd_selective_scan_step", step_args(state=STEP_AT[name], state_out=STEP_AT[name]), "state_out")
+
+
+@pytest.mark.parametrize("off", [4, 32 * 16 * 4, -32 * 16 * 4, POOL - 4])
+def test_step_states_beside_their_own_place(off):
+    """state_out is state or lies apart: a shifted pool holds other sequences' states."""
+    refused("ssd_selective_scan_step", step_args(state_out=STEP_AT["state"] + off), "state_out")
+
+
+CSTEP = ("x", "w", "bias", "state", "state_out", "slots", "y")
+CSTEP_AT = {n: (16 + 4 * i) * MB for i, n in enumerate(CSTEP)}
+
+
+def conv_step_args(**over):
+    a = ssd.SsdConvStepArgs()
+    a.B, a.C, a.W, a.nslots, a.dtype = 4, 32, 4, 6, 2
+    return place(a, CSTEP, **over)
+
+
+@pytest.mark.parametrize("name", ["w", "bias", "state", "state_out", "slots"])
+def test_conv_step_output_over_what_others_read(name):
+    refused("ssd_causal_conv_step", conv_step_args(y=CSTEP_AT[name]), "y")
+
+
+def test_conv_step_output_beside_its_own_place():
+    for off in (2, 64, 4 - ROWS):
+        refused("ssd_causal_conv_step", conv_step_args(y=CSTEP_AT["x"] + off), "y")
+    refused("ssd_causal_conv_step", conv_step_args(y=CSTEP_AT["x"], x_row=40), "y")
+
+
+@pytest.mark.parametrize("name", ["x", "w", "bias", "slots"])
+def test_conv_step_states_over_inputs(name):
+    refused("ssd_causal_conv_step", conv_step_args(state_out=CSTEP_AT[name]), "state_out")
+
+
+@pytest.mark.parametrize("off", [2, 3 * 32 * 2, -3 * 32 * 2])
+def test_conv_step_states_beside_their_own_place(off):
+    refused("ssd_causal_conv_step", conv_step_args(state_out=CSTEP_AT["state"] + off), "state_out")
