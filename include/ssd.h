@@ -593,10 +593,12 @@ ssd_status ssd_causal_conv_step(const ssd_conv_step_args *args, void *stream);
  * n is of r' as stored, rounded to the stream's type.  Without o, r' = r and
  * only n is written (the norm before the first block).
  *   o, n      [rows,D] dtype
- *   r, r_out  [rows,D] stream_dtype: dtype or SSD_F32; r_out may be r
+ *   r, r_out  [rows,D] stream_dtype: dtype or SSD_F32
  *   gate      [rows/rows_per_gate, D] dtype: 1 for a gate per token, a
  *             sequence's length for a gate per sequence
  *   w_post, w_pre, scale  [D] fp32
+ * r_out may be r; n and r_out may each be o, r or a gate per token itself, of
+ * the output's type.  Other overlaps of an output are refused.
  * D <= 16384.
  */
 typedef struct {

@@ -468,6 +468,22 @@ ssd_status ssd_block_norm(const ssd_block_norm_args *a, void *stream) {
     if (st != SSD_OK) return st;
     if (!a->r || !a->n) return fail(SSD_ERR_INVALID_ARG, "r and n are required");
     if (a->o && !a->r_out) return fail(SSD_ERR_INVALID_ARG, "r_out is required with o");
+    const long long dense[2] = {0, a->D};
+    const size_t f = sizeof(float), nd = (size_t)a->rows * a->D;
+    const int64_t gates = a->gate ? a->rows / a->rows_per_gate : 0;
+    const Span w_pre = {a->w_pre, a->D * f, "w_pre"}, w_post = {a->w_post, a->D * f, "w_post"}, scale = {a->scale, a->D * f, "scale"};
+    auto clear = [&](const void *out, int32_t type, const char *what) {  // o, r and a gate per token may be written over in place
+        auto in = [&](const void *p, int32_t t, int64_t rows, const char *name) {
+            return rows == a->rows ? replaced(out, type, p, t, 1, rows, a->D, dense, name)
+                                   : Span{p, (size_t)rows * a->D * element(t), name};
+        };
+        return apart({out, nd * element(type), what}, {in(a->o, a->dtype, a->rows, "o"), in(a->r, a->stream_dtype, a->rows, "r"),
+                                                       in(a->gate, a->dtype, gates, "gate"), w_pre, w_post, scale});
+    };
+    const void *r_out = a->o ? a->r_out : nullptr;
+    if ((st = clear(a->n, a->dtype, "n")) != SSD_OK || (st = clear(r_out, a->stream_dtype, "r_out")) != SSD_OK) return st;
+    st = apart({a->n, nd * element(a->dtype), "n"}, {{r_out, nd * element(a->stream_dtype), "r_out"}});
+    if (st != SSD_OK) return st;
     cudaError_t e = ssd::launch_block_norm(p, a->dtype, a->stream_dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "block_norm");
     return ok();

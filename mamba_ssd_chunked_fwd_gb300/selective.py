@@ -317,7 +317,8 @@ def block_norm(o, r, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5, dty
     Returns (n, r').  o [..., D] (None: only the norm of r, in ``dtype`` or r's);
     the residual stream r has o's dtype or fp32; gate, in o's dtype, has o's
     shape or is [B, D] for o [B, ..., D]; w_post (None: o is added as it is),
-    w_pre and scale [D] fp32.  ``r_out`` may be r itself."""
+    w_pre and scale [D] fp32.  ``r_out`` may be r itself; ``out`` and ``r_out`` are
+    refused where they overlap each other, a weight or part of an input."""
     like = None if o is not None or dtype is None else torch.empty(0, dtype=dtype)
     return _run("block_norm", "ssd_block_norm", r, o, r, w_pre, w_post, gate, scale, eps, like, out, r_out)
 

@@ -169,3 +169,48 @@ def test_conv_step_states_over_inputs(name):
 @pytest.mark.parametrize("off", [2, 3 * 32 * 2, -3 * 32 * 2])
 def test_conv_step_states_beside_their_own_place(off):
     refused("ssd_causal_conv_step", conv_step_args(state_out=CSTEP_AT["state"] + off), "state_out")
+
+
+NORM = ("o", "r", "gate", "w_post", "w_pre", "scale", "n", "r_out")
+NORM_AT = {n: (16 + 4 * i) * MB for i, n in enumerate(NORM)}
+NROWS = 6 * 32 * 2
+
+
+def norm_args(**over):
+    a = ssd.SsdBlockNormArgs()
+    a.rows, a.D, a.rows_per_gate, a.eps, a.dtype, a.stream_dtype = 6, 32, 1, 1e-5, 2, 2
+    return place(a, NORM, **over)
+
+
+@pytest.mark.parametrize("out", ["n", "r_out"])
+@pytest.mark.parametrize("name", ["w_post", "w_pre", "scale"])
+def test_norm_output_over_weights(out, name):
+    refused("ssd_block_norm", norm_args(**{out: NORM_AT[name]}), out)
+
+
+def test_norm_outputs_over_each_other():
+    refused("ssd_block_norm", norm_args(n=NORM_AT["r_out"]), "n")
+    refused("ssd_block_norm", norm_args(n=NORM_AT["r_out"] + NROWS - 2), "n")
+    refused("ssd_block_norm", norm_args(n=NORM_AT["r"], r_out=NORM_AT["r"]), "n")
+
+
+@pytest.mark.parametrize("out", ["n", "r_out"])
+@pytest.mark.parametrize("name", ["o", "r", "gate"])
+def test_norm_output_beside_its_own_place(out, name):
+    """An output may be o, r or a gate per token itself, in its own type, but not shifted against it."""
+    for off in (2, 32 * 2, 2 - NROWS):
+        refused("ssd_block_norm", norm_args(**{out: NORM_AT[name] + off}), out)
+
+
+def test_norm_output_over_another_type_or_a_shared_gate():
+    refused("ssd_block_norm", norm_args(n=NORM_AT["r"], stream_dtype=0), "n")
+    refused("ssd_block_norm", norm_args(r_out=NORM_AT["o"], stream_dtype=0), "r_out")
+    refused("ssd_block_norm", norm_args(r_out=NORM_AT["gate"], stream_dtype=0), "r_out")
+    refused("ssd_block_norm", norm_args(n=NORM_AT["gate"], rows_per_gate=3), "n")
+    refused("ssd_block_norm", norm_args(r_out=NORM_AT["gate"], rows_per_gate=3), "r_out")
+
+
+def test_norm_of_the_stream_alone():
+    a = norm_args(n=NORM_AT["r"] + 64)
+    a.o = a.gate = a.w_post = a.scale = a.r_out = None
+    refused("ssd_block_norm", a, "n")
