@@ -509,8 +509,6 @@ dim3 row_block(int D, int K) {
 // unit and two: 148 and 154 us (262144 rows); rows of 2048 with one, two and four: 132, 134 and 138.
 int norm_k(int D, bool backward) { return D <= 256 ? 1 : backward && D > 8192 ? 4 : 2; }
 
-constexpr int kNormSmem = 227 * 1024 - 1024;  // the most a CTA may hold, less the sums
-
 // Whether every tensor moves in whole, aligned units (absent ones do).
 bool norm_vec(const BlockNormParams &p) {
     bool ok = p.D % 8 == 0;
@@ -526,8 +524,8 @@ cudaError_t launch_norm_as(const BlockNormParams &p, cudaStream_t s) {
     const dim3 block = row_block(p.D, K);
     auto *kernel = norm_vec(p) ? block_norm_kernel<IO, SIO, K, true, MAXT> : block_norm_kernel<IO, SIO, K, false, MAXT>;
     const int row = (int)(block.x * block.y) * NormSlots<IO, SIO, K, 2, 1>::kPerThread;
-    const int stages = 2 * row <= kNormSmem ? 2 : 1, bytes = stages * row;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const int stages = 2 * row <= kSmemMost ? 2 : 1, bytes = stages * row;
+    cudaError_t e = allow_smem<kSmemMost>(kernel);  // bytes depend on D
     if (e != cudaSuccess) return e;
     const long long need = (p.rows + block.y - 1) / block.y;
     long long grid = scan_sm_count();
@@ -553,8 +551,8 @@ cudaError_t launch_norm_bwd_as(const BlockNormParams &p, cudaStream_t s) {
     auto *kernel = norm_vec(p) ? block_norm_bwd_kernel<IO, SIO, K, true, MAXT, WHOLE>
                                : block_norm_bwd_kernel<IO, SIO, K, false, MAXT, WHOLE>;
     const int row = block.x * block.y * NormSlots<IO, SIO, K, WHOLE ? 3 : 2, WHOLE ? 2 : 1>::kPerThread;
-    const int stages = 2 * row <= kNormSmem ? 2 : 1, bytes = stages * row;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const int stages = 2 * row <= kSmemMost ? 2 : 1, bytes = stages * row;
+    cudaError_t e = allow_smem<kSmemMost>(kernel);  // bytes depend on D
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)((p.chunks + block.y - 1) / block.y), block, bytes, s>>>(p, stages);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

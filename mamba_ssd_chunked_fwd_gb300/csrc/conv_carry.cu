@@ -347,7 +347,7 @@ cudaError_t launch_conv_bwd_io(const ConvParams &p, cudaStream_t s) {
          {conv_bwd_kernel<IO, 8, true, false>, conv_bwd_kernel<IO, 8, true, true>}}};
     auto *kernel = kernels[p.W > 4][conv_vec(p, IO)][p.silu != 0];
     constexpr int kBytes = 2 * kAhead * 2 * kCx * kCy * (IO == IO_F32 ? 16 : 8);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    cudaError_t e = allow_smem<kBytes>(kernel);
     if (e != cudaSuccess) return e;
     kernel<<<grid, dim3(kCx, kCy), kBytes, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

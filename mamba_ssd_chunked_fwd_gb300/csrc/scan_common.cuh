@@ -510,6 +510,18 @@ __device__ __forceinline__ void store4_io(void *base, long long i, int nv, const
     }
 }
 
+// The shared memory of a CTA: 227 KB, less a little for a kernel's static arrays.
+constexpr int kSmemMost = 227 * 1024 - 1024;
+
+// Lets a kernel be launched with up to BYTES of dynamic shared memory.  The limit belongs to the
+// function, not to the launch, and another host thread may set it between this one's
+// setting and its launch: so BYTES is a constant of the kernel, the most that any call of it takes.
+template <int BYTES, class K>
+cudaError_t allow_smem(K *kernel) {
+    static_assert(BYTES <= kSmemMost, "more shared memory than a CTA may hold");
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+}
+
 // A launch that may start while the kernel before it on the stream still runs (`after`):
 // that one has let it with pdl_launch_dependents, and this one's threads all begin with
 // pdl_wait, so nothing is read or written early; what is saved is the gap between the two.

@@ -522,7 +522,7 @@ cudaError_t launch_walk_as(ScanParams p, cudaStream_t s) {
     constexpr int kMost = MODE == WALK_BOTH ? (int)WALK_ADJ : MODE;  // the mode that needs the most
     const int bytes = WalkSmem<IO, LPC, kMost>::bytes(IO != IO_F32 && p.dt32);
     auto *kernel = walk_vec(p, IO, MODE) ? scan_walk_kernel<IO, LPC, MODE, true> : scan_walk_kernel<IO, LPC, MODE, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<WalkSmem<IO, LPC, kMost>::bytes(IO != IO_F32)>(kernel);  // bytes depend on dt's type
     if (e != cudaSuccess) return e;
     const bool after = (MODE == WALK_Y || MODE == WALK_CKPT) && p.nseg > 1;  // the cut's kernels
     return launch_kernel(after, kernel, dim3(p.G * p.tiles, segs, p.B), WalkShape<IO, LPC>::kThreads, bytes, s, p);

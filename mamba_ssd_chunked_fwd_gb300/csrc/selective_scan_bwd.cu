@@ -616,7 +616,7 @@ cudaError_t launch_bwd_as(ScanParams p, ScanSums o, cudaStream_t s) {
     const int bytes = S::bytes(IO != IO_F32 && p.dt32);
     p.tiles = scan_bwd_tiles(p);
     auto *kernel = bwd_vec(p, IO) ? scan_bwd_kernel<IO, LPC, true> : scan_bwd_kernel<IO, LPC, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem<S::bytes(IO != IO_F32)>(kernel);  // bytes depend on dt's type
     if (e != cudaSuccess) return e;
     e = launch_kernel(true, kernel, dim3(p.G * p.tiles, p.nseg, p.B), kBthreads, bytes, s, p);
     if (e != cudaSuccess) return e;
