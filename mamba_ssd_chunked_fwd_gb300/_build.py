@@ -2,8 +2,9 @@
 the Python extension ``_ssd_binding.so`` with g++.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then one ``nvcc
--shared`` link; ``csrc/binding.cpp`` compiles beside them against torch's
-headers.  Outputs go to ``_build/`` beside this file (git-ignored).
+-shared`` link.  ``csrc/binding.cpp`` compiles against Python's and torch's
+headers, for the calls of ``selective.py`` alone: the library builds and loads
+without it.  Outputs go to ``_build/`` beside this file (git-ignored).
 """
 from __future__ import annotations
 
@@ -40,18 +41,23 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]
+        os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]
+
+
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, _deps())
 
 
-def _build_binding():
+def build_binding(force: bool = False) -> str:
+    """Builds the Python extension if its source is newer; returns its path."""
+    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]):
+        return BINDING
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
@@ -64,6 +70,7 @@ def _build_binding():
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -84,10 +91,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_build_binding)
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(compile_one, srcs))
-        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -98,4 +103,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    print(build(force=True, verbose=True))
+    print(build(force=True, verbose=True), build_binding(force=True))

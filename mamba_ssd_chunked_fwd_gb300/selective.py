@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import math
+import threading
 
 import torch
 
@@ -105,19 +106,21 @@ SIGNATURES = {
 
 _CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _pkg = _ext = None
+_lock = threading.Lock()
 
 
 def _binding():
-    """The package and its C++ binding, loaded on first use."""
+    """The package and its C++ binding, loaded (and built, if stale) on first use."""
     global _pkg, _ext
-    if _ext is None:
-        import mamba_ssd_chunked_fwd_gb300 as pkg
-        pkg.load_library()  # builds both if stale
-        spec = importlib.util.spec_from_file_location("_ssd_binding", pkg._build.BINDING)
-        ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(ext)
-        ext.load(pkg.library_path())
-        _pkg, _ext = pkg, ext
+    with _lock:
+        if _ext is None:
+            import mamba_ssd_chunked_fwd_gb300 as pkg
+            pkg.load_library()
+            spec = importlib.util.spec_from_file_location("_ssd_binding", pkg._build.build_binding())
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+            ext.load(pkg.library_path())
+            _pkg, _ext = pkg, ext
     return _ext
 
 
