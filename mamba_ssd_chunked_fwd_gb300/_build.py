@@ -1,5 +1,5 @@
 """Build the CUDA library ``libssd_gb300.so`` in-tree with nvcc (sm_103a), and
-the Python extension ``_ssd_binding.so`` with g++.
+the Python extension ``_ssd_binding.*.so`` with g++.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then one ``nvcc
 -shared`` link.  ``csrc/binding.cpp`` compiles against Python's and torch's
@@ -20,7 +20,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libssd_gb300.so")
-BINDING = os.path.join(BUILD, "_ssd_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -52,14 +51,21 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def binding_path() -> str:
+    """The Python extension of this torch and this interpreter: it holds to the layout of both."""
+    import torch
+    return os.path.join(BUILD, f"_ssd_binding.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
 def build_binding(force: bool = False) -> str:
     """Builds the Python extension if its source is newer; returns its path."""
-    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]):
-        return BINDING
+    path = binding_path()
+    if not force and _newer(path, [BINDING_SRC, os.path.join(INCLUDE, "ssd.h"), os.path.abspath(__file__)]):
+        return path
     import torch
     os.makedirs(BUILD, exist_ok=True)
     root = os.path.dirname(torch.__file__)
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{INCLUDE}", f"-I{os.path.join(root, 'include')}",
@@ -69,8 +75,8 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

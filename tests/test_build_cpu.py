@@ -2,6 +2,9 @@
 import os
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 import mamba_ssd_chunked_fwd_gb300 as ssd
 from mamba_ssd_chunked_fwd_gb300 import _build
@@ -18,6 +21,16 @@ def test_library_does_not_need_the_binding(monkeypatch, tmp_path):
         raise AssertionError("a compiler was called")
     monkeypatch.setattr(subprocess, "run", no_compiler)
     assert _build.build() == _build.LIB
+
+
+def test_binding_belongs_to_its_torch_and_interpreter(monkeypatch):
+    """A binding of another torch or Python is another file, so it is never imported here."""
+    here = _build.build_binding()
+    assert os.path.exists(here) and torch.__version__ in os.path.basename(here)
+    assert sysconfig.get_config_var("SOABI") in os.path.basename(here)
+    assert _build.binding_path() == here
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    assert _build.binding_path() != here
 
 
 def test_binding_is_built_again_when_its_source_is_newer(monkeypatch, tmp_path):
