@@ -522,9 +522,10 @@ scan_bwd_kernel(ScanParams p) {
             if (p.z) st_io<IO>(p.dz, at, 0.f);
         }
     }
-    // dD and ddt_bias over the threads of a quad, in order
+    // dD and ddt_bias over the threads of a quad, in order; past this barrier the tiles' buffers are free
+    static_assert(kBside * 2 * S::kCh <= S::kFloats, "the sums' rows must fit the tiles' buffers");
     __syncthreads();
-    float *red = s_p;  // [kBside][2 kCh]
+    float *red = smem;  // [kBside][2 kCh]
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
         *reinterpret_cast<float2 *>(red + ta * 2 * S::kCh + 2 * j) = acc_d[j];
