@@ -107,7 +107,11 @@ const void *tokens(const Tensor *t, IntArrayRef shape, ScalarType type, int64_t 
     if (!inner_dense(*t, 2)) refuse(what, ": the values of a token must be contiguous");
     st[0] = t->size(0) == 1 ? 0 : t->stride(0);
     st[1] = t->size(1) == 1 ? 0 : t->stride(1);
-    if (st[0] == 0 && st[1] == 0 && t->numel()) refuse(what, ": broadcast over every token");
+    if (st[0] == 0 && st[1] == 0 && t->numel()) {
+        if (t->size(1) != 1) refuse(what, ": broadcast over every token");
+        // one token for every sequence; its stride leads nowhere, and two zeros would mean dense
+        st[1] = t->numel() / t->size(0);
+    }
     return t->data_ptr();
 }
 

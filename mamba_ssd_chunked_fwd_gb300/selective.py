@@ -193,7 +193,9 @@ def _tokens(t, shape, dtype, dev, what):
         raise ValueError(f"{what}: the values of a token must be contiguous")
     st = (0 if shape[0] == 1 else st[0], 0 if shape[1] == 1 else st[1])
     if st == _DENSE and t.numel():
-        raise ValueError(f"{what}: broadcast over every token")
+        if shape[1] != 1:
+            raise ValueError(f"{what}: broadcast over every token")
+        st = (0, t.numel() // shape[0])  # one token for every sequence; two zeros would mean dense
     return t.data_ptr(), st
 
 

@@ -1,6 +1,7 @@
 """The selective scan where it is cut into segments with ragged rows, where its
 grid fills the GPU, and where its tensors are strided, mixed or in place."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -217,3 +218,21 @@ def test_conv_gradients_on_a_full_grid():
     want = ref.gradients(plain, {"x": x.double(), "w": w.double(), "bias": bias.double()}, [dy.double()])
     for n, r in want.items():
         close(got["d" + n], r, "d" + n)
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_one_token_for_every_sequence(t):
+    """Rows of one token, shared by the batch: the batch stride is 0 and there is no other token."""
+    k = cuda(make(3, 1, 40, 16, 2, t))
+    for n in ("x", "dt", "z", "B", "C"):
+        k[n] = k[n][:1].expand(k[n].shape)
+    dense = {n: v.contiguous() if isinstance(v, torch.Tensor) else v for n, v in k.items()}
+    a, b = gpu_scan(k), gpu_scan(dense)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dy, df = (v.cuda() for v in grads_like(dense))
+    p, q = gpu_scan_bwd(k, dy, df), gpu_scan_bwd(dense, dy, df)
+    assert all(torch.equal(p[n], q[n]) for n in p)
+    w = torch.randn(40, 4, device="cuda")
+    assert torch.equal(ssd().causal_conv1d_carry(k["x"], w), ssd().causal_conv1d_carry(dense["x"], w))
+    sa = ssd().make_scan_args(k["x"], k["dt"], k["A"], k["B"], k["C"])
+    assert sa.x_stride[0] == 0 and sa.x_stride[1] > 0 and math.isinf(sa.dt_max)
