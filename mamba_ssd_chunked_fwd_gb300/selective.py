@@ -324,7 +324,14 @@ def block_norm(o, r, w_pre, *, w_post=None, gate=None, scale=None, eps=1e-5, dty
     shape or is [B, D] for o [B, ..., D]; w_post (None: o is added as it is),
     w_pre and scale [D] fp32.  ``r_out`` may be r itself; ``out`` and ``r_out`` are
     refused where they overlap each other, a weight or part of an input."""
-    like = None if o is not None or dtype is None else torch.empty(0, dtype=dtype)
+    like = None
+    if o is None:
+        if r_out is not None:
+            raise ValueError("r_out needs o")
+        if dtype is not None:
+            like = torch.empty(0, dtype=dtype)
+    elif dtype is not None and dtype is not o.dtype:
+        raise ValueError(f"dtype: {dtype}, but n has o's {o.dtype}")
     return _run("block_norm", "ssd_block_norm", r, o, r, w_pre, w_post, gate, scale, eps, like, out, r_out)
 
 
