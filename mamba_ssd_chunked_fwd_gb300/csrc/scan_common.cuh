@@ -233,9 +233,6 @@ __device__ __forceinline__ void unpack4(const Raw4 &r, float (&v)[4]) {
     }
 }
 
-template <int IO, bool VEC>
-__device__ __forceinline__ void store4_io(void *base, long long i, int nv, const float (&v)[4]);
-
 // Copies from global to shared memory that run on while the thread goes on
 // (cp.async); the thread that issued them waits with cp_wait.  What is not read is filled with zeros.
 __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
@@ -369,12 +366,6 @@ __device__ __forceinline__ void read_quad(const void *src, float2 (&v)[2]) {
     }
 }
 
-template <int IO>
-__device__ __forceinline__ void write_quad(void *dst, const float2 (&v)[2]) {
-    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-    store4_io<IO, true>(dst, 0, 4, f);
-}
-
 // A chunk from shared memory as pairs of floats.
 template <int IO>
 __device__ __forceinline__ void read_chunk(const void *src, float2 *v) {
@@ -461,30 +452,6 @@ __device__ __forceinline__ float load_one(const void *base, long long i, bool ok
     uint16_t h = 0;
     ldg_u16(h, static_cast<const uint16_t *>(base) + i, ok);
     return IO == IO_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-}
-
-// dt, in the tensors' type or in fp32.
-template <int IO, bool VEC>
-__device__ __forceinline__ Raw4 load_raw4_dt(const void *base, long long i, int ok, int nv, int dt32) {
-    if (IO == IO_F32) return load_raw4<IO_F32, VEC>(base, i, ok, nv);
-    Raw4 r = load_raw4<IO, VEC>(base, i, dt32 ? 0 : ok, nv);
-    const uint32_t *p = static_cast<const uint32_t *>(base) + i;
-    if (VEC) {
-        ldg_v4(r.w, p, dt32 ? ok : 0);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ldg_u32(r.w[j], p + j, dt32 && j < nv ? ok : 0);
-    }
-    return r;
-}
-
-template <int IO, bool VEC>
-__device__ __forceinline__ void unpack4_dt(const Raw4 &r, float (&v)[4], int dt32) {
-    unpack4<IO, VEC>(r, v);
-    if (IO != IO_F32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = dt32 ? __uint_as_float(r.w[j]) : v[j];
-    }
 }
 
 template <int IO, bool VEC>
@@ -676,8 +643,6 @@ __device__ __forceinline__ float2 sigmoid2(float2 v) {
     return make_float2(rcp_approx(e.x), rcp_approx(e.y));
 }
 __device__ __forceinline__ float2 silu2(float2 v) { return __fmul2_rn(v, sigmoid2(v)); }
-
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 cudaError_t launch_scan(const ScanParams &p, int io, cudaStream_t s);
 cudaError_t launch_scan_ckpt(const ScanParams &p, int io, cudaStream_t s);  // and the adjoint after every segment
