@@ -419,7 +419,8 @@ ssd_status ssd_gated_rmsnorm(int64_t rows, int64_t D, int64_t groups, float eps,
  * y may be x, z or dt itself where that is dense and of y's type.  Otherwise an
  * output that overlaps an input (its range of memory, gaps between strided rows
  * included) or the other output is refused.
- * Every dim > 0, N <= 128, D % G == 0.  fp32 arithmetic and states.  No
+ * Every dim > 0, N <= 128, D % G == 0.  A step that is NaN stays NaN, clamped or
+ * not.  fp32 arithmetic and states.  No
  * alignment is required beyond the types' own.
  * A sequence is cut into segments walked in parallel when B and D alone do not
  * fill the GPU; the cut depends on the shape and the GPU's SM count only.
@@ -460,7 +461,8 @@ ssd_status ssd_selective_scan(const ssd_scan_args *args, void *stream);
  *   dB, dC   [B,L,G,N] x_dtype               dA      [D,N] fp32
  *   dD       [D] fp32, required with Dskip   dz      [B,L,D] x_dtype, required with z
  *   ddt_bias [D] fp32, required with dt_bias dh0     [B,D,N] fp32 or NULL
- * Outputs are dense; a row's padding gets zeros.  The clamp passes no gradient
+ * Outputs are dense and lie apart from the inputs and from each other (this is
+ * not checked); a row's padding gets zeros.  The clamp passes no gradient
  * where it is active.  Sums run in a fixed order: bitwise reproducible.
  * workspace: device, 256-byte aligned, ssd_selective_scan_bwd_workspace_size()
  * bytes (it holds the state before every eighth token).  Enqueue only.
@@ -549,7 +551,8 @@ ssd_status ssd_causal_conv_carry(const ssd_conv_args *args, void *stream);
 /* Its backward: gradients of sum(dy * y) + sum(dfinal * final_state).  dy, dx
  * [B,L,C] dtype, dense; dfinal, dh0 [B,W-1,C] dtype (optional); dw [C,W] fp32;
  * dbias [C] fp32, required with bias.  y and final_state of `fwd` are ignored.
- * Sums run in a fixed order.  workspace as elsewhere. */
+ * Outputs lie apart from the inputs and from each other (not checked).  Sums
+ * run in a fixed order.  workspace as elsewhere. */
 typedef struct {
     ssd_conv_args fwd;
     const void *dy;
@@ -621,7 +624,8 @@ ssd_status ssd_block_norm(const ssd_block_norm_args *args, void *stream);
  * [rows,D] dtype of n and dr_out [rows,D] stream_dtype of r' from above (NULL =
  * zero): dr [rows,D] stream_dtype, dw_pre [D]; with o also d_o [rows,D] dtype,
  * dw_post, dscale [D] fp32 and dgate (gate's shape and type), each required
- * with its input.  r and n of `fwd` are ignored.  Sums run in a fixed order. */
+ * with its input.  r and n of `fwd` are ignored.  Outputs lie apart from the
+ * inputs and from each other (not checked).  Sums run in a fixed order. */
 typedef struct {
     ssd_block_norm_args fwd;
     const void *dn;

@@ -14,9 +14,9 @@
 // one row run beside the reductions and stores of the one before, need no
 // registers, and every tensor moves once.  The weights, and backwards the two column
 // sums, stay in registers over the rows that the threads walk.
-// Measured: [8,4096,2048], bf16 with an fp32 stream and a gate per sequence, 141 us (5.7 TB/s,
-// 84 % of the copy rate); backwards [4,2048,2048] in bf16 with a gate per token 59 us
-// (4.6 TB/s): 16 warps per SM, registers bound.  A gate per sequence: 58 us (80 while one thread per column
+// Measured: [8,4096,2048], bf16 with an fp32 stream and a gate per sequence, 143 us (5.65 TB/s,
+// 83 % of the copy rate); backwards [4,2048,2048] in bf16 with a gate per token 59 us
+// (4.6 TB/s), 8 of it the column sums: 128 registers a thread, 13.7 warps active per SM.  A gate per sequence: 58 us (80 while one thread per column
 // summed a gate's partial rows; one sequence of 500 rows 25 and 109).
 #include "scan_common.cuh"
 
@@ -157,8 +157,7 @@ __device__ __forceinline__ void post_weights(const BlockNormParams &p, int c, in
 }
 
 // The slots of a CTA's threads for one row, K units each: NI tensors in the
-// block's type, then NS in the stream's; a unit's two chunks lie apart, so that
-// neighbouring threads' chunks are neighbours.
+// block's type, then NS in the stream's. A unit lies in one piece, 16 bytes of a 16-bit type or 32 of fp32 per thread.
 template <int IO, int SIO, int K, int NI, int NS>
 struct NormSlots {
     static constexpr int kPerThread = K * (NI * Eight<IO>::kBytes + NS * Eight<SIO>::kBytes);
@@ -506,7 +505,10 @@ dim3 row_block(int D, int K) {
 
 // Units per thread: two, but one for rows that a warp takes so, and backwards four for rows past 8192,
 // whose registers would not allow more threads; wider rows take more warps.  Rows of 256 with one
-// unit and two: 148 and 154 us (262144 rows); rows of 2048 with one, two and four: 132, 134 and 138.
+// unit and two: 148 and 154 us (262144 rows).  One unit and two are level at rows of 512 and 1024 (49.8 and
+// 88.7 us, 65536 rows) and within 2 % at 2048 (132 and 134 us; four 138), and with two 512 threads
+// take rows of up to 8192.  Four units backwards do not fit the registers: 488 to 656 bytes a thread are
+// spilled, and 2048 rows of 10240 take 168 us (148 and the sums 20; 49 for their bytes).
 int norm_k(int D, bool backward) { return D <= 256 ? 1 : backward && D > 8192 ? 4 : 2; }
 
 // Whether every tensor moves in whole, aligned units (absent ones do).

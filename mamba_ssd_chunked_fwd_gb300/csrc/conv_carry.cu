@@ -12,9 +12,9 @@
 // shared memory, two blocks of eight ahead, so the loads run on beside the arithmetic
 // and need neither registers nor a barrier.
 // Measured in bf16 (the copy rate of the card is 6.8 TB/s): [2,8192,8192] with a carried
-// state 86 us, 6.2 TB/s; backwards [4,2048,4096] 59 us, 3.4 TB/s: it reads x and dy once,
-// but recomputes pre and its sigmoid and runs 128 registers a thread, so 16 warps per SM
-// issue in 43 % of the cycles.  Rows that are not whole quads of four (8191 channels) go element by
+// state 86 us, 6.2 TB/s; backwards [4,2048,4096] 57 us, 3.5 TB/s: it reads x and dy once,
+// but recomputes pre and its sigmoid and runs 128 registers a thread (8 to 12 bytes spilled), so of 16 warps per
+// SM 12.3 are active on average and issue in 43 % of the cycles.  Rows that are not whole quads of four (8191 channels) go element by
 // element: 160 us.
 #include <math.h>
 

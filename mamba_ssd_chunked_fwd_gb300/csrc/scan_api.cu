@@ -111,7 +111,8 @@ ssd_status check_scan_shape(const ssd_scan_args *a) {
 // 1571 and 278 us, gradients of [2,333,328,8] 121 and 32; where the SMs are full, nothing is cut.
 void choose_segments(ssd::ScanParams &p, bool backward) {
     const int lanes = ssd::scan_lanes(p.N);
-    // backwards the model was fitted on CTAs of four walk warps
+    // Backwards the model was fitted with CTAs of four walk warps, and keeps that count where N <= 8 takes two: with
+    // two it cuts less, [4,2048,4096,8] 977 us instead of 640 ([6,8923,648,8] 1127 instead of 1166).
     const int dc = (backward ? 4 : ssd::scan_walk_warps(lanes)) * (32 / lanes) * 4;
     const double sms = ssd::scan_sm_count(), pair = 1.72;
     const double ctas = (double)p.B * p.G * ((p.D / p.G + dc - 1) / dc), state = (double)p.B * p.D * p.N;

@@ -6,8 +6,8 @@
 //
 // Both read and write their state once and are bound by it: 8 N bytes per
 // channel for the scan, 4 (W-1) bytes for a 16-bit convolution.  Measured: 256 sequences
-// of 8192 channels, N = 16, in fp16 54 us (5.3 TB/s, 78 % of the copy rate); one sequence
-// of 2048 channels 5.4 us, the launch; the convolution of 64 sequences 6.2 us.
+// of 8192 channels, N = 16, in fp16 49 us (5.8 TB/s, 85 % of the copy rate); one sequence
+// of 2048 channels 6.6 to 7.9 us called in turn, the host's part; the convolution of 64 sequences 6.6 to 8.5 us.
 #include "scan_common.cuh"
 
 namespace ssd {
@@ -113,7 +113,7 @@ cudaError_t launch_step_as(const ScanStepParams &p, cudaStream_t s) {
     const int tiles = (p.D + kCh - 1) / kCh;
     // Four sequences per lane once that leaves every SM four CTAs; below, one, so
     // that the few channels reach more SMs.  Two lanes per channel take one.  256
-    // sequences of 8192 channels: 58 us by fours, 80 by one; 64 of 2048: 11 and 13; 16 of 2048: level, 8.8.
+    // sequences of 8192 channels: 50 us by fours, 78 by one; 64 and 16 of 2048: level, 10.9 and 8.8 (with events around).
     if constexpr (LPC >= 4) {
         if ((long long)tiles * (p.B / 4) >= 4LL * scan_sm_count()) {
             auto *kernel = vec ? scan_step_kernel<IO, LPC, 4, true> : scan_step_kernel<IO, LPC, 4, false>;

@@ -25,8 +25,10 @@
 // of tensors, 23 % of the copy rate; its exponentials alone take 230 us, with the packed
 // multiply-adds and the sums of y about 410); 256 CTAs fill 84 % of the 304 places.
 // [1,16384,2048,16] cut into segments 275 us (1571 uncut: 16 CTAs); three fp32 rows of
-// 517 tokens and 202 channels 16.5 us (68 uncut).
-// Tried and slower: 8 side warps, CTAs of one or two walk warps, eight states per lane.
+// 517 tokens and 202 channels 17 to 18 us called in turn (68 uncut). Issue is active in 63 % of the
+// cycles of the first of these, with 12.4 warps per SM. N = 4 takes 812 us where N = 8 takes 529: its rows
+// of B and C are not whole chunks, and then no tensor moves in whole chunks (walk_vec).
+// Tried and slower at N = 16: 8 side warps, CTAs of one or two walk warps, eight states per lane.
 #include "scan_common.cuh"
 
 namespace ssd {

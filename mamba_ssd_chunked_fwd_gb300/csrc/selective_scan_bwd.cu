@@ -22,9 +22,10 @@
 // and over the channel tiles in a second kernel, each in a fixed order.
 // Walk and side warps as in the forward: the side warps stage d, d x, ds, B and
 // C of the next tile and turn the previous tile's sums into dx, ddt and dz.
-// Measured: [4,2048,4096,16] in bf16 with the gate 821 us (41e9 channel-tokens/s, the
-// checkpoint walk included; its bytes alone would take 70 us, its exponentials 115),
-// [4,2048,1024,64] 930 us; [2,333,328,8] in fp32, cut into segments, 32 us in five
+// Measured: [4,2048,4096,16] in bf16 with the gate 823 us (41e9 channel-tokens/s; its bytes alone
+// would take 70 us, its exponentials 115): the checkpoint walk 184, this kernel 621 (issue
+// active in 65 % of the cycles with 12.9 warps per SM), the last sums 16. [4,2048,4096,8] 640 us,
+// [4,2048,1024,64] 930 us; [2,333,328,8] in fp32, cut into segments, 30 us in five
 // dependent launches (120 uncut).
 #include "scan_common.cuh"
 
@@ -174,7 +175,7 @@ scan_bwd_kernel(ScanParams p) {
                         h[j][1] = __ffma2_rn(ww, b1, ah[tt][j][1]);
                     }
                 }
-// A token's values are loaded before the sums of the token after it are
+                // A token's values are loaded before the sums of the token after it are
                 // stored: the stores may alias them, as far as the compiler knows.
                 float2 dn, wn, gn;
                 float4 bn, cn;

@@ -7,6 +7,10 @@ library) or ``ValueError`` (a shape, type or device the binding cannot express).
 The functions here pass their arguments on to ``csrc/binding.cpp``, which does
 the marshalling; the ctypes structures and ``make_*_args`` are for callers of
 the C entries themselves.
+
+No call is recorded by autograd: from inputs that require gradients come results
+that carry none (the ``*_bwd`` functions give them), and a state that is updated
+in place keeps its version counter.
 """
 from __future__ import annotations
 
