@@ -643,6 +643,153 @@ typedef struct {
 ssd_status ssd_block_norm_bwd_workspace_size(const ssd_block_norm_bwd_args *args, size_t *bytes);
 ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream);
 
+/*
+ * Gated delta rule: a state that is written by replacing.  Where the SSD above adds
+ * each token's outer product to its state, here a token first takes out what the
+ * state holds under its key.  For every batch row b, token t and head h, with
+ * group j = h / (H/G) and the state S [P,N]:
+ *
+ *     S' = exp(g[b,t,h]) S_{t-1}
+ *     u  = beta[b,t,h] (v[b,t,h,:] - S' k[b,t,j,:])
+ *     S_t = S' + u k[b,t,j,:]^T
+ *     y[b,t,h,:] = scale S_t q[b,t,j,:]
+ *
+ * Shapes and types:
+ *   q, k           [B,L,G,N]  dtype
+ *   v, y           [B,L,H,P]  dtype
+ *   g              [B,L,H]    g_dtype: dtype or SSD_F32; the logarithm of the decay
+ *   beta           [B,L,H]    beta_dtype: dtype or SSD_F32
+ *   initial_state, final_state  [B,H,P,N] fp32 (optional; NULL = zero / not returned)
+ *   lengths        [B] int32, device (optional): as for the selective scan
+ * q, k, v, g and beta are read through strides as the selective scan's tensors are; y is
+ * dense.  An output that overlaps an input or the other output is refused.
+ * Every dim > 0, N <= 128, P <= 1024, H % G == 0.  g is meant to be <= 0 (minus
+ * infinity empties the state) and keys to be of length about one; neither is checked.
+ * States are fp32.  workspace: device, 256-byte aligned, ssd_delta_rule_workspace_size()
+ * bytes (may be 0; then NULL is accepted).  Enqueue only.
+ */
+typedef struct {
+    int64_t B, L, H, G, N, P;
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *g;
+    const void *beta;
+    const float *initial_state;
+    const int32_t *lengths;
+    void *y;
+    float *final_state;
+    int64_t q_stride[2], k_stride[2], v_stride[2], g_stride[2], beta_stride[2];
+    int32_t dtype, g_dtype, beta_dtype; /* ssd_dtype */
+    float scale;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_delta_args;
+
+ssd_status ssd_delta_rule_workspace_size(const ssd_delta_args *args, size_t *bytes);
+ssd_status ssd_delta_rule(const ssd_delta_args *args, void *stream);
+
+/*
+ * Its backward: gradients of sum(dy * y) + sum(dfinal * final_state).  States are
+ * recomputed (y, final_state and the workspace of `fwd` are ignored).
+ *   dy      [B,L,H,P] dtype, dense        dfinal  [B,H,P,N] fp32 or NULL
+ *   dq, dk  [B,L,G,N] dtype               dv      [B,L,H,P] dtype
+ *   dg      [B,L,H] g_dtype               dbeta   [B,L,H] beta_dtype
+ *   dh0     [B,H,P,N] fp32 or NULL
+ * Outputs are dense and lie apart from the inputs and from each other (not
+ * checked); a row's padding gets zeros.  Sums run in a fixed order: bitwise
+ * reproducible.  workspace: ssd_delta_rule_bwd_workspace_size() bytes (the state before
+ * every 64th token and its adjoint among them).  Enqueue only.
+ */
+typedef struct {
+    ssd_delta_args fwd;
+    const void *dy;
+    const float *dfinal;
+    void *dq;
+    void *dk;
+    void *dv;
+    void *dg;
+    void *dbeta;
+    float *dh0;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_delta_bwd_args;
+
+ssd_status ssd_delta_rule_bwd_workspace_size(const ssd_delta_bwd_args *args, size_t *bytes);
+ssd_status ssd_delta_rule_bwd(const ssd_delta_bwd_args *args, void *stream);
+
+/* One token of the gated delta rule for each of B sequences, from carried states:
+ * q, k [B,G,N], v [B,H,P], g, beta [B,H] (rows `*_row` elements apart, 0 = dense),
+ * y [B,H,P] dense; state, state_out [nslots,H,P,N] fp32, equal for an update in place;
+ * slots as for ssd_selective_scan_step.  Other overlaps of an output are refused. */
+typedef struct {
+    int64_t B, H, G, N, P, nslots;
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *g;
+    const void *beta;
+    const float *state;
+    float *state_out;
+    const int32_t *slots;
+    void *y;
+    int64_t q_row, k_row, v_row, g_row, beta_row;
+    int32_t dtype, g_dtype, beta_dtype;
+    float scale;
+} ssd_delta_step_args;
+
+ssd_status ssd_delta_rule_step(const ssd_delta_step_args *args, void *stream);
+
+/*
+ * Norm of queries and keys with the rotation by position, for every head of both:
+ *   x' = x / sqrt(m + eps) * w,   m = mean(x^2) (SSD_NORM_RMS) or sum(x^2) (SSD_NORM_L2) over the head
+ * then pair i < nfreq of x' turns by position * freqs[i].  The pairs are (i, nfreq + i), or
+ * (2 i, 2 i + 1) with `interleaved`; elements from 2 nfreq on are not turned.
+ *   q, q_out [B,L,H,N], k, k_out [B,L,G,N] dtype; q and k read through strides as
+ *   above, the outputs dense; w_q, w_k [N] fp32 (NULL = 1)
+ *   freqs [nfreq] fp32, device, finite (radians per position), 2 nfreq <= N
+ *   positions [B,L] int32, device (NULL = the token's index in its row)
+ * N <= 256.  q_out may be a dense q itself, k_out a dense k; other overlaps of an
+ * output are refused.  For one token of each of B sequences: B = 1, L = their number.
+ */
+enum { SSD_NORM_RMS = 0, SSD_NORM_L2 = 1 };
+
+typedef struct {
+    int64_t B, L, H, G, N, nfreq;
+    const void *q;
+    const void *k;
+    const float *w_q;
+    const float *w_k;
+    const float *freqs;
+    const int32_t *positions;
+    void *q_out;
+    void *k_out;
+    int64_t q_stride[2], k_stride[2];
+    int32_t dtype, kind, interleaved;
+    float eps;
+} ssd_qk_norm_args;
+
+ssd_status ssd_qk_norm(const ssd_qk_norm_args *args, void *stream);
+
+/* Its backward: from q, k and the gradients dq_out, dk_out (dense) of the outputs, dq
+ * [B,L,H,N], dk [B,L,G,N] (dense), and dw_q, dw_k [N] fp32, each required with its
+ * weight.  q_out and k_out of `fwd` are ignored.  Outputs lie apart from the inputs
+ * and from each other (not checked).  Sums run in a fixed order. */
+typedef struct {
+    ssd_qk_norm_args fwd;
+    const void *dq_out;
+    const void *dk_out;
+    void *dq;
+    void *dk;
+    float *dw_q;
+    float *dw_k;
+    void *workspace;
+    size_t workspace_bytes;
+} ssd_qk_norm_bwd_args;
+
+ssd_status ssd_qk_norm_bwd_workspace_size(const ssd_qk_norm_bwd_args *args, size_t *bytes);
+ssd_status ssd_qk_norm_bwd(const ssd_qk_norm_bwd_args *args, void *stream);
+
 /* Self-test of the bounded device-side waits (no counterpart on the pages;
  * the pages' kernels report errors only as exceptions on the host).  Every
  * mbarrier wait in the tensor-core kernels gives up after a time limit

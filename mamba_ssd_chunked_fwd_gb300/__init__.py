@@ -22,7 +22,10 @@ import threading
 import torch
 
 from . import _build
+from . import delta as _delta
 from . import selective as _selective
+from .delta import (SSD_NORM_L2, SSD_NORM_RMS, SsdDeltaArgs, SsdDeltaBwdArgs, SsdDeltaStepArgs, SsdQkNormArgs, SsdQkNormBwdArgs,
+                    delta_rule, delta_rule_bwd, delta_rule_step, qk_norm, qk_norm_bwd)
 from .selective import (SsdBlockNormArgs, SsdBlockNormBwdArgs, SsdConvArgs, SsdConvBwdArgs, SsdConvStepArgs, SsdScanArgs,
                         SsdScanBwdArgs, SsdScanStepArgs, block_norm, block_norm_bwd, causal_conv1d_bwd,
                         causal_conv1d_carry, causal_conv1d_step, make_conv_args, make_scan_args, selective_scan,
@@ -41,6 +44,8 @@ __all__ = [
     "SsdScanArgs", "SsdScanBwdArgs", "SsdScanStepArgs", "make_scan_args", "selective_scan", "selective_scan_bwd",
     "selective_scan_step", "SsdConvArgs", "SsdConvBwdArgs", "SsdConvStepArgs", "make_conv_args", "causal_conv1d_carry",
     "causal_conv1d_bwd", "causal_conv1d_step", "SsdBlockNormArgs", "SsdBlockNormBwdArgs", "block_norm", "block_norm_bwd",
+    "SsdDeltaArgs", "SsdDeltaBwdArgs", "SsdDeltaStepArgs", "delta_rule", "delta_rule_bwd", "delta_rule_step",
+    "SSD_NORM_RMS", "SSD_NORM_L2", "SsdQkNormArgs", "SsdQkNormBwdArgs", "qk_norm", "qk_norm_bwd",
 ]
 
 SSD_F32, SSD_F16, SSD_BF16 = 0, 1, 2
@@ -143,6 +148,7 @@ _SIGS = {
     "ssd_state_fold": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
     **_selective.SIGNATURES,
+    **_delta.SIGNATURES,
 }
 
 

@@ -1,11 +1,11 @@
-// binding.cpp -- the Python side of the selective scan, its convolution and the
-// block norm, in C++: checks torch tensors, fills the C structures of
+// binding.cpp -- the Python side of the selective scan, its convolution, the
+// block norm, the gated delta rule and the norm of queries and keys, in C++: checks torch tensors, fills the C structures of
 // include/ssd.h, allocates outputs and workspaces with torch, and calls the
 // library on the stream it is given.  A single-token call takes a few
 // microseconds on the GPU; the same checks in Python take ten.
 //
-// Each function takes its arguments by position (selective.py has the
-// signatures), raises ValueError for what the binding cannot express, and
+// Each function takes its arguments by position (selective.py and
+// delta.py have the signatures), raises ValueError for what the binding cannot express, and
 // returns the result, or the library's status as an int when that is not 0.
 #include <Python.h>
 
@@ -15,6 +15,7 @@
 
 #include <dlfcn.h>
 
+#include <cmath>
 #include <sstream>
 #include <stdexcept>
 
@@ -34,7 +35,15 @@ namespace {
     X(ssd_causal_conv_step)                  \
     X(ssd_block_norm)                        \
     X(ssd_block_norm_bwd_workspace_size)     \
-    X(ssd_block_norm_bwd)
+    X(ssd_block_norm_bwd)                    \
+    X(ssd_delta_rule_workspace_size)         \
+    X(ssd_delta_rule)                        \
+    X(ssd_delta_rule_bwd_workspace_size)     \
+    X(ssd_delta_rule_bwd)                    \
+    X(ssd_delta_rule_step)                   \
+    X(ssd_qk_norm)                           \
+    X(ssd_qk_norm_bwd_workspace_size)        \
+    X(ssd_qk_norm_bwd)
 
 #define X(name) decltype(&::name) p_##name = nullptr;
 SSD_ENTRIES(X)
@@ -485,6 +494,194 @@ PyObject *block_norm_bwd(PyObject *const *a) {
     return d.release();
 }
 
+// ---- gated delta rule
+
+ScalarType gate_type(const Tensor &g, ScalarType io, const char *what) {
+    if (g.scalar_type() != io && g.scalar_type() != at::kFloat)
+        refuse(what, ": dtype ", g.scalar_type(), ", expected ", io, " or Float");
+    return g.scalar_type();
+}
+
+// scale, or 1 / sqrt(N) for None
+float scale_of(PyObject *o, int64_t n) { return o == Py_None ? (float)(1.0 / std::sqrt((double)n)) : (float)number(o); }
+
+// q, k, v, g, beta, scale, initial_states, lengths
+void delta_args(PyObject *const *a, const char *name, ssd_delta_args &p) {
+    const Tensor &q = needed(a[0], "q"), &k = needed(a[1], "k"), &v = needed(a[2], "v"), &g = needed(a[3], "g"), &beta = needed(a[4], "beta");
+    const int64_t dev = cuda_device(q, name);
+    ndim(q, 4, "q"), ndim(v, 4, "v");
+    p = ssd_delta_args{};
+    p.B = q.size(0), p.L = q.size(1), p.G = q.size(2), p.N = q.size(3), p.H = v.size(2), p.P = v.size(3);
+    const ScalarType io = q.scalar_type(), f32 = at::kFloat;
+    const int64_t vs[4] = {p.B, p.L, p.H, p.P}, gates[3] = {p.B, p.L, p.H}, state[4] = {p.B, p.H, p.P, p.N};
+    p.dtype = code_of(io, "q");
+    p.g_dtype = code_of(gate_type(g, io, "g"), "g"), p.beta_dtype = code_of(gate_type(beta, io, "beta"), "beta");
+    p.q = tokens(&q, q.sizes(), io, dev, "q", p.q_stride);
+    p.k = tokens(&k, q.sizes(), io, dev, "k", p.k_stride);
+    p.v = tokens(&v, vs, io, dev, "v", p.v_stride);
+    p.g = tokens(&g, gates, g.scalar_type(), dev, "g", p.g_stride);
+    p.beta = tokens(&beta, gates, beta.scalar_type(), dev, "beta", p.beta_stride);
+    p.scale = scale_of(a[5], p.N);
+    p.initial_state = dense<float>(tensor(a[6], "initial_states"), state, f32, dev, "initial_states");
+    p.lengths = dense<int32_t>(tensor(a[7], "lengths"), {p.B}, at::kInt, dev, "lengths");
+}
+
+// stream, the rule's 8, return_final_state, out
+PyObject *delta_rule(PyObject *const *a) {
+    ssd_delta_args p;
+    delta_args(a + 1, "delta_rule", p);
+    const Tensor &q = needed(a[1], "q"), &v = needed(a[3], "v");
+    const bool want = truth(a[9]);
+    Tensor y = output(a[10], v.sizes(), q, q.scalar_type(), q.get_device(), "out"), fin;
+    p.y = y.data_ptr();
+    if (want) {
+        fin = fresh({p.B, p.H, p.P, p.N}, q, at::kFloat);
+        p.final_state = fin.data_ptr<float>();
+    }
+    size_t bytes = 0;
+    ssd_status st = p_ssd_delta_rule_workspace_size(&p, &bytes);
+    if (st != SSD_OK) return status(st);
+    const Tensor ws = workspace(bytes, q);
+    if (bytes) p.workspace = ws.data_ptr(), p.workspace_bytes = bytes;
+    if ((st = p_ssd_delta_rule(&p, stream_of(a[0]))) != SSD_OK) return status(st);
+    return want ? pair(wrap(y), wrap(fin)) : wrap(y);
+}
+
+// stream, the rule's 8, dy, dfinal, want_dh0 (None: with initial_states)
+PyObject *delta_rule_bwd(PyObject *const *a) {
+    ssd_delta_bwd_args b = {};
+    delta_args(a + 1, "delta_rule_bwd", b.fwd);
+    const ssd_delta_args &p = b.fwd;
+    const Tensor &q = needed(a[1], "q"), &v = needed(a[3], "v"), &g = needed(a[4], "g"), &beta = needed(a[5], "beta"), &dy = needed(a[9], "dy");
+    const int64_t dev = q.get_device(), state[4] = {p.B, p.H, p.P, p.N};
+    b.dy = dense(&dy, v.sizes(), q.scalar_type(), dev, "dy");
+    b.dfinal = dense<float>(tensor(a[10], "dfinal"), state, at::kFloat, dev, "dfinal");
+    Dict d;
+    auto out = [&](const char *name, IntArrayRef shape, ScalarType type) {
+        Tensor t = fresh(shape, q, type);
+        put(d.d, name, t);
+        return t.data_ptr();
+    };
+    b.dq = out("dq", q.sizes(), q.scalar_type());
+    b.dk = out("dk", q.sizes(), q.scalar_type());
+    b.dv = out("dv", v.sizes(), q.scalar_type());
+    b.dg = out("dg", g.sizes(), g.scalar_type());
+    b.dbeta = out("dbeta", beta.sizes(), beta.scalar_type());
+    if (a[11] == Py_None ? p.initial_state != nullptr : truth(a[11])) b.dh0 = static_cast<float *>(out("dh0", state, at::kFloat));
+    size_t bytes = 0;
+    ssd_status st = p_ssd_delta_rule_bwd_workspace_size(&b, &bytes);
+    if (st != SSD_OK) return status(st);
+    const Tensor ws = workspace(bytes, q);
+    b.workspace = ws.data_ptr(), b.workspace_bytes = bytes;
+    if ((st = p_ssd_delta_rule_bwd(&b, stream_of(a[0]))) != SSD_OK) return status(st);
+    return d.release();
+}
+
+// stream, q, k, v, g, beta, state, scale, state_out, slots, out
+PyObject *delta_rule_step(PyObject *const *a) {
+    const Tensor &q = needed(a[1], "q"), &k = needed(a[2], "k"), &v = needed(a[3], "v"), &g = needed(a[4], "g"), &beta = needed(a[5], "beta"),
+                 &state = needed(a[6], "state");
+    const int64_t dev = cuda_device(q, "delta_rule_step");
+    ndim(q, 3, "q"), ndim(v, 3, "v"), ndim(state, 4, "state");
+    ssd_delta_step_args p = {};
+    p.B = q.size(0), p.G = q.size(1), p.N = q.size(2), p.H = v.size(1), p.P = v.size(2), p.nslots = state.size(0);
+    const ScalarType io = q.scalar_type(), f32 = at::kFloat;
+    p.dtype = code_of(io, "q");
+    p.g_dtype = code_of(gate_type(g, io, "g"), "g"), p.beta_dtype = code_of(gate_type(beta, io, "beta"), "beta");
+    const int64_t vs[3] = {p.B, p.H, p.P}, gates[2] = {p.B, p.H}, pool[4] = {p.nslots, p.H, p.P, p.N};
+    p.q = rows(&q, q.sizes(), io, dev, "q", p.q_row);
+    p.k = rows(&k, q.sizes(), io, dev, "k", p.k_row);
+    p.v = rows(&v, vs, io, dev, "v", p.v_row);
+    p.g = rows(&g, gates, g.scalar_type(), dev, "g", p.g_row);
+    p.beta = rows(&beta, gates, beta.scalar_type(), dev, "beta", p.beta_row);
+    float *s = dense<float>(&state, pool, f32, dev, "state"), *so = dense<float>(tensor(a[8], "state_out"), pool, f32, dev, "state_out");
+    p.state = s, p.state_out = so ? so : s;
+    p.slots = dense<int32_t>(tensor(a[9], "slots"), {p.B}, at::kInt, dev, "slots");
+    p.scale = scale_of(a[7], p.N);
+    Tensor y = output(a[10], v.sizes(), q, io, dev, "out");
+    p.y = y.data_ptr();
+    const ssd_status st = p_ssd_delta_rule_step(&p, stream_of(a[0]));
+    return st != SSD_OK ? status(st) : wrap(y);
+}
+
+// ---- norm of queries and keys
+
+// q, k, w_q, w_k, kind, eps, freqs, positions, interleaved
+void qk_norm_args(PyObject *const *a, const char *name, ssd_qk_norm_args &p) {
+    const Tensor &q = needed(a[0], "q"), &k = needed(a[1], "k");
+    const int64_t dev = cuda_device(q, name);
+    const bool single = q.dim() == 3;  // one token of each sequence: the sequences are the tokens of one row
+    if (!single) ndim(q, 4, "q");
+    ndim(k, q.dim(), "k");
+    p = ssd_qk_norm_args{};
+    p.B = single ? 1 : q.size(0), p.L = single ? q.size(0) : q.size(1), p.H = q.size(-2), p.N = q.size(-1), p.G = k.size(-2);
+    const ScalarType io = q.scalar_type(), f32 = at::kFloat;
+    p.dtype = code_of(io, "q");
+    if (single) {
+        const int64_t ks[3] = {p.L, p.G, p.N};
+        p.q = rows(&q, q.sizes(), io, dev, "q", p.q_stride[1]);
+        p.k = rows(&k, ks, io, dev, "k", p.k_stride[1]);
+    } else {
+        const int64_t ks[4] = {p.B, p.L, p.G, p.N};
+        p.q = tokens(&q, q.sizes(), io, dev, "q", p.q_stride);
+        p.k = tokens(&k, ks, io, dev, "k", p.k_stride);
+    }
+    p.w_q = dense<float>(tensor(a[2], "w_q"), {p.N}, f32, dev, "w_q");
+    p.w_k = dense<float>(tensor(a[3], "w_k"), {p.N}, f32, dev, "w_k");
+    p.kind = (int32_t)number(a[4]);
+    p.eps = (float)number(a[5]);
+    if (const Tensor *f = tensor(a[6], "freqs")) {
+        ndim(*f, 1, "freqs");
+        p.nfreq = f->size(0);
+        p.freqs = dense<float>(f, f->sizes(), f32, dev, "freqs");
+        if (single && a[7] == Py_None) refuse("positions are required for single tokens");
+    }
+    if (const Tensor *t = tensor(a[7], "positions")) {
+        if (single) p.positions = dense<int32_t>(t, {p.L}, at::kInt, dev, "positions");
+        else p.positions = dense<int32_t>(t, {p.B, p.L}, at::kInt, dev, "positions");
+    }
+    p.interleaved = truth(a[8]);
+}
+
+// stream, the norm's 9, out_q, out_k
+PyObject *qk_norm(PyObject *const *a) {
+    ssd_qk_norm_args p;
+    qk_norm_args(a + 1, "qk_norm", p);
+    const Tensor &q = needed(a[1], "q"), &k = needed(a[2], "k");
+    Tensor oq = output(a[10], q.sizes(), q, q.scalar_type(), q.get_device(), "out_q"),
+           ok = output(a[11], k.sizes(), q, q.scalar_type(), q.get_device(), "out_k");
+    p.q_out = oq.data_ptr(), p.k_out = ok.data_ptr();
+    const ssd_status st = p_ssd_qk_norm(&p, stream_of(a[0]));
+    return st != SSD_OK ? status(st) : pair(wrap(oq), wrap(ok));
+}
+
+// stream, the norm's 9, dq_out, dk_out
+PyObject *qk_norm_bwd(PyObject *const *a) {
+    ssd_qk_norm_bwd_args b = {};
+    qk_norm_args(a + 1, "qk_norm_bwd", b.fwd);
+    const Tensor &q = needed(a[1], "q"), &k = needed(a[2], "k");
+    const int64_t dev = q.get_device();
+    b.dq_out = dense(&needed(a[10], "dq_out"), q.sizes(), q.scalar_type(), dev, "dq_out");
+    b.dk_out = dense(&needed(a[11], "dk_out"), k.sizes(), q.scalar_type(), dev, "dk_out");
+    Dict d;
+    auto out = [&](const char *name, const Tensor &t) {
+        Tensor n = like(t);
+        put(d.d, name, n);
+        return n.data_ptr();
+    };
+    b.dq = out("dq", q);
+    b.dk = out("dk", k);
+    if (const Tensor *t = tensor(a[3], "w_q")) b.dw_q = static_cast<float *>(out("dw_q", *t));
+    if (const Tensor *t = tensor(a[4], "w_k")) b.dw_k = static_cast<float *>(out("dw_k", *t));
+    size_t bytes = 0;
+    ssd_status st = p_ssd_qk_norm_bwd_workspace_size(&b, &bytes);
+    if (st != SSD_OK) return status(st);
+    const Tensor ws = workspace(bytes, q);
+    if (bytes) b.workspace = ws.data_ptr(), b.workspace_bytes = bytes;
+    if ((st = p_ssd_qk_norm_bwd(&b, stream_of(a[0]))) != SSD_OK) return status(st);
+    return d.release();
+}
+
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
@@ -535,6 +732,11 @@ PyMethodDef methods[] = {{"load", load, METH_O, nullptr},
                          M(causal_conv1d_step, 9),
                          M(block_norm, 11),
                          M(block_norm_bwd, 10),
+                         M(delta_rule, 11),
+                         M(delta_rule_bwd, 12),
+                         M(delta_rule_step, 11),
+                         M(qk_norm, 12),
+                         M(qk_norm_bwd, 12),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ssd_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,328 @@
+// qk_norm.cu -- norm of queries and keys, head by head, with the rotation by
+// position in the same pass; forward and backward.
+//
+//   v = x / sqrt(mean(x^2) + eps) * w         (l2: the sum in place of the mean; w optional)
+//   pair i of v turns by the angle a = position * freqs[i]:  (v1, v2) -> (v1 cos a - v2 sin a, v2 cos a + v1 sin a)
+//
+// Backward, with d the incoming gradient turned by -a, r the inverse root and m the
+// divisor of the mean (N or 1):  dw = sum d x r,  dx = r (d w - x r^2 (d w . x) / m).
+//
+// Bound by HBM: each value is read once and written once.  A group of LPR lanes
+// holds a head's vector, two runs of Q elements to a lane, chosen so that both
+// members of a pair lie in one lane: no exchange but the sums.  The angles are worked out once
+// for a tile of tokens and shared by its heads through shared memory.
+#include "qk_norm.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHalf = 128;
+constexpr int kTokens = 8;  // most tokens of a tile
+
+// The position's turns are kept as a fraction of 2^64: position times
+// freq / (2 pi), whole turns dropped by the overflow.  The product loses nothing, however far
+// the position; freq / (2 pi) is off by 2^-52 of itself, 4e-10 of a turn at position 10^6.
+__device__ __forceinline__ unsigned long long turn_of(float freq) {
+    double f = (double)freq * 0.15915494309189535;  // 1 / (2 pi)
+    f -= floor(f);
+    return (unsigned long long)(f * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 cos_sin(unsigned long long turn, int position) {
+    const unsigned long long a = turn * (unsigned long long)(long long)position;
+    float c, s;
+    sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);  // half turns in [-1, 1)
+    return make_float2(c, s);
+}
+
+// Where unit u of a vector lies: its two runs of Q elements, and whether they are turned.
+struct Unit {
+    int a, b, f;  // first elements of the runs, first frequency
+    bool rot;
+};
+template <int Q>
+__device__ __forceinline__ Unit unit_of(int u, int half, int interleaved) {
+    Unit x;
+    if (interleaved) {
+        x.a = 2 * u * Q, x.b = x.a + Q, x.f = u * Q, x.rot = u * Q < half;
+    } else if (u * Q < half) {
+        x.a = u * Q, x.b = half + u * Q, x.f = u * Q, x.rot = true;
+    } else {
+        x.a = 2 * u * Q, x.b = x.a + Q, x.f = 0, x.rot = false;
+    }
+    return x;
+}
+
+template <int IO, int Q>
+struct Run {
+    Raw4 a, b;
+};
+template <int IO, int Q>
+__device__ __forceinline__ Raw4 load_run(const void *base, long long i, bool ok) {
+    if (Q == 4) return load_raw4<IO, true, false>(base, i, ok, 4);
+    return load_raw4<IO, false, false>(base, i, ok, 1);
+}
+template <int IO, int Q>
+__device__ __forceinline__ void unpack_run(const Raw4 &r, float (&v)[Q]) {
+    float f[4];
+    unpack4<IO, Q == 4>(r, f);
+#pragma unroll
+    for (int j = 0; j < Q; ++j) v[j] = f[j];
+}
+template <int IO, int Q>
+__device__ __forceinline__ void store_run(void *base, long long i, const float (&v)[Q]) {
+    const float f[4] = {v[0], Q == 4 ? v[Q > 1] : 0.f, Q == 4 ? v[Q > 2 ? 2 : 0] : 0.f, Q == 4 ? v[Q > 3 ? 3 : 0] : 0.f};
+    store4_io<IO, Q == 4>(base, i, Q, f);
+}
+
+// The pairs of a unit turned by their angles (sign -1: back).
+template <int Q>
+__device__ __forceinline__ void turn_unit(float (&a)[Q], float (&b)[Q], const float2 *cs, bool interleaved, float sign) {
+    float c[Q], s[Q];
+#pragma unroll
+    for (int j = 0; j < Q; ++j) c[j] = cs[j].x, s[j] = sign * cs[j].y;
+    if (Q == 1 || !interleaved) {
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = fmaf(x, c[j], -y * s[j]);
+            b[j] = fmaf(y, c[j], x * s[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < Q / 2; ++j) {
+            const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
+            a[2 * j] = fmaf(x, c[j], -y * s[j]), a[2 * j + 1] = fmaf(y, c[j], x * s[j]);
+            b[2 * j] = fmaf(z, c[j + Q / 2], -w * s[j + Q / 2]), b[2 * j + 1] = fmaf(w, c[j + Q / 2], z * s[j + Q / 2]);
+        }
+    }
+}
+
+template <int LPR>
+__device__ __forceinline__ float sum_group(float v) {
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+// One tensor's rows of a tile: `heads` of each of nt tokens, RU rows at a time so that their loads overlap.
+template <int IO, int Q, int M, int LPR, bool BWD>
+__device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long long tok0, int nt, const float2 *table, float (&dw)[M][2][Q]) {
+    constexpr int kGroups = kThreads / LPR, RU = M > 1 ? 1 : BWD ? 2 : 4;
+    const int heads = which ? p.G : p.H, ln = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const void *x = which ? p.k : p.q, *dy = which ? p.dk_out : p.dq_out;
+    const float *w = which ? p.w_k : p.w_q;
+    void *out = BWD ? (which ? p.dk : p.dq) : (which ? p.k_out : p.q_out);
+    const long long s0 = which ? p.ks[0] : p.qs[0], s1 = which ? p.ks[1] : p.qs[1];
+    const float div = p.l2 ? 1.f : 1.f / p.N;
+    Unit un[M];
+    bool oka[M], okb[M];
+    float wa[M][Q], wb[M][Q];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        un[m] = unit_of<Q>(ln + LPR * m, p.half, p.interleaved);
+        oka[m] = un[m].a < p.N, okb[m] = un[m].b < p.N;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            wa[m][j] = w && oka[m] ? __ldg(w + un[m].a + j) : 1.f;
+            wb[m][j] = w && okb[m] ? __ldg(w + un[m].b + j) : 1.f;
+        }
+    }
+    const int rows = nt * heads;
+    for (int r0 = grp; r0 - grp < rows; r0 += kGroups * RU) {  // the same number of rounds for every lane of a warp
+        Raw4 xa[RU][M], xb[RU][M], da[RU][M], db[RU][M];
+        long long to[RU];
+        int tk[RU];
+        bool ok[RU];
+#pragma unroll
+        for (int i = 0; i < RU; ++i) {
+            const int r = r0 + i * kGroups;
+            ok[i] = r < rows;
+            tk[i] = ok[i] ? r / heads : 0;
+            const int h = r - tk[i] * heads;
+            const long long t = tok0 + tk[i], at = (t / p.L) * s0 + (t % p.L) * s1 + (long long)h * p.N;
+            to[i] = (t * heads + h) * p.N;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                xa[i][m] = load_run<IO, Q>(x, at + un[m].a, ok[i] && oka[m]);
+                xb[i][m] = load_run<IO, Q>(x, at + un[m].b, ok[i] && okb[m]);
+                if (BWD) {
+                    da[i][m] = load_run<IO, Q>(dy, to[i] + un[m].a, ok[i] && oka[m]);
+                    db[i][m] = load_run<IO, Q>(dy, to[i] + un[m].b, ok[i] && okb[m]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RU; ++i) {
+            float a[M][Q], b[M][Q], sq = 0.f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                unpack_run<IO, Q>(xa[i][m], a[m]);
+                unpack_run<IO, Q>(xb[i][m], b[m]);
+#pragma unroll
+                for (int j = 0; j < Q; ++j) sq = fmaf(a[m][j], a[m][j], fmaf(b[m][j], b[m][j], sq));
+            }
+            const float inv = rsqrtf(fmaf(sum_group<LPR>(sq), div, p.eps));
+            if (!BWD) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) a[m][j] *= inv * wa[m][j], b[m][j] *= inv * wb[m][j];
+                    if (un[m].rot) turn_unit<Q>(a[m], b[m], table + tk[i] * p.half + un[m].f, p.interleaved, 1.f);
+                    if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, a[m]);
+                    if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, b[m]);
+                }
+                continue;
+            }
+            float ga[M][Q], gb[M][Q], dot = 0.f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                unpack_run<IO, Q>(da[i][m], ga[m]);
+                unpack_run<IO, Q>(db[i][m], gb[m]);
+                if (un[m].rot) turn_unit<Q>(ga[m], gb[m], table + tk[i] * p.half + un[m].f, p.interleaved, -1.f);
+#pragma unroll
+                for (int j = 0; j < Q; ++j) {
+                    if (ok[i]) {
+                        dw[m][0][j] = fmaf(ga[m][j], a[m][j] * inv, dw[m][0][j]);
+                        dw[m][1][j] = fmaf(gb[m][j], b[m][j] * inv, dw[m][1][j]);
+                    }
+                    ga[m][j] *= wa[m][j], gb[m][j] *= wb[m][j];
+                    dot = fmaf(ga[m][j], a[m][j], fmaf(gb[m][j], b[m][j], dot));
+                }
+            }
+            const float f = -inv * inv * inv * div * sum_group<LPR>(dot);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+#pragma unroll
+                for (int j = 0; j < Q; ++j) {
+                    ga[m][j] = fmaf(f, a[m][j], inv * ga[m][j]);
+                    gb[m][j] = fmaf(f, b[m][j], inv * gb[m][j]);
+                }
+                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, ga[m]);
+                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, gb[m]);
+            }
+        }
+    }
+}
+
+// The CTA's sums of dw, the groups one after another.
+template <int Q, int M, int LPR>
+__device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&dwq)[M][2][Q], const float (&dwk)[M][2][Q]) {
+    __shared__ float sums[2 * kMaxHalf * 2];
+    for (int i = threadIdx.x; i < 2 * p.N; i += kThreads) sums[i] = 0.f;
+    for (int g = 0; g < kThreads / LPR; ++g) {
+        __syncthreads();
+        if ((int)threadIdx.x / LPR != g) continue;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const Unit un = unit_of<Q>(threadIdx.x % LPR + LPR * m, p.half, p.interleaved);
+#pragma unroll
+            for (int j = 0; j < Q; ++j) {
+                if (un.a < p.N) sums[un.a + j] += dwq[m][0][j], sums[p.N + un.a + j] += dwk[m][0][j];
+                if (un.b < p.N) sums[un.b + j] += dwq[m][1][j], sums[p.N + un.b + j] += dwk[m][1][j];
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.N; i += kThreads) p.part[(size_t)blockIdx.x * 2 * p.N + i] = sums[i];
+}
+
+template <int IO, int Q, int M, int LPR, bool BWD>
+__global__ void __launch_bounds__(kThreads)
+qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile) {
+    __shared__ __align__(16) float2 table[kTokens * kMaxHalf];
+    __shared__ unsigned long long turn[kMaxHalf];
+    const long long tokens = (long long)p.B * p.L;
+    float dwq[M][2][Q] = {}, dwk[M][2][Q] = {};
+    for (int i = threadIdx.x; i < p.half; i += kThreads) turn[i] = turn_of(__ldg(p.freqs + i));
+    for (long long tok0 = (long long)blockIdx.x * tile; tok0 < tokens; tok0 += (long long)gridDim.x * tile) {
+        const int nt = (int)min((long long)tile, tokens - tok0);
+        if (p.half) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < nt * p.half; e += kThreads) {
+                const int t = e / p.half;
+                const long long tok = tok0 + t;
+                table[e] = cos_sin(turn[e - t * p.half], p.positions ? __ldg(p.positions + tok) : (int)(tok % p.L));
+            }
+            __syncthreads();
+        }
+        rows_of<IO, Q, M, LPR, BWD>(p, 0, tok0, nt, table, dwq);
+        rows_of<IO, Q, M, LPR, BWD>(p, 1, tok0, nt, table, dwk);
+    }
+    if constexpr (BWD) if (p.w_q || p.w_k) store_sums<Q, M, LPR>(p, dwq, dwk);
+}
+
+// dw_q, dw_k: the CTAs' sums, 8 threads to a column, each over every eighth row.
+__global__ void __launch_bounds__(256)
+qk_norm_weights_kernel(const __grid_constant__ QkNormParams p, int parts) {
+    __shared__ float s[8][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    float v = 0.f;
+    if (col < 2 * p.N)
+        for (int i = y; i < parts; i += 8) v += p.part[(size_t)i * 2 * p.N + col];
+    s[y][threadIdx.x & 31] = v;
+    __syncthreads();
+    if (y != 0 || col >= 2 * p.N) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x & 31];
+    if (col < p.N) {
+        if (p.dw_q) p.dw_q[col] = v;
+    } else if (p.dw_k) {
+        p.dw_k[col - p.N] = v;
+    }
+}
+
+// Tokens of a tile: as many as leave every SM eight CTAs.
+int tile_of(const QkNormParams &p) {
+    const long long tokens = (long long)p.B * p.L, most = tokens / (8LL * scan_sm_count());
+    int t = 1;
+    while (t < kTokens && 2 * t <= most) t *= 2;
+    return t;
+}
+
+template <int IO, int Q, int M, int LPR>
+cudaError_t norm_as(const QkNormParams &p, bool bwd, cudaStream_t s) {
+    const int tile = tile_of(p);
+    if (!bwd) {
+        const long long tiles = ((long long)p.B * p.L + tile - 1) / tile;
+        qk_norm_kernel<IO, Q, M, LPR, false><<<(unsigned)min(tiles, (long long)1 << 30), kThreads, 0, s>>>(p, tile);
+        return cudaGetLastError();
+    }
+    const int parts = qk_norm_parts(p);
+    qk_norm_kernel<IO, Q, M, LPR, true><<<parts, kThreads, 0, s>>>(p, tile);
+    if (p.w_q || p.w_k) qk_norm_weights_kernel<<<(2 * p.N + 31) / 32, 256, 0, s>>>(p, parts);
+    return cudaGetLastError();
+}
+
+template <int IO>
+cudaError_t norm_io(const QkNormParams &p, bool bwd, cudaStream_t s) {
+    auto fours = [&](const void *x) { return vec4_aligned(x, IO); };
+    bool vec = p.N % 4 == 0 && p.half % 4 == 0 && vec4_strided(p.q, IO, p.qs) && vec4_strided(p.k, IO, p.ks);
+    vec = vec && (bwd ? fours(p.dq_out) && fours(p.dk_out) && fours(p.dq) && fours(p.dk) : fours(p.q_out) && fours(p.k_out));
+    if (!vec) return norm_as<IO, 1, 4, 32>(p, bwd, s);
+    if (p.N <= 64) return norm_as<IO, 4, 1, 8>(p, bwd, s);
+    if (p.N <= 128) return norm_as<IO, 4, 1, 16>(p, bwd, s);
+    return norm_as<IO, 4, 1, 32>(p, bwd, s);
+}
+
+cudaError_t norm(const QkNormParams &p, int io, bool bwd, cudaStream_t s) {
+    switch (io) {
+        case IO_F32: return norm_io<IO_F32>(p, bwd, s);
+        case IO_F16: return norm_io<IO_F16>(p, bwd, s);
+        case IO_BF16: return norm_io<IO_BF16>(p, bwd, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int qk_norm_parts(const QkNormParams &p) {
+    const int tile = tile_of(p);
+    const long long tiles = ((long long)p.B * p.L + tile - 1) / tile, most = 4LL * scan_sm_count();
+    return (int)(tiles < most ? tiles : most);
+}
+cudaError_t launch_qk_norm(const QkNormParams &p, int io, cudaStream_t s) { return norm(p, io, false, s); }
+cudaError_t launch_qk_norm_bwd(const QkNormParams &p, int io, cudaStream_t s) { return norm(p, io, true, s); }
+
+}  // namespace ssd
