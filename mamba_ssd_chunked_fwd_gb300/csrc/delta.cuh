@@ -22,6 +22,10 @@ struct DeltaParams {
     int g32, b32;                                 // g, beta are fp32
     float scale;
     int nc;  // chunks of a row
+    // segments: tokens [s seg_len, (s+1) seg_len) of every row; seg_len a multiple of 64
+    int nseg, seg_len;
+    float *seg_states;  // [B,H,nseg,P,N] state entering a segment (slot 0 unused)
+    float *seg_trans;   // [B,H,nseg-1,N,N] a segment's transition: the state after it is S trans + (its own)
     // backward
     const void *dy;
     const float *dfinal;
@@ -47,6 +51,8 @@ struct DeltaStepParams {
 };
 
 cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);          // y, final_state
+bool delta_tc_takes(const DeltaParams &p, int io);
+cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s);            // the same in chunks
 cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s);
 cudaError_t launch_delta_states(const DeltaParams &p, int io, cudaStream_t s);        // states, u
 cudaError_t launch_delta_adjoint(const DeltaParams &p, int io, cudaStream_t s);       // adj, dr, dv, dh0

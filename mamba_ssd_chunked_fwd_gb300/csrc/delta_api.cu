@@ -132,7 +132,10 @@ ssd_status ssd_delta_rule(const ssd_delta_args *a, void *stream) {
                len = {a->lengths, a->B * sizeof(int32_t), "lengths"};
     if ((st = apart(y, {q, k, v, g, beta, h0, len, fin})) != SSD_OK) return st;
     if ((st = apart(fin, {q, k, v, g, beta, h0, len})) != SSD_OK) return st;
-    cudaError_t e = ssd::launch_delta_walk(p, a->dtype, static_cast<cudaStream_t>(stream));
+    p.nseg = 1;
+    p.seg_len = p.nc * ssd::kDeltaChunk;
+    cudaError_t e = ssd::delta_tc_takes(p, a->dtype) ? ssd::launch_delta_tc(p, a->dtype, static_cast<cudaStream_t>(stream))
+                                                     : ssd::launch_delta_walk(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "delta_rule");
     return ok();
 }

@@ -186,8 +186,10 @@ def test_padding_does_not_leak(shape, t):
 @pytest.mark.parametrize("offset", [8, 1])
 @pytest.mark.parametrize("shape", [(2, 150, 4, 2, 128, 128), (2, 70, 2, 1, 40, 20)])
 def test_strided_inputs(shape, t, offset):
-    """q, k and v as slices of one projection, g and beta as slices of another."""
-    k = cuda(make(*shape, t, g32=False))
+    """q, k and v as slices of one projection, g and beta as slices of another: to the bit what dense
+    tensors give where the slices are aligned as those are; elsewhere another kernel may take them."""
+    host = make(*shape, t, g32=False)
+    k = cuda(host)
     B, L = shape[:2]
     widths = [k[n][0, 0].numel() for n in NAMES]
     wide = torch.full((B, L, sum(widths) + 5 * offset), float("nan"), device="cuda", dtype=t)
@@ -198,11 +200,18 @@ def test_strided_inputs(shape, t, offset):
         s[n] = wide[..., at:at + w].unflatten(-1, k[n].shape[2:])
         at += w
     dy, df = grads(k)
-    for a, b in zip(gpu(s), gpu(k)):
-        assert torch.equal(a, b)
-    a, b = gpu_bwd(s, dy.cuda(), df.cuda()), gpu_bwd(k, dy.cuda(), df.cuda())
-    for n in a:
-        assert torch.equal(a[n], b[n]), n
+    a, ab = gpu(s), gpu_bwd(s, dy.cuda(), df.cuda())
+    if offset == 8 or t == F32:
+        b, bb = gpu(k), gpu_bwd(k, dy.cuda(), df.cuda())
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        for n in ab:
+            assert torch.equal(ab[n], bb[n]), n
+        return
+    for x, y in zip(a, plain(host)):
+        close(x, y)
+    want = plain_bwd(host, dy.cpu(), df.cpu())
+    for n in ab:
+        close(ab[n], want[n], n)
 
 
 @pytest.mark.parametrize("t", [F32, BF16])
