@@ -195,12 +195,12 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         tc::tmem_alloc(tc::smem_addr(&tmem_slot), TM::COLS);
         tc::tmem_relinquish();
     }
-    // the blocks of T above its diagonal stay zero
-    for (int e = tid; e < 2 * 16384 / 16; e += kThreads) tcop::st_shared_v4(sbase + SM::T + 16 * e, 0u, 0u, 0u, 0u);
+    // the blocks of T and M above their diagonals stay zero
+    for (int e = tid; e < 4 * 16384 / 16; e += kThreads) tcop::st_shared_v4(sbase + SM::T + 16 * e, 0u, 0u, 0u, 0u);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's, so they begin at column 0
     Waits wait{bars};
 
     if (warp < kChainWarps) {
@@ -393,13 +393,9 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             const float gh = gt.gh[i], gl = gt.gl[i], beta = gt.beta[i];
             const int last = (i | 31);  // of the warp's rows
 #pragma unroll 1
-            for (int j0 = 0; j0 < kC; j0 += 16) {
+            for (int j0 = 0; j0 <= last; j0 += 16) {
                 float v[16];
-                if (j0 <= last) tc::tmem_ld16(tl + TM::KQ + j0, v);
-                else {
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) v[m] = 0.f;
-                }
+                tc::tmem_ld16(tl + TM::KQ + j0, v);
 #pragma unroll
                 for (int m = 0; m < 16; m += 4) {
                     const int j = j0 + m;
@@ -506,6 +502,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             const bool ok = row < rows;
             const size_t step = (size_t)p.H * p.P;
             const size_t base = ((size_t)w.b * p.L * p.H + w.h) * p.P + w.p0 + row;
+            const int odd = lane & 1;
+            uint16_t *y = static_cast<uint16_t *>(p.y) + base - odd + odd * step;  // of an odd lane: the token after, from the row before
             for (int c = 0; c < w.chunks; ++c) {
                 const uint32_t par = c & 1;
                 const Gates &gt = gates[c % kSlots];
@@ -532,14 +530,18 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 tc::fence_after_sync();
                 const int tc0 = w.t0 + c * kC, n = min(kC, w.t1 - tc0);
                 const float scale = wait.dead ? __int_as_float(0x7fffffff) : p.scale;
+                uint16_t *to = y + (size_t)tc0 * step;
 #pragma unroll 1
-                for (int j = 0; j < kC; j += 16) {
+                for (int j = 0; j < kC; j += 16, to += 16 * step) {
                     float v[16];
                     tc::tmem_ld16(tl + j, v);
-                    const size_t to = base + (size_t)(tc0 + j) * step;
+                    // neighbouring lanes exchange: each then has two rows of every second token, a store of 4 bytes
 #pragma unroll
-                    for (int m = 0; m < 16; ++m)
-                        if (ok && j + m < n) st_io<IO>(p.y, to + m * step, scale * v[m]);
+                    for (int m = 0; m < 16; m += 2) {
+                        const uint32_t own = tcop::pack2(scale * v[m], scale * v[m + 1], BF16), other = __shfl_xor_sync(0xffffffffu, own, 1);
+                        const uint32_t two = __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+                        if (ok && j + m + odd < n) *reinterpret_cast<uint32_t *>(to + m * step) = two;
+                    }
                 }
                 tc::fence_before_sync();
                 tc::mbar_arrive(bars + 8 * kD4Read);
@@ -549,31 +551,36 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 for (int t = max(w.t1, w.t0); t < end; ++t) st_io<IO>(p.y, base + (size_t)t * step, 0.f);
         }
     } else if (set_registers<kMmaRegs, false>(); warp == kMmaWarp) {
-        // ---- the products
-        if (lane == 0) {
-            constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false), ID_V = tc::idesc_f16(128, kC, BF16, true, false),
-                               ID_DS = tc::idesc_f16(128, NN, BF16, false, true);
-            constexpr int NK = NN / 16;  // steps of 16 along a state's columns
-            auto s_term = [&](int k, int term) {  // 16 columns of the state's operand: first or second term
-                return tmem + TM::S + (k / (NK / 2)) * (NN / 2) + term * (NN / 4) + (k % (NK / 2)) * 8;
-            };
-            auto x_term = [&](uint32_t x, int k, int term) { return tmem + x + (k >> 1) * 32 + term * 16 + (k & 1) * 8; };
-            auto kq_product = [&](int c) {  // [k; q] k^T
-                const uint32_t kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES;
-                wait.on(kFullKQ + c % kStages, (c / kStages) & 1);
-                wait.on(kKQRead, (c & 1) ^ 1);
-                tc::fence_after_sync();
+        // ---- the products.  The warp stays together and one elected lane issues: the descriptors
+        // are then the warp's, not a thread's, and a product costs a few instructions in place of
+        // a dozen (measured beside busy warps: 16 products 540 to 2100 cycles, from a lane's branch 830 to 15000)
+        const bool go = tc::elect_one();
+        constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false), ID_V = tc::idesc_f16(128, kC, BF16, true, false),
+                           ID_DS = tc::idesc_f16(128, NN, BF16, false, true);
+        constexpr int NK = NN / 16;  // steps of 16 along a state's columns
+        auto s_term = [&](int k, int term) {  // 16 columns of the state's operand: first or second term
+            return tmem + TM::S + (k / (NK / 2)) * (NN / 2) + term * (NN / 4) + (k % (NK / 2)) * 8;
+        };
+        auto x_term = [&](uint32_t x, int k, int term) { return tmem + x + (k >> 1) * 32 + term * 16 + (k & 1) * 8; };
+        auto kq_product = [&](int c) {  // [k; q] k^T
+            const uint32_t kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES;
+            wait.on(kFullKQ + c % kStages, (c / kStages) & 1);
+            wait.on(kKQRead, (c & 1) ^ 1);
+            tc::fence_after_sync();
+            if (go) {
 #pragma unroll
                 for (int k = 0; k < NK; ++k)
                     tc::mma_f16(tmem + TM::KQ, tc::desc(kq + k * 4096, 2048, 128), tc::desc(kq + k * 4096, 2048, 128), ID, k > 0);
                 tc::commit(bars + 8 * kKQDone);
-            };
-            if (w.chunks > 0) kq_product(0);
-            for (int c = 0; c < w.chunks; ++c) {
-                const uint32_t par = c & 1, kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, v = sbase + SM::V + (c % kVStages) * SM::V_BYTES;
-                const uint32_t T = sbase + SM::T + par * 16384, M = sbase + SM::M + par * 16384;
-                wait.on(kS, par);
-                tc::fence_after_sync();
+            }
+        };
+        if (w.chunks > 0) kq_product(0);
+        for (int c = 0; c < w.chunks; ++c) {
+            const uint32_t par = c & 1, kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, v = sbase + SM::V + (c % kVStages) * SM::V_BYTES;
+            const uint32_t T = sbase + SM::T + par * 16384, M = sbase + SM::M + par * 16384;
+            wait.on(kS, par);
+            tc::fence_after_sync();
+            if (go) {
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {  // S k^T
                     const uint64_t b = tc::desc(kq + k * 4096, 2048, 128);
@@ -581,21 +588,12 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     tc::mma_f16_ts(tmem + TM::X1, s_term(k, 1), b, ID, 1);
                 }
                 tc::commit(bars + 8 * kD1);
-                if (!LOCAL) {
-                    wait.on(kD4Read, par ^ 1);
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < NK; ++k) {  // S q^T
-                        const uint64_t b = tc::desc(kq + 1024 + k * 4096, 2048, 128);
-                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 0), b, ID, k > 0);
-                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 1), b, ID, 1);
-                    }
-                    tc::commit(bars + 8 * kD3);
-                }
-                if (c + 1 < w.chunks) kq_product(c + 1);
-                wait.on(kFullT + par, (c >> 1) & 1);
-                wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
-                tc::fence_after_sync();
+            }
+            if (c + 1 < w.chunks) kq_product(c + 1);
+            wait.on(kFullT + par, (c >> 1) & 1);
+            wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
+            tc::fence_after_sync();
+            if (go) {
                 if (!unit) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {  // v^T (T diag(beta))^T
@@ -605,8 +603,10 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     }
                 }
                 tc::commit(bars + 8 * (kEmptyV + c % kVStages));
-                wait.on(kR, par);
-                tc::fence_after_sync();
+            }
+            wait.on(kR, par);
+            tc::fence_after_sync();
+            if (go) {
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k) {  // - (exp(G) S k^T) (T diag(beta))^T
                     const uint64_t hi = tc::desc(T + k * 2048, 1024, 128), lo = tc::desc(T + 8192 + k * 2048, 1024, 128);
@@ -615,8 +615,23 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k, 1), hi, ID, 1);
                 }
                 tc::commit(bars + 8 * kD2);
-                wait.on(kU, par);
+            }
+            if (!LOCAL) {  // while the chain splits U
+                wait.on(kD4Read, par ^ 1);
                 tc::fence_after_sync();
+                if (go) {
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {  // S q^T
+                        const uint64_t b = tc::desc(kq + 1024 + k * 4096, 2048, 128);
+                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 0), b, ID, k > 0);
+                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 1), b, ID, 1);
+                    }
+                    tc::commit(bars + 8 * kD3);
+                }
+            }
+            wait.on(kU, par);
+            tc::fence_after_sync();
+            if (go) {
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k) {  // the change of the state
                     const uint64_t b = tc::desc(kq + k * 256, 128, 2048);
@@ -625,9 +640,11 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 }
                 tc::commit(bars + 8 * kDS);
                 tc::commit(bars + 8 * (kEmptyKQ + c % kStages));
-                if (!LOCAL) {
-                    wait.on(kD3Read, par);
-                    tc::fence_after_sync();
+            }
+            if (!LOCAL) {
+                wait.on(kD3Read, par);
+                tc::fence_after_sync();
+                if (go) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {  // U^T M^T
                         const uint64_t hi = tc::desc(M + k * 2048, 1024, 128), lo = tc::desc(M + 8192 + k * 2048, 1024, 128);
@@ -637,11 +654,11 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     }
                     tc::commit(bars + 8 * kD4);
                 }
-                tc::commit(bars + 8 * (kEmptyT + par));
             }
-            // the last products may still read shared memory: wait for them before the CTA ends
-            if (w.chunks > 0) wait.on(kEmptyT + ((w.chunks - 1) & 1), ((w.chunks - 1) >> 1) & 1);
+            if (go) tc::commit(bars + 8 * (kEmptyT + par));
         }
+        // the last products may still read shared memory: wait for them before the CTA ends
+        if (w.chunks > 0) wait.on(kEmptyT + ((w.chunks - 1) & 1), ((w.chunks - 1) >> 1) & 1);
         __syncwarp();
     } else if (warp == kLoadWarp) {
         // ---- copies: lane = row of eight, 16-byte piece of four
@@ -700,7 +717,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, TM::COLS);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem_slot, TM::COLS);
 }
 
 template <int IO, int NN>
@@ -734,7 +751,7 @@ bool by_eights(const void *p, long long s0, long long s1) {
 // 16-byte pieces of k, q and v, and float4 of the states.
 bool delta_tc_takes(const DeltaParams &p, int io) {
     return io != IO_F32 && p.N % 8 == 0 && p.P % 8 == 0 && by_eights(p.k, p.ks[0], p.ks[1]) && by_eights(p.q, p.qs[0], p.qs[1]) &&
-           by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0);
+           by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0);
 }
 
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s) {
