@@ -86,6 +86,14 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
     lo = tcop::pack2(d.x, d.y, BF16);
 }
 
+// ex2 that stays where it is: moved into a branch on whether its result is wanted, each would wait for the one before
+// (measured: 68 cycles an element in place of 20).
+__device__ __forceinline__ float ex2_now(float v) {
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // D (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums.
 template <bool BF16>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -390,7 +398,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kKQDone, par);
             wait.on(kEmptyT + par, half_par ^ 1);
             tc::fence_after_sync();
-            const float gh = gt.gh[i], gl = gt.gl[i], beta = gt.beta[i];
+            const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
+            const int limit = pw < 2 ? i : i + 1;
             const int last = (i | 31);  // of the warp's rows
 #pragma unroll 1
             for (int j0 = 0; j0 <= last; j0 += 16) {
@@ -400,11 +409,13 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 for (int m = 0; m < 16; m += 4) {
                     const int j = j0 + m;
                     const float4 h4 = *reinterpret_cast<const float4 *>(&gt.gh[j]), l4 = *reinterpret_cast<const float4 *>(&gt.gl[j]);
-                    const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = ex2((gh - hs[e]) + (gl - ls[e]));
-                        v[m + e] = pw < 2 ? (j + e < i ? beta * d * v[m + e] : 0.f) : (j + e <= i ? d * v[m + e] : 0.f);
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 d = __fadd2_rn(__fadd2_rn(dup(gh), e ? make_float2(-h4.z, -h4.w) : make_float2(-h4.x, -h4.y)),
+                                                    __fadd2_rn(dup(gl), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y)));
+                        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(ex2_now(d.x), ex2_now(d.y)), dup(factor)), make_float2(v[m + e], v[m + e + 1]));
+                        v[m + e] = j + e < limit ? x.x : 0.f;
+                        v[m + e + 1] = j + e + 1 < limit ? x.y : 0.f;
                     }
                 }
                 if (pw < 2) {
