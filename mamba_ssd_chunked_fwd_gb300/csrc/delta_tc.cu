@@ -15,9 +15,10 @@
 // three products to a chunk; the rest runs beside it:
 //
 //   8 warps  the chain: split S K^T, U and S into operands; the state's fp32 in registers
-//   4 warps  A, T and M of the next chunk, and the gates
-//   4 warps  y
-//   1 warp   issues the products;  1 warp copies k, q and v, up to two chunks ahead
+//   4 warps  A and T of the next chunk
+//   4 warps  y, and M of the next chunk
+//   1 warp   issues the products
+//   3 warps  copy k, q and v ahead; the third works out the gates
 //
 // Operands.  q, k and v are 16-bit as they come.  What is computed (S, S K^T, U, T, M) goes
 // into a product as the sum of two 16-bit numbers, so that states keep 16 bits (bf16:
@@ -41,11 +42,10 @@ namespace {
 constexpr int kC = kDeltaChunk;
 constexpr int kChainWarps = 8, kPrepWarps = 4, kOutWarps = 4;
 constexpr int kPrepWarp0 = kChainWarps, kOutWarp0 = kPrepWarp0 + kPrepWarps, kMmaWarp = kOutWarp0 + kOutWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = (kLoadWarp + 3) * 32;  // whole warpgroups: registers are dealt out by them
+constexpr int kThreads = (kLoadWarp + 3) * 32;  // three warps copy: k, q, and v with the gates
 // Registers a thread, per warpgroup: 96 at launch; the chain 144 (its state is 64 of them), y 56, the last
 // warpgroup 40.  2 * 144 + 96 + 56 + 40 = 5 * 96.
 constexpr int kChainRegs = 144, kOutRegs = 56, kMmaRegs = 40;
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kStages = 3;   // of k and q
 constexpr int kVStages = 2;  // of v
 constexpr int kSlots = 4;    // of a chunk's gates
@@ -64,8 +64,8 @@ struct Smem {
     static constexpr uint32_t A = M + 2 * 16384, GATES = A + kC * kAW * 4, BYTES = GATES + kSlots * (uint32_t)sizeof(Gates) + 128;
 };
 
-enum Bar { kFullKQ = 0, kEmptyKQ = 3, kFullV = 6, kEmptyV = 8, kFullT = 10, kEmptyT = 12, kKQDone = 14, kKQRead, kD1, kR, kD2, kU, kDS, kS, kD3, kD3Read,
-           kD4, kD4Read, kBars };
+enum Bar { kFullKQ = 0, kEmptyKQ = 3, kFullV = 6, kEmptyV = 8, kFullT = 10, kEmptyT = 12, kFullM = 14, kFullG = 16, kKQDone = 20, kKQRead, kD1, kD2, kDS,
+           kD3, kD3Read, kD4, kD4Read, kUOut, kS, kR = kS + 4, kU = kR + 2, kBars = kU + 2 };
 
 // TMEM columns.
 template <int NN>
@@ -82,7 +82,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 template <bool BF16>
 __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
     hi = tcop::pack2(v.x, v.y, BF16);
-    const float2 h = unpack2<BF16>(hi), d = __fadd2_rn(v, make_float2(-h.x, -h.y));
+    const float2 d = __ffma2_rn(unpack2<BF16>(hi), make_float2(-1.f, -1.f), v);
     lo = tcop::pack2(d.x, d.y, BF16);
 }
 
@@ -105,6 +105,61 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// A chunk's gates by one warp, two tokens to a lane: the running sum of g as the sum of two floats, so that
+// differences keep their precision.
+__device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], const float (&beta)[2], int lane) {
+    auto add = [](float &h0, float &l0, float h1, float l1) {
+        const float sum = h0 + h1, t = sum - h0, err = (h0 - (sum - t)) + (h1 - t) + l0 + l1;
+        h0 = sum + err;
+        l0 = err - (h0 - sum);
+    };
+    float hi[2], lo[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float g = graw[m];
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // exp(-200) is 0, and sums stay finite
+        hi[m] = g * kLog2e;
+        lo[m] = fmaf(g, kLog2e, -hi[m]) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
+        gt.beta[2 * lane + m] = beta[m];
+    }
+    add(hi[1], lo[1], hi[0], lo[0]);
+    float th = hi[1], tl = lo[1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float oh = __shfl_up_sync(0xffffffffu, th, m), ol = __shfl_up_sync(0xffffffffu, tl, m);
+        if (lane >= m) add(th, tl, oh, ol);
+    }
+    const float ph = __shfl_up_sync(0xffffffffu, th, 1), pl = __shfl_up_sync(0xffffffffu, tl, 1);
+    if (lane > 0) add(hi[0], lo[0], ph, pl);
+    hi[1] = th, lo[1] = tl;
+    const float eh = __shfl_sync(0xffffffffu, th, 31), el = __shfl_sync(0xffffffffu, tl, 31);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int t = 2 * lane + m;
+        const float in = exp2f(hi[m] + lo[m]);
+        gt.gh[t] = hi[m], gt.gl[t] = lo[m], gt.into[t] = in, gt.neg_into[t] = -in;
+        gt.out[t] = exp2f((eh - hi[m]) + (el - lo[m]));
+    }
+    if (lane == 0) gt.over = exp2f(eh + el);
+}
+
+// 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
+__device__ __forceinline__ void decayed(float (&v)[16], const Gates &gt, int j0, float gh, float gl, float factor, int limit) {
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+        const int j = j0 + m;
+        const float4 h4 = *reinterpret_cast<const float4 *>(&gt.gh[j]), l4 = *reinterpret_cast<const float4 *>(&gt.gl[j]);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const float2 d = __fadd2_rn(__fadd2_rn(dup(gh), e ? make_float2(-h4.z, -h4.w) : make_float2(-h4.x, -h4.y)),
+                                        __fadd2_rn(dup(gl), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y)));
+            const float2 x = __fmul2_rn(__fmul2_rn(make_float2(ex2_now(d.x), ex2_now(d.y)), dup(factor)), make_float2(v[m + e], v[m + e + 1]));
+            v[m + e] = j + e < limit ? x.x : 0.f;
+            v[m + e + 1] = j + e + 1 < limit ? x.y : 0.f;
+        }
+    }
+}
+
 // A 16 x 16 block as the A operand of a product, in two terms.
 struct Frag {
     uint32_t hi[4], lo[4];
@@ -115,6 +170,15 @@ __device__ __forceinline__ Frag to_frag(const float (&acc)[2][4]) {
     Frag f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) split2<BF16>(make_float2(acc[i >> 1][2 * (i & 1)], acc[i >> 1][2 * (i & 1) + 1]), f.hi[i], f.lo[i]);
+    return f;
+}
+// Of a block in shared memory, rows kAW apart.
+template <bool BF16>
+__device__ __forceinline__ Frag load_frag(const float *x, int lane) {
+    const float *at = x + (lane >> 2) * kAW + 2 * (lane & 3);
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<BF16>(*reinterpret_cast<const float2 *>(at + (i & 1) * 8 * kAW + (i >> 1) * 8), f.hi[i], f.lo[i]);
     return f;
 }
 // acc += a X^T with X a 16 x 16 block of `x`, rows kAW apart.
@@ -138,18 +202,41 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  : "memory");
 }
 
+// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 16 columns on.
+template <bool BF16>
+__device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4 *>(f16 + 4 * i);
+        split2<BF16>(__fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
+        split2<BF16>(__fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
+    }
+    tc::tmem_st8(to, hi);
+    tc::tmem_st8(to + 16, lo);
+}
+
 template <int N, bool MORE>
 __device__ __forceinline__ void set_registers() {
     if (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A thread's waits: once one has given up, the rest return at once.
+// A thread's waits: each lasts 2000 tries of up to a millisecond; once one has given up, the rest return
+// at once.  Short code: five kinds of warps run side by side, and what they run has to stay in the
+// instruction cache (with unrolled loops and longer waits every second cycle went to fetching).
 struct Waits {
     uint32_t bars;
-    bool dead = false;
+    uint32_t tries = 2000;
+    __device__ __forceinline__ bool dead() const { return tries == 0; }
     __device__ __forceinline__ void on(int bar, uint32_t parity) {
-        if (!dead && !tc::mbar_wait(bars + 8 * bar, parity, kWaitNs)) dead = true;
+        uint32_t done = 0;
+#pragma unroll 1
+        for (uint32_t i = 0; i < tries && !done; ++i)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\tselp.u32 %0, 1, 0, p;\n}\n"
+                         : "=r"(done) : "r"(bars + 8 * bar), "r"(parity) : "memory");
+        tries = done ? tries : 0u;
+        asm volatile("" : "+r"(tries));  // or the code after it is laid out twice, for a thread that waits and one that does not
     }
 };
 
@@ -191,12 +278,13 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
 
     if (tid == 0) {
         auto init = [&](int bar, uint32_t count) { tc::mbar_init(bars + 8 * bar, count); };
-        for (int i = 0; i < kStages; ++i) init(kFullKQ + i, 32), init(kEmptyKQ + i, 1);
-        for (int i = 0; i < 2; ++i) init(kFullV + i, 32), init(kEmptyV + i, 1), init(kFullT + i, kPrepWarps * 32), init(kEmptyT + i, 1);
+        for (int i = 0; i < kStages; ++i) init(kFullKQ + i, 64), init(kEmptyKQ + i, 1);
+        for (int i = 0; i < 2; ++i) init(kFullV + i, 32), init(kEmptyV + i, 1), init(kFullT + i, kPrepWarps * 32), init(kEmptyT + i, 1), init(kFullM + i, 64);
+        for (int i = 0; i < kSlots; ++i) init(kFullG + i, 32);
         for (int b : {(int)kKQDone, (int)kD1, (int)kD2, (int)kDS, (int)kD3, (int)kD4}) init(b, 1);
-        init(kKQRead, kPrepWarps * 32);
-        for (int b : {(int)kR, (int)kU, (int)kS}) init(b, kChainWarps * 32);
-        init(kD3Read, kOutWarps * 32), init(kD4Read, kOutWarps * 32);
+        init(kKQRead, 128);
+        for (int b = kS; b < kBars; ++b) init(b, kChainWarps * 32);
+        init(kUOut, kChainWarps * 32), init(kD3Read, kOutWarps * 32), init(kD4Read, kOutWarps * 32);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -239,91 +327,76 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         } else {
             load_row(p.h0 ? p.h0 + bh * pn + (size_t)w.p0 * p.N : nullptr);
         }
-        auto publish = [&]() {  // the state as an operand: terms of 16 columns side by side
+        const uint32_t x1 = tl + TM::X1 + 32 * half, x2 = tl + TM::X2 + 32 * half;
+#pragma unroll 1
+        for (int c = 0;; ++c) {
+            const uint32_t par = c & 1;
+            if (c > 0) {
+                wait.on(kDS, par ^ 1);
+                tc::fence_after_sync();
+            }
+            const float2 over = dup(c > 0 ? gates[(c - 1) % kSlots].over : 1.f);
+            // the state after the chunk before, by 16 columns, and each of them as an operand: the product with k
+            // begins with the first
 #pragma unroll
             for (int j = 0; j < NH / 16; ++j) {
-                uint32_t hi[8], lo[8];
+                if (c > 0) {
+                    float v[16];
+                    tc::tmem_ld16(tl + TM::DS + half * NH + 16 * j, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split2<BF16>(S[8 * j + i], hi[i], lo[i]);
-                tc::tmem_st8(tl + TM::S + half * NH + 8 * j, hi);
-                tc::tmem_st8(tl + TM::S + half * NH + NH / 2 + 8 * j, lo);
+                    for (int i = 0; i < 8; ++i) S[8 * j + i] = __ffma2_rn(over, S[8 * j + i], make_float2(v[2 * i], v[2 * i + 1]));
+                }
+                if (c < w.chunks) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split2<BF16>(S[8 * j + i], hi[i], lo[i]);
+                    tc::tmem_st8(tl + TM::S + half * NH + 8 * j, hi);
+                    tc::tmem_st8(tl + TM::S + half * NH + NH / 2 + 8 * j, lo);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(bars + 8 * (kS + j));
+                }
             }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(bars + 8 * kS);
-        };
-        if (w.chunks > 0) publish();
-        for (int c = 0; c < w.chunks; ++c) {
-            const uint32_t par = c & 1;
+            if (c >= w.chunks) break;
             const Gates &gt = gates[c % kSlots];
-            wait.on(kFullT + par, (c >> 1) & 1);  // the gates
+            wait.on(kFullG + c % kSlots, (c / kSlots) & 1);
             wait.on(kD1, par);
             tc::fence_after_sync();
-            const uint32_t x1 = tl + TM::X1 + 32 * half, x2 = tl + TM::X2 + 32 * half;
-            {
-                float a[16], b[16];
-                tc::tmem_ld16x2(x1, x1 + 16, a, b);
+            // -exp(G) S k^T, by 16 tokens: the product with T begins with the first.  Twice 16 columns hold first terms, then
+            // second ones, so the values of both are read first
+            float v[2][16];
+            tc::tmem_ld16x2(x1, x1 + 16, v[0], v[1]);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const float(&v)[16] = s ? b : a;
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&gt.neg_into[32 * half + 16 * s + 4 * i]);
-                        split2<BF16>(__fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
-                        split2<BF16>(__fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tc::tmem_st8(x1 + 8 * s, hi);
-                    tc::tmem_st8(x1 + 16 + 8 * s, lo);
-                }
+            for (int s = 0; s < 2; ++s) {
+                split_scaled<BF16>(v[s], &gt.neg_into[32 * half + 16 * s], x1 + 8 * s);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * (kR + s));
             }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(bars + 8 * kR);
-
             wait.on(kD2, par);
             tc::fence_after_sync();
-            {
-                float a[16], b[16];
-                tc::tmem_ld16x2(x2, x2 + 16, a, b);
+            // what U adds to the state, then (for y) U itself
+            tc::tmem_ld16x2(x2, x2 + 16, v[0], v[1]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                split_scaled<BF16>(v[s], &gt.out[32 * half + 16 * s], x1 + 8 * s);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * (kU + s));
+            }
+            if (!LOCAL) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const float(&v)[16] = s ? b : a;
                     uint32_t hi[8], lo[8];
-                    if (!LOCAL) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
-                        tc::tmem_st8(x2 + 8 * s, hi);
-                        tc::tmem_st8(x2 + 16 + 8 * s, lo);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&gt.out[32 * half + 16 * s + 4 * i]);
-                        split2<BF16>(__fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
-                        split2<BF16>(__fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tc::tmem_st8(x1 + 8 * s, hi);
-                    tc::tmem_st8(x1 + 16 + 8 * s, lo);
+                    for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[s][2 * i], v[s][2 * i + 1]), hi[i], lo[i]);
+                    tc::tmem_st8(x2 + 8 * s, hi);
+                    tc::tmem_st8(x2 + 16 + 8 * s, lo);
                 }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * kUOut);
             }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(bars + 8 * kU);
-
-            const float2 over = dup(gt.over);
-            wait.on(kDS, par);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int j = 0; j < NH / 32; ++j) {
-                float a[16], b[16];
-                tc::tmem_ld16x2(tl + TM::DS + half * NH + 32 * j, tl + TM::DS + half * NH + 32 * j + 16, a, b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    S[16 * j + i] = __ffma2_rn(over, S[16 * j + i], make_float2(a[2 * i], a[2 * i + 1]));
-                    S[16 * j + 8 + i] = __ffma2_rn(over, S[16 * j + 8 + i], make_float2(b[2 * i], b[2 * i + 1]));
-                }
-            }
-            if (c + 1 < w.chunks) publish();
         }
         float *dst = nullptr;
         if (unit) dst = p.seg_trans + ((size_t)bh * nseg + seg) * nn;
@@ -336,104 +409,37 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             for (int j = 0; j < NH / 4; ++j) {
                 const int n = half * NH + 4 * j;
                 float4 f = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
-                if (wait.dead) f = make_float4(nan, nan, nan, nan);
+                if (wait.dead()) f = make_float4(nan, nan, nan, nan);
                 if (n < p.N) *reinterpret_cast<float4 *>(dst + (size_t)row * p.N + n) = f;
             }
         }
     } else if (warp < kOutWarp0) {
-        // ---- T and M of each chunk
+        // ---- T of each chunk
         const int pw = warp - kPrepWarp0, ptid = pw * 32 + lane, i = ptid & 63;
         const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
         float *A = reinterpret_cast<float *>(sm + SM::A);
-        float graw[2] = {0.f, 0.f}, braw[2] = {0.f, 0.f};
-        auto fetch = [&](int c) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int t = w.t0 + c * kC + 2 * lane + m;
-                graw[m] = load_gate<IO>(p.g, w.b * p.gs[0] + t * p.gs[1] + w.h, p.g32, t < w.t1);
-                braw[m] = load_gate<IO>(p.beta, w.b * p.bs[0] + t * p.bs[1] + w.h, p.b32, t < w.t1);
-            }
-        };
-        if (pw == 0 && w.chunks > 0) fetch(0);
         for (int c = 0; c < w.chunks; ++c) {
             const uint32_t par = c & 1, half_par = (c >> 1) & 1;
-            Gates &gt = gates[c % kSlots];
-            if (pw == 0) {  // the running sum of g as the sum of two floats, so that differences keep their precision
-                auto add = [](float &h0, float &l0, float h1, float l1) {
-                    const float sum = h0 + h1, t = sum - h0, err = (h0 - (sum - t)) + (h1 - t) + l0 + l1;
-                    h0 = sum + err;
-                    l0 = err - (h0 - sum);
-                };
-                float hi[2], lo[2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    float g = graw[m];
-                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // exp(-200) is 0, and sums stay finite
-                    hi[m] = g * kLog2e;
-                    lo[m] = fmaf(g, kLog2e, -hi[m]) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
-                    gt.beta[2 * lane + m] = braw[m];
-                }
-                if (c + 1 < w.chunks) fetch(c + 1);
-                add(hi[1], lo[1], hi[0], lo[0]);
-                float th = hi[1], tl2 = lo[1];
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const float oh = __shfl_up_sync(0xffffffffu, th, m), ol = __shfl_up_sync(0xffffffffu, tl2, m);
-                    if (lane >= m) add(th, tl2, oh, ol);
-                }
-                const float ph = __shfl_up_sync(0xffffffffu, th, 1), pl = __shfl_up_sync(0xffffffffu, tl2, 1);
-                if (lane > 0) add(hi[0], lo[0], ph, pl);
-                hi[1] = th, lo[1] = tl2;
-                const float eh = __shfl_sync(0xffffffffu, th, 31), el = __shfl_sync(0xffffffffu, tl2, 31);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int t = 2 * lane + m;
-                    const float in = exp2f(hi[m] + lo[m]);
-                    gt.gh[t] = hi[m], gt.gl[t] = lo[m], gt.into[t] = in, gt.neg_into[t] = -in;
-                    gt.out[t] = exp2f((eh - hi[m]) + (el - lo[m]));
-                }
-                if (lane == 0) gt.over = exp2f(eh + el);
-            }
-            tc::named_barrier(1, kPrepWarps * 32);  // the gates; and A of the chunk before is done with
-            wait.on(kKQDone, par);
-            wait.on(kEmptyT + par, half_par ^ 1);
-            tc::fence_after_sync();
-            const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
-            const int limit = pw < 2 ? i : i + 1;
-            const int last = (i | 31);  // of the warp's rows
+            const Gates &gt = gates[c % kSlots];
+            tc::named_barrier(1, kPrepWarps * 32);  // A of the chunk before is done with
+            wait.on(kFullG + c % kSlots, (c / kSlots) & 1);
+            if (pw < 2) {
+                wait.on(kKQDone, par);
+                tc::fence_after_sync();
+                const float gh = gt.gh[i], gl = gt.gl[i], beta = gt.beta[i];
+                const int last = i | 31;  // of the warp's rows
 #pragma unroll 1
-            for (int j0 = 0; j0 <= last; j0 += 16) {
-                float v[16];
-                tc::tmem_ld16(tl + TM::KQ + j0, v);
-#pragma unroll
-                for (int m = 0; m < 16; m += 4) {
-                    const int j = j0 + m;
-                    const float4 h4 = *reinterpret_cast<const float4 *>(&gt.gh[j]), l4 = *reinterpret_cast<const float4 *>(&gt.gl[j]);
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float2 d = __fadd2_rn(__fadd2_rn(dup(gh), e ? make_float2(-h4.z, -h4.w) : make_float2(-h4.x, -h4.y)),
-                                                    __fadd2_rn(dup(gl), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y)));
-                        const float2 x = __fmul2_rn(__fmul2_rn(make_float2(ex2_now(d.x), ex2_now(d.y)), dup(factor)), make_float2(v[m + e], v[m + e + 1]));
-                        v[m + e] = j + e < limit ? x.x : 0.f;
-                        v[m + e + 1] = j + e + 1 < limit ? x.y : 0.f;
-                    }
-                }
-                if (pw < 2) {
+                for (int j0 = 0; j0 <= last; j0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(tl + TM::KQ + j0, v);
+                    decayed(v, gt, j0, gh, gl, beta, i);
 #pragma unroll
                     for (int m = 0; m < 16; m += 4) *reinterpret_cast<float4 *>(A + i * kAW + j0 + m) = make_float4(v[m], v[m + 1], v[m + 2], v[m + 3]);
-                } else if (!LOCAL) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) split2<BF16>(make_float2(v[2 * m], v[2 * m + 1]), hi[m], lo[m]);
-                    const uint32_t dst = sbase + SM::M + par * 16384 + ((j0 >> 3) * 8 + (i >> 3)) * 128 + (i & 7) * 16;
-                    tcop::st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
-                    tcop::st_shared_v4(dst + 1024, hi[4], hi[5], hi[6], hi[7]);
-                    tcop::st_shared_v4(dst + 8192, lo[0], lo[1], lo[2], lo[3]);
-                    tcop::st_shared_v4(dst + 8192 + 1024, lo[4], lo[5], lo[6], lo[7]);
                 }
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * kKQRead);
             }
-            tc::fence_before_sync();
-            tc::mbar_arrive(bars + 8 * kKQRead);
+            wait.on(kEmptyT + par, half_par ^ 1);
             tc::named_barrier(1, kPrepWarps * 32);
             // the diagonal block pw: lane = column, both halves of the warp alike; the inverse takes its place
             float *D = A + 16 * pw * kAW + 16 * pw;
@@ -475,29 +481,33 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     stmatrix_x4_trans(to + bi * 256, hi);
                     stmatrix_x4_trans(to + bi * 256 + 8192, lo);
                 };
-                Frag T[3];
+                // element (c, r) of block (pw, k) of the buffer, above its diagonal, will be T[r][c] of T's block (k, pw)
+                float *mine = A + 16 * pw * kAW;
                 float acc[2][4];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[m][e] = D[(8 * m + 2 * t + (e & 1)) * kAW + g + 8 * (e >> 1)];
                 store(acc, pw);
-                T[0] = to_frag<BF16>(acc);
+                const Frag first = to_frag<BF16>(acc);
+#pragma unroll 1
+                for (int bi = pw + 1; bi < 4; ++bi) {
+                    float sum[2][4] = {};
+                    times_transposed<BF16>(sum, first, A + 16 * bi * kAW + 16 * pw, lane);
+#pragma unroll 1
+                    for (int k = pw + 1; k < bi; ++k) times_transposed<BF16>(sum, load_frag<BF16>(mine + 16 * k, lane), A + 16 * bi * kAW + 16 * k, lane);
 #pragma unroll
-                for (int s = 1; s < 4; ++s) {
-                    const int bi = pw + s;
-                    if (bi < 4) {
-                        float sum[2][4] = {};
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int k = 0; k < s; ++k) times_transposed<BF16>(sum, T[k], A + 16 * bi * kAW + 16 * (pw + k), lane);
-                        float res[2][4] = {};
-                        times_transposed<BF16>(res, to_frag<BF16>(sum), A + 16 * bi * kAW + 16 * bi, lane);
+                        for (int e = 0; e < 4; ++e) sum[m][e] = -sum[m][e], acc[m][e] = 0.f;
+                    times_transposed<BF16>(acc, to_frag<BF16>(sum), A + 16 * bi * kAW + 16 * bi, lane);
+                    store(acc, bi);
+                    if (bi < 3) {
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) res[m][e] = -res[m][e];
-                        store(res, bi);
-                        if (s < 3) T[s < 3 ? s : 0] = to_frag<BF16>(res);
+                        for (int m = 0; m < 4; ++m)
+                            *reinterpret_cast<float2 *>(mine + 16 * bi + (g + 8 * (m & 1)) * kAW + 2 * t + 8 * (m >> 1)) =
+                                make_float2(acc[m >> 1][2 * (m & 1)], acc[m >> 1][2 * (m & 1) + 1]);
+                        __syncwarp();
                     }
                 }
             }
@@ -507,51 +517,90 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
     } else if (warp < kMmaWarp) {
         // ---- y: thread = row of the state
         set_registers<kOutRegs, false>();
-        if (!LOCAL) {
+        if (LOCAL) {  // no y, no M: what the other half of a product's lanes would be read for
+            if (warp - kOutWarp0 >= 2)
+                for (int c = 0; c < w.chunks; ++c) {
+                    wait.on(kKQDone, c & 1);
+                    tc::mbar_arrive(bars + 8 * kKQRead);
+                }
+        } else {
             const int quarter = warp - kOutWarp0, row = quarter * 32 + lane;
             const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM::O;
             const bool ok = row < rows;
             const size_t step = (size_t)p.H * p.P;
+            // M: q's rows of the product with k lie in lanes 64 to 127
+            auto make_m = [&](int c) {
+                if (quarter < 2) return;
+                const Gates &gt = gates[c % kSlots];
+                const int i = row - 64, last = i | 31;
+                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM::KQ, to = sbase + SM::M + (c & 1) * 16384 + (i >> 3) * 128 + (i & 7) * 16;
+                wait.on(kFullG + c % kSlots, (c / kSlots) & 1);
+                wait.on(kKQDone, c & 1);
+                tc::fence_after_sync();
+                const float gh = gt.gh[i], gl = gt.gl[i];
+#pragma unroll 1
+                for (int j0 = 0; j0 <= last; j0 += 16) {
+                    float v[16];
+                    uint32_t hi[8], lo[8];
+                    tc::tmem_ld16(from + j0, v);
+                    decayed(v, gt, j0, gh, gl, 1.f, i + 1);
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) split2<BF16>(make_float2(v[2 * m], v[2 * m + 1]), hi[m], lo[m]);
+                    const uint32_t dst = to + (j0 >> 3) * 1024;
+                    tcop::st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
+                    tcop::st_shared_v4(dst + 1024, hi[4], hi[5], hi[6], hi[7]);
+                    tcop::st_shared_v4(dst + 8192, lo[0], lo[1], lo[2], lo[3]);
+                    tcop::st_shared_v4(dst + 8192 + 1024, lo[4], lo[5], lo[6], lo[7]);
+                }
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * kKQRead);
+                tc::fence_smem_to_async();
+                tc::mbar_arrive(bars + 8 * (kFullM + (c & 1)));
+            };
             const size_t base = ((size_t)w.b * p.L * p.H + w.h) * p.P + w.p0 + row;
             const int odd = lane & 1;
             uint16_t *y = static_cast<uint16_t *>(p.y) + base - odd + odd * step;  // of an odd lane: the token after, from the row before
-            for (int c = 0; c < w.chunks; ++c) {
-                const uint32_t par = c & 1;
-                const Gates &gt = gates[c % kSlots];
-                wait.on(kFullT + par, (c >> 1) & 1);
-                wait.on(kD3, par);
-                tc::fence_after_sync();
 #pragma unroll 1
-                for (int j = 0; j < kC; j += 16) {  // diag(exp G) Q S^T, onto which M U is summed
-                    float v[16];
-                    uint32_t r[16];
-                    tc::tmem_ld16(tl + j, v);
+            for (int c = 0; c <= w.chunks; ++c) {  // the y of chunk c - 1; in between M of chunk c, whose buffer's last product the y before waited for
+                const uint32_t par = (c & 1) ^ 1;
+                if (c > 0) {
+                    const Gates &gt = gates[(c - 1) % kSlots];
+                    wait.on(kD3, par);
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int j = 0; j < kC; j += 16) {  // diag(exp G) Q S^T, onto which M U is summed
+                        float v[16];
+                        uint32_t r[16];
+                        tc::tmem_ld16(tl + j, v);
 #pragma unroll
-                    for (int m = 0; m < 16; m += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&gt.into[j + m]);
-                        r[m] = __float_as_uint(v[m] * f.x), r[m + 1] = __float_as_uint(v[m + 1] * f.y);
-                        r[m + 2] = __float_as_uint(v[m + 2] * f.z), r[m + 3] = __float_as_uint(v[m + 3] * f.w);
+                        for (int m = 0; m < 16; m += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&gt.into[j + m]);
+                            r[m] = __float_as_uint(v[m] * f.x), r[m + 1] = __float_as_uint(v[m + 1] * f.y);
+                            r[m + 2] = __float_as_uint(v[m + 2] * f.z), r[m + 3] = __float_as_uint(v[m + 3] * f.w);
+                        }
+                        tc::tmem_st16(tl + j, r);
                     }
-                    tc::tmem_st16(tl + j, r);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(bars + 8 * kD3Read);
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::mbar_arrive(bars + 8 * kD3Read);
+                if (c < w.chunks) make_m(c);
+                if (c == 0) continue;
                 wait.on(kD4, par);
                 tc::fence_after_sync();
-                const int tc0 = w.t0 + c * kC, n = min(kC, w.t1 - tc0);
-                const float scale = wait.dead ? __int_as_float(0x7fffffff) : p.scale;
+                const int tc0 = w.t0 + (c - 1) * kC, n = min(kC, w.t1 - tc0);
+                const float scale = wait.dead() ? __int_as_float(0x7fffffff) : p.scale;
                 uint16_t *to = y + (size_t)tc0 * step;
 #pragma unroll 1
-                for (int j = 0; j < kC; j += 16, to += 16 * step) {
+                for (int j = 0; j < kC; j += 16) {
                     float v[16];
                     tc::tmem_ld16(tl + j, v);
                     // neighbouring lanes exchange: each then has two rows of every second token, a store of 4 bytes
 #pragma unroll
-                    for (int m = 0; m < 16; m += 2) {
+                    for (int m = 0; m < 16; m += 2, to += 2 * step) {
                         const uint32_t own = tcop::pack2(scale * v[m], scale * v[m + 1], BF16), other = __shfl_xor_sync(0xffffffffu, own, 1);
                         const uint32_t two = __byte_perm(own, other, odd ? 0x3276 : 0x5410);
-                        if (ok && j + m + odd < n) *reinterpret_cast<uint32_t *>(to + m * step) = two;
+                        if (ok && j + m + odd < n) *reinterpret_cast<uint32_t *>(to) = two;
                     }
                 }
                 tc::fence_before_sync();
@@ -569,99 +618,108 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false), ID_V = tc::idesc_f16(128, kC, BF16, true, false),
                            ID_DS = tc::idesc_f16(128, NN, BF16, false, true);
         constexpr int NK = NN / 16;  // steps of 16 along a state's columns
-        auto s_term = [&](int k, int term) {  // 16 columns of the state's operand: first or second term
-            return tmem + TM::S + (k / (NK / 2)) * (NN / 2) + term * (NN / 4) + (k % (NK / 2)) * 8;
-        };
-        auto x_term = [&](uint32_t x, int k, int term) { return tmem + x + (k >> 1) * 32 + term * 16 + (k & 1) * 8; };
+        constexpr uint32_t K2 = 2 * 128 * 16 / 16;  // of a descriptor: from one step of 16 columns of k, q or v to the next
+        auto s_term = [&](int k) { return tmem + TM::S + (k / (NK / 2)) * (NN / 2) + (k % (NK / 2)) * 8; };  // second term NN / 4 on
+        auto x_term = [&](uint32_t x, int k) { return tmem + x + (k >> 1) * 32 + (k & 1) * 8; };              // second term 16 on
         auto kq_product = [&](int c) {  // [k; q] k^T
-            const uint32_t kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES;
             wait.on(kFullKQ + c % kStages, (c / kStages) & 1);
             wait.on(kKQRead, (c & 1) ^ 1);
             tc::fence_after_sync();
             if (go) {
-#pragma unroll
-                for (int k = 0; k < NK; ++k)
-                    tc::mma_f16(tmem + TM::KQ, tc::desc(kq + k * 4096, 2048, 128), tc::desc(kq + k * 4096, 2048, 128), ID, k > 0);
+                uint64_t d = tc::desc(sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, 2048, 128);
+#pragma unroll 1
+                for (int k = 0; k < NK; ++k, d += K2) tc::mma_f16(tmem + TM::KQ, d, d, ID, k > 0);
                 tc::commit(bars + 8 * kKQDone);
             }
         };
         if (w.chunks > 0) kq_product(0);
+#pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
-            const uint32_t par = c & 1, kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, v = sbase + SM::V + (c % kVStages) * SM::V_BYTES;
-            const uint32_t T = sbase + SM::T + par * 16384, M = sbase + SM::M + par * 16384;
-            wait.on(kS, par);
-            tc::fence_after_sync();
-            if (go) {
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {  // S k^T
-                    const uint64_t b = tc::desc(kq + k * 4096, 2048, 128);
-                    tc::mma_f16_ts(tmem + TM::X1, s_term(k, 0), b, ID, k > 0);
-                    tc::mma_f16_ts(tmem + TM::X1, s_term(k, 1), b, ID, 1);
+            const uint32_t par = c & 1, kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES;
+            const uint64_t kd = tc::desc(kq, 2048, 128), td = tc::desc(sbase + SM::T + par * 16384, 1024, 128);
+#pragma unroll 1
+            for (int j = 0; j < NK; ++j) {  // S k^T, as the state's columns come
+                const int k = (j >> 1) + (j & 1) * (NK / 2);
+                if (!(j & 1)) {
+                    wait.on(kS + (j >> 1), par);
+                    tc::fence_after_sync();
                 }
-                tc::commit(bars + 8 * kD1);
+                if (go) {
+                    tc::mma_f16_ts(tmem + TM::X1, s_term(k), kd + k * K2, ID, j > 0);
+                    tc::mma_f16_ts(tmem + TM::X1, s_term(k) + NN / 4, kd + k * K2, ID, 1);
+                }
             }
+            if (go) tc::commit(bars + 8 * kD1);
             if (c + 1 < w.chunks) kq_product(c + 1);
             wait.on(kFullT + par, (c >> 1) & 1);
             wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
             tc::fence_after_sync();
             if (go) {
                 if (!unit) {
-#pragma unroll
+                    const uint64_t vd = tc::desc(sbase + SM::V + (c % kVStages) * SM::V_BYTES, 2048, 128);
+#pragma unroll 1
                     for (int k = 0; k < kC / 16; ++k) {  // v^T (T diag(beta))^T
-                        const uint64_t a = tc::desc(v + k * 4096, 2048, 128);
-                        tc::mma_f16(tmem + TM::X2, a, tc::desc(T + k * 2048, 1024, 128), ID_V, k > 0);
-                        tc::mma_f16(tmem + TM::X2, a, tc::desc(T + 8192 + k * 2048, 1024, 128), ID_V, 1);
+                        tc::mma_f16(tmem + TM::X2, vd + k * K2, td + k * 128, ID_V, k > 0);
+                        tc::mma_f16(tmem + TM::X2, vd + k * K2, td + 512 + k * 128, ID_V, 1);
                     }
                 }
                 tc::commit(bars + 8 * (kEmptyV + c % kVStages));
             }
-            wait.on(kR, par);
-            tc::fence_after_sync();
-            if (go) {
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k) {  // - (exp(G) S k^T) (T diag(beta))^T
-                    const uint64_t hi = tc::desc(T + k * 2048, 1024, 128), lo = tc::desc(T + 8192 + k * 2048, 1024, 128);
-                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k, 0), hi, ID, !unit || k > 0);
-                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k, 0), lo, ID, 1);
-                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k, 1), hi, ID, 1);
+#pragma unroll 1
+            for (int j = 0; j < kC / 16; ++j) {  // - (exp(G) S k^T) (T diag(beta))^T
+                const int k = (j >> 1) + (j & 1) * 2;
+                if (!(j & 1)) {
+                    wait.on(kR + (j >> 1), par);
+                    tc::fence_after_sync();
                 }
-                tc::commit(bars + 8 * kD2);
+                if (go) {
+                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + k * 128, ID, !unit || j > 0);
+                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + 512 + k * 128, ID, 1);
+                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k) + 16, td + k * 128, ID, 1);
+                }
             }
+            if (go) tc::commit(bars + 8 * kD2);
             if (!LOCAL) {  // while the chain splits U
                 wait.on(kD4Read, par ^ 1);
                 tc::fence_after_sync();
                 if (go) {
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < NK; ++k) {  // S q^T
-                        const uint64_t b = tc::desc(kq + 1024 + k * 4096, 2048, 128);
-                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 0), b, ID, k > 0);
-                        tc::mma_f16_ts(tmem + TM::O, s_term(k, 1), b, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, s_term(k), kd + 64 + k * K2, ID, k > 0);
+                        tc::mma_f16_ts(tmem + TM::O, s_term(k) + NN / 4, kd + 64 + k * K2, ID, 1);
                     }
                     tc::commit(bars + 8 * kD3);
                 }
             }
-            wait.on(kU, par);
-            tc::fence_after_sync();
-            if (go) {
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k) {  // the change of the state
-                    const uint64_t b = tc::desc(kq + k * 256, 128, 2048);
-                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k, 0), b, ID_DS, k > 0);
-                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k, 1), b, ID_DS, 1);
+            const uint64_t kt = tc::desc(kq, 128, 2048);
+#pragma unroll 1
+            for (int j = 0; j < kC / 16; ++j) {  // the change of the state
+                const int k = (j >> 1) + (j & 1) * 2;
+                if (!(j & 1)) {
+                    wait.on(kU + (j >> 1), par);
+                    tc::fence_after_sync();
                 }
+                if (go) {
+                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k), kt + k * 16, ID_DS, j > 0);
+                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k) + 16, kt + k * 16, ID_DS, 1);
+                }
+            }
+            if (go) {
                 tc::commit(bars + 8 * kDS);
                 tc::commit(bars + 8 * (kEmptyKQ + c % kStages));
             }
             if (!LOCAL) {
+                wait.on(kFullM + par, (c >> 1) & 1);
+                wait.on(kUOut, par);
                 wait.on(kD3Read, par);
                 tc::fence_after_sync();
                 if (go) {
-#pragma unroll
+                    const uint64_t md = tc::desc(sbase + SM::M + par * 16384, 1024, 128);
+#pragma unroll 1
                     for (int k = 0; k < kC / 16; ++k) {  // U^T M^T
-                        const uint64_t hi = tc::desc(M + k * 2048, 1024, 128), lo = tc::desc(M + 8192 + k * 2048, 1024, 128);
-                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k, 0), hi, ID, 1);
-                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k, 0), lo, ID, 1);
-                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k, 1), hi, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k), md + k * 128, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k), md + 512 + k * 128, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k) + 16, md + k * 128, ID, 1);
                     }
                     tc::commit(bars + 8 * kD4);
                 }
@@ -671,59 +729,55 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         // the last products may still read shared memory: wait for them before the CTA ends
         if (w.chunks > 0) wait.on(kEmptyT + ((w.chunks - 1) & 1), ((w.chunks - 1) >> 1) & 1);
         __syncwarp();
-    } else if (warp == kLoadWarp) {
-        // ---- copies: lane = row of eight, 16-byte piece of four
-        const int r = lane & 7, piece = lane >> 3;
-        const char *kb = static_cast<const char *>(p.k) + 2 * (w.b * p.ks[0] + (long long)grp * p.N);
-        const char *qb = static_cast<const char *>(p.q) + 2 * (w.b * p.qs[0] + (long long)grp * p.N);
-        const char *vb = static_cast<const char *>(p.v) + 2 * (w.b * p.vs[0] + (long long)w.h * p.P + w.p0);
-        auto copy = [&](uint32_t dst, const char *src, bool ok) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(ok ? src : nullptr), "r"(ok ? 16 : 0) : "memory");
-        };
-        for (int i = 0; i < w.chunks + 2; ++i) {
-            if (i < w.chunks) {
-                wait.on(kEmptyKQ + i % kStages, ((i / kStages) & 1) ^ 1);
-                const uint32_t kq = sbase + SM::KQ + (i % kStages) * SM::KQ_BYTES;
-#pragma unroll 2
-                for (int rg = 0; rg < 8; ++rg) {
-                    const int t = w.t0 + i * kC + rg * 8 + r;
-                    const bool live = t < w.t1;
-                    const char *ks = kb + 2 * (t * p.ks[1]), *qs = qb + 2 * (t * p.qs[1]);
+    } else {
+        // ---- copies: lane = row of eight, 16-byte piece of four.  The first warp takes k, the second q, the third v and the gates
+        const int r = lane & 7, piece = lane >> 3, which = warp - kLoadWarp;
+        const void *src = which == 0 ? p.k : which == 1 ? p.q : p.v;
+        const long long s0 = which == 0 ? p.ks[0] : which == 1 ? p.qs[0] : p.vs[0], s1 = which == 0 ? p.ks[1] : which == 1 ? p.qs[1] : p.vs[1];
+        const char *from = static_cast<const char *>(src) + 2 * (w.b * s0 + (which < 2 ? (long long)grp * p.N : (long long)w.h * p.P + w.p0) + 8 * piece);
+        // of a row of 16-byte pieces, those that exist from this lane's on; none of q in a pass without y, nor of v in a transition's
+        const int width = (which == 1 && LOCAL) || (which == 2 && unit) ? 0 : (which < 2 ? p.N : rows) - 8 * piece;
+        const uint32_t to = sbase + (which < 2 ? SM::KQ + which * 1024 + piece * 2048 : SM::V + piece * 128) + r * 16;
+        const uint32_t stage = which < 2 ? SM::KQ_BYTES : SM::V_BYTES, row_step = which < 2 ? 128 : 2048, col_step = which < 2 ? 8192 : 512;
+        const int stages = which < 2 ? kStages : kVStages, empty = which < 2 ? kEmptyKQ : kEmptyV, full = which < 2 ? kFullKQ : kFullV;
+        int at = 0;
+        uint32_t parity = 1;
+        float graw[2] = {0.f, 0.f}, braw[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int c = -1; c < w.chunks; ++c) {
+            if (c >= 0) {
+                wait.on(empty + at, parity);  // with a place of v's, the gates four chunks back are done with too
+                const char *row = from + 2 * ((w.t0 + c * kC + r) * s1);
+                uint32_t dst = to + at * stage;
+#pragma unroll 1
+                for (int rg = 0; rg < 8; ++rg, row += 16 * s1, dst += row_step) {
+                    const int live = w.t0 + c * kC + rg * 8 + r < w.t1 ? width : 0;
 #pragma unroll
-                    for (int cg = 0; cg < NN / 32; ++cg) {
-                        const int col = cg * 4 + piece;
-                        const uint32_t dst = kq + (col * 16 + rg) * 128 + r * 16;
-                        const bool ok = live && col * 8 < p.N;
-                        copy(dst, ks + 16 * col, ok);
-                        if (!LOCAL) copy(dst + 1024, qs + 16 * col, ok);
-                    }
+                    for (int cg = 0; cg < 4; ++cg)
+                        if (which == 2 || cg < NN / 32)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + cg * col_step),
+                                         "l"(live > 32 * cg ? row + 64 * cg : nullptr), "r"(live > 32 * cg ? 16 : 0) : "memory");
+                }
+                cp_commit();
+            }
+            if (which == 2) {
+                if (c >= 0) {
+                    make_gates(gates[c % kSlots], graw, braw, lane);
+                    tc::mbar_arrive(bars + 8 * (kFullG + c % kSlots));
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {  // of the next chunk
+                    const int t = w.t0 + (c + 1) * kC + 2 * lane + m;
+                    graw[m] = load_gate<IO>(p.g, w.b * p.gs[0] + t * p.gs[1] + w.h, p.g32, t < w.t1);
+                    braw[m] = load_gate<IO>(p.beta, w.b * p.bs[0] + t * p.bs[1] + w.h, p.b32, t < w.t1);
                 }
             }
-            cp_commit();
-            if (i >= 1 && i - 1 < w.chunks) {
-                const int c = i - 1;
-                wait.on(kEmptyV + c % kVStages, ((c / kVStages) & 1) ^ 1);
-                const uint32_t v = sbase + SM::V + (c % kVStages) * SM::V_BYTES;
-                if (!unit) {
-#pragma unroll 2
-                    for (int rg = 0; rg < 8; ++rg) {
-                        const int t = w.t0 + c * kC + rg * 8 + r;
-                        const char *vs = vb + 2 * (t * p.vs[1]);
-#pragma unroll
-                        for (int cg = 0; cg < 4; ++cg) {
-                            const int col = cg * 4 + piece;
-                            copy(v + (rg * 16 + col) * 128 + r * 16, vs + 16 * col, t < w.t1 && col * 8 < rows);
-                        }
-                    }
-                }
-            }
-            cp_commit();
-            cp_wait<2>();  // all but this round's two groups
+            if (c < 0) continue;
+            cp_wait<0>();
             tc::fence_smem_to_async();
-            if (i >= 1 && i - 1 < w.chunks) tc::mbar_arrive(bars + 8 * (kFullKQ + (i - 1) % kStages));
-            if (i >= 2) tc::mbar_arrive(bars + 8 * (kFullV + (i - 2) % kVStages));
+            tc::mbar_arrive(bars + 8 * (full + at));
+            if (++at == stages) at = 0, parity ^= 1;
         }
-        cp_wait<0>();
     }
     tc::fence_before_sync();
     __syncthreads();
