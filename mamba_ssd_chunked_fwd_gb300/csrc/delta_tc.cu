@@ -14,7 +14,7 @@
 // product takes it as its A operand.  Only the chain S K^T -> U -> S is sequential,
 // three products to a chunk; the rest runs beside it:
 //
-//   8 warps  the chain: split S K^T, U and S into operands; the state's fp32 in registers
+//   16 warps the chain: split S K^T, U and S into operands; the state's fp32 in registers
 //   4 warps  A and T of the next chunk
 //   4 warps  y, and M of the next chunk
 //   1 warp   issues the products
@@ -40,12 +40,12 @@ namespace ssd {
 namespace {
 
 constexpr int kC = kDeltaChunk;
-constexpr int kChainWarps = 8, kPrepWarps = 4, kOutWarps = 4;
+constexpr int kChainWarps = 16, kPrepWarps = 4, kOutWarps = 4;
 constexpr int kPrepWarp0 = kChainWarps, kOutWarp0 = kPrepWarp0 + kPrepWarps, kMmaWarp = kOutWarp0 + kOutWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = (kLoadWarp + 3) * 32;  // three warps copy: k, q, and v with the gates
-// Registers a thread, per warpgroup: 96 at launch; the chain 144 (its state is 64 of them), y 56, the last
-// warpgroup 40.  2 * 144 + 96 + 56 + 40 = 5 * 96.
-constexpr int kChainRegs = 144, kOutRegs = 56, kMmaRegs = 40;
+// Registers a thread, per warpgroup: 72 at launch; the chain's four 80 (the state is 32 of them), T 88, y 48, the last
+// 48.  4 * 80 + 88 + 48 + 48 = 7 * 72.
+constexpr int kChainRegs = 80, kPrepRegs = 88, kOutRegs = 48, kMmaRegs = 48;
 constexpr int kStages = 3;   // of k and q
 constexpr int kVStages = 2;  // of v
 constexpr int kSlots = 4;    // of a chunk's gates
@@ -65,7 +65,7 @@ struct Smem {
 };
 
 enum Bar { kFullKQ = 0, kEmptyKQ = 3, kFullV = 6, kEmptyV = 8, kFullT = 10, kEmptyT = 12, kFullM = 14, kFullG = 16, kKQDone = 20, kKQRead, kD1, kD2, kDS,
-           kD3, kD3Read, kD4, kD4Read, kUOut, kS, kR = kS + 4, kU = kR + 2, kBars = kU + 2 };
+           kD3, kD3Read, kD4, kD4Read, kUOut, kS, kR = kS + 2, kU = kR + 4, kBars = kU + 4 };
 
 // TMEM columns.
 template <int NN>
@@ -202,7 +202,7 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  : "memory");
 }
 
-// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 16 columns on.
+// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 8 columns on.
 template <bool BF16>
 __device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to) {
     uint32_t hi[8], lo[8];
@@ -213,7 +213,7 @@ __device__ __forceinline__ void split_scaled(const float (&x)[16], const float *
         split2<BF16>(__fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
     }
     tc::tmem_st8(to, hi);
-    tc::tmem_st8(to + 16, lo);
+    tc::tmem_st8(to + 8, lo);
 }
 
 template <int N, bool MORE>
@@ -283,7 +283,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         for (int i = 0; i < kSlots; ++i) init(kFullG + i, 32);
         for (int b : {(int)kKQDone, (int)kD1, (int)kD2, (int)kDS, (int)kD3, (int)kD4}) init(b, 1);
         init(kKQRead, 128);
-        for (int b = kS; b < kBars; ++b) init(b, kChainWarps * 32);
+        for (int b = kS; b < kR; ++b) init(b, kChainWarps * 32);
+        for (int b = kR; b < kBars; ++b) init(b, kChainWarps * 8);
         init(kUOut, kChainWarps * 32), init(kD3Read, kOutWarps * 32), init(kD4Read, kOutWarps * 32);
         tc::mbar_init_fence();
     }
@@ -300,34 +301,26 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
     Waits wait{bars};
 
     if (warp < kChainWarps) {
-        // ---- the chain: thread = row of the state, half of the columns
+        // ---- the chain: thread = row of the state, a quarter of its columns, 16 of the 64 tokens
         set_registers<kChainRegs, true>();
-        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+        const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        constexpr int NH = NN / 2;
-        float2 S[NH / 2];
-        auto load_row = [&](const float *src) {
-            const bool ok = src && row < rows;
+        constexpr int CW = NN / 4;
+        float2 S[CW / 2];
+        {
+            const float *src = nullptr;
+            if (!LOCAL && seg > 0) src = p.seg_states + ((size_t)bh * p.nseg + seg) * pn + (size_t)w.p0 * p.N;
+            else if (!LOCAL && p.h0) src = p.h0 + bh * pn + (size_t)w.p0 * p.N;
 #pragma unroll
-            for (int j = 0; j < NH / 4; ++j) {
-                const int n = half * NH + 4 * j;
+            for (int j = 0; j < CW / 4; ++j) {
+                const int n = part * CW + 4 * j;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (ok && n < p.N) f = *reinterpret_cast<const float4 *>(src + (size_t)row * p.N + n);
+                if (src && row < rows && n < p.N) f = *reinterpret_cast<const float4 *>(src + (size_t)row * p.N + n);
+                if (unit && row < p.N && (row & ~3) == n) f = make_float4(row == n, row == n + 1, row == n + 2, row == n + 3);
                 S[2 * j] = make_float2(f.x, f.y), S[2 * j + 1] = make_float2(f.z, f.w);
             }
-        };
-        if (unit) {
-#pragma unroll
-            for (int j = 0; j < NH / 2; ++j)
-                S[j] = make_float2(row == half * NH + 2 * j && row < p.N ? 1.f : 0.f, row == half * NH + 2 * j + 1 && row < p.N ? 1.f : 0.f);
-        } else if (LOCAL) {
-            load_row(nullptr);
-        } else if (seg > 0) {
-            load_row(p.seg_states + ((size_t)bh * p.nseg + seg) * pn + (size_t)w.p0 * p.N);
-        } else {
-            load_row(p.h0 ? p.h0 + bh * pn + (size_t)w.p0 * p.N : nullptr);
         }
-        const uint32_t x1 = tl + TM::X1 + 32 * half, x2 = tl + TM::X2 + 32 * half;
+        const uint32_t x1 = tl + TM::X1 + 16 * part, x2 = tl + TM::X2 + 16 * part;
 #pragma unroll 1
         for (int c = 0;; ++c) {
             const uint32_t par = c & 1;
@@ -339,10 +332,10 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             // the state after the chunk before, by 16 columns, and each of them as an operand: the product with k
             // begins with the first
 #pragma unroll
-            for (int j = 0; j < NH / 16; ++j) {
+            for (int j = 0; j < CW / 16; ++j) {
                 if (c > 0) {
                     float v[16];
-                    tc::tmem_ld16(tl + TM::DS + half * NH + 16 * j, v);
+                    tc::tmem_ld16(tl + TM::DS + part * CW + 16 * j, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) S[8 * j + i] = __ffma2_rn(over, S[8 * j + i], make_float2(v[2 * i], v[2 * i + 1]));
                 }
@@ -350,8 +343,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split2<BF16>(S[8 * j + i], hi[i], lo[i]);
-                    tc::tmem_st8(tl + TM::S + half * NH + 8 * j, hi);
-                    tc::tmem_st8(tl + TM::S + half * NH + NH / 2 + 8 * j, lo);
+                    tc::tmem_st8(tl + TM::S + part * CW + 8 * j, hi);
+                    tc::tmem_st8(tl + TM::S + part * CW + CW / 2 + 8 * j, lo);
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     tc::mbar_arrive(bars + 8 * (kS + j));
@@ -362,37 +355,25 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kFullG + c % kSlots, (c / kSlots) & 1);
             wait.on(kD1, par);
             tc::fence_after_sync();
-            // -exp(G) S k^T, by 16 tokens: the product with T begins with the first.  Twice 16 columns hold first terms, then
-            // second ones, so the values of both are read first
-            float v[2][16];
-            tc::tmem_ld16x2(x1, x1 + 16, v[0], v[1]);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                split_scaled<BF16>(v[s], &gt.neg_into[32 * half + 16 * s], x1 + 8 * s);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::mbar_arrive(bars + 8 * (kR + s));
-            }
+            float v[16];
+            tc::tmem_ld16(x1, v);
+            split_scaled<BF16>(v, &gt.neg_into[16 * part], x1);  // -exp(G) S k^T
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            tc::mbar_arrive(bars + 8 * (kR + part));
             wait.on(kD2, par);
             tc::fence_after_sync();
-            // what U adds to the state, then (for y) U itself
-            tc::tmem_ld16x2(x2, x2 + 16, v[0], v[1]);
+            tc::tmem_ld16(x2, v);
+            split_scaled<BF16>(v, &gt.out[16 * part], x1);  // what U adds to the state
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            tc::mbar_arrive(bars + 8 * (kU + part));
+            if (!LOCAL) {  // U itself, for y
+                uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                split_scaled<BF16>(v[s], &gt.out[32 * half + 16 * s], x1 + 8 * s);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::mbar_arrive(bars + 8 * (kU + s));
-            }
-            if (!LOCAL) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[s][2 * i], v[s][2 * i + 1]), hi[i], lo[i]);
-                    tc::tmem_st8(x2 + 8 * s, hi);
-                    tc::tmem_st8(x2 + 16 + 8 * s, lo);
-                }
+                for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
+                tc::tmem_st8(x2, hi);
+                tc::tmem_st8(x2 + 8, lo);
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 tc::mbar_arrive(bars + 8 * kUOut);
@@ -406,8 +387,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         if (dst && row < rows) {
             const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
-            for (int j = 0; j < NH / 4; ++j) {
-                const int n = half * NH + 4 * j;
+            for (int j = 0; j < CW / 4; ++j) {
+                const int n = part * CW + 4 * j;
                 float4 f = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
                 if (wait.dead()) f = make_float4(nan, nan, nan, nan);
                 if (n < p.N) *reinterpret_cast<float4 *>(dst + (size_t)row * p.N + n) = f;
@@ -415,6 +396,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         }
     } else if (warp < kOutWarp0) {
         // ---- T of each chunk
+        set_registers<kPrepRegs, true>();
         const int pw = warp - kPrepWarp0, ptid = pw * 32 + lane, i = ptid & 63;
         const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
         float *A = reinterpret_cast<float *>(sm + SM::A);
@@ -617,18 +599,18 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         const bool go = tc::elect_one();
         constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false), ID_V = tc::idesc_f16(128, kC, BF16, true, false),
                            ID_DS = tc::idesc_f16(128, NN, BF16, false, true);
-        constexpr int NK = NN / 16;  // steps of 16 along a state's columns
+        constexpr int NK = NN / 16, J = NN / 64;  // steps of 16 along a state's columns; of a thread's part of them
         constexpr uint32_t K2 = 2 * 128 * 16 / 16;  // of a descriptor: from one step of 16 columns of k, q or v to the next
-        auto s_term = [&](int k) { return tmem + TM::S + (k / (NK / 2)) * (NN / 2) + (k % (NK / 2)) * 8; };  // second term NN / 4 on
-        auto x_term = [&](uint32_t x, int k) { return tmem + x + (k >> 1) * 32 + (k & 1) * 8; };              // second term 16 on
+        auto s_term = [&](int k) { return tmem + TM::S + (k / J) * (NN / 4) + (k % J) * 8; };  // second term NN / 8 on
+        auto x_term = [&](uint32_t x, int k) { return tmem + x + k * 16; };                     // second term 8 on
         auto kq_product = [&](int c) {  // [k; q] k^T
             wait.on(kFullKQ + c % kStages, (c / kStages) & 1);
             wait.on(kKQRead, (c & 1) ^ 1);
             tc::fence_after_sync();
             if (go) {
-                uint64_t d = tc::desc(sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, 2048, 128);
-#pragma unroll 1
-                for (int k = 0; k < NK; ++k, d += K2) tc::mma_f16(tmem + TM::KQ, d, d, ID, k > 0);
+                const uint64_t d = tc::desc(sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES, 2048, 128);
+#pragma unroll
+                for (int k = 0; k < NK; ++k) tc::mma_f16(tmem + TM::KQ, d + k * K2, d + k * K2, ID, k > 0);
                 tc::commit(bars + 8 * kKQDone);
             }
         };
@@ -637,16 +619,16 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         for (int c = 0; c < w.chunks; ++c) {
             const uint32_t par = c & 1, kq = sbase + SM::KQ + (c % kStages) * SM::KQ_BYTES;
             const uint64_t kd = tc::desc(kq, 2048, 128), td = tc::desc(sbase + SM::T + par * 16384, 1024, 128);
-#pragma unroll 1
-            for (int j = 0; j < NK; ++j) {  // S k^T, as the state's columns come
-                const int k = (j >> 1) + (j & 1) * (NK / 2);
-                if (!(j & 1)) {
-                    wait.on(kS + (j >> 1), par);
-                    tc::fence_after_sync();
-                }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {  // S k^T, as the state's columns come
+                wait.on(kS + j, par);
+                tc::fence_after_sync();
                 if (go) {
-                    tc::mma_f16_ts(tmem + TM::X1, s_term(k), kd + k * K2, ID, j > 0);
-                    tc::mma_f16_ts(tmem + TM::X1, s_term(k) + NN / 4, kd + k * K2, ID, 1);
+#pragma unroll
+                    for (int k = j; k < NK; k += J) {
+                        tc::mma_f16_ts(tmem + TM::X1, s_term(k), kd + k * K2, ID, k > 0);
+                        tc::mma_f16_ts(tmem + TM::X1, s_term(k) + NN / 8, kd + k * K2, ID, 1);
+                    }
                 }
             }
             if (go) tc::commit(bars + 8 * kD1);
@@ -657,7 +639,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             if (go) {
                 if (!unit) {
                     const uint64_t vd = tc::desc(sbase + SM::V + (c % kVStages) * SM::V_BYTES, 2048, 128);
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {  // v^T (T diag(beta))^T
                         tc::mma_f16(tmem + TM::X2, vd + k * K2, td + k * 128, ID_V, k > 0);
                         tc::mma_f16(tmem + TM::X2, vd + k * K2, td + 512 + k * 128, ID_V, 1);
@@ -665,17 +647,14 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 }
                 tc::commit(bars + 8 * (kEmptyV + c % kVStages));
             }
-#pragma unroll 1
-            for (int j = 0; j < kC / 16; ++j) {  // - (exp(G) S k^T) (T diag(beta))^T
-                const int k = (j >> 1) + (j & 1) * 2;
-                if (!(j & 1)) {
-                    wait.on(kR + (j >> 1), par);
-                    tc::fence_after_sync();
-                }
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k) {  // - (exp(G) S k^T) (T diag(beta))^T
+                wait.on(kR + k, par);
+                tc::fence_after_sync();
                 if (go) {
-                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + k * 128, ID, !unit || j > 0);
+                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + k * 128, ID, !unit || k > 0);
                     tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + 512 + k * 128, ID, 1);
-                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k) + 16, td + k * 128, ID, 1);
+                    tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k) + 8, td + k * 128, ID, 1);
                 }
             }
             if (go) tc::commit(bars + 8 * kD2);
@@ -683,25 +662,22 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 wait.on(kD4Read, par ^ 1);
                 tc::fence_after_sync();
                 if (go) {
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < NK; ++k) {  // S q^T
                         tc::mma_f16_ts(tmem + TM::O, s_term(k), kd + 64 + k * K2, ID, k > 0);
-                        tc::mma_f16_ts(tmem + TM::O, s_term(k) + NN / 4, kd + 64 + k * K2, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, s_term(k) + NN / 8, kd + 64 + k * K2, ID, 1);
                     }
                     tc::commit(bars + 8 * kD3);
                 }
             }
             const uint64_t kt = tc::desc(kq, 128, 2048);
-#pragma unroll 1
-            for (int j = 0; j < kC / 16; ++j) {  // the change of the state
-                const int k = (j >> 1) + (j & 1) * 2;
-                if (!(j & 1)) {
-                    wait.on(kU + (j >> 1), par);
-                    tc::fence_after_sync();
-                }
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k) {  // the change of the state
+                wait.on(kU + k, par);
+                tc::fence_after_sync();
                 if (go) {
-                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k), kt + k * 16, ID_DS, j > 0);
-                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k) + 16, kt + k * 16, ID_DS, 1);
+                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k), kt + k * 16, ID_DS, k > 0);
+                    tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k) + 8, kt + k * 16, ID_DS, 1);
                 }
             }
             if (go) {
@@ -715,11 +691,11 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 tc::fence_after_sync();
                 if (go) {
                     const uint64_t md = tc::desc(sbase + SM::M + par * 16384, 1024, 128);
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {  // U^T M^T
                         tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k), md + k * 128, ID, 1);
                         tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k), md + 512 + k * 128, ID, 1);
-                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k) + 16, md + k * 128, ID, 1);
+                        tc::mma_f16_ts(tmem + TM::O, x_term(TM::X2, k) + 8, md + k * 128, ID, 1);
                     }
                     tc::commit(bars + 8 * kD4);
                 }
