@@ -24,7 +24,9 @@ struct DeltaParams {
     int nc;  // chunks of a row
     // segments: tokens [s seg_len, (s+1) seg_len) of every row; seg_len a multiple of 64
     int nseg, seg_len;
+    bool chunked;  // by the kernels of delta_tc.cu
     float *seg_states;  // [B,H,nseg,P,N] state entering a segment (slot 0 unused)
+    unsigned char *ops;  // [B,H,nc] a chunk's operands (delta_tc.cuh)
     float *seg_trans;   // [B,H,nseg-1,N,N] a segment's transition: the state after it is S trans + (its own)
     // backward
     const void *dy;
@@ -51,6 +53,8 @@ struct DeltaStepParams {
 };
 
 cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);          // y, final_state
+size_t delta_op_bytes();
+cudaError_t launch_delta_prep(const DeltaParams &p, int io, cudaStream_t s);          // a chunk's operands for the next
 bool delta_tc_takes(const DeltaParams &p, int io);
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s);            // the same in chunks
 cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s);

@@ -56,6 +56,19 @@ ssd_status check_delta_inputs(const ssd_delta_args *a) {
     return SSD_OK;
 }
 
+struct DeltaLayout {
+    size_t ops, total;
+};
+
+DeltaLayout delta_layout(ssd::DeltaParams &p, int32_t dtype) {
+    p.chunked = ssd::delta_tc_takes(p, dtype);
+    p.nseg = 1;
+    p.seg_len = p.nc * ssd::kDeltaChunk;
+    DeltaLayout l = {0, 0};
+    if (p.chunked) l.total = align_up((size_t)p.B * p.H * p.nc * ssd::delta_op_bytes());
+    return l;
+}
+
 struct DeltaBwdLayout {
     size_t states, adj, u, dr, dqh, dkh, total;
 };
@@ -113,7 +126,7 @@ ssd_status ssd_delta_rule_workspace_size(const ssd_delta_args *a, size_t *bytes)
     ssd_status st = check_delta(a, p);
     if (st != SSD_OK) return st;
     if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = 0;
+    *bytes = delta_layout(p, a->dtype).total;
     return ok();
 }
 
@@ -132,10 +145,11 @@ ssd_status ssd_delta_rule(const ssd_delta_args *a, void *stream) {
                len = {a->lengths, a->B * sizeof(int32_t), "lengths"};
     if ((st = apart(y, {q, k, v, g, beta, h0, len, fin})) != SSD_OK) return st;
     if ((st = apart(fin, {q, k, v, g, beta, h0, len})) != SSD_OK) return st;
-    p.nseg = 1;
-    p.seg_len = p.nc * ssd::kDeltaChunk;
-    cudaError_t e = ssd::delta_tc_takes(p, a->dtype) ? ssd::launch_delta_tc(p, a->dtype, static_cast<cudaStream_t>(stream))
-                                                     : ssd::launch_delta_walk(p, a->dtype, static_cast<cudaStream_t>(stream));
+    const DeltaLayout l = delta_layout(p, a->dtype);
+    if ((st = check_workspace(a->workspace, a->workspace_bytes, l.total)) != SSD_OK) return st;
+    p.ops = static_cast<unsigned char *>(a->workspace) + l.ops;
+    cudaError_t e = p.chunked ? ssd::launch_delta_tc(p, a->dtype, static_cast<cudaStream_t>(stream))
+                              : ssd::launch_delta_walk(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "delta_rule");
     return ok();
 }

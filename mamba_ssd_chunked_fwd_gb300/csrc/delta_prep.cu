@@ -1,0 +1,353 @@
+// delta_prep.cu -- per chunk of 64 tokens and head, what the chunked delta rule's walks
+// (delta_tc.cu) read beside k, q and v, for 16-bit tensors.  With G the running sum of g in the
+// chunk and W_ij = exp(G_i - G_j):
+//
+//     A_ij = beta_i W_ij (k_i . k_j)  (j < i),   T = (I + A)^-1,   M_ij = W_ij (q_i . k_j)  (j <= i)
+//
+// The products of k and q with k are one product of 128 rows on the tensor cores.  The diagonal
+// blocks of 16 of T are inverted by substitution in fp32, the blocks below by
+// T_ij = -T_ii sum_k A_ik T_kj with mma.sync on operands of two terms: blocks this small would leave
+// tcgen05's 128 rows empty, and each needs the one before it.  No power of A is formed:
+// with keys alike those would cancel.
+//
+// A kernel of its own, not warps of the walk: there it took a third of the code that every
+// chunk pulled through the instruction cache, and the walk waited for it (prompts of [4,4096,32,128,128]
+// 278 us with it inside); here chunks are independent, four CTAs share an SM, and the walks of
+// segments and of the gradients read its results again.
+#include "delta_tc.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAW = 68;  // floats between rows of A
+
+// ex2 that stays where it is: moved into a branch on whether its result is wanted, each would wait for the one before
+// (measured: 68 cycles an element in place of 20).
+__device__ __forceinline__ float ex2_now(float v) {
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// D (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums.
+template <bool BF16>
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// A chunk's gates by one warp, two tokens to a lane: the running sum of g as the sum of two floats, so that
+// differences keep their precision.
+__device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], const float (&beta)[2], int lane) {
+    auto add = [](float &h0, float &l0, float h1, float l1) {
+        const float sum = h0 + h1, t = sum - h0, err = (h0 - (sum - t)) + (h1 - t) + l0 + l1;
+        h0 = sum + err;
+        l0 = err - (h0 - sum);
+    };
+    float hi[2], lo[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float g = graw[m];
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // exp(-200) is 0, and sums stay finite
+        hi[m] = g * kLog2e;
+        lo[m] = fmaf(g, kLog2e, -hi[m]) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
+        gt.beta[2 * lane + m] = beta[m];
+    }
+    add(hi[1], lo[1], hi[0], lo[0]);
+    float th = hi[1], tl = lo[1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float oh = __shfl_up_sync(0xffffffffu, th, m), ol = __shfl_up_sync(0xffffffffu, tl, m);
+        if (lane >= m) add(th, tl, oh, ol);
+    }
+    const float ph = __shfl_up_sync(0xffffffffu, th, 1), pl = __shfl_up_sync(0xffffffffu, tl, 1);
+    if (lane > 0) add(hi[0], lo[0], ph, pl);
+    hi[1] = th, lo[1] = tl;
+    const float eh = __shfl_sync(0xffffffffu, th, 31), el = __shfl_sync(0xffffffffu, tl, 31);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int t = 2 * lane + m;
+        const float in = exp2f(hi[m] + lo[m]);
+        gt.gh[t] = hi[m], gt.gl[t] = lo[m], gt.into[t] = in, gt.neg_into[t] = -in;
+        gt.out[t] = exp2f((eh - hi[m]) + (el - lo[m]));
+    }
+    if (lane == 0) gt.over = exp2f(eh + el);
+}
+
+// 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
+__device__ __forceinline__ void decayed(float (&v)[16], const Gates &gt, int j0, float gh, float gl, float factor, int limit) {
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+        const int j = j0 + m;
+        const float4 h4 = *reinterpret_cast<const float4 *>(&gt.gh[j]), l4 = *reinterpret_cast<const float4 *>(&gt.gl[j]);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const float2 d = __fadd2_rn(__fadd2_rn(dup(gh), e ? make_float2(-h4.z, -h4.w) : make_float2(-h4.x, -h4.y)),
+                                        __fadd2_rn(dup(gl), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y)));
+            const float2 x = __fmul2_rn(__fmul2_rn(make_float2(ex2_now(d.x), ex2_now(d.y)), dup(factor)), make_float2(v[m + e], v[m + e + 1]));
+            v[m + e] = j + e < limit ? x.x : 0.f;
+            v[m + e + 1] = j + e + 1 < limit ? x.y : 0.f;
+        }
+    }
+}
+
+// A 16 x 16 block as the A operand of a product, in two terms.
+struct Frag {
+    uint32_t hi[4], lo[4];
+};
+// Of an accumulated block, acc[half][4]: columns 8 half + ..
+template <bool BF16>
+__device__ __forceinline__ Frag to_frag(const float (&acc)[2][4]) {
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<BF16>(make_float2(acc[i >> 1][2 * (i & 1)], acc[i >> 1][2 * (i & 1) + 1]), f.hi[i], f.lo[i]);
+    return f;
+}
+// Of a block in shared memory, rows kAW apart.
+template <bool BF16>
+__device__ __forceinline__ Frag load_frag(const float *x, int lane) {
+    const float *at = x + (lane >> 2) * kAW + 2 * (lane & 3);
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<BF16>(*reinterpret_cast<const float2 *>(at + (i & 1) * 8 * kAW + (i >> 1) * 8), f.hi[i], f.lo[i]);
+    return f;
+}
+// acc += a X^T with X a 16 x 16 block of `x`, rows kAW apart.
+template <bool BF16>
+__device__ __forceinline__ void times_transposed(float (&acc)[2][4], const Frag &a, const float *x, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const float *row = x + (8 * half + g) * kAW + 2 * t;
+        uint32_t hi[2], lo[2];
+        split2<BF16>(*reinterpret_cast<const float2 *>(row), hi[0], lo[0]);
+        split2<BF16>(*reinterpret_cast<const float2 *>(row + 8), hi[1], lo[1]);
+        mma_16x8x16<BF16>(acc[half], a.lo, hi);
+        mma_16x8x16<BF16>(acc[half], a.hi, lo);
+        mma_16x8x16<BF16>(acc[half], a.hi, hi);
+    }
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+
+template <int NN>
+struct Smem {
+    static constexpr uint32_t KQ = 0, OP = 0;  // k (rows 0-63) and q; once multiplied, T and M take their place
+    static constexpr uint32_t KQ_BYTES = 128 * NN * 2 > 32768 ? 128 * NN * 2 : 32768;
+    static constexpr uint32_t GATES = KQ_BYTES, A = GATES + (uint32_t)sizeof(Gates), BYTES = A + kC * kAW * 4;
+    static_assert(KQ_BYTES == kOpGates, "the gates follow T and M, as in global memory");
+};
+
+template <int IO, int NN>
+__global__ void __launch_bounds__(kThreads)
+delta_prep_kernel(const __grid_constant__ DeltaParams p) {
+    constexpr bool BF16 = IO == IO_BF16;
+    using SM = Smem<NN>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    __shared__ __align__(8) uint64_t bar_mem;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t sbase = tc::smem_addr(sm);
+    Gates &gt = *reinterpret_cast<Gates *>(sm + SM::GATES);
+    float *A = reinterpret_cast<float *>(sm + SM::A);
+    const int tid = threadIdx.x, pw = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x % p.nc, bh = blockIdx.x / p.nc, h = bh % p.H, b = bh / p.H, grp = h / (p.H / p.G);
+    const int t0 = c * kC, len = delta_length(p, b);
+    if (t0 >= len) return;  // no walk comes here
+
+    if (tid == 0) {
+        tc::mbar_init(tc::smem_addr(&bar_mem), 1);
+        tc::mbar_init_fence();
+    }
+    if (pw == 1) {
+        tc::tmem_alloc(tc::smem_addr(&tmem_slot), 64);
+        tc::tmem_relinquish();
+    }
+    {
+        const int r = lane & 7, piece = lane >> 3;
+#pragma unroll
+        for (int rg = pw; rg < 16; rg += 4) {  // row groups of k, then of q
+            const int t = t0 + (rg & 7) * 8 + r;
+            const char *row = static_cast<const char *>(rg < 8 ? p.k : p.q) +
+                              2 * (b * (rg < 8 ? p.ks[0] : p.qs[0]) + t * (rg < 8 ? p.ks[1] : p.qs[1]) + (long long)grp * p.N + 8 * piece);
+            const int live = t < len ? p.N - 8 * piece : 0;
+#pragma unroll
+            for (int cg = 0; cg < NN / 32; ++cg)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbase + SM::KQ + ((cg * 4 + piece) * 16 + rg) * 128 + r * 16),
+                             "l"(live > 32 * cg ? row + 64 * cg : nullptr), "r"(live > 32 * cg ? 16 : 0) : "memory");
+        }
+        cp_commit();
+    }
+    if (pw == 0) {
+        float graw[2], braw[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int t = t0 + 2 * lane + m;
+            graw[m] = load_gate<IO>(p.g, b * p.gs[0] + t * p.gs[1] + h, p.g32, t < len);
+            braw[m] = load_gate<IO>(p.beta, b * p.bs[0] + t * p.bs[1] + h, p.b32, t < len);
+        }
+        make_gates(gt, graw, braw, lane);
+    }
+    cp_wait<0>();
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    if (tid == 0) {
+        constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false);
+        uint64_t d = tc::desc(sbase + SM::KQ, 2048, 128);
+#pragma unroll 1
+        for (int k = 0; k < NN / 16; ++k, d += 256) tc::mma_f16(tmem, d, d, ID, k > 0);
+        tc::commit(tc::smem_addr(&bar_mem));
+    }
+    __syncwarp();
+    Waits wait{tc::smem_addr(&bar_mem)};
+    wait.on(0, 0);
+    tc::fence_after_sync();
+    // what the blocks above the diagonals of T and M stay
+#pragma unroll 4
+    for (int e = tid; e < 2048; e += kThreads) tcop::st_shared_v4(sbase + SM::OP + 16 * e, 0u, 0u, 0u, 0u);
+    __syncthreads();
+    {
+        const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
+        const int i = tid & 63, last = i | 31;  // of the warp's rows
+        const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
+        const int limit = pw < 2 ? i : i + 1;
+#pragma unroll 1
+        for (int j0 = 0; j0 <= last; j0 += 16) {
+            float v[16];
+            tc::tmem_ld16(tl + j0, v);
+            decayed(v, gt, j0, gh, gl, factor, limit);
+            if (pw < 2) {
+#pragma unroll
+                for (int m = 0; m < 16; m += 4) *reinterpret_cast<float4 *>(A + i * kAW + j0 + m) = make_float4(v[m], v[m + 1], v[m + 2], v[m + 3]);
+            } else {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) split2<BF16>(make_float2(v[2 * m], v[2 * m + 1]), hi[m], lo[m]);
+                const uint32_t dst = sbase + SM::OP + kOpM + ((j0 >> 3) * 8 + (i >> 3)) * 128 + (i & 7) * 16;
+                tcop::st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
+                tcop::st_shared_v4(dst + 1024, hi[4], hi[5], hi[6], hi[7]);
+                tcop::st_shared_v4(dst + kOpTerm, lo[0], lo[1], lo[2], lo[3]);
+                tcop::st_shared_v4(dst + kOpTerm + 1024, lo[4], lo[5], lo[6], lo[7]);
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (pw == 1) tc::tmem_dealloc(tmem, 64);
+    // the diagonal block pw: lane = column, both halves of the warp alike; the inverse takes its place
+    float *D = A + 16 * pw * kAW + 16 * pw;
+    {
+        const int col = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float s0 = r == col ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < r; k += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(D + r * kAW + k);
+                s0 = fmaf(-f.x, x[k], s0);
+                if (k + 1 < r) s1 = fmaf(-f.y, x[k + 1 < 16 ? k + 1 : 0], s1);
+                if (k + 2 < r) s0 = fmaf(-f.z, x[k + 2 < 16 ? k + 2 : 0], s0);
+                if (k + 3 < r) s1 = fmaf(-f.w, x[k + 3 < 16 ? k + 3 : 0], s1);
+            }
+            x[r] = s0 + s1;
+        }
+        __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) D[r * kAW + col] = x[r];
+        }
+    }
+    __syncthreads();
+    // column pw of blocks, transposed: element (c, r) of a block is T[r][c]
+    {
+        const int g = lane >> 2, t = lane & 3;
+        const float b0 = gt.beta[16 * pw + g], b1 = gt.beta[16 * pw + g + 8];
+        const uint32_t to = sbase + SM::OP + kOpT + ((2 * pw + ((lane >> 3) & 1)) * 8 + (lane >> 4)) * 128 + (lane & 7) * 16;
+        auto store = [&](const float(&acc)[2][4], int bi) {  // T diag(beta) in two terms
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float b = m & 1 ? b1 : b0;
+                split2<BF16>(make_float2(b * acc[m >> 1][2 * (m & 1)], b * acc[m >> 1][2 * (m & 1) + 1]), hi[m], lo[m]);
+            }
+            stmatrix_x4_trans(to + bi * 256, hi);
+            stmatrix_x4_trans(to + bi * 256 + kOpTerm, lo);
+        };
+        // element (c, r) of block (pw, k) of the buffer, above its diagonal, will be T[r][c] of T's block (k, pw)
+        float *mine = A + 16 * pw * kAW;
+        float acc[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][e] = D[(8 * m + 2 * t + (e & 1)) * kAW + g + 8 * (e >> 1)];
+        store(acc, pw);
+        const Frag first = to_frag<BF16>(acc);
+#pragma unroll 1
+        for (int bi = pw + 1; bi < 4; ++bi) {
+            float sum[2][4] = {};
+            times_transposed<BF16>(sum, first, A + 16 * bi * kAW + 16 * pw, lane);
+#pragma unroll 1
+            for (int k = pw + 1; k < bi; ++k) times_transposed<BF16>(sum, load_frag<BF16>(mine + 16 * k, lane), A + 16 * bi * kAW + 16 * k, lane);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[m][e] = -sum[m][e], acc[m][e] = 0.f;
+            times_transposed<BF16>(acc, to_frag<BF16>(sum), A + 16 * bi * kAW + 16 * bi, lane);
+            store(acc, bi);
+            if (bi < 3) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    *reinterpret_cast<float2 *>(mine + 16 * bi + (g + 8 * (m & 1)) * kAW + 2 * t + 8 * (m >> 1)) =
+                        make_float2(acc[m >> 1][2 * (m & 1)], acc[m >> 1][2 * (m & 1) + 1]);
+                __syncwarp();
+            }
+        }
+    }
+    if (wait.dead() && lane == 0) gt.over = gt.into[0] = __int_as_float(0x7fffffff);  // every walk's results
+    tc::fence_smem_to_async();
+    __syncthreads();
+    if (tid == 0) {
+        unsigned char *dst = p.ops + (size_t)blockIdx.x * kOpBytes;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(sbase + SM::OP), "r"(kOpBytes) : "memory");
+        tc::bulk_commit();
+        tc::bulk_wait_all();
+    }
+}
+
+template <int IO, int NN>
+cudaError_t prep_as(const DeltaParams &p, cudaStream_t s) {
+    auto *kernel = delta_prep_kernel<IO, NN>;
+    const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)((long long)p.B * p.H * p.nc), kThreads, Smem<NN>::BYTES, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int IO>
+cudaError_t prep_io(const DeltaParams &p, cudaStream_t s) {
+    return p.N <= 64 ? prep_as<IO, 64>(p, s) : prep_as<IO, 128>(p, s);
+}
+
+}  // namespace
+
+size_t delta_op_bytes() { return kOpBytes; }
+
+cudaError_t launch_delta_prep(const DeltaParams &p, int io, cudaStream_t s) {
+    return io == IO_BF16 ? prep_io<IO_BF16>(p, s) : prep_io<IO_F16>(p, s);
+}
+
+}  // namespace ssd

@@ -1,0 +1,55 @@
+// delta_tc.cuh -- what the delta rule's tensor-core kernels share: a chunk's operands in
+// global memory, numbers as two 16-bit terms, bounded waits.
+#pragma once
+
+#include "delta.cuh"
+#include "tc_operands.cuh"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+
+constexpr int kC = kDeltaChunk;
+
+// A chunk's gates.  With G the running sum of g: gh + gl = G log2(e), into = exp(G), out = exp(G_end - G),
+// over = exp(G_end).
+struct alignas(16) Gates {
+    float gh[kC], gl[kC], beta[kC], into[kC], neg_into[kC], out[kC];
+    float over;
+};
+
+// What delta_prep.cu leaves of every chunk of every head: T diag(beta) and M, both 64 x 64 in blocks of 8 rows x 16
+// bytes (block (column / 8, row / 8) at (column / 8) * 1024 + (row / 8) * 128), as first terms, then second ones; the gates.
+constexpr uint32_t kOpT = 0, kOpM = 16384, kOpTerm = 8192, kOpGates = 32768, kOpBytes = kOpGates + (uint32_t)sizeof(Gates);
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+// Two numbers as sums of two 16-bit numbers each.
+template <bool BF16>
+__device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
+    hi = tcop::pack2(v.x, v.y, BF16);
+    const float2 d = __ffma2_rn(unpack2<BF16>(hi), make_float2(-1.f, -1.f), v);
+    lo = tcop::pack2(d.x, d.y, BF16);
+}
+
+// A thread's waits: each lasts 2000 tries of up to a millisecond; once one has given up, the rest return
+// at once.  Short code: five kinds of warps run side by side, and what they run has to stay in the
+// instruction cache (with unrolled loops and longer waits every second cycle went to fetching).
+struct Waits {
+    uint32_t bars;
+    uint32_t tries = 2000;
+    __device__ __forceinline__ bool dead() const { return tries == 0; }
+    __device__ __forceinline__ void on(int bar, uint32_t parity) {
+        uint32_t done = 0;
+#pragma unroll 1
+        for (uint32_t i = 0; i < tries && !done; ++i)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\tselp.u32 %0, 1, 0, p;\n}\n"
+                         : "=r"(done) : "r"(bars + 8 * bar), "r"(parity) : "memory");
+        tries = done ? tries : 0u;
+        asm volatile("" : "+r"(tries));  // or the code after it is laid out twice, for a thread that waits and one that does not
+    }
+};
+
+}  // namespace ssd
