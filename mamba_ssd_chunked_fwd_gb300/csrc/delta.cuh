@@ -55,6 +55,7 @@ struct DeltaStepParams {
 cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);          // y, final_state
 size_t delta_op_bytes();
 cudaError_t launch_delta_prep(const DeltaParams &p, int io, cudaStream_t s);          // a chunk's operands for the next
+void delta_segments(DeltaParams &p);
 bool delta_tc_takes(const DeltaParams &p, int io);
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s);            // the same in chunks
 cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s);

@@ -57,15 +57,19 @@ ssd_status check_delta_inputs(const ssd_delta_args *a) {
 }
 
 struct DeltaLayout {
-    size_t ops, total;
+    size_t ops, states, trans, total;
 };
 
+// And by which kernels: in chunks, maybe of segments, or token by token.
 DeltaLayout delta_layout(ssd::DeltaParams &p, int32_t dtype) {
     p.chunked = ssd::delta_tc_takes(p, dtype);
-    p.nseg = 1;
-    p.seg_len = p.nc * ssd::kDeltaChunk;
-    DeltaLayout l = {0, 0};
-    if (p.chunked) l.total = align_up((size_t)p.B * p.H * p.nc * ssd::delta_op_bytes());
+    DeltaLayout l = {0, 0, 0, 0};
+    if (!p.chunked) return l;
+    ssd::delta_segments(p);
+    const size_t f = sizeof(float), heads = (size_t)p.B * p.H;
+    l.states = align_up(heads * p.nc * ssd::delta_op_bytes());
+    l.trans = l.states + (p.nseg > 1 ? align_up(heads * p.nseg * p.P * p.N * f) : 0);
+    l.total = l.trans + (p.nseg > 1 ? align_up(heads * (p.nseg - 1) * p.N * p.N * f) : 0);
     return l;
 }
 
@@ -147,7 +151,10 @@ ssd_status ssd_delta_rule(const ssd_delta_args *a, void *stream) {
     if ((st = apart(fin, {q, k, v, g, beta, h0, len})) != SSD_OK) return st;
     const DeltaLayout l = delta_layout(p, a->dtype);
     if ((st = check_workspace(a->workspace, a->workspace_bytes, l.total)) != SSD_OK) return st;
-    p.ops = static_cast<unsigned char *>(a->workspace) + l.ops;
+    unsigned char *ws = static_cast<unsigned char *>(a->workspace);
+    p.ops = ws + l.ops;
+    p.seg_states = reinterpret_cast<float *>(ws + l.states);
+    p.seg_trans = reinterpret_cast<float *>(ws + l.trans);
     cudaError_t e = p.chunked ? ssd::launch_delta_tc(p, a->dtype, static_cast<cudaStream_t>(stream))
                               : ssd::launch_delta_walk(p, a->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "delta_rule");

@@ -12,7 +12,7 @@
 //
 // A kernel of its own, not warps of the walk: there it took a third of the code that every
 // chunk pulled through the instruction cache, and the walk waited for it (prompts of [4,4096,32,128,128]
-// 278 us with it inside); here chunks are independent, four CTAs share an SM, and the walks of
+// 278 us with it inside); here chunks are independent, six CTAs share an SM, and the walks of
 // segments and of the gradients read its results again.
 #include "delta_tc.cuh"
 
@@ -42,42 +42,42 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// A chunk's gates by one warp, two tokens to a lane: the running sum of g as the sum of two floats, so that
-// differences keep their precision.
+// A chunk's gates by one warp, two tokens to a lane.  The running sum of g log2(e) is taken in whole
+// numbers of 2^-40, exactly, and handed on as the sum of two floats: differences of far larger sums then keep
+// their precision (floats added in pairs did the same in four times the steps, one after another: 5000 cycles of this
+// kernel's 24000).
 __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], const float (&beta)[2], int lane) {
-    auto add = [](float &h0, float &l0, float h1, float l1) {
-        const float sum = h0 + h1, t = sum - h0, err = (h0 - (sum - t)) + (h1 - t) + l0 + l1;
-        h0 = sum + err;
-        l0 = err - (h0 - sum);
-    };
-    float hi[2], lo[2];
+    constexpr double kScale = 1.4426950408889634 * 1099511627776.0;
+    long long sum[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        float g = graw[m];
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // exp(-200) is 0, and sums stay finite
-        hi[m] = g * kLog2e;
-        lo[m] = fmaf(g, kLog2e, -hi[m]) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
+        // exp(-200) is 0, and so is every product with it; above, sums have room for 64 tokens
+        sum[m] = __double2ll_rn((double)fminf(fmaxf(graw[m], -200.f), 4000.f) * kScale);
         gt.beta[2 * lane + m] = beta[m];
     }
-    add(hi[1], lo[1], hi[0], lo[0]);
-    float th = hi[1], tl = lo[1];
+    const uint32_t nan0 = __ballot_sync(0xffffffffu, isnan(graw[0])), nan1 = __ballot_sync(0xffffffffu, isnan(graw[1]));
+    sum[1] += sum[0];
+    long long pair = sum[1];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const float oh = __shfl_up_sync(0xffffffffu, th, m), ol = __shfl_up_sync(0xffffffffu, tl, m);
-        if (lane >= m) add(th, tl, oh, ol);
+        const long long o = __shfl_up_sync(0xffffffffu, pair, m);
+        if (lane >= m) pair += o;
     }
-    const float ph = __shfl_up_sync(0xffffffffu, th, 1), pl = __shfl_up_sync(0xffffffffu, tl, 1);
-    if (lane > 0) add(hi[0], lo[0], ph, pl);
-    hi[1] = th, lo[1] = tl;
-    const float eh = __shfl_sync(0xffffffffu, th, 31), el = __shfl_sync(0xffffffffu, tl, 31);
+    sum[0] += pair - sum[1];
+    sum[1] = pair;
+    const long long end = __shfl_sync(0xffffffffu, pair, 31);
+    const uint32_t before = (1u << lane) - 1u, upto = before | (1u << lane);
+    const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         const int t = 2 * lane + m;
-        const float in = exp2f(hi[m] + lo[m]);
-        gt.gh[t] = hi[m], gt.gl[t] = lo[m], gt.into[t] = in, gt.neg_into[t] = -in;
-        gt.out[t] = exp2f((eh - hi[m]) + (el - lo[m]));
+        const float hi = __ll2float_rn(sum[m]) * 9.094947017729282e-13f, lo = __ll2float_rn(sum[m] - __float2ll_rn(hi * 1099511627776.f)) * 9.094947017729282e-13f;
+        const bool bad = (nan0 & upto) || (nan1 & (m ? upto : before));
+        const float in = bad ? nan : exp2f(hi + lo);
+        gt.gh[t] = bad ? nan : hi, gt.gl[t] = lo, gt.into[t] = in, gt.neg_into[t] = -in;
+        gt.out[t] = nan0 | nan1 ? nan : exp2f(__ll2float_rn(end - sum[m]) * 9.094947017729282e-13f);
     }
-    if (lane == 0) gt.over = exp2f(eh + el);
+    if (lane == 0) gt.over = nan0 | nan1 ? nan : exp2f(__ll2float_rn(end) * 9.094947017729282e-13f);
 }
 
 // 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
@@ -140,12 +140,16 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
 }
 
 
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 template <int NN>
 struct Smem {
-    static constexpr uint32_t KQ = 0, OP = 0;  // k (rows 0-63) and q; once multiplied, T and M take their place
-    static constexpr uint32_t KQ_BYTES = 128 * NN * 2 > 32768 ? 128 * NN * 2 : 32768;
-    static constexpr uint32_t GATES = KQ_BYTES, A = GATES + (uint32_t)sizeof(Gates), BYTES = A + kC * kAW * 4;
-    static_assert(KQ_BYTES == kOpGates, "the gates follow T and M, as in global memory");
+    static constexpr uint32_t KQ = 0;                          // k (rows 0-63) and q; once multiplied, T and A take their place
+    static constexpr uint32_t T = 0, A = 16384;
+    static constexpr uint32_t GATES = A + kC * kAW * 4, BYTES = GATES + (uint32_t)sizeof(Gates);  // 35 KB: six CTAs to an SM
+    static_assert(128 * NN * 2 <= GATES, "k and q");
 };
 
 template <int IO, int NN>
@@ -172,6 +176,15 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         tc::tmem_alloc(tc::smem_addr(&tmem_slot), 64);
         tc::tmem_relinquish();
     }
+    float graw[2] = {0.f, 0.f}, braw[2] = {0.f, 0.f};
+    if (pw == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int t = t0 + 2 * lane + m;
+            graw[m] = load_gate<IO>(p.g, b * p.gs[0] + t * p.gs[1] + h, p.g32, t < len);
+            braw[m] = load_gate<IO>(p.beta, b * p.bs[0] + t * p.bs[1] + h, p.b32, t < len);
+        }
+    }
     {
         const int r = lane & 7, piece = lane >> 3;
 #pragma unroll
@@ -187,16 +200,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         }
         cp_commit();
     }
-    if (pw == 0) {
-        float graw[2], braw[2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const int t = t0 + 2 * lane + m;
-            graw[m] = load_gate<IO>(p.g, b * p.gs[0] + t * p.gs[1] + h, p.g32, t < len);
-            braw[m] = load_gate<IO>(p.beta, b * p.bs[0] + t * p.bs[1] + h, p.b32, t < len);
-        }
-        make_gates(gt, graw, braw, lane);
-    }
+    if (pw == 0) make_gates(gt, graw, braw, lane);
     cp_wait<0>();
     tc::fence_smem_to_async();
     tc::fence_before_sync();
@@ -214,18 +218,24 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     Waits wait{tc::smem_addr(&bar_mem)};
     wait.on(0, 0);
     tc::fence_after_sync();
-    // what the blocks above the diagonals of T and M stay
-#pragma unroll 4
-    for (int e = tid; e < 2048; e += kThreads) tcop::st_shared_v4(sbase + SM::OP + 16 * e, 0u, 0u, 0u, 0u);
-    __syncthreads();
+    unsigned char *dst = p.ops + (size_t)blockIdx.x * kOpBytes;
+    // what the blocks above the diagonal of T stay
+#pragma unroll
+    for (int e = 0; e < 1024 / kThreads; ++e) tcop::st_shared_v4(sbase + SM::T + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
     {
         const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
         const int i = tid & 63, last = i | 31;  // of the warp's rows
         const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
         const int limit = pw < 2 ? i : i + 1;
 #pragma unroll 1
-        for (int j0 = 0; j0 <= last; j0 += 16) {
+        for (int j0 = 0; j0 < kC; j0 += 16) {
             float v[16];
+            uint4 *to = reinterpret_cast<uint4 *>(dst + kOpM + ((j0 >> 3) * 8 + (i >> 3)) * 128 + (i & 7) * 16);
+            if (j0 > last) {  // above the diagonal: of A nothing is read, M is zero
+                if (pw < 2) break;
+                to[0] = to[64] = to[kOpTerm / 16] = to[kOpTerm / 16 + 64] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             tc::tmem_ld16(tl + j0, v);
             decayed(v, gt, j0, gh, gl, factor, limit);
             if (pw < 2) {
@@ -235,11 +245,10 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) split2<BF16>(make_float2(v[2 * m], v[2 * m + 1]), hi[m], lo[m]);
-                const uint32_t dst = sbase + SM::OP + kOpM + ((j0 >> 3) * 8 + (i >> 3)) * 128 + (i & 7) * 16;
-                tcop::st_shared_v4(dst, hi[0], hi[1], hi[2], hi[3]);
-                tcop::st_shared_v4(dst + 1024, hi[4], hi[5], hi[6], hi[7]);
-                tcop::st_shared_v4(dst + kOpTerm, lo[0], lo[1], lo[2], lo[3]);
-                tcop::st_shared_v4(dst + kOpTerm + 1024, lo[4], lo[5], lo[6], lo[7]);
+                to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                to[64] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                to[kOpTerm / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                to[kOpTerm / 16 + 64] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
             }
         }
     }
@@ -276,7 +285,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     {
         const int g = lane >> 2, t = lane & 3;
         const float b0 = gt.beta[16 * pw + g], b1 = gt.beta[16 * pw + g + 8];
-        const uint32_t to = sbase + SM::OP + kOpT + ((2 * pw + ((lane >> 3) & 1)) * 8 + (lane >> 4)) * 128 + (lane & 7) * 16;
+        const uint32_t to = sbase + SM::T + ((2 * pw + ((lane >> 3) & 1)) * 8 + (lane >> 4)) * 128 + (lane & 7) * 16;
         auto store = [&](const float(&acc)[2][4], int bi) {  // T diag(beta) in two terms
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -321,8 +330,8 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     tc::fence_smem_to_async();
     __syncthreads();
     if (tid == 0) {
-        unsigned char *dst = p.ops + (size_t)blockIdx.x * kOpBytes;
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(sbase + SM::OP), "r"(kOpBytes) : "memory");
+        bulk_store(dst + kOpT, sbase + SM::T, 16384);
+        bulk_store(dst + kOpGates, sbase + SM::GATES, (uint32_t)sizeof(Gates));
         tc::bulk_commit();
         tc::bulk_wait_all();
     }

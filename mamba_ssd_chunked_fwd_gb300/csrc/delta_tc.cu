@@ -24,6 +24,8 @@
 // its own rounding alone.  With fp16 a state must stay below 65504.
 //
 // Every wait is bounded; one that gives up fills what its CTA still writes with NaN.
+#include <math.h>
+
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -431,6 +433,59 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem_slot, TM::COLS);
 }
 
+// The state entering each segment: S_{s+1} = S_s trans_s + own_s, row by row, from the initial state; `own` lies where the
+// result goes.  A CTA takes 16 rows of a head; the next transition is copied while one is multiplied.
+constexpr int kFoldRows = 16, kFoldThreads = 256;
+constexpr int kFoldBytes = 2 * 128 * 128 * 4 + kFoldRows * 132 * 4;
+__global__ void __launch_bounds__(kFoldThreads)
+delta_fold_kernel(const __grid_constant__ DeltaParams p) {
+    extern __shared__ __align__(16) float fold_mem[];
+    float *trans = fold_mem, *state = fold_mem + 2 * 128 * 128;
+    const int tiles = (p.P + kFoldRows - 1) / kFoldRows, bh = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * kFoldRows;
+    const int tid = threadIdx.x, n = tid & 127, r0 = (tid >> 7) * (kFoldRows / 2), N = p.N;
+    const size_t pn = (size_t)p.P * N, nn = (size_t)N * N;
+    auto copy = [&](int s) {
+        const float *src = p.seg_trans + ((size_t)bh * (p.nseg - 1) + s) * nn;
+        for (int e = 4 * tid; e < (int)nn; e += 4 * kFoldThreads) cp_async16(trans + (s & 1) * 128 * 128 + e, src + e, 16);
+        cp_commit();
+    };
+    copy(0);
+#pragma unroll
+    for (int r = 0; r < kFoldRows / 2; ++r) {
+        const bool ok = p.h0 && n < N && p0 + r0 + r < p.P;
+        state[(r0 + r) * 132 + n] = ok ? __ldg(p.h0 + bh * pn + (size_t)(p0 + r0 + r) * N + n) : 0.f;
+    }
+    for (int s = 0; s + 1 < p.nseg; ++s) {
+        if (s + 2 < p.nseg) copy(s + 1);
+        else cp_commit();
+        cp_wait<1>();
+        __syncthreads();
+        float *own = p.seg_states + ((size_t)bh * p.nseg + s + 1) * pn + (size_t)(p0 + r0) * N + n;
+        float acc[kFoldRows / 2];
+#pragma unroll
+        for (int r = 0; r < kFoldRows / 2; ++r) acc[r] = n < N && p0 + r0 + r < p.P ? own[(size_t)r * N] : 0.f;
+        const float *t = trans + (s & 1) * 128 * 128 + n;
+#pragma unroll 2
+        for (int m = 0; m < N; m += 4) {
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = n < N ? t[(m + j) * N] : 0.f;
+#pragma unroll
+            for (int r = 0; r < kFoldRows / 2; ++r) {
+                const float4 x = *reinterpret_cast<const float4 *>(state + (r0 + r) * 132 + m);
+                acc[r] = fmaf(x.x, f[0], fmaf(x.y, f[1], fmaf(x.z, f[2], fmaf(x.w, f[3], acc[r]))));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kFoldRows / 2; ++r) {
+            state[(r0 + r) * 132 + n] = acc[r];
+            if (n < N && p0 + r0 + r < p.P) own[(size_t)r * N] = acc[r];
+        }
+        __syncthreads();
+    }
+}
+
 template <int IO, int NN>
 cudaError_t tc_as(const DeltaParams &p, bool local, cudaStream_t s) {
     const long long tiles = (p.P + 127) / 128;
@@ -450,6 +505,15 @@ cudaError_t tc_as(const DeltaParams &p, bool local, cudaStream_t s) {
 
 template <int IO>
 cudaError_t tc_io(const DeltaParams &p, cudaStream_t s) {
+    cudaError_t e = launch_delta_prep(p, IO, s);
+    if (e == cudaSuccess && p.nseg > 1) {
+        e = p.N <= 64 ? tc_as<IO, 64>(p, true, s) : tc_as<IO, 128>(p, true, s);
+        if (e == cudaSuccess) e = allow_smem<kFoldBytes>(delta_fold_kernel);
+        if (e != cudaSuccess) return e;
+        delta_fold_kernel<<<(unsigned)((long long)p.B * p.H * ((p.P + kFoldRows - 1) / kFoldRows)), kFoldThreads, kFoldBytes, s>>>(p);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
     return p.N <= 64 ? tc_as<IO, 64>(p, false, s) : tc_as<IO, 128>(p, false, s);
 }
 
@@ -465,9 +529,25 @@ bool delta_tc_takes(const DeltaParams &p, int io) {
            by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0);
 }
 
+// The cut of the rows into segments.  A walk takes an SM for itself, and a chunk about 3.3 us of it (a pass of a segment's own
+// state and of its transition 2.6); few heads are cut until there are walks for the SMs.  The cut costs that first pass, a
+// fold (a state through a segment's transition, about 1.5 us) and two launches.
+void delta_segments(DeltaParams &p) {
+    const double sms = scan_sm_count(), heads = (double)p.B * p.H, tiles = (p.P + 127) / 128;
+    auto cost = [&](int m) {
+        const int len = (p.nc + m - 1) / m, n = (p.nc + len - 1) / len;
+        const double walk = ceil(heads * tiles * n / sms) * 3.3 * len;
+        return n == 1 ? walk : walk + ceil(heads * (tiles + 1) * (n - 1) / sms) * 2.6 * len + 1.5 * n + 10.;
+    };
+    int best = 1;
+    for (int m = 2; m <= 64 && m <= p.nc; ++m)
+        if (cost(m) < cost(best)) best = m;
+    const int len = (p.nc + best - 1) / best;
+    p.seg_len = len * kC;
+    p.nseg = (p.nc + len - 1) / len;
+}
+
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s) {
-    const cudaError_t e = launch_delta_prep(p, io, s);
-    if (e != cudaSuccess) return e;
     return io == IO_BF16 ? tc_io<IO_BF16>(p, s) : tc_io<IO_F16>(p, s);
 }
 
