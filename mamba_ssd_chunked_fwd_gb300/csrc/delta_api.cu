@@ -67,17 +67,20 @@ DeltaLayout delta_layout(ssd::DeltaParams &p, int32_t dtype) {
     if (!p.chunked) return l;
     ssd::delta_segments(p);
     const size_t f = sizeof(float), heads = (size_t)p.B * p.H;
-    l.states = align_up(heads * p.nc * ssd::delta_op_bytes());
+    l.states = align_up(heads * p.nc * ssd::delta_op_bytes(false));
     l.trans = l.states + (p.nseg > 1 ? align_up(heads * p.nseg * p.P * p.N * f) : 0);
     l.total = l.trans + (p.nseg > 1 ? align_up(heads * (p.nseg - 1) * p.N * p.N * f) : 0);
     return l;
 }
 
 struct DeltaBwdLayout {
-    size_t states, adj, u, dr, dqh, dkh, total;
+    size_t states, adj, u, dr, dqh, dkh, ops, total;
 };
 
-DeltaBwdLayout delta_bwd_layout(const ssd::DeltaParams &p) {
+DeltaBwdLayout delta_bwd_layout(ssd::DeltaParams &p, int32_t dtype) {
+    p.chunked = ssd::delta_tc_takes(p, dtype);
+    p.nseg = 1;
+    p.seg_len = p.nc * ssd::kDeltaChunk;
     const size_t f = sizeof(float), chunks = (size_t)p.B * p.H * p.nc;
     DeltaBwdLayout l;
     l.states = 0;
@@ -87,8 +90,14 @@ DeltaBwdLayout delta_bwd_layout(const ssd::DeltaParams &p) {
     l.dqh = l.dr + align_up(chunks * ssd::kDeltaChunk * p.P * f);
     const size_t share = p.H > p.G ? align_up((size_t)p.B * p.L * p.H * p.N * f) : 0;
     l.dkh = l.dqh + share;
-    l.total = l.dkh + share;
+    l.ops = l.dkh + share;
+    l.total = l.ops + (p.chunked ? align_up(chunks * ssd::delta_op_bytes(true)) : 0);
     return l;
+}
+
+void delta_bwd_params(const ssd_delta_bwd_args *b, ssd::DeltaParams &p) {
+    p.y = nullptr; p.final_state = nullptr;
+    p.dy = b->dy; p.dfinal = b->dfinal; p.dq = b->dq; p.dk = b->dk; p.dv = b->dv; p.dg = b->dg; p.dbeta = b->dbeta; p.dh0 = b->dh0;
 }
 
 ssd_status check_qk_norm(const ssd_qk_norm_args *a, ssd::QkNormParams &p) {
@@ -166,7 +175,8 @@ ssd_status ssd_delta_rule_bwd_workspace_size(const ssd_delta_bwd_args *b, size_t
     ssd_status st = check_delta(b ? &b->fwd : nullptr, p);
     if (st != SSD_OK) return st;
     if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = delta_bwd_layout(p).total;
+    delta_bwd_params(b, p);
+    *bytes = delta_bwd_layout(p, b->fwd.dtype).total;
     return ok();
 }
 
@@ -177,11 +187,11 @@ ssd_status ssd_delta_rule_bwd(const ssd_delta_bwd_args *b, void *stream) {
     if ((st = check_delta_inputs(&b->fwd)) != SSD_OK) return st;
     if (!b->dy || !b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)
         return fail(SSD_ERR_INVALID_ARG, "dy, dq, dk, dv, dg and dbeta are required");
-    const DeltaBwdLayout l = delta_bwd_layout(p);
+    delta_bwd_params(b, p);
+    const DeltaBwdLayout l = delta_bwd_layout(p, b->fwd.dtype);
     if ((st = check_workspace(b->workspace, b->workspace_bytes, l.total)) != SSD_OK) return st;
-    char *ws = static_cast<char *>(b->workspace);
-    p.y = nullptr; p.final_state = nullptr;
-    p.dy = b->dy; p.dfinal = b->dfinal; p.dq = b->dq; p.dk = b->dk; p.dv = b->dv; p.dg = b->dg; p.dbeta = b->dbeta; p.dh0 = b->dh0;
+    unsigned char *ws = static_cast<unsigned char *>(b->workspace);
+    p.ops = ws + l.ops;
     p.states = reinterpret_cast<float *>(ws + l.states);
     p.adj = reinterpret_cast<float *>(ws + l.adj);
     p.u = reinterpret_cast<float *>(ws + l.u);

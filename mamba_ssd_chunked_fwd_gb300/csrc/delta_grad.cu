@@ -366,9 +366,16 @@ cudaError_t launch_delta_grad(const DeltaParams &p, int io, cudaStream_t s) {
 }
 
 cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s) {
-    cudaError_t e = launch_delta_states(p, io, s);
-    if (e == cudaSuccess) e = launch_delta_adjoint(p, io, s);
-    return e == cudaSuccess ? launch_delta_grad(p, io, s) : e;
+    cudaError_t e;
+    if (p.chunked) {
+        if ((e = launch_delta_prep(p, io, true, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_tc_states(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_tc_adjoint(p, io, s)) != cudaSuccess) return e;
+    } else {
+        if ((e = launch_delta_states(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_adjoint(p, io, s)) != cudaSuccess) return e;
+    }
+    return launch_delta_grad(p, io, s);
 }
 
 }  // namespace ssd

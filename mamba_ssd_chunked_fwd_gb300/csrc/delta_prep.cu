@@ -149,10 +149,12 @@ struct Smem {
     static constexpr uint32_t KQ = 0;                          // k (rows 0-63) and q; once multiplied, T and A take their place
     static constexpr uint32_t T = 0, A = 16384;
     static constexpr uint32_t GATES = A + kC * kAW * 4, BYTES = GATES + (uint32_t)sizeof(Gates);  // 35 KB: six CTAs to an SM
+    static constexpr uint32_t PURE = BYTES, PURE_BYTES = PURE + 16384;
     static_assert(128 * NN * 2 <= GATES, "k and q");
 };
 
-template <int IO, int NN>
+// PURE: T itself as well, for the gradients.
+template <int IO, int NN, bool PURE>
 __global__ void __launch_bounds__(kThreads)
 delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     constexpr bool BF16 = IO == IO_BF16;
@@ -218,10 +220,13 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     Waits wait{tc::smem_addr(&bar_mem)};
     wait.on(0, 0);
     tc::fence_after_sync();
-    unsigned char *dst = p.ops + (size_t)blockIdx.x * kOpBytes;
+    unsigned char *dst = p.ops + (size_t)blockIdx.x * op_bytes(PURE);
     // what the blocks above the diagonal of T stay
 #pragma unroll
-    for (int e = 0; e < 1024 / kThreads; ++e) tcop::st_shared_v4(sbase + SM::T + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
+    for (int e = 0; e < 1024 / kThreads; ++e) {
+        tcop::st_shared_v4(sbase + SM::T + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
+        if (PURE) tcop::st_shared_v4(sbase + SM::PURE + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
+    }
     {
         const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
         const int i = tid & 63, last = i | 31;  // of the warp's rows
@@ -295,6 +300,11 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
             }
             stmatrix_x4_trans(to + bi * 256, hi);
             stmatrix_x4_trans(to + bi * 256 + kOpTerm, lo);
+            if (PURE) {
+                const Frag f = to_frag<BF16>(acc);
+                stmatrix_x4_trans(to + bi * 256 + SM::PURE - SM::T, f.hi);
+                stmatrix_x4_trans(to + bi * 256 + SM::PURE - SM::T + kOpTerm, f.lo);
+            }
         };
         // element (c, r) of block (pw, k) of the buffer, above its diagonal, will be T[r][c] of T's block (k, pw)
         float *mine = A + 16 * pw * kAW;
@@ -332,31 +342,34 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     if (tid == 0) {
         bulk_store(dst + kOpT, sbase + SM::T, 16384);
         bulk_store(dst + kOpGates, sbase + SM::GATES, (uint32_t)sizeof(Gates));
+        if (PURE) bulk_store(dst + kOpPure, sbase + SM::PURE, 16384);
         tc::bulk_commit();
         tc::bulk_wait_all();
     }
 }
 
-template <int IO, int NN>
+template <int IO, int NN, bool PURE>
 cudaError_t prep_as(const DeltaParams &p, cudaStream_t s) {
-    auto *kernel = delta_prep_kernel<IO, NN>;
-    const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
+    auto *kernel = delta_prep_kernel<IO, NN, PURE>;
+    constexpr uint32_t bytes = PURE ? Smem<NN>::PURE_BYTES : Smem<NN>::BYTES;
+    const cudaError_t e = allow_smem<bytes>(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long long)p.B * p.H * p.nc), kThreads, Smem<NN>::BYTES, s>>>(p);
+    kernel<<<(unsigned)((long long)p.B * p.H * p.nc), kThreads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 
 template <int IO>
-cudaError_t prep_io(const DeltaParams &p, cudaStream_t s) {
-    return p.N <= 64 ? prep_as<IO, 64>(p, s) : prep_as<IO, 128>(p, s);
+cudaError_t prep_io(const DeltaParams &p, bool pure, cudaStream_t s) {
+    if (pure) return p.N <= 64 ? prep_as<IO, 64, true>(p, s) : prep_as<IO, 128, true>(p, s);
+    return p.N <= 64 ? prep_as<IO, 64, false>(p, s) : prep_as<IO, 128, false>(p, s);
 }
 
 }  // namespace
 
-size_t delta_op_bytes() { return kOpBytes; }
+size_t delta_op_bytes(bool pure) { return op_bytes(pure); }
 
-cudaError_t launch_delta_prep(const DeltaParams &p, int io, cudaStream_t s) {
-    return io == IO_BF16 ? prep_io<IO_BF16>(p, s) : prep_io<IO_F16>(p, s);
+cudaError_t launch_delta_prep(const DeltaParams &p, int io, bool pure, cudaStream_t s) {
+    return io == IO_BF16 ? prep_io<IO_BF16>(p, pure, s) : prep_io<IO_F16>(p, pure, s);
 }
 
 }  // namespace ssd

@@ -56,36 +56,18 @@ struct Tm {
     static constexpr uint32_t S = 0, X1 = NN, X2 = NN + 64, DS = NN + 128, O = 2 * NN + 128, COLS = 512;  // two of O
 };
 
-// Global to shared memory, completing on an mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 8 columns on.
-template <bool BF16>
-__device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 f = *reinterpret_cast<const float4 *>(f16 + 4 * i);
-        split2<BF16>(__fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
-        split2<BF16>(__fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
-    }
-    tc::tmem_st8(to, hi);
-    tc::tmem_st8(to + 8, lo);
-}
-
 // What a CTA walks: tokens [t0, t1) of a head, from a state to a state.
 struct Walk {
     int b, h, p0, t0, t1, chunks;
 };
 
-// LOCAL: a segment's own state (from zero, the rows of v) and its transition (from the unit matrix, v = 0), no y.
-template <int IO, int NN, bool LOCAL>
+// What a walk gives: y and the last state; LOCAL: a segment's own state (from zero, the rows of v) and its transition
+// (from the unit matrix, v = 0); STATES: for the gradients, the state before every chunk and U.
+enum Mode { Y, LOCAL_STATE, STATES };
+template <int IO, int NN, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_tc_kernel(const __grid_constant__ DeltaParams p) {
-    constexpr bool BF16 = IO == IO_BF16;
+    constexpr bool BF16 = IO == IO_BF16, LOCAL = MODE == LOCAL_STATE;
     using SM = Smem<NN>;
     using TM = Tm<NN>;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -182,6 +164,12 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 }
             }
             if (c >= w.chunks) break;
+            if (MODE == STATES && row < rows) {
+                float *dst = p.states + ((size_t)bh * p.nc + c) * pn + (size_t)(w.p0 + row) * p.N + part * CW;
+#pragma unroll
+                for (int j = 0; j < CW / 4; ++j)
+                    if (part * CW + 4 * j < p.N) *reinterpret_cast<float4 *>(dst + 4 * j) = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+            }
             const Gates &gt = gates[c % kSlots];
             wait.on(kFullOp + par, (c >> 1) & 1);  // the gates
             wait.on(kD1, par);
@@ -199,7 +187,13 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kU + part));
-            if (!LOCAL) {  // U itself, for y
+            if (MODE == STATES && row < rows) {
+                float *dst = p.u + ((size_t)bh * p.nc * kC + c * kC + 16 * part) * p.P + w.p0 + row;
+                const float bad = wait.dead() ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dst[(size_t)i * p.P] = v[i] + bad;
+            }
+            if (MODE == Y) {  // U itself, for y
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
@@ -227,7 +221,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         }
     } else if (warp < kMmaWarp) {
         // ---- y: thread = row of the state
-        if (!LOCAL) {
+        if (MODE == Y) {
             const int quarter = warp - kOutWarp0, row = quarter * 32 + lane;
             const bool ok = row < rows;
             const size_t step = (size_t)p.H * p.P;
@@ -268,8 +262,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     // neighbouring lanes exchange: each then has two rows of every second token, a store of 4 bytes
 #pragma unroll
                     for (int m = 0; m < 16; m += 2, to += 2 * step) {
-                        const uint32_t own = tcop::pack2(scale * v[m], scale * v[m + 1], BF16), other = __shfl_xor_sync(0xffffffffu, own, 1);
-                        const uint32_t two = __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+                        const uint32_t two = exchange_rows<BF16>(scale * v[m], scale * v[m + 1], odd);
                         if (ok && j + m + odd < n) *reinterpret_cast<uint32_t *>(to) = two;
                     }
                 }
@@ -336,7 +329,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 }
             }
             if (go) tc::commit(bars + 8 * kD2);
-            if (!LOCAL) {  // while the chain splits U
+            if (MODE == Y) {  // while the chain splits U
                 wait.on(kD4Read + par, par2 ^ 1);
                 tc::fence_after_sync();
                 if (go) {
@@ -362,7 +355,7 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                 tc::commit(bars + 8 * kDS);
                 tc::commit(bars + 8 * (kEmptyKQ + c % kStages));
             }
-            if (!LOCAL) {
+            if (MODE == Y) {
                 wait.on(kUOut, par);
                 wait.on(kD3Read + par, par2);
                 tc::fence_after_sync();
@@ -388,23 +381,25 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
         const void *src = which == 0 ? p.k : which == 1 ? p.q : p.v;
         const long long s0 = which == 0 ? p.ks[0] : which == 1 ? p.qs[0] : p.vs[0], s1 = which == 0 ? p.ks[1] : which == 1 ? p.qs[1] : p.vs[1];
         const char *from = static_cast<const char *>(src) + 2 * (w.b * s0 + (which < 2 ? (long long)grp * p.N : (long long)w.h * p.P + w.p0) + 8 * piece);
-        // of a row of 16-byte pieces, those that exist from this lane's on; none of q in a pass without y, nor of v in a transition's
-        const int width = (which == 1 && LOCAL) || (which == 2 && unit) ? 0 : (which < 2 ? p.N : rows) - 8 * piece;
+        // of a row of 16-byte pieces, those that exist from this lane's on; none of q in a walk without y, nor of v in a transition's
+        const int width = (which == 1 && MODE != Y) || (which == 2 && unit) ? 0 : (which < 2 ? p.N : rows) - 8 * piece;
         const uint32_t to = sbase + (which < 2 ? SM::KQ + which * 1024 + piece * 2048 : SM::V + piece * 128) + r * 16;
         const uint32_t stage = which < 2 ? SM::KQ_BYTES : SM::V_BYTES, row_step = which < 2 ? 128 : 2048, col_step = which < 2 ? 8192 : 512;
         const int stages = which < 2 ? kStages : kVStages, empty = which < 2 ? kEmptyKQ : kEmptyV, full = which < 2 ? kFullKQ : kFullV;
         int at = 0;
         uint32_t parity = 1;
-        const unsigned char *ops = p.ops + ((size_t)bh * p.nc + w.t0 / kC) * kOpBytes;
+        const unsigned char *ops = p.ops + ((size_t)bh * p.nc + w.t0 / kC) * op_bytes(MODE == STATES);
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
             if (which == 2) {  // with a place of T's, the gates four chunks back are done with too
                 wait.on(kEmptyOp + (c & 1), ((c >> 1) & 1) ^ 1);
                 if (lane == 0) {
                     const uint32_t bar = bars + 8 * (kFullOp + (c & 1));
-                    tc::mbar_arrive_expect_tx(bar, kOpBytes);
-                    bulk_load(sbase + SM::OP + (c & 1) * kOpGates, ops + (size_t)c * kOpBytes, kOpGates, bar);
-                    bulk_load(sbase + SM::GATES + (c % kSlots) * (uint32_t)sizeof(Gates), ops + (size_t)c * kOpBytes + kOpGates, (uint32_t)sizeof(Gates), bar);
+                    constexpr uint32_t bytes = MODE == Y ? kOpGates : kOpM;  // T and M, or T alone
+                    const unsigned char *op = ops + (size_t)c * op_bytes(MODE == STATES);
+                    tc::mbar_arrive_expect_tx(bar, bytes + (uint32_t)sizeof(Gates));
+                    bulk_load(sbase + SM::OP + (c & 1) * kOpGates, op, bytes, bar);
+                    bulk_load(sbase + SM::GATES + (c % kSlots) * (uint32_t)sizeof(Gates), op + kOpGates, (uint32_t)sizeof(Gates), bar);
                 }
                 __syncwarp();
             }
@@ -486,35 +481,31 @@ delta_fold_kernel(const __grid_constant__ DeltaParams p) {
     }
 }
 
-template <int IO, int NN>
-cudaError_t tc_as(const DeltaParams &p, bool local, cudaStream_t s) {
-    const long long tiles = (p.P + 127) / 128;
-    if (local) {
-        auto *kernel = delta_tc_kernel<IO, NN, true>;
-        const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
-        if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)((long long)p.B * p.H * (p.nseg - 1) * (tiles + 1)), kThreads, Smem<NN>::BYTES, s>>>(p);
-    } else {
-        auto *kernel = delta_tc_kernel<IO, NN, false>;
-        const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
-        if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)((long long)p.B * p.H * p.nseg * tiles), kThreads, Smem<NN>::BYTES, s>>>(p);
-    }
+template <int IO, int NN, int MODE>
+cudaError_t tc_as(const DeltaParams &p, cudaStream_t s) {
+    const long long tiles = (p.P + 127) / 128, heads = (long long)p.B * p.H;
+    auto *kernel = delta_tc_kernel<IO, NN, MODE>;
+    const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(MODE == LOCAL_STATE ? heads * (p.nseg - 1) * (tiles + 1) : heads * p.nseg * tiles), kThreads, Smem<NN>::BYTES, s>>>(p);
     return cudaGetLastError();
+}
+template <int IO, int MODE>
+cudaError_t tc_mode(const DeltaParams &p, cudaStream_t s) {
+    return p.N <= 64 ? tc_as<IO, 64, MODE>(p, s) : tc_as<IO, 128, MODE>(p, s);
 }
 
 template <int IO>
 cudaError_t tc_io(const DeltaParams &p, cudaStream_t s) {
-    cudaError_t e = launch_delta_prep(p, IO, s);
+    cudaError_t e = launch_delta_prep(p, IO, false, s);
     if (e == cudaSuccess && p.nseg > 1) {
-        e = p.N <= 64 ? tc_as<IO, 64>(p, true, s) : tc_as<IO, 128>(p, true, s);
+        e = tc_mode<IO, LOCAL_STATE>(p, s);
         if (e == cudaSuccess) e = allow_smem<kFoldBytes>(delta_fold_kernel);
         if (e != cudaSuccess) return e;
         delta_fold_kernel<<<(unsigned)((long long)p.B * p.H * ((p.P + kFoldRows - 1) / kFoldRows)), kFoldThreads, kFoldBytes, s>>>(p);
         e = cudaGetLastError();
     }
-    if (e != cudaSuccess) return e;
-    return p.N <= 64 ? tc_as<IO, 64>(p, false, s) : tc_as<IO, 128>(p, false, s);
+    return e == cudaSuccess ? tc_mode<IO, Y>(p, s) : e;
 }
 
 bool by_eights(const void *p, long long s0, long long s1) {
@@ -526,7 +517,8 @@ bool by_eights(const void *p, long long s0, long long s1) {
 // 16-byte pieces of k, q and v, and float4 of the states.
 bool delta_tc_takes(const DeltaParams &p, int io) {
     return io != IO_F32 && p.N % 8 == 0 && p.P % 8 == 0 && by_eights(p.k, p.ks[0], p.ks[1]) && by_eights(p.q, p.qs[0], p.qs[1]) &&
-           by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0);
+           by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0) &&
+           by_eights(p.dy, 0, 0) && by_eights(p.dv, 0, 0) && by_eights(p.dfinal, 0, 0) && by_eights(p.dh0, 0, 0);
 }
 
 // The cut of the rows into segments.  A walk takes an SM for itself, and a chunk about 3.3 us of it (a pass of a segment's own
@@ -545,6 +537,10 @@ void delta_segments(DeltaParams &p) {
     const int len = (p.nc + best - 1) / best;
     p.seg_len = len * kC;
     p.nseg = (p.nc + len - 1) / len;
+}
+
+cudaError_t launch_delta_tc_states(const DeltaParams &p, int io, cudaStream_t s) {
+    return io == IO_BF16 ? tc_mode<IO_BF16, STATES>(p, s) : tc_mode<IO_F16, STATES>(p, s);
 }
 
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s) {

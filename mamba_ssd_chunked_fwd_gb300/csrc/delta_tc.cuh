@@ -19,7 +19,9 @@ struct alignas(16) Gates {
 
 // What delta_prep.cu leaves of every chunk of every head: T diag(beta) and M, both 64 x 64 in blocks of 8 rows x 16
 // bytes (block (column / 8, row / 8) at (column / 8) * 1024 + (row / 8) * 128), as first terms, then second ones; the gates.
-constexpr uint32_t kOpT = 0, kOpM = 16384, kOpTerm = 8192, kOpGates = 32768, kOpBytes = kOpGates + (uint32_t)sizeof(Gates);
+// For the gradients T itself follows.
+constexpr uint32_t kOpT = 0, kOpM = 16384, kOpTerm = 8192, kOpGates = 32768, kOpPure = kOpGates + (uint32_t)sizeof(Gates);
+__host__ __device__ constexpr uint32_t op_bytes(bool pure) { return kOpPure + (pure ? 16384u : 0u); }
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -51,5 +53,33 @@ struct Waits {
         asm volatile("" : "+r"(tries));  // or the code after it is laid out twice, for a thread that waits and one that does not
     }
 };
+
+// Global to shared memory, completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 8 columns on.
+template <bool BF16>
+__device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4 *>(f16 + 4 * i);
+        split2<BF16>(__fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
+        split2<BF16>(__fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
+    }
+    tc::tmem_st8(to, hi);
+    tc::tmem_st8(to + 8, lo);
+}
+
+// A pair of neighbouring tokens' values of neighbouring lanes' rows exchanged: an even lane gets its row and the next of the
+// first token, an odd lane the row before and its own of the second.
+template <bool BF16>
+__device__ __forceinline__ uint32_t exchange_rows(float first, float second, int odd) {
+    const uint32_t own = tcop::pack2(first, second, BF16), other = __shfl_xor_sync(0xffffffffu, own, 1);
+    return __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+}
 
 }  // namespace ssd
