@@ -33,6 +33,7 @@ struct DeltaParams {
     const float *dfinal;
     void *dq, *dk, *dv, *dg, *dbeta;
     float *dh0;
+    // (in chunks on the tensor cores these four are operands of the same size, N and P rounded up: delta_tc.cuh)
     float *states;  // [B,H,nc,P,N] state before a chunk
     float *adj;     // [B,H,nc,P,N] adjoint of the state after a chunk
     float *u, *dr;  // [B,H,64 nc,P] u, and the gradient of v_t - S' k_t over beta
@@ -56,6 +57,7 @@ cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);    
 size_t delta_op_bytes(bool pure);
 cudaError_t launch_delta_prep(const DeltaParams &p, int io, bool pure, cudaStream_t s);   // a chunk's operands for the next three
 cudaError_t launch_delta_tc_states(const DeltaParams &p, int io, cudaStream_t s);         // as launch_delta_states
+cudaError_t launch_delta_grad_tc(const DeltaParams &p, int io, cudaStream_t s);           // as launch_delta_grad
 cudaError_t launch_delta_tc_adjoint(const DeltaParams &p, int io, cudaStream_t s);        // as launch_delta_adjoint
 void delta_segments(DeltaParams &p);
 bool delta_tc_takes(const DeltaParams &p, int io);

@@ -13,7 +13,7 @@
 //   16 warps the chain;  4 warps make an operand of d;  1 warp issues the products
 //   3 warps  copy k, q, and dy with a chunk's operands ahead
 //
-// It writes D after every chunk and R, in fp32, for delta_grad.cu's kernels, and dv.
+// It leaves D after every chunk and R as operands for delta_grad_tc.cu, and writes dv.
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -131,11 +131,11 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     tc::mbar_arrive(bars + 8 * (kS + j));
+                    store_op(state_op<NN>(p.adj, (size_t)bh * p.nc + chunks - 1 - i, tiles, p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
                 }
             }
             if (i >= chunks) break;
             const int c = chunks - 1 - i;
-            store_rows(p.adj + ((size_t)bh * p.nc + c) * pn);
             const Gates &gt = gates[i % kSlots];
             wait.on(kFullOp + par, (i >> 1) & 1);  // the gates
             wait.on(kD1, par);
@@ -182,11 +182,13 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
             {
                 const float bad = wait.dead() ? __int_as_float(0x7fffffff) : 0.f;
                 const int t = c * kC + 16 * part;
-                float *dr = p.dr + ((size_t)bh * p.nc * kC + t) * p.P + p0 + row;
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split2<BF16>(make_float2(v[2 * e] + bad, v[2 * e + 1] + bad), hi[e], lo[e]);
+                store_op(token_op(p.dr, (size_t)bh * p.nc + c, tiles, p0 + row) + 2 * part * 128, hi, lo, 1024);
                 uint16_t *to = dv + (size_t)t * step;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                    if (ok) dr[(size_t)e * p.P] = v[e] + bad, dr[(size_t)(e + 1) * p.P] = v[e + 1] + bad;
                     const uint32_t two = exchange_rows<BF16>(beta[e] * v[e] + bad, beta[e + 1] * v[e + 1] + bad, odd);
                     if (ok && t + e + odd < len) *reinterpret_cast<uint32_t *>(to + e * step) = two;
                 }

@@ -82,12 +82,14 @@ DeltaBwdLayout delta_bwd_layout(ssd::DeltaParams &p, int32_t dtype) {
     p.nseg = 1;
     p.seg_len = p.nc * ssd::kDeltaChunk;
     const size_t f = sizeof(float), chunks = (size_t)p.B * p.H * p.nc;
+    // as operands, whole tiles of rows and columns
+    const size_t P = p.chunked ? (p.P + 127) / 128 * 128 : p.P, N = p.chunked ? (p.N <= 64 ? 64 : 128) : p.N;
     DeltaBwdLayout l;
     l.states = 0;
-    l.adj = l.states + align_up(chunks * p.P * p.N * f);
-    l.u = l.adj + align_up(chunks * p.P * p.N * f);
-    l.dr = l.u + align_up(chunks * ssd::kDeltaChunk * p.P * f);
-    l.dqh = l.dr + align_up(chunks * ssd::kDeltaChunk * p.P * f);
+    l.adj = l.states + align_up(chunks * P * N * f);
+    l.u = l.adj + align_up(chunks * P * N * f);
+    l.dr = l.u + align_up(chunks * ssd::kDeltaChunk * P * f);
+    l.dqh = l.dr + align_up(chunks * ssd::kDeltaChunk * P * f);
     const size_t share = p.H > p.G ? align_up((size_t)p.B * p.L * p.H * p.N * f) : 0;
     l.dkh = l.dqh + share;
     l.ops = l.dkh + share;

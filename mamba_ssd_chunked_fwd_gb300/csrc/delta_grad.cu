@@ -347,10 +347,15 @@ cudaError_t grad_as(const DeltaParams &p, cudaStream_t s) {
 
 template <int IO>
 cudaError_t grad_io(const DeltaParams &p, cudaStream_t s) {
-    cudaError_t e = p.N <= 64 ? grad_as<IO, 64>(p, s) : grad_as<IO, 128>(p, s);
-    if (e != cudaSuccess || p.H == p.G) return e;
+    return p.N <= 64 ? grad_as<IO, 64>(p, s) : grad_as<IO, 128>(p, s);
+}
+
+cudaError_t launch_delta_heads(const DeltaParams &p, int io, cudaStream_t s) {
     const long long count = (long long)p.B * p.L * p.G * p.N;
-    delta_heads_kernel<IO><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(p);
+    const unsigned grid = (unsigned)((count + 255) / 256);
+    if (io == IO_F32) delta_heads_kernel<IO_F32><<<grid, 256, 0, s>>>(p);
+    else if (io == IO_F16) delta_heads_kernel<IO_F16><<<grid, 256, 0, s>>>(p);
+    else delta_heads_kernel<IO_BF16><<<grid, 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -371,11 +376,13 @@ cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s) {
         if ((e = launch_delta_prep(p, io, true, s)) != cudaSuccess) return e;
         if ((e = launch_delta_tc_states(p, io, s)) != cudaSuccess) return e;
         if ((e = launch_delta_tc_adjoint(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_grad_tc(p, io, s)) != cudaSuccess) return e;
     } else {
         if ((e = launch_delta_states(p, io, s)) != cudaSuccess) return e;
         if ((e = launch_delta_adjoint(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_grad(p, io, s)) != cudaSuccess) return e;
     }
-    return launch_delta_grad(p, io, s);
+    return p.H > p.G ? launch_delta_heads(p, io, s) : cudaSuccess;
 }
 
 }  // namespace ssd

@@ -23,14 +23,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kAW = 68;  // floats between rows of A
 
-// ex2 that stays where it is: moved into a branch on whether its result is wanted, each would wait for the one before
-// (measured: 68 cycles an element in place of 20).
-__device__ __forceinline__ float ex2_now(float v) {
-    float r;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // D (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums.
 template <bool BF16>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {

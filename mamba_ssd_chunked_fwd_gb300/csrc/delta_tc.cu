@@ -161,15 +161,11 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     tc::mbar_arrive(bars + 8 * (kS + j));
+                    if (MODE == STATES)
+                        store_op(state_op<NN>(p.states, (size_t)bh * p.nc + c, ptiles, w.p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
                 }
             }
             if (c >= w.chunks) break;
-            if (MODE == STATES && row < rows) {
-                float *dst = p.states + ((size_t)bh * p.nc + c) * pn + (size_t)(w.p0 + row) * p.N + part * CW;
-#pragma unroll
-                for (int j = 0; j < CW / 4; ++j)
-                    if (part * CW + 4 * j < p.N) *reinterpret_cast<float4 *>(dst + 4 * j) = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
-            }
             const Gates &gt = gates[c % kSlots];
             wait.on(kFullOp + par, (c >> 1) & 1);  // the gates
             wait.on(kD1, par);
@@ -187,16 +183,15 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kU + part));
-            if (MODE == STATES && row < rows) {
-                float *dst = p.u + ((size_t)bh * p.nc * kC + c * kC + 16 * part) * p.P + w.p0 + row;
+            if (MODE != LOCAL_STATE) {  // U itself, for y or the gradients
                 const float bad = wait.dead() ? __int_as_float(0x7fffffff) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) dst[(size_t)i * p.P] = v[i] + bad;
-            }
-            if (MODE == Y) {  // U itself, for y
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[2 * i], v[2 * i + 1]), hi[i], lo[i]);
+                for (int i = 0; i < 8; ++i) split2<BF16>(make_float2(v[2 * i] + bad, v[2 * i + 1] + bad), hi[i], lo[i]);
+                if (MODE == STATES) {
+                    store_op(token_op(p.u, (size_t)bh * p.nc + c, ptiles, w.p0 + row) + 2 * part * 128, hi, lo, 1024);
+                    continue;
+                }
                 tc::tmem_st8(x2, hi);
                 tc::tmem_st8(x2 + 8, lo);
                 tc::tmem_wait_st();
@@ -518,7 +513,7 @@ bool by_eights(const void *p, long long s0, long long s1) {
 bool delta_tc_takes(const DeltaParams &p, int io) {
     return io != IO_F32 && p.N % 8 == 0 && p.P % 8 == 0 && by_eights(p.k, p.ks[0], p.ks[1]) && by_eights(p.q, p.qs[0], p.qs[1]) &&
            by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0) &&
-           by_eights(p.dy, 0, 0) && by_eights(p.dv, 0, 0) && by_eights(p.dfinal, 0, 0) && by_eights(p.dh0, 0, 0);
+           by_eights(p.dy, 0, 0) && by_eights(p.dq, 0, 0) && by_eights(p.dk, 0, 0) && by_eights(p.dv, 0, 0) && by_eights(p.dfinal, 0, 0) && by_eights(p.dh0, 0, 0);
 }
 
 // The cut of the rows into segments.  A walk takes an SM for itself, and a chunk about 3.3 us of it (a pass of a segment's own
