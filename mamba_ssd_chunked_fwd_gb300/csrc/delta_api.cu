@@ -129,7 +129,7 @@ ssd_status check_qk_norm(const ssd_qk_norm_args *a, ssd::QkNormParams &p) {
 }
 
 size_t qk_norm_bwd_bytes(const ssd::QkNormParams &p) {
-    return p.w_q || p.w_k ? align_up((size_t)ssd::qk_norm_parts(p) * 2 * p.N * sizeof(float)) : 0;
+    return p.w_q || p.w_k ? align_up((size_t)ssd::qk_norm_parts(p) * p.N * sizeof(float)) : 0;
 }
 
 }  // namespace

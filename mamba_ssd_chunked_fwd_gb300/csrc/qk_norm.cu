@@ -54,26 +54,50 @@ __device__ __forceinline__ Unit unit_of(int u, int half, int interleaved) {
     return x;
 }
 
-template <int IO, int Q>
-struct Run {
-    Raw4 a, b;
-};
+// A run of Q elements: 16 or 8 bytes, or one element.
 template <int IO, int Q>
 __device__ __forceinline__ Raw4 load_run(const void *base, long long i, bool ok) {
-    if (Q == 4) return load_raw4<IO, true, false>(base, i, ok, 4);
-    return load_raw4<IO, false, false>(base, i, ok, 1);
+    if (Q == 1) return load_raw4<IO, false, false>(base, i, ok, 1);
+    Raw4 r = {{0u, 0u, 0u, 0u}};
+    const char *at = static_cast<const char *>(base) + i * (IO == IO_F32 ? 4 : 2);
+    if (IO == IO_F32 || Q == 8) ld_v4(r.w, at, ok);
+    else ld_v2(r.w, at, ok);
+    return r;
 }
 template <int IO, int Q>
 __device__ __forceinline__ void unpack_run(const Raw4 &r, float (&v)[Q]) {
-    float f[4];
-    unpack4<IO, Q == 4>(r, f);
+    if (Q == 1) {
+        float f[4];
+        unpack4<IO, false>(r, f);
+        v[0] = f[0];
+    } else if (IO == IO_F32) {
 #pragma unroll
-    for (int j = 0; j < Q; ++j) v[j] = f[j];
+        for (int j = 0; j < Q; ++j) v[j] = __uint_as_float(r.w[j & 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < Q / 2; ++j) {
+            if (IO == IO_BF16) {
+                v[2 * j] = __uint_as_float(r.w[j & 3] << 16), v[2 * j + 1] = __uint_as_float(r.w[j & 3] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[j & 3]));
+                v[2 * j] = f.x, v[2 * j + 1] = f.y;
+            }
+        }
+    }
 }
 template <int IO, int Q>
 __device__ __forceinline__ void store_run(void *base, long long i, const float (&v)[Q]) {
-    const float f[4] = {v[0], Q == 4 ? v[Q > 1] : 0.f, Q == 4 ? v[Q > 2 ? 2 : 0] : 0.f, Q == 4 ? v[Q > 3 ? 3 : 0] : 0.f};
-    store4_io<IO, Q == 4>(base, i, Q, f);
+    if (Q == 1) {
+        st_io<IO>(base, i, v[0]);
+    } else if (IO == IO_F32) {
+        reinterpret_cast<float4 *>(static_cast<float *>(base) + i)[0] = make_float4(v[0], v[Q > 1], v[Q > 2 ? 2 : 0], v[Q > 3 ? 3 : 0]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack16<IO>(make_float2(v[(2 * j) % Q], v[(2 * j + 1) % Q]));
+        if (Q == 8) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = make_uint2(w[0], w[1]);
+    }
 }
 
 // The pairs of a unit turned by their angles (sign -1: back).
@@ -107,14 +131,15 @@ __device__ __forceinline__ float sum_group(float v) {
 }
 
 // One tensor's rows of a tile: `heads` of each of nt tokens, RU rows at a time so that their loads overlap.
+// `from`: where the tile's tokens begin; `magic`: ceil(2^32 / heads), for r / heads (0: one head).
 template <int IO, int Q, int M, int LPR, bool BWD>
-__device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long long tok0, int nt, const float2 *table, float (&dw)[M][2][Q]) {
-    constexpr int kGroups = kThreads / LPR, RU = M > 1 ? 1 : BWD ? 2 : 4;
+__device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long long tok0, int nt, const float2 *table, const long long *from,
+                                        uint32_t magic, float (&dw)[M][2][Q]) {
+    constexpr int kGroups = kThreads / LPR, RU = M > 1 ? 1 : BWD || Q == 8 ? 2 : 4;
     const int heads = which ? p.G : p.H, ln = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const void *x = which ? p.k : p.q, *dy = which ? p.dk_out : p.dq_out;
     const float *w = which ? p.w_k : p.w_q;
     void *out = BWD ? (which ? p.dk : p.dq) : (which ? p.k_out : p.q_out);
-    const long long s0 = which ? p.ks[0] : p.qs[0], s1 = which ? p.ks[1] : p.qs[1];
     const float div = p.l2 ? 1.f : 1.f / p.N;
     Unit un[M];
     bool oka[M], okb[M];
@@ -139,10 +164,9 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
         for (int i = 0; i < RU; ++i) {
             const int r = r0 + i * kGroups;
             ok[i] = r < rows;
-            tk[i] = ok[i] ? r / heads : 0;
-            const int h = r - tk[i] * heads;
-            const long long t = tok0 + tk[i], at = (t / p.L) * s0 + (t % p.L) * s1 + (long long)h * p.N;
-            to[i] = (t * heads + h) * p.N;
+            tk[i] = ok[i] ? (magic ? (int)__umulhi((uint32_t)r, magic) : r) : 0;
+            const long long at = from[tk[i]] + (long long)(r - tk[i] * heads) * p.N;
+            to[i] = (tok0 * heads + r) * p.N;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 xa[i][m] = load_run<IO, Q>(x, at + un[m].a, ok[i] && oka[m]);
@@ -208,9 +232,9 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
 
 // The CTA's sums of dw, the groups one after another.
 template <int Q, int M, int LPR>
-__device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&dwq)[M][2][Q], const float (&dwk)[M][2][Q]) {
-    __shared__ float sums[2 * kMaxHalf * 2];
-    for (int i = threadIdx.x; i < 2 * p.N; i += kThreads) sums[i] = 0.f;
+__device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&dw)[M][2][Q]) {
+    __shared__ float sums[2 * kMaxHalf];
+    for (int i = threadIdx.x; i < p.N; i += kThreads) sums[i] = 0.f;
     for (int g = 0; g < kThreads / LPR; ++g) {
         __syncthreads();
         if ((int)threadIdx.x / LPR != g) continue;
@@ -219,88 +243,109 @@ __device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&
             const Unit un = unit_of<Q>(threadIdx.x % LPR + LPR * m, p.half, p.interleaved);
 #pragma unroll
             for (int j = 0; j < Q; ++j) {
-                if (un.a < p.N) sums[un.a + j] += dwq[m][0][j], sums[p.N + un.a + j] += dwk[m][0][j];
-                if (un.b < p.N) sums[un.b + j] += dwq[m][1][j], sums[p.N + un.b + j] += dwk[m][1][j];
+                if (un.a < p.N) sums[un.a + j] += dw[m][0][j];
+                if (un.b < p.N) sums[un.b + j] += dw[m][1][j];
             }
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.N; i += kThreads) p.part[(size_t)blockIdx.x * 2 * p.N + i] = sums[i];
+    for (int i = threadIdx.x; i < p.N; i += kThreads) p.part[(size_t)blockIdx.x * p.N + i] = sums[i];
 }
 
+// Backward a CTA takes one of the two tensors (the first nq of them the queries), so that one set of sums lies in registers.
 template <int IO, int Q, int M, int LPR, bool BWD>
-__global__ void __launch_bounds__(kThreads)
-qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile) {
+__global__ void __launch_bounds__(kThreads, M > 1 || BWD ? 2 : 3)
+qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile, int nq, uint32_t magic_q, uint32_t magic_k) {
     __shared__ __align__(16) float2 table[kTokens * kMaxHalf];
     __shared__ unsigned long long turn[kMaxHalf];
+    __shared__ long long from[2][kTokens];
     const long long tokens = (long long)p.B * p.L;
-    float dwq[M][2][Q] = {}, dwk[M][2][Q] = {};
+    float dw[M][2][Q] = {};
     for (int i = threadIdx.x; i < p.half; i += kThreads) turn[i] = turn_of(__ldg(p.freqs + i));
-    for (long long tok0 = (long long)blockIdx.x * tile; tok0 < tokens; tok0 += (long long)gridDim.x * tile) {
+    const int which = BWD && (int)blockIdx.x >= nq, first = blockIdx.x - which * nq, step = BWD ? (which ? gridDim.x - nq : nq) : gridDim.x;
+    for (long long tok0 = (long long)first * tile; tok0 < tokens; tok0 += (long long)step * tile) {
         const int nt = (int)min((long long)tile, tokens - tok0);
-        if (p.half) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < nt * p.half; e += kThreads) {
-                const int t = e / p.half;
-                const long long tok = tok0 + t;
-                table[e] = cos_sin(turn[e - t * p.half], p.positions ? __ldg(p.positions + tok) : (int)(tok % p.L));
-            }
-            __syncthreads();
+        __syncthreads();
+        if ((int)threadIdx.x < 2 * nt) {
+            const long long tok = tok0 + (threadIdx.x >> 1), row = tok / p.L, t = tok - row * p.L;
+            from[threadIdx.x & 1][threadIdx.x >> 1] = threadIdx.x & 1 ? row * p.ks[0] + t * p.ks[1] : row * p.qs[0] + t * p.qs[1];
         }
-        rows_of<IO, Q, M, LPR, BWD>(p, 0, tok0, nt, table, dwq);
-        rows_of<IO, Q, M, LPR, BWD>(p, 1, tok0, nt, table, dwk);
+        for (int e = threadIdx.x; e < nt * p.half; e += kThreads) {
+            const int t = e / p.half;
+            const long long tok = tok0 + t;
+            table[e] = cos_sin(turn[e - t * p.half], p.positions ? __ldg(p.positions + tok) : (int)(tok % p.L));
+        }
+        __syncthreads();
+        if (!BWD || which == 0) rows_of<IO, Q, M, LPR, BWD>(p, 0, tok0, nt, table, from[0], magic_q, dw);
+        if (!BWD || which == 1) rows_of<IO, Q, M, LPR, BWD>(p, 1, tok0, nt, table, from[1], magic_k, dw);
     }
-    if constexpr (BWD) if (p.w_q || p.w_k) store_sums<Q, M, LPR>(p, dwq, dwk);
+    if constexpr (BWD) if (which ? p.w_k : p.w_q) store_sums<Q, M, LPR>(p, dw);
 }
 
 // dw_q, dw_k: the CTAs' sums, 8 threads to a column, each over every eighth row.
 __global__ void __launch_bounds__(256)
-qk_norm_weights_kernel(const __grid_constant__ QkNormParams p, int parts) {
+qk_norm_weights_kernel(const __grid_constant__ QkNormParams p, int nq, int parts) {
     __shared__ float s[8][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x, which = blockIdx.y;
+    float *out = which ? p.dw_k : p.dw_q;
+    if (!out) return;
     float v = 0.f;
-    if (col < 2 * p.N)
-        for (int i = y; i < parts; i += 8) v += p.part[(size_t)i * 2 * p.N + col];
-    s[y][threadIdx.x & 31] = v;
+    if (col < p.N)
+        for (int i = (which ? nq : 0) + y; i < (which ? parts : nq); i += 8) v += p.part[(size_t)i * p.N + col];
+    s[y][x] = v;
     __syncthreads();
-    if (y != 0 || col >= 2 * p.N) return;
+    if (y != 0 || col >= p.N) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x & 31];
-    if (col < p.N) {
-        if (p.dw_q) p.dw_q[col] = v;
-    } else if (p.dw_k) {
-        p.dw_k[col - p.N] = v;
-    }
+    for (int i = 1; i < 8; ++i) v += s[i][x];
+    out[col] = v;
 }
 
-// Tokens of a tile: as many as leave every SM eight CTAs.
+// Tokens of a tile: as many as leave every SM two CTAs, and rows that the division by a product serves (65536).
 int tile_of(const QkNormParams &p) {
-    const long long tokens = (long long)p.B * p.L, most = tokens / (8LL * scan_sm_count());
+    if (p.H > 2048 || p.G > 2048) return 1;
+    const long long tokens = (long long)p.B * p.L, most = tokens / (2LL * scan_sm_count());
     int t = 1;
     while (t < kTokens && 2 * t <= most) t *= 2;
     return t;
 }
 
+// Of the backward's CTAs, two to an SM, those that take the queries: their share of the heads.
+int parts_of_q(const QkNormParams &p, int parts) {
+    const int q = (int)((long long)parts * p.H / (p.H + p.G));
+    return q < 1 ? 1 : q > parts - 1 ? parts - 1 : q;
+}
+
 template <int IO, int Q, int M, int LPR>
 cudaError_t norm_as(const QkNormParams &p, bool bwd, cudaStream_t s) {
     const int tile = tile_of(p);
+    const uint32_t mq = (uint32_t)((0x100000000ull + p.H - 1) / p.H), mk = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
     if (!bwd) {
         const long long tiles = ((long long)p.B * p.L + tile - 1) / tile;
-        qk_norm_kernel<IO, Q, M, LPR, false><<<(unsigned)min(tiles, (long long)1 << 30), kThreads, 0, s>>>(p, tile);
+        qk_norm_kernel<IO, Q, M, LPR, false><<<(unsigned)min(tiles, (long long)1 << 30), kThreads, 0, s>>>(p, tile, 0, mq, mk);
         return cudaGetLastError();
     }
-    const int parts = qk_norm_parts(p);
-    qk_norm_kernel<IO, Q, M, LPR, true><<<parts, kThreads, 0, s>>>(p, tile);
-    if (p.w_q || p.w_k) qk_norm_weights_kernel<<<(2 * p.N + 31) / 32, 256, 0, s>>>(p, parts);
+    const int parts = qk_norm_parts(p), nq = parts_of_q(p, parts);
+    qk_norm_kernel<IO, Q, M, LPR, true><<<parts, kThreads, 0, s>>>(p, tile, nq, mq, mk);
+    if (p.w_q || p.w_k) qk_norm_weights_kernel<<<dim3((p.N + 31) / 32, 2), 256, 0, s>>>(p, nq, parts);
     return cudaGetLastError();
 }
 
 template <int IO>
 cudaError_t norm_io(const QkNormParams &p, bool bwd, cudaStream_t s) {
-    auto fours = [&](const void *x) { return vec4_aligned(x, IO); };
-    bool vec = p.N % 4 == 0 && p.half % 4 == 0 && vec4_strided(p.q, IO, p.qs) && vec4_strided(p.k, IO, p.ks);
-    vec = vec && (bwd ? fours(p.dq_out) && fours(p.dk_out) && fours(p.dq) && fours(p.dk) : fours(p.q_out) && fours(p.k_out));
-    if (!vec) return norm_as<IO, 1, 4, 32>(p, bwd, s);
+    // Runs of 16 bytes, of 8 (16-bit elements), or elements: what every row begins and the rotated part ends at.
+    auto by = [&](int q) {
+        auto aligned = [&](const void *x) { return reinterpret_cast<uintptr_t>(x) % (q * (IO == IO_F32 ? 4 : 2)) == 0; };
+        auto strided = [&](const void *x, const long long (&st)[2]) { return aligned(x) && st[0] % q == 0 && st[1] % q == 0; };
+        return p.N % q == 0 && p.half % q == 0 && strided(p.q, p.qs) && strided(p.k, p.ks) &&
+               (bwd ? aligned(p.dq_out) && aligned(p.dk_out) && aligned(p.dq) && aligned(p.dk) : aligned(p.q_out) && aligned(p.k_out));
+    };
+    if (IO != IO_F32 && by(8)) {
+        constexpr int Q = IO == IO_F32 ? 4 : 8;
+        if (p.N <= 64) return norm_as<IO, Q, 1, 32 / Q>(p, bwd, s);
+        if (p.N <= 128) return norm_as<IO, Q, 1, 64 / Q>(p, bwd, s);
+        return norm_as<IO, Q, 1, 128 / Q>(p, bwd, s);
+    }
+    if (!by(4)) return norm_as<IO, 1, 4, 32>(p, bwd, s);
     if (p.N <= 64) return norm_as<IO, 4, 1, 8>(p, bwd, s);
     if (p.N <= 128) return norm_as<IO, 4, 1, 16>(p, bwd, s);
     return norm_as<IO, 4, 1, 32>(p, bwd, s);
@@ -318,9 +363,8 @@ cudaError_t norm(const QkNormParams &p, int io, bool bwd, cudaStream_t s) {
 }  // namespace
 
 int qk_norm_parts(const QkNormParams &p) {
-    const int tile = tile_of(p);
-    const long long tiles = ((long long)p.B * p.L + tile - 1) / tile, most = 4LL * scan_sm_count();
-    return (int)(tiles < most ? tiles : most);
+    const long long tiles = ((long long)p.B * p.L + tile_of(p) - 1) / tile_of(p), most = scan_sm_count();
+    return (int)(2 * (tiles < most ? tiles : most));
 }
 cudaError_t launch_qk_norm(const QkNormParams &p, int io, cudaStream_t s) { return norm(p, io, false, s); }
 cudaError_t launch_qk_norm_bwd(const QkNormParams &p, int io, cudaStream_t s) { return norm(p, io, true, s); }

@@ -18,7 +18,7 @@ struct QkNormParams {
     const void *dq_out, *dk_out;
     void *dq, *dk;
     float *dw_q, *dw_k;
-    float *part;  // [qk_norm_parts, 2, N]
+    float *part;  // [qk_norm_parts, N]
 };
 int qk_norm_parts(const QkNormParams &p);
 cudaError_t launch_qk_norm(const QkNormParams &p, int io, cudaStream_t s);
