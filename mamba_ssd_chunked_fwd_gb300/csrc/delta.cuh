@@ -56,9 +56,8 @@ struct DeltaStepParams {
 cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);          // y, final_state
 size_t delta_op_bytes(bool pure);
 cudaError_t launch_delta_prep(const DeltaParams &p, int io, bool pure, cudaStream_t s);   // a chunk's operands for the next three
-cudaError_t launch_delta_tc_states(const DeltaParams &p, int io, cudaStream_t s);         // as launch_delta_states
 cudaError_t launch_delta_grad_tc(const DeltaParams &p, int io, cudaStream_t s);           // as launch_delta_grad
-cudaError_t launch_delta_tc_adjoint(const DeltaParams &p, int io, cudaStream_t s);        // as launch_delta_adjoint
+cudaError_t launch_delta_tc_walks(const DeltaParams &p, int io, cudaStream_t s);          // as launch_delta_states and _adjoint
 void delta_segments(DeltaParams &p);
 bool delta_tc_takes(const DeltaParams &p, int io);
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s);            // the same in chunks

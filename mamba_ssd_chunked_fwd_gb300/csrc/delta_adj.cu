@@ -1,5 +1,6 @@
 // delta_adj.cu -- the adjoint of the delta rule's state, chunk by chunk from the end, on the tensor
-// cores, for 16-bit tensors: the backward counterpart of delta_tc.cu.
+// cores, for 16-bit tensors: the backward counterpart of delta_walk_tc.cuh, with which
+// it shares a launch.
 //
 // With D the adjoint of the state after a chunk, d = scale dy, and T, M and the gates of delta_prep.cu:
 //
@@ -7,14 +8,14 @@
 //     R  = T^T dU                                     (the gradient of v - S' k over beta)
 //     D <- exp(G_end) D + (diag(exp G) d)^T Q - (diag(beta exp G) R)^T K
 //
-// and dv = beta R.  The layout is that of the forward walk: rows of the state in TMEM's lanes, tokens
+// and dv = beta R.  The layout is that of the forward walk (delta_walk_tc.cuh): rows of the state in TMEM's lanes, tokens
 // along its columns, computed operands in two terms; the chain is D K^T -> dU -> R -> D:
 //
 //   16 warps the chain;  4 warps make an operand of d;  1 warp issues the products
 //   3 warps  copy k, q, and dy with a chunk's operands ahead
 //
 // It leaves D after every chunk and R as operands for delta_grad_tc.cu, and writes dv.
-#include "delta_tc.cuh"
+#include "delta_walk_tc.cuh"
 
 namespace ssd {
 
@@ -45,8 +46,7 @@ struct Tm {
 };
 
 template <int IO, int NN>
-__global__ void __launch_bounds__(kThreads, 1)
-delta_adj_kernel(const __grid_constant__ DeltaParams p) {
+__device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
     constexpr bool BF16 = IO == IO_BF16;
     using SM = Smem<NN>;
     using TM = Tm<NN>;
@@ -56,7 +56,7 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     Gates *gates = reinterpret_cast<Gates *>(sm + SM::GATES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tiles = (p.P + 127) / 128, p0 = (blockIdx.x % tiles) * 128, bh = blockIdx.x / tiles, h = bh % p.H, b = bh / p.H;
+    const int tiles = (p.P + 127) / 128, p0 = (block % tiles) * 128, bh = block / tiles, h = bh % p.H, b = bh / p.H;
     const int len = delta_length(p, b), chunks = (len + kC - 1) / kC, grp = h / (p.H / p.G), rows = min(128, p.P - p0);
     const size_t pn = (size_t)p.P * p.N;
 
@@ -140,14 +140,15 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kFullOp + par, (i >> 1) & 1);  // the gates
             wait.on(kD1, par);
             tc::fence_after_sync();
-            float v[16], u[16];
-            tc::tmem_ld16x2(x1, x2, v, u);
+            float v[16];
             {
+                float u[16];
                 uint32_t hi[8], lo[8];
+                tc::tmem_ld16x2(x1, x2, v, u);
+                const float2 s2 = dup(p.scale);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float4 f = *reinterpret_cast<const float4 *>(&gt.out[16 * part + 4 * e]);
-                    const float2 s2 = dup(p.scale);
                     split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e], u[4 * e + 1]), __fmul2_rn(make_float2(v[4 * e], v[4 * e + 1]), make_float2(f.x, f.y))), hi[2 * e], lo[2 * e]);
                     split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e + 2], u[4 * e + 3]), __fmul2_rn(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(f.z, f.w))),
                                  hi[2 * e + 1], lo[2 * e + 1]);
@@ -161,18 +162,14 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kD2, par);
             tc::fence_after_sync();
             tc::tmem_ld16(x3, v);
-            float beta[16];
             {
-                float f[16];
+                uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 b4 = *reinterpret_cast<const float4 *>(&gt.beta[16 * part + e]), n4 = *reinterpret_cast<const float4 *>(&gt.neg_into[16 * part + e]);
-                    beta[e] = b4.x, beta[e + 1] = b4.y, beta[e + 2] = b4.z, beta[e + 3] = b4.w;
-                    f[e] = b4.x * n4.x, f[e + 1] = b4.y * n4.y, f[e + 2] = b4.z * n4.z, f[e + 3] = b4.w * n4.w;
+                    split2<BF16>(__fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(b4.x * n4.x, b4.y * n4.y)), hi[e / 2], lo[e / 2]);
+                    split2<BF16>(__fmul2_rn(make_float2(v[e + 2], v[e + 3]), make_float2(b4.z * n4.z, b4.w * n4.w)), hi[e / 2 + 1], lo[e / 2 + 1]);
                 }
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) split2<BF16>(__fmul2_rn(make_float2(v[2 * e], v[2 * e + 1]), make_float2(f[2 * e], f[2 * e + 1])), hi[e], lo[e]);
                 tc::tmem_st8(x1, hi);
                 tc::tmem_st8(x1 + 8, lo);
             }
@@ -189,7 +186,8 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
                 uint16_t *to = dv + (size_t)t * step;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                    const uint32_t two = exchange_rows<BF16>(beta[e] * v[e] + bad, beta[e + 1] * v[e + 1] + bad, odd);
+                    const float2 beta = *reinterpret_cast<const float2 *>(&gt.beta[16 * part + e]);
+                    const uint32_t two = exchange_rows<BF16>(beta.x * v[e] + bad, beta.y * v[e + 1] + bad, odd);
                     if (ok && t + e + odd < len) *reinterpret_cast<uint32_t *>(to + e * step) = two;
                 }
             }
@@ -236,7 +234,7 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
         if (row < rows)
             for (int t = len; t < p.L; ++t) st_io<IO>(p.dv, ((size_t)b * p.L + t) * step + (size_t)h * p.P + p0 + row, 0.f);
     } else if (warp == kMmaWarp) {
-        // ---- the products, by an elected lane (see delta_tc.cu)
+        // ---- the products, by an elected lane (see delta_walk_tc.cuh)
         const bool go = tc::elect_one();
         constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false), ID_B = tc::idesc_f16(128, kC, BF16, false, true),
                            ID_M = tc::idesc_f16(128, kC, BF16, true, true), ID_DS = tc::idesc_f16(128, NN, BF16, false, true);
@@ -375,20 +373,31 @@ delta_adj_kernel(const __grid_constant__ DeltaParams p) {
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem_slot, TM::COLS);
 }
 
+// Both walks of the gradients in one launch: they need nothing of one another, and few heads leave SMs for both.
 template <int IO, int NN>
-cudaError_t adj_as(const DeltaParams &p, cudaStream_t s) {
-    auto *kernel = delta_adj_kernel<IO, NN>;
-    const cudaError_t e = allow_smem<Smem<NN>::BYTES>(kernel);
+__global__ void __launch_bounds__(kThreads, 1)
+delta_both_kernel(const __grid_constant__ DeltaParams p) {
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half) adjoint<IO, NN>(p, blockIdx.x);  // the longer ones first
+    else delta_walk::walk<IO, NN, delta_walk::STATES>(p, blockIdx.x - half);
+}
+
+template <int IO, int NN>
+cudaError_t both_as(const DeltaParams &p, cudaStream_t s) {
+    auto *kernel = delta_both_kernel<IO, NN>;
+    static_assert(kThreads == delta_walk::kThreads, "one launch");
+    constexpr uint32_t bytes = Smem<NN>::BYTES > delta_walk::Smem<NN>::BYTES ? Smem<NN>::BYTES : delta_walk::Smem<NN>::BYTES;
+    const cudaError_t e = allow_smem<bytes>(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long long)p.B * p.H * ((p.P + 127) / 128)), kThreads, Smem<NN>::BYTES, s>>>(p);
+    kernel<<<(unsigned)(2LL * p.B * p.H * ((p.P + 127) / 128)), kThreads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_delta_tc_adjoint(const DeltaParams &p, int io, cudaStream_t s) {
-    if (io == IO_BF16) return p.N <= 64 ? adj_as<IO_BF16, 64>(p, s) : adj_as<IO_BF16, 128>(p, s);
-    return p.N <= 64 ? adj_as<IO_F16, 64>(p, s) : adj_as<IO_F16, 128>(p, s);
+cudaError_t launch_delta_tc_walks(const DeltaParams &p, int io, cudaStream_t s) {
+    if (io == IO_BF16) return p.N <= 64 ? both_as<IO_BF16, 64>(p, s) : both_as<IO_BF16, 128>(p, s);
+    return p.N <= 64 ? both_as<IO_F16, 64>(p, s) : both_as<IO_F16, 128>(p, s);
 }
 
 }  // namespace ssd

@@ -374,8 +374,7 @@ cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s) {
     cudaError_t e;
     if (p.chunked) {
         if ((e = launch_delta_prep(p, io, true, s)) != cudaSuccess) return e;
-        if ((e = launch_delta_tc_states(p, io, s)) != cudaSuccess) return e;
-        if ((e = launch_delta_tc_adjoint(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_tc_walks(p, io, s)) != cudaSuccess) return e;
         if ((e = launch_delta_grad_tc(p, io, s)) != cudaSuccess) return e;
     } else {
         if ((e = launch_delta_states(p, io, s)) != cudaSuccess) return e;

@@ -279,25 +279,28 @@ qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile, int nq, uint32_
         if (!BWD || which == 0) rows_of<IO, Q, M, LPR, BWD>(p, 0, tok0, nt, table, from[0], magic_q, dw);
         if (!BWD || which == 1) rows_of<IO, Q, M, LPR, BWD>(p, 1, tok0, nt, table, from[1], magic_k, dw);
     }
+    if constexpr (BWD) tc::pdl_launch_dependents();
     if constexpr (BWD) if (which ? p.w_k : p.w_q) store_sums<Q, M, LPR>(p, dw);
 }
 
-// dw_q, dw_k: the CTAs' sums, 8 threads to a column, each over every eighth row.
-__global__ void __launch_bounds__(256)
+// dw_q, dw_k: the CTAs' sums, 32 threads to a column, each over every 32nd row.
+__global__ void __launch_bounds__(1024)
 qk_norm_weights_kernel(const __grid_constant__ QkNormParams p, int nq, int parts) {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x, which = blockIdx.y;
     float *out = which ? p.dw_k : p.dw_q;
+    tc::pdl_wait();
     if (!out) return;
     float v = 0.f;
     if (col < p.N)
-        for (int i = (which ? nq : 0) + y; i < (which ? parts : nq); i += 8) v += p.part[(size_t)i * p.N + col];
+#pragma unroll 4
+        for (int i = (which ? nq : 0) + y; i < (which ? parts : nq); i += 32) v += p.part[(size_t)i * p.N + col];
     s[y][x] = v;
     __syncthreads();
-    if (y != 0 || col >= p.N) return;
+    v = s[x][y];  // a warp to a column
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][x];
-    out[col] = v;
+    for (int m = 1; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (x == 0 && blockIdx.x * 32 + y < p.N) out[blockIdx.x * 32 + y] = v;
 }
 
 // Tokens of a tile: as many as leave every SM two CTAs, and rows that the division by a product serves (65536).
@@ -326,8 +329,9 @@ cudaError_t norm_as(const QkNormParams &p, bool bwd, cudaStream_t s) {
     }
     const int parts = qk_norm_parts(p), nq = parts_of_q(p, parts);
     qk_norm_kernel<IO, Q, M, LPR, true><<<parts, kThreads, 0, s>>>(p, tile, nq, mq, mk);
-    if (p.w_q || p.w_k) qk_norm_weights_kernel<<<dim3((p.N + 31) / 32, 2), 256, 0, s>>>(p, nq, parts);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || (!p.w_q && !p.w_k)) return e;
+    return launch_kernel(true, qk_norm_weights_kernel, dim3((p.N + 31) / 32, 2), dim3(1024), 0, s, p, nq, parts);
 }
 
 template <int IO>
