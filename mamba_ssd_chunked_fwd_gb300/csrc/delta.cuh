@@ -57,13 +57,12 @@ cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s);    
 size_t delta_op_bytes(bool pure);
 cudaError_t launch_delta_prep(const DeltaParams &p, int io, bool pure, cudaStream_t s);   // a chunk's operands for the next three
 cudaError_t launch_delta_grad_tc(const DeltaParams &p, int io, cudaStream_t s);           // as launch_delta_grad
-cudaError_t launch_delta_tc_walks(const DeltaParams &p, int io, cudaStream_t s);          // as launch_delta_states and _adjoint
+cudaError_t launch_delta_tc_walks(const DeltaParams &p, int io, cudaStream_t s);          // as launch_delta_walks
 void delta_segments(DeltaParams &p);
 bool delta_tc_takes(const DeltaParams &p, int io);
 cudaError_t launch_delta_tc(const DeltaParams &p, int io, cudaStream_t s);            // the same in chunks
 cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s);
-cudaError_t launch_delta_states(const DeltaParams &p, int io, cudaStream_t s);        // states, u
-cudaError_t launch_delta_adjoint(const DeltaParams &p, int io, cudaStream_t s);       // adj, dr, dv, dh0
+cudaError_t launch_delta_walks(const DeltaParams &p, int io, cudaStream_t s);        // states, u; adj, dr, dv, dh0
 cudaError_t launch_delta_grad(const DeltaParams &p, int io, cudaStream_t s);          // the other gradients
 cudaError_t launch_delta_step(const DeltaStepParams &p, int io, cudaStream_t s);
 

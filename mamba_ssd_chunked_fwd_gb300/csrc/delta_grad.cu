@@ -377,8 +377,7 @@ cudaError_t launch_delta_bwd(const DeltaParams &p, int io, cudaStream_t s) {
         if ((e = launch_delta_tc_walks(p, io, s)) != cudaSuccess) return e;
         if ((e = launch_delta_grad_tc(p, io, s)) != cudaSuccess) return e;
     } else {
-        if ((e = launch_delta_states(p, io, s)) != cudaSuccess) return e;
-        if ((e = launch_delta_adjoint(p, io, s)) != cudaSuccess) return e;
+        if ((e = launch_delta_walks(p, io, s)) != cudaSuccess) return e;
         if ((e = launch_delta_grad(p, io, s)) != cudaSuccess) return e;
     }
     return p.H > p.G ? launch_delta_heads(p, io, s) : cudaSuccess;

@@ -1,8 +1,9 @@
 // delta_walk.cu -- the gated delta rule token by token in fp32: forward, and the
-// adjoint of the state backwards.  Any N <= 128 and any P.
+// adjoint of the state backwards.  Any N <= 128 and any P: fp32 tensors, and 16-bit ones that
+// delta_tc.cu does not take.
 //
 // The rows of a head's state (one for each of the P values) do not mix: row p
-// needs the keys, the gates and v[p].  So a warp keeps 16 rows in registers, four to
+// needs the keys, the gates and v[p].  So a warp keeps its rows in registers, R to
 // a lane with N / 8 columns each, and walks the tokens with no word to other
 // warps but the tile of 16 tokens that the CTA loads for its four.
 // Forward, with S the state before the token:
@@ -10,32 +11,37 @@
 // so that both sums over the state's columns come from the same S, side by side.
 // Backward, with D the adjoint of the state after the token:
 //     r = D k + d (q . k),  d = scale dy,  D <- a (D + d q^T - beta r k^T),  dv = beta r
+// A tile's tokens behind the row's end have a = 1 and zeros elsewhere, which leaves a state as it is, so that
+// every tile takes the same steps, laid out four at a time.
 //
-// Bound by the latency of a token's sums over eight lanes.
+// Bound by the latency of a token's sums over eight lanes, so few heads get more warps with
+// a row to a lane (R = 1), many heads R = 4.
 #include "delta.cuh"
 
 namespace ssd {
 
 namespace {
 
-constexpr int kTile = 16, kRows = 64, kThreads = 128;
+constexpr int kTile = 16, kThreads = 128;
 
 // A tile of `kTile` tokens as loaded, four elements at a time.
-template <int NP>
+template <int NP, int R>
 struct Staged {
-    Raw4 k[NP / 32], q[NP / 32], v[2];
+    Raw4 k[NP / 32], q[NP / 32], v[(R + 1) / 2];
     float gate;
 };
 
-template <int NP>
+// ROWS = 16 R rows of the state to a CTA.
+template <int NP, int R>
 struct Tile {
-    float k[kTile][NP], q[kTile][NP], v[kTile][kRows], out[kTile][kRows], dv[kTile][kRows];
+    static constexpr int ROWS = 16 * R;
+    float k[kTile][NP], q[kTile][NP], v[kTile][ROWS], out[kTile][ROWS], dv[kTile][ROWS];
     float a[kTile], beta[kTile], kq[kTile];
 };
 
-template <int IO, int NP, bool VEC>
+template <int IO, int NP, int R, bool VEC>
 __device__ __forceinline__ void load_tile(const DeltaParams &p, const void *vals, const long long (&vst)[2], int b, int h, int p0, int t0,
-                                          int len, Staged<NP> &r) {
+                                          int len, Staged<NP, R> &r) {
     const int tid = threadIdx.x, gn = (h / (p.H / p.G)) * p.N;
 #pragma unroll
     for (int i = 0; i < NP / 32; ++i) {
@@ -45,17 +51,17 @@ __device__ __forceinline__ void load_tile(const DeltaParams &p, const void *vals
         r.q[i] = load_raw4<IO, VEC>(p.q, b * p.qs[0] + t * p.qs[1] + gn + n, ok, p.N - n);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = tid + kThreads * i, t = t0 + e / (kRows / 4), c = p0 + (e % (kRows / 4)) * 4;
-        r.v[i] = load_raw4<IO, VEC>(vals, b * vst[0] + t * vst[1] + (long long)h * p.P + c, t < len && c < p.P, p.P - c);
+    for (int i = 0; i < (R + 1) / 2; ++i) {
+        const int e = tid + kThreads * i, t = t0 + e / (4 * R), c = p0 + (e % (4 * R)) * 4;
+        r.v[i] = load_raw4<IO, VEC>(vals, b * vst[0] + t * vst[1] + (long long)h * p.P + c, e < kTile * 4 * R && t < len && c < p.P, p.P - c);
     }
     const int t = t0 + (tid & 15);
     if (tid < 16) r.gate = load_gate<IO>(p.g, b * p.gs[0] + t * p.gs[1] + h, p.g32, t < len);
     else if (tid < 32) r.gate = load_gate<IO>(p.beta, b * p.bs[0] + t * p.bs[1] + h, p.b32, t < len);
 }
 
-template <int IO, int NP, bool VEC>
-__device__ __forceinline__ void put_tile(const Staged<NP> &r, Tile<NP> &s) {
+template <int IO, int NP, int R, bool VEC>
+__device__ __forceinline__ void put_tile(const Staged<NP, R> &r, Tile<NP, R> &s) {
     const int tid = threadIdx.x;
     float f[4];
 #pragma unroll
@@ -67,18 +73,18 @@ __device__ __forceinline__ void put_tile(const Staged<NP> &r, Tile<NP> &s) {
         *reinterpret_cast<float4 *>(&s.q[t][n]) = make_float4(f[0], f[1], f[2], f[3]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (R + 1) / 2; ++i) {
         const int e = tid + kThreads * i;
         unpack4<IO, VEC>(r.v[i], f);
-        *reinterpret_cast<float4 *>(&s.v[e / (kRows / 4)][(e % (kRows / 4)) * 4]) = make_float4(f[0], f[1], f[2], f[3]);
+        if (e < kTile * 4 * R) *reinterpret_cast<float4 *>(&s.v[e / (4 * R)][(e % (4 * R)) * 4]) = make_float4(f[0], f[1], f[2], f[3]);
     }
     if (tid < 16) s.a[tid] = expf(r.gate);
     else if (tid < 32) s.beta[tid - 16] = r.gate;
 }
 
 // k . q of the tile's tokens, eight lanes to each.
-template <int NP>
-__device__ __forceinline__ void dot_tile(Tile<NP> &s) {
+template <int NP, int R>
+__device__ __forceinline__ void dot_tile(Tile<NP, R> &s) {
     const int t = threadIdx.x >> 3, ln = threadIdx.x & 7;
     float v = 0.f;
 #pragma unroll
@@ -98,11 +104,23 @@ __device__ __forceinline__ float sum8(float2 v) {
     return r;
 }
 
-// Rows of a state in registers: lane ln of a group of eight holds columns 32 j + 4 ln + 0..3.
-template <int NP, bool VEC>
-__device__ __forceinline__ void load_state(const float *src, int P, int N, int row0, int ln, float2 (&S)[4][NP / 16]) {
+// A lane's columns of a row with those of k or q, in two sums side by side.
+template <int NP>
+__device__ __forceinline__ float2 dot_row(const float2 (&s)[NP / 16], const float2 (&x)[NP / 16]) {
+    float2 a = __fmul2_rn(s[0], x[0]), b = __fmul2_rn(s[1], x[1]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int m = 2; m < NP / 16; m += 2) {
+        a = __ffma2_rn(s[m], x[m], a);
+        b = __ffma2_rn(s[m + 1], x[m + 1], b);
+    }
+    return __fadd2_rn(a, b);
+}
+
+// Rows of a state in registers: lane ln of a group of eight holds columns 32 j + 4 ln + 0..3.
+template <int NP, int R, bool VEC>
+__device__ __forceinline__ void load_state(const float *src, int P, int N, int row0, int ln, float2 (&S)[R][NP / 16]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int j = 0; j < NP / 32; ++j) {
             const int n = 32 * j + 4 * ln;
@@ -112,10 +130,10 @@ __device__ __forceinline__ void load_state(const float *src, int P, int N, int r
             S[r][2 * j + 1] = make_float2(f[2], f[3]);
         }
 }
-template <int NP, bool VEC>
-__device__ __forceinline__ void store_state(float *dst, int P, int N, int row0, int ln, const float2 (&S)[4][NP / 16]) {
+template <int NP, int R, bool VEC>
+__device__ __forceinline__ void store_state(float *dst, int P, int N, int row0, int ln, const float2 (&S)[R][NP / 16]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int j = 0; j < NP / 32; ++j) {
             const int n = 32 * j + 4 * ln;
@@ -134,55 +152,64 @@ __device__ __forceinline__ void read_row(const float *src, int ln, float2 (&v)[N
     }
 }
 
+// A lane's R values of a token's.
+template <int R>
+__device__ __forceinline__ void read_rows(const float *src, float (&v)[R]) {
+    if (R == 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(src);
+        v[0] = f.x, v[R > 1] = f.y, v[R > 2 ? 2 : 0] = f.z, v[R > 3 ? 3 : 0] = f.w;
+    } else {
+        v[0] = src[0];
+    }
+}
+template <int R>
+__device__ __forceinline__ void write_rows(float *dst, const float (&v)[R]) {
+    if (R == 4) *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[R > 1], v[R > 2 ? 2 : 0], v[R > 3 ? 3 : 0]);
+    else dst[0] = v[0];
+}
+
 // STATES: for the gradients, the state before every chunk and u, in place of y.
-template <int IO, int NP, bool VEC, bool STATES>
-__global__ void __launch_bounds__(kThreads)
-delta_walk_kernel(const __grid_constant__ DeltaParams p) {
-    __shared__ __align__(16) Tile<NP> s;
-    const int tiles = (p.P + kRows - 1) / kRows, p0 = (blockIdx.x % tiles) * kRows;
-    const int bh = blockIdx.x / tiles, h = bh % p.H, b = bh / p.H;
-    const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7, lrow = (tid >> 5) * 16 + (lane >> 3) * 4, row0 = p0 + lrow;
+template <int IO, int NP, int R, bool VEC, bool STATES>
+__device__ __forceinline__ void walk_rows(const DeltaParams &p, int block, Tile<NP, R> &s) {
+    constexpr int kRows = 16 * R;
+    const int tiles = (p.P + kRows - 1) / kRows, p0 = (block % tiles) * kRows;
+    const int bh = block / tiles, h = bh % p.H, b = bh / p.H;
+    const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7, lrow = (tid >> 5) * 4 * R + (lane >> 3) * R, row0 = p0 + lrow;
     const int len = delta_length(p, b);
     const size_t pn = (size_t)p.P * p.N;
-    float2 S[4][NP / 16];
-    load_state<NP, VEC>(p.h0 ? p.h0 + bh * pn : nullptr, p.P, p.N, row0, ln, S);
-    Staged<NP> next;
-    load_tile<IO, NP, VEC>(p, p.v, p.vs, b, h, p0, 0, len, next);
+    float2 S[R][NP / 16];
+    load_state<NP, R, VEC>(p.h0 ? p.h0 + bh * pn : nullptr, p.P, p.N, row0, ln, S);
+    Staged<NP, R> next;
+    load_tile<IO, NP, R, VEC>(p, p.v, p.vs, b, h, p0, 0, len, next);
     for (int t0 = 0; t0 < len; t0 += kTile) {
         __syncthreads();
-        put_tile<IO, NP, VEC>(next, s);
-        load_tile<IO, NP, VEC>(p, p.v, p.vs, b, h, p0, t0 + kTile, len, next);
+        put_tile<IO, NP, R, VEC>(next, s);
+        load_tile<IO, NP, R, VEC>(p, p.v, p.vs, b, h, p0, t0 + kTile, len, next);
         __syncthreads();
         if (STATES) {
             if (t0 % kDeltaChunk == 0)
-                store_state<NP, VEC>(p.states + ((size_t)bh * p.nc + t0 / kDeltaChunk) * pn, p.P, p.N, row0, ln, S);
+                store_state<NP, R, VEC>(p.states + ((size_t)bh * p.nc + t0 / kDeltaChunk) * pn, p.P, p.N, row0, ln, S);
         } else {
-            dot_tile<NP>(s);
+            dot_tile<NP, R>(s);
             __syncthreads();
         }
         const int nt = min(kTile, len - t0);
-        for (int i = 0; i < nt; ++i) {
+#pragma unroll (R == 1 ? 4 : 1)
+        for (int i = 0; i < kTile; ++i) {
             float2 k[NP / 16], q[NP / 16];
             read_row<NP>(s.k[i], ln, k);
             if (!STATES) read_row<NP>(s.q[i], ln, q);
             const float a = s.a[i], beta = s.beta[i];
-            const float4 v4 = *reinterpret_cast<const float4 *>(&s.v[i][lrow]);
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-            float out[4];
+            float v[R], out[R];
+            read_rows<R>(&s.v[i][lrow], v);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float2 sk = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
+            for (int r = 0; r < R; ++r) {
+                const float u = beta * fmaf(-a, sum8(dot_row<NP>(S[r], k)), v[r]);
+                out[r] = STATES ? u : p.scale * fmaf(a, sum8(dot_row<NP>(S[r], q)), u * s.kq[i]);
 #pragma unroll
-                for (int m = 0; m < NP / 16; ++m) {
-                    sk = __ffma2_rn(S[r][m], k[m], sk);
-                    if (!STATES) sq = __ffma2_rn(S[r][m], q[m], sq);
-                }
-                const float u = beta * fmaf(-a, sum8(sk), v[r]);
-                out[r] = STATES ? u : p.scale * fmaf(a, sum8(sq), u * s.kq[i]);
-#pragma unroll
-                for (int m = 0; m < NP / 16; ++m) S[r][m] = __ffma2_rn(dup(a), S[r][m], __fmul2_rn(dup(u), k[m]));
+                for (int m = 0; m < NP / 16; ++m) S[r][m] = __ffma2_rn(dup(u), k[m], __fmul2_rn(dup(a), S[r][m]));
             }
-            if (ln == 0) *reinterpret_cast<float4 *>(&s.out[i][lrow]) = make_float4(out[0], out[1], out[2], out[3]);
+            if (ln == 0) write_rows<R>(&s.out[i][lrow], out);
         }
         __syncthreads();
         for (int e = tid; e < nt * (kRows / 4); e += kThreads) {
@@ -195,7 +222,7 @@ delta_walk_kernel(const __grid_constant__ DeltaParams p) {
         }
     }
     if (STATES) return;
-    if (p.final_state) store_state<NP, VEC>(p.final_state + bh * pn, p.P, p.N, row0, ln, S);
+    if (p.final_state) store_state<NP, R, VEC>(p.final_state + bh * pn, p.P, p.N, row0, ln, S);
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (long long e = tid; e < (long long)(p.L - len) * (kRows / 4); e += kThreads) {
         const long long t = len + e / (kRows / 4);
@@ -204,52 +231,52 @@ delta_walk_kernel(const __grid_constant__ DeltaParams p) {
     }
 }
 
-template <int IO, int NP, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-delta_adjoint_kernel(const __grid_constant__ DeltaParams p) {
-    __shared__ __align__(16) Tile<NP> s;
-    const int tiles = (p.P + kRows - 1) / kRows, p0 = (blockIdx.x % tiles) * kRows;
-    const int bh = blockIdx.x / tiles, h = bh % p.H, b = bh / p.H;
-    const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7, lrow = (tid >> 5) * 16 + (lane >> 3) * 4, row0 = p0 + lrow;
+template <int IO, int NP, int R, bool VEC>
+__device__ __forceinline__ void adjoint_rows(const DeltaParams &p, int block, Tile<NP, R> &s) {
+    constexpr int kRows = 16 * R;
+    const int tiles = (p.P + kRows - 1) / kRows, p0 = (block % tiles) * kRows;
+    const int bh = block / tiles, h = bh % p.H, b = bh / p.H;
+    const int tid = threadIdx.x, lane = tid & 31, ln = lane & 7, lrow = (tid >> 5) * 4 * R + (lane >> 3) * R, row0 = p0 + lrow;
     const int len = delta_length(p, b);
     const size_t pn = (size_t)p.P * p.N;
     const long long dys[2] = {(long long)p.L * p.H * p.P, (long long)p.H * p.P};
-    float2 D[4][NP / 16];
-    load_state<NP, VEC>(p.dfinal ? p.dfinal + bh * pn : nullptr, p.P, p.N, row0, ln, D);
-    Staged<NP> next;
+    float2 D[R][NP / 16];
+    load_state<NP, R, VEC>(p.dfinal ? p.dfinal + bh * pn : nullptr, p.P, p.N, row0, ln, D);
+    Staged<NP, R> next;
     const int last = len > 0 ? (len - 1) / kTile * kTile : -kTile;
-    if (len > 0) load_tile<IO, NP, VEC>(p, p.dy, dys, b, h, p0, last, len, next);
+    if (len > 0) load_tile<IO, NP, R, VEC>(p, p.dy, dys, b, h, p0, last, len, next);
     for (int t0 = last; t0 >= 0; t0 -= kTile) {
         __syncthreads();
-        put_tile<IO, NP, VEC>(next, s);
-        if (t0 > 0) load_tile<IO, NP, VEC>(p, p.dy, dys, b, h, p0, t0 - kTile, len, next);
+        put_tile<IO, NP, R, VEC>(next, s);
+        if (t0 > 0) load_tile<IO, NP, R, VEC>(p, p.dy, dys, b, h, p0, t0 - kTile, len, next);
         __syncthreads();
-        dot_tile<NP>(s);
+        dot_tile<NP, R>(s);
         __syncthreads();
         const int nt = min(kTile, len - t0);
         if ((t0 + kTile) % kDeltaChunk == 0 || t0 + nt == len)
-            store_state<NP, VEC>(p.adj + ((size_t)bh * p.nc + t0 / kDeltaChunk) * pn, p.P, p.N, row0, ln, D);
-        for (int i = nt - 1; i >= 0; --i) {
+            store_state<NP, R, VEC>(p.adj + ((size_t)bh * p.nc + t0 / kDeltaChunk) * pn, p.P, p.N, row0, ln, D);
+#pragma unroll (R == 1 ? 4 : 1)
+        for (int i = kTile - 1; i >= 0; --i) {
             float2 k[NP / 16], q[NP / 16];
             read_row<NP>(s.k[i], ln, k);
             read_row<NP>(s.q[i], ln, q);
             const float a = s.a[i], beta = s.beta[i], kq = s.kq[i];
-            const float4 d4 = *reinterpret_cast<const float4 *>(&s.v[i][lrow]);
-            const float d[4] = {p.scale * d4.x, p.scale * d4.y, p.scale * d4.z, p.scale * d4.w};
-            float out[4];
+            float d[R], out[R], dv[R];
+            read_rows<R>(&s.v[i][lrow], d);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float2 dk = make_float2(0.f, 0.f);
+            for (int r = 0; r < R; ++r) d[r] *= p.scale;
 #pragma unroll
-                for (int m = 0; m < NP / 16; ++m) dk = __ffma2_rn(D[r][m], k[m], dk);
-                out[r] = fmaf(d[r], kq, sum8(dk));
+            for (int r = 0; r < R; ++r) {
+                out[r] = fmaf(d[r], kq, sum8(dot_row<NP>(D[r], k)));
                 const float2 wq = dup(a * d[r]), wk = dup(-a * beta * out[r]);
 #pragma unroll
-                for (int m = 0; m < NP / 16; ++m) D[r][m] = __ffma2_rn(dup(a), D[r][m], __ffma2_rn(wq, q[m], __fmul2_rn(wk, k[m])));
+                for (int m = 0; m < NP / 16; ++m) D[r][m] = __ffma2_rn(wk, k[m], __ffma2_rn(wq, q[m], __fmul2_rn(dup(a), D[r][m])));
             }
+#pragma unroll
+            for (int r = 0; r < R; ++r) dv[r] = beta * out[r];
             if (ln == 0) {
-                *reinterpret_cast<float4 *>(&s.out[i][lrow]) = make_float4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<float4 *>(&s.dv[i][lrow]) = make_float4(beta * out[0], beta * out[1], beta * out[2], beta * out[3]);
+                write_rows<R>(&s.out[i][lrow], out);
+                write_rows<R>(&s.dv[i][lrow], dv);
             }
         }
         __syncthreads();
@@ -262,13 +289,30 @@ delta_adjoint_kernel(const __grid_constant__ DeltaParams p) {
             store4_io<IO, VEC>(p.dv, (((long long)b * p.L + t) * p.H + h) * p.P + p0 + c, nv, v);
         }
     }
-    if (p.dh0) store_state<NP, VEC>(p.dh0 + bh * pn, p.P, p.N, row0, ln, D);
+    if (p.dh0) store_state<NP, R, VEC>(p.dh0 + bh * pn, p.P, p.N, row0, ln, D);
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (long long e = tid; e < (long long)(p.L - len) * (kRows / 4); e += kThreads) {
         const long long t = len + e / (kRows / 4);
         const int c = p0 + (e % (kRows / 4)) * 4;
         if (c < p.P) store4_io<IO, VEC>(p.dv, ((b * (long long)p.L + t) * p.H + h) * p.P + c, min(4, p.P - c), zero);
     }
+}
+
+template <int IO, int NP, int R, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+delta_walk_kernel(const __grid_constant__ DeltaParams p) {
+    __shared__ __align__(16) Tile<NP, R> s;
+    walk_rows<IO, NP, R, VEC, false>(p, blockIdx.x, s);
+}
+
+// The gradients' two walks in one launch: they need nothing of one another, and few heads leave SMs for both.
+template <int IO, int NP, int R, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+delta_both_kernel(const __grid_constant__ DeltaParams p) {
+    __shared__ __align__(16) Tile<NP, R> s;
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half) adjoint_rows<IO, NP, R, VEC>(p, blockIdx.x, s);  // the longer ones first
+    else walk_rows<IO, NP, R, VEC, true>(p, blockIdx.x - half, s);
 }
 
 // ---- one token of each of B sequences
@@ -344,30 +388,37 @@ bool by_fours(const void *p, int io, long long s0, long long s1, int n) {
     return vec4_aligned(p, io) && s0 % 4 == 0 && s1 % 4 == 0 && n % 4 == 0;
 }
 
-template <int IO, int NP, bool VEC>
-cudaError_t walk_as(const DeltaParams &p, int what, cudaStream_t s) {
-    const unsigned grid = (unsigned)(p.B * (long long)p.H * ((p.P + kRows - 1) / kRows));
-    if (what == 0) delta_walk_kernel<IO, NP, VEC, false><<<grid, kThreads, 0, s>>>(p);
-    else if (what == 1) delta_walk_kernel<IO, NP, VEC, true><<<grid, kThreads, 0, s>>>(p);
-    else delta_adjoint_kernel<IO, NP, VEC><<<grid, kThreads, 0, s>>>(p);
+template <int IO, int NP, int R, bool VEC>
+cudaError_t launch_rows(const DeltaParams &p, bool both, cudaStream_t s) {
+    const unsigned grid = (unsigned)(p.B * (long long)p.H * ((p.P + 16 * R - 1) / (16 * R)));
+    if (both) delta_both_kernel<IO, NP, R, VEC><<<2 * grid, kThreads, 0, s>>>(p);
+    else delta_walk_kernel<IO, NP, R, VEC><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
+template <int IO, int NP, bool VEC>
+cudaError_t walk_as(const DeltaParams &p, bool both, cudaStream_t s) {
+    // A row to a lane until CTAs of 16 rows would give an SM more than four: above, the walks wait for issue slots, of which
+    // four rows to a lane need fewer.
+    const bool wide = p.B * (long long)p.H * ((p.P + 15) / 16) > 4LL * scan_sm_count();
+    return wide ? launch_rows<IO, NP, 4, VEC>(p, both, s) : launch_rows<IO, NP, 1, VEC>(p, both, s);
+}
+
 template <int IO>
-cudaError_t walk_io(const DeltaParams &p, int what, cudaStream_t s) {
+cudaError_t walk_io(const DeltaParams &p, bool both, cudaStream_t s) {
     const bool vec = by_fours(p.k, IO, p.ks[0], p.ks[1], p.N) && by_fours(p.q, IO, p.qs[0], p.qs[1], p.N) &&
                      by_fours(p.v, IO, p.vs[0], p.vs[1], p.P) && by_fours(p.h0, IO_F32, 0, 0, 4) && by_fours(p.y, IO, 0, 0, 4) &&
                      by_fours(p.final_state, IO_F32, 0, 0, 4) && by_fours(p.dy, IO, 0, 0, 4) && by_fours(p.dfinal, IO_F32, 0, 0, 4) &&
                      by_fours(p.dv, IO, 0, 0, 4) && by_fours(p.dh0, IO_F32, 0, 0, 4);
-    if (p.N <= 64) return vec ? walk_as<IO, 64, true>(p, what, s) : walk_as<IO, 64, false>(p, what, s);
-    return vec ? walk_as<IO, 128, true>(p, what, s) : walk_as<IO, 128, false>(p, what, s);
+    if (p.N <= 64) return vec ? walk_as<IO, 64, true>(p, both, s) : walk_as<IO, 64, false>(p, both, s);
+    return vec ? walk_as<IO, 128, true>(p, both, s) : walk_as<IO, 128, false>(p, both, s);
 }
 
-cudaError_t walk(const DeltaParams &p, int io, int what, cudaStream_t s) {
+cudaError_t walk(const DeltaParams &p, int io, bool both, cudaStream_t s) {
     switch (io) {
-        case IO_F32: return walk_io<IO_F32>(p, what, s);
-        case IO_F16: return walk_io<IO_F16>(p, what, s);
-        case IO_BF16: return walk_io<IO_BF16>(p, what, s);
+        case IO_F32: return walk_io<IO_F32>(p, both, s);
+        case IO_F16: return walk_io<IO_F16>(p, both, s);
+        case IO_BF16: return walk_io<IO_BF16>(p, both, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -392,9 +443,8 @@ cudaError_t step_io(const DeltaStepParams &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s) { return walk(p, io, 0, s); }
-cudaError_t launch_delta_states(const DeltaParams &p, int io, cudaStream_t s) { return walk(p, io, 1, s); }
-cudaError_t launch_delta_adjoint(const DeltaParams &p, int io, cudaStream_t s) { return walk(p, io, 2, s); }
+cudaError_t launch_delta_walk(const DeltaParams &p, int io, cudaStream_t s) { return walk(p, io, false, s); }
+cudaError_t launch_delta_walks(const DeltaParams &p, int io, cudaStream_t s) { return walk(p, io, true, s); }
 
 cudaError_t launch_delta_step(const DeltaStepParams &p, int io, cudaStream_t s) {
     switch (io) {
