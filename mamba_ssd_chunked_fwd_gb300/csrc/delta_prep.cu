@@ -36,15 +36,17 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4
 
 // A chunk's gates by one warp, two tokens to a lane.  The running sum of g log2(e) is taken in whole
 // numbers of 2^-40, exactly, and handed on as the sum of two floats: differences of far larger sums then keep
-// their precision (floats added in pairs did the same in four times the steps, one after another: 5000 cycles of this
-// kernel's 24000).
+// their precision.  To and from whole numbers in halves of 32 bits: through fp64, or with floats added
+// in pairs, this took 5600 of the kernel's 23000 cycles.
 __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], const float (&beta)[2], int lane) {
-    constexpr double kScale = 1.4426950408889634 * 1099511627776.0;
     long long sum[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         // exp(-200) is 0, and so is every product with it; above, sums have room for 64 tokens
-        sum[m] = __double2ll_rn((double)fminf(fmaxf(graw[m], -200.f), 4000.f) * kScale);
+        const float g = fminf(fmaxf(graw[m], -200.f), 4000.f), hi = g * kLog2e;
+        const float lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
+        const float big = rintf(hi * 16384.f);
+        sum[m] = ((long long)(int)big << 26) + __float2int_rn((hi * 16384.f - big) * 67108864.f + lo * 1099511627776.f);
         gt.beta[2 * lane + m] = beta[m];
     }
     const uint32_t nan0 = __ballot_sync(0xffffffffu, isnan(graw[0])), nan1 = __ballot_sync(0xffffffffu, isnan(graw[1]));
@@ -58,18 +60,24 @@ __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], co
     sum[0] += pair - sum[1];
     sum[1] = pair;
     const long long end = __shfl_sync(0xffffffffu, pair, 31);
+    auto parts = [](long long v) {  // v 2^-40 as two floats
+        const int a = (int)(v >> 26), b = (int)(v & 0x3ffffff);
+        const float fa = (float)a;
+        return make_float2(fa * 6.103515625e-5f, fmaf((float)(a - (int)fa), 6.103515625e-5f, (float)b * 9.094947017729282e-13f));
+    };
     const uint32_t before = (1u << lane) - 1u, upto = before | (1u << lane);
     const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         const int t = 2 * lane + m;
-        const float hi = __ll2float_rn(sum[m]) * 9.094947017729282e-13f, lo = __ll2float_rn(sum[m] - __float2ll_rn(hi * 1099511627776.f)) * 9.094947017729282e-13f;
+        const float2 v = parts(sum[m]), rest = parts(end - sum[m]);
         const bool bad = (nan0 & upto) || (nan1 & (m ? upto : before));
-        const float in = bad ? nan : exp2f(hi + lo);
-        gt.gh[t] = bad ? nan : hi, gt.gl[t] = lo, gt.into[t] = in, gt.neg_into[t] = -in;
-        gt.out[t] = nan0 | nan1 ? nan : exp2f(__ll2float_rn(end - sum[m]) * 9.094947017729282e-13f);
+        const float in = bad ? nan : ex2(v.x + v.y);
+        gt.gh[t] = bad ? nan : v.x, gt.gl[t] = v.y, gt.into[t] = in, gt.neg_into[t] = -in;
+        gt.out[t] = nan0 | nan1 ? nan : ex2(rest.x + rest.y);
     }
-    if (lane == 0) gt.over = nan0 | nan1 ? nan : exp2f(__ll2float_rn(end) * 9.094947017729282e-13f);
+    const float2 all = parts(end);
+    if (lane == 0) gt.over = nan0 | nan1 ? nan : ex2(all.x + all.y);
 }
 
 // 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
@@ -80,8 +88,9 @@ __device__ __forceinline__ void decayed(float (&v)[16], const Gates &gt, int j0,
         const float4 h4 = *reinterpret_cast<const float4 *>(&gt.gh[j]), l4 = *reinterpret_cast<const float4 *>(&gt.gl[j]);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const float2 d = __fadd2_rn(__fadd2_rn(dup(gh), e ? make_float2(-h4.z, -h4.w) : make_float2(-h4.x, -h4.y)),
-                                        __fadd2_rn(dup(gl), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y)));
+            const float2 minus = make_float2(-1.f, -1.f);
+            const float2 d = __fadd2_rn(__ffma2_rn(e ? make_float2(h4.z, h4.w) : make_float2(h4.x, h4.y), minus, dup(gh)),
+                                        __ffma2_rn(e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y), minus, dup(gl)));
             const float2 x = __fmul2_rn(__fmul2_rn(make_float2(ex2_now(d.x), ex2_now(d.y)), dup(factor)), make_float2(v[m + e], v[m + e + 1]));
             v[m + e] = j + e < limit ? x.x : 0.f;
             v[m + e + 1] = j + e + 1 < limit ? x.y : 0.f;
