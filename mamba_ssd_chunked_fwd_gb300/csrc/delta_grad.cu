@@ -36,7 +36,7 @@ struct GradSmem {
         } m;
     } x;
     float gh[kC], gl[kC], beta[kC], into[kC], out[kC];
-    float state_in[kC], key_read[kC], written[kC], row_e[kC], col_e[kC], bdot[kC], prior[kC];
+    float state_in[kC], key_read[kC], written[kC], row_e[kC], bdot[kC], prior[kC], over[2];
     float warp_sum[kThreads / 32];
 };
 
@@ -296,26 +296,30 @@ delta_grad_kernel(const __grid_constant__ DeltaParams p) {
                 }
             }
     }
-    // dbeta, dg: thread t sums for its token
-    if (tid < kC) {
-        float col = 0.f;
-        for (int i = tid + 1; i < kC; ++i) col += s.x.m.e[i * YW + tid];
-        s.col_e[tid] = col;
+    // dbeta, dg: thread t for its token.  Sums over the tokens before, and from this one on: over a warp, then over both
+    float own = 0.f;
+    if (tid < kC)
+#pragma unroll 8
+        for (int i = tid + 1; i < kC; ++i) own += s.x.m.e[i * YW + tid];  // its column of E
+    float w = tid < kC ? s.written[tid] : 0.f, x = tid < kC ? s.state_in[tid] + (s.row_e[tid] - own) : 0.f;
+    const int lane = tid & 31;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float down = __shfl_up_sync(0xffffffffu, w, m), up = __shfl_down_sync(0xffffffffu, x, m);
+        if (lane >= m) w += down;
+        if (lane + m < 32) x += up;
     }
+    if (tid == 31) s.over[0] = w;
+    if (tid == 32) s.over[1] = x;
+    const float before = __shfl_up_sync(0xffffffffu, w, 1);
     __syncthreads();
     if (tid < rows) {
         float total = 0.f;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) total += s.warp_sum[i];
-        total *= s.into[kC - 1];
-        float before = 0.f, after = 0.f, pairs = 0.f;
-        for (int i = 0; i < tid; ++i) before += s.written[i];
-        for (int i = kC - 1; i >= tid; --i) {
-            after += s.state_in[i];
-            pairs += s.row_e[i] - s.col_e[i];
-        }
+        const float g = s.into[kC - 1] * total + ((lane > 0 ? before : 0.f) + (tid >= 32 ? s.over[0] : 0.f)) + (x + (tid < 32 ? s.over[1] : 0.f));
         const long long at = ((long long)b * p.L + t0 + tid) * p.H + h;
-        store_gate<IO>(p.dg, at, p.g32, tid < n ? total + before + after + pairs : 0.f);
+        store_gate<IO>(p.dg, at, p.g32, tid < n ? g : 0.f);
         store_gate<IO>(p.dbeta, at, p.b32, tid < n ? s.bdot[tid] - s.key_read[tid] - s.prior[tid] : 0.f);
     }
 }

@@ -99,7 +99,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 32 * half;
         float *part = reinterpret_cast<float *>(sm + SM::SUMS);  // [5][4 quarters][64]: sums over lanes
         float *once = part + 5 * 4 * kC;                         // [3][64]: a thread's sums of its columns, by halves; r . v
-        float *sds = once + 3 * kC;                              // [8]: shares of <S, D>
+        float *sds = once + 3 * kC;                              // [8]: shares of <S, D>; two sums over 32 tokens
         const bool shared_keys = p.H > p.G;
         int n_unit = 0, stage_count = 0;
 #pragma unroll 1
@@ -246,16 +246,24 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 float total = 0.f;
 #pragma unroll
                 for (int m = 0; m < kMathWarps; ++m) total += sds[m];
-                float before = 0.f, after = 0.f, pairs = 0.f;
-                for (int i = 0; i < tid; ++i) before += lanes(2, i);
-                for (int i = kC - 1; i >= tid; --i) {
-                    after += lanes(0, i);
-                    pairs += tokens2(3, i) - (once[i] + once[kC + i]);
+                // sums over the tokens before, and from this one on: over a warp, then over both
+                float w = lanes(2, tid), x = lanes(0, tid) + (tokens2(3, tid) - (once[tid] + once[kC + tid]));
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const float down = __shfl_up_sync(0xffffffffu, w, m), up = __shfl_down_sync(0xffffffffu, x, m);
+                    if (lane >= m) w += down;
+                    if (lane + m < 32) x += up;
                 }
+                float *over = sds + kMathWarps;
+                if (tid == 31) over[0] = w;
+                if (tid == 32) over[1] = x;
+                tc::named_barrier(2, kC);
+                const float left = __shfl_up_sync(0xffffffffu, w, 1);
+                const float before = (lane > 0 ? left : 0.f) + (tid >= 32 ? over[0] : 0.f), after = x + (tid < 32 ? over[1] : 0.f);
                 if (tid < tokens) {
                     const long long at = ((long long)b * p.L + t0 + tid) * p.H + h;
                     const float bad = wait.dead() ? __int_as_float(0x7fffffff) : 0.f;
-                    store_gate<IO>(p.dg, at, p.g32, tid < n ? gt.over * total + before + after + pairs + bad : 0.f);
+                    store_gate<IO>(p.dg, at, p.g32, tid < n ? gt.over * total + before + after + bad : 0.f);
                     store_gate<IO>(p.dbeta, at, p.b32, tid < n ? dbeta + bad : 0.f);
                 }
             }

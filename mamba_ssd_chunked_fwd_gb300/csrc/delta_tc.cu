@@ -42,12 +42,12 @@ delta_fold_kernel(const __grid_constant__ DeltaParams p) {
     for (int s = 0; s + 1 < p.nseg; ++s) {
         if (s + 2 < p.nseg) copy(s + 1);
         else cp_commit();
-        cp_wait<1>();
-        __syncthreads();
         float *own = p.seg_states + ((size_t)bh * p.nseg + s + 1) * pn + (size_t)(p0 + r0) * N + n;
         float acc[kFoldRows / 2];
 #pragma unroll
         for (int r = 0; r < kFoldRows / 2; ++r) acc[r] = n < N && p0 + r0 + r < p.P ? own[(size_t)r * N] : 0.f;
+        cp_wait<1>();
+        __syncthreads();
         const float *t = trans + (s & 1) * 128 * 128 + n;
 #pragma unroll 2
         for (int m = 0; m < N; m += 4) {
