@@ -272,27 +272,31 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             tc::fence_after_sync();
             const int odd = lane & 1;
             const float bad = wait.dead() ? __int_as_float(0x7fffffff) : 0.f;
+            const long long t = (long long)b * p.L + t0 + 32 * half;
+            const size_t step = (size_t)(shared_keys ? p.H : p.G) * p.N;
 #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
-                float *share = which ? p.dkh : p.dqh;
-                uint16_t *out = static_cast<uint16_t *>(which ? p.dk : p.dq);
+                float *share = (which ? p.dkh : p.dqh) + t * step + (size_t)h * p.N + row;
+                uint16_t *out = static_cast<uint16_t *>(which ? p.dk : p.dq) + (t + odd) * step + (size_t)grp * p.N + row - odd;
 #pragma unroll 1
                 for (int i0 = 0; i0 < 32; i0 += 16) {
                     float v[16];
                     tc::tmem_ld16(tl + (which ? TM::P2 : TM::P1) + i0, v);
-                    const int i = 32 * half + i0;
-                    const long long t = (long long)b * p.L + t0 + i;
+                    const int i = 32 * half + i0, left = row < p.N ? tokens - i : 0;
+                    if (i + 16 > n) {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m) v[m] = i + m < n ? v[m] : 0.f;
+                    }
 #pragma unroll
                     for (int m = 0; m < 16; m += 2) {
                         if (shared_keys) {
-                            if (row < p.N) {
-                                if (i + m < tokens) share[((t + m) * p.H + h) * p.N + row] = i + m < n ? v[m] + bad : 0.f;
-                                if (i + m + 1 < tokens) share[((t + m + 1) * p.H + h) * p.N + row] = i + m + 1 < n ? v[m + 1] + bad : 0.f;
-                            }
+                            if (m < left) share[0] = v[m] + bad;
+                            if (m + 1 < left) share[step] = v[m + 1] + bad;
+                            share += 2 * step;
                         } else {
-                            const uint32_t two = exchange_rows<BF16>(i + m < n ? v[m] + bad : 0.f, i + m + 1 < n ? v[m + 1] + bad : 0.f, odd);
-                            if (row < p.N && i + m + odd < tokens)
-                                *reinterpret_cast<uint32_t *>(out + ((t + m + odd) * p.G + grp) * p.N + row - odd) = two;
+                            const uint32_t two = exchange_rows<BF16>(v[m] + bad, v[m + 1] + bad, odd);
+                            if (m + odd < left) *reinterpret_cast<uint32_t *>(out) = two;
+                            out += 2 * step;
                         }
                     }
                 }

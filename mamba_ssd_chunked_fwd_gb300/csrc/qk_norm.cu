@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHalf = 128;
-constexpr int kTokens = 8;  // most tokens of a tile
+constexpr int kTokens = 16;  // most tokens of a tile (forward 8)
 
 // The position's turns are kept as a fraction of 2^64: position times
 // freq / (2 pi), whole turns dropped by the overflow.  The product loses nothing, however far
@@ -130,7 +130,7 @@ __device__ __forceinline__ float sum_group(float v) {
     return v;
 }
 
-// One tensor's rows of a tile: `heads` of each of nt tokens, RU rows at a time so that their loads overlap.
+// One tensor's rows of a tile: `heads` of each of nt tokens, RU rows in flight so that their loads overlap.
 // `from`: where the tile's tokens begin; `magic`: ceil(2^32 / heads), for r / heads (0: one head).
 template <int IO, int Q, int M, int LPR, bool BWD>
 __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long long tok0, int nt, const float2 *table, const long long *from,
@@ -155,50 +155,45 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
         }
     }
     const int rows = nt * heads;
-    for (int r0 = grp; r0 - grp < rows; r0 += kGroups * RU) {  // the same number of rounds for every lane of a warp
-        Raw4 xa[RU][M], xb[RU][M], da[RU][M], db[RU][M];
-        long long to[RU];
-        int tk[RU];
-        bool ok[RU];
+    Raw4 xa[RU][M], xb[RU][M], da[RU][M], db[RU][M];
+    long long to[RU];
+    int tk[RU];
+    bool ok[RU];
+    auto load = [&](int i, int r) {
+        ok[i] = r < rows;
+        tk[i] = ok[i] ? (magic ? (int)__umulhi((uint32_t)r, magic) : r) : 0;
+        const long long at = from[tk[i]] + (long long)(r - tk[i] * heads) * p.N;
+        to[i] = (tok0 * heads + r) * p.N;
 #pragma unroll
-        for (int i = 0; i < RU; ++i) {
-            const int r = r0 + i * kGroups;
-            ok[i] = r < rows;
-            tk[i] = ok[i] ? (magic ? (int)__umulhi((uint32_t)r, magic) : r) : 0;
-            const long long at = from[tk[i]] + (long long)(r - tk[i] * heads) * p.N;
-            to[i] = (tok0 * heads + r) * p.N;
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                xa[i][m] = load_run<IO, Q>(x, at + un[m].a, ok[i] && oka[m]);
-                xb[i][m] = load_run<IO, Q>(x, at + un[m].b, ok[i] && okb[m]);
-                if (BWD) {
-                    da[i][m] = load_run<IO, Q>(dy, to[i] + un[m].a, ok[i] && oka[m]);
-                    db[i][m] = load_run<IO, Q>(dy, to[i] + un[m].b, ok[i] && okb[m]);
-                }
+        for (int m = 0; m < M; ++m) {
+            xa[i][m] = load_run<IO, Q>(x, at + un[m].a, ok[i] && oka[m]);
+            xb[i][m] = load_run<IO, Q>(x, at + un[m].b, ok[i] && okb[m]);
+            if (BWD) {
+                da[i][m] = load_run<IO, Q>(dy, to[i] + un[m].a, ok[i] && oka[m]);
+                db[i][m] = load_run<IO, Q>(dy, to[i] + un[m].b, ok[i] && okb[m]);
             }
         }
+    };
+    auto work = [&](int i) {
+        float a[M][Q], b[M][Q], sq = 0.f;
 #pragma unroll
-        for (int i = 0; i < RU; ++i) {
-            float a[M][Q], b[M][Q], sq = 0.f;
+        for (int m = 0; m < M; ++m) {
+            unpack_run<IO, Q>(xa[i][m], a[m]);
+            unpack_run<IO, Q>(xb[i][m], b[m]);
+#pragma unroll
+            for (int j = 0; j < Q; ++j) sq = fmaf(a[m][j], a[m][j], fmaf(b[m][j], b[m][j], sq));
+        }
+        const float inv = rsqrtf(fmaf(sum_group<LPR>(sq), div, p.eps));
+        if constexpr (!BWD) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                unpack_run<IO, Q>(xa[i][m], a[m]);
-                unpack_run<IO, Q>(xb[i][m], b[m]);
 #pragma unroll
-                for (int j = 0; j < Q; ++j) sq = fmaf(a[m][j], a[m][j], fmaf(b[m][j], b[m][j], sq));
+                for (int j = 0; j < Q; ++j) a[m][j] *= inv * wa[m][j], b[m][j] *= inv * wb[m][j];
+                if (un[m].rot) turn_unit<Q>(a[m], b[m], table + tk[i] * p.half + un[m].f, p.interleaved, 1.f);
+                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, a[m]);
+                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, b[m]);
             }
-            const float inv = rsqrtf(fmaf(sum_group<LPR>(sq), div, p.eps));
-            if (!BWD) {
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-#pragma unroll
-                    for (int j = 0; j < Q; ++j) a[m][j] *= inv * wa[m][j], b[m][j] *= inv * wb[m][j];
-                    if (un[m].rot) turn_unit<Q>(a[m], b[m], table + tk[i] * p.half + un[m].f, p.interleaved, 1.f);
-                    if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, a[m]);
-                    if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, b[m]);
-                }
-                continue;
-            }
+        } else {
             float ga[M][Q], gb[M][Q], dot = 0.f;
 #pragma unroll
             for (int m = 0; m < M; ++m) {
@@ -226,6 +221,23 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
                 if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, ga[m]);
                 if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, gb[m]);
             }
+        }
+    };
+    // r0 - grp < rows: the same number of rounds for every lane of a warp
+    if constexpr (BWD && RU == 2) {  // a row's loads run while the one before is worked on
+        load(0, grp);
+        for (int r0 = grp; r0 - grp < rows; r0 += 2 * kGroups) {
+            load(1, r0 + kGroups);
+            work(0);
+            load(0, r0 + 2 * kGroups);
+            work(1);
+        }
+    } else {
+        for (int r0 = grp; r0 - grp < rows; r0 += kGroups * RU) {
+#pragma unroll
+            for (int i = 0; i < RU; ++i) load(i, r0 + i * kGroups);
+#pragma unroll
+            for (int i = 0; i < RU; ++i) work(i);
         }
     }
 }
@@ -304,11 +316,11 @@ qk_norm_weights_kernel(const __grid_constant__ QkNormParams p, int nq, int parts
 }
 
 // Tokens of a tile: as many as leave every SM two CTAs, and rows that the division by a product serves (65536).
-int tile_of(const QkNormParams &p) {
+int tile_of(const QkNormParams &p, bool bwd) {
     if (p.H > 2048 || p.G > 2048) return 1;
     const long long tokens = (long long)p.B * p.L, most = tokens / (2LL * scan_sm_count());
     int t = 1;
-    while (t < kTokens && 2 * t <= most) t *= 2;
+    while (t < (bwd ? kTokens : kTokens / 2) && 2 * t <= most) t *= 2;
     return t;
 }
 
@@ -320,7 +332,7 @@ int parts_of_q(const QkNormParams &p, int parts) {
 
 template <int IO, int Q, int M, int LPR>
 cudaError_t norm_as(const QkNormParams &p, bool bwd, cudaStream_t s) {
-    const int tile = tile_of(p);
+    const int tile = tile_of(p, bwd);
     const uint32_t mq = (uint32_t)((0x100000000ull + p.H - 1) / p.H), mk = (uint32_t)((0x100000000ull + p.G - 1) / p.G);
     if (!bwd) {
         const long long tiles = ((long long)p.B * p.L + tile - 1) / tile;
@@ -367,7 +379,7 @@ cudaError_t norm(const QkNormParams &p, int io, bool bwd, cudaStream_t s) {
 }  // namespace
 
 int qk_norm_parts(const QkNormParams &p) {
-    const long long tiles = ((long long)p.B * p.L + tile_of(p) - 1) / tile_of(p), most = scan_sm_count();
+    const long long tiles = ((long long)p.B * p.L + tile_of(p, true) - 1) / tile_of(p, true), most = scan_sm_count();
     return (int)(2 * (tiles < most ? tiles : most));
 }
 cudaError_t launch_qk_norm(const QkNormParams &p, int io, cudaStream_t s) { return norm(p, io, false, s); }
