@@ -64,61 +64,59 @@ __device__ __forceinline__ Raw4 load_run(const void *base, long long i, bool ok)
     else ld_v2(r.w, at, ok);
     return r;
 }
+template <int IO>
+__device__ __forceinline__ float first_of(uint32_t w) {
+    return IO == IO_F32 ? __uint_as_float(w) : IO == IO_BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((unsigned short)w));
+}
+template <int IO>
+__device__ __forceinline__ float second_of(uint32_t w) {
+    return IO == IO_BF16 ? __uint_as_float(w & 0xffff0000u) : __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+// Two runs as pairs, element j of both side by side: what follows is packed arithmetic, one instruction to a pair.
 template <int IO, int Q>
-__device__ __forceinline__ void unpack_run(const Raw4 &r, float (&v)[Q]) {
-    if (Q == 1) {
-        float f[4];
-        unpack4<IO, false>(r, f);
-        v[0] = f[0];
-    } else if (IO == IO_F32) {
+__device__ __forceinline__ void unpack_runs(const Raw4 &a, const Raw4 &b, float2 (&v)[Q]) {
 #pragma unroll
-        for (int j = 0; j < Q; ++j) v[j] = __uint_as_float(r.w[j & 3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < Q / 2; ++j) {
-            if (IO == IO_BF16) {
-                v[2 * j] = __uint_as_float(r.w[j & 3] << 16), v[2 * j + 1] = __uint_as_float(r.w[j & 3] & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[j & 3]));
-                v[2 * j] = f.x, v[2 * j + 1] = f.y;
-            }
-        }
+    for (int j = 0; j < Q; ++j) {
+        if (IO == IO_F32 || Q == 1) v[j] = make_float2(first_of<IO>(a.w[j & 3]), first_of<IO>(b.w[j & 3]));
+        else if (j % 2 == 0) v[j] = make_float2(first_of<IO>(a.w[(j / 2) & 3]), first_of<IO>(b.w[(j / 2) & 3]));
+        else v[j] = make_float2(second_of<IO>(a.w[(j / 2) & 3]), second_of<IO>(b.w[(j / 2) & 3]));
     }
 }
+// The first (second) of the pairs as a run in memory.
 template <int IO, int Q>
-__device__ __forceinline__ void store_run(void *base, long long i, const float (&v)[Q]) {
+__device__ __forceinline__ void store_run(void *base, long long i, const float2 (&v)[Q], bool second) {
+    auto of = [&](int j) { return second ? v[j % Q].y : v[j % Q].x; };
     if (Q == 1) {
-        st_io<IO>(base, i, v[0]);
+        st_io<IO>(base, i, of(0));
     } else if (IO == IO_F32) {
-        reinterpret_cast<float4 *>(static_cast<float *>(base) + i)[0] = make_float4(v[0], v[Q > 1], v[Q > 2 ? 2 : 0], v[Q > 3 ? 3 : 0]);
+        reinterpret_cast<float4 *>(static_cast<float *>(base) + i)[0] = make_float4(of(0), of(1), of(2), of(3));
     } else {
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack16<IO>(make_float2(v[(2 * j) % Q], v[(2 * j + 1) % Q]));
+        for (int j = 0; j < 4; ++j) w[j] = pack16<IO>(make_float2(of(2 * j), of(2 * j + 1)));
         if (Q == 8) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
         else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = make_uint2(w[0], w[1]);
     }
 }
 
-// The pairs of a unit turned by their angles (sign -1: back).
+// The pairs of a unit turned by their angles (sign -1: back).  Angle j of the unit lies at cs[j step], so that lanes read
+// neighbours.
 template <int Q>
-__device__ __forceinline__ void turn_unit(float (&a)[Q], float (&b)[Q], const float2 *cs, bool interleaved, float sign) {
-    float c[Q], s[Q];
-#pragma unroll
-    for (int j = 0; j < Q; ++j) c[j] = cs[j].x, s[j] = sign * cs[j].y;
-    if (Q == 1 || !interleaved) {
+__device__ __forceinline__ void turn_unit(float2 (&v)[Q], const float2 *cs, int step, bool interleaved, float sign) {
+    if (Q == 1 || !interleaved) {  // the partners are the pair
 #pragma unroll
         for (int j = 0; j < Q; ++j) {
-            const float x = a[j], y = b[j];
-            a[j] = fmaf(x, c[j], -y * s[j]);
-            b[j] = fmaf(y, c[j], x * s[j]);
+            const float2 t = cs[j * step];
+            const float s = sign * t.y;
+            v[j] = __ffma2_rn(make_float2(v[j].y, v[j].x), make_float2(-s, s), __fmul2_rn(v[j], dup(t.x)));
         }
-    } else {
+    } else {  // partners are neighbours of each run
 #pragma unroll
         for (int j = 0; j < Q / 2; ++j) {
-            const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
-            a[2 * j] = fmaf(x, c[j], -y * s[j]), a[2 * j + 1] = fmaf(y, c[j], x * s[j]);
-            b[2 * j] = fmaf(z, c[j + Q / 2], -w * s[j + Q / 2]), b[2 * j + 1] = fmaf(w, c[j + Q / 2], z * s[j + Q / 2]);
+            const float2 t = cs[j * step], u = cs[(j + Q / 2) * step];
+            const float2 c = make_float2(t.x, u.x), s = make_float2(sign * t.y, sign * u.y), x = v[2 * j], y = v[2 * j + 1];
+            v[2 * j] = __ffma2_rn(y, make_float2(-s.x, -s.y), __fmul2_rn(x, c));
+            v[2 * j + 1] = __ffma2_rn(x, s, __fmul2_rn(y, c));
         }
     }
 }
@@ -134,7 +132,7 @@ __device__ __forceinline__ float sum_group(float v) {
 // `from`: where the tile's tokens begin; `magic`: ceil(2^32 / heads), for r / heads (0: one head).
 template <int IO, int Q, int M, int LPR, bool BWD>
 __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long long tok0, int nt, const float2 *table, const long long *from,
-                                        uint32_t magic, float (&dw)[M][2][Q]) {
+                                        uint32_t magic, float2 (&dw)[M][Q]) {
     constexpr int kGroups = kThreads / LPR, RU = M > 1 ? 1 : BWD || Q == 8 ? 2 : 4;
     const int heads = which ? p.G : p.H, ln = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const void *x = which ? p.k : p.q, *dy = which ? p.dk_out : p.dq_out;
@@ -143,15 +141,14 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
     const float div = p.l2 ? 1.f : 1.f / p.N;
     Unit un[M];
     bool oka[M], okb[M];
-    float wa[M][Q], wb[M][Q];
+    float2 wt[M][Q];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         un[m] = unit_of<Q>(ln + LPR * m, p.half, p.interleaved);
         oka[m] = un[m].a < p.N, okb[m] = un[m].b < p.N;
 #pragma unroll
         for (int j = 0; j < Q; ++j) {
-            wa[m][j] = w && oka[m] ? __ldg(w + un[m].a + j) : 1.f;
-            wb[m][j] = w && okb[m] ? __ldg(w + un[m].b + j) : 1.f;
+            wt[m][j] = make_float2(w && oka[m] ? __ldg(w + un[m].a + j) : 1.f, w && okb[m] ? __ldg(w + un[m].b + j) : 1.f);
         }
     }
     const int rows = nt * heads;
@@ -174,52 +171,48 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
             }
         }
     };
+    const int apart = p.half / Q;  // the units that turn
     auto work = [&](int i) {
-        float a[M][Q], b[M][Q], sq = 0.f;
+        float2 v[M][Q], sq = make_float2(0.f, 0.f);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            unpack_run<IO, Q>(xa[i][m], a[m]);
-            unpack_run<IO, Q>(xb[i][m], b[m]);
+            unpack_runs<IO, Q>(xa[i][m], xb[i][m], v[m]);
 #pragma unroll
-            for (int j = 0; j < Q; ++j) sq = fmaf(a[m][j], a[m][j], fmaf(b[m][j], b[m][j], sq));
+            for (int j = 0; j < Q; ++j) sq = __ffma2_rn(v[m][j], v[m][j], sq);
         }
-        const float inv = rsqrtf(fmaf(sum_group<LPR>(sq), div, p.eps));
+        const float inv = rsqrtf(fmaf(sum_group<LPR>(sq.x + sq.y), div, p.eps));
+        const float2 *cs = table + tk[i] * p.half;
         if constexpr (!BWD) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
 #pragma unroll
-                for (int j = 0; j < Q; ++j) a[m][j] *= inv * wa[m][j], b[m][j] *= inv * wb[m][j];
-                if (un[m].rot) turn_unit<Q>(a[m], b[m], table + tk[i] * p.half + un[m].f, p.interleaved, 1.f);
-                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, a[m]);
-                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, b[m]);
+                for (int j = 0; j < Q; ++j) v[m][j] = __fmul2_rn(v[m][j], __fmul2_rn(dup(inv), wt[m][j]));
+                if (un[m].rot) turn_unit<Q>(v[m], cs + un[m].f / Q, apart, p.interleaved, 1.f);
+                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, v[m], false);
+                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, v[m], true);
             }
         } else {
-            float ga[M][Q], gb[M][Q], dot = 0.f;
+            float2 g[M][Q], dot = make_float2(0.f, 0.f);
+            const float2 part = dup(ok[i] ? inv : 0.f);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                unpack_run<IO, Q>(da[i][m], ga[m]);
-                unpack_run<IO, Q>(db[i][m], gb[m]);
-                if (un[m].rot) turn_unit<Q>(ga[m], gb[m], table + tk[i] * p.half + un[m].f, p.interleaved, -1.f);
+                unpack_runs<IO, Q>(da[i][m], db[i][m], g[m]);
+                if (un[m].rot) turn_unit<Q>(g[m], cs + un[m].f / Q, apart, p.interleaved, -1.f);
 #pragma unroll
                 for (int j = 0; j < Q; ++j) {
-                    if (ok[i]) {
-                        dw[m][0][j] = fmaf(ga[m][j], a[m][j] * inv, dw[m][0][j]);
-                        dw[m][1][j] = fmaf(gb[m][j], b[m][j] * inv, dw[m][1][j]);
-                    }
-                    ga[m][j] *= wa[m][j], gb[m][j] *= wb[m][j];
-                    dot = fmaf(ga[m][j], a[m][j], fmaf(gb[m][j], b[m][j], dot));
+                    const float2 x = __fmul2_rn(g[m][j], v[m][j]);
+                    dw[m][j] = __ffma2_rn(x, part, dw[m][j]);
+                    dot = __ffma2_rn(x, wt[m][j], dot);
+                    g[m][j] = __fmul2_rn(g[m][j], wt[m][j]);
                 }
             }
-            const float f = -inv * inv * inv * div * sum_group<LPR>(dot);
+            const float2 f = dup(-inv * inv * inv * div * sum_group<LPR>(dot.x + dot.y));
 #pragma unroll
             for (int m = 0; m < M; ++m) {
 #pragma unroll
-                for (int j = 0; j < Q; ++j) {
-                    ga[m][j] = fmaf(f, a[m][j], inv * ga[m][j]);
-                    gb[m][j] = fmaf(f, b[m][j], inv * gb[m][j]);
-                }
-                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, ga[m]);
-                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, gb[m]);
+                for (int j = 0; j < Q; ++j) g[m][j] = __ffma2_rn(f, v[m][j], __fmul2_rn(dup(inv), g[m][j]));
+                if (ok[i] && oka[m]) store_run<IO, Q>(out, to[i] + un[m].a, g[m], false);
+                if (ok[i] && okb[m]) store_run<IO, Q>(out, to[i] + un[m].b, g[m], true);
             }
         }
     };
@@ -244,7 +237,7 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
 
 // The CTA's sums of dw, the groups one after another.
 template <int Q, int M, int LPR>
-__device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&dw)[M][2][Q]) {
+__device__ __forceinline__ void store_sums(const QkNormParams &p, const float2 (&dw)[M][Q]) {
     __shared__ float sums[2 * kMaxHalf];
     for (int i = threadIdx.x; i < p.N; i += kThreads) sums[i] = 0.f;
     for (int g = 0; g < kThreads / LPR; ++g) {
@@ -255,8 +248,8 @@ __device__ __forceinline__ void store_sums(const QkNormParams &p, const float (&
             const Unit un = unit_of<Q>(threadIdx.x % LPR + LPR * m, p.half, p.interleaved);
 #pragma unroll
             for (int j = 0; j < Q; ++j) {
-                if (un.a < p.N) sums[un.a + j] += dw[m][0][j];
-                if (un.b < p.N) sums[un.b + j] += dw[m][1][j];
+                if (un.a < p.N) sums[un.a + j] += dw[m][j].x;
+                if (un.b < p.N) sums[un.b + j] += dw[m][j].y;
             }
         }
     }
@@ -272,7 +265,11 @@ qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile, int nq, uint32_
     __shared__ unsigned long long turn[kMaxHalf];
     __shared__ long long from[2][kTokens];
     const long long tokens = (long long)p.B * p.L;
-    float dw[M][2][Q] = {};
+    float2 dw[M][Q];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < Q; ++j) dw[m][j] = make_float2(0.f, 0.f);
     for (int i = threadIdx.x; i < p.half; i += kThreads) turn[i] = turn_of(__ldg(p.freqs + i));
     const int which = BWD && (int)blockIdx.x >= nq, first = blockIdx.x - which * nq, step = BWD ? (which ? gridDim.x - nq : nq) : gridDim.x;
     for (long long tok0 = (long long)first * tile; tok0 < tokens; tok0 += (long long)step * tile) {
@@ -285,7 +282,8 @@ qk_norm_kernel(const __grid_constant__ QkNormParams p, int tile, int nq, uint32_
         for (int e = threadIdx.x; e < nt * p.half; e += kThreads) {
             const int t = e / p.half;
             const long long tok = tok0 + t;
-            table[e] = cos_sin(turn[e - t * p.half], p.positions ? __ldg(p.positions + tok) : (int)(tok % p.L));
+            const int f = e - t * p.half;  // angle f % Q of unit f / Q
+            table[t * p.half + (f % Q) * (p.half / Q) + f / Q] = cos_sin(turn[f], p.positions ? __ldg(p.positions + tok) : (int)(tok % p.L));
         }
         __syncthreads();
         if (!BWD || which == 0) rows_of<IO, Q, M, LPR, BWD>(p, 0, tok0, nt, table, from[0], magic_q, dw);
