@@ -42,8 +42,8 @@ __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], co
     long long sum[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        // exp(-200) is 0, and so is every product with it; above, sums have room for 64 tokens
-        const float g = fminf(fmaxf(graw[m], -200.f), 4000.f), hi = g * kLog2e;
+        // exp(-200) is 0, and so is every product with it, and exp(1400) infinite; sums of 64 tokens stay below 2^17
+        const float g = fminf(fmaxf(graw[m], -200.f), 1400.f), hi = g * kLog2e;
         const float lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
         const float big = rintf(hi * 16384.f);
         sum[m] = ((long long)(int)big << 26) + __float2int_rn((hi * 16384.f - big) * 67108864.f + lo * 1099511627776.f);
