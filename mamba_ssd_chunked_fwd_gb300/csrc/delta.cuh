@@ -27,7 +27,7 @@ struct DeltaParams {
     bool chunked;  // by the kernels of delta_tc.cu
     float *seg_states;  // [B,H,nseg,P,N] state entering a segment (slot 0 unused)
     unsigned char *ops;  // [B,H,nc] a chunk's operands (delta_tc.cuh)
-    float *seg_trans;   // [B,H,nseg-1,N,N] a segment's transition: the state after it is S trans + (its own)
+    float *seg_trans;   // [B,H,nseg-1,N,N] a segment's transition: the state after it is S trans + (its own); slot 0 unused
     // backward
     const void *dy;
     const float *dfinal;

@@ -16,7 +16,8 @@
 // A CTA takes one chunk of one head after another; while its warps finish one, the next one's tiles are copied:
 //
 //   8 warps  Y, Z, the sums over N and the stores: thread = lane, half of the tokens
-//   1 warp   issues the products;  2 warps copy (k and q; S, D, U, R, dy and v by 32 of the P rows)
+//   1 warp   issues the products;  3 warps copy (k and q; S, D, U, R, dy and v by 32 of the P rows, a warp to
+//            a stage: with one for both, a stage's copies began when the other's had landed)
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -24,8 +25,8 @@ namespace ssd {
 namespace {
 
 constexpr int kMathWarps = 8, kMmaWarp = kMathWarps, kCopyWarp = kMmaWarp + 1;
-constexpr int kThreads = (kCopyWarp + 2) * 32;
 constexpr int kStages = 2, kRowsP = 32;  // rows of P in a stage
+constexpr int kThreads = (kCopyWarp + 1 + kStages) * 32;
 
 template <int NN>
 struct Smem {
@@ -421,7 +422,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
         }
     } else {
         // ---- 32 rows of P at a time: S, D, U and R as they lie, dy and v (lane = token of eight, 16-byte piece of the 32 rows)
-        const int r = lane & 7, piece = lane >> 3;
+        const int r = lane & 7, piece = lane >> 3, at = warp - kCopyWarp - 1;
         int stage_count = 0;
 #pragma unroll 1
         for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -432,7 +433,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             const char *v = static_cast<const char *>(p.v) + 2 * (b * p.vs[0] + (c * kC + r) * p.vs[1] + (long long)h * p.P + 8 * piece);
 #pragma unroll 1
             for (int s = 0; s < steps; ++s, ++stage_count) {
-                const int at = stage_count % kStages;
+                if (stage_count % kStages != at) continue;
                 const uint32_t st = sbase + at * SM::STAGE, bar = bars + 8 * (kFull + at);
                 wait.on(kEmpty + at, ((stage_count / kStages) & 1) ^ 1);
                 if (lane == 0) {

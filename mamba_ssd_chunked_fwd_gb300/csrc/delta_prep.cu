@@ -345,7 +345,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         bulk_store(dst + kOpGates, sbase + SM::GATES, (uint32_t)sizeof(Gates));
         if (PURE) bulk_store(dst + kOpPure, sbase + SM::PURE, 16384);
         tc::bulk_commit();
-        tc::bulk_wait_all();
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // shared memory is read; the grid's end covers the rest
     }
 }
 

@@ -17,8 +17,9 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
     delta_walk::walk<IO, NN, MODE>(p, blockIdx.x);
 }
 
-// The state entering each segment: S_{s+1} = S_s trans_s + own_s, row by row, from the initial state; `own` lies where the
-// result goes.  A CTA takes 16 rows of a head; the next transition is copied while one is multiplied.
+// The state entering each segment from the third on: S_{s+1} = S_s trans_s + own_s, row by row; `own` lies where the
+// result goes.  A CTA takes 16 rows of a head; the next transition is copied while one is multiplied.  A thread has four rows of
+// two columns, so that a column's float2 and a row's float4 from shared memory feed eight multiply-adds each.
 constexpr int kFoldRows = 16, kFoldThreads = 256;
 constexpr int kFoldBytes = 2 * 128 * 128 * 4 + kFoldRows * 132 * 4;
 __global__ void __launch_bounds__(kFoldThreads)
@@ -26,45 +27,43 @@ delta_fold_kernel(const __grid_constant__ DeltaParams p) {
     extern __shared__ __align__(16) float fold_mem[];
     float *trans = fold_mem, *state = fold_mem + 2 * 128 * 128;
     const int tiles = (p.P + kFoldRows - 1) / kFoldRows, bh = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * kFoldRows;
-    const int tid = threadIdx.x, n = tid & 127, r0 = (tid >> 7) * (kFoldRows / 2), N = p.N;
+    const int tid = threadIdx.x, n = 2 * (tid & 63), r0 = (tid >> 6) * 4, N = p.N;
     const size_t pn = (size_t)p.P * N, nn = (size_t)N * N;
     auto copy = [&](int s) {
         const float *src = p.seg_trans + ((size_t)bh * (p.nseg - 1) + s) * nn;
         for (int e = 4 * tid; e < (int)nn; e += 4 * kFoldThreads) cp_async16(trans + (s & 1) * 128 * 128 + e, src + e, 16);
         cp_commit();
     };
-    copy(0);
+    auto entering = [&](int s, int r) { return reinterpret_cast<float2 *>(p.seg_states + ((size_t)bh * p.nseg + s) * pn + (size_t)(p0 + r0 + r) * N + n); };
+    copy(1);
 #pragma unroll
-    for (int r = 0; r < kFoldRows / 2; ++r) {
-        const bool ok = p.h0 && n < N && p0 + r0 + r < p.P;
-        state[(r0 + r) * 132 + n] = ok ? __ldg(p.h0 + bh * pn + (size_t)(p0 + r0 + r) * N + n) : 0.f;
-    }
-    for (int s = 0; s + 1 < p.nseg; ++s) {
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float2 *>(state + (r0 + r) * 132 + n) = n < N && p0 + r0 + r < p.P ? *entering(1, r) : make_float2(0.f, 0.f);
+    for (int s = 1; s + 1 < p.nseg; ++s) {
         if (s + 2 < p.nseg) copy(s + 1);
         else cp_commit();
-        float *own = p.seg_states + ((size_t)bh * p.nseg + s + 1) * pn + (size_t)(p0 + r0) * N + n;
-        float acc[kFoldRows / 2];
+        float2 acc[4];
 #pragma unroll
-        for (int r = 0; r < kFoldRows / 2; ++r) acc[r] = n < N && p0 + r0 + r < p.P ? own[(size_t)r * N] : 0.f;
+        for (int r = 0; r < 4; ++r) acc[r] = n < N && p0 + r0 + r < p.P ? *entering(s + 1, r) : make_float2(0.f, 0.f);
         cp_wait<1>();
         __syncthreads();
         const float *t = trans + (s & 1) * 128 * 128 + n;
-#pragma unroll 2
+#pragma unroll 4
         for (int m = 0; m < N; m += 4) {
-            float f[4];
+            float2 f[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = n < N ? t[(m + j) * N] : 0.f;
+            for (int j = 0; j < 4; ++j) f[j] = n < N ? *reinterpret_cast<const float2 *>(t + (m + j) * N) : make_float2(0.f, 0.f);
 #pragma unroll
-            for (int r = 0; r < kFoldRows / 2; ++r) {
+            for (int r = 0; r < 4; ++r) {
                 const float4 x = *reinterpret_cast<const float4 *>(state + (r0 + r) * 132 + m);
-                acc[r] = fmaf(x.x, f[0], fmaf(x.y, f[1], fmaf(x.z, f[2], fmaf(x.w, f[3], acc[r]))));
+                acc[r] = __ffma2_rn(dup(x.x), f[0], __ffma2_rn(dup(x.y), f[1], __ffma2_rn(dup(x.z), f[2], __ffma2_rn(dup(x.w), f[3], acc[r]))));
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kFoldRows / 2; ++r) {
-            state[(r0 + r) * 132 + n] = acc[r];
-            if (n < N && p0 + r0 + r < p.P) own[(size_t)r * N] = acc[r];
+        for (int r = 0; r < 4; ++r) {
+            *reinterpret_cast<float2 *>(state + (r0 + r) * 132 + n) = acc[r];
+            if (n < N && p0 + r0 + r < p.P) *entering(s + 1, r) = acc[r];
         }
         __syncthreads();
     }
@@ -89,7 +88,9 @@ cudaError_t tc_io(const DeltaParams &p, cudaStream_t s) {
     cudaError_t e = launch_delta_prep(p, IO, false, s);
     if (e == cudaSuccess && p.nseg > 1) {
         e = tc_mode<IO, LOCAL_STATE>(p, s);
-        if (e == cudaSuccess) e = allow_smem<kFoldBytes>(delta_fold_kernel);
+    }
+    if (e == cudaSuccess && p.nseg > 2) {
+        e = allow_smem<kFoldBytes>(delta_fold_kernel);
         if (e != cudaSuccess) return e;
         delta_fold_kernel<<<(unsigned)((long long)p.B * p.H * ((p.P + kFoldRows - 1) / kFoldRows)), kFoldThreads, kFoldBytes, s>>>(p);
         e = cudaGetLastError();
@@ -118,7 +119,7 @@ void delta_segments(DeltaParams &p) {
     auto cost = [&](int m) {
         const int len = (p.nc + m - 1) / m, n = (p.nc + len - 1) / len;
         const double walk = ceil(heads * tiles * n / sms) * 3.3 * len;
-        return n == 1 ? walk : walk + ceil(heads * (tiles + 1) * (n - 1) / sms) * 2.6 * len + 1.5 * n + 10.;
+        return n == 1 ? walk : walk + ceil(heads * ((tiles + 1) * (n - 1) - 1) / sms) * 2.6 * len + 1.5 * n + 10.;
     };
     int best = 1;
     for (int m = 2; m <= 64 && m <= p.nc; ++m)

@@ -60,8 +60,8 @@ struct Walk {
     int b, h, p0, t0, t1, chunks;
 };
 
-// What a walk gives: y and the last state; LOCAL: a segment's own state (from zero, the rows of v) and its transition
-// (from the unit matrix, v = 0); STATES: for the gradients, the state before every chunk and U.
+// What a walk gives: y and the last state; LOCAL: a segment's own state (the rows of v; from zero, the first segment from the
+// initial state) and, but for the first, its transition (from the unit matrix, v = 0); STATES: for the gradients, the state before every chunk and U.
 enum Mode { Y, LOCAL_STATE, STATES };
 template <int IO, int NN, int MODE>
 __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
@@ -84,6 +84,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
     Walk w;
     w.h = at % p.H, w.b = at / p.H;
     const bool unit = LOCAL && tile == ptiles;  // the transition: rows are the state's columns
+    if (unit && seg == 0) return;  // nothing enters it but the initial state
     w.p0 = unit ? 0 : tile * 128;
     const int len = delta_length(p, w.b);
     w.t0 = seg * p.seg_len;
@@ -121,7 +122,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
         {
             const float *src = nullptr;
             if (!LOCAL && seg > 0) src = p.seg_states + ((size_t)bh * p.nseg + seg) * pn + (size_t)w.p0 * p.N;
-            else if (!LOCAL && p.h0) src = p.h0 + bh * pn + (size_t)w.p0 * p.N;
+            else if (seg == 0 && p.h0) src = p.h0 + bh * pn + (size_t)w.p0 * p.N;
 #pragma unroll
             for (int j = 0; j < CW / 4; ++j) {
                 const int n = part * CW + 4 * j;
