@@ -665,7 +665,13 @@ ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream)
  * dense.  An output that overlaps an input or the other output is refused.
  * Every dim > 0, N <= 128, P <= 1024, H % G == 0.  g is meant to be <= 0 (minus
  * infinity empties the state) and keys to be of length about one; neither is checked.
- * States are fp32.  workspace: device, 256-byte aligned, ssd_delta_rule_workspace_size()
+ * States are fp32.  16-bit tensors whose N, P, strides and addresses are whole 16-byte
+ * pieces run in chunks of 64 tokens on the tensor cores, all others token by token in fp32.
+ * In chunks, what is computed enters a product as two 16-bit terms: states are off by about
+ * 4e-6 of themselves; with SSD_F16 states, values and u must stay below 65504; and a NaN or an
+ * infinity in a live token may reach the outputs of its whole chunk.  Every wait in these
+ * kernels is bounded; one that gives up leaves NaN in what its part still writes.
+ * workspace: device, 256-byte aligned, ssd_delta_rule_workspace_size()
  * bytes (may be 0; then NULL is accepted).  Enqueue only.
  */
 typedef struct {

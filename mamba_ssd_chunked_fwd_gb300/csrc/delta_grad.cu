@@ -15,6 +15,8 @@
 // dg is the sum over every decay that contains g_t.  It is taken from these pieces,
 // not from q . dq and k . dk: those hold terms without a decay, which cancel, and with
 // strong decays little more than their rounding is left.
+//
+// [2,333] with 6 heads of 64 x 64: 42 us on 72 CTAs, a chunk and head each; issue 39 %, the rest of the SMs idle.
 #include "delta.cuh"
 
 namespace ssd {

@@ -1,5 +1,5 @@
 // delta_prep.cu -- per chunk of 64 tokens and head, what the chunked delta rule's walks
-// (delta_tc.cu) read beside k, q and v, for 16-bit tensors.  With G the running sum of g in the
+// (delta_walk_tc.cuh) read beside k, q and v, for 16-bit tensors.  With G the running sum of g in the
 // chunk and W_ij = exp(G_i - G_j):
 //
 //     A_ij = beta_i W_ij (k_i . k_j)  (j < i),   T = (I + A)^-1,   M_ij = W_ij (q_i . k_j)  (j <= i)
@@ -14,6 +14,9 @@
 // chunk pulled through the instruction cache, and the walk waited for it (prompts of [4,4096,32,128,128]
 // 278 us with it inside); here chunks are independent, six CTAs share an SM, and the walks of
 // segments and of the gradients read its results again.
+//
+// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 140 us, with T for the gradients 50 us for 2048 of them.  No pipe is
+// above 25 %; bound by latency (barriers, the loads, the blocks of T's first column one after another).
 #include "delta_tc.cuh"
 
 namespace ssd {

@@ -19,7 +19,8 @@ delta_tc_kernel(const __grid_constant__ DeltaParams p) {
 
 // The state entering each segment from the third on: S_{s+1} = S_s trans_s + own_s, row by row; `own` lies where the
 // result goes.  A CTA takes 16 rows of a head; the next transition is copied while one is multiplied.  A thread has four rows of
-// two columns, so that a column's float2 and a row's float4 from shared memory feed eight multiply-adds each.
+// two columns, so that a column's float2 and a row's float4 from shared memory feed eight multiply-adds each: 16 heads of
+// 128 x 128 in 9 segments 29 us (eight rows of one column a thread, and a transition more: 41).
 constexpr int kFoldRows = 16, kFoldThreads = 256;
 constexpr int kFoldBytes = 2 * 128 * 128 * 4 + kFoldRows * 132 * 4;
 __global__ void __launch_bounds__(kFoldThreads)

@@ -15,7 +15,7 @@
 // every tile takes the same steps, laid out four at a time.
 //
 // Bound by the latency of a token's sums over eight lanes, so few heads get more warps with
-// a row to a lane (R = 1), many heads R = 4.
+// a row to a lane (R = 1), many heads R = 4.  [3,517] with 6 heads of 72 x 100: 98 us, 0.19 us a token (R = 4: 180).
 #include "delta.cuh"
 
 namespace ssd {
@@ -317,7 +317,8 @@ delta_both_kernel(const __grid_constant__ DeltaParams p) {
 
 // ---- one token of each of B sequences
 
-// The same layout, R rows to a lane.  Bound by the state's bytes, read and written once.
+// The same layout, R rows to a lane.  Bound by the state's bytes, read and written once: 256 sequences of 32 heads of 128 x 128
+// 157 us, 6.9 TB/s (101 % of a plain copy's rate); one sequence of 16 heads 5.6 us, the launch.
 template <int IO, int NP, int R, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 delta_step_kernel(const __grid_constant__ DeltaStepParams p) {

@@ -78,7 +78,9 @@ def delta_rule(q, k, v, g, beta, *, scale=None, initial_states=None, lengths=Non
     <= 0) and beta [B,L,H] each have it too or are fp32; all five may be slices of
     wider tensors along the last dimension.  N <= 128.  ``scale``: 1 / sqrt(N) by default.
     initial_states [B,H,P,N] fp32.  ``lengths`` (int32 [B], on the GPU): tokens per
-    row; y is 0 past them.  ``out``: y's memory, refused where it overlaps an input."""
+    row; y is 0 past them.  ``out``: y's memory, refused where it overlaps an input.
+    16-bit tensors in whole 16-byte pieces (N, P, strides, addresses) run in chunks on the tensor
+    cores, all others token by token; in chunks of fp16 a state must stay below 65504."""
     return _run("delta_rule", "ssd_delta_rule", q, q, k, v, g, beta, scale, initial_states, lengths, return_final_state, out)
 
 
