@@ -138,37 +138,32 @@ __device__ __forceinline__ void times_transposed(float (&acc)[2][4], const Frag 
     }
 }
 
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
+// An 8 x 8 block of a product's result, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
-
 
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
-template <int NN>
-struct Smem {
-    static constexpr uint32_t KQ = 0;                          // k (rows 0-63) and q; once multiplied, T and A take their place
-    static constexpr uint32_t T = 0, A = 16384;
-    static constexpr uint32_t GATES = A + kC * kAW * 4, BYTES = GATES + (uint32_t)sizeof(Gates);  // 35 KB: six CTAs to an SM
-    static constexpr uint32_t PURE = BYTES, PURE_BYTES = PURE + 16384;
-    static_assert(128 * NN * 2 <= GATES, "k and q");
-};
+// 64 columns of k (rows 0-63) and q at a time; once multiplied, A takes their place.
+constexpr uint32_t kKQ = 0, kA = 0, kGates = kA + kC * kAW * 4, kSmem = 26624;  // eight CTAs to an SM, whose TMEM has places for eight
+static_assert(kGates % 16 == 0 && 128 * 64 * 2 <= kGates && kGates + sizeof(Gates) <= kSmem, "shared memory");
 
 // PURE: T itself as well, for the gradients.
 template <int IO, int NN, bool PURE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     constexpr bool BF16 = IO == IO_BF16;
-    using SM = Smem<NN>;
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
     const uint32_t sbase = tc::smem_addr(sm);
-    Gates &gt = *reinterpret_cast<Gates *>(sm + SM::GATES);
-    float *A = reinterpret_cast<float *>(sm + SM::A);
+    Gates &gt = *reinterpret_cast<Gates *>(sm + kGates);
+    float *A = reinterpret_cast<float *>(sm + kA);
     const int tid = threadIdx.x, pw = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x % p.nc, bh = blockIdx.x / p.nc, h = bh % p.H, b = bh / p.H, grp = h / (p.H / p.G);
     const int t0 = c * kC, len = delta_length(p, b);
@@ -191,46 +186,46 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
             braw[m] = load_gate<IO>(p.beta, b * p.bs[0] + t * p.bs[1] + h, p.b32, t < len);
         }
     }
-    {
+    auto load = [&](int half) {
         const int r = lane & 7, piece = lane >> 3;
 #pragma unroll
         for (int rg = pw; rg < 16; rg += 4) {  // row groups of k, then of q
-            const int t = t0 + (rg & 7) * 8 + r;
+            const int t = t0 + (rg & 7) * 8 + r, col = 64 * half + 8 * piece;
             const char *row = static_cast<const char *>(rg < 8 ? p.k : p.q) +
-                              2 * (b * (rg < 8 ? p.ks[0] : p.qs[0]) + t * (rg < 8 ? p.ks[1] : p.qs[1]) + (long long)grp * p.N + 8 * piece);
-            const int live = t < len ? p.N - 8 * piece : 0;
+                              2 * (b * (rg < 8 ? p.ks[0] : p.qs[0]) + t * (rg < 8 ? p.ks[1] : p.qs[1]) + (long long)grp * p.N + col);
+            const int live = t < len ? p.N - col : 0;
 #pragma unroll
-            for (int cg = 0; cg < NN / 32; ++cg)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbase + SM::KQ + ((cg * 4 + piece) * 16 + rg) * 128 + r * 16),
+            for (int cg = 0; cg < 2; ++cg)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbase + kKQ + ((cg * 4 + piece) * 16 + rg) * 128 + r * 16),
                              "l"(live > 32 * cg ? row + 64 * cg : nullptr), "r"(live > 32 * cg ? 16 : 0) : "memory");
         }
         cp_commit();
-    }
+    };
+    load(0);
     if (pw == 0) make_gates(gt, graw, braw, lane);
-    cp_wait<0>();
-    tc::fence_smem_to_async();
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = tmem_slot;
-    if (tid == 0) {
-        constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false);
-        uint64_t d = tc::desc(sbase + SM::KQ, 2048, 128);
-#pragma unroll 1
-        for (int k = 0; k < NN / 16; ++k, d += 256) tc::mma_f16(tmem, d, d, ID, k > 0);
-        tc::commit(tc::smem_addr(&bar_mem));
-    }
-    __syncwarp();
     Waits wait{tc::smem_addr(&bar_mem)};
-    wait.on(0, 0);
-    tc::fence_after_sync();
-    unsigned char *dst = p.ops + (size_t)blockIdx.x * op_bytes(PURE);
-    // what the blocks above the diagonal of T stay
-#pragma unroll
-    for (int e = 0; e < 1024 / kThreads; ++e) {
-        tcop::st_shared_v4(sbase + SM::T + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
-        if (PURE) tcop::st_shared_v4(sbase + SM::PURE + 16 * (tid + kThreads * e), 0u, 0u, 0u, 0u);
+    uint32_t tmem = 0;
+#pragma unroll 1
+    for (int half = 0; half < NN / 64; ++half) {
+        if (half > 0) load(half);
+        cp_wait<0>();
+        tc::fence_smem_to_async();
+        tc::fence_before_sync();
+        __syncthreads();
+        tc::fence_after_sync();
+        tmem = tmem_slot;
+        if (tid == 0) {
+            constexpr uint32_t ID = tc::idesc_f16(128, kC, BF16, false, false);
+            uint64_t d = tc::desc(sbase + kKQ, 2048, 128);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k, d += 256) tc::mma_f16(tmem, d, d, ID, half + k > 0);
+            tc::commit(tc::smem_addr(&bar_mem));
+        }
+        __syncwarp();
+        wait.on(0, half);
+        tc::fence_after_sync();
     }
+    unsigned char *dst = p.ops + (size_t)blockIdx.x * op_bytes(PURE);
     {
         const uint32_t tl = tmem + (static_cast<uint32_t>(pw * 32) << 16);
         const int i = tid & 63, last = i | 31;  // of the warp's rows
@@ -294,7 +289,11 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     {
         const int g = lane >> 2, t = lane & 3;
         const float b0 = gt.beta[16 * pw + g], b1 = gt.beta[16 * pw + g + 8];
-        const uint32_t to = sbase + SM::T + ((2 * pw + ((lane >> 3) & 1)) * 8 + (lane >> 4)) * 128 + (lane & 7) * 16;
+        // of a 16 x 16 block of T four blocks of 8 x 8, one after another along its columns, 128 bytes a warp
+        auto put = [&](uint32_t op, int bi, const uint32_t(&v)[4]) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + op + ((2 * pw + (m & 1)) * 8 + (m >> 1) + 2 * bi) * 128 + 4 * lane) = transposed(v[m]);
+        };
         auto store = [&](const float(&acc)[2][4], int bi) {  // T diag(beta) in two terms
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -302,16 +301,22 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
                 const float b = m & 1 ? b1 : b0;
                 split2<BF16>(make_float2(b * acc[m >> 1][2 * (m & 1)], b * acc[m >> 1][2 * (m & 1) + 1]), hi[m], lo[m]);
             }
-            stmatrix_x4_trans(to + bi * 256, hi);
-            stmatrix_x4_trans(to + bi * 256 + kOpTerm, lo);
+            put(kOpT, bi, hi);
+            put(kOpT + kOpTerm, bi, lo);
             if (PURE) {
                 const Frag f = to_frag<BF16>(acc);
-                stmatrix_x4_trans(to + bi * 256 + SM::PURE - SM::T, f.hi);
-                stmatrix_x4_trans(to + bi * 256 + SM::PURE - SM::T + kOpTerm, f.lo);
+                put(kOpPure, bi, f.hi);
+                put(kOpPure + kOpTerm, bi, f.lo);
             }
         };
         // element (c, r) of block (pw, k) of the buffer, above its diagonal, will be T[r][c] of T's block (k, pw)
         float *mine = A + 16 * pw * kAW;
+#pragma unroll 1
+        for (int bi = 0; bi < pw; ++bi) {  // above the diagonal
+            const uint32_t none[4] = {0, 0, 0, 0};
+            put(kOpT, bi, none), put(kOpT + kOpTerm, bi, none);
+            if (PURE) put(kOpPure, bi, none), put(kOpPure + kOpTerm, bi, none);
+        }
         float acc[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -344,9 +349,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     tc::fence_smem_to_async();
     __syncthreads();
     if (tid == 0) {
-        bulk_store(dst + kOpT, sbase + SM::T, 16384);
-        bulk_store(dst + kOpGates, sbase + SM::GATES, (uint32_t)sizeof(Gates));
-        if (PURE) bulk_store(dst + kOpPure, sbase + SM::PURE, 16384);
+        bulk_store(dst + kOpGates, sbase + kGates, (uint32_t)sizeof(Gates));
         tc::bulk_commit();
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // shared memory is read; the grid's end covers the rest
     }
@@ -355,10 +358,9 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
 template <int IO, int NN, bool PURE>
 cudaError_t prep_as(const DeltaParams &p, cudaStream_t s) {
     auto *kernel = delta_prep_kernel<IO, NN, PURE>;
-    constexpr uint32_t bytes = PURE ? Smem<NN>::PURE_BYTES : Smem<NN>::BYTES;
-    const cudaError_t e = allow_smem<bytes>(kernel);
+    const cudaError_t e = allow_smem<kSmem>(kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long long)p.B * p.H * p.nc), kThreads, bytes, s>>>(p);
+    kernel<<<(unsigned)((long long)p.B * p.H * p.nc), kThreads, kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
