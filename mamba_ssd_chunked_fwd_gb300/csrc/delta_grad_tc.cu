@@ -12,7 +12,7 @@
 //     dq^T = scale exp(G_i) P1 + K^T Y
 //     dk^T = -beta_i exp(G_i) P2 + exp(G_end - G_i) P3 - K^T (Z + Z^T) + Q^T Y^T
 //
-// [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 187 us, 2.9 TB/s of operands read.  A chunk's 22000 cycles are products
+// [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 177 us, 3.0 TB/s of operands read.  A chunk's 22000 cycles are products
 // 7000 (both operands from shared memory: 56 cycles each), waits for S and D 3000, Y and Z 3000, sums over N 2600, second
 // products and stores 3500; with 16 warps in place of 8 the same.  TMEM is full, so that two chunks do not overlap.
 //

@@ -12,11 +12,12 @@
 //
 // A kernel of its own, not warps of the walk: there it took a third of the code that every
 // chunk pulled through the instruction cache, and the walk waited for it (prompts of [4,4096,32,128,128]
-// 278 us with it inside); here chunks are independent, six CTAs share an SM, and the walks of
+// 278 us with it inside); here chunks are independent, eight CTAs share an SM, and the walks of
 // segments and of the gradients read its results again.
 //
-// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 140 us, with T for the gradients 50 us for 2048 of them.  No pipe is
-// above 25 %; bound by latency (barriers, the loads, the blocks of T's first column one after another).
+// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 132 us, with T for the gradients 42 us for 2048 of them.  No pipe is
+// above 25 %; bound by latency (barriers, the loads, the blocks of T's first column one after another).  With k and q
+// whole and T in shared memory, six CTAs to an SM: 140 and 50 us.
 #include "delta_tc.cuh"
 
 namespace ssd {
