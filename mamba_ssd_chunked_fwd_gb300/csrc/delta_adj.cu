@@ -371,6 +371,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             if (++at == stages) at = 0, parity ^= 1;
         }
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

@@ -191,12 +191,14 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     tcop::st_shared_v4(to + 24576 + 1024, zl[4], zl[5], zl[6], zl[7]);
                     const float se = sum_columns(kqv, lane), sp = sum_columns(kk, lane);
                     if (!(lane & 1)) part[(3 * 4 + quarter) * kC + i + (lane >> 1)] = se, part[(4 * 4 + quarter) * kC + i + (lane >> 1)] = sp;
+                    __syncwarp();
                     // r . v: the diagonal
                     tc::tmem_ld16(tl + TM::X6 + i0, x4);
                     float rv = 0.f;
 #pragma unroll
                     for (int m = 0; m < 16; ++m) rv = i + m == j ? x4[m] : rv;
                     if (j >= i && j < i + 16) once[2 * kC + j] = rv;
+                    __syncwarp();
                 }
                 once[half * kC + j] = col_e;
                 tc::fence_smem_to_async();
@@ -236,6 +238,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     const int at = i + (lane >> 1);
                     part[quarter * kC + at] = s1, part[(4 + quarter) * kC + at] = s2, part[(8 + quarter) * kC + at] = s3;
                 }
+                __syncwarp();
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
@@ -262,6 +265,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 float *over = sds + kMathWarps;
                 if (tid == 31) over[0] = w;
                 if (tid == 32) over[1] = x;
+                __syncwarp();
                 tc::named_barrier(2, kC);
                 const float left = __shfl_up_sync(0xffffffffu, w, 1);
                 const float before = (lane > 0 ? left : 0.f) + (tid >= 32 ? over[0] : 0.f), after = x + (tid < 32 ? over[1] : 0.f);
@@ -306,6 +310,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     }
                 }
             }
+            __syncwarp();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kEmptyKQ + (n_unit & 1)));
             tc::mbar_arrive(bars + 8 * kDone);
@@ -463,6 +468,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             }
         }
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

@@ -39,6 +39,8 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
 // A thread's waits: each lasts 2000 tries of up to a millisecond; once one has given up, the rest return
 // at once.  Short code: five kinds of warps run side by side, and what they run has to stay in the
 // instruction cache (with unrolled loops and longer waits every second cycle went to fetching).
+// Every lane of a warp calls it, and the warp goes on together: tcgen05.ld and .st and the named barriers want that, and a
+// store by some of the lanes before them leaves the compiler free to run the rest apart.
 struct Waits {
     uint32_t bars;
     uint32_t tries = 2000;
@@ -51,6 +53,7 @@ struct Waits {
                          : "=r"(done) : "r"(bars + 8 * bar), "r"(parity) : "memory");
         tries = done ? tries : 0u;
         asm volatile("" : "+r"(tries));  // or the code after it is laid out twice, for a thread that waits and one that does not
+        __syncwarp();
     }
 };
 

@@ -263,6 +263,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                         if (ok && j + m + odd < n) *reinterpret_cast<uint32_t *>(to) = two;
                     }
                 }
+                __syncwarp();
                 tc::fence_before_sync();
                 tc::mbar_arrive(bars + 8 * (kD4Read + o));
             }
@@ -419,6 +420,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             if (++at == stages) at = 0, parity ^= 1;
         }
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
