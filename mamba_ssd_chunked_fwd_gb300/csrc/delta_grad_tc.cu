@@ -146,6 +146,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                         sd = fmaf(x.x, y.x, fmaf(x.y, y.y, sd));
                     }
                 }
+                tc::fence_smem_to_async();  // or a load still under way reads what the next copy writes
                 tc::mbar_arrive(bars + 8 * (kEmpty + at));
             }
 #pragma unroll
