@@ -16,7 +16,8 @@
 //
 // Bound by what it stores, 112 KB of D, R and dv to a chunk and SM, beside the chain: [4,2048] with 16 heads of 128 x 128, bf16,
 // 193 us with the states' walk on the other SMs.  The stores of D, or of D and R, by the side warps from TMEM in place of
-// the chain's took 7 and 14 us longer.
+// the chain's took 7 and 14 us longer.  In fp16, with the powers of two that D, d and R are held times (the largest of the
+// CTA's rows, D, d and M^T d, by a barrier of the chain's warps; the side warps wait for it), 247 us.
 //
 // It leaves D after every chunk and R as operands for delta_grad_tc.cu, and writes dv.
 #include "delta_walk_tc.cuh"
@@ -41,7 +42,7 @@ struct Smem {
 };
 
 enum Bar { kFullKQ = 0, kEmptyKQ = kFullKQ + kStages, kFullV = kEmptyKQ + kStages, kEmptyV = kFullV + kVStages, kFullOp = kEmptyV + kVStages,
-           kEmptyOp = kFullOp + kOps, kD1 = kEmptyOp + kOps, kD2, kDS, kDFree, kDReady, kS, kR = kS + 2, kU = kR + 4, kBars = kU + 4 };
+           kEmptyOp = kFullOp + kOps, kD1 = kEmptyOp + kOps, kD2, kDS, kDFree, kX2, kUnit, kDReady, kS, kR = kS + 2, kU = kR + 4, kBars = kU + 4 };
 
 // TMEM columns: D's operand, D K^T and then the operands dU and R, M^T d, R, the change of D, d's operand.
 template <int NN>
@@ -57,6 +58,10 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_slot;
+    // fp16: D, d and what follows from them are held times a power of two (delta_tc.cuh)
+    constexpr bool UNITS = !BF16;
+    __shared__ float2 most_mem[UNITS ? kChainWarps : 1];
+    __shared__ float unit_mem[UNITS ? kSlots : 1];
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     Gates *gates = reinterpret_cast<Gates *>(sm + SM::GATES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -69,7 +74,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             for (int i = 0; i < count; ++i) tc::mbar_init(bars + 8 * (bar + i), arrivals);
         };
         init(kFullKQ, kStages, 64), init(kEmptyKQ, kStages, 1), init(kFullV, kVStages, 32), init(kEmptyV, kVStages, 1 + kSideWarps * 32);
-        init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD1, 4, 1), init(kDReady, 1, kSideWarps * 32);
+        init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD1, 6, 1), init(kDReady, 1, kSideWarps * 32);
         init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8);
         tc::mbar_init_fence();
     }
@@ -110,38 +115,83 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                 if (part * CW + 4 * j < p.N)
                     *reinterpret_cast<float4 *>(dst + 4 * j) = make_float4(D[2 * j].x + bad, D[2 * j].y + bad, D[2 * j + 1].x + bad, D[2 * j + 1].y + bad);
         };
+        float down = 1.f;
 #pragma unroll 1
         for (int i = 0;; ++i) {
             const uint32_t par = i & 1;
+            float dmost = 0.f;
+            if constexpr (UNITS) {
+                if (i < chunks) {  // the largest of d, a 32-byte share of the tile to a thread
+                    wait.on(kFullV + i % kVStages, (i / kVStages) & 1);
+                    const uint4 *at = reinterpret_cast<const uint4 *>(sm + SM::DY + (i % kVStages) * SM::DY_BYTES) + 2 * tid;
+                    const uint4 a = at[0], e = at[1];
+                    const uint32_t dw[8] = {a.x, a.y, a.z, a.w, e.x, e.y, e.z, e.w};
+                    __half2 most = __float2half2_rn(0.f);
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) most = larger_of_halves(most, dw[m]);
+                    dmost = fabsf(p.scale) * larger_half(most);
+                }
+            }
             if (i > 0) {
                 wait.on(kDS, par ^ 1);
                 tc::fence_after_sync();
             }
             const float2 over = dup(i > 0 ? gates[(i - 1) % kSlots].over : 1.f);
+            auto send = [&](int j, float up) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split2<BF16>(UNITS ? __fmul2_rn(dup(up), D[8 * j + e]) : D[8 * j + e], hi[e], lo[e]);
+                tc::tmem_st8(tl + TM::S + part * CW + 8 * j, hi);
+                tc::tmem_st8(tl + TM::S + part * CW + CW / 2 + 8 * j, lo);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * (kS + j));
+                store_op(state_op<NN>(p.adj, (size_t)bh * p.nc + chunks - 1 - i, tiles, p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
+            };
 #pragma unroll
             for (int j = 0; j < CW / 16; ++j) {
                 if (i > 0) {
                     float v[16];
                     tc::tmem_ld16(tl + TM::DS + part * CW + 16 * j, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) D[8 * j + e] = __ffma2_rn(over, D[8 * j + e], make_float2(v[2 * e], v[2 * e + 1]));
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 ds = make_float2(v[2 * e], v[2 * e + 1]);
+                        D[8 * j + e] = __ffma2_rn(over, D[8 * j + e], UNITS ? __fmul2_rn(dup(down), ds) : ds);
+                    }
                 }
-                if (i < chunks) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) split2<BF16>(D[8 * j + e], hi[e], lo[e]);
-                    tc::tmem_st8(tl + TM::S + part * CW + 8 * j, hi);
-                    tc::tmem_st8(tl + TM::S + part * CW + CW / 2 + 8 * j, lo);
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(bars + 8 * (kS + j));
-                    store_op(state_op<NN>(p.adj, (size_t)bh * p.nc + chunks - 1 - i, tiles, p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
-                }
+                if (!UNITS && i < chunks) send(j, 1.f);
             }
             if (i >= chunks) break;
             const int c = chunks - 1 - i;
             const Gates &gt = gates[i % kSlots];
             wait.on(kFullOp + par, (i >> 1) & 1);  // the gates
+            float unit = 1.f;
+            if constexpr (UNITS) {
+                // Of D and d; where M^T d and D are far below d (short queries), up to what d leaves room for
+                float v[16], most = 0.f;
+                wait.on(kX2, par);
+                tc::fence_after_sync();
+                tc::tmem_ld16(x2, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(v[e]));
+                most = warp_largest(fmaxf(finite_or_zero(most * fabsf(p.scale) * gt.m_unit), largest(D)));
+                dmost = warp_largest(dmost);
+                if (lane == 0) most_mem[warp] = make_float2(most, dmost);
+                __syncwarp();
+                tc::named_barrier(1, kChainWarps * 32);
+#pragma unroll
+                for (int e = 0; e < kChainWarps; ++e) most = fmaxf(most, most_mem[e].x), dmost = fmaxf(dmost, most_mem[e].y);
+                unit = fmaxf(to_unit(fmaxf(most, dmost)), fminf(to_unit(most), to_unit(dmost) * kUp));
+                down = inverse_power(unit);
+                if (tid == 0) {
+                    unit_mem[i % kSlots] = unit;
+                    p.units[(((size_t)bh * p.nc + c) * tiles + p0 / 128) * 2 + 1] = unit;
+                    tc::mbar_arrive(bars + 8 * kUnit);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < CW / 16; ++j) send(j, unit * kUp);
+            }
             wait.on(kD1, par);
             tc::fence_after_sync();
             float v[16];
@@ -149,10 +199,11 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                 float u[16];
                 uint32_t hi[8], lo[8];
                 tc::tmem_ld16x2(x1, x2, v, u);
-                const float2 s2 = dup(p.scale);
+                const float2 s2 = dup(UNITS ? p.scale * gt.m_unit * unit : p.scale);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float4 f = *reinterpret_cast<const float4 *>(&gt.out[16 * part + 4 * e]);
+                    float4 f = *reinterpret_cast<const float4 *>(&gt.out[16 * part + 4 * e]);
+                    if (UNITS) f.x *= kDown, f.y *= kDown, f.z *= kDown, f.w *= kDown;
                     split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e], u[4 * e + 1]), __fmul2_rn(make_float2(v[4 * e], v[4 * e + 1]), make_float2(f.x, f.y))), hi[2 * e], lo[2 * e]);
                     split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e + 2], u[4 * e + 3]), __fmul2_rn(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(f.z, f.w))),
                                  hi[2 * e + 1], lo[2 * e + 1]);
@@ -191,7 +242,8 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const float2 beta = *reinterpret_cast<const float2 *>(&gt.beta[16 * part + e]);
-                    const uint32_t two = exchange_rows<BF16>(beta.x * v[e] + bad, beta.y * v[e + 1] + bad, odd);
+                    const float2 r = UNITS ? make_float2(down * v[e], down * v[e + 1]) : make_float2(v[e], v[e + 1]);
+                    const uint32_t two = exchange_rows<BF16>(beta.x * r.x + bad, beta.y * r.y + bad, odd);
                     if (ok && t + e + odd < len) *reinterpret_cast<uint32_t *>(to + e * step) = two;
                 }
             }
@@ -207,6 +259,11 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             wait.on(kFullOp + (i & 1), (i >> 1) & 1);
             wait.on(kFullV + i % kVStages, (i / kVStages) & 1);
             wait.on(kDFree, (i & 1) ^ 1);
+            float scale = p.scale;
+            if constexpr (UNITS) {
+                wait.on(kUnit, i & 1);
+                scale *= unit_mem[i % kSlots];
+            }
             tc::fence_after_sync();
             const unsigned char *dy = sm + SM::DY + (i % kVStages) * SM::DY_BYTES + (row >> 3) * 128 + (row & 7) * 2;
 #pragma unroll 1
@@ -221,7 +278,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {  // token t + e: row group (t + e) / 8, its row (t + e) % 8
                     const uint16_t raw = *reinterpret_cast<const uint16_t *>(dy + ((t + e) >> 3) * 2048 + (e & 7) * 16);
-                    f[e] *= p.scale * (BF16 ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw)));
+                    f[e] *= scale * (BF16 ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw)));
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) split2<BF16>(make_float2(f[2 * e], f[2 * e + 1]), hi[e], lo[e]);
@@ -266,6 +323,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                     tc::mma_f16(tmem + TM::X2, vd + k * K2, md + LO + k * 16, ID_M, 1);
                 }
                 tc::commit(bars + 8 * (kEmptyV + i % kVStages));
+                if (UNITS) tc::commit(bars + 8 * kX2);
             }
             wait.on(kFullKQ + i % kStages, (i / kStages) & 1);
 #pragma unroll

@@ -74,7 +74,7 @@ DeltaLayout delta_layout(ssd::DeltaParams &p, int32_t dtype) {
 }
 
 struct DeltaBwdLayout {
-    size_t states, adj, u, dr, dqh, dkh, ops, total;
+    size_t states, adj, u, dr, dqh, dkh, ops, units, total;
 };
 
 DeltaBwdLayout delta_bwd_layout(ssd::DeltaParams &p, int32_t dtype) {
@@ -93,7 +93,8 @@ DeltaBwdLayout delta_bwd_layout(ssd::DeltaParams &p, int32_t dtype) {
     const size_t share = p.H > p.G ? align_up((size_t)p.B * p.L * p.H * p.N * f) : 0;
     l.dkh = l.dqh + share;
     l.ops = l.dkh + share;
-    l.total = l.ops + (p.chunked ? align_up(chunks * ssd::delta_op_bytes(true)) : 0);
+    l.units = l.ops + (p.chunked ? align_up(chunks * ssd::delta_op_bytes(true)) : 0);
+    l.total = l.units + (p.chunked && dtype == SSD_F16 ? align_up(chunks * (P / 128) * 2 * f) : 0);
     return l;
 }
 
@@ -200,6 +201,7 @@ ssd_status ssd_delta_rule_bwd(const ssd_delta_bwd_args *b, void *stream) {
     p.dr = reinterpret_cast<float *>(ws + l.dr);
     p.dqh = reinterpret_cast<float *>(ws + l.dqh);
     p.dkh = reinterpret_cast<float *>(ws + l.dkh);
+    p.units = reinterpret_cast<float *>(ws + l.units);
     cudaError_t e = ssd::launch_delta_bwd(p, b->fwd.dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "delta_rule_bwd");
     return ok();

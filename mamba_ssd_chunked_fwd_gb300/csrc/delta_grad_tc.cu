@@ -14,7 +14,7 @@
 //
 // [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 177 us, 3.0 TB/s of operands read.  A chunk's 22000 cycles are products
 // 7000 (both operands from shared memory: 56 cycles each), waits for S and D 3000, Y and Z 3000, sums over N 2600, second
-// products and stores 3500; with 16 warps in place of 8 the same.  TMEM is full, so that two chunks do not overlap.
+// products and stores 3500; with 16 warps in place of 8 the same.  In fp16, Y and Z made twice, once for their largest, 196 us.  TMEM is full, so that two chunks do not overlap.
 //
 // Y and Z lie in shared memory once: read along j they are an operand, read along i its transpose.
 // A CTA takes one chunk of one head after another; while its warps finish one, the next one's tiles are copied:
@@ -22,6 +22,8 @@
 //   8 warps  Y, Z, the sums over N and the stores: thread = lane, half of the tokens
 //   1 warp   issues the products;  3 warps copy (k and q; S, D, U, R, dy and v by 32 of the P rows, a warp to
 //            a stage: with one for both, a stage's copies began when the other's had landed)
+#include <math.h>
+
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -42,7 +44,7 @@ struct Smem {
     static constexpr uint32_t GATES = YZ + 32768, SUMS = GATES + 2 * (uint32_t)sizeof(Gates), BYTES = SUMS + 4096 + 2048;
 };
 
-enum Bar { kFull = 0, kEmpty = kFull + kStages, kFullKQ = kEmpty + kStages, kEmptyKQ = kFullKQ + 2, kX = kEmptyKQ + 2, kYZ, kIn, kOut, kDone, kBars };
+enum Bar { kFull = 0, kEmpty = kFull + kStages, kFullKQ = kEmpty + kStages, kEmptyKQ = kFullKQ + 2, kX = kEmptyKQ + 2, kYZ, kIn, kOut, kDone, kScaled, kBars = kScaled + kStages };
 
 template <int NN>
 struct Tm {  // columns
@@ -75,6 +77,10 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ptiles = (p.P + 127) / 128, steps = ptiles * 4, units = p.B * p.H * p.nc;
+    // fp16: the operands come times powers of two, one for S and U, one for D and R, of each 128 rows of P (delta_tc.cuh).  Where those of
+    // several differ, what has the larger one is brought down in place
+    constexpr bool UNITS = !BF16;
+    const bool level = UNITS && ptiles > 1;
 
     if (tid == 0) {
         auto init = [&](int bar, int count, uint32_t arrivals) {
@@ -82,6 +88,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
         };
         init(kFull, kStages, 33), init(kEmpty, kStages, 1 + kMathWarps * 32), init(kFullKQ, 2, 33), init(kEmptyKQ, 2, 1 + kMathWarps * 32);
         init(kX, 1, 1), init(kYZ, 1, 128), init(kIn, 1, kMathWarps * 32), init(kOut, 1, 1), init(kDone, 1, kMathWarps * 32);
+        init(kScaled, kStages, kMathWarps * 32);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -104,7 +111,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 32 * half;
         float *part = reinterpret_cast<float *>(sm + SM::SUMS);  // [5][4 quarters][64]: sums over lanes
         float *once = part + 5 * 4 * kC;                         // [3][64]: a thread's sums of its columns, by halves; r . v
-        float *sds = once + 3 * kC;                              // [8]: shares of <S, D>; two sums over 32 tokens
+        float *sds = once + 3 * kC;                              // [8]: shares of <S, D>; two sums over 32 tokens; [8]: the largest of Y and Z
         const bool shared_keys = p.H > p.G;
         int n_unit = 0, stage_count = 0;
 #pragma unroll 1
@@ -127,13 +134,44 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             const uint32_t par = n_unit & 1;
             const unsigned char *kq = sm + SM::KQ + (n_unit & 1) * SM::KQ_BYTES;
             const Gates &gt = *reinterpret_cast<const Gates *>(sm + SM::GATES + (n_unit & 1) * sizeof(Gates));
+            float s_unit = 1.f, d_unit = 1.f;
+            if constexpr (UNITS) {
+                s_unit = d_unit = INFINITY;
+                for (int m = 0; m < ptiles; ++m) {
+                    const float2 two = __ldg(reinterpret_cast<const float2 *>(p.units) + (size_t)unit * ptiles + m);
+                    s_unit = fminf(s_unit, two.x), d_unit = fminf(d_unit, two.y);
+                }
+            }
             // <S, D>, as the tiles pass
             float sd = 0.f;
 #pragma unroll 1
             for (int s = 0; s < steps; ++s, ++stage_count) {
                 const int at = stage_count % kStages;
                 wait.on(kFull + at, (stage_count / kStages) & 1);
-                const unsigned char *st = sm + at * SM::STAGE;
+                unsigned char *st = sm + at * SM::STAGE;
+                if constexpr (UNITS) {
+                    if (level) {
+                        const float2 two = __ldg(reinterpret_cast<const float2 *>(p.units) + (size_t)unit * ptiles + s / 4);
+                        const __half2 fs = __float2half2_rn(s_unit * inverse_power(two.x)), fd = __float2half2_rn(d_unit * inverse_power(two.y));
+                        auto bring = [&](uint32_t from, uint32_t bytes, __half2 f) {
+                            for (uint32_t e = 16 * tid; e < bytes; e += 16 * kMathWarps * 32) {
+                                uint4 v = *reinterpret_cast<const uint4 *>(st + from + e);
+                                uint32_t *x = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) {
+                                    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&x[m]), f);
+                                    x[m] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                                *reinterpret_cast<uint4 *>(st + from + e) = v;
+                            }
+                        };
+                        bring(SM::S, SM::ST, fs), bring(SM::D, SM::ST, fd), bring(SM::U, SM::UT, fs), bring(SM::R, SM::UT, fd);
+                        tc::fence_smem_to_async();
+                        tc::mbar_arrive(bars + 8 * (kScaled + at));
+                        __syncwarp();
+                        tc::named_barrier(1, kMathWarps * 32);  // the rows that another thread brought down
+                    }
+                }
 #pragma unroll 1
                 for (int e = tid; e < kRowsP * NN / 8; e += kMathWarps * 32) {  // 16 bytes: row group, then columns' group and row
                     const uint32_t off = (e / NN) * (2 * NN * 16) + (e % NN) * 16;
@@ -155,6 +193,38 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kFullKQ + (n_unit & 1), (n_unit >> 1) & 1);  // the gates
             wait.on(kX, par);
             tc::fence_after_sync();
+            // what the sums over P carry: of S, U (in units of t_unit), R, D
+            const float of_s = UNITS ? inverse_power(s_unit) * kDown : 1.f, of_u = UNITS ? inverse_power(s_unit) * gt.t_unit : 1.f;
+            const float of_r = UNITS ? inverse_power(d_unit) : 1.f, of_d = UNITS ? of_r * kDown : 1.f;
+            // 16 tokens i of row j of Y and Z, and what dbeta takes off before beta and k . k
+            auto make_yz = [&](int j, int i, float gh, float gl, float(&y)[16], float(&z)[16], float(&wx)[16]) {
+#pragma unroll
+                for (int m = 0; m < 16; ++m) {
+                    const float w = ex2_now((gt.gh[i + m] - gh) + (gt.gl[i + m] - gl));
+                    const float x4 = UNITS ? of_u * y[m] : y[m], x5 = UNITS ? of_u * of_r * z[m] : z[m];
+                    y[m] = i + m >= j ? p.scale * w * x4 : 0.f, wx[m] = i + m > j ? w * x5 : 0.f, z[m] = gt.beta[i + m] * wx[m];
+                }
+            };
+            float up = 1.f;
+            if constexpr (UNITS) {
+                if (quarter < 2) {
+                    float most = 0.f;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32; i0 += 16) {
+                        float y[16], z[16], wx[16];
+                        tc::tmem_ld16x2(tl + TM::X4 + i0, tl + TM::X5 + i0, y, z);
+                        make_yz(row, 32 * half + i0, gt.gh[row], gt.gl[row], y, z, wx);
+#pragma unroll
+                        for (int m = 0; m < 16; ++m) most = fmaxf(most, fmaxf(finite_or_zero(fabsf(y[m])), finite_or_zero(fabsf(z[m]))));
+                    }
+                    most = warp_largest(most);
+                    if (lane == 0) sds[kMathWarps + 2 + warp] = most;
+                }
+                __syncwarp();
+                tc::named_barrier(1, kMathWarps * 32);
+                const float *most = sds + kMathWarps + 2;  // warps 0, 1, 4 and 5
+                up = fminf(to_unit(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[4], most[5]))), 1.152921504606847e18f) * (kUp / 2.f);
+            }
             if (quarter < 2) {  // lanes 0-63: Y and Z, thread = token j, columns = tokens i of this half
                 const int j = row;
                 const float gh = gt.gh[j], gl = gt.gl[j];
@@ -162,24 +232,23 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
 #pragma unroll 1
                 for (int i0 = 0; i0 < 32; i0 += 16) {
                     const int i = 32 * half + i0;
-                    float x4[16], x5[16], kk[16], kqv[16];
+                    float x4[16], x5[16], wx[16], kk[16], kqv[16];
                     tc::tmem_ld16x2(tl + TM::X4 + i0, tl + TM::X5 + i0, x4, x5);
                     tc::tmem_ld16x2(tl + TM::KK + i0, tl + TM::KK + 64 + i0, kk, kqv);
                     uint32_t yh[8], yl[8], zh[8], zl[8];
+                    make_yz(j, i, gh, gl, x4, x5, wx);
 #pragma unroll
                     for (int m = 0; m < 16; ++m) {
-                        const float w = ex2_now((gt.gh[i + m] - gh) + (gt.gl[i + m] - gl));
-                        const float y = i + m >= j ? p.scale * w * x4[m] : 0.f, wx = i + m > j ? w * x5[m] : 0.f, z = gt.beta[i + m] * wx;
-                        const float e = i + m > j ? y * kqv[m] - z * kk[m] : 0.f;
-                        x4[m] = y, x5[m] = z;
-                        kk[m] = wx * kk[m];  // what dbeta takes off
+                        const float e = i + m > j ? x4[m] * kqv[m] - x5[m] * kk[m] : 0.f;
+                        kk[m] = wx[m] * kk[m];  // what dbeta takes off
                         kqv[m] = e;
                         col_e += e;
                     }
 #pragma unroll
                     for (int m = 0; m < 8; ++m) {
-                        split2<BF16>(make_float2(x4[2 * m], x4[2 * m + 1]), yh[m], yl[m]);
-                        split2<BF16>(make_float2(-x5[2 * m], -x5[2 * m + 1]), zh[m], zl[m]);
+                        const float2 y = make_float2(x4[2 * m], x4[2 * m + 1]), z = make_float2(-x5[2 * m], -x5[2 * m + 1]);
+                        split2<BF16>(UNITS ? __fmul2_rn(dup(up), y) : y, yh[m], yl[m]);
+                        split2<BF16>(UNITS ? __fmul2_rn(dup(up), z) : z, zh[m], zl[m]);
                     }
                     const uint32_t to = sbase + SM::YZ + (i >> 3) * 1024 + (j >> 3) * 128 + (j & 7) * 16;
                     tcop::st_shared_v4(to, yh[0], yh[1], yh[2], yh[3]);
@@ -198,7 +267,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     float rv = 0.f;
 #pragma unroll
                     for (int m = 0; m < 16; ++m) rv = i + m == j ? x4[m] : rv;
-                    if (j >= i && j < i + 16) once[2 * kC + j] = rv;
+                    if (j >= i && j < i + 16) once[2 * kC + j] = UNITS ? of_r * rv : rv;
                     __syncwarp();
                 }
                 once[half * kC + j] = col_e;
@@ -226,11 +295,13 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     const float k = BF16 ? __uint_as_float((uint32_t)kraw << 16) : __half2float(__ushort_as_half(kraw));
                     const float q = BF16 ? __uint_as_float((uint32_t)qraw << 16) : __half2float(__ushort_as_half(qraw));
                     const float into = gt.into[i + m], f1 = p.scale * into, f2 = -gt.beta[i + m] * into, f3 = gt.out[i + m];
+                    if (UNITS) p1[m] *= of_s, p2[m] *= of_s * of_r, p3[m] *= of_d * of_u;
                     t1[m] = col_ok ? f1 * q * p1[m] + f2 * k * p2[m] : 0.f;
                     t2[m] = col_ok ? into * k * p2[m] : 0.f;
                     t3[m] = col_ok ? f3 * k * p3[m] : 0.f;
-                    r1[m] = __float_as_uint(f1 * p1[m]);
-                    r2[m] = __float_as_uint(fmaf(f3, p3[m], f2 * p2[m]));
+                    r1[m] = __float_as_uint(UNITS ? up * (f1 * p1[m]) : f1 * p1[m]);
+                    const float dk = fmaf(f3, p3[m], f2 * p2[m]);
+                    r2[m] = __float_as_uint(UNITS ? up * dk : dk);
                 }
                 tc::tmem_st16(tl + TM::P1 + i0, r1);
                 tc::tmem_st16(tl + TM::P2 + i0, r2);
@@ -255,6 +326,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 float total = 0.f;
 #pragma unroll
                 for (int m = 0; m < kMathWarps; ++m) total += sds[m];
+                if (UNITS) total *= of_s * of_d;
                 // sums over the tokens before, and from this one on: over a warp, then over both
                 float w = lanes(2, tid), x = lanes(0, tid) + (tokens2(3, tid) - (once[tid] + once[kC + tid]));
 #pragma unroll
@@ -293,6 +365,10 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                     float v[16];
                     tc::tmem_ld16(tl + (which ? TM::P2 : TM::P1) + i0, v);
                     const int i = 32 * half + i0, left = row < p.N ? tokens - i : 0;
+                    if (UNITS) {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m) v[m] *= inverse_power(up);
+                    }
                     if (i + 16 > n) {
 #pragma unroll
                         for (int m = 0; m < 16; ++m) v[m] = i + m < n ? v[m] : 0.f;
@@ -342,6 +418,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 const int at = stage_count % kStages;
                 const uint32_t st = sbase + at * SM::STAGE;
                 wait.on(kFull + at, (stage_count / kStages) & 1);
+                if (level) wait.on(kScaled + at, (stage_count / kStages) & 1);
                 tc::fence_after_sync();
                 if (go) {
                     const uint64_t sd = tc::desc(st + SM::S, 2 * NN * 16, 128), dd = tc::desc(st + SM::D, 2 * NN * 16, 128);

@@ -81,7 +81,7 @@ __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], co
         gt.out[t] = nan0 | nan1 ? nan : ex2(rest.x + rest.y);
     }
     const float2 all = parts(end);
-    if (lane == 0) gt.over = nan0 | nan1 ? nan : ex2(all.x + all.y);
+    if (lane == 0) gt.over = nan0 | nan1 ? nan : ex2(all.x + all.y), gt.t_unit = gt.m_unit = 1.f;
 }
 
 // 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
@@ -162,6 +162,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
+    __shared__ float m_most[2];  // (fp16) the largest of M, by warps
     const uint32_t sbase = tc::smem_addr(sm);
     Gates &gt = *reinterpret_cast<Gates *>(sm + kGates);
     float *A = reinterpret_cast<float *>(sm + kA);
@@ -203,7 +204,13 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         cp_commit();
     };
     load(0);
-    if (pw == 0) make_gates(gt, graw, braw, lane);
+    if (pw == 0) {
+        make_gates(gt, graw, braw, lane);
+        if constexpr (!BF16) {
+            const float most = warp_largest(fmaxf(finite_or_zero(fabsf(braw[0])), finite_or_zero(fabsf(braw[1]))));
+            if (lane == 0) gt.t_unit = __uint_as_float(min(max(__float_as_uint(most) >> 23, 67u), 187u) << 23);  // 2^-60 .. 2^60
+        }
+    }
     Waits wait{tc::smem_addr(&bar_mem)};
     uint32_t tmem = 0;
 #pragma unroll 1
@@ -232,6 +239,28 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         const int i = tid & 63, last = i | 31;  // of the warp's rows
         const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
         const int limit = pw < 2 ? i : i + 1;
+        float up = 1.f;
+        if constexpr (!BF16) {
+            if (pw >= 2) {  // the largest of M first
+                float most = 0.f;
+#pragma unroll 1
+                for (int j0 = 0; j0 <= last; j0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(tl + j0, v);
+                    decayed(v, gt, j0, gh, gl, 1.f, limit);
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) most = fmaxf(most, finite_or_zero(fabsf(v[m])));
+                }
+                most = warp_largest(most);
+                if (lane == 0) m_most[pw - 2] = most;
+                __syncwarp();
+                tc::named_barrier(1, 64);
+                // never down: what decays that grow push past fp16 ends as infinity, not as zeros beside it
+                up = __uint_as_float((267u - min(max(__float_as_uint(fmaxf(m_most[0], m_most[1])) >> 23, 100u), 140u)) << 23);
+                if (tid == 64) gt.m_unit = inverse_power(up);
+                __syncwarp();
+            }
+        }
 #pragma unroll 1
         for (int j0 = 0; j0 < kC; j0 += 16) {
             float v[16];
@@ -242,7 +271,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
                 continue;
             }
             tc::tmem_ld16(tl + j0, v);
-            decayed(v, gt, j0, gh, gl, factor, limit);
+            decayed(v, gt, j0, gh, gl, BF16 || pw < 2 ? factor : up, limit);
             if (pw < 2) {
 #pragma unroll
                 for (int m = 0; m < 16; m += 4) *reinterpret_cast<float4 *>(A + i * kAW + j0 + m) = make_float4(v[m], v[m + 1], v[m + 2], v[m + 3]);
@@ -289,7 +318,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     // column pw of blocks, transposed: element (c, r) of a block is T[r][c]
     {
         const int g = lane >> 2, t = lane & 3;
-        const float b0 = gt.beta[16 * pw + g], b1 = gt.beta[16 * pw + g + 8];
+        const float unit = BF16 ? 1.f : inverse_power(gt.t_unit), b0 = unit * gt.beta[16 * pw + g], b1 = unit * gt.beta[16 * pw + g + 8];
         // of a 16 x 16 block of T four blocks of 8 x 8, one after another along its columns, 128 bytes a warp
         auto put = [&](uint32_t op, int bi, const uint32_t(&v)[4]) {
 #pragma unroll

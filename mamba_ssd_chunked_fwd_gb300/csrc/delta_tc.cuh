@@ -11,10 +11,10 @@ namespace ssd {
 constexpr int kC = kDeltaChunk;
 
 // A chunk's gates.  With G the running sum of g: gh + gl = G log2(e), into = exp(G), out = exp(G_end - G),
-// over = exp(G_end).
+// over = exp(G_end).  t_unit, m_unit (fp16): powers of two, what T diag(beta) and M were divided by.
 struct alignas(16) Gates {
     float gh[kC], gl[kC], beta[kC], into[kC], neg_into[kC], out[kC];
-    float over;
+    float over, t_unit, m_unit;
 };
 
 // What delta_prep.cu leaves of every chunk of every head: T diag(beta) and M, both 64 x 64 in blocks of 8 rows x 16
@@ -35,6 +35,51 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
     const float2 d = __ffma2_rn(unpack2<BF16>(hi), make_float2(-1.f, -1.f), v);
     lo = tcop::pack2(d.x, d.y, BF16);
 }
+
+// Two terms of bf16 have fp32's range; two of fp16 hold a value to 2^-22 of itself only between 2^-3 and 2^16, below that to
+// 2^-25 whatever its size.  So in fp16 every operand that is computed is first multiplied by a power of two that
+// comes from the largest magnitude around it, which is taken out again where the product's fp32 sums are read:
+//
+//     S, D           to [2^13, 2^14): the largest of a row (the walk for y), or of a CTA's rows (the gradients')
+//     v, U, d, R     by 2^-12 of that, with v (or d) among those that the largest is taken of
+//     T diag(beta)   the largest beta to [1, 2)
+//     M              its largest to [2^13, 2^14), never down
+//     Y, Z           their largest to [2^12, 2^13)
+//
+// Values far smaller than the largest keep 2^-38 of it (S, D, M, Y, Z) or 2^-26 (U, R).
+constexpr float kUp = 4096.f, kDown = 1.f / 4096.f;
+__device__ __forceinline__ float inverse_power(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
+// The power of two that takes a magnitude to [2, 4), 2^100 at most.
+__device__ __forceinline__ float to_unit(float most) { return __uint_as_float((255u - min(max(__float_as_uint(most) >> 23, 30u), 252u)) << 23); }
+// A magnitude for the largest: what is not finite poisons its own row and says nothing about the others.
+__device__ __forceinline__ float finite_or_zero(float v) { return v <= 3.402823466e38f ? v : 0.f; }
+template <int W>
+__device__ __forceinline__ float largest(const float2 (&v)[W]) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) most = fmaxf(most, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+    return finite_or_zero(most);
+}
+// The larger of both, of each half; infinities (0 * inf is NaN) and NaN drop out.
+__device__ __forceinline__ __half2 larger_of_halves(__half2 most, uint32_t w) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return __hmax2(most, __hfma2(h, __float2half2_rn(0.f), __habs2(h)));
+}
+// Of eight rows, a token's (two) to a lane: the largest of rows 2 i and 2 i + 1, i = lane / 8, over the warp's tokens.
+__device__ __forceinline__ float2 largest_of_rows(const uint4 &a, const uint4 &b, int lane) {
+    const __half2 none = __float2half2_rn(0.f);
+    const __half2 v0 = larger_of_halves(larger_of_halves(none, a.x), b.x), v1 = larger_of_halves(larger_of_halves(none, a.y), b.y),
+                  v2 = larger_of_halves(larger_of_halves(none, a.z), b.z), v3 = larger_of_halves(larger_of_halves(none, a.w), b.w);
+    const bool up = lane & 16, odd = lane & 8;
+    auto swap = [](__half2 v, int bit) { return __shfl_xor_sync(0xffffffffu, v, bit); };
+    const __half2 w0 = __hmax2(up ? v2 : v0, swap(up ? v0 : v2, 16)), w1 = __hmax2(up ? v3 : v1, swap(up ? v1 : v3, 16));
+    __half2 m = __hmax2(odd ? w1 : w0, swap(odd ? w0 : w1, 8));
+#pragma unroll
+    for (int bit = 4; bit >= 1; bit >>= 1) m = __hmax2(m, swap(m, bit));
+    return __half22float2(m);
+}
+__device__ __forceinline__ float larger_half(__half2 v) { return fmaxf(__low2float(v), __high2float(v)); }
+__device__ __forceinline__ float warp_largest(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
 
 // A thread's waits: each lasts 2000 tries of up to a millisecond; once one has given up, the rest return
 // at once.  Short code: five kinds of warps run side by side, and what they run has to stay in the
@@ -71,13 +116,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// 16 tokens' values, each times its factor, as an operand: first terms at `to`, second ones 8 columns on.
+// 16 tokens' values, each times its factor (in fp16 and `by`), as an operand: first terms at `to`, second ones 8 columns on.
 template <bool BF16>
-__device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to) {
+__device__ __forceinline__ void split_scaled(const float (&x)[16], const float *f16, uint32_t to, float by = 1.f) {
     uint32_t hi[8], lo[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 f = *reinterpret_cast<const float4 *>(f16 + 4 * i);
+        float4 f = *reinterpret_cast<const float4 *>(f16 + 4 * i);
+        if (!BF16) f.x *= by, f.y *= by, f.z *= by, f.w *= by;
         split2<BF16>(__fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y)), hi[2 * i], lo[2 * i]);
         split2<BF16>(__fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w)), hi[2 * i + 1], lo[2 * i + 1]);
     }

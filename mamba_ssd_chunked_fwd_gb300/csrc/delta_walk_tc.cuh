@@ -21,10 +21,12 @@
 // Operands.  q, k and v are 16-bit as they come.  What is computed (S, S K^T, U, T, M) goes
 // into a product as the sum of two 16-bit numbers, so that states keep 16 bits (bf16:
 // relative error 4e-6 of a state, measured; one term would give 3e-3) and y is off by
-// its own rounding alone.  With fp16 a state must stay below 65504.
+// its own rounding alone.  In fp16 these terms hold values times powers of two (delta_tc.cuh), which the chain takes anew for
+// every chunk, of a row of the state with its v: its largest over four threads, and v written back scaled while S k^T
+// runs.  That and the state's columns leaving only once all are known make the walk 283 us for 223 in the case below.
 //
 // Bound by the chain: 6400 cycles a chunk for three products and three round trips through registers, with the
-// tensor pipe busy 39 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 219 us, 785 TFLOP/s of the products as formed.
+// tensor pipe busy 39 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 219-223 us, 785 TFLOP/s of the products as formed.
 //
 // Every wait is bounded; one that gives up fills what its CTA still writes with NaN.
 #pragma once
@@ -50,7 +52,7 @@ struct Smem {
 
 enum Bar { kFullKQ = 0, kEmptyKQ = kFullKQ + kStages, kFullV = kEmptyKQ + kStages, kEmptyV = kFullV + kVStages, kFullOp = kEmptyV + kVStages,
            kEmptyOp = kFullOp + kOps, kD3 = kEmptyOp + kOps, kD3Read = kD3 + 2, kD4 = kD3Read + 2, kD4Read = kD4 + 2, kD1 = kD4Read + 2, kD2, kDS, kUOut, kS,
-           kR = kS + 2, kU = kR + 4, kBars = kU + 4 };
+           kR = kS + 2, kU = kR + 4, kVUnit = kU + 4, kBars };
 
 // TMEM columns.
 template <int NN>
@@ -74,6 +76,11 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_slot;
+    // fp16: the state, v and what follows from them are held times a power of two for each row (for the gradients, whose sums
+    // run over the rows, one for the CTA): delta_tc.cuh
+    constexpr bool UNITS = !BF16;
+    __shared__ float most_mem[UNITS ? 4 * 128 : 1], down_mem[UNITS ? kSlots * 128 : 1];
+    __shared__ __align__(16) float vmost_mem[UNITS ? 128 : 4];  // written by pairs
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     Gates *gates = reinterpret_cast<Gates *>(sm + SM::GATES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -103,7 +110,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
         init(kFullKQ, kStages, 64), init(kEmptyKQ, kStages, 1), init(kFullV, kVStages, 32), init(kEmptyV, kVStages, 1);
         init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD3, 2, 1), init(kD3Read, 2, kOutWarps * 32);
         init(kD4, 2, 1), init(kD4Read, 2, kOutWarps * 32), init(kD1, 3, 1), init(kUOut, 1, kChainWarps * 32);
-        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8);
+        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kVUnit, 1, kChainWarps * 32);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -136,14 +143,42 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             }
         }
         const uint32_t x1 = tl + TM::X1 + 16 * part, x2 = tl + TM::X2 + 16 * part;
+        // v as this warp scales it: eight rows of its quarter, a lane to a token (and the one 32 on)
+        const int group = 4 * quarter + part;
+        unsigned char *vat = sm + SM::V + (lane >> 3) * 2048 + group * 128 + (lane & 7) * 16;
+        float down = 1.f;
 #pragma unroll 1
         for (int c = 0;; ++c) {
             const uint32_t par = c & 1;
+            uint4 vw[UNITS ? 2 : 1];
+            if constexpr (UNITS) {
+                if (c < w.chunks) {
+                    wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
+                    vw[0] = *reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES);
+                    vw[1] = *reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES + 4 * 2048);
+                    const float2 most = largest_of_rows(vw[0], vw[1], lane);
+                    if ((lane & 7) == 0) *reinterpret_cast<float2 *>(vmost_mem + 8 * group + (lane >> 2)) = most;
+                    __syncwarp();
+                }
+            }
             if (c > 0) {
                 wait.on(kDS, par ^ 1);
                 tc::fence_after_sync();
             }
             const float2 over = dup(c > 0 ? gates[(c - 1) % kSlots].over : 1.f);
+            const float2 back = dup(UNITS && c > 0 ? down * gates[(c - 1) % kSlots].t_unit : 1.f);
+            auto send = [&](int j, float up) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split2<BF16>(UNITS ? __fmul2_rn(dup(up), S[8 * j + i]) : S[8 * j + i], hi[i], lo[i]);
+                tc::tmem_st8(tl + TM::S + part * CW + 8 * j, hi);
+                tc::tmem_st8(tl + TM::S + part * CW + CW / 2 + 8 * j, lo);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(bars + 8 * (kS + j));
+                if (MODE == STATES)
+                    store_op(state_op<NN>(p.states, (size_t)bh * p.nc + c, ptiles, w.p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
+            };
             // the state after the chunk before, by 16 columns, and each of them as an operand: the product with k
             // begins with the first
 #pragma unroll
@@ -152,29 +187,59 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                     float v[16];
                     tc::tmem_ld16(tl + TM::DS + part * CW + 16 * j, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) S[8 * j + i] = __ffma2_rn(over, S[8 * j + i], make_float2(v[2 * i], v[2 * i + 1]));
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 ds = make_float2(v[2 * i], v[2 * i + 1]);
+                        S[8 * j + i] = __ffma2_rn(over, S[8 * j + i], UNITS ? __fmul2_rn(back, ds) : ds);
+                    }
                 }
-                if (c < w.chunks) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split2<BF16>(S[8 * j + i], hi[i], lo[i]);
-                    tc::tmem_st8(tl + TM::S + part * CW + 8 * j, hi);
-                    tc::tmem_st8(tl + TM::S + part * CW + CW / 2 + 8 * j, lo);
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(bars + 8 * (kS + j));
-                    if (MODE == STATES)
-                        store_op(state_op<NN>(p.states, (size_t)bh * p.nc + c, ptiles, w.p0 + row) + (part * CW / 8 + 2 * j) * 128, hi, lo, NN * 16);
-                }
+                if (!UNITS && c < w.chunks) send(j, 1.f);
             }
             if (c >= w.chunks) break;
+            if constexpr (UNITS) {
+                float most = largest(S);
+                if (MODE == STATES) {
+                    most = warp_largest(fmaxf(most, lane < 8 ? vmost_mem[8 * group + lane] : 0.f));
+                    if (lane == 0) most_mem[warp] = most;
+                    __syncwarp();
+                    tc::named_barrier(1, kChainWarps * 32);
+#pragma unroll
+                    for (int i = 0; i < kChainWarps; ++i) most = fmaxf(most, most_mem[i]);
+                } else {
+                    most_mem[part * 128 + row] = most;
+                    __syncwarp();
+                    tc::named_barrier(1 + quarter, 128);
+                    most = fmaxf(fmaxf(fmaxf(most_mem[row], most_mem[128 + row]), fmaxf(most_mem[256 + row], most_mem[384 + row])), vmost_mem[row]);
+                }
+                const float unit = to_unit(most);
+                down = inverse_power(unit);
+                if (MODE == Y && part == 0) down_mem[(c % kSlots) * 128 + row] = down;
+                if (MODE == STATES && tid == 0) p.units[(((size_t)bh * p.nc + c) * ptiles + tile) * 2] = unit;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < CW / 16; ++j) send(j, unit * kUp);
+                uint32_t two[8] = {vw[0].x, vw[0].y, vw[0].z, vw[0].w, vw[1].x, vw[1].y, vw[1].z, vw[1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // the units of rows 2 i and 2 i + 1 of the eight lie with the lanes that have these rows
+                    const float2 by = MODE == STATES ? dup(unit) : make_float2(__shfl_sync(0xffffffffu, unit, 8 * part + 2 * i),
+                                                                               __shfl_sync(0xffffffffu, unit, 8 * part + 2 * i + 1));
+#pragma unroll
+                    for (int m = i; m < 8; m += 4) {
+                        const float2 f = __fmul2_rn(by, unpack2<BF16>(two[m]));
+                        two[m] = tcop::pack2(f.x, f.y, BF16);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(vat + (c % kVStages) * SM::V_BYTES) = make_uint4(two[0], two[1], two[2], two[3]);
+                *reinterpret_cast<uint4 *>(vat + (c % kVStages) * SM::V_BYTES + 4 * 2048) = make_uint4(two[4], two[5], two[6], two[7]);
+                tc::fence_smem_to_async();
+                tc::mbar_arrive(bars + 8 * kVUnit);
+            }
             const Gates &gt = gates[c % kSlots];
             wait.on(kFullOp + par, (c >> 1) & 1);  // the gates
             wait.on(kD1, par);
             tc::fence_after_sync();
             float v[16];
             tc::tmem_ld16(x1, v);
-            split_scaled<BF16>(v, &gt.neg_into[16 * part], x1);  // -exp(G) S k^T
+            split_scaled<BF16>(v, &gt.neg_into[16 * part], x1, kDown);  // -exp(G) S k^T
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kR + part));
@@ -231,6 +296,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 const Gates &gt = gates[c % kSlots];
                 wait.on(kD3 + o, par);
                 tc::fence_after_sync();
+                const float up = UNITS ? kDown * inverse_power(gt.m_unit) * inverse_power(gt.t_unit) : 1.f;  // from S's scale to that of M U
 #pragma unroll 1
                 for (int j = 0; j < kC; j += 16) {  // diag(exp G) Q S^T, onto which M U is summed
                     float v[16];
@@ -238,7 +304,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                     tc::tmem_ld16(tl + j, v);
 #pragma unroll
                     for (int m = 0; m < 16; m += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&gt.into[j + m]);
+                        float4 f = *reinterpret_cast<const float4 *>(&gt.into[j + m]);
+                        if (UNITS) f.x *= up, f.y *= up, f.z *= up, f.w *= up;
                         r[m] = __float_as_uint(v[m] * f.x), r[m + 1] = __float_as_uint(v[m + 1] * f.y);
                         r[m + 2] = __float_as_uint(v[m + 2] * f.z), r[m + 3] = __float_as_uint(v[m + 3] * f.w);
                     }
@@ -250,7 +317,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 wait.on(kD4 + o, par);
                 tc::fence_after_sync();
                 const int tc0 = w.t0 + c * kC, n = min(kC, w.t1 - tc0);
-                const float scale = wait.dead() ? __int_as_float(0x7fffffff) : p.scale;
+                float scale = wait.dead() ? __int_as_float(0x7fffffff) : p.scale;
+                if (UNITS) scale *= down_mem[(c % kSlots) * 128 + row] * gt.t_unit * gt.m_unit;
                 uint16_t *to = y + (size_t)tc0 * step;
 #pragma unroll 1
                 for (int j = 0; j < kC; j += 16) {
@@ -303,7 +371,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             }
             if (go) tc::commit(bars + 8 * kD1);
             wait.on(kFullOp + par, par2);
-            wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
+            if (UNITS) wait.on(kVUnit, par);
+            else wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
             tc::fence_after_sync();
             if (go) {
                 if (!unit) {
