@@ -674,7 +674,8 @@ ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream)
  * largest beside it keeps 2^-26 of that one; u must stay below 2^14 times the larger of state and v
  * (keys of length one, or a few hundred), and the products q . k with their decay below 65504.
  * A NaN or an infinity in a live token may reach the outputs of its whole chunk.  Every wait in these
- * kernels is bounded; one that gives up leaves NaN in what its part still writes.
+ * kernels is bounded (2000 tries of up to a millisecond).  Once one gives up, what that part of
+ * the call has still to write is NaN; no error word and no status tell of it.
  * workspace: device, 256-byte aligned, ssd_delta_rule_workspace_size()
  * bytes (may be 0; then NULL is accepted).  Enqueue only.
  */
@@ -802,7 +803,8 @@ ssd_status ssd_qk_norm_bwd(const ssd_qk_norm_bwd_args *args, void *stream);
 
 /* Self-test of the bounded device-side waits (no counterpart on the pages;
  * the pages' kernels report errors only as exceptions on the host).  Every
- * mbarrier wait in the tensor-core kernels gives up after a time limit
+ * mbarrier wait in the tensor-core kernels of the SSD (not of the delta rule,
+ * see ssd_selftest_chunk_wait) gives up after a time limit
  * instead of hanging, records the timeout in the workspace error word and
  * lets the kernel finish; ssd_check_device_error then returns
  * SSD_ERR_TIMEOUT.  This call exercises that path on purpose: it clears the
@@ -815,6 +817,14 @@ ssd_status ssd_qk_norm_bwd(const ssd_qk_norm_bwd_args *args, void *stream);
  * read the outcome with ssd_check_device_error on args whose workspace is
  * this buffer.  Returns SSD_OK, SSD_ERR_INVALID_ARG or SSD_ERR_CUDA. */
 ssd_status ssd_selftest_wait_timeout(void *workspace, uint32_t timeout_us, int32_t arrive, void *stream);
+
+/* The same for the delta rule's kernels in chunks, whose waits record nothing and
+ * leave NaN: one warp waits as the preparation of a chunk does, on an mbarrier that
+ * nothing arrives on (with `arrive` nonzero: that is arrived on first), gives up after two tries of
+ * up to a millisecond, and stores into `out` (device, 388 floats) the gates that the
+ * preparation then leaves: every one NaN (released: 1).  Nothing else is in
+ * flight.  Asynchronous on `stream`.  Returns SSD_OK, SSD_ERR_INVALID_ARG or SSD_ERR_CUDA. */
+ssd_status ssd_selftest_chunk_wait(float *out, int64_t out_count, int32_t arrive, void *stream);
 
 /* A measurement kernel, not part of the SSD: `grid` CTAs of 256 threads, each
  * thread running 8 independent fp32 FMA chains of `iters` steps (a multiple

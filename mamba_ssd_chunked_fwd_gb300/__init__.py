@@ -128,6 +128,7 @@ _SIGS = {
     "ssd_fwd_host": [_P, ctypes.c_void_p],
     "ssd_check_device_error": [_P, ctypes.c_void_p],
     "ssd_selftest_wait_timeout": [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int32, ctypes.c_void_p],
+    "ssd_selftest_chunk_wait": [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p],
     "ssd_selftest_fma_rate": [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p],
     "ssd_fwd_describe": [_P, ctypes.c_char_p, ctypes.c_size_t],
     "ssd_fwd_noalloc": [_P, ctypes.c_void_p],
@@ -322,6 +323,16 @@ def ssd_selftest_wait_timeout(workspace, timeout_us: int, arrive: bool = False, 
         raise ValueError("the self-test needs a workspace of at least 256 bytes")
     _check(load_library().ssd_selftest_wait_timeout(_ptr(workspace), int(timeout_us), int(bool(arrive)), s),
            "ssd_selftest_wait_timeout")
+
+
+def ssd_selftest_chunk_wait(out, arrive: bool = False, stream=None):
+    """Run the self-test of the delta rule's bounded waits into ``out`` (a CUDA
+    float32 tensor of 388 elements): the gates that a chunk's preparation leaves when
+    its wait gives up (with ``arrive``: when it does not)."""
+    s = stream if stream is not None else _stream_handle()
+    if out.dtype != torch.float32:
+        raise ValueError("out must be float32")
+    _check(load_library().ssd_selftest_chunk_wait(_ptr(out), out.numel(), int(bool(arrive)), s), "ssd_selftest_chunk_wait")
 
 
 def ssd_selftest_fma_rate(out, iters: int, grid: int, stream=None):

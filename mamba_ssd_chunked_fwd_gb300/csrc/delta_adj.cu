@@ -42,7 +42,7 @@ struct Smem {
 };
 
 enum Bar { kFullKQ = 0, kEmptyKQ = kFullKQ + kStages, kFullV = kEmptyKQ + kStages, kEmptyV = kFullV + kVStages, kFullOp = kEmptyV + kVStages,
-           kEmptyOp = kFullOp + kOps, kD1 = kEmptyOp + kOps, kD2, kDS, kDFree, kX2, kUnit, kDReady, kS, kR = kS + 2, kU = kR + 4, kBars = kU + 4 };
+           kEmptyOp = kFullOp + kOps, kD1 = kEmptyOp + kOps, kD2, kDS, kDFree, kX2, kUnit, kDReady, kS, kR = kS + 2, kU = kR + 4, kDrain = kU + 4, kBars };
 
 // TMEM columns: D's operand, D K^T and then the operands dU and R, M^T d, R, the change of D, d's operand.
 template <int NN>
@@ -75,7 +75,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
         };
         init(kFullKQ, kStages, 64), init(kEmptyKQ, kStages, 1), init(kFullV, kVStages, 32), init(kEmptyV, kVStages, 1 + kSideWarps * 32);
         init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD1, 6, 1), init(kDReady, 1, kSideWarps * 32);
-        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8);
+        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kDrain, 1, 1);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -264,6 +264,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                 wait.on(kUnit, i & 1);
                 scale *= unit_mem[i % kSlots];
             }
+            if (wait.dead()) break;
             tc::fence_after_sync();
             const unsigned char *dy = sm + SM::DY + (i % kVStages) * SM::DY_BYTES + (row >> 3) * 128 + (row & 7) * 2;
 #pragma unroll 1
@@ -314,6 +315,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             if (i > 0) {  // the M^T d before is read
                 for (int k = 0; k < 4; ++k) wait.on(kR + k, par ^ 1);
             }
+            if (wait.dead()) goto given_up;
             tc::fence_after_sync();
             if (go) {
                 const uint64_t vd = tc::desc(sbase + SM::DY + (i % kVStages) * SM::DY_BYTES, 2048, 128);
@@ -329,6 +331,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {  // D k^T, as the state's columns come
                 wait.on(kS + j, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
 #pragma unroll
@@ -341,6 +344,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             if (go) tc::commit(bars + 8 * kD1);
             const uint64_t kt = tc::desc(kq, 128, 2048);
             wait.on(kDReady, par);
+            if (wait.dead()) goto given_up;
             tc::fence_after_sync();
             if (go) {
 #pragma unroll
@@ -353,6 +357,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {  // dU^T T
                 wait.on(kR + k, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     tc::mma_f16_ts(tmem + TM::X3, x_term(TM::X1, k), td + k * 16, ID_B, k > 0);
@@ -367,6 +372,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {  // - (beta exp(G) R)^T k
                 wait.on(kU + k, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k), kt + k * 16, ID_DS, 1);
@@ -378,9 +384,10 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                 tc::commit(bars + 8 * (kEmptyKQ + i % kStages));
             }
         }
+    given_up:
         // the last products may still read shared memory: wait for them before the CTA ends
-        if (chunks > 0) wait.on(kEmptyKQ + (chunks - 1) % kStages, ((chunks - 1) / kStages) & 1);
-        __syncwarp();
+        if (go) tc::commit(bars + 8 * kDrain);
+        Waits{bars}.on(kDrain, 0);
     } else {
         // ---- copies: lane = row of eight, 16-byte piece of four.  The first warp takes k, the second q, the third dy and a chunk's operands
         const int r = lane & 7, piece = lane >> 3, which = warp - kLoadWarp;
@@ -392,7 +399,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
         const uint32_t to = sbase + (which < 2 ? SM::KQ + which * 1024 + piece * 2048 : SM::DY + piece * 128) + r * 16;
         const uint32_t stage = which < 2 ? SM::KQ_BYTES : SM::DY_BYTES, row_step = which < 2 ? 128 : 2048, col_step = which < 2 ? 8192 : 512;
         const int stages = which < 2 ? kStages : kVStages, empty = which < 2 ? kEmptyKQ : kEmptyV, full = which < 2 ? kFullKQ : kFullV;
-        int at = 0;
+        int at = 0, issued = 0;
         uint32_t parity = 1;
         const unsigned char *ops = p.ops + (size_t)bh * p.nc * op_bytes(true);
 #pragma unroll 1
@@ -400,6 +407,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             const int c = chunks - 1 - i;
             if (which == 2) {  // with a place of T's, the gates four chunks back are done with too
                 wait.on(kEmptyOp + (i & 1), ((i >> 1) & 1) ^ 1);
+                if (wait.dead()) break;
                 if (lane == 0) {
                     const uint32_t bar = bars + 8 * (kFullOp + (i & 1)), dst = sbase + SM::OP + (i & 1) * 32768;
                     const unsigned char *op = ops + (size_t)c * op_bytes(true);
@@ -409,8 +417,10 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                     bulk_load(sbase + SM::GATES + (i % kSlots) * (uint32_t)sizeof(Gates), op + kOpGates, (uint32_t)sizeof(Gates), bar);
                 }
                 __syncwarp();
+                issued = i + 1;
             }
             wait.on(empty + at, parity);
+            if (wait.dead()) break;
             const char *row = from + 2 * ((c * kC + r) * s1);
             uint32_t dst = to + at * stage;
 #pragma unroll 1
@@ -428,6 +438,8 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             tc::mbar_arrive(bars + 8 * (full + at));
             if (++at == stages) at = 0, parity ^= 1;
         }
+        if (wait.dead())  // nobody may have waited for these
+            for (int i = max(issued - kOps, 0); i < issued; ++i) Waits{bars}.on(kFullOp + (i & 1), (i >> 1) & 1);
     }
     __syncwarp();
     tc::fence_before_sync();

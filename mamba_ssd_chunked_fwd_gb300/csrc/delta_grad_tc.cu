@@ -44,7 +44,7 @@ struct Smem {
     static constexpr uint32_t GATES = YZ + 32768, SUMS = GATES + 2 * (uint32_t)sizeof(Gates), BYTES = SUMS + 4096 + 2048;
 };
 
-enum Bar { kFull = 0, kEmpty = kFull + kStages, kFullKQ = kEmpty + kStages, kEmptyKQ = kFullKQ + 2, kX = kEmptyKQ + 2, kYZ, kIn, kOut, kDone, kScaled, kBars = kScaled + kStages };
+enum Bar { kFull = 0, kEmpty = kFull + kStages, kFullKQ = kEmpty + kStages, kEmptyKQ = kFullKQ + 2, kX = kEmptyKQ + 2, kYZ, kIn, kOut, kDone, kScaled, kDrain = kScaled + kStages, kBars };
 
 template <int NN>
 struct Tm {  // columns
@@ -88,7 +88,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
         };
         init(kFull, kStages, 33), init(kEmpty, kStages, 1 + kMathWarps * 32), init(kFullKQ, 2, 33), init(kEmptyKQ, 2, 1 + kMathWarps * 32);
         init(kX, 1, 1), init(kYZ, 1, 128), init(kIn, 1, kMathWarps * 32), init(kOut, 1, 1), init(kDone, 1, kMathWarps * 32);
-        init(kScaled, kStages, kMathWarps * 32);
+        init(kScaled, kStages, kMathWarps * 32), init(kDrain, 1, 1);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -189,7 +189,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             }
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
-            if (lane == 0) sds[warp] = sd;
+            if (lane == 0) sds[warp] = wait.dead() ? __int_as_float(0x7fffffff) : sd;
             wait.on(kFullKQ + (n_unit & 1), (n_unit >> 1) & 1);  // the gates
             wait.on(kX, par);
             tc::fence_after_sync();
@@ -407,6 +407,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             const uint32_t par = n_unit & 1, kq = sbase + SM::KQ + par * SM::KQ_BYTES;
             wait.on(kFullKQ + par, (n_unit >> 1) & 1);
             wait.on(kDone, par ^ 1);  // the unit before has been read
+            if (wait.dead()) goto given_up;
             tc::fence_after_sync();
             if (go) {
                 const uint64_t d = tc::desc(kq, 2048, 128);
@@ -419,6 +420,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 const uint32_t st = sbase + at * SM::STAGE;
                 wait.on(kFull + at, (stage_count / kStages) & 1);
                 if (level) wait.on(kScaled + at, (stage_count / kStages) & 1);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     const uint64_t sd = tc::desc(st + SM::S, 2 * NN * 16, 128), dd = tc::desc(st + SM::D, 2 * NN * 16, 128);
@@ -450,6 +452,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             if (go) tc::commit(bars + 8 * kX);
             wait.on(kYZ, par);
             wait.on(kIn, par);
+            if (wait.dead()) goto given_up;
             tc::fence_after_sync();
             if (go) {
                 const uint64_t kt = tc::desc(kq, 128, 2048), qt = kt + 64;  // k^T, q^T as first operands: 16 tokens are 256 bytes
@@ -472,9 +475,10 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             }
             ++n_unit;
         }
+    given_up:
         // the last products may still read shared memory: wait for them before the CTA ends
-        if (n_unit > 0) wait.on(kOut, (n_unit - 1) & 1);
-        __syncwarp();
+        if (go) tc::commit(bars + 8 * kDrain);
+        Waits{bars}.on(kDrain, 0);
     } else if (warp == kCopyWarp) {
         // ---- k, q and the gates
         const int r = lane & 7, piece = lane >> 3;
@@ -485,6 +489,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             if (n == 0) continue;
             const uint32_t at = n_unit & 1, bar = bars + 8 * (kFullKQ + at);
             wait.on(kEmptyKQ + at, ((n_unit >> 1) & 1) ^ 1);
+            if (wait.dead()) break;
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(bar, (uint32_t)sizeof(Gates));
                 bulk_load(sbase + SM::GATES + at * (uint32_t)sizeof(Gates), p.ops + (size_t)unit * op_bytes(true) + kOpGates, (uint32_t)sizeof(Gates), bar);
@@ -507,10 +512,12 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             tc::mbar_arrive(bar);
             ++n_unit;
         }
+        if (wait.dead())  // nobody may have waited for these
+            for (int n = max(n_unit - 2, 0); n < n_unit; ++n) Waits{bars}.on(kFullKQ + (n & 1), (n >> 1) & 1);
     } else {
         // ---- 32 rows of P at a time: S, D, U and R as they lie, dy and v (lane = token of eight, 16-byte piece of the 32 rows)
         const int r = lane & 7, piece = lane >> 3, at = warp - kCopyWarp - 1;
-        int stage_count = 0;
+        int stage_count = 0, issued = 0;  // of this stage
 #pragma unroll 1
         for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
             const int n = tokens_of(unit), c = unit % p.nc, bh = unit / p.nc, h = bh % p.H, b = bh / p.H;
@@ -523,6 +530,7 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 if (stage_count % kStages != at) continue;
                 const uint32_t st = sbase + at * SM::STAGE, bar = bars + 8 * (kFull + at);
                 wait.on(kEmpty + at, ((stage_count / kStages) & 1) ^ 1);
+                if (wait.dead()) break;
                 if (lane == 0) {
                     const size_t from = (size_t)unit * steps + s;
                     tc::mbar_arrive_expect_tx(bar, 2 * SM::ST + 2 * SM::UT);
@@ -543,8 +551,10 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 cp_wait<0>();
                 tc::fence_smem_to_async();
                 tc::mbar_arrive(bar);
+                ++issued;
             }
         }
+        if (wait.dead() && issued > 0) Waits{bars}.on(kFull + at, (issued - 1) & 1);  // nobody may have waited for it
     }
     __syncwarp();
     tc::fence_before_sync();

@@ -375,7 +375,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
             }
         }
     }
-    if (wait.dead() && lane == 0) gt.over = gt.into[0] = __int_as_float(0x7fffffff);  // every walk's results
+    if (wait.dead()) poison(gt, lane);
     tc::fence_smem_to_async();
     __syncthreads();
     if (tid == 0) {

@@ -86,6 +86,8 @@ __device__ __forceinline__ float warp_largest(float v) { return __uint_as_float(
 // instruction cache (with unrolled loops and longer waits every second cycle went to fetching).
 // Every lane of a warp calls it, and the warp goes on together: tcgen05.ld and .st and the named barriers want that, and a
 // store by some of the lanes before them leaves the compiler free to run the rest apart.
+// A wait that gives up: what its warp would store is NaN from then on, and a warp that only hands on (products, copies, side
+// operands) hands on nothing more, so that those behind it give up too.
 struct Waits {
     uint32_t bars;
     uint32_t tries = 2000;
@@ -96,11 +98,16 @@ struct Waits {
         for (uint32_t i = 0; i < tries && !done; ++i)
             asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\tselp.u32 %0, 1, 0, p;\n}\n"
                          : "=r"(done) : "r"(bars + 8 * bar), "r"(parity) : "memory");
-        tries = done ? tries : 0u;
+        tries = __all_sync(0xffffffffu, done) ? tries : 0u;
         asm volatile("" : "+r"(tries));  // or the code after it is laid out twice, for a thread that waits and one that does not
-        __syncwarp();
     }
 };
+
+// A chunk's gates where its preparation has given up: every factor of every walk's results is NaN.  By one warp.
+__device__ __forceinline__ void poison(Gates &gt, int lane) {
+    float *f = reinterpret_cast<float *>(&gt);
+    for (int i = lane; i < (int)(sizeof(Gates) / sizeof(float)); i += 32) f[i] = __int_as_float(0x7fffffff);
+}
 
 // ex2 that stays where it is: moved into a branch on whether its result is wanted, each would wait for the one before
 // (measured: 68 cycles an element in place of 20).

@@ -28,7 +28,7 @@
 // Bound by the chain: 6400 cycles a chunk for three products and three round trips through registers, with the
 // tensor pipe busy 39 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 219-223 us, 785 TFLOP/s of the products as formed.
 //
-// Every wait is bounded; one that gives up fills what its CTA still writes with NaN.
+// Every wait is bounded; once one gives up, what the CTA still writes is NaN.
 #pragma once
 
 #include "delta_tc.cuh"
@@ -52,7 +52,7 @@ struct Smem {
 
 enum Bar { kFullKQ = 0, kEmptyKQ = kFullKQ + kStages, kFullV = kEmptyKQ + kStages, kEmptyV = kFullV + kVStages, kFullOp = kEmptyV + kVStages,
            kEmptyOp = kFullOp + kOps, kD3 = kEmptyOp + kOps, kD3Read = kD3 + 2, kD4 = kD3Read + 2, kD4Read = kD4 + 2, kD1 = kD4Read + 2, kD2, kDS, kUOut, kS,
-           kR = kS + 2, kU = kR + 4, kVUnit = kU + 4, kBars };
+           kR = kS + 2, kU = kR + 4, kVUnit = kU + 4, kDrain, kBars };
 
 // TMEM columns.
 template <int NN>
@@ -110,7 +110,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
         init(kFullKQ, kStages, 64), init(kEmptyKQ, kStages, 1), init(kFullV, kVStages, 32), init(kEmptyV, kVStages, 1);
         init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD3, 2, 1), init(kD3Read, 2, kOutWarps * 32);
         init(kD4, 2, 1), init(kD4Read, 2, kOutWarps * 32), init(kD1, 3, 1), init(kUOut, 1, kChainWarps * 32);
-        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kVUnit, 1, kChainWarps * 32);
+        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kVUnit, 1, kChainWarps * 32), init(kDrain, 1, 1);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -360,6 +360,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {  // S k^T, as the state's columns come
                 wait.on(kS + j, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
 #pragma unroll
@@ -373,6 +374,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             wait.on(kFullOp + par, par2);
             if (UNITS) wait.on(kVUnit, par);
             else wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
+            if (wait.dead()) goto given_up;
             tc::fence_after_sync();
             if (go) {
                 if (!unit) {
@@ -388,6 +390,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {  // - (exp(G) S k^T) (T diag(beta))^T
                 wait.on(kR + k, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     tc::mma_f16_ts(tmem + TM::X2, x_term(TM::X1, k), td + k * 128, ID, !unit || k > 0);
@@ -398,6 +401,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             if (go) tc::commit(bars + 8 * kD2);
             if (MODE == Y) {  // while the chain splits U
                 wait.on(kD4Read + par, par2 ^ 1);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
 #pragma unroll
@@ -412,6 +416,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {  // the change of the state
                 wait.on(kU + k, par);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     tc::mma_f16_ts(tmem + TM::DS, x_term(TM::X1, k), kt + k * 16, ID_DS, k > 0);
@@ -425,6 +430,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             if (MODE == Y) {
                 wait.on(kUOut, par);
                 wait.on(kD3Read + par, par2);
+                if (wait.dead()) goto given_up;
                 tc::fence_after_sync();
                 if (go) {
                     const uint64_t md = tc::desc(op + kOpM, 1024, 128);
@@ -439,9 +445,10 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             }
             if (go) tc::commit(bars + 8 * (kEmptyOp + par));
         }
+    given_up:
         // the last products may still read shared memory: wait for them before the CTA ends
-        if (w.chunks > 0) wait.on(kEmptyOp + ((w.chunks - 1) & 1), ((w.chunks - 1) >> 1) & 1);
-        __syncwarp();
+        if (go) tc::commit(bars + 8 * kDrain);
+        Waits{bars}.on(kDrain, 0);
     } else {
         // ---- copies: lane = row of eight, 16-byte piece of four.  The first warp takes k, the second q, the third v and a chunk's operands
         const int r = lane & 7, piece = lane >> 3, which = warp - kLoadWarp;
@@ -453,13 +460,14 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
         const uint32_t to = sbase + (which < 2 ? SM::KQ + which * 1024 + piece * 2048 : SM::V + piece * 128) + r * 16;
         const uint32_t stage = which < 2 ? SM::KQ_BYTES : SM::V_BYTES, row_step = which < 2 ? 128 : 2048, col_step = which < 2 ? 8192 : 512;
         const int stages = which < 2 ? kStages : kVStages, empty = which < 2 ? kEmptyKQ : kEmptyV, full = which < 2 ? kFullKQ : kFullV;
-        int at = 0;
+        int at = 0, issued = 0;
         uint32_t parity = 1;
         const unsigned char *ops = p.ops + ((size_t)bh * p.nc + w.t0 / kC) * op_bytes(MODE == STATES);
 #pragma unroll 1
         for (int c = 0; c < w.chunks; ++c) {
             if (which == 2) {  // with a place of T's, the gates four chunks back are done with too
                 wait.on(kEmptyOp + (c & 1), ((c >> 1) & 1) ^ 1);
+                if (wait.dead()) break;
                 if (lane == 0) {
                     const uint32_t bar = bars + 8 * (kFullOp + (c & 1));
                     constexpr uint32_t bytes = MODE == Y ? kOpGates : kOpM;  // T and M, or T alone
@@ -469,8 +477,10 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                     bulk_load(sbase + SM::GATES + (c % kSlots) * (uint32_t)sizeof(Gates), op + kOpGates, (uint32_t)sizeof(Gates), bar);
                 }
                 __syncwarp();
+                issued = c + 1;
             }
             wait.on(empty + at, parity);
+            if (wait.dead()) break;
             const char *row = from + 2 * ((w.t0 + c * kC + r) * s1);
             uint32_t dst = to + at * stage;
 #pragma unroll 1
@@ -488,6 +498,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             tc::mbar_arrive(bars + 8 * (full + at));
             if (++at == stages) at = 0, parity ^= 1;
         }
+        if (wait.dead())  // nobody may have waited for these
+            for (int c = max(issued - kOps, 0); c < issued; ++c) Waits{bars}.on(kFullOp + (c & 1), (c >> 1) & 1);
     }
     __syncwarp();
     tc::fence_before_sync();

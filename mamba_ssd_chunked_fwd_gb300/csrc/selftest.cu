@@ -6,9 +6,13 @@
 // ssd_check_device_error maps the word to SSD_ERR_TIMEOUT.  No TMA copy,
 // tensor-core operation or TMEM allocation is in flight when the wait gives up.
 //
+// ssd_selftest_chunk_wait: the same for the waits of the delta rule's chunk kernels
+// (Waits in delta_tc.cuh), and for what a preparation that gives up leaves as a chunk's gates.
+//
 // ssd_selftest_fma_rate: a plain fp32 FMA-chain kernel whose CUDA-event time
 // gives this GPU's fp32 CUDA-core throughput (the denominator of the
 // backward's roofline, which runs on the CUDA cores).
+#include "delta_tc.cuh"
 #include "ssd_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -29,6 +33,34 @@ __global__ void selftest_wait_kernel(unsigned int *err, uint64_t timeout_ns, int
         if (arrive) ssd::tc::mbar_arrive(b);
         if (!ssd::tc::mbar_wait(b, 0u, timeout_ns)) atomicOr(err, 1u);
     }
+}
+
+// One warp waits on phase 0 of a fresh mbarrier as the preparation of a chunk does, for two tries of at most a
+// millisecond, and then leaves the chunk's gates, ones before, as that does.  A second wait, on a barrier that is
+// released, tells whether the warp stays given up.
+__global__ void selftest_chunk_wait_kernel(float *out, int arrive) {
+    __shared__ __align__(8) uint64_t bar[2];
+    __shared__ ssd::Gates gates;
+    const uint32_t b = ssd::tc::smem_addr(bar);
+    constexpr int count = sizeof(ssd::Gates) / sizeof(float);
+    float *g = reinterpret_cast<float *>(&gates);
+    if (threadIdx.x == 0) {
+        ssd::tc::mbar_init(b, 1);
+        ssd::tc::mbar_init(b + 8, 1);
+        ssd::tc::mbar_init_fence();
+    }
+    for (int i = threadIdx.x; i < count; i += 32) g[i] = 1.f;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (arrive) ssd::tc::mbar_arrive(b);
+        ssd::tc::mbar_arrive(b + 8);
+    }
+    ssd::Waits wait{b, 2};
+    wait.on(0, 0);
+    wait.on(1, 0);
+    if (wait.dead()) ssd::poison(gates, threadIdx.x);
+    __syncwarp();
+    for (int i = threadIdx.x; i < count; i += 32) out[i] = g[i];
 }
 
 constexpr int kFmaThreads = 256;
@@ -66,6 +98,17 @@ extern "C" ssd_status ssd_selftest_fma_rate(float *out, int64_t out_count, int32
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     selftest_fma_kernel<<<grid, kFmaThreads, 0, s>>>(out, iters, 0.9999f, 1e-4f);
     cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return ssd::report_error(SSD_ERR_CUDA, cudaGetErrorString(e));
+    return ssd::report_error(SSD_OK, "");
+}
+
+extern "C" ssd_status ssd_selftest_chunk_wait(float *out, int64_t out_count, int32_t arrive, void *stream) {
+    constexpr int64_t count = sizeof(ssd::Gates) / sizeof(float);
+    if (!out) return ssd::report_error(SSD_ERR_INVALID_ARG, "ssd_selftest_chunk_wait: out is null");
+    if (out_count != count) return ssd::report_error(SSD_ERR_INVALID_ARG, "ssd_selftest_chunk_wait: out must hold 388 floats");
+    static_assert(count == 388, "the message");
+    selftest_chunk_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(out, arrive ? 1 : 0);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return ssd::report_error(SSD_ERR_CUDA, cudaGetErrorString(e));
     return ssd::report_error(SSD_OK, "");
 }
