@@ -760,6 +760,7 @@ ssd_status ssd_delta_rule_step(const ssd_delta_step_args *args, void *stream);
  *   above, the outputs dense; w_q, w_k [N] fp32 (NULL = 1)
  *   freqs [nfreq] fp32, device, finite (radians per position), 2 nfreq <= N
  *   positions [B,L] int32, device (NULL = the token's index in its row)
+ * Squares and their sum are fp32: rows between about 1e-18 and 1e18 in size.
  * N <= 256.  q_out may be a dense q itself, k_out a dense k; other overlaps of an
  * output are refused.  For one token of each of B sequences: B = 1, L = their number.
  */

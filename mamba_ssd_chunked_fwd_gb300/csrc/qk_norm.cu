@@ -207,7 +207,8 @@ __device__ __forceinline__ void rows_of(const QkNormParams &p, int which, long l
                     g[m][j] = __fmul2_rn(g[m][j], wt[m][j]);
                 }
             }
-            const float2 f = dup(-inv * inv * inv * div * sum_group<LPR>(dot.x + dot.y));
+            // r^3 alone leaves fp32's range where rows are near 1e-13 or 1e13; with the sum, which has their size, r^2 is the most
+            const float2 f = dup(-inv * (inv * (inv * (div * sum_group<LPR>(dot.x + dot.y)))));
 #pragma unroll
             for (int m = 0; m < M; ++m) {
 #pragma unroll
