@@ -664,7 +664,8 @@ ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream)
  * q, k, v, g and beta are read through strides as the selective scan's tensors are; y is
  * dense.  An output that overlaps an input or the other output is refused.
  * Every dim > 0, N <= 128, P <= 1024, H % G == 0.  g is meant to be <= 0 (minus
- * infinity empties the state) and keys to be of length about one; neither is checked.
+ * infinity empties the state) and keys to be of length about one; neither is checked.  Where gates
+ * grow, a sum above 88 between two of 64 tokens gives infinities and NaN.
  * States are fp32.  16-bit tensors whose N, P, strides and addresses are whole 16-byte
  * pieces run in chunks of 64 tokens on the tensor cores, all others token by token in fp32.
  * In chunks, what is computed enters a product as two 16-bit terms: states are off by about

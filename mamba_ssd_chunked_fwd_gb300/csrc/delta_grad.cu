@@ -110,7 +110,7 @@ delta_grad_kernel(const __grid_constant__ DeltaParams p) {
         for (int m = 0; m < 2; ++m) {
             const int i = 2 * tid + m;
             float g = load_gate<IO>(p.g, b * p.gs[0] + (t0 + i) * p.gs[1] + h, p.g32, i < n);
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // exp(-200) is 0, and sums stay finite
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(g) : "f"(-200.f));  // sums stay finite; on growth beside it see delta_prep.cu
             hi[m] = g, lo[m] = 0.f;
             s.beta[i] = load_gate<IO>(p.beta, b * p.bs[0] + (t0 + i) * p.bs[1] + h, p.b32, i < n);
         }

@@ -46,7 +46,9 @@ __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], co
     long long sum[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        // exp(-200) is 0, and so is every product with it, and exp(1400) infinite; sums of 64 tokens stay below 2^17
+        // Sums of 64 tokens stay below 2^17.  exp(1400) is infinite.  A gate that empties the state counts as -200: no growth that
+        // leaves every factor of the chunk finite (a sum of 88 between any two of its tokens) brings exp(-200) back above 0
+        // in fp32, and more of it makes factors that span it infinite, and what they enter infinite or NaN.
         const float g = fminf(fmaxf(graw[m], -200.f), 1400.f), hi = g * kLog2e;
         const float lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - fl(log2(e))
         const float big = rintf(hi * 16384.f);
