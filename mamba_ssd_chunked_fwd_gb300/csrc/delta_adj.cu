@@ -17,7 +17,7 @@
 // Bound by what it stores, 112 KB of D, R and dv to a chunk and SM, beside the chain: [4,2048] with 16 heads of 128 x 128, bf16,
 // 193 us with the states' walk on the other SMs.  The stores of D, or of D and R, by the side warps from TMEM in place of
 // the chain's took 7 and 14 us longer.  In fp16, with the powers of two that D, d and R are held times (the largest of the
-// CTA's rows, D, d and M^T d, by a barrier of the chain's warps; the side warps wait for it), 247 us.
+// CTA's rows, D, d and M^T d, by a barrier of the chain's warps; the side warps wait for it), 252 us.
 //
 // It leaves D after every chunk and R as operands for delta_grad_tc.cu, and writes dv.
 #include "delta_walk_tc.cuh"

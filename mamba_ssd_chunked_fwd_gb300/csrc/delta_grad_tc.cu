@@ -12,9 +12,9 @@
 //     dq^T = scale exp(G_i) P1 + K^T Y
 //     dk^T = -beta_i exp(G_i) P2 + exp(G_end - G_i) P3 - K^T (Z + Z^T) + Q^T Y^T
 //
-// [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 177 us, 3.0 TB/s of operands read.  A chunk's 22000 cycles are products
+// [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 183 us, 2.9 TB/s of operands read.  A chunk's 22000 cycles are products
 // 7000 (both operands from shared memory: 56 cycles each), waits for S and D 3000, Y and Z 3000, sums over N 2600, second
-// products and stores 3500; with 16 warps in place of 8 the same.  In fp16, Y and Z made twice, once for their largest, 196 us.  TMEM is full, so that two chunks do not overlap.
+// products and stores 3500; with 16 warps in place of 8 the same.  In fp16, Y and Z made twice, once for their largest, 200 us.  TMEM is full, so that two chunks do not overlap.
 //
 // Y and Z lie in shared memory once: read along j they are an operand, read along i its transpose.
 // A CTA takes one chunk of one head after another; while its warps finish one, the next one's tiles are copied:

@@ -10,12 +10,13 @@
 // tcgen05's 128 rows empty, and each needs the one before it.  No power of A is formed:
 // with keys alike those would cancel.
 //
-// A kernel of its own, not warps of the walk: there it took a third of the code that every
-// chunk pulled through the instruction cache, and the walk waited for it (prompts of [4,4096,32,128,128]
-// 278 us with it inside); here chunks are independent, eight CTAs share an SM, and the walks of
-// segments and of the gradients read its results again.
+// A kernel of its own, not warps of the walk, for rows that are cut and for the gradients: chunks are independent, eight CTAs
+// share an SM, and the walks of segments and of the gradients read its results again (one row of 16384
+// tokens 1058 us with it inside the walk, 877 with it apart).  Where heads fill the SMs, it costs: prompts of [4,4096,32,128,128]
+// took 278 us as one kernel and take 347 as two, though the walk alone went from 278 to 213 (a third less code
+// for the instruction cache).  Both forms side by side are not built.
 //
-// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 132 us, with T for the gradients 42 us for 2048 of them.  No pipe is
+// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 132 us (fp16, M looked at twice, 140), with T for the gradients 42 us for 2048 of them.  No pipe is
 // above 25 %; bound by latency (barriers, the loads, the blocks of T's first column one after another).  With k and q
 // whole and T in shared memory, six CTAs to an SM: 140 and 50 us.
 #include "delta_tc.cuh"

@@ -106,8 +106,9 @@ bool by_eights(const void *p, long long s0, long long s1) {
 }  // namespace
 
 // 16-byte pieces of k, q and v, and float4 of the states.  What is not taken is walked token by token, [4,4096] with 32 heads of
-// 128 rows in bf16 (and its gradients, [4,2048] with 16 heads): N = 128 in chunks 356 us (418), N = 124 by tokens 2232 us (2324); fp32
-// with N = 128 by tokens 2140 us (2320).  One chunk of one row takes 7 us longer than its 64 tokens, 512 tokens half as long.
+// 128 rows in bf16 (and its gradients, [4,2048] with 16 heads): N = 128 in chunks 347 us (424), N = 124 by tokens 2231 us (2321); fp32
+// with N = 128 by tokens 2137 us (2318).  One chunk of one row takes 6 us longer than its 64 tokens, 512 tokens half as long; the rule
+// has no term for the length.
 bool delta_tc_takes(const DeltaParams &p, int io) {
     return io != IO_F32 && p.N % 8 == 0 && p.P % 8 == 0 && by_eights(p.k, p.ks[0], p.ks[1]) && by_eights(p.q, p.qs[0], p.qs[1]) &&
            by_eights(p.v, p.vs[0], p.vs[1]) && by_eights(p.y, 0, 0) && by_eights(p.h0, 0, 0) && by_eights(p.final_state, 0, 0) &&
@@ -115,7 +116,7 @@ bool delta_tc_takes(const DeltaParams &p, int io) {
 }
 
 // The cut of the rows into segments.  A walk takes an SM for itself, and a chunk about 3.3 us of it (a pass of a segment's own
-// state and of its transition 2.6); few heads are cut until there are walks for the SMs.  The cut costs that first pass, a
+// state and of its transition 2.6), both measured with 128 x 128 in bf16 and taken for every N and P; few heads are cut until there are walks for the SMs.  The cut costs that first pass, a
 // fold (a state through a segment's transition, about 1.5 us) and two launches.
 void delta_segments(DeltaParams &p) {
     const double sms = scan_sm_count(), heads = (double)p.B * p.H, tiles = (p.P + 127) / 128;

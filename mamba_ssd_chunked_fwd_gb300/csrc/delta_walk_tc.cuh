@@ -23,10 +23,10 @@
 // relative error 4e-6 of a state, measured; one term would give 3e-3) and y is off by
 // its own rounding alone.  In fp16 these terms hold values times powers of two (delta_tc.cuh), which the chain takes anew for
 // every chunk, of a row of the state with its v: its largest over four threads, and v written back scaled while S k^T
-// runs.  That and the state's columns leaving only once all are known make the walk 283 us for 223 in the case below.
+// runs.  That and the state's columns leaving only once all are known make the walk 286 us for 213 in the case below.
 //
-// Bound by the chain: 6400 cycles a chunk for three products and three round trips through registers, with the
-// tensor pipe busy 39 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 219-223 us, 785 TFLOP/s of the products as formed.
+// Bound by the chain: 6300 cycles a chunk for three products and three round trips through registers, with the
+// tensor pipe busy 41 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 213 us, 807 TFLOP/s of the products as formed.
 //
 // Every wait is bounded; once one gives up, what the CTA still writes is NaN.
 #pragma once
