@@ -669,11 +669,11 @@ ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream)
  * States are fp32.  16-bit tensors whose N, P, strides and addresses are whole 16-byte
  * pieces run in chunks of 64 tokens on the tensor cores, all others token by token in fp32.
  * In chunks, what is computed enters a product as two 16-bit terms: states are off by about
- * 4e-6 of themselves after a call, where fp32 tensors keep 3e-7.  With SSD_F16 the terms are those of a value times a power of two, taken
- * from the largest state and v of a row of P in a chunk (in the gradients: of 128 rows, and from dfinal
- * and dy), so that neither their size nor a loss scale matters.  What is far smaller than the
- * largest beside it keeps 2^-26 of that one; u must stay below 2^14 times the larger of state and v
- * (keys of length one, or a few hundred), and the products q . k with their decay below 65504.
+ * 4e-6 of themselves after a call, where fp32 tensors keep 3e-7.  With SSD_F16 they are off by about
+ * 1e-6: the terms are those of a value times a power of two, taken from the largest state, v and key of a
+ * row of P in a chunk (in the gradients: of 128 rows, and from dfinal and dy), so that neither
+ * their size nor a loss scale matters.  What is far smaller than the largest beside it keeps 2^-31 of that
+ * one; the products q . k with their decay must stay below 65504.
  * A NaN or an infinity in a live token may reach the outputs of its whole chunk.  Every wait in these
  * kernels is bounded (2000 tries of up to a millisecond).  Once one gives up, what that part of
  * the call has still to write is NaN; no error word and no status tell of it.

@@ -38,7 +38,7 @@ struct DeltaParams {
     float *adj;     // [B,H,nc,P,N] adjoint of the state after a chunk
     float *u, *dr;  // [B,H,64 nc,P] u, and the gradient of v_t - S' k_t over beta
     float *dqh, *dkh;  // [B,L,H,N] a head's share of dq, dk (H > G)
-    float *units;  // fp16 in chunks, [B,H,nc,P tiles of 128][2]: the powers of two that the states and u, the adjoint and r are held times
+    float *units;  // fp16 in chunks, [B,H,nc,P tiles of 128][4]: the powers of two that states, u, adjoint and r are held times
 };
 
 struct DeltaStepParams {

@@ -16,8 +16,8 @@
 //
 // Bound by what it stores, 112 KB of D, R and dv to a chunk and SM, beside the chain: [4,2048] with 16 heads of 128 x 128, bf16,
 // 193 us with the states' walk on the other SMs.  The stores of D, or of D and R, by the side warps from TMEM in place of
-// the chain's took 7 and 14 us longer.  In fp16, with the powers of two that D, d and R are held times (the largest of the
-// CTA's rows, D, d and M^T d, by a barrier of the chain's warps; the side warps wait for it), 252 us.
+// the chain's took 7 and 14 us longer.  In fp16, with the powers of two of the operands (the largest D, d and M^T d of the
+// CTA's rows by a barrier of the chain's warps, for which the side warps wait; the largest dU of a row over four threads), 269 us.
 //
 // It leaves D after every chunk and R as operands for delta_grad_tc.cu, and writes dv.
 #include "delta_walk_tc.cuh"
@@ -60,8 +60,7 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
     __shared__ uint32_t tmem_slot;
     // fp16: D, d and what follows from them are held times a power of two (delta_tc.cuh)
     constexpr bool UNITS = !BF16;
-    __shared__ float2 most_mem[UNITS ? kChainWarps : 1];
-    __shared__ float unit_mem[UNITS ? kSlots : 1];
+    __shared__ float most_mem[UNITS ? 3 * kChainWarps : 1], row_mem[UNITS ? 4 * 128 : 1], unit_mem[UNITS ? kSlots : 1];
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     Gates *gates = reinterpret_cast<Gates *>(sm + SM::GATES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -121,15 +120,18 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             const uint32_t par = i & 1;
             float dmost = 0.f;
             if constexpr (UNITS) {
-                if (i < chunks) {  // the largest of d, a 32-byte share of the tile to a thread
+                if (i < chunks) {  // the largest of exp(G) d, eight rows of two neighbouring tokens to a thread
+                    const Gates &gt = gates[i % kSlots];
+                    wait.on(kFullOp + par, (i >> 1) & 1);
                     wait.on(kFullV + i % kVStages, (i / kVStages) & 1);
                     const uint4 *at = reinterpret_cast<const uint4 *>(sm + SM::DY + (i % kVStages) * SM::DY_BYTES) + 2 * tid;
                     const uint4 a = at[0], e = at[1];
                     const uint32_t dw[8] = {a.x, a.y, a.z, a.w, e.x, e.y, e.z, e.w};
-                    __half2 most = __float2half2_rn(0.f);
+                    __half2 most[2] = {__float2half2_rn(0.f), __float2half2_rn(0.f)};
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) most = larger_of_halves(most, dw[m]);
-                    dmost = fabsf(p.scale) * larger_half(most);
+                    for (int m = 0; m < 8; ++m) most[m >> 2] = larger_of_halves(most[m >> 2], dw[m]);
+                    const float2 into = *reinterpret_cast<const float2 *>(&gt.into[8 * (tid >> 6) + ((2 * tid) & 7)]);
+                    dmost = finite_or_zero(fabsf(p.scale) * fmaxf(into.x * larger_half(most[0]), into.y * larger_half(most[1])));
                 }
             }
             if (i > 0) {
@@ -165,49 +167,63 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             const int c = chunks - 1 - i;
             const Gates &gt = gates[i % kSlots];
             wait.on(kFullOp + par, (i >> 1) & 1);  // the gates
-            float unit = 1.f;
+            float r_up = 1.f, d_up = 1.f, ds_up = 1.f;  // what R, D, and what is summed onto D are held times
             if constexpr (UNITS) {
-                // Of D and d; where M^T d and D are far below d (short queries), up to what d leaves room for
-                float v[16], most = 0.f;
+                float v[16], most = 0.f, wmost = 0.f, x = largest(D);
                 wait.on(kX2, par);
                 tc::fence_after_sync();
                 tc::tmem_ld16(x2, v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(v[e]));
-                most = warp_largest(fmaxf(finite_or_zero(most * fabsf(p.scale) * gt.m_unit), largest(D)));
-                dmost = warp_largest(dmost);
-                if (lane == 0) most_mem[warp] = make_float2(most, dmost);
+                for (int e = 0; e < 16; ++e) {
+                    most = fmaxf(most, fabsf(v[e]));
+                    wmost = fmaxf(wmost, gt.into[16 * part + e] * fabsf(v[e]));
+                }
+                const float by = fabsf(p.scale) * gt.m_unit;
+                most = warp_largest(fmaxf(finite_or_zero(most * by), finite_or_zero(x * gt.k_len4)));
+                wmost = warp_largest(fmaxf(fmaxf(finite_or_zero(wmost * by), finite_or_zero(gt.over * x * gt.k_len4)), dmost));
+                x = warp_largest(x);
+                if (lane == 0) most_mem[warp] = most, most_mem[kChainWarps + warp] = wmost, most_mem[2 * kChainWarps + warp] = x;
                 __syncwarp();
                 tc::named_barrier(1, kChainWarps * 32);
-#pragma unroll
-                for (int e = 0; e < kChainWarps; ++e) most = fmaxf(most, most_mem[e].x), dmost = fmaxf(dmost, most_mem[e].y);
-                unit = fmaxf(to_unit(fmaxf(most, dmost)), fminf(to_unit(most), to_unit(dmost) * kUp));
-                down = inverse_power(unit);
+                const float *at = most_mem + (lane & 15);
+                r_up = to_unit(warp_largest(at[0])) * room(gt), ds_up = to_unit(warp_largest(at[kChainWarps])) * room(gt), d_up = to_unit(warp_largest(at[2 * kChainWarps])) * kUp;
+                down = inverse_power(ds_up);
                 if (tid == 0) {
-                    unit_mem[i % kSlots] = unit;
-                    p.units[(((size_t)bh * p.nc + c) * tiles + p0 / 128) * 2 + 1] = unit;
+                    unit_mem[i % kSlots] = ds_up;
+                    *reinterpret_cast<float2 *>(p.units + (((size_t)bh * p.nc + c) * tiles + p0 / 128) * 4 + 2) = make_float2(d_up, r_up);
                     tc::mbar_arrive(bars + 8 * kUnit);
                 }
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < CW / 16; ++j) send(j, unit * kUp);
+                for (int j = 0; j < CW / 16; ++j) send(j, d_up);
             }
             wait.on(kD1, par);
             tc::fence_after_sync();
-            float v[16];
+            float v[16], of_row = 1.f;  // (fp16) what of a row's R comes out of the product
             {
                 float u[16];
                 uint32_t hi[8], lo[8];
                 tc::tmem_ld16x2(x1, x2, v, u);
-                const float2 s2 = dup(UNITS ? p.scale * gt.m_unit * unit : p.scale);
+                const float2 s2 = dup(UNITS ? p.scale * gt.m_unit : p.scale);
+                const float d_down = UNITS ? inverse_power(d_up) : 1.f;
+                float2 du[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float4 f = *reinterpret_cast<const float4 *>(&gt.out[16 * part + 4 * e]);
-                    if (UNITS) f.x *= kDown, f.y *= kDown, f.z *= kDown, f.w *= kDown;
-                    split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e], u[4 * e + 1]), __fmul2_rn(make_float2(v[4 * e], v[4 * e + 1]), make_float2(f.x, f.y))), hi[2 * e], lo[2 * e]);
-                    split2<BF16>(__ffma2_rn(s2, make_float2(u[4 * e + 2], u[4 * e + 3]), __fmul2_rn(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(f.z, f.w))),
-                                 hi[2 * e + 1], lo[2 * e + 1]);
+                    if (UNITS) f.x *= d_down, f.y *= d_down, f.z *= d_down, f.w *= d_down;
+                    du[2 * e] = __ffma2_rn(s2, make_float2(u[4 * e], u[4 * e + 1]), __fmul2_rn(make_float2(v[4 * e], v[4 * e + 1]), make_float2(f.x, f.y)));
+                    du[2 * e + 1] = __ffma2_rn(s2, make_float2(u[4 * e + 2], u[4 * e + 3]), __fmul2_rn(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(f.z, f.w)));
                 }
+                float up = 1.f;
+                if constexpr (UNITS) {
+                    row_mem[part * 128 + row] = largest(du);
+                    __syncwarp();
+                    tc::named_barrier(2 + quarter, 128);
+                    up = to_unit(fmaxf(fmaxf(row_mem[row], row_mem[128 + row]), fmaxf(row_mem[256 + row], row_mem[384 + row]))) * kUp;
+                    of_row = inverse_power(up) * gt.t_unit;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split2<BF16>(UNITS ? __fmul2_rn(dup(up), du[e]) : du[e], hi[e], lo[e]);
                 tc::tmem_st8(x1, hi);
                 tc::tmem_st8(x1 + 8, lo);
             }
@@ -219,9 +235,12 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
             tc::tmem_ld16(x3, v);
             {
                 uint32_t hi[8], lo[8];
+                const float by = UNITS ? ds_up * of_row : 1.f;
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
-                    const float4 b4 = *reinterpret_cast<const float4 *>(&gt.beta[16 * part + e]), n4 = *reinterpret_cast<const float4 *>(&gt.neg_into[16 * part + e]);
+                    float4 b4 = *reinterpret_cast<const float4 *>(&gt.beta[16 * part + e]);
+                    if (UNITS) b4.x *= by, b4.y *= by, b4.z *= by, b4.w *= by;
+                    const float4 n4 = *reinterpret_cast<const float4 *>(&gt.neg_into[16 * part + e]);
                     split2<BF16>(__fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(b4.x * n4.x, b4.y * n4.y)), hi[e / 2], lo[e / 2]);
                     split2<BF16>(__fmul2_rn(make_float2(v[e + 2], v[e + 3]), make_float2(b4.z * n4.z, b4.w * n4.w)), hi[e / 2 + 1], lo[e / 2 + 1]);
                 }
@@ -236,14 +255,18 @@ __device__ __forceinline__ void adjoint(const DeltaParams &p, int block) {
                 const int t = c * kC + 16 * part;
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) split2<BF16>(make_float2(v[2 * e] + bad, v[2 * e + 1] + bad), hi[e], lo[e]);
+                for (int e = 0; e < 16; ++e) v[e] = UNITS ? v[e] * of_row : v[e];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 r = make_float2(v[2 * e] + bad, v[2 * e + 1] + bad);
+                    split2<BF16>(UNITS ? __fmul2_rn(dup(r_up), r) : r, hi[e], lo[e]);
+                }
                 store_op(token_op(p.dr, (size_t)bh * p.nc + c, tiles, p0 + row) + 2 * part * 128, hi, lo, 1024);
                 uint16_t *to = dv + (size_t)t * step;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const float2 beta = *reinterpret_cast<const float2 *>(&gt.beta[16 * part + e]);
-                    const float2 r = UNITS ? make_float2(down * v[e], down * v[e + 1]) : make_float2(v[e], v[e + 1]);
-                    const uint32_t two = exchange_rows<BF16>(beta.x * r.x + bad, beta.y * r.y + bad, odd);
+                    const uint32_t two = exchange_rows<BF16>(beta.x * v[e] + bad, beta.y * v[e + 1] + bad, odd);
                     if (ok && t + e + odd < len) *reinterpret_cast<uint32_t *>(to + e * step) = two;
                 }
             }

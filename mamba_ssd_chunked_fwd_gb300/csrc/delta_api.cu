@@ -94,7 +94,7 @@ DeltaBwdLayout delta_bwd_layout(ssd::DeltaParams &p, int32_t dtype) {
     l.dkh = l.dqh + share;
     l.ops = l.dkh + share;
     l.units = l.ops + (p.chunked ? align_up(chunks * ssd::delta_op_bytes(true)) : 0);
-    l.total = l.units + (p.chunked && dtype == SSD_F16 ? align_up(chunks * (P / 128) * 2 * f) : 0);
+    l.total = l.units + (p.chunked && dtype == SSD_F16 ? align_up(chunks * (P / 128) * 4 * f) : 0);
     return l;
 }
 

@@ -14,7 +14,7 @@
 //
 // [4,2048] with 16 heads of 128 x 128, bf16 (2048 chunks): 183 us, 2.9 TB/s of operands read.  A chunk's 22000 cycles are products
 // 7000 (both operands from shared memory: 56 cycles each), waits for S and D 3000, Y and Z 3000, sums over N 2600, second
-// products and stores 3500; with 16 warps in place of 8 the same.  In fp16, Y and Z made twice, once for their largest, 200 us.  TMEM is full, so that two chunks do not overlap.
+// products and stores 3500; with 16 warps in place of 8 the same.  In fp16, Y and Z made twice, once for their largest, 203 us.  TMEM is full, so that two chunks do not overlap.
 //
 // Y and Z lie in shared memory once: read along j they are an operand, read along i its transpose.
 // A CTA takes one chunk of one head after another; while its warps finish one, the next one's tiles are copied:
@@ -77,8 +77,8 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ptiles = (p.P + 127) / 128, steps = ptiles * 4, units = p.B * p.H * p.nc;
-    // fp16: the operands come times powers of two, one for S and U, one for D and R, of each 128 rows of P (delta_tc.cuh).  Where those of
-    // several differ, what has the larger one is brought down in place
+    // fp16: the operands come times powers of two, of each 128 rows of P (delta_tc.cuh).  Where those of several differ, what has
+    // the larger one is brought down in place
     constexpr bool UNITS = !BF16;
     const bool level = UNITS && ptiles > 1;
 
@@ -134,12 +134,12 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             const uint32_t par = n_unit & 1;
             const unsigned char *kq = sm + SM::KQ + (n_unit & 1) * SM::KQ_BYTES;
             const Gates &gt = *reinterpret_cast<const Gates *>(sm + SM::GATES + (n_unit & 1) * sizeof(Gates));
-            float s_unit = 1.f, d_unit = 1.f;
+            float4 held = make_float4(1.f, 1.f, 1.f, 1.f);  // what S, U, D and R are held times
             if constexpr (UNITS) {
-                s_unit = d_unit = INFINITY;
-                for (int m = 0; m < ptiles; ++m) {
-                    const float2 two = __ldg(reinterpret_cast<const float2 *>(p.units) + (size_t)unit * ptiles + m);
-                    s_unit = fminf(s_unit, two.x), d_unit = fminf(d_unit, two.y);
+                held = __ldg(reinterpret_cast<const float4 *>(p.units) + (size_t)unit * ptiles);
+                for (int m = 1; m < ptiles; ++m) {
+                    const float4 x = __ldg(reinterpret_cast<const float4 *>(p.units) + (size_t)unit * ptiles + m);
+                    held = make_float4(fminf(held.x, x.x), fminf(held.y, x.y), fminf(held.z, x.z), fminf(held.w, x.w));
                 }
             }
             // <S, D>, as the tiles pass
@@ -151,9 +151,9 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                 unsigned char *st = sm + at * SM::STAGE;
                 if constexpr (UNITS) {
                     if (level) {
-                        const float2 two = __ldg(reinterpret_cast<const float2 *>(p.units) + (size_t)unit * ptiles + s / 4);
-                        const __half2 fs = __float2half2_rn(s_unit * inverse_power(two.x)), fd = __float2half2_rn(d_unit * inverse_power(two.y));
-                        auto bring = [&](uint32_t from, uint32_t bytes, __half2 f) {
+                        const float4 own = __ldg(reinterpret_cast<const float4 *>(p.units) + (size_t)unit * ptiles + s / 4);
+                        auto bring = [&](uint32_t from, uint32_t bytes, float to, float was) {
+                            const __half2 f = __float2half2_rn(to * inverse_power(was));
                             for (uint32_t e = 16 * tid; e < bytes; e += 16 * kMathWarps * 32) {
                                 uint4 v = *reinterpret_cast<const uint4 *>(st + from + e);
                                 uint32_t *x = reinterpret_cast<uint32_t *>(&v);
@@ -165,7 +165,8 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
                                 *reinterpret_cast<uint4 *>(st + from + e) = v;
                             }
                         };
-                        bring(SM::S, SM::ST, fs), bring(SM::D, SM::ST, fd), bring(SM::U, SM::UT, fs), bring(SM::R, SM::UT, fd);
+                        bring(SM::S, SM::ST, held.x, own.x), bring(SM::U, SM::UT, held.y, own.y);
+                        bring(SM::D, SM::ST, held.z, own.z), bring(SM::R, SM::UT, held.w, own.w);
                         tc::fence_smem_to_async();
                         tc::mbar_arrive(bars + 8 * (kScaled + at));
                         __syncwarp();
@@ -193,9 +194,9 @@ delta_grad_tc_kernel(const __grid_constant__ DeltaParams p) {
             wait.on(kFullKQ + (n_unit & 1), (n_unit >> 1) & 1);  // the gates
             wait.on(kX, par);
             tc::fence_after_sync();
-            // what the sums over P carry: of S, U (in units of t_unit), R, D
-            const float of_s = UNITS ? inverse_power(s_unit) * kDown : 1.f, of_u = UNITS ? inverse_power(s_unit) * gt.t_unit : 1.f;
-            const float of_r = UNITS ? inverse_power(d_unit) : 1.f, of_d = UNITS ? of_r * kDown : 1.f;
+            // what the sums over P carry: of S, U (over the largest beta), R, D
+            const float of_s = inverse_power(held.x), of_u = UNITS ? inverse_power(held.y) * beta_unit(gt, lane) : 1.f, of_d = inverse_power(held.z),
+                        of_r = inverse_power(held.w);
             // 16 tokens i of row j of Y and Z, and what dbeta takes off before beta and k . k
             auto make_yz = [&](int j, int i, float gh, float gl, float(&y)[16], float(&z)[16], float(&wx)[16]) {
 #pragma unroll

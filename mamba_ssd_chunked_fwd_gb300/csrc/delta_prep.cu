@@ -6,7 +6,8 @@
 //
 // The products of k and q with k are one product of 128 rows on the tensor cores.  The diagonal
 // blocks of 16 of T are inverted by substitution in fp32, the blocks below by
-// T_ij = -T_ii sum_k A_ik T_kj with mma.sync on operands of two terms: blocks this small would leave
+// T_ij = -T_ii sum_k A_ik T_kj with mma.sync on operands of two terms (bf16, or tf32 for fp16 tensors, whose range does not hold
+// decays): blocks this small would leave
 // tcgen05's 128 rows empty, and each needs the one before it.  No power of A is formed:
 // with keys alike those would cancel.
 //
@@ -16,7 +17,7 @@
 // took 278 us as one kernel and take 347 as two, though the walk alone went from 278 to 213 (a third less code
 // for the instruction cache).  Both forms side by side are not built.
 //
-// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 132 us (fp16, M looked at twice, 140), with T for the gradients 42 us for 2048 of them.  No pipe is
+// [4,4096] with 32 heads of 128 x 128, bf16 (8192 chunks): 132 us (fp16, M looked at twice and T's blocks in tf32, 150), with T for the gradients 42 us for 2048 of them.  No pipe is
 // above 25 %; bound by latency (barriers, the loads, the blocks of T's first column one after another).  With k and q
 // whole and T in shared memory, six CTAs to an SM: 140 and 50 us.
 #include "delta_tc.cuh"
@@ -84,7 +85,7 @@ __device__ __forceinline__ void make_gates(Gates &gt, const float (&graw)[2], co
         gt.out[t] = nan0 | nan1 ? nan : ex2(rest.x + rest.y);
     }
     const float2 all = parts(end);
-    if (lane == 0) gt.over = nan0 | nan1 ? nan : ex2(all.x + all.y), gt.t_unit = gt.m_unit = 1.f;
+    if (lane == 0) gt.over = nan0 | nan1 ? nan : ex2(all.x + all.y), gt.t_unit = gt.m_unit = gt.k_len4 = 1.f;
 }
 
 // 16 columns from j0 on of a row of products, each times its decay and the row's factor; zero from column `limit` on.
@@ -142,6 +143,49 @@ __device__ __forceinline__ void times_transposed(float (&acc)[2][4], const Frag 
     }
 }
 
+// The same in fp16's preparation, with two tf32 terms: A and T hold decays, which fp16 loses.  Slot t of the eight columns stands for
+// column 2 t, slot t + 4 for 2 t + 1, in both operands, so that an accumulated block is an operand as it lies.
+__device__ __forceinline__ uint32_t tf32_of(float v) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void mma_16x8x8(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc += a X^T; `a` as it is accumulated: a[half][..], columns 8 half + 2 t + (0, 1) of rows g (0, 1) and g + 8 (2, 3).
+__device__ __forceinline__ void times_transposed(float (&acc)[2][4], const float (&a)[2][4], const float *x, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v = a[k][(e & 1) * 2 + (e >> 1)];
+            ah[e] = tf32_of(v), al[e] = tf32_of(v - __uint_as_float(ah[e]));
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float2 b = *reinterpret_cast<const float2 *>(x + (8 * half + g) * kAW + 2 * t + 8 * k);
+            const uint32_t bh[2] = {tf32_of(b.x), tf32_of(b.y)};
+            const uint32_t bl[2] = {tf32_of(b.x - __uint_as_float(bh[0])), tf32_of(b.y - __uint_as_float(bh[1]))};
+            mma_16x8x8(acc[half], al, bh);
+            mma_16x8x8(acc[half], ah, bl);
+            mma_16x8x8(acc[half], ah, bh);
+        }
+    }
+}
+// A block in shared memory as an accumulated one.
+__device__ __forceinline__ void load_block(float (&a)[2][4], const float *x, int lane) {
+    const float *at = x + (lane >> 2) * kAW + 2 * (lane & 3);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const float2 v = *reinterpret_cast<const float2 *>(at + (m & 1) * 8 * kAW + (m >> 1) * 8);
+        a[m >> 1][2 * (m & 1)] = v.x, a[m >> 1][2 * (m & 1) + 1] = v.y;
+    }
+}
+
 // An 8 x 8 block of a product's result, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t r;
@@ -165,7 +209,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bar_mem;
     __shared__ uint32_t tmem_slot;
-    __shared__ float m_most[2];  // (fp16) the largest of M, by warps
+    __shared__ float m_most[2], k_most[2], t_most[4];  // (fp16) the largest of M, of a key's length squared, of T, by warps
     const uint32_t sbase = tc::smem_addr(sm);
     Gates &gt = *reinterpret_cast<Gates *>(sm + kGates);
     float *A = reinterpret_cast<float *>(sm + kA);
@@ -207,13 +251,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         cp_commit();
     };
     load(0);
-    if (pw == 0) {
-        make_gates(gt, graw, braw, lane);
-        if constexpr (!BF16) {
-            const float most = warp_largest(fmaxf(finite_or_zero(fabsf(braw[0])), finite_or_zero(fabsf(braw[1]))));
-            if (lane == 0) gt.t_unit = __uint_as_float(min(max(__float_as_uint(most) >> 23, 67u), 187u) << 23);  // 2^-60 .. 2^60
-        }
-    }
+    if (pw == 0) make_gates(gt, graw, braw, lane);
     Waits wait{tc::smem_addr(&bar_mem)};
     uint32_t tmem = 0;
 #pragma unroll 1
@@ -242,7 +280,7 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
         const int i = tid & 63, last = i | 31;  // of the warp's rows
         const float gh = gt.gh[i], gl = gt.gl[i], factor = pw < 2 ? gt.beta[i] : 1.f;
         const int limit = pw < 2 ? i : i + 1;
-        float up = 1.f;
+        float up = 1.f, length = 0.f;
         if constexpr (!BF16) {
             if (pw >= 2) {  // the largest of M first
                 float most = 0.f;
@@ -274,6 +312,10 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
                 continue;
             }
             tc::tmem_ld16(tl + j0, v);
+            if constexpr (!BF16) {
+#pragma unroll
+                for (int m = 0; m < 16; ++m) length = j0 + m == i ? v[m] : length;
+            }
             decayed(v, gt, j0, gh, gl, BF16 || pw < 2 ? factor : up, limit);
             if (pw < 2) {
 #pragma unroll
@@ -288,7 +330,13 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
                 to[kOpTerm / 16 + 64] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
             }
         }
+        if constexpr (!BF16) {
+            __syncwarp();
+            length = warp_largest(finite_or_zero(length));
+            if (pw < 2 && lane == 0) k_most[pw] = length;
+        }
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -321,25 +369,34 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
     // column pw of blocks, transposed: element (c, r) of a block is T[r][c]
     {
         const int g = lane >> 2, t = lane & 3;
-        const float unit = BF16 ? 1.f : inverse_power(gt.t_unit), b0 = unit * gt.beta[16 * pw + g], b1 = unit * gt.beta[16 * pw + g + 8];
+        const float unit = BF16 ? 1.f : inverse_power(beta_unit(gt, lane)), b0 = unit * gt.beta[16 * pw + g], b1 = unit * gt.beta[16 * pw + g + 8];
+        float up = BF16 ? 1.f : kT, most = 0.f;
         // of a 16 x 16 block of T four blocks of 8 x 8, one after another along its columns, 128 bytes a warp
         auto put = [&](uint32_t op, int bi, const uint32_t(&v)[4]) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) *reinterpret_cast<uint32_t *>(dst + op + ((2 * pw + (m & 1)) * 8 + (m >> 1) + 2 * bi) * 128 + 4 * lane) = transposed(v[m]);
         };
-        auto store = [&](const float(&acc)[2][4], int bi) {  // T diag(beta) in two terms
+        auto store = [&](float(&acc)[2][4], int bi) {  // T diag(beta) in two terms
             uint32_t hi[4], lo[4];
+            if constexpr (!BF16) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) most = fmaxf(most, fabsf(acc[m >> 2][m & 3]));
+            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const float b = m & 1 ? b1 : b0;
+                const float b = BF16 ? (m & 1 ? b1 : b0) : up * (m & 1 ? b1 : b0);
                 split2<BF16>(make_float2(b * acc[m >> 1][2 * (m & 1)], b * acc[m >> 1][2 * (m & 1) + 1]), hi[m], lo[m]);
             }
             put(kOpT, bi, hi);
             put(kOpT + kOpTerm, bi, lo);
             if (PURE) {
-                const Frag f = to_frag<BF16>(acc);
-                put(kOpPure, bi, f.hi);
-                put(kOpPure + kOpTerm, bi, f.lo);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 v = make_float2(acc[m >> 1][2 * (m & 1)], acc[m >> 1][2 * (m & 1) + 1]);
+                    split2<BF16>(BF16 ? v : __fmul2_rn(dup(up), v), hi[m], lo[m]);
+                }
+                put(kOpPure, bi, hi);
+                put(kOpPure + kOpTerm, bi, lo);
             }
         };
         // element (c, r) of block (pw, k) of the buffer, above its diagonal, will be T[r][c] of T's block (k, pw)
@@ -350,31 +407,65 @@ delta_prep_kernel(const __grid_constant__ DeltaParams p) {
             put(kOpT, bi, none), put(kOpT + kOpTerm, bi, none);
             if (PURE) put(kOpPure, bi, none), put(kOpPure + kOpTerm, bi, none);
         }
-        float acc[2][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][e] = D[(8 * m + 2 * t + (e & 1)) * kAW + g + 8 * (e >> 1)];
-        store(acc, pw);
-        const Frag first = to_frag<BF16>(acc);
 #pragma unroll 1
-        for (int bi = pw + 1; bi < 4; ++bi) {
-            float sum[2][4] = {};
-            times_transposed<BF16>(sum, first, A + 16 * bi * kAW + 16 * pw, lane);
-#pragma unroll 1
-            for (int k = pw + 1; k < bi; ++k) times_transposed<BF16>(sum, load_frag<BF16>(mine + 16 * k, lane), A + 16 * bi * kAW + 16 * k, lane);
+        for (;;) {
+            float acc[2][4];
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[m][e] = -sum[m][e], acc[m][e] = 0.f;
-            times_transposed<BF16>(acc, to_frag<BF16>(sum), A + 16 * bi * kAW + 16 * bi, lane);
-            store(acc, bi);
-            if (bi < 3) {
+                for (int e = 0; e < 4; ++e) acc[m][e] = D[(8 * m + 2 * t + (e & 1)) * kAW + g + 8 * (e >> 1)];
+            store(acc, pw);
+            float first[2][4];
+            Frag first_frag;
+            if constexpr (BF16) first_frag = to_frag<BF16>(acc);
+            else
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    *reinterpret_cast<float2 *>(mine + 16 * bi + (g + 8 * (m & 1)) * kAW + 2 * t + 8 * (m >> 1)) =
-                        make_float2(acc[m >> 1][2 * (m & 1)], acc[m >> 1][2 * (m & 1) + 1]);
-                __syncwarp();
+                for (int m = 0; m < 8; ++m) first[m >> 2][m & 3] = acc[m >> 2][m & 3];
+#pragma unroll 1
+            for (int bi = pw + 1; bi < 4; ++bi) {
+                float sum[2][4] = {};
+                if constexpr (BF16) {
+                    times_transposed<BF16>(sum, first_frag, A + 16 * bi * kAW + 16 * pw, lane);
+#pragma unroll 1
+                    for (int k = pw + 1; k < bi; ++k) times_transposed<BF16>(sum, load_frag<BF16>(mine + 16 * k, lane), A + 16 * bi * kAW + 16 * k, lane);
+                } else {
+                    times_transposed(sum, first, A + 16 * bi * kAW + 16 * pw, lane);
+#pragma unroll 1
+                    for (int k = pw + 1; k < bi; ++k) {
+                        float block[2][4];
+                        load_block(block, mine + 16 * k, lane);
+                        times_transposed(sum, block, A + 16 * bi * kAW + 16 * k, lane);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[m][e] = -sum[m][e], acc[m][e] = 0.f;
+                if constexpr (BF16) times_transposed<BF16>(acc, to_frag<BF16>(sum), A + 16 * bi * kAW + 16 * bi, lane);
+                else times_transposed(acc, sum, A + 16 * bi * kAW + 16 * bi, lane);
+                store(acc, bi);
+                if (bi < 3) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        *reinterpret_cast<float2 *>(mine + 16 * bi + (g + 8 * (m & 1)) * kAW + 2 * t + 8 * (m >> 1)) =
+                            make_float2(acc[m >> 1][2 * (m & 1)], acc[m >> 1][2 * (m & 1) + 1]);
+                    __syncwarp();
+                }
+            }
+            if constexpr (BF16) break;
+            // steps that expand (beta |k|^2 > 2) may leave T above 8: once more, by its largest
+            most = warp_largest(most);
+            if (lane == 0) t_most[pw] = most;
+            __syncthreads();
+            most = fmaxf(fmaxf(t_most[0], t_most[1]), fmaxf(t_most[2], t_most[3]));
+            if (!(most * up > 65504.f) || most > 3e38f || up < kT) break;
+            up = to_unit(most) * kUp;
+            __syncthreads();
+        }
+        if constexpr (!BF16) {
+            if (tid == 0) {
+                gt.t_unit = inverse_power(up);
+                gt.k_len4 = 4.f * sqrtf(fmaxf(k_most[0], k_most[1]));
             }
         }
     }

@@ -11,10 +11,10 @@ namespace ssd {
 constexpr int kC = kDeltaChunk;
 
 // A chunk's gates.  With G the running sum of g: gh + gl = G log2(e), into = exp(G), out = exp(G_end - G),
-// over = exp(G_end).  t_unit, m_unit (fp16): powers of two, what T diag(beta) and M were divided by.
+// over = exp(G_end).  For fp16: the powers of two that T and M were divided by; four times the longest key.
 struct alignas(16) Gates {
     float gh[kC], gl[kC], beta[kC], into[kC], neg_into[kC], out[kC];
-    float over, t_unit, m_unit;
+    float over, t_unit, m_unit, k_len4;
 };
 
 // What delta_prep.cu leaves of every chunk of every head: T diag(beta) and M, both 64 x 64 in blocks of 8 rows x 16
@@ -38,16 +38,24 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo) {
 
 // Two terms of bf16 have fp32's range; two of fp16 hold a value to 2^-22 of itself only between 2^-3 and 2^16, below that to
 // 2^-25 whatever its size.  So in fp16 every operand that is computed is first multiplied by a power of two that
-// comes from the largest magnitude around it, which is taken out again where the product's fp32 sums are read:
+// comes from the largest magnitude around it, which is taken out again where the product's fp32 sums are read.  `Row`: taken of a row
+// of the state (for the gradients, whose sums run over the rows, of a CTA's); `chunk`: of all of it.
 //
-//     S, D           to [2^13, 2^14): the largest of a row (the walk for y), or of a CTA's rows (the gradients')
-//     v, U, d, R     by 2^-12 of that, with v (or d) among those that the largest is taken of
-//     T diag(beta)   the largest beta to [1, 2)
-//     M              its largest to [2^13, 2^14), never down
-//     Y, Z           their largest to [2^12, 2^13)
+//     S            its largest to [2^13, 2^14)                                              row
+//     v, exp(G) S k^T, U over beta       the larger of v and exp(G) S |k| to [2^6, 2^7)                     row
+//     exp(G_end - G) U                   the larger of exp(G_end - G) beta v and exp(G_end) S |k| to [2^6, 2^7)   row
+//     D            its largest to [2^13, 2^14)                                              the CTA's rows
+//     dU           its largest to [2^13, 2^14)                                              always a row
+//     exp(G) d, beta exp(G) R            the largest of exp(G) d, exp(G) M^T d and exp(G_end) D |k| to [2^6, 2^7)   the CTA's rows
+//     R            the larger of M^T d and D |k| to [2^6, 2^7)                             the CTA's rows
+//     T, T diag(beta)                    by 2^13 (or, of expanding steps, its largest to [2^13, 2^14)), and beta by its largest   chunk
+//     M            its largest to [2^13, 2^14), never down                                  chunk
+//     Y, Z         their largest to [2^12, 2^13)                                            chunk
 //
-// Values far smaller than the largest keep 2^-38 of it (S, D, M, Y, Z) or 2^-26 (U, R).
-constexpr float kUp = 4096.f, kDown = 1.f / 4096.f;
+// with |k| four times the longest key.  Those to [2^6, 2^7) are bounds of single terms: 2^9 is left for what T makes of 64 of them (each
+// at most beta |k_i| |k_j| while steps do not expand; less of it is used by as much as T is beyond 8).  What is far smaller than the
+// largest keeps 2^-31 of that bound, and 2^-38 where the largest itself is known.
+constexpr float kUp = 4096.f, kT = 8192.f;
 __device__ __forceinline__ float inverse_power(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 // The power of two that takes a magnitude to [2, 4), 2^100 at most.
 __device__ __forceinline__ float to_unit(float most) { return __uint_as_float((255u - min(max(__float_as_uint(most) >> 23, 30u), 252u)) << 23); }
@@ -65,21 +73,39 @@ __device__ __forceinline__ __half2 larger_of_halves(__half2 most, uint32_t w) {
     const __half2 h = *reinterpret_cast<const __half2 *>(&w);
     return __hmax2(most, __hfma2(h, __float2half2_rn(0.f), __habs2(h)));
 }
-// Of eight rows, a token's (two) to a lane: the largest of rows 2 i and 2 i + 1, i = lane / 8, over the warp's tokens.
-__device__ __forceinline__ float2 largest_of_rows(const uint4 &a, const uint4 &b, int lane) {
-    const __half2 none = __float2half2_rn(0.f);
-    const __half2 v0 = larger_of_halves(larger_of_halves(none, a.x), b.x), v1 = larger_of_halves(larger_of_halves(none, a.y), b.y),
-                  v2 = larger_of_halves(larger_of_halves(none, a.z), b.z), v3 = larger_of_halves(larger_of_halves(none, a.w), b.w);
-    const bool up = lane & 16, odd = lane & 8;
-    auto swap = [](__half2 v, int bit) { return __shfl_xor_sync(0xffffffffu, v, bit); };
-    const __half2 w0 = __hmax2(up ? v2 : v0, swap(up ? v0 : v2, 16)), w1 = __hmax2(up ? v3 : v1, swap(up ? v1 : v3, 16));
-    __half2 m = __hmax2(odd ? w1 : w0, swap(odd ? w0 : w1, 8));
+// Of eight rows, two tokens of them to a lane with the factors fa and fb: the largest of row lane / 4 over the warp's tokens, and
+// with the factors.
+__device__ __forceinline__ float2 largest_of_rows(const uint4 &a, const uint4 &b, float fa, float fb, int lane) {
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    float2 v[8];
 #pragma unroll
-    for (int bit = 4; bit >= 1; bit >>= 1) m = __hmax2(m, swap(m, bit));
-    return __half22float2(m);
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = __half22float2(larger_of_halves(__float2half2_rn(0.f), aw[i])), y = __half22float2(larger_of_halves(__float2half2_rn(0.f), bw[i]));
+        v[2 * i] = make_float2(fmaxf(x.x, y.x), fmaxf(fa * x.x, fb * y.x));
+        v[2 * i + 1] = make_float2(fmaxf(x.y, y.y), fmaxf(fa * x.y, fb * y.y));
+    }
+    auto larger = [&](float2 p, float2 q, int bit) {
+        return make_float2(fmaxf(p.x, __shfl_xor_sync(0xffffffffu, q.x, bit)), fmaxf(p.y, __shfl_xor_sync(0xffffffffu, q.y, bit)));
+    };
+#pragma unroll
+    for (int half = 4, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int m = 0; m < half; ++m) v[m] = larger(up ? v[m + half] : v[m], up ? v[m] : v[m + half], bit);
+    }
+    v[0] = larger(v[0], v[0], 2);
+    return larger(v[0], v[0], 1);
 }
 __device__ __forceinline__ float larger_half(__half2 v) { return fmaxf(__low2float(v), __high2float(v)); }
 __device__ __forceinline__ float warp_largest(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
+// The power of two that a chunk's beta are divided by, the largest one's; by a warp.
+__device__ __forceinline__ float beta_unit(const Gates &gt, int lane) {
+    const float most = warp_largest(fmaxf(finite_or_zero(fabsf(gt.beta[lane])), finite_or_zero(fabsf(gt.beta[lane + 32]))));
+    return __uint_as_float(min(max(__float_as_uint(most) >> 23, 67u), 187u) << 23);  // 2^-60 .. 2^60
+}
+
+// What a bound in [2, 4) is multiplied by: 2^5, less where T is beyond 8.
+__device__ __forceinline__ float room(const Gates &gt) { return inverse_power(gt.t_unit) * (32.f / kT); }
 
 // A thread's waits: each lasts 2000 tries of up to a millisecond; once one has given up, the rest return
 // at once.  Short code: five kinds of warps run side by side, and what they run has to stay in the

@@ -22,8 +22,9 @@
 // into a product as the sum of two 16-bit numbers, so that states keep 16 bits (bf16:
 // relative error 4e-6 of a state, measured; one term would give 3e-3) and y is off by
 // its own rounding alone.  In fp16 these terms hold values times powers of two (delta_tc.cuh), which the chain takes anew for
-// every chunk, of a row of the state with its v: its largest over four threads, and v written back scaled while S k^T
-// runs.  That and the state's columns leaving only once all are known make the walk 286 us for 213 in the case below.
+// every chunk, of a row of the state with its v: the state's largest over four threads, v's as the y warps have found it two
+// chunks ahead, and v written back scaled while S k^T runs.  That and the state's columns leaving only once all are known make
+// the walk 319 us for 213 in the case below (v's largest found by the chain's own warps: 344).
 //
 // Bound by the chain: 6300 cycles a chunk for three products and three round trips through registers, with the
 // tensor pipe busy 41 % of them.  [4,4096] with 32 heads of 128 x 128, bf16: 213 us, 807 TFLOP/s of the products as formed.
@@ -52,7 +53,7 @@ struct Smem {
 
 enum Bar { kFullKQ = 0, kEmptyKQ = kFullKQ + kStages, kFullV = kEmptyKQ + kStages, kEmptyV = kFullV + kVStages, kFullOp = kEmptyV + kVStages,
            kEmptyOp = kFullOp + kOps, kD3 = kEmptyOp + kOps, kD3Read = kD3 + 2, kD4 = kD3Read + 2, kD4Read = kD4 + 2, kD1 = kD4Read + 2, kD2, kDS, kUOut, kS,
-           kR = kS + 2, kU = kR + 4, kVUnit = kU + 4, kDrain, kBars };
+           kR = kS + 2, kU = kR + 4, kVUnit = kU + 4, kVMost, kDrain = kVMost + 2, kBars };
 
 // TMEM columns.
 template <int NN>
@@ -79,8 +80,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
     // fp16: the state, v and what follows from them are held times a power of two for each row (for the gradients, whose sums
     // run over the rows, one for the CTA): delta_tc.cuh
     constexpr bool UNITS = !BF16;
-    __shared__ float most_mem[UNITS ? 4 * 128 : 1], down_mem[UNITS ? kSlots * 128 : 1];
-    __shared__ __align__(16) float vmost_mem[UNITS ? 128 : 4];  // written by pairs
+    __shared__ float most_mem[UNITS ? 4 * 128 : 1];
+    __shared__ float2 vmost_mem[UNITS ? kSlots * 128 : 1], row_mem[UNITS ? kSlots * 128 : 1], gate_mem[UNITS ? kSlots : 1];
     const uint32_t sbase = tc::smem_addr(sm), bars = tc::smem_addr(bar_mem);
     Gates *gates = reinterpret_cast<Gates *>(sm + SM::GATES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,7 +111,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
         init(kFullKQ, kStages, 64), init(kEmptyKQ, kStages, 1), init(kFullV, kVStages, 32), init(kEmptyV, kVStages, 1);
         init(kFullOp, kOps, 1), init(kEmptyOp, kOps, 1), init(kD3, 2, 1), init(kD3Read, 2, kOutWarps * 32);
         init(kD4, 2, 1), init(kD4Read, 2, kOutWarps * 32), init(kD1, 3, 1), init(kUOut, 1, kChainWarps * 32);
-        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kVUnit, 1, kChainWarps * 32), init(kDrain, 1, 1);
+        init(kS, 2, kChainWarps * 32), init(kR, 8, kChainWarps * 8), init(kVUnit, 1, kChainWarps * 32), init(kVMost, 2, kOutWarps * 32), init(kDrain, 1, 1);
         tc::mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -150,23 +151,13 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
 #pragma unroll 1
         for (int c = 0;; ++c) {
             const uint32_t par = c & 1;
-            uint4 vw[UNITS ? 2 : 1];
-            if constexpr (UNITS) {
-                if (c < w.chunks) {
-                    wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
-                    vw[0] = *reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES);
-                    vw[1] = *reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES + 4 * 2048);
-                    const float2 most = largest_of_rows(vw[0], vw[1], lane);
-                    if ((lane & 7) == 0) *reinterpret_cast<float2 *>(vmost_mem + 8 * group + (lane >> 2)) = most;
-                    __syncwarp();
-                }
-            }
+            if (UNITS && c < w.chunks) wait.on(kVMost + par, (c >> 1) & 1);
             if (c > 0) {
                 wait.on(kDS, par ^ 1);
                 tc::fence_after_sync();
             }
             const float2 over = dup(c > 0 ? gates[(c - 1) % kSlots].over : 1.f);
-            const float2 back = dup(UNITS && c > 0 ? down * gates[(c - 1) % kSlots].t_unit : 1.f);
+            const float2 back = dup(down);
             auto send = [&](int j, float up) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
@@ -195,33 +186,45 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 if (!UNITS && c < w.chunks) send(j, 1.f);
             }
             if (c >= w.chunks) break;
+            float s_up = 1.f, u_up = 1.f, ds_up = 1.f, b_unit = 1.f;  // what S, then v and U over beta, then U for the state are held times
             if constexpr (UNITS) {
+                const Gates &gt = gates[c % kSlots];
+                float2 v = vmost_mem[(c % kSlots) * 128 + row];
+                const float2 g2 = gate_mem[c % kSlots];  // the largest beta's power of two; what S |k| counts times beside v
+                b_unit = g2.x;
                 float most = largest(S);
                 if (MODE == STATES) {
-                    most = warp_largest(fmaxf(most, lane < 8 ? vmost_mem[8 * group + lane] : 0.f));
-                    if (lane == 0) most_mem[warp] = most;
+                    most = warp_largest(most), v = make_float2(warp_largest(v.x), warp_largest(v.y));
+                    if (lane == 0) most_mem[warp] = most, most_mem[16 + warp] = v.x, most_mem[32 + warp] = v.y;
                     __syncwarp();
                     tc::named_barrier(1, kChainWarps * 32);
-#pragma unroll
-                    for (int i = 0; i < kChainWarps; ++i) most = fmaxf(most, most_mem[i]);
+                    const float *x = most_mem + (lane & 15);
+                    most = warp_largest(x[0]), v = make_float2(warp_largest(x[16]), warp_largest(x[32]));
                 } else {
                     most_mem[part * 128 + row] = most;
                     __syncwarp();
                     tc::named_barrier(1 + quarter, 128);
-                    most = fmaxf(fmaxf(fmaxf(most_mem[row], most_mem[128 + row]), fmaxf(most_mem[256 + row], most_mem[384 + row])), vmost_mem[row]);
+                    most = fmaxf(fmaxf(most_mem[row], most_mem[128 + row]), fmaxf(most_mem[256 + row], most_mem[384 + row]));
                 }
-                const float unit = to_unit(most);
-                down = inverse_power(unit);
-                if (MODE == Y && part == 0) down_mem[(c % kSlots) * 128 + row] = down;
-                if (MODE == STATES && tid == 0) p.units[(((size_t)bh * p.nc + c) * ptiles + tile) * 2] = unit;
+                s_up = to_unit(most) * kUp;
+                u_up = to_unit(fmaxf(finite_or_zero(most * g2.y), v.x)) * room(gt);
+                ds_up = to_unit(fmaxf(finite_or_zero(v.y), finite_or_zero(most * gt.over * gt.k_len4))) * room(gt);
+                down = inverse_power(ds_up);
+                if (MODE == Y && part == 0)  // from S's scale to that of M U, and from there to y
+                    row_mem[(c % kSlots) * 128 + row] = make_float2(u_up * inverse_power(s_up) * inverse_power(b_unit) * inverse_power(gt.m_unit),
+                                                                    inverse_power(u_up) * b_unit * gt.m_unit);
+                if (MODE == STATES && tid == 0)
+                    *reinterpret_cast<float2 *>(p.units + (((size_t)bh * p.nc + c) * ptiles + tile) * 4) = make_float2(s_up, u_up);
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < CW / 16; ++j) send(j, unit * kUp);
+                for (int j = 0; j < CW / 16; ++j) send(j, s_up);
+                const uint4 vw[2] = {*reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES),
+                                     *reinterpret_cast<const uint4 *>(vat + (c % kVStages) * SM::V_BYTES + 4 * 2048)};
                 uint32_t two[8] = {vw[0].x, vw[0].y, vw[0].z, vw[0].w, vw[1].x, vw[1].y, vw[1].z, vw[1].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // the units of rows 2 i and 2 i + 1 of the eight lie with the lanes that have these rows
-                    const float2 by = MODE == STATES ? dup(unit) : make_float2(__shfl_sync(0xffffffffu, unit, 8 * part + 2 * i),
-                                                                               __shfl_sync(0xffffffffu, unit, 8 * part + 2 * i + 1));
+                    const float2 by = MODE == STATES ? dup(u_up) : make_float2(__shfl_sync(0xffffffffu, u_up, 8 * part + 2 * i),
+                                                                               __shfl_sync(0xffffffffu, u_up, 8 * part + 2 * i + 1));
 #pragma unroll
                     for (int m = i; m < 8; m += 4) {
                         const float2 f = __fmul2_rn(by, unpack2<BF16>(two[m]));
@@ -239,14 +242,18 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             tc::fence_after_sync();
             float v[16];
             tc::tmem_ld16(x1, v);
-            split_scaled<BF16>(v, &gt.neg_into[16 * part], x1, kDown);  // -exp(G) S k^T
+            split_scaled<BF16>(v, &gt.neg_into[16 * part], x1, UNITS ? u_up * inverse_power(s_up) : 1.f);  // -exp(G) S k^T
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kR + part));
             wait.on(kD2, par);
             tc::fence_after_sync();
             tc::tmem_ld16(x2, v);
-            split_scaled<BF16>(v, &gt.out[16 * part], x1);  // what U adds to the state
+            if constexpr (UNITS) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= gt.t_unit;
+            }
+            split_scaled<BF16>(v, &gt.out[16 * part], x1, UNITS ? ds_up * inverse_power(u_up) * b_unit : 1.f);  // what U adds to the state
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(bars + 8 * (kU + part));
@@ -282,7 +289,28 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
             }
         }
     } else if (warp < kMmaWarp) {
-        // ---- y: thread = row of the state
+        // ---- y: thread = row of the state.  In fp16 also, two chunks ahead, the largest of v in every row
+        auto look = [&](int c) {
+            const Gates &gt = gates[c % kSlots];
+            wait.on(kFullOp + (c & 1), (c >> 1) & 1);
+            wait.on(kFullV + c % kVStages, (c / kVStages) & 1);
+            const float fa = fabsf(gt.out[lane] * gt.beta[lane]), fb = fabsf(gt.out[lane + 32] * gt.beta[lane + 32]);
+            const unsigned char *at = sm + SM::V + (c % kVStages) * SM::V_BYTES + (lane >> 3) * 2048 + (lane & 7) * 16;
+#pragma unroll 1
+            for (int group = 4 * (warp - kOutWarp0); group < 4 * (warp - kOutWarp0) + 4; ++group) {
+                const float2 most = largest_of_rows(*reinterpret_cast<const uint4 *>(at + group * 128),
+                                                    *reinterpret_cast<const uint4 *>(at + group * 128 + 4 * 2048), fa, fb, lane);
+                if ((lane & 3) == 0) vmost_mem[(c % kSlots) * 128 + 8 * group + (lane >> 2)] = most;
+                __syncwarp();
+            }
+            const float into = warp_largest(fmaxf(finite_or_zero(gt.into[lane]), finite_or_zero(gt.into[lane + 32]))), b_unit = beta_unit(gt, lane);
+            if (warp == kOutWarp0 && lane == 0) gate_mem[c % kSlots] = make_float2(b_unit, gt.k_len4 * into);
+            __syncwarp();
+            if (!wait.dead()) tc::mbar_arrive(bars + 8 * (kVMost + (c & 1)));  // two: the chain may be two chunks behind
+        };
+        if constexpr (UNITS)
+#pragma unroll 1
+            for (int c = 0; c < (MODE == Y ? min(2, w.chunks) : w.chunks); ++c) look(c);
         if (MODE == Y) {
             const int quarter = warp - kOutWarp0, row = quarter * 32 + lane;
             const bool ok = row < rows;
@@ -296,7 +324,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 const Gates &gt = gates[c % kSlots];
                 wait.on(kD3 + o, par);
                 tc::fence_after_sync();
-                const float up = UNITS ? kDown * inverse_power(gt.m_unit) * inverse_power(gt.t_unit) : 1.f;  // from S's scale to that of M U
+                float up = 1.f;  // from S's scale to that of M U
+                if (UNITS) up = row_mem[(c % kSlots) * 128 + row].x;
 #pragma unroll 1
                 for (int j = 0; j < kC; j += 16) {  // diag(exp G) Q S^T, onto which M U is summed
                     float v[16];
@@ -318,7 +347,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 tc::fence_after_sync();
                 const int tc0 = w.t0 + c * kC, n = min(kC, w.t1 - tc0);
                 float scale = wait.dead() ? __int_as_float(0x7fffffff) : p.scale;
-                if (UNITS) scale *= down_mem[(c % kSlots) * 128 + row] * gt.t_unit * gt.m_unit;
+                if (UNITS) scale *= row_mem[(c % kSlots) * 128 + row].y;
                 uint16_t *to = y + (size_t)tc0 * step;
 #pragma unroll 1
                 for (int j = 0; j < kC; j += 16) {
@@ -334,6 +363,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, int block) {
                 __syncwarp();
                 tc::fence_before_sync();
                 tc::mbar_arrive(bars + 8 * (kD4Read + o));
+                if (UNITS && c + 2 < w.chunks) look(c + 2);
             }
             const int end = min(p.L, w.t0 + p.seg_len);
             if (ok)

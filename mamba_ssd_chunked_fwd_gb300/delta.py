@@ -80,8 +80,8 @@ def delta_rule(q, k, v, g, beta, *, scale=None, initial_states=None, lengths=Non
     initial_states [B,H,P,N] fp32.  ``lengths`` (int32 [B], on the GPU): tokens per
     row; y is 0 past them.  ``out``: y's memory, refused where it overlaps an input.
     16-bit tensors in whole 16-byte pieces (N, P, strides, addresses) run in chunks on the tensor
-    cores, all others token by token.  In chunks of fp16, sizes are relative to the largest state and value of a row
-    of P (gradients: of 128 rows): u below 2^14 times that, q . k below 65504."""
+    cores, all others token by token.  In chunks of fp16, precision is relative to the largest state and value
+    of a row of P (gradients: of 128 rows), and q . k must stay below 65504."""
     return _run("delta_rule", "ssd_delta_rule", q, q, k, v, g, beta, scale, initial_states, lengths, return_final_state, out)
 
 
