@@ -663,7 +663,8 @@ ssd_status ssd_block_norm_bwd(const ssd_block_norm_bwd_args *args, void *stream)
  *   lengths        [B] int32, device (optional): as for the selective scan
  * q, k, v, g and beta are read through strides as the selective scan's tensors are; y is
  * dense.  An output that overlaps an input or the other output is refused.
- * Every dim > 0, N <= 128, P <= 1024, H % G == 0.  g is meant to be <= 0 (minus
+ * Every dim > 0, N <= 128, P <= 1024, H % G == 0, B and H <= 65536, B H <= 2^20 (the step's rows
+ * are its B), L < 2^31 - 65536 and B H L / 64 < 2^31.  g is meant to be <= 0 (minus
  * infinity empties the state) and keys to be of length about one; neither is checked.  Where gates
  * grow, a sum above 88 between two of 64 tokens gives infinities and NaN.
  * States are fp32.  16-bit tensors whose N, P, strides and addresses are whole 16-byte
